@@ -34,7 +34,9 @@ GDN_CP_AUTO = 3
 EXPORTED = ["gdn_cp_plan", "gdn_chunk_fwd", "gdn_status_string", "gdn_last_cuda_error",
             "gdn_get_device_status", "gdn_cp_head_modes", "gdn_set_trace_events", "gdn_trace_last", "gdn_chunk_fwd_static",
             "gdn_get_static_device_status", "gdn_decode_step", "gdn_debug_stall_ns", "gdn_bwd_workspace_bytes",
-            "gdn_chunk_bwd", "gdn_chunk_fwd_train"]
+            "gdn_chunk_bwd", "gdn_chunk_fwd_train", "gdn_kv_append", "gdn_kv_read", "gdn_kv_attn_plan", "gdn_kv_attn"]
+
+GDN_KV_PAGE = 64
 
 
 class gdn_dims(ctypes.Structure):
@@ -59,6 +61,27 @@ class gdn_cp_plan_t(ctypes.Structure):
                 ("off_R", ctypes.c_size_t), ("off_Sloc", ctypes.c_size_t), ("off_Sstart", ctypes.c_size_t),
                 ("n_chunks_total", ctypes.c_int), ("off_chunk_map", ctypes.c_size_t),
                 ("off_wy", ctypes.c_size_t)]
+
+
+class gdn_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("status", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("h_kv", ctypes.c_int), ("d", ctypes.c_int)]
+
+
+class gdn_kv_dims(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("T", ctypes.c_int), ("h_q", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("causal", ctypes.c_int), ("window", ctypes.c_int), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64)]
+
+
+class gdn_kv_plan_t(ctypes.Structure):
+    _fields_ = [("path", ctypes.c_int), ("rows", ctypes.c_int), ("max_row_tiles", ctypes.c_int),
+                ("n_ctas", ctypes.c_int), ("n_seqs", ctypes.c_int), ("T", ctypes.c_int), ("h_q", ctypes.c_int),
+                ("h_kv", ctypes.c_int), ("dtype", ctypes.c_int), ("max_q_len", ctypes.c_int),
+                ("off_desc", ctypes.c_size_t), ("off_ml", ctypes.c_size_t), ("off_o", ctypes.c_size_t),
+                ("workspace_bytes", ctypes.c_size_t)]
 
 
 _lock = threading.Lock()
@@ -112,6 +135,14 @@ def load(path: str = LIB_PATH):
         lib.gdn_chunk_bwd.restype = ctypes.c_int
         lib.gdn_debug_stall_ns.argtypes = [ctypes.c_uint32]
         lib.gdn_debug_stall_ns.restype = ctypes.c_int
+        kc, kd, kp = ctypes.POINTER(gdn_kv_cache), ctypes.POINTER(gdn_kv_dims), ctypes.POINTER(gdn_kv_plan_t)
+        for fn in (lib.gdn_kv_append, lib.gdn_kv_read):
+            fn.argtypes = [vp, vp, vp, vp, vp, kc, kd, vp]
+            fn.restype = ctypes.c_int
+        lib.gdn_kv_attn_plan.argtypes = [kd, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, kp]
+        lib.gdn_kv_attn_plan.restype = ctypes.c_int
+        lib.gdn_kv_attn.argtypes = [vp, vp, vp, vp, kc, vp, vp, kd, kp, vp, ctypes.c_size_t, vp]
+        lib.gdn_kv_attn.restype = ctypes.c_int
         _lib = lib
         return lib
 

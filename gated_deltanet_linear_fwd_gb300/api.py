@@ -207,7 +207,8 @@ def gdn_get_device_status(workspace: torch.Tensor, stream=None):
 
 _DETAILS = {1: "a bulk copy's wait", 2: "an MMA's wait", 3: "the chunk index or segments disagree with the plan",
             4: "segments combined out of order", 5: "a value outside the fp16 range of the MMA operands",
-            6: "the test hook's stall"}
+            6: "the test hook's stall", 7: "key/value offsets or lengths outside their bounds",
+            8: "a key/value page outside the pool"}
 
 
 def describe_device_status(code: int, detail: int) -> str:
@@ -280,3 +281,167 @@ def gdn_chunk_fwd_static(q, k, v, g, beta, initial_state=None, cu_seqlens=None, 
                                        ctypes.byref(plan.raw), _stream_handle(stream))
     L.check(st, "gdn_chunk_fwd_static")
     return out, final_state
+
+
+class KVCache:
+    """The 8-bit key/value cache (gdn_kv_cache): k, v [n_pages, h_kv, 64, 128]
+    float8_e4m3fn codes, k_scale, v_scale [n_pages, h_kv] fp32 powers of two,
+    all contiguous on one device; status int32 [2], zeroed here.
+
+    KVCache.empty makes a new one; which pages belong to which sequence is the
+    caller's (page_table)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if k.dim() != 4 or k.shape[2] != L.GDN_KV_PAGE or k.shape != v.shape:
+            raise ValueError(f"k and v must be [n_pages, h_kv, {L.GDN_KV_PAGE}, 128]")
+        for name, t, dt in (("k", k, torch.float8_e4m3fn), ("v", v, torch.float8_e4m3fn),
+                            ("k_scale", k_scale, torch.float32), ("v_scale", v_scale, torch.float32)):
+            if t.dtype != dt or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {dt}")
+        if k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
+            raise ValueError("k_scale and v_scale must be [n_pages, h_kv]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.status = torch.zeros(2, dtype=torch.int32, device=k.device)
+        self.raw = L.gdn_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                  self.status.data_ptr(), k.shape[0], k.shape[1], k.shape[3])
+
+    @classmethod
+    def empty(cls, n_pages: int, h_kv: int, device="cuda") -> "KVCache":
+        codes = lambda: torch.zeros(n_pages, h_kv, L.GDN_KV_PAGE, 128, dtype=torch.uint8,  # noqa: E731
+                                    device=device).view(torch.float8_e4m3fn)
+        scale = lambda: torch.ones(n_pages, h_kv, dtype=torch.float32, device=device)  # noqa: E731
+        return cls(codes(), codes(), scale(), scale())
+
+
+def _kv_rows(name: str, t: torch.Tensor, heads: int) -> int:
+    """Token stride of a [T, heads, 128] tensor whose tokens are whole."""
+    if not t.is_cuda or t.dim() != 3 or t.shape[1] != heads:
+        raise ValueError(f"{name} must be a CUDA tensor [T, {heads}, 128]")
+    s = t.stride()
+    if s[2] != 1 or (s[1] != t.shape[2] and heads > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return s[0] if t.shape[0] > 1 else 0
+
+
+def _kv_ints(kv_lens: torch.Tensor, page_table: torch.Tensor, cu_seqlens: Optional[torch.Tensor]):
+    n = kv_lens.shape[0]
+    if kv_lens.dtype != torch.int32 or page_table.dtype != torch.int32 or not kv_lens.is_cuda:
+        raise ValueError("kv_lens and page_table must be int32 CUDA tensors")
+    if page_table.dim() != 2 or page_table.shape[0] != n or not page_table.is_contiguous() or not kv_lens.is_contiguous():
+        raise ValueError("page_table must be contiguous [n_seqs, max_pages]")
+    if cu_seqlens is None:
+        return n, page_table.shape[1], None
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (n + 1,) or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous int32 [n_seqs + 1]")
+    return n, page_table.shape[1], cu_seqlens.data_ptr()
+
+
+def _raw_stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def gdn_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor,
+                  cu_seqlens: Optional[torch.Tensor] = None, *, stream=None) -> None:
+    """Quantises new tokens into the cache (gdn_kv_append): k, v [T, h_kv, 128]
+    bf16 or fp32, packed over the sequences by cu_seqlens (None: T / n_seqs
+    each); kv_lens int32 [n_seqs] counts the new tokens too.  k and v may be
+    views with a larger token stride (parts of one projection's output)."""
+    n, max_pages, cu = _kv_ints(kv_lens, page_table, cu_seqlens)
+    h_kv = cache.raw.h_kv
+    ks, vs = _kv_rows("k", k, h_kv), _kv_rows("v", v, h_kv)
+    if v.dtype != k.dtype or v.shape != k.shape or k.shape[2] != 128:
+        raise ValueError("k and v must be alike, with 128 elements a head")
+    dims = L.gdn_kv_dims(n, k.shape[0], h_kv, max_pages, 1, 0, 0.0, _DT.get(k.dtype, -1), 0, ks, vs, 0)
+    st = L.load().gdn_kv_append(k.data_ptr(), v.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), cu, cache.raw,
+                                dims, _raw_stream(stream))
+    L.check(st, "gdn_kv_append")
+
+
+def gdn_kv_read(cache: KVCache, kv_lens: torch.Tensor, page_table: torch.Tensor,
+                cu_seqlens: Optional[torch.Tensor] = None, *, T: Optional[int] = None,
+                dtype: torch.dtype = torch.bfloat16, k_out: Optional[torch.Tensor] = None,
+                v_out: Optional[torch.Tensor] = None, stream=None):
+    """The cache's values of the last n_i tokens of each sequence (gdn_kv_read),
+    exact in bf16 or fp32: (k, v), each [T, h_kv, 128].  T: their number over
+    all sequences, when no outputs are given."""
+    n, max_pages, cu = _kv_ints(kv_lens, page_table, cu_seqlens)
+    h_kv = cache.raw.h_kv
+    if k_out is None or v_out is None:
+        if T is None:
+            raise ValueError("gdn_kv_read needs T or both outputs")
+        shape = (T, h_kv, 128)
+        k_out = torch.empty(shape, dtype=dtype, device=cache.k.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dtype, device=cache.k.device) if v_out is None else v_out
+    ks, vs = _kv_rows("k_out", k_out, h_kv), _kv_rows("v_out", v_out, h_kv)
+    if v_out.dtype != k_out.dtype or v_out.shape != k_out.shape or k_out.shape[2] != 128:
+        raise ValueError("k_out and v_out must be alike, with 128 elements a head")
+    dims = L.gdn_kv_dims(n, k_out.shape[0], h_kv, max_pages, 1, 0, 0.0, _DT.get(k_out.dtype, -1), 0, ks, vs, 0)
+    st = L.load().gdn_kv_read(k_out.data_ptr(), v_out.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), cu,
+                              cache.raw, dims, _raw_stream(stream))
+    L.check(st, "gdn_kv_read")
+    return k_out, v_out
+
+
+@dataclasses.dataclass
+class KVPlan:
+    """A filled gdn_kv_plan_t and the masks and scale it was made for."""
+    raw: L.gdn_kv_plan_t
+    causal: bool
+    window: int
+    scale: float
+
+    @property
+    def workspace_bytes(self) -> int:
+        return int(self.raw.workspace_bytes)
+
+
+def gdn_kv_attn_plan(*, T: int, n_seqs: int, h_q: int, h_kv: int, max_q_len: int = 0, max_kv_len: int = 0,
+                     max_pages: int = 0, dtype: torch.dtype = torch.bfloat16, causal: bool = True, window: int = 0,
+                     scale: float = 0.0, sm_count: int = 0) -> KVPlan:
+    """Host-only planning of gdn_kv_attn.  max_q_len: the most tokens a sequence
+    brings (0: T); max_kv_len: the longest sequence expected (0: 64 max_pages)."""
+    if not max_pages:
+        max_pages = max(1, -(-max_kv_len // L.GDN_KV_PAGE))
+    dims = L.gdn_kv_dims(n_seqs, T, h_q, max_pages, int(causal), window, scale, _DT.get(dtype, -1), 0, 0, 0, 0)
+    raw = L.gdn_kv_plan_t()
+    L.check(L.load().gdn_kv_attn_plan(dims, h_kv, max_q_len, max_kv_len, sm_count, raw), "gdn_kv_attn_plan")
+    return KVPlan(raw, causal, window, scale)
+
+
+def gdn_kv_attn(q: torch.Tensor, cache: KVCache, kv_lens: torch.Tensor, page_table: torch.Tensor,
+                cu_seqlens: Optional[torch.Tensor] = None, *, plan: Optional[KVPlan] = None,
+                out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, return_lse: bool = True,
+                workspace: Optional[torch.Tensor] = None, causal: bool = True, window: int = 0, scale: float = 0.0,
+                max_q_len: int = 0, max_kv_len: int = 0, stream=None):
+    """Attention of each new token over its sequence's cached keys and values
+    (gdn_kv_attn): q [T, h_q, 128] bf16 or fp32, packed like gdn_kv_append's k
+    and v, which go into the cache first.  Returns (out [T, h_q, 128],
+    lse [T, h_q] fp32 or None).  causal, window, scale and the bounds are the
+    plan's when one is given; a plan holds for calls of the same sizes."""
+    n, max_pages, cu = _kv_ints(kv_lens, page_table, cu_seqlens)
+    T, h_q, d = q.shape
+    qs = _kv_rows("q", q, h_q)
+    if d != 128:
+        raise ValueError("q must have 128 elements a head")
+    if plan is None:
+        plan = gdn_kv_attn_plan(T=T, n_seqs=n, h_q=h_q, h_kv=cache.raw.h_kv,
+                                max_q_len=max_q_len or (T // n if cu is None else T), max_kv_len=max_kv_len,
+                                max_pages=max_pages, dtype=q.dtype, causal=causal, window=window, scale=scale)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("out must be like q")
+    if lse is None:
+        if return_lse:
+            lse = torch.empty(T, h_q, dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or lse.shape != (T, h_q) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [T, h_q]")
+    if workspace is None:
+        workspace = torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=q.device)
+    dims = L.gdn_kv_dims(n, T, h_q, max_pages, int(plan.causal), plan.window, plan.scale, _DT.get(q.dtype, -1), qs, 0, 0,
+                         _kv_rows("out", out, h_q))
+    st = L.load().gdn_kv_attn(q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), cu, cache.raw, out.data_ptr(),
+                              None if lse is None else lse.data_ptr(), dims, plan.raw, workspace.data_ptr(),
+                              workspace.numel(), _raw_stream(stream))
+    L.check(st, "gdn_kv_attn")
+    return out, lse

@@ -10,6 +10,7 @@
 
 #include "gdn.h"
 #include "gdn_internal.cuh"
+#include "gdn_kv.cuh"
 
 using namespace gdn;
 
@@ -84,6 +85,7 @@ gdn_status device_setup(int* dev_out) {
   if ((e = combine_kernel_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = f32_kernel_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = bwd_kernel_setup()) != cudaSuccess) return cuda_fail(e);
+  if ((e = kv_simt_setup()) != cudaSuccess) return cuda_fail(e);
   int sms = 0;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_fail(e);
   g_sm_count[dev] = sms;
@@ -281,6 +283,84 @@ gdn_status static_workspace(void** out) {
   *out = g_static_ws_dev[dev];
   return GDN_OK;
 }
+
+// ---- the 8-bit key/value cache ----
+// Checks shared by its entry points; es: bytes of an element.
+gdn_status check_kv(const gdn_kv_dims* d, const gdn_kv_cache* c, const int32_t* lens, const int32_t* table,
+                    const int32_t* cu) {
+  if (!d || !c) return GDN_ERR_INVALID_ARG;
+  if (c->d != kHeadDim) return GDN_ERR_UNSUPPORTED;
+  if (d->dtype != GDN_BF16 && d->dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->status || !lens || !table) return GDN_ERR_INVALID_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v)) return GDN_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale) |
+       reinterpret_cast<uintptr_t>(c->status) | reinterpret_cast<uintptr_t>(lens) |
+       reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(cu)) & 3u)
+    return GDN_ERR_MISALIGNED;
+  if (d->n_seqs < 1 || d->T < 0 || d->max_pages < 1 || c->n_pages < 1 || c->h_kv < 1 || c->h_kv > 65535)
+    return GDN_ERR_INVALID_ARG;
+  if ((int64_t)c->n_pages * c->h_kv > 0x7fffffff || d->max_pages > 0x7fffffff / kPage) return GDN_ERR_INVALID_ARG;
+  if (!cu && d->T % d->n_seqs) return GDN_ERR_INVALID_ARG;
+  return GDN_OK;
+}
+
+// A token stride in elements: 0 selects packed rows of `heads` heads.
+gdn_status kv_stride(int64_t given, int heads, int dtype, int64_t* out) {
+  const int64_t packed = (int64_t)heads * kHeadDim;
+  *out = given ? given : packed;
+  if (*out < packed || *out > ((int64_t)1 << 40)) return GDN_ERR_INVALID_ARG;
+  return *out % (dtype == GDN_F32 ? 4 : 8) ? GDN_ERR_MISALIGNED : GDN_OK;
+}
+
+KvArgs kv_args(const gdn_kv_dims* d, const gdn_kv_cache* c, const int32_t* lens, const int32_t* table,
+               const int32_t* cu) {
+  KvArgs a;
+  a.lens = lens;
+  a.table = table;
+  a.cu = cu;
+  a.k = static_cast<uint8_t*>(c->k);
+  a.v = static_cast<uint8_t*>(c->v);
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.status = c->status;
+  a.n_seqs = d->n_seqs;
+  a.T = d->T;
+  a.n_each = cu ? 0 : d->T / d->n_seqs;
+  a.h_q = d->h_q;
+  a.h_kv = c->h_kv;
+  a.max_pages = d->max_pages;
+  a.n_pages = c->n_pages;
+  return a;
+}
+
+gdn_status kv_move(bool read, void* k, void* v, const int32_t* lens, const int32_t* table, const int32_t* cu,
+                   const gdn_kv_cache* cache, const gdn_kv_dims* d, void* stream) {
+  gdn_status st = check_kv(d, cache, lens, table, cu);
+  if (st != GDN_OK) return st;
+  KvAppendArgs a;
+  if ((st = kv_stride(d->k_stride, cache->h_kv, d->dtype, &a.k_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->v_stride, cache->h_kv, d->dtype, &a.v_stride)) != GDN_OK) return st;
+  if (d->T == 0) return GDN_OK;
+  if (!k || !v) return GDN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return GDN_ERR_MISALIGNED;
+  a.c = kv_args(d, cache, lens, table, cu);
+  a.k = k;
+  a.v = v;
+  // n tokens from any position lie in at most (n + 62) / 64 + 1 pages
+  a.pages_each = cu ? 0 : (a.c.n_each + 62) / kPage + 1;
+  const int64_t entries = cu ? (int64_t)d->T / kPage + 2 * (int64_t)std::min(d->n_seqs, d->T)
+                             : (int64_t)d->n_seqs * a.pages_each;
+  if (entries > 0x7fffffff) return GDN_ERR_INVALID_ARG;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const bool f32 = d->dtype == GDN_F32;
+  LaunchLog log;
+  cudaError_t e = log.before(cs);
+  if (e == cudaSuccess) e = read ? launch_kv_read(a, f32, (unsigned)entries, cs) : launch_kv_append(a, f32, (unsigned)entries, cs);
+  if (e == cudaSuccess) e = log.after(read ? "kv_read" : "kv_append", cs);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+constexpr int kKvPathSimt = 0;
 
 }  // namespace
 
@@ -718,6 +798,112 @@ gdn_status gdn_decode_step(const void* q, const void* k, const void* v, const fl
   cudaError_t e = log.before(cs);
   if (e == cudaSuccess) e = launch_decode(a, dims->dtype == GDN_F32, cs);
   if (e == cudaSuccess) e = log.after("decode", cs);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+gdn_status gdn_kv_append(const void* k, const void* v, const int32_t* lens, const int32_t* table, const int32_t* cu,
+                         const gdn_kv_cache* cache, const gdn_kv_dims* dims, void* stream) {
+  return kv_move(false, const_cast<void*>(k), const_cast<void*>(v), lens, table, cu, cache, dims, stream);
+}
+
+gdn_status gdn_kv_read(void* k_out, void* v_out, const int32_t* lens, const int32_t* table, const int32_t* cu,
+                       const gdn_kv_cache* cache, const gdn_kv_dims* dims, void* stream) {
+  return kv_move(true, k_out, v_out, lens, table, cu, cache, dims, stream);
+}
+
+gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int max_kv_len, int sm_count,
+                            gdn_kv_plan_t* out) {
+  if (!d || !out) return GDN_ERR_INVALID_ARG;
+  if (d->dtype != GDN_BF16 && d->dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if (d->causal != 0 && d->causal != 1) return GDN_ERR_UNSUPPORTED;
+  if (d->n_seqs < 1 || d->T < 0 || d->h_q < 1 || h_kv < 1 || h_kv > d->h_q || d->h_q > 65535 || d->max_pages < 1 ||
+      d->window < 0 || d->max_pages > 0x7fffffff / kPage || !(std::isfinite(d->scale)))
+    return GDN_ERR_INVALID_ARG;
+  if (max_q_len <= 0 || max_q_len > d->T) max_q_len = d->T;
+  const int64_t longest = (int64_t)d->max_pages * kPage;
+  if (max_kv_len <= 0 || max_kv_len > longest) max_kv_len = (int)std::min<int64_t>(longest, 0x7fffffff);
+  if (sm_count <= 0) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sm_count, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  gdn_kv_plan_t p;
+  std::memset(&p, 0, sizeof(p));
+  const int group = (d->h_q + h_kv - 1) / h_kv;
+  if ((int64_t)d->T * group > 0x7fffffff - 4096) return GDN_ERR_INVALID_ARG;
+  p.path = kKvPathSimt;
+  p.rows = 16;
+  int per_sm = 2;
+  p.max_row_tiles = std::max<int>(1, (int)(((int64_t)max_q_len * group + p.rows - 1) / p.rows));
+  const int64_t items = (int64_t)d->n_seqs * p.max_row_tiles * h_kv;
+  const int64_t tiles = std::max<int64_t>(1, (max_kv_len + kKvTile - 1) / kKvTile);
+  // Short sequences: a CTA walks an item's few tiles in less time than a second kernel takes to join parts.
+  p.n_ctas = tiles <= 4 && items <= 0x7fffffff ? 0 : (int)std::min<int64_t>((int64_t)per_sm * sm_count, items * tiles);
+  p.n_seqs = d->n_seqs;
+  p.T = d->T;
+  p.h_q = d->h_q;
+  p.h_kv = h_kv;
+  p.dtype = d->dtype;
+  p.max_q_len = max_q_len;
+  p.off_desc = 0;
+  p.off_ml = align_up((size_t)p.n_ctas * sizeof(int4), 256);
+  p.off_o = align_up(p.off_ml + (size_t)2 * p.n_ctas * p.rows * sizeof(float2), 256);
+  p.workspace_bytes = p.off_o + (size_t)2 * p.n_ctas * p.rows * kHeadDim * sizeof(float);
+  *out = p;
+  return GDN_OK;
+}
+
+gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table, const int32_t* cu,
+                       const gdn_kv_cache* cache, void* out, float* lse, const gdn_kv_dims* d,
+                       const gdn_kv_plan_t* plan, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_status st = check_kv(d, cache, lens, table, cu);
+  if (st != GDN_OK) return st;
+  if (!plan || plan->n_seqs != d->n_seqs || plan->T != d->T || plan->h_q != d->h_q || plan->h_kv != cache->h_kv ||
+      plan->dtype != d->dtype)
+    return GDN_ERR_INVALID_ARG;
+  if (d->causal != 0 && d->causal != 1) return GDN_ERR_UNSUPPORTED;
+  if (d->window < 0 || !std::isfinite(d->scale)) return GDN_ERR_INVALID_ARG;
+  KvAttnArgs a;
+  if ((st = kv_stride(d->q_stride, d->h_q, d->dtype, &a.q_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->out_stride, d->h_q, d->dtype, &a.out_stride)) != GDN_OK) return st;
+  if (d->T == 0) return GDN_OK;
+  if (!q || !out) return GDN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return GDN_ERR_MISALIGNED;
+  if (!cu && d->T / d->n_seqs > plan->max_q_len) return GDN_ERR_INVALID_ARG;
+  if (plan->n_ctas > 0) {
+    if (!workspace || workspace_bytes < plan->workspace_bytes) return GDN_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GDN_ERR_MISALIGNED;
+  }
+  int dev = 0;
+  if ((st = device_setup(&dev)) != GDN_OK) return st;
+  a.c = kv_args(d, cache, lens, table, cu);
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.causal = d->causal;
+  a.window = d->window;
+  a.scale_log2 = (d->scale != 0.f ? d->scale : 1.0f / std::sqrt((float)kHeadDim)) * 1.44269504088896341f;
+  a.group = (d->h_q + cache->h_kv - 1) / cache->h_kv;
+  a.rows = plan->rows;
+  a.max_row_tiles = plan->max_row_tiles;
+  a.n_ctas = plan->n_ctas;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.desc = reinterpret_cast<int4*>(ws + plan->off_desc);
+  a.ml = reinterpret_cast<float2*>(ws + plan->off_ml);
+  a.o = reinterpret_cast<float*>(ws + plan->off_o);
+  const unsigned grid = a.n_ctas ? (unsigned)a.n_ctas : (unsigned)((int64_t)d->n_seqs * a.max_row_tiles * cache->h_kv);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const bool f32 = d->dtype == GDN_F32;
+  LaunchLog log;
+  cudaError_t e = log.before(cs);
+  if (e == cudaSuccess) e = launch_kv_attn_simt(a, f32, grid, cs);
+  if (e == cudaSuccess) e = log.after("kv_attn", cs);
+  if (a.n_ctas) {
+    if (e == cudaSuccess) e = log.before(cs);
+    if (e == cudaSuccess) e = launch_kv_combine(a, f32, cs);
+    if (e == cudaSuccess) e = log.after("kv_combine", cs);
+  }
   return e == cudaSuccess ? GDN_OK : cuda_fail(e);
 }
 

@@ -1,0 +1,297 @@
+// Shared definitions of the 8-bit key/value cache: its arguments, e4m3
+// conversions, and how the key tiles of an attention call are shared out to
+// CTAs.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "gdn_internal.cuh"
+
+namespace gdn {
+
+constexpr int kPage = 64;      // tokens of a page and of a scale
+constexpr int kKvTile = 128;   // keys of an attention tile: two pages
+constexpr int kHeadDim = 128;
+constexpr int kPageBytes = kPage * kHeadDim;  // codes of one (page, head)
+
+constexpr int kDetKvLengths = 7;  // offsets or a length outside their bounds
+constexpr int kDetKvPage = 8;     // a page outside the pool
+
+// The cache and the batch.
+struct KvArgs {
+  const int32_t* lens;   // [n_seqs]
+  const int32_t* table;  // [n_seqs, max_pages]
+  const int32_t* cu;     // [n_seqs + 1] or null
+  uint8_t* k;            // [n_pages, h_kv, 64, 128]
+  uint8_t* v;
+  float* k_scale;        // [n_pages, h_kv]
+  float* v_scale;
+  int* status;
+  int n_seqs, T, n_each; // n_each: tokens of every sequence when cu is null
+  int h_q, h_kv, max_pages, n_pages;
+};
+
+struct KvAppendArgs {
+  KvArgs c;
+  void* k;  // append: const inputs; read: outputs
+  void* v;
+  int64_t k_stride, v_stride;
+  int pages_each;  // cu null: page slots per sequence
+};
+
+struct KvAttnArgs {
+  KvArgs c;
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_stride, out_stride;
+  int causal, window;
+  float scale_log2;        // score scale times log2(e)
+  int group;               // query heads per key/value head, rounded up
+  int rows, max_row_tiles; // rows of a row tile; row tiles per (sequence, head)
+  int n_ctas;              // 0: CTA i takes item i whole
+  int4* desc;              // [n_ctas] item whose first part this CTA made: {sequence, row tile, head, last CTA}
+  float2* ml;              // [2 n_ctas, rows] running maximum (log2) and sum of a part
+  float* o;                // [2 n_ctas, rows, 128] unnormalised output of a part
+};
+
+// First packed token, number of new tokens and length of sequence s.  What
+// does not fit the call's bounds is reported and counts as empty.
+struct KvSeq {
+  int tok0, n, len;
+};
+__device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int s) {
+  KvSeq r;
+  int b, e;
+  if (a.cu) {
+    b = a.cu[s];
+    e = a.cu[s + 1];
+  } else {
+    b = s * a.n_each;
+    e = b + a.n_each;
+  }
+  r.tok0 = b;
+  r.n = e - b;
+  r.len = a.lens[s];
+  if (b < 0 || e < b || e > a.T || r.len < 0 || r.len > (int64_t)a.max_pages * kPage) {
+    report(a.status, kDevCheck, kDetKvLengths);
+    r.tok0 = 0;
+    r.n = r.len = 0;
+  }
+  return r;
+}
+
+// Pool page of page slot `slot` of sequence s, or -1 (reported) for one
+// outside the pool.
+__device__ __forceinline__ int kv_page(const KvArgs& a, int s, int slot) {
+  const int p = a.table[(int64_t)s * a.max_pages + slot];
+  if ((unsigned)p < (unsigned)a.n_pages) return p;
+  report(a.status, kDevCheck, kDetKvPage);
+  return -1;
+}
+
+// Query heads of key/value head h: those j with floor(j h_kv / h_q) = h.
+__device__ __forceinline__ int kv_first_q_head(const KvArgs& a, int h) {
+  return (int)(((int64_t)h * a.h_q + a.h_kv - 1) / a.h_kv);
+}
+
+// ---- e4m3 ----
+// Two codes (low byte first) to fp32; exact.
+__device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+  float lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(h));
+  return make_float2(lo, hi);
+}
+// Two fp32 to codes: nearest even, saturating at 448, NaN to NaN.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+  return c;
+}
+
+// ---- sharing out an attention call ----
+// An item is (sequence, row tile, key/value head); its units are its key
+// tiles, at least one (an item without keys still writes zeros).  All units,
+// in the order sequence, row tile, head, tile, are cut into n_ctas equal
+// runs, one a CTA, so the SMs get the same number of key tiles whatever the
+// lengths are.  A run covers whole items and at most one part of an item at
+// each end; parts go to the workspace and the combine kernel joins them.
+struct KvItem {
+  int tok0, n, len;       // the sequence
+  int first_tile, tiles;  // key tiles its masks touch; tiles < 0: no such item
+};
+__device__ __forceinline__ KvItem kv_item(const KvAttnArgs& a, int seq, int rt) {
+  KvItem it;
+  const KvSeq s = kv_seq(a.c, seq);
+  it.tok0 = s.tok0;
+  it.n = s.n;
+  it.len = s.len;
+  it.first_tile = 0;
+  const int r0 = rt * a.rows, rows = s.n * a.group;
+  if (rows > a.max_row_tiles * a.rows) report(a.c.status, kDevCheck, kDetKvLengths);  // more tokens than the plan's bound
+  if (r0 >= rows) {
+    it.tiles = -1;
+    return it;
+  }
+  const int t0 = r0 / a.group, t1 = min(s.n - 1, (r0 + a.rows - 1) / a.group);
+  const int past = s.len - s.n;  // position of the first new token; negative for idle slots
+  const int hi = a.causal ? min(max(past + t1 + 1, 0), s.len) : s.len;
+  const int lo = a.window > 0 ? max(0, past + t0 - a.window + 1) : 0;
+  it.first_tile = lo / kKvTile;
+  it.tiles = hi > lo ? (hi + kKvTile - 1) / kKvTile - it.first_tile : 0;
+  return it;
+}
+__device__ __forceinline__ int kv_units(const KvItem& it) { return it.tiles < 0 ? 0 : max(1, it.tiles); }
+
+struct KvRun {
+  int seq, rt, head, off;  // first item of the run and the unit of it that the run starts with
+  int64_t begin, end;      // units
+  int64_t total;           // units of the call
+  int ctas;                // CTAs that have a run: no more than there are units, so none is empty
+};
+
+// A CTA's run, found by all its threads (NT of them, a multiple of 32) from
+// the lengths; `scratch` is shared memory.
+struct KvRunScratch {
+  int64_t part[32];
+  KvRun run;
+};
+template <int NT>
+__device__ __forceinline__ int64_t block_inclusive_scan(int64_t v, KvRunScratch* sc, int64_t& total) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += u;
+  }
+  __syncthreads();
+  if (lane == 31) sc->part[warp] = v;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    const int64_t p = sc->part[w];
+    if (w < warp) before += p;
+    total += p;
+  }
+  return v + before;
+}
+template <int NT>
+__device__ __forceinline__ KvRun kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
+  const int tid = threadIdx.x;
+  const int64_t entries = (int64_t)a.c.n_seqs * a.max_row_tiles;
+  if (a.n_ctas == 0) {  // one whole item a CTA
+    KvRun r;
+    r.head = blockIdx.x % a.c.h_kv;
+    const int e = blockIdx.x / a.c.h_kv;
+    r.seq = e / a.max_row_tiles;
+    r.rt = e % a.max_row_tiles;
+    r.off = 0;
+    r.begin = 0;
+    r.end = r.total = kv_units(kv_item(a, r.seq, r.rt));
+    r.ctas = 0;
+    return r;
+  }
+  int64_t sum = 0;
+  for (int64_t e = tid; e < entries; e += NT)
+    sum += kv_units(kv_item(a, (int)(e / a.max_row_tiles), (int)(e % a.max_row_tiles)));
+  int64_t total;
+  block_inclusive_scan<NT>(sum, sc, total);
+  total *= a.c.h_kv;
+  const int ctas = (int)min((int64_t)a.n_ctas, total);
+  const int64_t begin = (int)blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
+  const int64_t end = (int)blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
+  int64_t base = 0;
+  for (int64_t e0 = 0; e0 < entries && base <= begin && begin < end; e0 += NT) {
+    const int64_t e = e0 + tid;
+    const int u = e < entries ? kv_units(kv_item(a, (int)(e / a.max_row_tiles), (int)(e % a.max_row_tiles))) : 0;
+    int64_t sub;
+    const int64_t incl = base + block_inclusive_scan<NT>((int64_t)u * a.c.h_kv, sc, sub);
+    const int64_t excl = incl - (int64_t)u * a.c.h_kv;
+    if (excl <= begin && begin < incl) {
+      const int64_t in = begin - excl;
+      KvRun r;
+      r.seq = (int)(e / a.max_row_tiles);
+      r.rt = (int)(e % a.max_row_tiles);
+      r.head = (int)(in / u);
+      r.off = (int)(in % u);
+      sc->run = r;
+    }
+    base += sub;
+  }
+  __syncthreads();
+  KvRun r = sc->run;
+  r.begin = begin;
+  r.end = end;
+  r.total = total;
+  r.ctas = ctas;
+  return r;
+}
+
+// Walks the items of a run; every warp that needs it walks its own.
+struct KvCursor {
+  KvItem it;
+  int seq, rt, head;
+  int off, len;       // units [off, off + len) of the item belong to the run
+  int64_t at, end;    // next unit, end of the run
+  __device__ __forceinline__ void start(const KvAttnArgs& a, const KvRun& r) {
+    seq = r.seq;
+    rt = r.rt;
+    head = r.head;
+    off = r.off;
+    at = r.begin;
+    end = r.end;
+    if (at < end) {
+      it = kv_item(a, seq, rt);
+      len = (int)min(end - at, (int64_t)(kv_units(it) - off));
+    }
+  }
+  __device__ __forceinline__ bool valid() const { return at < end; }
+  __device__ __forceinline__ void next(const KvAttnArgs& a) {
+    at += len;
+    off = 0;
+    if (at >= end) return;
+    if (++head == a.c.h_kv) {
+      head = 0;
+      ++rt;
+      while (true) {  // a run ends before the items do, so there is a next one
+        if (rt < a.max_row_tiles) {
+          it = kv_item(a, seq, rt);
+          if (it.tiles >= 0) break;
+        }
+        rt = 0;
+        if (++seq >= a.c.n_seqs) {
+          at = end;
+          return;
+        }
+      }
+    }
+    len = (int)min(end - at, (int64_t)kv_units(it));
+  }
+  // key tiles [tile_begin, tile_begin + tiles) of the run's part of the item
+  __device__ __forceinline__ int tiles() const { return it.tiles == 0 ? 0 : len; }
+  __device__ __forceinline__ int tile_begin() const { return it.first_tile + off; }
+  __device__ __forceinline__ bool whole() const { return off == 0 && len == kv_units(it); }
+  __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (off > 0 ? 0 : 1); }
+};
+
+// The last CTA that has a part of the item whose first part this cursor
+// stands on: CTA c owns unit u when c = floor(((u + 1) ctas - 1) / total).
+__device__ __forceinline__ int kv_last_cta(const KvRun& r, const KvCursor& c) {
+  const int64_t item_end = c.at + kv_units(c.it);
+  return (int)((item_end * r.ctas - 1) / r.total);
+}
+
+// ---- launchers ----
+cudaError_t launch_kv_append(const KvAppendArgs& a, bool f32, unsigned entries, cudaStream_t st);
+cudaError_t launch_kv_read(const KvAppendArgs& a, bool f32, unsigned entries, cudaStream_t st);
+cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, bool f32, unsigned grid, cudaStream_t st);
+cudaError_t launch_kv_combine(const KvAttnArgs& a, bool f32, cudaStream_t st);
+cudaError_t kv_simt_setup();
+
+}  // namespace gdn

@@ -1,0 +1,262 @@
+// Attention over the 8-bit key/value cache on the CUDA cores in fp32, and
+// the kernel that joins the parts of items several CTAs worked on.
+//
+// For a row (token at position p, query head) and the keys j its masks leave,
+// with x_j = scale log2(e) q . k_j: running maximum m and sum l = sum
+// 2^(x_j - m), output sum 2^(x_j - m) v_j / l, one pass over the keys, both
+// rescaled by 2^(m_old - m) when m grows.
+//
+// A CTA takes 16 rows of a key/value head's group and one page (64 keys) at a
+// time: thread (r, c) forms the scores of row r with keys c, c + 16, ...,
+// then columns 8 c .. 8 c + 7 of row r's output.  Bound by shared-memory reads
+// (a key or value element feeds 16 rows) and fp32 FMAs.
+#include "gdn_kv.cuh"
+#include "sm103_ptx.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 16;
+constexpr int kKeyStride = kHeadDim + 4;  // floats; rows 4 banks apart
+constexpr int kSStride = kPage + 4;
+
+struct SimtSmem {
+  float q[kRows][kHeadDim];
+  float k[kPage][kKeyStride];
+  float v[kPage][kHeadDim];
+  float s[kRows][kSStride];
+  KvRunScratch run;
+};
+
+__device__ __forceinline__ float load_elem(const float* p) { return *p; }
+__device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store_elem(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store_elem(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+constexpr float kLn2 = 0.693147180559945309f;
+
+// log sum exp from the running maximum (log2) and sum.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * kLn2;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const KvAttnArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SimtSmem& sm = *reinterpret_cast<SimtSmem*>(smem_raw);
+  const int tid = threadIdx.x, r = tid >> 4, c = tid & 15;
+  const KvRun run = kv_run<kThreads>(a, &sm.run);
+  if (a.n_ctas && tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  KvCursor cur;
+  for (cur.start(a, run); cur.valid(); cur.next(a)) {
+    const KvItem& it = cur.it;
+    // row r of the item: token t of the sequence, query head j
+    const int rr = cur.rt * kRows + r, t = rr / a.group;
+    const int j = kv_first_q_head(a.c, cur.head) + rr % a.group;
+    const bool live = t < it.n && j < kv_first_q_head(a.c, cur.head + 1);
+    const int p = it.len - it.n + t;
+    const int key_end = live ? (a.causal ? min(p + 1, it.len) : it.len) : 0;
+    const int key_begin = a.window > 0 ? max(0, p - a.window + 1) : 0;
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      sm.q[r][c + 16 * e] =
+          live ? load_elem(reinterpret_cast<const T*>(a.q) + (int64_t)(it.tok0 + t) * a.q_stride + j * kHeadDim + c + 16 * e)
+               : 0.f;
+    float m = -__int_as_float(0x7f800000), l = 0.f, o[8] = {};
+    const int page_begin = 2 * cur.tile_begin(), page_end = min(page_begin + 2 * cur.tiles(), (it.len + kPage - 1) / kPage);
+    for (int pg = page_begin; pg < page_end; ++pg) {
+      __syncthreads();
+      const int page = kv_page(a.c, cur.seq, pg);
+      const size_t head = (size_t)max(page, 0) * a.c.h_kv + cur.head;
+      const float sk = a.c.k_scale[head], sv = a.c.v_scale[head];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int ch = i * kThreads + tid, row = ch >> 3, col = (ch & 7) * 16;
+        const bool in = pg * kPage + row < it.len;  // rows past the sequence may hold anything
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const uint4 wk = in ? __ldg(reinterpret_cast<const uint4*>(a.c.k + head * kPageBytes) + ch) : zero;
+        const uint4 wv = in ? __ldg(reinterpret_cast<const uint4*>(a.c.v + head * kPageBytes) + ch) : zero;
+        const uint32_t kk[4] = {wk.x, wk.y, wk.z, wk.w}, vv[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 k0 = e4m3x2_to_f32x2(kk[w]), k1 = e4m3x2_to_f32x2(kk[w] >> 16);
+          const float2 v0 = e4m3x2_to_f32x2(vv[w]), v1 = e4m3x2_to_f32x2(vv[w] >> 16);
+          *reinterpret_cast<float4*>(&sm.k[row][col + 4 * w]) = make_float4(k0.x * sk, k0.y * sk, k1.x * sk, k1.y * sk);
+          *reinterpret_cast<float4*>(&sm.v[row][col + 4 * w]) = make_float4(v0.x * sv, v0.y * sv, v1.x * sv, v1.y * sv);
+        }
+      }
+      __syncthreads();
+      float x[4] = {};
+#pragma unroll 4
+      for (int d = 0; d < kHeadDim; d += 4) {
+        const float4 q4 = *reinterpret_cast<const float4*>(&sm.q[r][d]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 k4 = *reinterpret_cast<const float4*>(&sm.k[c + 16 * i][d]);
+          x[i] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, x[i]))));
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = pg * kPage + c + 16 * i;
+        x[i] = key >= key_begin && key < key_end ? x[i] * a.scale_log2 : -__int_as_float(0x7f800000);
+        top = fmaxf(top, x[i]);
+      }
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float ref = top == -__int_as_float(0x7f800000) ? 0.f : top;
+      const float alpha = exp2f(m - ref);
+      l *= alpha;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float w = exp2f(x[i] - ref);
+        l += w;
+        sm.s[r][c + 16 * i] = w;
+      }
+      m = top;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] *= alpha;
+      __syncwarp();  // a row's 16 threads are in one warp
+#pragma unroll 4
+      for (int i = 0; i < kPage; ++i) {
+        const float w = sm.s[r][i];
+        if (w == 0.f) continue;  // a masked value may be NaN
+        const float4 v0 = *reinterpret_cast<const float4*>(&sm.v[i][8 * c]);
+        const float4 v1 = *reinterpret_cast<const float4*>(&sm.v[i][8 * c + 4]);
+        o[0] = fmaf(w, v0.x, o[0]);
+        o[1] = fmaf(w, v0.y, o[1]);
+        o[2] = fmaf(w, v0.z, o[2]);
+        o[3] = fmaf(w, v0.w, o[3]);
+        o[4] = fmaf(w, v1.x, o[4]);
+        o[5] = fmaf(w, v1.y, o[5]);
+        o[6] = fmaf(w, v1.z, o[6]);
+        o[7] = fmaf(w, v1.w, o[7]);
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if (cur.whole()) {
+      if (live) {
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        T* dst = reinterpret_cast<T*>(a.out) + (int64_t)(it.tok0 + t) * a.out_stride + j * kHeadDim + 8 * c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) store_elem(dst + e, o[e] * inv);
+        if (a.lse && c == 0) a.lse[(int64_t)(it.tok0 + t) * a.c.h_q + j] = lse_of(m, l);
+      }
+    } else {
+      const size_t row = (size_t)cur.slot() * kRows + r;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a.o[row * kHeadDim + 8 * c + e] = o[e];
+      if (c == 0) a.ml[row] = make_float2(m, l);
+      if (tid == 0 && cur.off == 0)
+        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(run, cur));
+    }
+  }
+}
+
+// Joins the parts of an item: with M the largest of their maxima m_i,
+// out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Block (c, y) looks after
+// the item whose first part CTA c made, rows y kRowsPerBlock ...; kWarps warps
+// share a row's parts (many when few rows meet a long axis), a lane holds 4
+// columns.  Reads each part once.
+template <typename T, int kWarps>
+__global__ void __launch_bounds__(256) combine_kernel(const KvAttnArgs a) {
+  constexpr int kRowsPerBlock = 8 / kWarps;
+  __shared__ float4 so[8][32];
+  __shared__ float2 sml[8];
+  grid_dependency_wait();
+  const int4 d = a.desc[blockIdx.x];
+  if (d.x < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kRowsPerBlock + warp / kWarps, w = warp % kWarps;
+  const KvSeq s = kv_seq(a.c, d.x);
+  const int rr = d.y * a.rows + row, t = rr / a.group, j = kv_first_q_head(a.c, d.z) + rr % a.group;
+  const bool live = row < a.rows && t < s.n && j < kv_first_q_head(a.c, d.z + 1);
+  float m = -__int_as_float(0x7f800000), l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (live) {
+    // parts: slot 2 c + 1 of the first CTA, slot 2 c of the others
+    const int parts = d.w - (int)blockIdx.x + 1;
+#pragma unroll 4
+    for (int i = w; i < parts; i += kWarps) {
+      const size_t at = (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * a.rows + row;
+      const float2 ml = a.ml[at];
+      const float4 x = reinterpret_cast<const float4*>(a.o + at * kHeadDim)[lane];
+      const float top = fmaxf(m, ml.x), ref = top == -__int_as_float(0x7f800000) ? 0.f : top;
+      const float f = exp2f(m - ref), g = exp2f(ml.x - ref);
+      l = l * f + ml.y * g;
+      o.x = o.x * f + x.x * g;
+      o.y = o.y * f + x.y * g;
+      o.z = o.z * f + x.z * g;
+      o.w = o.w * f + x.w * g;
+      m = top;
+    }
+  }
+  if (kWarps > 1) {
+    so[warp][lane] = o;
+    if (lane == 0) sml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (w != 0) return;
+    float top = m;
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) top = fmaxf(top, sml[warp + i].x);
+    const float ref = top == -__int_as_float(0x7f800000) ? 0.f : top;
+    const float f = exp2f(m - ref);
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int i = 1; i < kWarps; ++i) {
+      const float g = exp2f(sml[warp + i].x - ref);
+      const float4 x = so[warp + i][lane];
+      l += sml[warp + i].y * g;
+      o.x += x.x * g;
+      o.y += x.y * g;
+      o.z += x.z * g;
+      o.w += x.w * g;
+    }
+    m = top;
+  }
+  if (!live) return;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  T* dst = reinterpret_cast<T*>(a.out) + (int64_t)(s.tok0 + t) * a.out_stride + j * kHeadDim + 4 * lane;
+  store_elem(dst, o.x * inv);
+  store_elem(dst + 1, o.y * inv);
+  store_elem(dst + 2, o.z * inv);
+  store_elem(dst + 3, o.w * inv);
+  if (a.lse && lane == 0) a.lse[(int64_t)(s.tok0 + t) * a.c.h_q + j] = lse_of(m, l);
+}
+
+}  // namespace
+
+cudaError_t kv_simt_setup() {
+  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)sizeof(SimtSmem));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(attn_simt_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)sizeof(SimtSmem));
+}
+
+cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, bool f32, unsigned grid, cudaStream_t st) {
+  if (f32)
+    attn_simt_kernel<float><<<grid, kThreads, sizeof(SimtSmem), st>>>(a);
+  else
+    attn_simt_kernel<__nv_bfloat16><<<grid, kThreads, sizeof(SimtSmem), st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_combine(const KvAttnArgs& a, bool f32, cudaStream_t st) {
+  // up to 64 rows the parts are what there is to spread over warps
+  if (a.rows <= 64) {
+    const dim3 grid(a.n_ctas, a.rows);
+    return f32 ? launch_kernel(combine_kernel<float, 8>, grid, dim3(256), 0, st, true, a)
+               : launch_kernel(combine_kernel<__nv_bfloat16, 8>, grid, dim3(256), 0, st, true, a);
+  }
+  const dim3 grid(a.n_ctas, (a.rows + 7) / 8);
+  return f32 ? launch_kernel(combine_kernel<float, 1>, grid, dim3(256), 0, st, true, a)
+             : launch_kernel(combine_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, st, true, a);
+}
+
+}  // namespace gdn

@@ -362,6 +362,143 @@ gdn_status gdn_chunk_fwd_train(const void* q, const void* k, const void* v, cons
                                void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * ---- 8-bit key/value cache and attention over it ----
+ * What a model that mixes gated-delta-rule layers with softmax-attention
+ * layers keeps for the latter while it generates (no counterpart on the
+ * FlashQLA pages).
+ *
+ * The cache holds keys and values of d = 128 elements in pages of 64 tokens
+ * (GDN_KV_PAGE), as e4m3 codes c with one fp32 scale s per (page, key/value
+ * head) for the keys and one for the values: x = c s.  Scales are powers of
+ * two from 2^-40 to 2^40, so c s is exact in bf16 and fp32, and a scale that
+ * grows re-encodes earlier codes exactly unless they fall into e4m3's
+ * subnormal range.
+ *
+ * A batch: sequence i brings n_i tokens, packed over the batch by
+ * cu_seqlens_dev (int32 [n_seqs + 1]; NULL: T / n_seqs tokens each).  They
+ * are the last n_i of its kv_lens_dev[i] tokens: packed token t of sequence i
+ * has position p = kv_lens[i] - n_i + t.  Position p lives in row p % 64 of
+ * pool page page_table_dev[i * max_pages + p / 64].  kv_lens[i] < n_i is
+ * allowed (an idle slot of a captured decode batch has kv_lens[i] = 0):
+ * tokens at p < 0 are not stored, read as zeros, and attend to nothing under
+ * the causal mask.
+ *
+ * The lengths and the table are device data, so a captured call may be
+ * replayed while the caller advances them.  The kernels check them before
+ * following them: offsets that leave [0, T] or go back, a length outside
+ * [0, 64 max_pages], or a page outside [0, n_pages) is recorded as
+ * GDN_ERR_DEVICE_CHECK with detail 7 (offsets, length) or 8 (page) in
+ * cache->status and no access follows it outside the buffers; the outputs of
+ * that sequence are then undefined.  cache->status keeps the first failure
+ * until the caller zeroes it; read it with gdn_get_device_status(cache->status, ...).
+ */
+#define GDN_KV_PAGE 64
+
+typedef struct gdn_kv_cache {
+  void* k;          /* device, [n_pages, h_kv, 64, 128] e4m3 codes */
+  void* v;          /* device, the same */
+  float* k_scale;   /* device, [n_pages, h_kv] */
+  float* v_scale;   /* device, [n_pages, h_kv] */
+  int32_t* status;  /* device, int32[2] {code, detail}; zeroed by the caller at the start */
+  int n_pages;
+  int h_kv;
+  int d;            /* must be 128 */
+} gdn_kv_cache;
+
+typedef struct gdn_kv_dims {
+  int n_seqs;
+  int T;          /* tokens of the call, over all sequences */
+  int h_q;        /* query heads; query head j reads key/value head floor(j h_kv / h_q) */
+  int max_pages;  /* row length of page_table */
+  int causal;     /* attention: 1: keys at positions <= p; 0: all kv_lens keys */
+  int window;     /* attention: > 0: only keys at positions > p - window; 0: no bound */
+  float scale;    /* attention: score scale; 0 selects 1/sqrt(128) */
+  int dtype;      /* GDN_BF16 or GDN_F32: type of k, v, q and out */
+  int64_t q_stride;   /* elements from one token to the next in q, k, v and out; 0: */
+  int64_t k_stride;   /* heads * 128 (packed).  A multiple of 16 bytes and at least */
+  int64_t v_stride;   /* heads * 128, so k and v may be parts of one fused projection. */
+  int64_t out_stride;
+} gdn_kv_dims;
+
+/*
+ * gdn_kv_append -- quantises n_i new tokens of each sequence into the cache.
+ * Per (page, key/value head) that receives tokens, with r tokens of the
+ * sequence already in the page (positions before the new ones), a the largest
+ * finite |x| of the new ones, and s(a) the smallest power of two with
+ * a / s <= 448, held within [2^-40, 2^40] (s(0) = 2^-40):
+ *   s = s(a) if r = 0, else max(old scale, s(a));
+ *   earlier codes c <- e4m3(c s_old / s) if s > s_old; new codes e4m3(x / s),
+ * rounded to nearest even, saturating at 448.  Infinities and NaN are stored
+ * as e4m3's NaN and do not enter a.  Rows of a page after the last token are
+ * left as they are.  Asynchronous on `stream`; no workspace.
+ *   k, v : device, [T, h_kv, 128] with token strides dims->k_stride, v_stride.
+ * A page may receive tokens of one sequence only.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED (16 bytes), CUDA.
+ */
+gdn_status gdn_kv_append(const void* k, const void* v, const int32_t* kv_lens_dev, const int32_t* page_table_dev,
+                         const int32_t* cu_seqlens_dev, const gdn_kv_cache* cache, const gdn_kv_dims* dims,
+                         void* stream);
+
+/*
+ * gdn_kv_read -- the cache's values of the last n_i tokens of each sequence
+ * (n_i = kv_lens[i]: all of it), as bf16 or fp32: x = c s, exact.
+ *   k_out, v_out : device, [T, h_kv, 128], packed; dims->k_stride and
+ *                  v_stride apply to them.
+ * Errors: as gdn_kv_append.
+ */
+gdn_status gdn_kv_read(void* k_out, void* v_out, const int32_t* kv_lens_dev, const int32_t* page_table_dev,
+                       const int32_t* cu_seqlens_dev, const gdn_kv_cache* cache, const gdn_kv_dims* dims,
+                       void* stream);
+
+/* How gdn_kv_attn runs; plain data, fill with gdn_kv_attn_plan, do not edit. */
+typedef struct gdn_kv_plan_t {
+  int path;          /* which kernel: see gdn_kv_attn_plan */
+  int rows;          /* query rows (token, query head of one group) per row tile */
+  int max_row_tiles; /* row tiles of one sequence and key/value head, at most */
+  int n_ctas;        /* CTAs the key tiles of all row tiles are shared out to */
+  int n_seqs, T, h_q, h_kv, dtype; /* copied, checked by gdn_kv_attn */
+  int max_q_len;
+  size_t off_desc, off_ml, off_o;  /* workspace sections */
+  size_t workspace_bytes;
+} gdn_kv_plan_t;
+
+/*
+ * gdn_kv_attn_plan -- host-only planning of gdn_kv_attn.
+ *   max_q_len  : no sequence brings more tokens than this (<= 0: T).
+ *   max_kv_len : the longest sequence expected (<= 0: 64 max_pages); sizes the
+ *                split only, so replays of a captured call may pass it.
+ *   sm_count   : SMs to plan for; <= 0 queries the current device.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA (device query).
+ */
+gdn_status gdn_kv_attn_plan(const gdn_kv_dims* dims, int h_kv, int max_q_len, int max_kv_len, int sm_count,
+                            gdn_kv_plan_t* out_plan);
+
+/*
+ * gdn_kv_attn -- attention of each new token over its sequence's cached keys
+ * and values (the new tokens' own included: append them first).  For the
+ * token at position p and query head j, over the keys the masks leave:
+ *   w = softmax(scale q . k),  out = sum w v,  lse = log sum exp(scale q . k).
+ * A token whose masks leave no key has out = 0 and lse = -inf.  Keys outside
+ * the masks do not enter, whatever their codes; a NaN code among the attended
+ * keys, or a q that is not finite, gives NaN.
+ *   q    : device, [T, h_q, 128], dims->dtype, token stride dims->q_stride.
+ *   out  : device, [T, h_q, 128], dims->dtype, token stride dims->out_stride.
+ *   lse  : device, [T, h_q] fp32, or NULL.
+ *   dims, plan : host; the plan must come from gdn_kv_attn_plan with these dims.
+ *   workspace  : device, 256-byte aligned, >= plan->workspace_bytes; its
+ *                contents on entry do not matter.  Not to be shared by calls
+ *                that may run concurrently.
+ * GDN_BF16 runs on the tensor cores (keys and values enter the products
+ * exactly; the softmax and all sums are fp32), GDN_F32 in fp32 throughout on
+ * the CUDA cores.  Asynchronous on `stream`.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
+ */
+gdn_status gdn_kv_attn(const void* q, const int32_t* kv_lens_dev, const int32_t* page_table_dev,
+                       const int32_t* cu_seqlens_dev, const gdn_kv_cache* cache, void* out, float* lse,
+                       const gdn_kv_dims* dims, const gdn_kv_plan_t* plan, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
  * gdn_debug_stall_ns -- test hook of the failure path (no counterpart on the
  * FlashQLA pages).  While ns > 0, each later gdn_chunk_fwd of this process on
  * the bf16 path makes the blocks of its chunk-local kernel first wait ns

@@ -86,6 +86,7 @@ gdn_status device_setup(int* dev_out) {
   if ((e = f32_kernel_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = bwd_kernel_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = kv_simt_setup()) != cudaSuccess) return cuda_fail(e);
+  if ((e = kv_few_setup()) != cudaSuccess) return cuda_fail(e);
   int sms = 0;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_fail(e);
   g_sm_count[dev] = sms;
@@ -360,7 +361,26 @@ gdn_status kv_move(bool read, void* k, void* v, const int32_t* lens, const int32
   return e == cudaSuccess ? GDN_OK : cuda_fail(e);
 }
 
-constexpr int kKvPathSimt = 0;
+// A pool of codes as [page and head][64 tokens][128 bytes]: boxes of one page's
+// codes of one head, in the swizzled image the MMAs read.
+gdn_status encode_kv_map(CUtensorMap* m, void* base, const gdn_kv_cache* c) {
+  cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)kPage, (cuuint64_t)c->n_pages * c->h_kv};
+  cuuint64_t strides[2] = {(cuuint64_t)kHeadDim, (cuuint64_t)kPageBytes};
+  cuuint32_t box[3] = {(cuuint32_t)kHeadDim, (cuuint32_t)kPage, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    g_last_cuda_error = (int)r;
+    return GDN_ERR_CUDA;
+  }
+  return GDN_OK;
+}
+
+// Kernels of gdn_kv_attn.
+constexpr int kKvPathSimt = 0;  // fp32 on the CUDA cores
+constexpr int kKvPathFew = 1;   // bf16, up to 64 rows per (sequence, key/value head)
 
 }  // namespace
 
@@ -835,6 +855,12 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   p.path = kKvPathSimt;
   p.rows = 16;
   int per_sm = 2;
+  const int64_t rows = (int64_t)max_q_len * group;
+  if (d->dtype == GDN_BF16 && rows <= 64) {
+    p.path = kKvPathFew;
+    p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    per_sm = kv_few_ctas_per_sm(p.rows);
+  }
   p.max_row_tiles = std::max<int>(1, (int)(((int64_t)max_q_len * group + p.rows - 1) / p.rows));
   const int64_t items = (int64_t)d->n_seqs * p.max_row_tiles * h_kv;
   const int64_t tiles = std::max<int64_t>(1, (max_kv_len + kKvTile - 1) / kKvTile);
@@ -859,7 +885,7 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
                        const gdn_kv_plan_t* plan, void* workspace, size_t workspace_bytes, void* stream) {
   gdn_status st = check_kv(d, cache, lens, table, cu);
   if (st != GDN_OK) return st;
-  if (!plan || plan->n_seqs != d->n_seqs || plan->T != d->T || plan->h_q != d->h_q || plan->h_kv != cache->h_kv ||
+  if (!plan || plan->path < kKvPathSimt || plan->path > kKvPathFew || plan->n_seqs != d->n_seqs || plan->T != d->T || plan->h_q != d->h_q || plan->h_kv != cache->h_kv ||
       plan->dtype != d->dtype)
     return GDN_ERR_INVALID_ARG;
   if (d->causal != 0 && d->causal != 1) return GDN_ERR_UNSUPPORTED;
@@ -897,7 +923,16 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
   const bool f32 = d->dtype == GDN_F32;
   LaunchLog log;
   cudaError_t e = log.before(cs);
-  if (e == cudaSuccess) e = launch_kv_attn_simt(a, f32, grid, cs);
+  if (e == cudaSuccess) {
+    if (plan->path == kKvPathFew) {
+      CUtensorMap km, vm;
+      if ((st = encode_kv_map(&km, cache->k, cache)) != GDN_OK) return st;
+      if ((st = encode_kv_map(&vm, cache->v, cache)) != GDN_OK) return st;
+      e = launch_kv_attn_few(a, km, vm, grid, cs);
+    } else {
+      e = launch_kv_attn_simt(a, f32, grid, cs);
+    }
+  }
   if (e == cudaSuccess) e = log.after("kv_attn", cs);
   if (a.n_ctas) {
     if (e == cudaSuccess) e = log.before(cs);

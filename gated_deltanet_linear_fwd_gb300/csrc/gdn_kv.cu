@@ -23,16 +23,6 @@ constexpr int kChunks = kPage * kHeadDim / 8 / kThreads;  // 8-element chunks a 
 
 constexpr int kScaleMinExp = -40, kScaleMaxExp = 40;
 
-__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
-
-// The exponent of s(a) from a's fp32 bits (a finite, >= 0): a = m 2^x with
-// 1 <= m < 2, and 448 = 1.75 2^8, so it is x - 8, or x - 7 when m > 1.75.
-__device__ __forceinline__ int scale_exp(uint32_t a_bits) {
-  const int x = (int)(a_bits >> 23) - 127;
-  const int e = x - 8 + ((a_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return min(max(e, kScaleMinExp), kScaleMaxExp);
-}
-
 // 8 elements of a row as fp32.
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
@@ -193,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const KvAppendArgs a) 
   for (int w = 0; w < 2; ++w) {
     const float old_s = w ? old_v : old_k;
     uint8_t* codes = (w ? a.c.v : a.c.k) + head * kPageBytes;
-    float s = pow2f(scale_exp(top[w]));
+    float s = pow2f(min(e4m3_scale_exp(top[w], kScaleMinExp), kScaleMaxExp));
     if (lo > 0) s = fmaxf(s, old_s);
     const float inv = 1.0f / s;  // exact: a power of two
 #pragma unroll

@@ -238,17 +238,17 @@ struct KvCursor {
   KvItem it;
   int seq, rt, head;
   int off, len;       // units [off, off + len) of the item belong to the run
-  int64_t at, end;    // next unit, end of the run
+  int at, end;        // next unit and end, from the run's first unit
   __device__ __forceinline__ void start(const KvAttnArgs& a, const KvRun& r) {
     seq = r.seq;
     rt = r.rt;
     head = r.head;
     off = r.off;
-    at = r.begin;
-    end = r.end;
+    at = 0;
+    end = (int)(r.end - r.begin);
     if (at < end) {
       it = kv_item(a, seq, rt);
-      len = (int)min(end - at, (int64_t)(kv_units(it) - off));
+      len = min(end, kv_units(it) - off);
     }
   }
   __device__ __forceinline__ bool valid() const { return at < end; }
@@ -271,7 +271,7 @@ struct KvCursor {
         }
       }
     }
-    len = (int)min(end - at, (int64_t)kv_units(it));
+    len = min(end - at, kv_units(it));
   }
   // key tiles [tile_begin, tile_begin + tiles) of the run's part of the item
   __device__ __forceinline__ int tiles() const { return it.tiles == 0 ? 0 : len; }
@@ -283,8 +283,23 @@ struct KvCursor {
 // The last CTA that has a part of the item whose first part this cursor
 // stands on: CTA c owns unit u when c = floor(((u + 1) ctas - 1) / total).
 __device__ __forceinline__ int kv_last_cta(const KvRun& r, const KvCursor& c) {
-  const int64_t item_end = c.at + kv_units(c.it);
+  const int64_t item_end = r.begin + c.at + kv_units(c.it);
   return (int)((item_end * r.ctas - 1) / r.total);
+}
+
+// log sum exp from a running maximum (log2) and sum.
+__device__ __forceinline__ float kv_lse(float m, float l) {
+  return l == 0.f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * 0.693147180559945309f;
+}
+
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+// The exponent of the smallest power of two s with a / s <= 448, from a's
+// fp32 bits (a finite, >= 0): a = m 2^x with 1 <= m < 2 and 448 = 1.75 2^8,
+// so it is x - 8, or x - 7 when m > 1.75; not below `least`.
+__device__ __forceinline__ int e4m3_scale_exp(uint32_t a_bits, int least) {
+  const int x = (int)(a_bits >> 23) - 127;
+  return max(x - 8 + ((a_bits & 0x7fffffu) > 0x600000u ? 1 : 0), least);
 }
 
 // ---- launchers ----
@@ -293,5 +308,10 @@ cudaError_t launch_kv_read(const KvAppendArgs& a, bool f32, unsigned entries, cu
 cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, bool f32, unsigned grid, cudaStream_t st);
 cudaError_t launch_kv_combine(const KvAttnArgs& a, bool f32, cudaStream_t st);
 cudaError_t kv_simt_setup();
+// rows: 8, 16, 32 or 64 (KvAttnArgs::rows); kmap, vmap: the pools as [page and head][64][128 bytes]
+cudaError_t launch_kv_attn_few(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, unsigned grid,
+                               cudaStream_t st);
+cudaError_t kv_few_setup();
+int kv_few_ctas_per_sm(int rows);
 
 }  // namespace gdn

@@ -34,13 +34,6 @@ __device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bf
 __device__ __forceinline__ void store_elem(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_elem(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-constexpr float kLn2 = 0.693147180559945309f;
-
-// log sum exp from the running maximum (log2) and sum.
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l == 0.f ? -__int_as_float(0x7f800000) : (m + log2f(l)) * kLn2;
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const KvAttnArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -144,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const KvAttnArgs a)
         T* dst = reinterpret_cast<T*>(a.out) + (int64_t)(it.tok0 + t) * a.out_stride + j * kHeadDim + 8 * c;
 #pragma unroll
         for (int e = 0; e < 8; ++e) store_elem(dst + e, o[e] * inv);
-        if (a.lse && c == 0) a.lse[(int64_t)(it.tok0 + t) * a.c.h_q + j] = lse_of(m, l);
+        if (a.lse && c == 0) a.lse[(int64_t)(it.tok0 + t) * a.c.h_q + j] = kv_lse(m, l);
       }
     } else {
       const size_t row = (size_t)cur.slot() * kRows + r;
@@ -226,7 +219,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const KvAttnArgs a) {
   store_elem(dst + 1, o.y * inv);
   store_elem(dst + 2, o.z * inv);
   store_elem(dst + 3, o.w * inv);
-  if (a.lse && lane == 0) a.lse[(int64_t)(s.tok0 + t) * a.c.h_q + j] = lse_of(m, l);
+  if (a.lse && lane == 0) a.lse[(int64_t)(s.tok0 + t) * a.c.h_q + j] = kv_lse(m, l);
 }
 
 }  // namespace

@@ -87,6 +87,7 @@ gdn_status device_setup(int* dev_out) {
   if ((e = bwd_kernel_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = kv_simt_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = kv_few_setup()) != cudaSuccess) return cuda_fail(e);
+  if ((e = kv_many_setup()) != cudaSuccess) return cuda_fail(e);
   int sms = 0;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_fail(e);
   g_sm_count[dev] = sms;
@@ -381,6 +382,7 @@ gdn_status encode_kv_map(CUtensorMap* m, void* base, const gdn_kv_cache* c) {
 // Kernels of gdn_kv_attn.
 constexpr int kKvPathSimt = 0;  // fp32 on the CUDA cores
 constexpr int kKvPathFew = 1;   // bf16, up to 64 rows per (sequence, key/value head)
+constexpr int kKvPathMany = 2;  // bf16, more rows
 
 }  // namespace
 
@@ -860,6 +862,10 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
     p.path = kKvPathFew;
     p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     per_sm = kv_few_ctas_per_sm(p.rows);
+  } else if (d->dtype == GDN_BF16) {
+    p.path = kKvPathMany;
+    p.rows = 256;
+    per_sm = 1;
   }
   p.max_row_tiles = std::max<int>(1, (int)(((int64_t)max_q_len * group + p.rows - 1) / p.rows));
   const int64_t items = (int64_t)d->n_seqs * p.max_row_tiles * h_kv;
@@ -885,7 +891,7 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
                        const gdn_kv_plan_t* plan, void* workspace, size_t workspace_bytes, void* stream) {
   gdn_status st = check_kv(d, cache, lens, table, cu);
   if (st != GDN_OK) return st;
-  if (!plan || plan->path < kKvPathSimt || plan->path > kKvPathFew || plan->n_seqs != d->n_seqs || plan->T != d->T || plan->h_q != d->h_q || plan->h_kv != cache->h_kv ||
+  if (!plan || plan->path < kKvPathSimt || plan->path > kKvPathMany || plan->n_seqs != d->n_seqs || plan->T != d->T || plan->h_q != d->h_q || plan->h_kv != cache->h_kv ||
       plan->dtype != d->dtype)
     return GDN_ERR_INVALID_ARG;
   if (d->causal != 0 && d->causal != 1) return GDN_ERR_UNSUPPORTED;
@@ -924,11 +930,11 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
   LaunchLog log;
   cudaError_t e = log.before(cs);
   if (e == cudaSuccess) {
-    if (plan->path == kKvPathFew) {
+    if (plan->path != kKvPathSimt) {
       CUtensorMap km, vm;
       if ((st = encode_kv_map(&km, cache->k, cache)) != GDN_OK) return st;
       if ((st = encode_kv_map(&vm, cache->v, cache)) != GDN_OK) return st;
-      e = launch_kv_attn_few(a, km, vm, grid, cs);
+      e = plan->path == kKvPathFew ? launch_kv_attn_few(a, km, vm, grid, cs) : launch_kv_attn_many(a, km, vm, grid, cs);
     } else {
       e = launch_kv_attn_simt(a, f32, grid, cs);
     }

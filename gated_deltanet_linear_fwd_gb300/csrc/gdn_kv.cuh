@@ -313,5 +313,8 @@ cudaError_t launch_kv_attn_few(const KvAttnArgs& a, const CUtensorMap& kmap, con
                                cudaStream_t st);
 cudaError_t kv_few_setup();
 int kv_few_ctas_per_sm(int rows);
+cudaError_t launch_kv_attn_many(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, unsigned grid,
+                                cudaStream_t st);
+cudaError_t kv_many_setup();
 
 }  // namespace gdn

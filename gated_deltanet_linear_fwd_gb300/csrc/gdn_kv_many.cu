@@ -1,0 +1,614 @@
+// Attention over the 8-bit key/value cache for many query rows (prompts and
+// pieces of prompts): bound by the tensor cores, 4 x 128 operations a row and
+// key, with the exponentials next.
+//
+// A CTA takes 256 rows (token, query head of one group) as two tiles of 128
+// and walks the keys in tiles of 128 (two pages); each key tile serves both.
+//   S [128 rows, 128 keys] = Q K^T: e4m3 operands.  The keys' codes enter as
+//     they are; a bf16 query row, scaled by a power of two so that its largest
+//     magnitude is in (224, 448], is the sum of two e4m3 rows (four leading
+//     bits, then the remaining four, exact to 2^-17.8 of the row's largest).
+//     Both accumulate into one S: as many steps as one bf16 product.
+//   O [128 rows, 128 d] += P V: fp16 operands.  The values' codes are exact in
+//     fp16 and converted once per CTA by a warpgroup of their own; the weights
+//     P are rounded to fp16's 11 bits.
+// Converting only the values keeps the conversion (48 KB of shared-memory
+// traffic a tile) beside the products' own reads; splitting P into two e4m3
+// parts instead would cost the softmax warps four more instructions a weight.
+//
+// Softmax: a thread owns a row.  x_j = scale log2(e) q . k_j; the values' page
+// scale 2^e_v is folded into the exponent, P_j = 2^(x_j + e_v - m), so P times
+// the codes is the output in units of 2^m; the softmax's sum is of P_j 2^-e_v in
+// fp32.  m follows the running maximum of x + e_v only when that has grown by
+// more than 8, so O in tensor memory is rarely rescaled; P stays below 2^8.
+//
+// Tensor memory (512 columns): S of either tile (P over its second half) and O
+// of either tile.  The MMA thread alternates P V of one tile's previous keys
+// with Q K^T of its next, so one tile's softmax runs under the other's products.
+#include <cuda_fp16.h>
+
+#include "gdn_dev.cuh"
+#include "gdn_kv.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kRows = 256;
+constexpr int kThreads = 640;  // two softmax warpgroups, one converting values, one of TMA and MMA warps
+constexpr int kTmaWarp = 12, kMmaWarp = 13;
+constexpr int kSoftRegs = 144, kOtherRegs = 64;  // 256 x 144 + 384 x 64 = 640 x 96, the registers at launch
+constexpr int kTileBytes = kKvTile * kHeadDim;
+constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScaleRing = 8;
+
+constexpr uint32_t kOffQ = 0;                                  // tile, part (hi, lo): 16 KB each
+constexpr uint32_t kOffK = kOffQ + 4 * kTileBytes;
+constexpr uint32_t kOffV = kOffK + kKStages * kTileBytes;
+constexpr uint32_t kOffH = kOffV + kVStages * kTileBytes;      // fp16 values: two panels of 64 columns
+constexpr uint32_t kSmem = kOffH + kHStages * 2 * kTileBytes + 1024;
+
+constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for the second tile
+constexpr uint32_t kColP = 64;              // P (two weights a column) over the second half of S
+
+enum { kBarK = 1, kBarV, kBarKFree, kBarVFree, kBarQ, kBarS, kBarP, kBarO, kBarScale, kBarH, kBarHFree };
+
+struct ManyCtl {
+  uint64_t k_full[kKStages], k_free[kKStages], v_full[kVStages], v_free[kVStages], h_full[kHStages], h_free[kHStages];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], scale_full[kScaleRing];
+  float scale[kScaleRing][4];       // key scales of the tile's two pages, value scales
+  uint32_t nan_keys[kHStages][4];   // keys of a masked tile whose values hold a NaN code
+  KvRunScratch run;
+  uint32_t tmem;
+  int abort;
+};
+
+// What every role derives from an item.
+struct ManyItem {
+  int past;            // position of the first new token
+  int all_lo, all_hi;  // keys that every live row attends to
+  int q_tiles;         // 1 when the second tile has no rows
+};
+__device__ __forceinline__ ManyItem many_item(const KvAttnArgs& a, const KvCursor& c) {
+  ManyItem m;
+  const int r0 = c.rt * kRows, t0 = r0 / a.group, t1 = min(c.it.n - 1, (r0 + kRows - 1) / a.group);
+  m.past = c.it.len - c.it.n;
+  m.all_lo = a.window > 0 ? m.past + t1 - a.window + 1 : 0;
+  m.all_hi = a.causal ? min(m.past + t0 + 1, c.it.len) : c.it.len;
+  m.q_tiles = c.it.n * a.group - r0 > 128 ? 2 : 1;
+  return m;
+}
+
+// ---------------------------------------------------------------- TMA warp
+__device__ __forceinline__ void many_load(const KvAttnArgs& a, const KvRun& run, ManyCtl* ctl, uint8_t* sm,
+                                          const CUtensorMap* kmap, const CUtensorMap* vmap) {
+  const int lane = threadIdx.x & 31;
+  int i = 0;
+  KvCursor cur;
+  for (cur.start(a, run); cur.valid(); cur.next(a)) {
+    const int tiles = cur.tiles();
+    int page = -1, next_page = -1;
+    float sk = 1.f, sv = 1.f, next_sk = 1.f, next_sv = 1.f;
+    // 16 tiles' pages and scales at a time, one batch ahead: lane 2 i + j holds page j of tile i
+    auto fetch = [&](int b) {
+      const int slot = 2 * (cur.tile_begin() + 16 * b) + lane;
+      next_page = -1;
+      next_sk = next_sv = 1.f;
+      if (16 * b + (lane >> 1) < tiles && slot * kPage < cur.it.len) {
+        next_page = max(kv_page(a.c, cur.seq, slot), 0) * a.c.h_kv + cur.head;
+        next_sk = a.c.k_scale[next_page];
+        next_sv = a.c.v_scale[next_page];
+      }
+    };
+    fetch(0);
+    for (int b = 0; 16 * b < tiles; ++b) {
+      page = next_page;
+      sk = next_sk;
+      sv = next_sv;
+      fetch(b + 1);
+      const int n = min(16, tiles - 16 * b);
+      for (int j = 0; j < n; ++j, ++i) {
+        const int ks = i % kKStages, vs = i % kVStages;
+        const int p0 = __shfl_sync(0xffffffffu, page, 2 * j), p1 = __shfl_sync(0xffffffffu, page, 2 * j + 1);
+        // a tile's second page may lie past the sequence: its rows keep what they hold and are masked
+        const uint32_t bytes = p1 >= 0 ? kTileBytes : kTileBytes / 2;
+        if (!__all_sync(0xffffffffu, wait_phase(&ctl->k_free[ks], ((i / kKStages) & 1) ^ 1, &ctl->abort, 100 + kBarKFree))) return;
+        if ((lane >> 1) == j) {
+          float* s = ctl->scale[i % kScaleRing];
+          s[lane & 1] = sk;
+          s[2 + (lane & 1)] = sv;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctl->scale_full[i % kScaleRing]);
+          uint8_t* dst = sm + kOffK + ks * kTileBytes;
+          mbar_arrive_expect_tx(&ctl->k_full[ks], bytes);
+          tma_load_3d(dst, kmap, &ctl->k_full[ks], 0, 0, p0);
+          if (p1 >= 0) tma_load_3d(dst + kTileBytes / 2, kmap, &ctl->k_full[ks], 0, 0, p1);
+        }
+        if (!__all_sync(0xffffffffu, wait_phase(&ctl->v_free[vs], ((i / kVStages) & 1) ^ 1, &ctl->abort, 100 + kBarVFree))) return;
+        if (lane == 0) {
+          uint8_t* dst = sm + kOffV + vs * kTileBytes;
+          mbar_arrive_expect_tx(&ctl->v_full[vs], bytes);
+          tma_load_3d(dst, vmap, &ctl->v_full[vs], 0, 0, p0);
+          if (p1 >= 0) tma_load_3d(dst + kTileBytes / 2, vmap, &ctl->v_full[vs], 0, 0, p1);
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- MMA thread
+__device__ __forceinline__ void many_mma(const KvAttnArgs& a, const KvRun& run, ManyCtl* ctl, uint32_t sm,
+                                         uint32_t tmem) {
+  constexpr uint32_t kIdS = idesc_e4m3(128, 128, false, false), kIdO = idesc_f16(128, 128, false, true);
+  const uint64_t dq = sdesc_sw128(sm + kOffQ, 0, 1024), dk = sdesc_sw128(sm + kOffK, 0, 1024);
+  const uint64_t dh = sdesc_sw128(sm + kOffH, kTileBytes, 1024);
+  int i = 0, items = 0, items2 = 0;
+  int n[2] = {0, 0};  // tiles of keys that each query tile has seen
+  auto second = [&](int q, int t, bool first, bool last) {  // O of tile q += P V of key tile t
+    const int hs = t % kHStages;
+    if (!wait_phase(&ctl->p_full[q], (n[q] - 1) & 1, &ctl->abort, 100 + kBarP)) return false;
+    if (!wait_phase(&ctl->h_full[hs], (t / kHStages) & 1, &ctl->abort, 100 + kBarH)) return false;
+    tc_fence_after();
+    const uint32_t d = tmem + kColO + q * 128, p = tmem + kColS + kColP + q * 128;
+    const uint64_t h = dh + hs * (2 * kTileBytes >> 4);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mma_f16_ts(d, p + 8 * k, h + k * 128, kIdO, !first || k > 0);
+    mma_commit(&ctl->o_full[q]);
+    if (last) mma_commit(&ctl->h_free[hs]);
+    return true;
+  };
+  KvCursor cur;
+  for (cur.start(a, run); cur.valid(); cur.next(a)) {
+    const int tiles = cur.tiles();
+    if (tiles == 0) continue;
+    const int q_tiles = many_item(a, cur).q_tiles;
+    for (int j = 0; j < tiles; ++j, ++i) {
+      const int ks = i % kKStages;
+      for (int q = 0; q < q_tiles; ++q) {
+        if (j > 0 && !second(q, i - 1, j == 1, q == q_tiles - 1)) return;
+        if (j == 0 && !wait_phase(&ctl->q_full[q], (q ? items2 : items) & 1, &ctl->abort, 100 + kBarQ)) return;
+        if (q == 0 && !wait_phase(&ctl->k_full[ks], (i / kKStages) & 1, &ctl->abort, 100 + kBarK)) return;
+        tc_fence_after();
+        const uint32_t d = tmem + kColS + q * 128;
+        const uint64_t kk = dk + ks * (kTileBytes >> 4), qq = dq + q * (2 * kTileBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_f8(d, qq + k * 2, kk + k * 2, kIdS, k > 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_f8(d, qq + (kTileBytes >> 4) + k * 2, kk + k * 2, kIdS, 1);
+        mma_commit(&ctl->s_full[q]);
+        ++n[q];
+      }
+      mma_commit(&ctl->k_free[ks]);
+    }
+    for (int q = 0; q < q_tiles; ++q)
+      if (!second(q, i - 1, tiles == 1, q == q_tiles - 1)) return;
+    ++items;
+    if (q_tiles == 2) ++items2;
+  }
+}
+
+// ---------------------------------------------------------------- values to fp16
+// Thread = key of the tile.  Four codes to four fp16 by the hardware's exact
+// conversion; 16 codes are a 16-byte chunk of the e4m3 tile and two chunks of
+// a panel of the fp16 tile, both in the swizzled image (conflict-free).
+__device__ __forceinline__ void many_values(const KvAttnArgs& a, const KvRun& run, ManyCtl* ctl, uint8_t* sm) {
+  const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
+  int i = 0;
+  KvCursor cur;
+  for (cur.start(a, run); cur.valid(); cur.next(a)) {
+    const int tiles = cur.tiles();
+    if (tiles == 0) continue;
+    const ManyItem mi = many_item(a, cur);
+    for (int j = 0; j < tiles; ++j, ++i) {
+      const int vs = i % kVStages, hs = i % kHStages;
+      const int key0 = (cur.tile_begin() + j) * kKvTile, key = key0 + tid;
+      const bool masked = key0 < mi.all_lo || key0 + kKvTile > mi.all_hi;
+      bool ok = wait_phase(&ctl->v_full[vs], (i / kVStages) & 1, &ctl->abort, 100 + kBarV) &&
+                wait_phase(&ctl->h_free[hs], ((i / kHStages) & 1) ^ 1, &ctl->abort, 100 + kBarHFree);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      const uint8_t* v = sm + kOffV + vs * kTileBytes;
+      uint8_t* h = sm + kOffH + hs * 2 * kTileBytes;
+      uint4 w[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4*>(v + sw128_offset(tid, c));
+      mbar_arrive(&ctl->v_free[vs]);
+      if (masked) {
+        // Values no row may use must not meet a zero weight as NaN: a key past
+        // the sequence, or one that holds a NaN code, becomes zeros; the rows
+        // that do attend to the latter become NaN in the softmax.
+        uint32_t carry = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)  // b & 0x7f = 0x7f: adding 1 to the low seven bits carries into the eighth
+          carry |= ((w[c].x & 0x7f7f7f7fu) + 0x01010101u) | ((w[c].y & 0x7f7f7f7fu) + 0x01010101u) |
+                   ((w[c].z & 0x7f7f7f7fu) + 0x01010101u) | ((w[c].w & 0x7f7f7f7fu) + 0x01010101u);
+        const bool nan = (carry & 0x80808080u) != 0;
+        const uint32_t word = __ballot_sync(0xffffffffu, nan && key < cur.it.len);
+        if (lane == 0) ctl->nan_keys[hs][warp] = word;
+        if (nan || key >= cur.it.len) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) w[c] = make_uint4(0, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        uint32_t f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * e]) : "h"((uint16_t)u[e]));
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f[2 * e + 1]) : "h"((uint16_t)(u[e] >> 16)));
+        }
+        uint8_t* panel = h + (c >> 2) * kTileBytes;
+        *reinterpret_cast<uint4*>(panel + sw128_offset(tid, 2 * (c & 3))) = make_uint4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<uint4*>(panel + sw128_offset(tid, 2 * (c & 3) + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&ctl->h_full[hs]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- softmax warpgroups
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Waits for this thread's tensor-memory loads; the fence on 32 registers keeps
+// the compiler from using them before.
+__device__ __forceinline__ void tmem_ld_done(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (a0, a1) * (b, b) + (c, c) and (a0, a1) + (b0, b1) in one instruction each.
+__device__ __forceinline__ float2 fma2(float a0, float a1, float b, float c) {
+  uint64_t x, y, z, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(y) : "f"(b));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(z) : "f"(c));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float b0, float b1) {
+  uint64_t x, y, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b0), "f"(b1));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLazy = 8.f;
+
+// 64 scores of this thread's row; under the masks, -inf for keys outside them
+// and NaN for keys whose values hold one.
+__device__ __forceinline__ void tile_scores(const ManyCtl* ctl, uint32_t t_s, uint32_t (&s)[64], bool masked, int c0,
+                                            int lo, int hi, int stage) {
+  tmem_ld32(t_s, s);
+  tmem_ld32(t_s + 32, s + 32);
+  tmem_ld_done(s);
+  tmem_ld_done(s + 32);
+  if (masked) {
+    const uint32_t nan[2] = {ctl->nan_keys[stage][c0 >> 5], ctl->nan_keys[stage][(c0 >> 5) + 1]};
+#pragma unroll
+    for (int c = 0; c < 64; ++c) {
+      if ((nan[c >> 5] >> (c & 31)) & 1) s[c] = 0x7fffffffu;
+      if (c0 + c < lo || c0 + c >= hi) s[c] = 0xff800000u;
+    }
+  }
+}
+__device__ __forceinline__ float max64(const uint32_t (&s)[64]) {
+  float t[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) t[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[4 + e]));
+#pragma unroll
+  for (int c = 8; c < 64; c += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[e] = max3(t[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+// Weights 2^(s f + bias) to tensor memory as fp16 pairs; returns their sum.
+__device__ __forceinline__ float weights64(uint32_t t_p, const uint32_t (&s)[64], float f, float bias) {
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int at = 32 * c + 2 * e;
+      const float2 x = fma2(__uint_as_float(s[at]), __uint_as_float(s[at + 1]), f, bias);
+      const float p0 = ex2(x.x), p1 = ex2(x.y);
+      sum = add2(sum, p0, p1);
+      w[e] = pack_f16x2(p0, p1);
+    }
+    tmem_st16(t_p + 16 * c, w);
+  }
+  return sum.x + sum.y;
+}
+
+// The item's query rows of tile q into their two e4m3 parts; a warp takes
+// every fourth row, a lane four columns.  Returns, to the thread that owns the
+// row, its score factor.
+__device__ __forceinline__ float many_queries(const KvAttnArgs& a, const KvCursor& cur, int q, uint8_t* sm) {
+  const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
+  const int head0 = kv_first_q_head(a.c, cur.head), group = kv_first_q_head(a.c, cur.head + 1) - head0;
+  const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;  // the row's factor stays positive
+  uint8_t* hi_tile = sm + kOffQ + q * 2 * kTileBytes;
+  float f = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < 32; ++k) {
+    const int r = 32 * warp + k, rr = cur.rt * kRows + q * 128 + r, t = rr / a.group, g = rr % a.group;
+    uint2 w = make_uint2(0, 0);
+    if (t < cur.it.n && g < group)
+      w = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                          (int64_t)(cur.it.tok0 + t) * a.q_stride + (head0 + g) * kHeadDim + 4 * lane);
+    float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                  __uint_as_float(w.y & 0xffff0000u)};
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
+    m = __reduce_max_sync(0xffffffffu, m);
+    // below 2^-102 a row's scores are zero for any key the cache can hold
+    const int ex = m < 0x7f800000u ? e4m3_scale_exp(m, -110) : 0;
+    const float inv = pow2f(-ex) * sign;
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float y0 = x[2 * e] * inv, y1 = x[2 * e + 1] * inv;
+      hi[e] = f32x2_to_e4m3x2(y0, y1);
+      const float2 h = e4m3x2_to_f32x2(hi[e]);
+      lo[e] = f32x2_to_e4m3x2(y0 - h.x, y1 - h.y);
+    }
+    const uint32_t at = sw128_offset(r, lane >> 2) + 4 * (lane & 3);
+    *reinterpret_cast<uint32_t*>(hi_tile + at) = hi[0] | hi[1] << 16;
+    *reinterpret_cast<uint32_t*>(hi_tile + kTileBytes + at) = lo[0] | lo[1] << 16;
+    // a row that is not finite gives NaN
+    if (lane == k) f = m < 0x7f800000u ? pow2f(ex) * fabsf(a.scale_log2) : __int_as_float(0x7fffffff);
+  }
+  return f;
+}
+
+__device__ __forceinline__ void many_softmax(const KvAttnArgs& a, const KvRun& run, ManyCtl* ctl, uint8_t* sm,
+                                             uint32_t tmem) {
+  const int q = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5;
+  const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+  const uint32_t t_s = tmem + lane_base + kColS + q * 128, t_o = tmem + lane_base + kColO + q * 128, t_p = t_s + kColP;
+  int i = 0, n = 0;  // key tiles of the run, and those this query tile took part in
+  KvCursor cur;
+  for (cur.start(a, run); cur.valid(); cur.next(a)) {
+    const KvItem& it = cur.it;
+    const int tiles = cur.tiles();
+    const ManyItem mi = many_item(a, cur);
+    if (q >= mi.q_tiles) {
+      i += tiles;
+      continue;
+    }
+    const int head0 = kv_first_q_head(a.c, cur.head), group = kv_first_q_head(a.c, cur.head + 1) - head0;
+    const int rr = cur.rt * kRows + q * 128 + tid, t = rr / a.group, g = rr % a.group, p = mi.past + t;
+    const bool live = t < it.n && g < group;
+    const int key_lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+    const int key_hi = live ? (a.causal ? min(max(p + 1, 0), it.len) : it.len) : 0;
+    float f = 0.f, m = kNegInf, l = 0.f;
+    if (tiles > 0) {
+      f = many_queries(a, cur, q, sm);
+      fence_proxy_async_smem();
+      mbar_arrive(&ctl->q_full[q]);
+    }
+    for (int j = 0; j < tiles; ++j, ++i, ++n) {
+      const int key0 = (cur.tile_begin() + j) * kKvTile;
+      const bool masked = key0 < mi.all_lo || key0 + kKvTile > mi.all_hi;
+      bool ok = wait_phase(&ctl->scale_full[i % kScaleRing], (i / kScaleRing) & 1, &ctl->abort, 100 + kBarScale) &&
+                wait_phase(&ctl->s_full[q], n & 1, &ctl->abort, 100 + kBarS);
+      if (masked) ok = ok && wait_phase(&ctl->h_full[i % kHStages], (i / kHStages) & 1, &ctl->abort, 100 + kBarH);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      tc_fence_after();
+      const float* sc = ctl->scale[i % kScaleRing];
+      const float4 sc4 = *reinterpret_cast<const float4*>(sc);
+      // log2 and inverse of the value scales, powers of two
+      const float ev[2] = {(float)((int)(__float_as_uint(sc4.z) >> 23) - 127), (float)((int)(__float_as_uint(sc4.w) >> 23) - 127)};
+      const float inv_sv[2] = {__int_as_float((254 << 23) - __float_as_int(sc4.z)), __int_as_float((254 << 23) - __float_as_int(sc4.w))};
+      const float fk[2] = {f * sc4.x, f * sc4.y};
+      // The two pages in turn: the first one's scores are read again after the
+      // maximum is known, the second one's stay in registers.
+      uint32_t s[64];
+      float top = kNegInf;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        tile_scores(ctl, t_s + 64 * h, s, masked, 64 * h, key_lo - key0, key_hi - key0, i % kHStages);
+        top = fmaxf(top, fmaf(max64(s), fk[h], ev[h]));
+      }
+      // -inf * 0 (a row of zeros) is NaN: such a key is masked and must stay out
+      const bool grow = top > m + kLazy || (m == kNegInf && top > kNegInf);
+      if (__any_sync(0xffffffffu, grow)) {
+        const float alpha = grow ? ex2(m - top) : 1.f;
+        if (j > 0) {
+          // O holds the tiles before this one: wait for the last of them, then rescale
+          ok = wait_phase(&ctl->o_full[q], (n - 1) & 1, &ctl->abort, 100 + kBarO);
+          if (!__all_sync(0xffffffffu, ok)) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[16], o2[16];
+            tmem_ld16(t_o + 32 * c, o);
+            tmem_ld16(t_o + 32 * c + 16, o2);
+            tmem_ld_wait(o, o2);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              o2[e] = __float_as_uint(__uint_as_float(o2[e]) * alpha);
+            }
+            tmem_st16(t_o + 32 * c, o);
+            tmem_st16(t_o + 32 * c + 16, o2);
+          }
+        }
+        if (grow) {
+          l *= alpha;
+          m = top;
+        }
+      }
+      const float ref = m == kNegInf ? 0.f : m;
+      l = fmaf(weights64(t_p + 32, s, fk[1], ev[1] - ref), inv_sv[1], l);
+      tile_scores(ctl, t_s, s, masked, 0, key_lo - key0, key_hi - key0, i % kHStages);
+      l = fmaf(weights64(t_p, s, fk[0], ev[0] - ref), inv_sv[0], l);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&ctl->p_full[q]);
+    }
+    // ---- the row's output ----
+    const int64_t tok = it.tok0 + t;
+    const size_t part = (size_t)cur.slot() * kRows + q * 128 + tid;
+    const bool whole = cur.whole();
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + (head0 + g) * kHeadDim;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    if (tiles > 0) {
+      const bool ok = wait_phase(&ctl->o_full[q], (n - 1) & 1, &ctl->abort, 100 + kBarO);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      tc_fence_after();
+    }
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      if (tiles > 0) {
+        tmem_ld32(t_o + 32 * c, o);
+        tmem_ld_done(o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+      }
+      if (whole) {
+        if (live) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+            reinterpret_cast<uint4*>(dst + 32 * c)[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          reinterpret_cast<uint4*>(a.o + part * kHeadDim + 32 * c)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+      }
+    }
+    tc_fence_before();
+    if (whole) {
+      if (live && a.lse) a.lse[tok * a.c.h_q + head0 + g] = kv_lse(m, l);
+    } else {
+      a.ml[part] = make_float2(m, l);
+      if (threadIdx.x == 0 && cur.off == 0)
+        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(run, cur));
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_many_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const __grid_constant__ KvAttnArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  __shared__ ManyCtl ctl;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&ctl.k_full[s], 1);
+      mbar_init(&ctl.k_free[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&ctl.v_full[s], 1);
+      mbar_init(&ctl.v_free[s], 128);
+      mbar_init(&ctl.h_full[s], 128);
+      mbar_init(&ctl.h_free[s], 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(&ctl.q_full[q], 128);
+      mbar_init(&ctl.s_full[q], 1);
+      mbar_init(&ctl.p_full[q], 128);
+      mbar_init(&ctl.o_full[q], 1);
+    }
+    for (int s = 0; s < kScaleRing; ++s) mbar_init(&ctl.scale_full[s], 1);
+    fence_mbar_init();
+    ctl.abort = 0;
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+    if (a.n_ctas) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  }
+  if (warp == kTmaWarp) {
+    tmem_alloc(&ctl.tmem, 512);
+    tmem_relinquish();
+  }
+  const KvRun run = kv_run<kThreads>(a, &ctl.run);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  if (warp < 8) {
+    setmaxnreg_inc<kSoftRegs>();
+    many_softmax(a, run, &ctl, sm, tmem);
+  } else {
+    setmaxnreg_dec<kOtherRegs>();
+    if (warp < 12) {
+      many_values(a, run, &ctl, sm);
+    } else if (warp == kTmaWarp) {
+      many_load(a, run, &ctl, sm, &kmap, &vmap);
+    } else if (warp == kMmaWarp && (tid & 31) == 0) {
+      many_mma(a, run, &ctl, smem_u32(sm), tmem);
+    }
+  }
+  __syncwarp();
+  grid_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  if (ctl.abort) {
+    if (tid == 0) report(a.c.status, kDevTimeout, ctl.abort);
+    // let copies and MMAs already in flight land before the memory is released
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 2000000ull) {
+    }
+  }
+  __syncthreads();
+  if (warp == kTmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t kv_many_setup() {
+  return cudaFuncSetAttribute(attn_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+}
+
+cudaError_t launch_kv_attn_many(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, unsigned grid,
+                                cudaStream_t st) {
+  return launch_kernel(attn_many_kernel, dim3(grid), dim3(kThreads), kSmem, st, false, kmap, vmap, a);
+}
+
+}  // namespace gdn

@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 
 #include "gdn_internal.cuh"
+#include "sm103_ptx.cuh"
 
 namespace gdn {
 
@@ -92,7 +93,7 @@ __device__ __forceinline__ int kv_page(const KvArgs& a, int s, int slot) {
 
 // Query heads of key/value head h: those j with floor(j h_kv / h_q) = h.
 __device__ __forceinline__ int kv_first_q_head(const KvArgs& a, int h) {
-  return (int)(((int64_t)h * a.h_q + a.h_kv - 1) / a.h_kv);
+  return (int)(((unsigned)h * (unsigned)a.h_q + (unsigned)a.h_kv - 1u) / (unsigned)a.h_kv);  // heads are at most 65535
 }
 
 // ---- e4m3 ----
@@ -155,7 +156,7 @@ struct KvRun {
 };
 
 // A CTA's run, found by all its threads (NT of them, a multiple of 32) from
-// the lengths; `scratch` is shared memory.
+// the lengths and left in shared memory.
 struct KvRunScratch {
   int64_t part[32];
   KvRun run;
@@ -182,55 +183,58 @@ __device__ __forceinline__ int64_t block_inclusive_scan(int64_t v, KvRunScratch*
   return v + before;
 }
 template <int NT>
-__device__ __forceinline__ KvRun kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
+__device__ __noinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
   const int tid = threadIdx.x;
-  const int64_t entries = (int64_t)a.c.n_seqs * a.max_row_tiles;
+  const int entries = a.c.n_seqs * a.max_row_tiles;
   if (a.n_ctas == 0) {  // one whole item a CTA
-    KvRun r;
-    r.head = blockIdx.x % a.c.h_kv;
-    const int e = blockIdx.x / a.c.h_kv;
-    r.seq = e / a.max_row_tiles;
-    r.rt = e % a.max_row_tiles;
-    r.off = 0;
-    r.begin = 0;
-    r.end = r.total = kv_units(kv_item(a, r.seq, r.rt));
-    r.ctas = 0;
-    return r;
+    if (tid == 0) {
+      KvRun r;
+      r.head = blockIdx.x % a.c.h_kv;
+      const int e = blockIdx.x / a.c.h_kv;
+      r.seq = e / a.max_row_tiles;
+      r.rt = e % a.max_row_tiles;
+      r.off = 0;
+      r.begin = 0;
+      r.end = r.total = kv_units(kv_item(a, r.seq, r.rt));
+      r.ctas = 0;
+      sc->run = r;
+    }
+    __syncthreads();
+    return;
   }
   int64_t sum = 0;
-  for (int64_t e = tid; e < entries; e += NT)
-    sum += kv_units(kv_item(a, (int)(e / a.max_row_tiles), (int)(e % a.max_row_tiles)));
+#pragma unroll 1
+  for (int e = tid; e < entries; e += NT) sum += kv_units(kv_item(a, e / a.max_row_tiles, e % a.max_row_tiles));
   int64_t total;
   block_inclusive_scan<NT>(sum, sc, total);
   total *= a.c.h_kv;
   const int ctas = (int)min((int64_t)a.n_ctas, total);
   const int64_t begin = (int)blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
   const int64_t end = (int)blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
+  if (tid == 0) {
+    sc->run.begin = begin;
+    sc->run.end = end;
+    sc->run.total = total;
+    sc->run.ctas = ctas;
+  }
   int64_t base = 0;
-  for (int64_t e0 = 0; e0 < entries && base <= begin && begin < end; e0 += NT) {
-    const int64_t e = e0 + tid;
-    const int u = e < entries ? kv_units(kv_item(a, (int)(e / a.max_row_tiles), (int)(e % a.max_row_tiles))) : 0;
+#pragma unroll 1
+  for (int e0 = 0; e0 < entries && base <= begin && begin < end; e0 += NT) {
+    const int e = e0 + tid, seq = e / a.max_row_tiles, rt = e % a.max_row_tiles;
+    const int u = e < entries ? kv_units(kv_item(a, seq, rt)) : 0;
     int64_t sub;
     const int64_t incl = base + block_inclusive_scan<NT>((int64_t)u * a.c.h_kv, sc, sub);
     const int64_t excl = incl - (int64_t)u * a.c.h_kv;
     if (excl <= begin && begin < incl) {
-      const int64_t in = begin - excl;
-      KvRun r;
-      r.seq = (int)(e / a.max_row_tiles);
-      r.rt = (int)(e % a.max_row_tiles);
-      r.head = (int)(in / u);
-      r.off = (int)(in % u);
-      sc->run = r;
+      const int in = (int)(begin - excl);  // units of one row tile over all heads fit 32 bits
+      sc->run.seq = seq;
+      sc->run.rt = rt;
+      sc->run.head = in / u;
+      sc->run.off = in % u;
     }
     base += sub;
   }
   __syncthreads();
-  KvRun r = sc->run;
-  r.begin = begin;
-  r.end = end;
-  r.total = total;
-  r.ctas = ctas;
-  return r;
 }
 
 // Walks the items of a run; every warp that needs it walks its own.
@@ -285,6 +289,33 @@ struct KvCursor {
 __device__ __forceinline__ int kv_last_cta(const KvRun& r, const KvCursor& c) {
   const int64_t item_end = r.begin + c.at + kv_units(c.it);
   return (int)((item_end * r.ctas - 1) / r.total);
+}
+
+// Bounded wait on an mbarrier phase: gives up (false) after kWaitTries tries,
+// recording `code` in *abort, or when another role has.  A try that fails
+// suspends the thread for about 4 us (measured), so the limit is about a
+// second.  Counting tries keeps the loop a few instructions: with the
+// nanosecond clock in it the waits of the many-rows kernel, all of them
+// complete or nearly so, took 700 cycles each, twice the kernel's time.
+constexpr int kWaitTries = 1 << 18;
+__device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, int* abort, int code) {
+#pragma unroll 1
+  for (int i = 0; i < kWaitTries; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(abort)) return false;
+  }
+  *reinterpret_cast<volatile int*>(abort) = code;
+  return false;
+}
+// The same by all lanes of a converged warp, which then agree.
+template <typename W>
+__device__ __forceinline__ bool kv_wait_warp(W wait) {
+  return __all_sync(0xffffffffu, wait());
+}
+// One arrival for a converged warp's work before it.
+__device__ __forceinline__ void kv_arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // log sum exp from a running maximum (log2) and sum.

@@ -72,7 +72,7 @@ struct FewCtl {
 
 // ---------------------------------------------------------------- TMA warp
 template <int NR>
-__device__ __forceinline__ void few_load(const KvAttnArgs& a, const KvRun& run, FewCtl<NR>* ctl, uint8_t* sm,
+__device__ __forceinline__ void few_load(const KvAttnArgs& a, FewCtl<NR>* ctl, uint8_t* sm,
                                          const CUtensorMap* kmap, const CUtensorMap* vmap) {
   using F = Few<NR>;
   const int lane = threadIdx.x & 31;
@@ -90,13 +90,15 @@ __device__ __forceinline__ void few_load(const KvAttnArgs& a, const KvRun& run, 
       sv = a.c.v_scale[page];
     }
   };
-  ahead.start(a, run);
+  ahead.start(a, ctl->run.run);
   while (ahead.valid() && ahead.tiles() == 0) ahead.next(a);
   fetch();
   int i = 0;  // tile of the run
   KvCursor cur;
-  for (cur.start(a, run); cur.valid(); cur.next(a)) {
+#pragma unroll 1
+  for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
     const int tiles = cur.tiles();
+#pragma unroll 1
     for (int b = 0; 16 * b < tiles; ++b) {
       const int my_page = page;
       const float my_sk = sk, my_sv = sv;
@@ -107,11 +109,12 @@ __device__ __forceinline__ void few_load(const KvAttnArgs& a, const KvRun& run, 
       }
       fetch();
       const int n = min(16, tiles - 16 * b);
+#pragma unroll 1
       for (int j = 0; j < n; ++j, ++i) {
         const int stage = i % F::kStages;
         const uint32_t parity = (i / F::kStages) & 1;
         const int p0 = __shfl_sync(0xffffffffu, my_page, 2 * j), p1 = __shfl_sync(0xffffffffu, my_page, 2 * j + 1);
-        if (!__all_sync(0xffffffffu, wait_phase(&ctl->k_free[stage], parity ^ 1, &ctl->abort, 100 + kBarKFree))) return;
+        if (!kv_wait_warp([&] { return kv_wait(&ctl->k_free[stage], parity ^ 1, &ctl->abort, 100 + kBarKFree); })) return;
         if ((lane >> 1) == j) {
           float* s = ctl->scale[i % kScaleRing];
           s[lane & 1] = my_page >= 0 ? my_sk : 1.f;
@@ -127,7 +130,7 @@ __device__ __forceinline__ void few_load(const KvAttnArgs& a, const KvRun& run, 
           tma_load_3d(dst, kmap, &ctl->k_full[stage], 0, 0, p0);
           if (p1 >= 0) tma_load_3d(dst + kTileBytes / 2, kmap, &ctl->k_full[stage], 0, 0, p1);
         }
-        if (!__all_sync(0xffffffffu, wait_phase(&ctl->v_free[stage], parity ^ 1, &ctl->abort, 100 + kBarVFree))) return;
+        if (!kv_wait_warp([&] { return kv_wait(&ctl->v_free[stage], parity ^ 1, &ctl->abort, 100 + kBarVFree); })) return;
         if (lane == 0) {
           const uint32_t bytes = p1 >= 0 ? kTileBytes : kTileBytes / 2;
           uint8_t* dst = sm + F::kOffV + stage * kTileBytes;
@@ -142,7 +145,7 @@ __device__ __forceinline__ void few_load(const KvAttnArgs& a, const KvRun& run, 
 
 // ---------------------------------------------------------------- MMA thread
 template <int NR>
-__device__ __forceinline__ void few_mma(const KvAttnArgs& a, const KvRun& run, FewCtl<NR>* ctl, uint32_t sm,
+__device__ __forceinline__ void few_mma(const KvAttnArgs& a, FewCtl<NR>* ctl, uint32_t sm,
                                         uint32_t tmem) {
   using F = Few<NR>;
   constexpr uint32_t kIdS = idesc_e4m3(128, F::kN, false, false), kIdO = idesc_e4m3(128, F::kN, true, true);
@@ -153,8 +156,8 @@ __device__ __forceinline__ void few_mma(const KvAttnArgs& a, const KvRun& run, F
   // O^T of tile t, once its weights are in shared memory
   auto second = [&](int t) {
     const int stage = t % F::kStages, buf = t & 1;
-    if (!wait_phase(&ctl->p_full[buf], (t >> 1) & 1, &ctl->abort, 100 + kBarP)) return false;
-    if (!wait_phase(&ctl->v_full[stage], (t / F::kStages) & 1, &ctl->abort, 100 + kBarV)) return false;
+    if (!kv_wait(&ctl->p_full[buf], (t >> 1) & 1, &ctl->abort, 100 + kBarP)) return false;
+    if (!kv_wait(&ctl->v_full[stage], (t / F::kStages) & 1, &ctl->abort, 100 + kBarV)) return false;
     tc_fence_after();
     const uint32_t d = tmem + (2 + buf) * F::kN;
     const uint64_t v = dv + stage * (kTileBytes >> 4), p = dp + buf * (F::kN * kKvTile >> 4);
@@ -165,16 +168,18 @@ __device__ __forceinline__ void few_mma(const KvAttnArgs& a, const KvRun& run, F
     return true;
   };
   KvCursor cur;
-  for (cur.start(a, run); cur.valid(); cur.next(a)) {
+#pragma unroll 1
+  for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
     const int tiles = cur.tiles();
+#pragma unroll 1
     for (int j = 0; j < tiles; ++j, ++i) {
       const int stage = i % F::kStages, buf = i & 1;
       // A new item's queries arrive only after the last tile's softmax: finish that tile first.
       if (j == 0) {
         if (i > 0 && !second(i - 1)) return;
-        if (!wait_phase(&ctl->q_full, items++ & 1, &ctl->abort, 100 + kBarQ)) return;
+        if (!kv_wait(&ctl->q_full, items++ & 1, &ctl->abort, 100 + kBarQ)) return;
       }
-      if (!wait_phase(&ctl->k_full[stage], (i / F::kStages) & 1, &ctl->abort, 100 + kBarK)) return;
+      if (!kv_wait(&ctl->k_full[stage], (i / F::kStages) & 1, &ctl->abort, 100 + kBarK)) return;
       tc_fence_after();
       const uint32_t d = tmem + buf * F::kN;
       const uint64_t kk = dk + stage * (kTileBytes >> 4);
@@ -216,7 +221,7 @@ __device__ __forceinline__ float warp_max(float x) {
 constexpr float kNegInf = -__builtin_huge_valf();
 
 template <int NR>
-__device__ __forceinline__ void few_softmax(const KvAttnArgs& a, const KvRun& run, FewCtl<NR>* ctl, uint8_t* sm,
+__device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl, uint8_t* sm,
                                             uint32_t tmem) {
   using F = Few<NR>;
   constexpr int R = F::kRowsWg;
@@ -226,7 +231,8 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, const KvRun& ru
   bool bad = false;
   int i = 0;  // tile of the run
   KvCursor cur;
-  for (cur.start(a, run); cur.valid(); cur.next(a)) {
+#pragma unroll 1
+  for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
     const KvItem& it = cur.it;
     const int past = it.len - it.n, head0 = kv_first_q_head(a.c, cur.head);
     const int group = kv_first_q_head(a.c, cur.head + 1) - head0;
@@ -270,7 +276,7 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, const KvRun& ru
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&ctl->q_full);
+      kv_arrive_warp(&ctl->q_full);
       named_bar_sync(1, F::kSoft);
     }
     // tiles that lie within every live row's keys need no mask
@@ -283,18 +289,19 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, const KvRun& ru
       l[r] = 0.f;
       o[r] = 0.f;
     }
+#pragma unroll 1
     for (int j = 0; j < tiles; ++j, ++i) {
       const int buf = i & 1, key0 = (cur.tile_begin() + j) * kKvTile, key = key0 + tid;
       float x[R];
       float ev = 0.f, inv_sv = 1.f;
-      bool ok = wait_phase(&ctl->scale_full[i % kScaleRing], (i / kScaleRing) & 1, &ctl->abort, 100 + kBarScale) &&
-                wait_phase(&ctl->s_full[buf], (i >> 1) & 1, &ctl->abort, 100 + kBarS);
-      bad |= !__all_sync(0xffffffffu, ok);
+      bad |= !kv_wait_warp([&] {
+        return kv_wait(&ctl->scale_full[i % kScaleRing], (i / kScaleRing) & 1, &ctl->abort, 100 + kBarScale) &&
+               kv_wait(&ctl->s_full[buf], (i >> 1) & 1, &ctl->abort, 100 + kBarS);
+      });
       const bool masked = key0 < all_lo || key0 + kKvTile > all_hi;
       if (masked && !bad) {
         const int stage = i % F::kStages;
-        ok = wait_phase(&ctl->v_full[stage], (i / F::kStages) & 1, &ctl->abort, 100 + kBarV);
-        bad |= !__all_sync(0xffffffffu, ok);
+        bad |= !kv_wait_warp([&] { return kv_wait(&ctl->v_full[stage], (i / F::kStages) & 1, &ctl->abort, 100 + kBarV); });
       }
       if (!bad) {
         tc_fence_after();
@@ -385,11 +392,10 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, const KvRun& ru
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(&ctl->p_full[buf]);
+      kv_arrive_warp(&ctl->p_full[buf]);
       // the tile before: its O^T is in units of 2^(m before this tile)
       if (j > 0) {
-        ok = wait_phase(&ctl->o_full[buf ^ 1], ((i - 1) >> 1) & 1, &ctl->abort, 100 + kBarO);
-        bad |= !__all_sync(0xffffffffu, ok);
+        bad |= !kv_wait_warp([&] { return kv_wait(&ctl->o_full[buf ^ 1], ((i - 1) >> 1) & 1, &ctl->abort, 100 + kBarO); });
         if (!bad) {
           tc_fence_after();
           uint32_t h[16], q[16];
@@ -408,8 +414,7 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, const KvRun& ru
     }
     if (tiles > 0) {
       const int buf = (i - 1) & 1;
-      const bool ok = wait_phase(&ctl->o_full[buf], ((i - 1) >> 1) & 1, &ctl->abort, 100 + kBarO);
-      bad |= !__all_sync(0xffffffffu, ok);
+      bad |= !kv_wait_warp([&] { return kv_wait(&ctl->o_full[buf], ((i - 1) >> 1) & 1, &ctl->abort, 100 + kBarO); });
       if (!bad) {
         tc_fence_after();
         uint32_t h[16], q[16];
@@ -458,7 +463,7 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, const KvRun& ru
         if (tid == r) a.ml[row + r] = make_float2(m[r] - 8.f, l[r]);
       }
       if (threadIdx.x == 0 && cur.off == 0)
-        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(run, cur));
+        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(ctl->run.run, cur));
     }
     if (tiles > 0) named_bar_sync(1, F::kSoft);  // the sums are read before the next item's are written
   }
@@ -480,10 +485,10 @@ __global__ void __launch_bounds__(Few<NR>::kThreads, Few<NR>::kCtasPerSm)
       mbar_init(&ctl.v_full[s], 1);
       mbar_init(&ctl.v_free[s], 1);
     }
-    mbar_init(&ctl.q_full, F::kSoft);
+    mbar_init(&ctl.q_full, F::kSoft / 32);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl.s_full[b], 1);
-      mbar_init(&ctl.p_full[b], F::kSoft);
+      mbar_init(&ctl.p_full[b], F::kSoft / 32);
       mbar_init(&ctl.o_full[b], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&ctl.scale_full[s], 1);
@@ -497,17 +502,17 @@ __global__ void __launch_bounds__(Few<NR>::kThreads, Few<NR>::kCtasPerSm)
     tmem_alloc(&ctl.tmem, F::kTmemCols);
     tmem_relinquish();
   }
-  const KvRun run = kv_run<F::kThreads>(a, &ctl.run);
+  kv_run<F::kThreads>(a, &ctl.run);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
   if (warp < F::kSoft / 32) {
-    few_softmax<NR>(a, run, &ctl, sm, tmem);
+    few_softmax<NR>(a, &ctl, sm, tmem);
   } else if (warp == F::kSoft / 32) {
-    few_load<NR>(a, run, &ctl, sm, &kmap, &vmap);
+    few_load<NR>(a, &ctl, sm, &kmap, &vmap);
   } else if ((tid & 31) == 0) {
-    few_mma<NR>(a, run, &ctl, smem_u32(sm), tmem);
+    few_mma<NR>(a, &ctl, smem_u32(sm), tmem);
   }
   __syncwarp();
   grid_launch_dependents();

@@ -22,7 +22,7 @@
 // fp32.  m follows the running maximum of x + e_v only when that has grown by
 // more than 8, so O in tensor memory is rarely rescaled; P stays below 2^8.
 //
-// Tensor memory (512 columns): S of either tile (P over its second half) and O
+// Tensor memory (512 columns): S of either tile (a page's P over its scores) and O
 // of either tile.  The MMA thread alternates P V of one tile's previous keys
 // with Q K^T of its next, so one tile's softmax runs under the other's products.
 #include <cuda_fp16.h>
@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kRows = 256;
 constexpr int kThreads = 640;  // two softmax warpgroups, one converting values, one of TMA and MMA warps
-constexpr int kTmaWarp = 12, kMmaWarp = 13;
+constexpr int kValuesWarp = 8, kTmaWarp = 12, kMmaWarp = 13;
 constexpr int kSoftRegs = 144, kOtherRegs = 64;  // 256 x 144 + 384 x 64 = 640 x 96, the registers at launch
 constexpr int kTileBytes = kKvTile * kHeadDim;
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScaleRing = 8;
@@ -47,14 +47,13 @@ constexpr uint32_t kOffH = kOffV + kVStages * kTileBytes;      // fp16 values: t
 constexpr uint32_t kSmem = kOffH + kHStages * 2 * kTileBytes + 1024;
 
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for the second tile
-constexpr uint32_t kColP = 64;              // P (two weights a column) over the second half of S
 
 enum { kBarK = 1, kBarV, kBarKFree, kBarVFree, kBarQ, kBarS, kBarP, kBarO, kBarScale, kBarH, kBarHFree };
 
 struct ManyCtl {
   uint64_t k_full[kKStages], k_free[kKStages], v_full[kVStages], v_free[kVStages], h_full[kHStages], h_free[kHStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], scale_full[kScaleRing];
-  float scale[kScaleRing][4];       // key scales of the tile's two pages, value scales
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], scale_full[kScaleRing];
+  alignas(16) float scale[kScaleRing][4];  // key scales of the tile's two pages, value scales
   uint32_t nan_keys[kHStages][4];   // keys of a masked tile whose values hold a NaN code
   KvRunScratch run;
   uint32_t tmem;
@@ -78,12 +77,13 @@ __device__ __forceinline__ ManyItem many_item(const KvAttnArgs& a, const KvCurso
 }
 
 // ---------------------------------------------------------------- TMA warp
-__device__ __forceinline__ void many_load(const KvAttnArgs& a, const KvRun& run, ManyCtl* ctl, uint8_t* sm,
+__device__ __forceinline__ void many_load(const KvAttnArgs& a, ManyCtl* ctl, uint8_t* sm,
                                           const CUtensorMap* kmap, const CUtensorMap* vmap) {
   const int lane = threadIdx.x & 31;
   int i = 0;
   KvCursor cur;
-  for (cur.start(a, run); cur.valid(); cur.next(a)) {
+#pragma unroll 1
+  for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
     const int tiles = cur.tiles();
     int page = -1, next_page = -1;
     float sk = 1.f, sv = 1.f, next_sk = 1.f, next_sv = 1.f;
@@ -99,18 +99,20 @@ __device__ __forceinline__ void many_load(const KvAttnArgs& a, const KvRun& run,
       }
     };
     fetch(0);
+#pragma unroll 1
     for (int b = 0; 16 * b < tiles; ++b) {
       page = next_page;
       sk = next_sk;
       sv = next_sv;
       fetch(b + 1);
       const int n = min(16, tiles - 16 * b);
+#pragma unroll 1
       for (int j = 0; j < n; ++j, ++i) {
         const int ks = i % kKStages, vs = i % kVStages;
         const int p0 = __shfl_sync(0xffffffffu, page, 2 * j), p1 = __shfl_sync(0xffffffffu, page, 2 * j + 1);
         // a tile's second page may lie past the sequence: its rows keep what they hold and are masked
         const uint32_t bytes = p1 >= 0 ? kTileBytes : kTileBytes / 2;
-        if (!__all_sync(0xffffffffu, wait_phase(&ctl->k_free[ks], ((i / kKStages) & 1) ^ 1, &ctl->abort, 100 + kBarKFree))) return;
+        if (!kv_wait_warp([&] { return kv_wait(&ctl->k_free[ks], ((i / kKStages) & 1) ^ 1, &ctl->abort, 100 + kBarKFree); })) return;
         if ((lane >> 1) == j) {
           float* s = ctl->scale[i % kScaleRing];
           s[lane & 1] = sk;
@@ -124,7 +126,7 @@ __device__ __forceinline__ void many_load(const KvAttnArgs& a, const KvRun& run,
           tma_load_3d(dst, kmap, &ctl->k_full[ks], 0, 0, p0);
           if (p1 >= 0) tma_load_3d(dst + kTileBytes / 2, kmap, &ctl->k_full[ks], 0, 0, p1);
         }
-        if (!__all_sync(0xffffffffu, wait_phase(&ctl->v_free[vs], ((i / kVStages) & 1) ^ 1, &ctl->abort, 100 + kBarVFree))) return;
+        if (!kv_wait_warp([&] { return kv_wait(&ctl->v_free[vs], ((i / kVStages) & 1) ^ 1, &ctl->abort, 100 + kBarVFree); })) return;
         if (lane == 0) {
           uint8_t* dst = sm + kOffV + vs * kTileBytes;
           mbar_arrive_expect_tx(&ctl->v_full[vs], bytes);
@@ -136,54 +138,90 @@ __device__ __forceinline__ void many_load(const KvAttnArgs& a, const KvRun& run,
   }
 }
 
-// ---------------------------------------------------------------- MMA thread
-__device__ __forceinline__ void many_mma(const KvAttnArgs& a, const KvRun& run, ManyCtl* ctl, uint32_t sm,
-                                         uint32_t tmem) {
+// ---------------------------------------------------------------- MMA warp
+// The whole warp walks the loop, so addresses and descriptors stay in uniform
+// registers, and one elected lane issues: a loop of one lane alone takes some
+// 50 instructions an MMA, which the softmax warps' issue slots stretch from 64
+// to over 300 cycles; this form takes about 20.
+__device__ __forceinline__ void many_mma(const KvAttnArgs& a, ManyCtl* ctl, uint32_t sm, uint32_t tmem_any) {
   constexpr uint32_t kIdS = idesc_e4m3(128, 128, false, false), kIdO = idesc_f16(128, 128, false, true);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
   const uint64_t dq = sdesc_sw128(sm + kOffQ, 0, 1024), dk = sdesc_sw128(sm + kOffK, 0, 1024);
   const uint64_t dh = sdesc_sw128(sm + kOffH, kTileBytes, 1024);
-  int i = 0, items = 0, items2 = 0;
-  int n[2] = {0, 0};  // tiles of keys that each query tile has seen
-  auto second = [&](int q, int t, bool first, bool last) {  // O of tile q += P V of key tile t
-    const int hs = t % kHStages;
-    if (!wait_phase(&ctl->p_full[q], (n[q] - 1) & 1, &ctl->abort, 100 + kBarP)) return false;
-    if (!wait_phase(&ctl->h_full[hs], (t / kHStages) & 1, &ctl->abort, 100 + kBarH)) return false;
-    tc_fence_after();
-    const uint32_t d = tmem + kColO + q * 128, p = tmem + kColS + kColP + q * 128;
+  const bool issue = elect_one();
+  int ks = 0, hs = 1;                     // stages of the current key tile, and of the one before
+  uint32_t k_par = 0, h_par = 1;          // and the parities of their barriers
+  uint32_t p_par[2] = {1, 1};             // parity of the weights of the tile before
+  uint32_t q_par[2] = {0, 0};
+  // O of tile q += P V: the second page's weights come first
+  auto second = [&](int q, bool first, bool last) {
+    const uint32_t d = tmem + kColO + q * 128, p = tmem + kColS + q * 128;
     const uint64_t h = dh + hs * (2 * kTileBytes >> 4);
+    if (!kv_wait_warp([&] {
+          return kv_wait(&ctl->p_full[q][1], p_par[q], &ctl->abort, 100 + kBarP) &&
+                 kv_wait(&ctl->h_full[hs], h_par, &ctl->abort, 100 + kBarH);
+        }))
+      return false;
+    tc_fence_after();
+    if (issue) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) mma_f16_ts(d, p + 8 * k, h + k * 128, kIdO, !first || k > 0);
-    mma_commit(&ctl->o_full[q]);
-    if (last) mma_commit(&ctl->h_free[hs]);
+      for (int k = 4; k < 8; ++k) mma_f16_ts(d, p + 64 + (k - 4) * 8, h + k * 128, kIdO, k > 4 || !first);
+    }
+    if (!kv_wait_warp([&] { return kv_wait(&ctl->p_full[q][0], p_par[q], &ctl->abort, 100 + kBarP); })) return false;
+    tc_fence_after();
+    if (issue) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mma_f16_ts(d, p + k * 8, h + k * 128, kIdO, 1);
+      mma_commit(&ctl->o_full[q]);
+      if (last) mma_commit(&ctl->h_free[hs]);
+    }
+    __syncwarp();
     return true;
   };
   KvCursor cur;
-  for (cur.start(a, run); cur.valid(); cur.next(a)) {
-    const int tiles = cur.tiles();
+#pragma unroll 1
+  for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
+    const int tiles = __shfl_sync(0xffffffffu, cur.tiles(), 0);
     if (tiles == 0) continue;
-    const int q_tiles = many_item(a, cur).q_tiles;
-    for (int j = 0; j < tiles; ++j, ++i) {
-      const int ks = i % kKStages;
-      for (int q = 0; q < q_tiles; ++q) {
-        if (j > 0 && !second(q, i - 1, j == 1, q == q_tiles - 1)) return;
-        if (j == 0 && !wait_phase(&ctl->q_full[q], (q ? items2 : items) & 1, &ctl->abort, 100 + kBarQ)) return;
-        if (q == 0 && !wait_phase(&ctl->k_full[ks], (i / kKStages) & 1, &ctl->abort, 100 + kBarK)) return;
+    const int q_tiles = __shfl_sync(0xffffffffu, many_item(a, cur).q_tiles, 0);
+#pragma unroll 1
+    for (int j = 0; j <= tiles; ++j) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (q >= q_tiles) continue;
+        if (j > 0 && !second(q, j == 1, q == q_tiles - 1)) return;
+        if (j == tiles) continue;
+        if (!kv_wait_warp([&] {
+              return (j > 0 || kv_wait(&ctl->q_full[q], q_par[q], &ctl->abort, 100 + kBarQ)) &&
+                     (q > 0 || kv_wait(&ctl->k_full[ks], k_par, &ctl->abort, 100 + kBarK));
+            }))
+          return;
         tc_fence_after();
         const uint32_t d = tmem + kColS + q * 128;
         const uint64_t kk = dk + ks * (kTileBytes >> 4), qq = dq + q * (2 * kTileBytes >> 4);
+        if (issue) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_f8(d, qq + k * 2, kk + k * 2, kIdS, k > 0);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mma_f8(d, qq + (kTileBytes >> 4) + k * 2, kk + k * 2, kIdS, 1);
-        mma_commit(&ctl->s_full[q]);
-        ++n[q];
+          for (int k = 0; k < 8; ++k)  // four steps with the high parts, four with the low ones
+            mma_f8(d, qq + (k >> 2) * (kTileBytes >> 4) + (k & 3) * 2, kk + (k & 3) * 2, kIdS, k > 0);
+          mma_commit(&ctl->s_full[q]);
+          if (q == q_tiles - 1) mma_commit(&ctl->k_free[ks]);
+        }
+        __syncwarp();
+        p_par[q] ^= 1;
       }
-      mma_commit(&ctl->k_free[ks]);
+      if (j < tiles) {
+        if (++ks == kKStages) {
+          ks = 0;
+          k_par ^= 1;
+        }
+        if (++hs == kHStages) {
+          hs = 0;
+          h_par ^= 1;
+        }
+      }
     }
-    for (int q = 0; q < q_tiles; ++q)
-      if (!second(q, i - 1, tiles == 1, q == q_tiles - 1)) return;
-    ++items;
-    if (q_tiles == 2) ++items2;
+    q_par[0] ^= 1;
+    if (q_tiles == 2) q_par[1] ^= 1;
   }
 }
 
@@ -191,47 +229,48 @@ __device__ __forceinline__ void many_mma(const KvAttnArgs& a, const KvRun& run, 
 // Thread = key of the tile.  Four codes to four fp16 by the hardware's exact
 // conversion; 16 codes are a 16-byte chunk of the e4m3 tile and two chunks of
 // a panel of the fp16 tile, both in the swizzled image (conflict-free).
-__device__ __forceinline__ void many_values(const KvAttnArgs& a, const KvRun& run, ManyCtl* ctl, uint8_t* sm) {
+__device__ __forceinline__ void many_values(const KvAttnArgs& a, ManyCtl* ctl, uint8_t* sm) {
   const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
   int i = 0;
   KvCursor cur;
-  for (cur.start(a, run); cur.valid(); cur.next(a)) {
+#pragma unroll 1
+  for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
     const int tiles = cur.tiles();
     if (tiles == 0) continue;
     const ManyItem mi = many_item(a, cur);
+#pragma unroll 1
     for (int j = 0; j < tiles; ++j, ++i) {
       const int vs = i % kVStages, hs = i % kHStages;
       const int key0 = (cur.tile_begin() + j) * kKvTile, key = key0 + tid;
       const bool masked = key0 < mi.all_lo || key0 + kKvTile > mi.all_hi;
-      bool ok = wait_phase(&ctl->v_full[vs], (i / kVStages) & 1, &ctl->abort, 100 + kBarV) &&
-                wait_phase(&ctl->h_free[hs], ((i / kHStages) & 1) ^ 1, &ctl->abort, 100 + kBarHFree);
-      if (!__all_sync(0xffffffffu, ok)) return;
+      if (!kv_wait_warp([&] {
+            return kv_wait(&ctl->v_full[vs], (i / kVStages) & 1, &ctl->abort, 100 + kBarV) &&
+                   kv_wait(&ctl->h_free[hs], ((i / kHStages) & 1) ^ 1, &ctl->abort, 100 + kBarHFree);
+          }))
+        return;
       const uint8_t* v = sm + kOffV + vs * kTileBytes;
       uint8_t* h = sm + kOffH + hs * 2 * kTileBytes;
-      uint4 w[8];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) w[c] = *reinterpret_cast<const uint4*>(v + sw128_offset(tid, c));
-      mbar_arrive(&ctl->v_free[vs]);
+      uint32_t keep = 0xffffffffu;
       if (masked) {
         // Values no row may use must not meet a zero weight as NaN: a key past
         // the sequence, or one that holds a NaN code, becomes zeros; the rows
         // that do attend to the latter become NaN in the softmax.
         uint32_t carry = 0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)  // b & 0x7f = 0x7f: adding 1 to the low seven bits carries into the eighth
-          carry |= ((w[c].x & 0x7f7f7f7fu) + 0x01010101u) | ((w[c].y & 0x7f7f7f7fu) + 0x01010101u) |
-                   ((w[c].z & 0x7f7f7f7fu) + 0x01010101u) | ((w[c].w & 0x7f7f7f7fu) + 0x01010101u);
+#pragma unroll 2
+        for (int c = 0; c < 8; ++c) {  // b & 0x7f = 0x7f: adding 1 to the low seven bits carries into the eighth
+          const uint4 w = *reinterpret_cast<const uint4*>(v + sw128_offset(tid, c));
+          carry |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
+                   ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
+        }
         const bool nan = (carry & 0x80808080u) != 0;
         const uint32_t word = __ballot_sync(0xffffffffu, nan && key < cur.it.len);
         if (lane == 0) ctl->nan_keys[hs][warp] = word;
-        if (nan || key >= cur.it.len) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) w[c] = make_uint4(0, 0, 0, 0);
-        }
+        if (nan || key >= cur.it.len) keep = 0;
       }
-#pragma unroll
+#pragma unroll 2
       for (int c = 0; c < 8; ++c) {
-        const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        const uint4 w = *reinterpret_cast<const uint4*>(v + sw128_offset(tid, c));
+        const uint32_t u[4] = {w.x & keep, w.y & keep, w.z & keep, w.w & keep};
         uint32_t f[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -242,8 +281,9 @@ __device__ __forceinline__ void many_values(const KvAttnArgs& a, const KvRun& ru
         *reinterpret_cast<uint4*>(panel + sw128_offset(tid, 2 * (c & 3))) = make_uint4(f[0], f[1], f[2], f[3]);
         *reinterpret_cast<uint4*>(panel + sw128_offset(tid, 2 * (c & 3) + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
       }
+      kv_arrive_warp(&ctl->v_free[vs]);
       fence_proxy_async_smem();
-      mbar_arrive(&ctl->h_full[hs]);
+      kv_arrive_warp(&ctl->h_full[hs]);
     }
   }
 }
@@ -306,102 +346,100 @@ __device__ __forceinline__ float2 add2(float2 a, float b0, float b1) {
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLazy = 8.f;
 
-// 64 scores of this thread's row; under the masks, -inf for keys outside them
-// and NaN for keys whose values hold one.
-__device__ __forceinline__ void tile_scores(const ManyCtl* ctl, uint32_t t_s, uint32_t (&s)[64], bool masked, int c0,
-                                            int lo, int hi, int stage) {
-  tmem_ld32(t_s, s);
-  tmem_ld32(t_s + 32, s + 32);
-  tmem_ld_done(s);
-  tmem_ld_done(s + 32);
-  if (masked) {
-    const uint32_t nan[2] = {ctl->nan_keys[stage][c0 >> 5], ctl->nan_keys[stage][(c0 >> 5) + 1]};
+// Under the masks: -inf for keys outside [lo, hi) of these 32, NaN for keys
+// whose values hold one.
+__device__ __forceinline__ void mask32(uint32_t (&s)[32], uint32_t nan, int lo, int hi) {
 #pragma unroll
-    for (int c = 0; c < 64; ++c) {
-      if ((nan[c >> 5] >> (c & 31)) & 1) s[c] = 0x7fffffffu;
-      if (c0 + c < lo || c0 + c >= hi) s[c] = 0xff800000u;
-    }
+  for (int c = 0; c < 32; ++c) {
+    if ((nan >> c) & 1) s[c] = 0x7fffffffu;
+    if (c < lo || c >= hi) s[c] = 0xff800000u;
   }
 }
-__device__ __forceinline__ float max64(const uint32_t (&s)[64]) {
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
   float t[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) t[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[4 + e]));
 #pragma unroll
-  for (int c = 8; c < 64; c += 8)
+  for (int c = 8; c < 32; c += 8)
 #pragma unroll
     for (int e = 0; e < 4; ++e) t[e] = max3(t[e], __uint_as_float(s[c + e]), __uint_as_float(s[c + 4 + e]));
   return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
-// Weights 2^(s f + bias) to tensor memory as fp16 pairs; returns their sum.
-__device__ __forceinline__ float weights64(uint32_t t_p, const uint32_t (&s)[64], float f, float bias) {
-  float2 sum = make_float2(0.f, 0.f);
+// Weights 2^(s f + bias) of 32 keys to tensor memory as fp16 pairs; adds them to sum.
+__device__ __forceinline__ void weights32(uint32_t t_p, const uint32_t (&s)[32], float f, float bias, float2& sum) {
+  uint32_t w[16];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    uint32_t w[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int at = 32 * c + 2 * e;
-      const float2 x = fma2(__uint_as_float(s[at]), __uint_as_float(s[at + 1]), f, bias);
-      const float p0 = ex2(x.x), p1 = ex2(x.y);
-      sum = add2(sum, p0, p1);
-      w[e] = pack_f16x2(p0, p1);
-    }
-    tmem_st16(t_p + 16 * c, w);
+  for (int e = 0; e < 16; ++e) {
+    const float2 x = fma2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]), f, bias);
+    const float p0 = ex2(x.x), p1 = ex2(x.y);
+    sum = add2(sum, p0, p1);
+    w[e] = pack_f16x2(p0, p1);
   }
-  return sum.x + sum.y;
+  tmem_st16(t_p, w);
 }
 
-// The item's query rows of tile q into their two e4m3 parts; a warp takes
-// every fourth row, a lane four columns.  Returns, to the thread that owns the
-// row, its score factor.
+// The item's query rows of tile q into their two e4m3 parts; a warp takes its
+// own 32 rows, a lane four columns.  Returns the score factor of the thread's row.
 __device__ __forceinline__ float many_queries(const KvAttnArgs& a, const KvCursor& cur, int q, uint8_t* sm) {
-  const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
+  const int warp = (threadIdx.x & 127) >> 5, lane = threadIdx.x & 31;
   const int head0 = kv_first_q_head(a.c, cur.head), group = kv_first_q_head(a.c, cur.head + 1) - head0;
   const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;  // the row's factor stays positive
   uint8_t* hi_tile = sm + kOffQ + q * 2 * kTileBytes;
   float f = 0.f;
-#pragma unroll 4
-  for (int k = 0; k < 32; ++k) {
-    const int r = 32 * warp + k, rr = cur.rt * kRows + q * 128 + r, t = rr / a.group, g = rr % a.group;
-    uint2 w = make_uint2(0, 0);
-    if (t < cur.it.n && g < group)
-      w = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                          (int64_t)(cur.it.tok0 + t) * a.q_stride + (head0 + g) * kHeadDim + 4 * lane);
-    float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                  __uint_as_float(w.y & 0xffff0000u)};
-    uint32_t m = 0;
+  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)cur.it.tok0 * a.q_stride +
+                             head0 * kHeadDim + 4 * lane;
+  const int rr = cur.rt * kRows + q * 128 + 32 * warp;
+  int t = rr / a.group, g = rr % a.group;
+#pragma unroll 1
+  for (int k0 = 0; k0 < 32; k0 += 16) {
+    uint2 row[16];  // 16 rows' loads in flight together
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m = max(m, __float_as_uint(x[e]) & 0x7fffffffu);
-    m = __reduce_max_sync(0xffffffffu, m);
-    // below 2^-102 a row's scores are zero for any key the cache can hold
-    const int ex = m < 0x7f800000u ? e4m3_scale_exp(m, -110) : 0;
-    const float inv = pow2f(-ex) * sign;
-    uint32_t hi[2], lo[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float y0 = x[2 * e] * inv, y1 = x[2 * e + 1] * inv;
-      hi[e] = f32x2_to_e4m3x2(y0, y1);
-      const float2 h = e4m3x2_to_f32x2(hi[e]);
-      lo[e] = f32x2_to_e4m3x2(y0 - h.x, y1 - h.y);
+    for (int e = 0; e < 16; ++e) {
+      row[e] = make_uint2(0, 0);
+      if (t < cur.it.n && g < group) row[e] = __ldg(reinterpret_cast<const uint2*>(src + t * a.q_stride + g * kHeadDim));
+      if (++g == a.group) {
+        g = 0;
+        ++t;
+      }
     }
-    const uint32_t at = sw128_offset(r, lane >> 2) + 4 * (lane & 3);
-    *reinterpret_cast<uint32_t*>(hi_tile + at) = hi[0] | hi[1] << 16;
-    *reinterpret_cast<uint32_t*>(hi_tile + kTileBytes + at) = lo[0] | lo[1] << 16;
-    // a row that is not finite gives NaN
-    if (lane == k) f = m < 0x7f800000u ? pow2f(ex) * fabsf(a.scale_log2) : __int_as_float(0x7fffffff);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint2 w = row[e];
+      const float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                          __uint_as_float(w.y & 0xffff0000u)};
+      uint32_t m = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) m = max(m, __float_as_uint(x[c]) & 0x7fffffffu);
+      m = __reduce_max_sync(0xffffffffu, m);
+      // below 2^-102 a row's scores are zero for any key the cache can hold
+      const int ex = m < 0x7f800000u ? e4m3_scale_exp(m, -110) : 0;
+      const float inv = pow2f(-ex) * sign;
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float y0 = x[2 * c] * inv, y1 = x[2 * c + 1] * inv;
+        hi[c] = f32x2_to_e4m3x2(y0, y1);
+        const float2 h = e4m3x2_to_f32x2(hi[c]);
+        lo[c] = f32x2_to_e4m3x2(y0 - h.x, y1 - h.y);
+      }
+      const uint32_t at = sw128_offset(32 * warp + k0 + e, lane >> 2) + 4 * (lane & 3);
+      *reinterpret_cast<uint32_t*>(hi_tile + at) = hi[0] | hi[1] << 16;
+      *reinterpret_cast<uint32_t*>(hi_tile + kTileBytes + at) = lo[0] | lo[1] << 16;
+      // a row that is not finite gives NaN
+      if (lane == k0 + e) f = m < 0x7f800000u ? pow2f(ex) * fabsf(a.scale_log2) : __int_as_float(0x7fffffff);
+    }
   }
   return f;
 }
 
-__device__ __forceinline__ void many_softmax(const KvAttnArgs& a, const KvRun& run, ManyCtl* ctl, uint8_t* sm,
-                                             uint32_t tmem) {
-  const int q = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5;
+__device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, uint8_t* sm, uint32_t tmem) {
+  const int q = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5;
   const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-  const uint32_t t_s = tmem + lane_base + kColS + q * 128, t_o = tmem + lane_base + kColO + q * 128, t_p = t_s + kColP;
+  const uint32_t t_s = tmem + lane_base + kColS + q * 128, t_o = tmem + lane_base + kColO + q * 128;
   int i = 0, n = 0;  // key tiles of the run, and those this query tile took part in
   KvCursor cur;
-  for (cur.start(a, run); cur.valid(); cur.next(a)) {
+#pragma unroll 1
+  for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
     const KvItem& it = cur.it;
     const int tiles = cur.tiles();
     const ManyItem mi = many_item(a, cur);
@@ -409,62 +447,75 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, const KvRun& r
       i += tiles;
       continue;
     }
-    const int head0 = kv_first_q_head(a.c, cur.head), group = kv_first_q_head(a.c, cur.head + 1) - head0;
-    const int rr = cur.rt * kRows + q * 128 + tid, t = rr / a.group, g = rr % a.group, p = mi.past + t;
-    const bool live = t < it.n && g < group;
-    const int key_lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
-    const int key_hi = live ? (a.causal ? min(max(p + 1, 0), it.len) : it.len) : 0;
+    const int head0 = kv_first_q_head(a.c, cur.head);
+    const int rr = cur.rt * kRows + q * 128 + row, t = rr / a.group, g = rr - t * a.group;
+    const bool live = t < it.n && g < kv_first_q_head(a.c, cur.head + 1) - head0;
     float f = 0.f, m = kNegInf, l = 0.f;
     if (tiles > 0) {
       f = many_queries(a, cur, q, sm);
       fence_proxy_async_smem();
-      mbar_arrive(&ctl->q_full[q]);
+      kv_arrive_warp(&ctl->q_full[q]);
     }
+#pragma unroll 1
     for (int j = 0; j < tiles; ++j, ++i, ++n) {
       const int key0 = (cur.tile_begin() + j) * kKvTile;
       const bool masked = key0 < mi.all_lo || key0 + kKvTile > mi.all_hi;
-      bool ok = wait_phase(&ctl->scale_full[i % kScaleRing], (i / kScaleRing) & 1, &ctl->abort, 100 + kBarScale) &&
-                wait_phase(&ctl->s_full[q], n & 1, &ctl->abort, 100 + kBarS);
-      if (masked) ok = ok && wait_phase(&ctl->h_full[i % kHStages], (i / kHStages) & 1, &ctl->abort, 100 + kBarH);
-      if (!__all_sync(0xffffffffu, ok)) return;
+      const int stage = i % kHStages;
+      if (!kv_wait_warp([&] {
+            return kv_wait(&ctl->scale_full[i % kScaleRing], (i / kScaleRing) & 1, &ctl->abort, 100 + kBarScale) &&
+                   kv_wait(&ctl->s_full[q], n & 1, &ctl->abort, 100 + kBarS) &&
+                   (!masked || kv_wait(&ctl->h_full[stage], (i / kHStages) & 1, &ctl->abort, 100 + kBarH));
+          }))
+        return;
       tc_fence_after();
-      const float* sc = ctl->scale[i % kScaleRing];
-      const float4 sc4 = *reinterpret_cast<const float4*>(sc);
-      // log2 and inverse of the value scales, powers of two
-      const float ev[2] = {(float)((int)(__float_as_uint(sc4.z) >> 23) - 127), (float)((int)(__float_as_uint(sc4.w) >> 23) - 127)};
-      const float inv_sv[2] = {__int_as_float((254 << 23) - __float_as_int(sc4.z)), __int_as_float((254 << 23) - __float_as_int(sc4.w))};
-      const float fk[2] = {f * sc4.x, f * sc4.y};
-      // The two pages in turn: the first one's scores are read again after the
-      // maximum is known, the second one's stay in registers.
-      uint32_t s[64];
-      float top = kNegInf;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        tile_scores(ctl, t_s + 64 * h, s, masked, 64 * h, key_lo - key0, key_hi - key0, i % kHStages);
-        top = fmaxf(top, fmaf(max64(s), fk[h], ev[h]));
+      uint32_t s0[32], s1[32];
+      tmem_ld32(t_s, s0);
+      tmem_ld32(t_s + 32, s1);
+      const float4 sc = *reinterpret_cast<const float4*>(ctl->scale[i % kScaleRing]);
+      // log2 of the value scales, powers of two
+      const float ev0 = (float)((int)(__float_as_uint(sc.z) >> 23) - 127), ev1 = (float)((int)(__float_as_uint(sc.w) >> 23) - 127);
+      const float fk0 = f * sc.x, fk1 = f * sc.y;
+      int lo = 0, hi = 0;
+      if (masked) {
+        const int p = mi.past + t;
+        lo = (a.window > 0 ? max(0, p - a.window + 1) : 0) - key0;
+        hi = (live ? (a.causal ? min(p + 1, it.len) : it.len) : 0) - key0;
       }
-      // -inf * 0 (a row of zeros) is NaN: such a key is masked and must stay out
+      const uint32_t* nan = ctl->nan_keys[stage];
+      // The maximum; the first page's scores are read again after it, the
+      // second one's stay in registers.  s is -inf only under a mask, and the
+      // factors are positive unless the row is NaN.
+      tmem_ld_done(s0);
+      tmem_ld_done(s1);
+      if (masked) {
+        mask32(s0, nan[0], lo, hi);
+        mask32(s1, nan[1], lo - 32, hi - 32);
+      }
+      float top = fmaf(fmaxf(max32(s0), max32(s1)), fk0, ev0);
+      tmem_ld32(t_s + 64, s0);
+      tmem_ld32(t_s + 96, s1);
+      tmem_ld_done(s0);
+      tmem_ld_done(s1);
+      if (masked) {
+        mask32(s0, nan[2], lo - 64, hi - 64);
+        mask32(s1, nan[3], lo - 96, hi - 96);
+      }
+      top = fmaxf(top, fmaf(fmaxf(max32(s0), max32(s1)), fk1, ev1));
       const bool grow = top > m + kLazy || (m == kNegInf && top > kNegInf);
       if (__any_sync(0xffffffffu, grow)) {
         const float alpha = grow ? ex2(m - top) : 1.f;
         if (j > 0) {
           // O holds the tiles before this one: wait for the last of them, then rescale
-          ok = wait_phase(&ctl->o_full[q], (n - 1) & 1, &ctl->abort, 100 + kBarO);
-          if (!__all_sync(0xffffffffu, ok)) return;
+          if (!kv_wait_warp([&] { return kv_wait(&ctl->o_full[q], (n - 1) & 1, &ctl->abort, 100 + kBarO); })) return;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[16], o2[16];
-            tmem_ld16(t_o + 32 * c, o);
-            tmem_ld16(t_o + 32 * c + 16, o2);
-            tmem_ld_wait(o, o2);
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld16(t_o + 16 * c, o);
+            tmem_ld_wait(o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              o2[e] = __float_as_uint(__uint_as_float(o2[e]) * alpha);
-            }
-            tmem_st16(t_o + 32 * c, o);
-            tmem_st16(t_o + 32 * c + 16, o2);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st16(t_o + 16 * c, o);
           }
         }
         if (grow) {
@@ -473,49 +524,66 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, const KvRun& r
         }
       }
       const float ref = m == kNegInf ? 0.f : m;
-      l = fmaf(weights64(t_p + 32, s, fk[1], ev[1] - ref), inv_sv[1], l);
-      tile_scores(ctl, t_s, s, masked, 0, key_lo - key0, key_hi - key0, i % kHStages);
-      l = fmaf(weights64(t_p, s, fk[0], ev[0] - ref), inv_sv[0], l);
+      // A page's weights go over its own scores, the second page's first: the
+      // MMA warp starts on them while the first page's are computed.
+      float2 sum = make_float2(0.f, 0.f);
+      weights32(t_s + 64, s0, fk1, ev1 - ref, sum);
+      tmem_ld32(t_s, s0);
+      weights32(t_s + 80, s1, fk1, ev1 - ref, sum);
+      l = fmaf(sum.x + sum.y, __int_as_float((254 << 23) - __float_as_int(sc.w)), l);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&ctl->p_full[q]);
+      kv_arrive_warp(&ctl->p_full[q][1]);
+      tmem_ld32(t_s + 32, s1);
+      tmem_ld_done(s0);
+      tmem_ld_done(s1);
+      if (masked) {
+        mask32(s0, nan[0], lo, hi);
+        mask32(s1, nan[1], lo - 32, hi - 32);
+      }
+      sum = make_float2(0.f, 0.f);
+      weights32(t_s, s0, fk0, ev0 - ref, sum);
+      weights32(t_s + 16, s1, fk0, ev0 - ref, sum);
+      l = fmaf(sum.x + sum.y, __int_as_float((254 << 23) - __float_as_int(sc.z)), l);
+      tmem_st_wait();
+      tc_fence_before();
+      kv_arrive_warp(&ctl->p_full[q][0]);
     }
     // ---- the row's output ----
+    if (tiles > 0) {
+      if (!kv_wait_warp([&] { return kv_wait(&ctl->o_full[q], (n - 1) & 1, &ctl->abort, 100 + kBarO); })) return;
+      tc_fence_after();
+    }
     const int64_t tok = it.tok0 + t;
-    const size_t part = (size_t)cur.slot() * kRows + q * 128 + tid;
+    const size_t part = (size_t)cur.slot() * kRows + q * 128 + row;
     const bool whole = cur.whole();
     __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + (head0 + g) * kHeadDim;
     const float inv = l == 0.f ? 0.f : 1.0f / l;
-    if (tiles > 0) {
-      const bool ok = wait_phase(&ctl->o_full[q], (n - 1) & 1, &ctl->abort, 100 + kBarO);
-      if (!__all_sync(0xffffffffu, ok)) return;
-      tc_fence_after();
-    }
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[32];
+    for (int c = 0; c < 8; ++c) {
+      uint32_t o[16];
       if (tiles > 0) {
-        tmem_ld32(t_o + 32 * c, o);
-        tmem_ld_done(o);
+        tmem_ld16(t_o + 16 * c, o);
+        tmem_ld_wait(o);
       } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0;
+        for (int e = 0; e < 16; ++e) o[e] = 0;
       }
       if (whole) {
         if (live) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 2; ++e) {
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               w[k] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-            reinterpret_cast<uint4*>(dst + 32 * c)[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(dst + 16 * c)[e] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          reinterpret_cast<uint4*>(a.o + part * kHeadDim + 32 * c)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        for (int e = 0; e < 4; ++e)
+          reinterpret_cast<uint4*>(a.o + part * kHeadDim + 16 * c)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
       }
     }
     tc_fence_before();
@@ -524,7 +592,7 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, const KvRun& r
     } else {
       a.ml[part] = make_float2(m, l);
       if (threadIdx.x == 0 && cur.off == 0)
-        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(run, cur));
+        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(ctl->run.run, cur));
     }
   }
 }
@@ -543,14 +611,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(&ctl.v_full[s], 1);
-      mbar_init(&ctl.v_free[s], 128);
-      mbar_init(&ctl.h_full[s], 128);
+      mbar_init(&ctl.v_free[s], 4);
+      mbar_init(&ctl.h_full[s], 4);
       mbar_init(&ctl.h_free[s], 1);
     }
     for (int q = 0; q < 2; ++q) {
-      mbar_init(&ctl.q_full[q], 128);
+      mbar_init(&ctl.q_full[q], 4);
       mbar_init(&ctl.s_full[q], 1);
-      mbar_init(&ctl.p_full[q], 128);
+      mbar_init(&ctl.p_full[q][0], 4);
+      mbar_init(&ctl.p_full[q][1], 4);
       mbar_init(&ctl.o_full[q], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&ctl.scale_full[s], 1);
@@ -564,22 +633,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&ctl.tmem, 512);
     tmem_relinquish();
   }
-  const KvRun run = kv_run<kThreads>(a, &ctl.run);
+  kv_run<kThreads>(a, &ctl.run);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl.tmem;
-  if (warp < 8) {
+  if (warp < kValuesWarp) {
     setmaxnreg_inc<kSoftRegs>();
-    many_softmax(a, run, &ctl, sm, tmem);
+    many_softmax(a, &ctl, sm, tmem);
   } else {
     setmaxnreg_dec<kOtherRegs>();
-    if (warp < 12) {
-      many_values(a, run, &ctl, sm);
+    if (warp < kTmaWarp) {
+      many_values(a, &ctl, sm);
     } else if (warp == kTmaWarp) {
-      many_load(a, run, &ctl, sm, &kmap, &vmap);
-    } else if (warp == kMmaWarp && (tid & 31) == 0) {
-      many_mma(a, run, &ctl, smem_u32(sm), tmem);
+      many_load(a, &ctl, sm, &kmap, &vmap);
+    } else if (warp == kMmaWarp) {
+      many_mma(a, &ctl, smem_u32(sm), tmem);
     }
   }
   __syncwarp();

@@ -39,9 +39,11 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const KvAttnArgs a)
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SimtSmem& sm = *reinterpret_cast<SimtSmem*>(smem_raw);
   const int tid = threadIdx.x, r = tid >> 4, c = tid & 15;
-  const KvRun run = kv_run<kThreads>(a, &sm.run);
+  kv_run<kThreads>(a, &sm.run);
+  const KvRun& run = sm.run.run;
   if (a.n_ctas && tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
   KvCursor cur;
+#pragma unroll 1
   for (cur.start(a, run); cur.valid(); cur.next(a)) {
     const KvItem& it = cur.it;
     // row r of the item: token t of the sequence, query head j

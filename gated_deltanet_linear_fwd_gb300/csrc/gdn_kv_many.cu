@@ -22,9 +22,10 @@
 // fp32.  m follows the running maximum of x + e_v only when that has grown by
 // more than 8, so O in tensor memory is rarely rescaled; P stays below 2^8.
 //
-// Tensor memory (512 columns): S of either tile (a page's P over its scores) and O
-// of either tile.  The MMA thread alternates P V of one tile's previous keys
-// with Q K^T of its next, so one tile's softmax runs under the other's products.
+// Tensor memory (512 columns): S of either tile (P over its middle) and O
+// of either tile.  Each tile has an MMA warp that alternates P V of
+// the previous keys with Q K^T of the next; one tile's softmax runs under the
+// other's products.
 #include <cuda_fp16.h>
 
 #include "gdn_dev.cuh"
@@ -35,7 +36,7 @@ namespace {
 
 constexpr int kRows = 256;
 constexpr int kThreads = 640;  // two softmax warpgroups, one converting values, one of TMA and MMA warps
-constexpr int kValuesWarp = 8, kTmaWarp = 12, kMmaWarp = 13;
+constexpr int kValuesWarp = 8, kTmaWarp = 12, kMmaWarp = 13;  // MMA warps 13 and 14
 constexpr int kSoftRegs = 144, kOtherRegs = 64;  // 256 x 144 + 384 x 64 = 640 x 96, the registers at launch
 constexpr int kTileBytes = kKvTile * kHeadDim;
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScaleRing = 8;
@@ -47,12 +48,13 @@ constexpr uint32_t kOffH = kOffV + kVStages * kTileBytes;      // fp16 values: t
 constexpr uint32_t kSmem = kOffH + kHStages * 2 * kTileBytes + 1024;
 
 constexpr uint32_t kColS = 0, kColO = 256;  // + 128 for the second tile
+constexpr uint32_t kColP = 32;              // P, two weights a column, within S
 
 enum { kBarK = 1, kBarV, kBarKFree, kBarVFree, kBarQ, kBarS, kBarP, kBarO, kBarScale, kBarH, kBarHFree };
 
 struct ManyCtl {
   uint64_t k_full[kKStages], k_free[kKStages], v_full[kVStages], v_free[kVStages], h_full[kHStages], h_free[kHStages];
-  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], scale_full[kScaleRing];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], scale_full[kScaleRing];
   alignas(16) float scale[kScaleRing][4];  // key scales of the tile's two pages, value scales
   uint32_t nan_keys[kHStages][4];   // keys of a masked tile whose values hold a NaN code
   KvRunScratch run;
@@ -138,77 +140,63 @@ __device__ __forceinline__ void many_load(const KvAttnArgs& a, ManyCtl* ctl, uin
   }
 }
 
-// ---------------------------------------------------------------- MMA warp
-// The whole warp walks the loop, so addresses and descriptors stay in uniform
-// registers, and one elected lane issues: a loop of one lane alone takes some
-// 50 instructions an MMA, which the softmax warps' issue slots stretch from 64
-// to over 300 cycles; this form takes about 20.
-__device__ __forceinline__ void many_mma(const KvAttnArgs& a, ManyCtl* ctl, uint32_t sm, uint32_t tmem_any) {
+// ---------------------------------------------------------------- MMA warps, one a query tile
+// One tile's waits run under the other tile's products.  The whole warp walks
+// the loop, so addresses and descriptors stay in uniform registers, and one
+// elected lane issues: a loop of one lane alone takes some 50 instructions an
+// MMA, which the softmax warps' issue slots stretch from 64 to over 300
+// cycles; this form takes about 20.
+__device__ __forceinline__ void many_mma(const KvAttnArgs& a, ManyCtl* ctl, uint32_t sm, uint32_t tmem_any, int q) {
   constexpr uint32_t kIdS = idesc_e4m3(128, 128, false, false), kIdO = idesc_f16(128, 128, false, true);
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
-  const uint64_t dq = sdesc_sw128(sm + kOffQ, 0, 1024), dk = sdesc_sw128(sm + kOffK, 0, 1024);
+  const uint32_t d_s = tmem + kColS + q * 128, d_o = tmem + kColO + q * 128;
+  const uint64_t dq = sdesc_sw128(sm + kOffQ + q * 2 * kTileBytes, 0, 1024), dk = sdesc_sw128(sm + kOffK, 0, 1024);
   const uint64_t dh = sdesc_sw128(sm + kOffH, kTileBytes, 1024);
   const bool issue = elect_one();
   int ks = 0, hs = 1;                     // stages of the current key tile, and of the one before
   uint32_t k_par = 0, h_par = 1;          // and the parities of their barriers
-  uint32_t p_par[2] = {1, 1};             // parity of the weights of the tile before
-  uint32_t q_par[2] = {0, 0};
-  // O of tile q += P V: the second page's weights come first
-  auto second = [&](int q, bool first, bool last) {
-    const uint32_t d = tmem + kColO + q * 128, p = tmem + kColS + q * 128;
-    const uint64_t h = dh + hs * (2 * kTileBytes >> 4);
-    if (!kv_wait_warp([&] {
-          return kv_wait(&ctl->p_full[q][1], p_par[q], &ctl->abort, 100 + kBarP) &&
-                 kv_wait(&ctl->h_full[hs], h_par, &ctl->abort, 100 + kBarH);
-        }))
-      return false;
-    tc_fence_after();
-    if (issue) {
-#pragma unroll
-      for (int k = 4; k < 8; ++k) mma_f16_ts(d, p + 64 + (k - 4) * 8, h + k * 128, kIdO, k > 4 || !first);
-    }
-    if (!kv_wait_warp([&] { return kv_wait(&ctl->p_full[q][0], p_par[q], &ctl->abort, 100 + kBarP); })) return false;
-    tc_fence_after();
-    if (issue) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mma_f16_ts(d, p + k * 8, h + k * 128, kIdO, 1);
-      mma_commit(&ctl->o_full[q]);
-      if (last) mma_commit(&ctl->h_free[hs]);
-    }
-    __syncwarp();
-    return true;
-  };
+  uint32_t p_par = 1, q_par = 0;          // weights of the tile before; queries
   KvCursor cur;
 #pragma unroll 1
   for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
     const int tiles = __shfl_sync(0xffffffffu, cur.tiles(), 0);
     if (tiles == 0) continue;
-    const int q_tiles = __shfl_sync(0xffffffffu, many_item(a, cur).q_tiles, 0);
+    const bool mine = __shfl_sync(0xffffffffu, (int)(q < many_item(a, cur).q_tiles), 0);
 #pragma unroll 1
     for (int j = 0; j <= tiles; ++j) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (q >= q_tiles) continue;
-        if (j > 0 && !second(q, j == 1, q == q_tiles - 1)) return;
-        if (j == tiles) continue;
+      // copies this step needs; long complete as a rule, and out of the way of the weights' wait
+      if (j > 0 && !kv_wait_warp([&] { return kv_wait(&ctl->h_full[hs], h_par, &ctl->abort, 100 + kBarH); })) return;
+      if (j < tiles && !kv_wait_warp([&] { return kv_wait(&ctl->k_full[ks], k_par, &ctl->abort, 100 + kBarK); })) return;
+      if (mine) {
+        // the weights of the key tile before, or a new item's queries
         if (!kv_wait_warp([&] {
-              return (j > 0 || kv_wait(&ctl->q_full[q], q_par[q], &ctl->abort, 100 + kBarQ)) &&
-                     (q > 0 || kv_wait(&ctl->k_full[ks], k_par, &ctl->abort, 100 + kBarK));
+              return j > 0 ? kv_wait(&ctl->p_full[q], p_par, &ctl->abort, 100 + kBarP)
+                           : kv_wait(&ctl->q_full[q], q_par, &ctl->abort, 100 + kBarQ);
             }))
           return;
         tc_fence_after();
-        const uint32_t d = tmem + kColS + q * 128;
-        const uint64_t kk = dk + ks * (kTileBytes >> 4), qq = dq + q * (2 * kTileBytes >> 4);
-        if (issue) {
+        if (j > 0 && issue) {  // O += P V
+          const uint64_t h = dh + hs * (2 * kTileBytes >> 4);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // 16 keys a step
+            mma_f16_ts(d_o, d_s + kColP + 8 * k, h + k * 128, kIdO, k > 0 || j > 1);
+          if (j == tiles) mma_commit(&ctl->o_full[q]);
+        }
+        if (j < tiles && issue) {
+          const uint64_t kk = dk + ks * (kTileBytes >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // four steps with the high parts, four with the low ones
-            mma_f8(d, qq + (k >> 2) * (kTileBytes >> 4) + (k & 3) * 2, kk + (k & 3) * 2, kIdS, k > 0);
-          mma_commit(&ctl->s_full[q]);
-          if (q == q_tiles - 1) mma_commit(&ctl->k_free[ks]);
+            mma_f8(d_s, dq + (k >> 2) * (kTileBytes >> 4) + (k & 3) * 2, kk + (k & 3) * 2, kIdS, k > 0);
+          mma_commit(&ctl->s_full[q]);  // says too that the products with earlier values are done
         }
-        __syncwarp();
-        p_par[q] ^= 1;
+        if (j < tiles) p_par ^= 1;
       }
+      // without products of its own in the item this only counts the stages on
+      if (issue) {
+        if (j < tiles) mma_commit(&ctl->k_free[ks]);
+        if (j > 0) mma_commit(&ctl->h_free[hs]);
+      }
+      __syncwarp();
       if (j < tiles) {
         if (++ks == kKStages) {
           ks = 0;
@@ -220,8 +208,7 @@ __device__ __forceinline__ void many_mma(const KvAttnArgs& a, ManyCtl* ctl, uint
         }
       }
     }
-    q_par[0] ^= 1;
-    if (q_tiles == 2) q_par[1] ^= 1;
+    if (mine) q_par ^= 1;
   }
 }
 
@@ -436,7 +423,7 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
   const int q = threadIdx.x >> 7, row = threadIdx.x & 127, warp = row >> 5;
   const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
   const uint32_t t_s = tmem + lane_base + kColS + q * 128, t_o = tmem + lane_base + kColO + q * 128;
-  int i = 0, n = 0;  // key tiles of the run, and those this query tile took part in
+  int i = 0, n = 0, items = 0;  // key tiles of the run, those this query tile took part in, and its items with keys
   KvCursor cur;
 #pragma unroll 1
   for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
@@ -468,13 +455,13 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
           }))
         return;
       tc_fence_after();
-      uint32_t s0[32], s1[32];
+      // Four chunks of 32 keys, three of them in registers at a time: all are
+      // read for the maximum, and the first once more for its weights.
+      uint32_t s0[32], s1[32], s2[32];
       tmem_ld32(t_s, s0);
       tmem_ld32(t_s + 32, s1);
+      tmem_ld32(t_s + 64, s2);
       const float4 sc = *reinterpret_cast<const float4*>(ctl->scale[i % kScaleRing]);
-      // log2 of the value scales, powers of two
-      const float ev0 = (float)((int)(__float_as_uint(sc.z) >> 23) - 127), ev1 = (float)((int)(__float_as_uint(sc.w) >> 23) - 127);
-      const float fk0 = f * sc.x, fk1 = f * sc.y;
       int lo = 0, hi = 0;
       if (masked) {
         const int p = mi.past + t;
@@ -482,32 +469,30 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
         hi = (live ? (a.causal ? min(p + 1, it.len) : it.len) : 0) - key0;
       }
       const uint32_t* nan = ctl->nan_keys[stage];
-      // The maximum; the first page's scores are read again after it, the
-      // second one's stay in registers.  s is -inf only under a mask, and the
-      // factors are positive unless the row is NaN.
+      // log2 of the value scales, powers of two
+      const float fk0 = f * sc.x, ev0 = (float)((int)(__float_as_uint(sc.z) >> 23) - 127);
+      const float fk1 = f * sc.y, ev1 = (float)((int)(__float_as_uint(sc.w) >> 23) - 127);
       tmem_ld_done(s0);
       tmem_ld_done(s1);
+      tmem_ld_done(s2);
       if (masked) {
         mask32(s0, nan[0], lo, hi);
         mask32(s1, nan[1], lo - 32, hi - 32);
+        mask32(s2, nan[2], lo - 64, hi - 64);
       }
-      float top = fmaf(fmaxf(max32(s0), max32(s1)), fk0, ev0);
-      tmem_ld32(t_s + 64, s0);
-      tmem_ld32(t_s + 96, s1);
+      // s is -inf only under a mask, and the factors are positive unless the row is NaN
+      float top0 = max32(s0);
+      tmem_ld32(t_s + 96, s0);
+      top0 = fmaxf(top0, max32(s1));
+      float top1 = max32(s2);
       tmem_ld_done(s0);
-      tmem_ld_done(s1);
-      if (masked) {
-        mask32(s0, nan[2], lo - 64, hi - 64);
-        mask32(s1, nan[3], lo - 96, hi - 96);
-      }
-      top = fmaxf(top, fmaf(fmaxf(max32(s0), max32(s1)), fk1, ev1));
-      const bool grow = top > m + kLazy || (m == kNegInf && top > kNegInf);
+      if (masked) mask32(s0, nan[3], lo - 96, hi - 96);
+      top1 = fmaxf(top1, max32(s0));
+      const float top = fmaxf(fmaf(top0, fk0, ev0), fmaf(top1, fk1, ev1));
+      const bool grow = top > m + kLazy;
       if (__any_sync(0xffffffffu, grow)) {
         const float alpha = grow ? ex2(m - top) : 1.f;
-        if (j > 0) {
-          // O holds the tiles before this one: wait for the last of them, then rescale
-          if (!kv_wait_warp([&] { return kv_wait(&ctl->o_full[q], (n - 1) & 1, &ctl->abort, 100 + kBarO); })) return;
-          tc_fence_after();
+        if (j > 0) {  // O holds earlier tiles, whose products are done: the scores at hand came after them
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
             uint32_t o[16];
@@ -518,40 +503,28 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
             tmem_st16(t_o + 16 * c, o);
           }
         }
-        if (grow) {
-          l *= alpha;
-          m = top;
-        }
+        l *= alpha;
+        if (grow) m = top;
       }
       const float ref = m == kNegInf ? 0.f : m;
-      // A page's weights go over its own scores, the second page's first: the
-      // MMA warp starts on them while the first page's are computed.
-      float2 sum = make_float2(0.f, 0.f);
-      weights32(t_s + 64, s0, fk1, ev1 - ref, sum);
-      tmem_ld32(t_s, s0);
-      weights32(t_s + 80, s1, fk1, ev1 - ref, sum);
-      l = fmaf(sum.x + sum.y, __int_as_float((254 << 23) - __float_as_int(sc.w)), l);
-      tmem_st_wait();
-      tc_fence_before();
-      kv_arrive_warp(&ctl->p_full[q][1]);
-      tmem_ld32(t_s + 32, s1);
-      tmem_ld_done(s0);
+      // The weights go over scores this thread has read: columns 32 to 95.
+      float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+      weights32(t_s + 48, s1, fk0, ev0 - ref, sum0);
+      tmem_ld32(t_s, s1);
+      weights32(t_s + 64, s2, fk1, ev1 - ref, sum1);
+      weights32(t_s + 80, s0, fk1, ev1 - ref, sum1);
       tmem_ld_done(s1);
-      if (masked) {
-        mask32(s0, nan[0], lo, hi);
-        mask32(s1, nan[1], lo - 32, hi - 32);
-      }
-      sum = make_float2(0.f, 0.f);
-      weights32(t_s, s0, fk0, ev0 - ref, sum);
-      weights32(t_s + 16, s1, fk0, ev0 - ref, sum);
-      l = fmaf(sum.x + sum.y, __int_as_float((254 << 23) - __float_as_int(sc.z)), l);
+      if (masked) mask32(s1, nan[0], lo, hi);
+      weights32(t_s + 32, s1, fk0, ev0 - ref, sum0);
+      l = fmaf(sum0.x + sum0.y, __int_as_float((254 << 23) - __float_as_int(sc.z)), l);
+      l = fmaf(sum1.x + sum1.y, __int_as_float((254 << 23) - __float_as_int(sc.w)), l);
       tmem_st_wait();
       tc_fence_before();
-      kv_arrive_warp(&ctl->p_full[q][0]);
+      kv_arrive_warp(&ctl->p_full[q]);
     }
     // ---- the row's output ----
     if (tiles > 0) {
-      if (!kv_wait_warp([&] { return kv_wait(&ctl->o_full[q], (n - 1) & 1, &ctl->abort, 100 + kBarO); })) return;
+      if (!kv_wait_warp([&] { return kv_wait(&ctl->o_full[q], items++ & 1, &ctl->abort, 100 + kBarO); })) return;
       tc_fence_after();
     }
     const int64_t tok = it.tok0 + t;
@@ -607,19 +580,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&ctl.k_full[s], 1);
-      mbar_init(&ctl.k_free[s], 1);
+      mbar_init(&ctl.k_free[s], 2);
     }
     for (int s = 0; s < kVStages; ++s) {
       mbar_init(&ctl.v_full[s], 1);
       mbar_init(&ctl.v_free[s], 4);
       mbar_init(&ctl.h_full[s], 4);
-      mbar_init(&ctl.h_free[s], 1);
+      mbar_init(&ctl.h_free[s], 2);
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(&ctl.q_full[q], 4);
       mbar_init(&ctl.s_full[q], 1);
-      mbar_init(&ctl.p_full[q][0], 4);
-      mbar_init(&ctl.p_full[q][1], 4);
+      mbar_init(&ctl.p_full[q], 4);
       mbar_init(&ctl.o_full[q], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&ctl.scale_full[s], 1);
@@ -647,8 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       many_values(a, &ctl, sm);
     } else if (warp == kTmaWarp) {
       many_load(a, &ctl, sm, &kmap, &vmap);
-    } else if (warp == kMmaWarp) {
-      many_mma(a, &ctl, smem_u32(sm), tmem);
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+      many_mma(a, &ctl, smem_u32(sm), tmem, __shfl_sync(0xffffffffu, warp - kMmaWarp, 0));
     }
   }
   __syncwarp();

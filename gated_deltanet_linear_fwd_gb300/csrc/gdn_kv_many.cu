@@ -20,7 +20,8 @@
 // scale 2^e_v is folded into the exponent, P_j = 2^(x_j + e_v - m), so P times
 // the codes is the output in units of 2^m; the softmax's sum is of P_j 2^-e_v in
 // fp32.  m follows the running maximum of x + e_v only when that has grown by
-// more than 8, so O in tensor memory is rarely rescaled; P stays below 2^8.
+// more than 12, so O in tensor memory is rarely rescaled; P stays below 2^12,
+// within fp16.
 //
 // Tensor memory (512 columns): S of either tile (P over its middle) and O
 // of either tile.  Each tile has an MMA warp that alternates P V of
@@ -54,7 +55,7 @@ enum { kBarK = 1, kBarV, kBarKFree, kBarVFree, kBarQ, kBarS, kBarP, kBarO, kBarS
 
 struct ManyCtl {
   uint64_t k_full[kKStages], k_free[kKStages], v_full[kVStages], v_free[kVStages], h_full[kHStages], h_free[kHStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], scale_full[kScaleRing];
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], scale_full[kScaleRing];
   alignas(16) float scale[kScaleRing][4];  // key scales of the tile's two pages, value scales
   uint32_t nan_keys[kHStages][4];   // keys of a masked tile whose values hold a NaN code
   KvRunScratch run;
@@ -168,19 +169,25 @@ __device__ __forceinline__ void many_mma(const KvAttnArgs& a, ManyCtl* ctl, uint
       if (j > 0 && !kv_wait_warp([&] { return kv_wait(&ctl->h_full[hs], h_par, &ctl->abort, 100 + kBarH); })) return;
       if (j < tiles && !kv_wait_warp([&] { return kv_wait(&ctl->k_full[ks], k_par, &ctl->abort, 100 + kBarK); })) return;
       if (mine) {
-        // the weights of the key tile before, or a new item's queries
-        if (!kv_wait_warp([&] {
-              return j > 0 ? kv_wait(&ctl->p_full[q], p_par, &ctl->abort, 100 + kBarP)
-                           : kv_wait(&ctl->q_full[q], q_par, &ctl->abort, 100 + kBarQ);
-            }))
-          return;
-        tc_fence_after();
-        if (j > 0 && issue) {  // O += P V
+        if (j > 0) {  // O += P V as the weights of the key tile before come, the second page's first
           const uint64_t h = dh + hs * (2 * kTileBytes >> 4);
+          if (!kv_wait_warp([&] { return kv_wait(&ctl->p_full[q][1], p_par, &ctl->abort, 100 + kBarP); })) return;
+          tc_fence_after();
+          if (issue) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // 16 keys a step
-            mma_f16_ts(d_o, d_s + kColP + 8 * k, h + k * 128, kIdO, k > 0 || j > 1);
-          if (j == tiles) mma_commit(&ctl->o_full[q]);
+            for (int k = 4; k < 8; ++k)  // 16 keys a step
+              mma_f16_ts(d_o, d_s + kColP + 8 * k, h + k * 128, kIdO, k > 4 || j > 1);
+          }
+          if (!kv_wait_warp([&] { return kv_wait(&ctl->p_full[q][0], p_par, &ctl->abort, 100 + kBarP); })) return;
+          tc_fence_after();
+          if (issue) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16_ts(d_o, d_s + kColP + 8 * k, h + k * 128, kIdO, 1);
+            if (j == tiles) mma_commit(&ctl->o_full[q]);
+          }
+        } else {
+          if (!kv_wait_warp([&] { return kv_wait(&ctl->q_full[q], q_par, &ctl->abort, 100 + kBarQ); })) return;
+          tc_fence_after();
         }
         if (j < tiles && issue) {
           const uint64_t kk = dk + ks * (kTileBytes >> 4);
@@ -331,7 +338,7 @@ __device__ __forceinline__ float2 add2(float2 a, float b0, float b1) {
 }
 
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kLazy = 8.f;
+constexpr float kLazy = 12.f;
 
 // Under the masks: -inf for keys outside [lo, hi) of these 32, NaN for keys
 // whose values hold one.
@@ -468,25 +475,35 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
         lo = (a.window > 0 ? max(0, p - a.window + 1) : 0) - key0;
         hi = (live ? (a.causal ? min(p + 1, it.len) : it.len) : 0) - key0;
       }
-      const uint32_t* nan = ctl->nan_keys[stage];
+      if (masked) {
+        // the masked scores back into tensor memory, by one copy of this code
+        tmem_ld_done(s0);
+        tmem_ld_done(s1);
+        tmem_ld_done(s2);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(t_s + 32 * c, s0);
+          tmem_ld_done(s0);
+          mask32(s0, ctl->nan_keys[stage][c], lo - 32 * c, hi - 32 * c);
+          tmem_st32(t_s + 32 * c, s0);
+        }
+        tmem_st_wait();
+        tmem_ld32(t_s, s0);
+        tmem_ld32(t_s + 32, s1);
+        tmem_ld32(t_s + 64, s2);
+      }
       // log2 of the value scales, powers of two
       const float fk0 = f * sc.x, ev0 = (float)((int)(__float_as_uint(sc.z) >> 23) - 127);
       const float fk1 = f * sc.y, ev1 = (float)((int)(__float_as_uint(sc.w) >> 23) - 127);
       tmem_ld_done(s0);
       tmem_ld_done(s1);
       tmem_ld_done(s2);
-      if (masked) {
-        mask32(s0, nan[0], lo, hi);
-        mask32(s1, nan[1], lo - 32, hi - 32);
-        mask32(s2, nan[2], lo - 64, hi - 64);
-      }
       // s is -inf only under a mask, and the factors are positive unless the row is NaN
       float top0 = max32(s0);
       tmem_ld32(t_s + 96, s0);
       top0 = fmaxf(top0, max32(s1));
       float top1 = max32(s2);
       tmem_ld_done(s0);
-      if (masked) mask32(s0, nan[3], lo - 96, hi - 96);
       top1 = fmaxf(top1, max32(s0));
       const float top = fmaxf(fmaf(top0, fk0, ev0), fmaf(top1, fk1, ev1));
       const bool grow = top > m + kLazy;
@@ -509,18 +526,20 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
       const float ref = m == kNegInf ? 0.f : m;
       // The weights go over scores this thread has read: columns 32 to 95.
       float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-      weights32(t_s + 48, s1, fk0, ev0 - ref, sum0);
-      tmem_ld32(t_s, s1);
       weights32(t_s + 64, s2, fk1, ev1 - ref, sum1);
+      tmem_ld32(t_s, s2);
       weights32(t_s + 80, s0, fk1, ev1 - ref, sum1);
-      tmem_ld_done(s1);
-      if (masked) mask32(s1, nan[0], lo, hi);
-      weights32(t_s + 32, s1, fk0, ev0 - ref, sum0);
+      tmem_st_wait();
+      tc_fence_before();
+      kv_arrive_warp(&ctl->p_full[q][1]);
+      weights32(t_s + 48, s1, fk0, ev0 - ref, sum0);
+      tmem_ld_done(s2);
+      weights32(t_s + 32, s2, fk0, ev0 - ref, sum0);
       l = fmaf(sum0.x + sum0.y, __int_as_float((254 << 23) - __float_as_int(sc.z)), l);
       l = fmaf(sum1.x + sum1.y, __int_as_float((254 << 23) - __float_as_int(sc.w)), l);
       tmem_st_wait();
       tc_fence_before();
-      kv_arrive_warp(&ctl->p_full[q]);
+      kv_arrive_warp(&ctl->p_full[q][0]);
     }
     // ---- the row's output ----
     if (tiles > 0) {
@@ -591,7 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int q = 0; q < 2; ++q) {
       mbar_init(&ctl.q_full[q], 4);
       mbar_init(&ctl.s_full[q], 1);
-      mbar_init(&ctl.p_full[q], 4);
+      mbar_init(&ctl.p_full[q][0], 4);
+      mbar_init(&ctl.p_full[q][1], 4);
       mbar_init(&ctl.o_full[q], 1);
     }
     for (int s = 0; s < kScaleRing; ++s) mbar_init(&ctl.scale_full[s], 1);

@@ -78,8 +78,8 @@ class gdn_kv_dims(ctypes.Structure):
 
 class gdn_kv_plan_t(ctypes.Structure):
     _fields_ = [("path", ctypes.c_int), ("rows", ctypes.c_int), ("max_row_tiles", ctypes.c_int),
-                ("n_ctas", ctypes.c_int), ("n_seqs", ctypes.c_int), ("T", ctypes.c_int), ("h_q", ctypes.c_int),
-                ("h_kv", ctypes.c_int), ("dtype", ctypes.c_int), ("max_q_len", ctypes.c_int),
+                ("n_ctas", ctypes.c_int), ("item_cost", ctypes.c_int), ("n_seqs", ctypes.c_int), ("T", ctypes.c_int),
+                ("h_q", ctypes.c_int), ("h_kv", ctypes.c_int), ("dtype", ctypes.c_int), ("max_q_len", ctypes.c_int),
                 ("off_desc", ctypes.c_size_t), ("off_ml", ctypes.c_size_t), ("off_o", ctypes.c_size_t),
                 ("workspace_bytes", ctypes.c_size_t)]
 

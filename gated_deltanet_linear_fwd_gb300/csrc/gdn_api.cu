@@ -856,15 +856,18 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   if ((int64_t)d->T * group > 0x7fffffff - 4096) return GDN_ERR_INVALID_ARG;
   p.path = kKvPathSimt;
   p.rows = 16;
+  p.item_cost = 1;
   int per_sm = 2;
   const int64_t rows = (int64_t)max_q_len * group;
   if (d->dtype == GDN_BF16 && rows <= 64) {
     p.path = kKvPathFew;
     p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p.item_cost = 2;
     per_sm = kv_few_ctas_per_sm(p.rows);
   } else if (d->dtype == GDN_BF16) {
     p.path = kKvPathMany;
     p.rows = 256;
+    p.item_cost = 6;
     per_sm = 1;
   }
   p.max_row_tiles = std::max<int>(1, (int)(((int64_t)max_q_len * group + p.rows - 1) / p.rows));
@@ -920,6 +923,7 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
   a.rows = plan->rows;
   a.max_row_tiles = plan->max_row_tiles;
   a.n_ctas = plan->n_ctas;
+  a.item_cost = plan->item_cost;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.desc = reinterpret_cast<int4*>(ws + plan->off_desc);
   a.ml = reinterpret_cast<float2*>(ws + plan->off_ml);

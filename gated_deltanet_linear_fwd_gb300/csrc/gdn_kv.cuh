@@ -4,6 +4,7 @@
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "gdn_internal.cuh"
 #include "sm103_ptx.cuh"
@@ -51,6 +52,7 @@ struct KvAttnArgs {
   int group;               // query heads per key/value head, rounded up
   int rows, max_row_tiles; // rows of a row tile; row tiles per (sequence, head)
   int n_ctas;              // 0: CTA i takes item i whole
+  int item_cost;           // what beginning and ending an item costs, in key tiles
   int4* desc;              // [n_ctas] item whose first part this CTA made: {sequence, row tile, head, last CTA}
   float2* ml;              // [2 n_ctas, rows] running maximum (log2) and sum of a part
   float* o;                // [2 n_ctas, rows, 128] unnormalised output of a part
@@ -114,13 +116,29 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   return c;
 }
 
+// Two fp32 (below 2^9) as e4m3 parts, x = hi + lo: four leading bits and the
+// next four; through fp16, whose 11 bits the parts do not reach.
+__device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  uint32_t x16, h16;
+  uint16_t h, l;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x16) : "f"(x1), "f"(x0));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(x16));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h));
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x16), *reinterpret_cast<const __half2*>(&h16));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t*>(&r)));
+  hi = h;
+  lo = l;
+}
+
 // ---- sharing out an attention call ----
 // An item is (sequence, row tile, key/value head); its units are its key
-// tiles, at least one (an item without keys still writes zeros).  All units,
-// in the order sequence, row tile, head, tile, are cut into n_ctas equal
-// runs, one a CTA, so the SMs get the same number of key tiles whatever the
-// lengths are.  A run covers whole items and at most one part of an item at
-// each end; parts go to the workspace and the combine kernel joins them.
+// tiles, at least one (an item without keys still writes zeros), after
+// item_cost units that stand for its beginning and end.  All units, in the
+// order sequence, row tile, head, tile, are cut into n_ctas equal runs, one a
+// CTA, so the SMs get the same amount of work whatever the lengths are.  A run
+// covers whole items and at most one part of an item at each end (a cut among
+// the item_cost units leaves the item whole to the later run); parts go to
+// the workspace and the combine kernel joins them.
 struct KvItem {
   int tok0, n, len;       // the sequence
   int first_tile, tiles;  // key tiles its masks touch; tiles < 0: no such item
@@ -147,12 +165,15 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs& a, int seq, int rt) 
   return it;
 }
 __device__ __forceinline__ int kv_units(const KvItem& it) { return it.tiles < 0 ? 0 : max(1, it.tiles); }
+__device__ __forceinline__ int kv_cost(const KvAttnArgs& a, const KvItem& it) {
+  return it.tiles < 0 ? 0 : a.item_cost + max(1, it.tiles);
+}
 
 struct KvRun {
-  int seq, rt, head, off;  // first item of the run and the unit of it that the run starts with
+  int seq, rt, head, off;  // first item of the run and the unit of it (of item_cost + tiles) that the run starts with
   int64_t begin, end;      // units
   int64_t total;           // units of the call
-  int ctas;                // CTAs that have a run: no more than there are units, so none is empty
+  int ctas;                // CTAs that have a run: no more than there are units
 };
 
 // A CTA's run, found by all its threads (NT of them, a multiple of 32) from
@@ -195,7 +216,7 @@ __device__ __noinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
       r.rt = e % a.max_row_tiles;
       r.off = 0;
       r.begin = 0;
-      r.end = r.total = kv_units(kv_item(a, r.seq, r.rt));
+      r.end = r.total = kv_cost(a, kv_item(a, r.seq, r.rt));
       r.ctas = 0;
       sc->run = r;
     }
@@ -204,7 +225,7 @@ __device__ __noinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
   }
   int64_t sum = 0;
 #pragma unroll 1
-  for (int e = tid; e < entries; e += NT) sum += kv_units(kv_item(a, e / a.max_row_tiles, e % a.max_row_tiles));
+  for (int e = tid; e < entries; e += NT) sum += kv_cost(a, kv_item(a, e / a.max_row_tiles, e % a.max_row_tiles));
   int64_t total;
   block_inclusive_scan<NT>(sum, sc, total);
   total *= a.c.h_kv;
@@ -221,7 +242,7 @@ __device__ __noinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
 #pragma unroll 1
   for (int e0 = 0; e0 < entries && base <= begin && begin < end; e0 += NT) {
     const int e = e0 + tid, seq = e / a.max_row_tiles, rt = e % a.max_row_tiles;
-    const int u = e < entries ? kv_units(kv_item(a, seq, rt)) : 0;
+    const int u = e < entries ? kv_cost(a, kv_item(a, seq, rt)) : 0;
     int64_t sub;
     const int64_t incl = base + block_inclusive_scan<NT>((int64_t)u * a.c.h_kv, sc, sub);
     const int64_t excl = incl - (int64_t)u * a.c.h_kv;
@@ -241,25 +262,29 @@ __device__ __noinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
 struct KvCursor {
   KvItem it;
   int seq, rt, head;
-  int off, len;       // units [off, off + len) of the item belong to the run
-  int at, end;        // next unit and end, from the run's first unit
+  int off, len;       // tiles [off, off + len) of the item belong to the run; len = 0: the run is over
+  int base, end;      // unit the item starts with, and the run's end, from the run's first unit
+  __device__ __forceinline__ void clip(const KvAttnArgs& a) {
+    len = max(0, min(kv_units(it), end - base - a.item_cost) - off);
+  }
   __device__ __forceinline__ void start(const KvAttnArgs& a, const KvRun& r) {
     seq = r.seq;
     rt = r.rt;
     head = r.head;
-    off = r.off;
-    at = 0;
     end = (int)(r.end - r.begin);
-    if (at < end) {
+    len = 0;
+    if (end > 0) {
+      base = -r.off;
+      off = max(0, r.off - a.item_cost);
       it = kv_item(a, seq, rt);
-      len = min(end, kv_units(it) - off);
+      clip(a);
     }
   }
-  __device__ __forceinline__ bool valid() const { return at < end; }
+  __device__ __forceinline__ bool valid() const { return len > 0; }
   __device__ __forceinline__ void next(const KvAttnArgs& a) {
-    at += len;
-    off = 0;
-    if (at >= end) return;
+    base += kv_cost(a, it);
+    off = len = 0;
+    if (base >= end) return;
     if (++head == a.c.h_kv) {
       head = 0;
       ++rt;
@@ -269,13 +294,10 @@ struct KvCursor {
           if (it.tiles >= 0) break;
         }
         rt = 0;
-        if (++seq >= a.c.n_seqs) {
-          at = end;
-          return;
-        }
+        if (++seq >= a.c.n_seqs) return;
       }
     }
-    len = min(end - at, kv_units(it));
+    clip(a);
   }
   // key tiles [tile_begin, tile_begin + tiles) of the run's part of the item
   __device__ __forceinline__ int tiles() const { return it.tiles == 0 ? 0 : len; }
@@ -286,8 +308,8 @@ struct KvCursor {
 
 // The last CTA that has a part of the item whose first part this cursor
 // stands on: CTA c owns unit u when c = floor(((u + 1) ctas - 1) / total).
-__device__ __forceinline__ int kv_last_cta(const KvRun& r, const KvCursor& c) {
-  const int64_t item_end = r.begin + c.at + kv_units(c.it);
+__device__ __forceinline__ int kv_last_cta(const KvAttnArgs& a, const KvRun& r, const KvCursor& c) {
+  const int64_t item_end = r.begin + c.base + kv_cost(a, c.it);
   return (int)((item_end * r.ctas - 1) / r.total);
 }
 

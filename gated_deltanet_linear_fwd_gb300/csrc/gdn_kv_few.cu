@@ -194,19 +194,6 @@ __device__ __forceinline__ void few_mma(const KvAttnArgs& a, FewCtl<NR>* ctl, ui
 }
 
 // ---------------------------------------------------------------- softmax warpgroups
-// Two fp32 pairs (a row pair's weights) to e4m3 parts: hi + lo.
-__device__ __forceinline__ void split_pair(float p0, float p1, uint32_t& hi, uint32_t& lo) {
-  uint32_t h16;
-  uint16_t h, l;
-  const uint32_t p16 = pack_f16x2(p0, p1);  // 11 bits: the parts keep 8
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(p16));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h));
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&p16), *reinterpret_cast<const __half2*>(&h16));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t*>(&r)));
-  hi = h;
-  lo = l;
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -380,7 +367,7 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
       uint8_t* p = sm + F::kOffP + buf * (F::kN * kKvTile) + (wg * (2 * R / 16)) * (16 * kKvTile) + tid * 16;
       uint32_t hi[R / 2], lo[R / 2];
 #pragma unroll
-      for (int r = 0; r < R / 2; ++r) split_pair(x[2 * r], x[2 * r + 1], hi[r], lo[r]);
+      for (int r = 0; r < R / 2; ++r) split_e4m3(x[2 * r], x[2 * r + 1], hi[r], lo[r]);
       if (R == 8) {
         *reinterpret_cast<uint4*>(p) = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
       } else {
@@ -463,7 +450,7 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
         if (tid == r) a.ml[row + r] = make_float2(m[r] - 8.f, l[r]);
       }
       if (threadIdx.x == 0 && cur.off == 0)
-        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(ctl->run.run, cur));
+        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(a, ctl->run.run, cur));
     }
     if (tiles > 0) named_bar_sync(1, F::kSoft);  // the sums are read before the next item's are written
   }

@@ -36,9 +36,9 @@ namespace gdn {
 namespace {
 
 constexpr int kRows = 256;
-constexpr int kThreads = 640;  // two softmax warpgroups, one converting values, one of TMA and MMA warps
+constexpr int kThreads = 512;  // two softmax warpgroups, one converting values, one of TMA and MMA warps
 constexpr int kValuesWarp = 8, kTmaWarp = 12, kMmaWarp = 13;  // MMA warps 13 and 14
-constexpr int kSoftRegs = 144, kOtherRegs = 64;  // 256 x 144 + 384 x 64 = 640 x 96, the registers at launch
+constexpr int kSoftRegs = 168, kOtherRegs = 88;  // 256 x 168 + 256 x 88 = 512 x 128, the registers at launch
 constexpr int kTileBytes = kKvTile * kHeadDim;
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScaleRing = 8;
 
@@ -372,58 +372,83 @@ __device__ __forceinline__ void weights32(uint32_t t_p, const uint32_t (&s)[32],
   tmem_st16(t_p, w);
 }
 
-// The item's query rows of tile q into their two e4m3 parts; a warp takes its
-// own 32 rows, a lane four columns.  Returns the score factor of the thread's row.
-__device__ __forceinline__ float many_queries(const KvAttnArgs& a, const KvCursor& cur, int q, uint8_t* sm) {
-  const int warp = (threadIdx.x & 127) >> 5, lane = threadIdx.x & 31;
-  const int head0 = kv_first_q_head(a.c, cur.head), group = kv_first_q_head(a.c, cur.head + 1) - head0;
-  const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;  // the row's factor stays positive
-  uint8_t* hi_tile = sm + kOffQ + q * 2 * kTileBytes;
-  float f = 0.f;
-  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)cur.it.tok0 * a.q_stride +
-                             head0 * kHeadDim + 4 * lane;
-  const int rr = cur.rt * kRows + q * 128 + 32 * warp;
-  int t = rr / a.group, g = rr % a.group;
-#pragma unroll 1
-  for (int k0 = 0; k0 < 32; k0 += 16) {
-    uint2 row[16];  // 16 rows' loads in flight together
+// This thread's query row (null: zeros) into its two e4m3 parts in shared
+// memory; returns its score factor.
+__device__ __noinline__ float many_query(float scale_log2, const __nv_bfloat16* src, int row, uint8_t* hi_tile) {
+  uint4 x[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      row[e] = make_uint2(0, 0);
-      if (t < cur.it.n && g < group) row[e] = __ldg(reinterpret_cast<const uint2*>(src + t * a.q_stride + g * kHeadDim));
-      if (++g == a.group) {
-        g = 0;
-        ++t;
+  for (int c = 0; c < 16; ++c) x[c] = src ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+  // the largest magnitude: bf16 bits without the sign are ordered like integers
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(x[c].x & 0x7fff7fffu, x[c].y & 0x7fff7fffu), __vmaxu2(x[c].z & 0x7fff7fffu, x[c].w & 0x7fff7fffu)));
+  const uint32_t m = max(m2 << 16, m2 & 0xffff0000u);
+  // below 2^-102 a row's scores are zero for any key the cache can hold
+  const int ex = m < 0x7f800000u ? e4m3_scale_exp(m, -110) : 0;
+  const float inv = scale_log2 < 0.f ? -pow2f(-ex) : pow2f(-ex);  // the row's factor stays positive
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t w[8] = {x[2 * c].x, x[2 * c].y, x[2 * c].z, x[2 * c].w, x[2 * c + 1].x, x[2 * c + 1].y, x[2 * c + 1].z, x[2 * c + 1].w};
+    uint32_t hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) split_e4m3(__uint_as_float(w[e] << 16) * inv, __uint_as_float(w[e] & 0xffff0000u) * inv, hi[e], lo[e]);
+    const uint32_t at = sw128_offset(row, c);
+    *reinterpret_cast<uint4*>(hi_tile + at) = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
+    *reinterpret_cast<uint4*>(hi_tile + kTileBytes + at) = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+  }
+  // a row that is not finite gives NaN
+  return m < 0x7f800000u ? pow2f(ex) * fabsf(scale_log2) : __int_as_float(0x7fffffff);
+}
+
+// 256 bytes of each of the warp's 32 rows to global memory, 512 contiguous
+// bytes an instruction, through the warp's part of `stage` (8 KB).  dst: this
+// thread's row, or null.
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&w)[64], uint8_t* dst) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    *reinterpret_cast<uint4*>(stage + lane * 256 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  __syncwarp();
+  const int c = lane & 15;
+#pragma unroll 4
+  for (int k = 0; k < 16; ++k) {
+    const int row = 2 * k + (lane >> 4);
+    uint8_t* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 256 + ((c ^ (row & 7)) << 4));
+    if (to) reinterpret_cast<uint4*>(to)[c] = v;
+  }
+  __syncwarp();
+}
+
+// The warp's 32 rows of O out of tensor memory: divided by l in bf16, or, for
+// a part of an item, as they are.  dst: this thread's row, or null.
+__device__ __noinline__ void many_output(uint32_t t_o, bool any, bool whole, float l, uint8_t* stage, uint8_t* dst) {
+  uint32_t w[64];
+  if (whole) {
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      uint32_t o[32];
+      if (any) {
+        tmem_ld32(t_o + 32 * h, o);
+        tmem_ld_done(o);
       }
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        w[16 * h + k] = !any || l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
     }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const uint2 w = row[e];
-      const float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                          __uint_as_float(w.y & 0xffff0000u)};
-      uint32_t m = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) m = max(m, __float_as_uint(x[c]) & 0x7fffffffu);
-      m = __reduce_max_sync(0xffffffffu, m);
-      // below 2^-102 a row's scores are zero for any key the cache can hold
-      const int ex = m < 0x7f800000u ? e4m3_scale_exp(m, -110) : 0;
-      const float inv = pow2f(-ex) * sign;
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float y0 = x[2 * c] * inv, y1 = x[2 * c + 1] * inv;
-        hi[c] = f32x2_to_e4m3x2(y0, y1);
-        const float2 h = e4m3x2_to_f32x2(hi[c]);
-        lo[c] = f32x2_to_e4m3x2(y0 - h.x, y1 - h.y);
-      }
-      const uint32_t at = sw128_offset(32 * warp + k0 + e, lane >> 2) + 4 * (lane & 3);
-      *reinterpret_cast<uint32_t*>(hi_tile + at) = hi[0] | hi[1] << 16;
-      *reinterpret_cast<uint32_t*>(hi_tile + kTileBytes + at) = lo[0] | lo[1] << 16;
-      // a row that is not finite gives NaN
-      if (lane == k0 + e) f = m < 0x7f800000u ? pow2f(ex) * fabsf(a.scale_log2) : __int_as_float(0x7fffffff);
+    store_rows(stage, w, dst);
+  } else {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      tmem_ld32(t_o + 64 * h, w);
+      tmem_ld32(t_o + 64 * h + 32, w + 32);
+      tmem_ld_done(w);
+      tmem_ld_done(w + 32);
+      store_rows(stage, w, dst + 256 * h);
     }
   }
-  return f;
 }
 
 __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, uint8_t* sm, uint32_t tmem) {
@@ -446,7 +471,8 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
     const bool live = t < it.n && g < kv_first_q_head(a.c, cur.head + 1) - head0;
     float f = 0.f, m = kNegInf, l = 0.f;
     if (tiles > 0) {
-      f = many_queries(a, cur, q, sm);
+      f = many_query(a.scale_log2, live ? reinterpret_cast<const __nv_bfloat16*>(a.q) + (int64_t)(it.tok0 + t) * a.q_stride + (head0 + g) * kHeadDim : nullptr,
+                     row, sm + kOffQ + q * 2 * kTileBytes);
       fence_proxy_async_smem();
       kv_arrive_warp(&ctl->q_full[q]);
     }
@@ -549,42 +575,17 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
     const int64_t tok = it.tok0 + t;
     const size_t part = (size_t)cur.slot() * kRows + q * 128 + row;
     const bool whole = cur.whole();
-    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + (head0 + g) * kHeadDim;
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-#pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
-      uint32_t o[16];
-      if (tiles > 0) {
-        tmem_ld16(t_o + 16 * c, o);
-        tmem_ld_wait(o);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0;
-      }
-      if (whole) {
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-            reinterpret_cast<uint4*>(dst + 16 * c)[e] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          reinterpret_cast<uint4*>(a.o + part * kHeadDim + 16 * c)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-      }
-    }
+    // through the tile's queries in shared memory, which no product reads any more
+    uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + (head0 + g) * kHeadDim)
+                         : reinterpret_cast<uint8_t*>(a.o + part * kHeadDim);
+    many_output(t_o, tiles > 0, whole, l, sm + kOffQ + q * 2 * kTileBytes + warp * 8192, whole && !live ? nullptr : dst);
     tc_fence_before();
     if (whole) {
       if (live && a.lse) a.lse[tok * a.c.h_q + head0 + g] = kv_lse(m, l);
     } else {
       a.ml[part] = make_float2(m, l);
       if (threadIdx.x == 0 && cur.off == 0)
-        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(ctl->run.run, cur));
+        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(a, ctl->run.run, cur));
     }
   }
 }

@@ -33,6 +33,12 @@ __device__ __forceinline__ float load_elem(const float* p) { return *p; }
 __device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store_elem(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store_elem(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float c, float d) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const KvAttnArgs a) {
@@ -147,81 +153,80 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const KvAttnArgs a)
       for (int e = 0; e < 8; ++e) a.o[row * kHeadDim + 8 * c + e] = o[e];
       if (c == 0) a.ml[row] = make_float2(m, l);
       if (tid == 0 && cur.off == 0)
-        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(run, cur));
+        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(a, run, cur));
     }
   }
 }
 
-// Joins the parts of an item: with M the largest of their maxima m_i,
-// out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Block (c, y) looks after
-// the item whose first part CTA c made, rows y kRowsPerBlock ...; kWarps warps
-// share a row's parts (many when few rows meet a long axis), a lane holds 4
-// columns.  Reads each part once.
+// Joins the parts of an item: with M the largest of their maxima m_i and
+// f_i = 2^(m_i - M), out = sum f_i o_i / sum f_i l_i.  Block (c, y) looks after
+// the item whose first part CTA c made and its rows y, y + gridDim.y, ... a
+// warp (or kWarps of them when few rows meet many parts) a row, a lane four
+// columns.  The factors come first, a part a lane, so that the outputs' loads
+// do not wait for one another.  Reads each part once.
 template <typename T, int kWarps>
 __global__ void __launch_bounds__(256) combine_kernel(const KvAttnArgs a) {
-  constexpr int kRowsPerBlock = 8 / kWarps;
+  constexpr int kRowsPerPass = 8 / kWarps;
   __shared__ float4 so[8][32];
-  __shared__ float2 sml[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp % kWarps;
   grid_dependency_wait();
   const int4 d = a.desc[blockIdx.x];
   if (d.x < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kRowsPerBlock + warp / kWarps, w = warp % kWarps;
   const KvSeq s = kv_seq(a.c, d.x);
-  const int rr = d.y * a.rows + row, t = rr / a.group, j = kv_first_q_head(a.c, d.z) + rr % a.group;
-  const bool live = row < a.rows && t < s.n && j < kv_first_q_head(a.c, d.z + 1);
-  float m = -__int_as_float(0x7f800000), l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (live) {
-    // parts: slot 2 c + 1 of the first CTA, slot 2 c of the others
-    const int parts = d.w - (int)blockIdx.x + 1;
-#pragma unroll 4
-    for (int i = w; i < parts; i += kWarps) {
-      const size_t at = (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * a.rows + row;
-      const float2 ml = a.ml[at];
-      const float4 x = reinterpret_cast<const float4*>(a.o + at * kHeadDim)[lane];
-      const float top = fmaxf(m, ml.x), ref = top == -__int_as_float(0x7f800000) ? 0.f : top;
-      const float f = exp2f(m - ref), g = exp2f(ml.x - ref);
-      l = l * f + ml.y * g;
-      o.x = o.x * f + x.x * g;
-      o.y = o.y * f + x.y * g;
-      o.z = o.z * f + x.z * g;
-      o.w = o.w * f + x.w * g;
-      m = top;
-    }
-  }
-  if (kWarps > 1) {
-    so[warp][lane] = o;
-    if (lane == 0) sml[warp] = make_float2(m, l);
-    __syncthreads();
-    if (w != 0) return;
-    float top = m;
+  const int head0 = kv_first_q_head(a.c, d.z), group = kv_first_q_head(a.c, d.z + 1) - head0;
+  const int parts = d.w - (int)blockIdx.x + 1;
+  // part i: slot 2 c + 1 of the first CTA, slot 2 (c + i) of the others
+  auto slot = [&](int i) { return (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)); };
+  for (int row0 = blockIdx.y * kRowsPerPass; row0 < a.rows; row0 += gridDim.y * kRowsPerPass) {
+    const int row = row0 + warp / kWarps, rr = d.y * a.rows + row, t = rr / a.group, g = rr - t * a.group;
+    const bool live = row < a.rows && t < s.n && g < group;
+    float m = -__int_as_float(0x7f800000), l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+      for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.ml[slot(i) * a.rows + row].x);
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i) top = fmaxf(top, sml[warp + i].x);
-    const float ref = top == -__int_as_float(0x7f800000) ? 0.f : top;
-    const float f = exp2f(m - ref);
-    l *= f;
-    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+      for (int e = 16; e > 0; e >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, e));
+      const float ref = m == -__int_as_float(0x7f800000) ? 0.f : m;
+      for (int i0 = 0; i0 < parts; i0 += 32) {
+        float f = 0.f;
+        if (i0 + lane < parts) {
+          const float2 ml = a.ml[slot(i0 + lane) * a.rows + row];
+          f = exp2f(ml.x - ref);
+          l += f * ml.y;
+        }
+        const int n = min(32, parts - i0);
+#pragma unroll 8
+        for (int i = w; i < n; i += kWarps) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(a.o + (slot(i0 + i) * a.rows + row) * kHeadDim) + lane);
+          const float fi = __shfl_sync(0xffffffffu, f, i);
+          o.x = fmaf(x.x, fi, o.x);
+          o.y = fmaf(x.y, fi, o.y);
+          o.z = fmaf(x.z, fi, o.z);
+          o.w = fmaf(x.w, fi, o.w);
+        }
+      }
 #pragma unroll
-    for (int i = 1; i < kWarps; ++i) {
-      const float g = exp2f(sml[warp + i].x - ref);
-      const float4 x = so[warp + i][lane];
-      l += sml[warp + i].y * g;
-      o.x += x.x * g;
-      o.y += x.y * g;
-      o.z += x.z * g;
-      o.w += x.w * g;
+      for (int e = 16; e > 0; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
     }
-    m = top;
+    if (kWarps > 1) {
+      so[warp][lane] = o;
+      __syncthreads();
+      if (w == 0) {
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) {
+          const float4 x = so[warp + i][lane];
+          o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+        }
+      }
+      __syncthreads();
+      if (w != 0) continue;
+    }
+    if (!live) continue;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    T* dst = reinterpret_cast<T*>(a.out) + (int64_t)(s.tok0 + t) * a.out_stride + (head0 + g) * kHeadDim + 4 * lane;
+    store4(dst, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (a.lse && lane == 0) a.lse[(int64_t)(s.tok0 + t) * a.c.h_q + head0 + g] = kv_lse(m, l);
   }
-  if (!live) return;
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  T* dst = reinterpret_cast<T*>(a.out) + (int64_t)(s.tok0 + t) * a.out_stride + j * kHeadDim + 4 * lane;
-  store_elem(dst, o.x * inv);
-  store_elem(dst + 1, o.y * inv);
-  store_elem(dst + 2, o.z * inv);
-  store_elem(dst + 3, o.w * inv);
-  if (a.lse && lane == 0) a.lse[(int64_t)(s.tok0 + t) * a.c.h_q + j] = kv_lse(m, l);
 }
 
 }  // namespace
@@ -243,15 +248,19 @@ cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, bool f32, unsigned grid, cu
 }
 
 cudaError_t launch_kv_combine(const KvAttnArgs& a, bool f32, cudaStream_t st) {
-  // up to 64 rows the parts are what there is to spread over warps
-  if (a.rows <= 64) {
-    const dim3 grid(a.n_ctas, a.rows);
-    return f32 ? launch_kernel(combine_kernel<float, 8>, grid, dim3(256), 0, st, true, a)
-               : launch_kernel(combine_kernel<__nv_bfloat16, 8>, grid, dim3(256), 0, st, true, a);
-  }
-  const dim3 grid(a.n_ctas, (a.rows + 7) / 8);
-  return f32 ? launch_kernel(combine_kernel<float, 1>, grid, dim3(256), 0, st, true, a)
-             : launch_kernel(combine_kernel<__nv_bfloat16, 1>, grid, dim3(256), 0, st, true, a);
+  // One wave of blocks (8 fit an SM) over all CTAs' items: more of them cost
+  // more in start-up than their rows take.  Up to 16 rows the parts are what
+  // there is to spread over warps.
+  const int y = a.rows <= 16 ? 4 : 8;
+  const dim3 grid(a.n_ctas, y), block(256);
+  if (a.rows <= 8)
+    return f32 ? launch_kernel(combine_kernel<float, 4>, grid, block, 0, st, true, a)
+               : launch_kernel(combine_kernel<__nv_bfloat16, 4>, grid, block, 0, st, true, a);
+  if (a.rows <= 16)
+    return f32 ? launch_kernel(combine_kernel<float, 2>, grid, block, 0, st, true, a)
+               : launch_kernel(combine_kernel<__nv_bfloat16, 2>, grid, block, 0, st, true, a);
+  return f32 ? launch_kernel(combine_kernel<float, 1>, grid, block, 0, st, true, a)
+             : launch_kernel(combine_kernel<__nv_bfloat16, 1>, grid, block, 0, st, true, a);
 }
 
 }  // namespace gdn

@@ -456,6 +456,7 @@ typedef struct gdn_kv_plan_t {
   int rows;          /* query rows (token, query head of one group) per row tile */
   int max_row_tiles; /* row tiles of one sequence and key/value head, at most */
   int n_ctas;        /* CTAs the key tiles of all row tiles are shared out to */
+  int item_cost;     /* what a row tile costs beyond its key tiles, in key tiles */
   int n_seqs, T, h_q, h_kv, dtype; /* copied, checked by gdn_kv_attn */
   int max_q_len;
   size_t off_desc, off_ml, off_o;  /* workspace sections */

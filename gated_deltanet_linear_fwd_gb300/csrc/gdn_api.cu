@@ -381,8 +381,11 @@ gdn_status encode_kv_map(CUtensorMap* m, void* base, const gdn_kv_cache* c) {
 
 // Kernels of gdn_kv_attn.
 constexpr int kKvPathSimt = 0;  // fp32 on the CUDA cores
-constexpr int kKvPathFew = 1;   // bf16, up to 64 rows per (sequence, key/value head)
+constexpr int kKvPathFew = 1;   // bf16, up to 32 rows per (sequence, key/value head)
 constexpr int kKvPathMany = 2;  // bf16, more rows
+// What parts and the second kernel cost, in key tiles: about 38 us at 1.35 us a
+// tile of 256 rows, about 6 us at 0.7 us a tile of few.
+constexpr int kKvJoinTilesMany = 28, kKvJoinTiles = 8;
 
 }  // namespace
 
@@ -859,10 +862,10 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   p.item_cost = 1;
   int per_sm = 2;
   const int64_t rows = (int64_t)max_q_len * group;
-  if (d->dtype == GDN_BF16 && rows <= 64) {
+  if (d->dtype == GDN_BF16 && rows <= 32) {
     p.path = kKvPathFew;
-    p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    p.item_cost = 2;
+    p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    p.item_cost = 4;
     per_sm = kv_few_ctas_per_sm(p.rows);
   } else if (d->dtype == GDN_BF16) {
     p.path = kKvPathMany;
@@ -872,9 +875,30 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   }
   p.max_row_tiles = std::max<int>(1, (int)(((int64_t)max_q_len * group + p.rows - 1) / p.rows));
   const int64_t items = (int64_t)d->n_seqs * p.max_row_tiles * h_kv;
-  const int64_t tiles = std::max<int64_t>(1, (max_kv_len + kKvTile - 1) / kKvTile);
-  // Short sequences: a CTA walks an item's few tiles in less time than a second kernel takes to join parts.
-  p.n_ctas = tiles <= 4 && items <= 0x7fffffff ? 0 : (int)std::min<int64_t>((int64_t)per_sm * sm_count, items * tiles);
+  const int64_t slots = (int64_t)per_sm * sm_count;
+  // Two ways to share out the items: each whole to one CTA, the longest first
+  // (n_ctas = 0), or all key tiles in equal runs, whose cut items are joined
+  // by a second kernel.  Both are estimated in key tiles, every sequence taken
+  // at its longest: whole items end with the longest one, or with the last
+  // round of equal ones; runs end together, plus the parts' way through
+  // memory and the second kernel (kKvJoinTiles).
+  int64_t total = 0, longest_item = 0, shortest = INT64_MAX;
+  const int64_t past = std::max(0, max_kv_len - max_q_len);
+  for (int rt = 0; rt < p.max_row_tiles; ++rt) {
+    const int64_t t0 = (int64_t)rt * p.rows / group;
+    const int64_t t1 = std::min<int64_t>(max_q_len - 1, ((int64_t)(rt + 1) * p.rows - 1) / group);
+    const int64_t hi = d->causal ? std::min<int64_t>(past + t1 + 1, max_kv_len) : max_kv_len;
+    const int64_t lo = d->window ? std::max<int64_t>(0, past + t0 - d->window + 1) : 0;
+    const int64_t cost = p.item_cost + std::max<int64_t>(1, (hi + kKvTile - 1) / kKvTile - lo / kKvTile);
+    total += cost;
+    longest_item = std::max(longest_item, cost);
+    shortest = std::min(shortest, cost);
+  }
+  total *= (int64_t)d->n_seqs * h_kv;
+  const int64_t whole = longest_item == shortest ? (items + slots - 1) / slots * longest_item
+                                                 : std::max(longest_item, (total + slots - 1) / slots + shortest);
+  const int64_t runs = (total + slots - 1) / slots + (p.path == kKvPathMany ? kKvJoinTilesMany : kKvJoinTiles);
+  p.n_ctas = whole <= runs && items <= 0x7fffffff ? 0 : (int)std::min<int64_t>(slots, total);
   p.n_seqs = d->n_seqs;
   p.T = d->T;
   p.h_q = d->h_q;
@@ -940,7 +964,7 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
       if ((st = encode_kv_map(&vm, cache->v, cache)) != GDN_OK) return st;
       e = plan->path == kKvPathFew ? launch_kv_attn_few(a, km, vm, grid, cs) : launch_kv_attn_many(a, km, vm, grid, cs);
     } else {
-      e = launch_kv_attn_simt(a, f32, grid, cs);
+      e = launch_kv_attn_simt(a, grid, cs);
     }
   }
   if (e == cudaSuccess) e = log.after("kv_attn", cs);

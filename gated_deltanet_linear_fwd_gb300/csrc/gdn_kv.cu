@@ -134,6 +134,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const KvAppendArgs a) 
   __shared__ uint32_t top[2];
   const int tid = threadIdx.x, h = blockIdx.y;
   if (tid < 2) top[tid] = 0;
+  grid_dependency_wait();
+  grid_launch_dependents();
   const Entry en = find_entry(a, blockIdx.x, part, &found);
   if (en.seq < 0) return;
   const int past = en.s.len - en.s.n;              // position of the first new token
@@ -207,6 +209,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const KvAppendArgs a) {
   __shared__ int part[kThreads / 32];
   __shared__ Entry found;
   const int tid = threadIdx.x, h = blockIdx.y;
+  grid_dependency_wait();
+  grid_launch_dependents();
   const Entry en = find_entry(a, blockIdx.x, part, &found);
   if (en.seq < 0) return;
   const int past = en.s.len - en.s.n, pos0 = en.slot * kPage;
@@ -244,20 +248,14 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const KvAppendArgs a) {
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool f32, unsigned entries, cudaStream_t st) {
   const dim3 grid(entries, a.c.h_kv);
-  if (f32)
-    append_kernel<float><<<grid, kThreads, 0, st>>>(a);
-  else
-    append_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return f32 ? launch_kernel(append_kernel<float>, grid, dim3(kThreads), 0, st, true, a)
+             : launch_kernel(append_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, true, a);
 }
 
 cudaError_t launch_kv_read(const KvAppendArgs& a, bool f32, unsigned entries, cudaStream_t st) {
   const dim3 grid(entries, a.c.h_kv);
-  if (f32)
-    read_kernel<float><<<grid, kThreads, 0, st>>>(a);
-  else
-    read_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return f32 ? launch_kernel(read_kernel<float>, grid, dim3(kThreads), 0, st, true, a)
+             : launch_kernel(read_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, true, a);
 }
 
 }  // namespace gdn

@@ -171,6 +171,7 @@ __device__ __forceinline__ int kv_cost(const KvAttnArgs& a, const KvItem& it) {
 
 struct KvRun {
   int seq, rt, head, off;  // first item of the run and the unit of it (of item_cost + tiles) that the run starts with
+  KvItem item;             // that item
   int64_t begin, end;      // units
   int64_t total;           // units of the call
   int ctas;                // CTAs that have a run: no more than there are units
@@ -182,76 +183,97 @@ struct KvRunScratch {
   int64_t part[32];
   KvRun run;
 };
+// Inclusive sum over the block's threads; total: the block's sum.
 template <int NT>
-__device__ __forceinline__ int64_t block_inclusive_scan(int64_t v, KvRunScratch* sc, int64_t& total) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ __forceinline__ int64_t block_inclusive_scan(int v, KvRunScratch* sc, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t sum = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += u;
+    const int64_t u = __shfl_up_sync(0xffffffffu, sum, d);
+    if (lane >= d) sum += u;
   }
   __syncthreads();
-  if (lane == 31) sc->part[warp] = v;
+  if (lane == 31) sc->part[warp] = sum;
   __syncthreads();
   int64_t before = 0;
   total = 0;
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < NT / 32; ++w) {
     const int64_t p = sc->part[w];
     if (w < warp) before += p;
     total += p;
   }
-  return v + before;
+  return sum + before;
 }
 template <int NT>
 __device__ __noinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
   const int tid = threadIdx.x;
-  const int entries = a.c.n_seqs * a.max_row_tiles;
   if (a.n_ctas == 0) {  // one whole item a CTA
     if (tid == 0) {
-      KvRun r;
-      r.head = blockIdx.x % a.c.h_kv;
-      const int e = blockIdx.x / a.c.h_kv;
-      r.seq = e / a.max_row_tiles;
-      r.rt = e % a.max_row_tiles;
+      KvRun& r = sc->run;
+      const int e = blockIdx.x / a.c.h_kv;  // the longest row tiles, under a causal mask the last ones, first
+      r.head = blockIdx.x - e * a.c.h_kv;
+      r.rt = a.max_row_tiles - 1 - e / a.c.n_seqs;
+      r.seq = e % a.c.n_seqs;
       r.off = 0;
+      r.item = kv_item(a, r.seq, r.rt);
       r.begin = 0;
-      r.end = r.total = kv_cost(a, kv_item(a, r.seq, r.rt));
+      r.end = r.total = kv_cost(a, r.item);
       r.ctas = 0;
-      sc->run = r;
     }
     __syncthreads();
     return;
   }
-  int64_t sum = 0;
+  const int entries = a.c.n_seqs * a.max_row_tiles;
+  // units over all entries, or, when the block's threads have one each (any
+  // decode batch of up to NT sequences), their running sum at once
+  int64_t total = 0, base = 0, incl = 0;
+  KvItem it;
+  int seq = 0, rt = 0, u = 0;
 #pragma unroll 1
-  for (int e = tid; e < entries; e += NT) sum += kv_cost(a, kv_item(a, e / a.max_row_tiles, e % a.max_row_tiles));
-  int64_t total;
-  block_inclusive_scan<NT>(sum, sc, total);
-  total *= a.c.h_kv;
-  const int ctas = (int)min((int64_t)a.n_ctas, total);
-  const int64_t begin = (int)blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
-  const int64_t end = (int)blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
+  for (int e0 = 0; e0 < entries; e0 += NT) {
+    const int e = e0 + tid;
+    seq = e / a.max_row_tiles;
+    rt = e - seq * a.max_row_tiles;
+    u = 0;
+    if (e < entries) {
+      it = kv_item(a, seq, rt);
+      u = kv_cost(a, it) * a.c.h_kv;
+    }
+    int64_t sub;
+    incl = block_inclusive_scan<NT>(u, sc, sub);
+    total += sub;
+  }
+  const int ctas = (int)min((int64_t)a.n_ctas, total), cta = blockIdx.x;
+  const int64_t begin = cta < ctas ? total * cta / ctas : 0, end = cta < ctas ? total * (cta + 1) / ctas : 0;
   if (tid == 0) {
     sc->run.begin = begin;
     sc->run.end = end;
     sc->run.total = total;
     sc->run.ctas = ctas;
   }
-  int64_t base = 0;
 #pragma unroll 1
   for (int e0 = 0; e0 < entries && base <= begin && begin < end; e0 += NT) {
-    const int e = e0 + tid, seq = e / a.max_row_tiles, rt = e % a.max_row_tiles;
-    const int u = e < entries ? kv_cost(a, kv_item(a, seq, rt)) : 0;
-    int64_t sub;
-    const int64_t incl = base + block_inclusive_scan<NT>((int64_t)u * a.c.h_kv, sc, sub);
-    const int64_t excl = incl - (int64_t)u * a.c.h_kv;
-    if (excl <= begin && begin < incl) {
-      const int in = (int)(begin - excl);  // units of one row tile over all heads fit 32 bits
+    int64_t sub = total;
+    if (entries > NT) {
+      const int e = e0 + tid;
+      seq = e / a.max_row_tiles;
+      rt = e - seq * a.max_row_tiles;
+      u = 0;
+      if (e < entries) {
+        it = kv_item(a, seq, rt);
+        u = kv_cost(a, it) * a.c.h_kv;
+      }
+      incl = base + block_inclusive_scan<NT>(u, sc, sub);
+    }
+    if (incl - u <= begin && begin < incl) {
+      const int in = (int)(begin - (incl - u)), cost = kv_cost(a, it);
       sc->run.seq = seq;
       sc->run.rt = rt;
-      sc->run.head = in / u;
-      sc->run.off = in % u;
+      sc->run.head = in / cost;
+      sc->run.off = in % cost;
+      sc->run.item = it;
     }
     base += sub;
   }
@@ -276,7 +298,7 @@ struct KvCursor {
     if (end > 0) {
       base = -r.off;
       off = max(0, r.off - a.item_cost);
-      it = kv_item(a, seq, rt);
+      it = r.item;
       clip(a);
     }
   }
@@ -358,10 +380,10 @@ __device__ __forceinline__ int e4m3_scale_exp(uint32_t a_bits, int least) {
 // ---- launchers ----
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool f32, unsigned entries, cudaStream_t st);
 cudaError_t launch_kv_read(const KvAppendArgs& a, bool f32, unsigned entries, cudaStream_t st);
-cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, bool f32, unsigned grid, cudaStream_t st);
+cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, unsigned grid, cudaStream_t st);  // fp32 q and out
 cudaError_t launch_kv_combine(const KvAttnArgs& a, bool f32, cudaStream_t st);
 cudaError_t kv_simt_setup();
-// rows: 8, 16, 32 or 64 (KvAttnArgs::rows); kmap, vmap: the pools as [page and head][64][128 bytes]
+// rows: 8, 16 or 32 (KvAttnArgs::rows); kmap, vmap: the pools as [page and head][64][128 bytes]
 cudaError_t launch_kv_attn_few(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, unsigned grid,
                                cudaStream_t st);
 cudaError_t kv_few_setup();

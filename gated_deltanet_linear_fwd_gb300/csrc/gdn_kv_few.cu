@@ -1,5 +1,5 @@
 // Attention over the 8-bit key/value cache for few query rows (one generated
-// token, or a few drafted ones, times the heads of a group): up to 64 rows
+// token, or a few drafted ones, times the heads of a group): up to 32 rows
 // meet a long axis, so the call is bound by reading the codes, 256 bytes a
 // token and key/value head, from HBM.
 //
@@ -23,9 +23,10 @@
 // fp32 from the unrounded P.  Each tile's O^T is read from tensor memory and
 // accumulated in fp32 registers, where the rescaling by 2^(m_old - m) happens.
 //
-// Roles: warpgroups of four warps, 16 rows each (8 for 8 rows), one TMA warp,
-// one MMA warp.  Two CTAs an SM (one for 64 rows) hide one another's tile
-// latency.
+// Roles: warpgroups of four warps with 8 rows each (one with 16 for 16 rows),
+// one TMA warp, one MMA warp.  Two CTAs an SM hide one another's tile latency;
+// 32 rows take one CTA of four warpgroups (two of 16 rows took 2600 cycles a
+// tile, four of 8 rows 1500, against 1400 for the tile's bytes from HBM).
 #include <cuda_fp16.h>
 
 #include "gdn_dev.cuh"
@@ -42,13 +43,13 @@ enum { kBarK = 1, kBarV, kBarKFree, kBarVFree, kBarQ, kBarS, kBarP, kBarO, kBarS
 
 template <int NR>
 struct Few {
-  static constexpr int kRowsWg = NR < 16 ? NR : 16;      // rows of a warpgroup
+  static constexpr int kRowsWg = NR == 16 ? 16 : 8;      // rows of a warpgroup
   static constexpr int kWgs = NR / kRowsWg;
   static constexpr int kSoft = kWgs * 128;               // softmax threads
   static constexpr int kThreads = kSoft + 64;
   static constexpr int kN = 2 * NR;                      // columns of the products
-  static constexpr int kStages = NR == 64 ? 4 : NR == 32 ? 2 : 3;
-  static constexpr int kCtasPerSm = NR == 64 ? 1 : 2;
+  static constexpr int kStages = NR == 32 ? 5 : 3;
+  static constexpr int kCtasPerSm = NR == 32 ? 1 : 2;
   static constexpr uint32_t kTmemCols = 4 * kN;          // S and O, two of each
   static constexpr uint32_t kOffV = kStages * kTileBytes;
   static constexpr uint32_t kOffQ = 2 * kStages * kTileBytes;
@@ -58,7 +59,7 @@ struct Few {
 
 template <int NR>
 struct FewCtl {
-  uint64_t k_full[4], k_free[4], v_full[4], v_free[4];
+  uint64_t k_full[5], k_free[5], v_full[5], v_free[5];
   uint64_t q_full, s_full[2], p_full[2], o_full[2], scale_full[kScaleRing];
   float scale[kScaleRing][4];  // key scales of the tile's two pages, value scales
   float f[NR];                 // score factor of a row: its power of two times scale log2(e)
@@ -143,54 +144,76 @@ __device__ __forceinline__ void few_load(const KvAttnArgs& a, FewCtl<NR>* ctl, u
   }
 }
 
-// ---------------------------------------------------------------- MMA thread
+// ---------------------------------------------------------------- MMA warp
+// The whole warp walks the loop and one elected lane issues, so addresses and
+// descriptors stay in uniform registers.
 template <int NR>
-__device__ __forceinline__ void few_mma(const KvAttnArgs& a, FewCtl<NR>* ctl, uint32_t sm,
-                                        uint32_t tmem) {
+__device__ __forceinline__ void few_mma(const KvAttnArgs& a, FewCtl<NR>* ctl, uint32_t sm, uint32_t tmem_any) {
   using F = Few<NR>;
   constexpr uint32_t kIdS = idesc_e4m3(128, F::kN, false, false), kIdO = idesc_e4m3(128, F::kN, true, true);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
   const uint64_t dk = sdesc_sw128(sm, 0, 1024), dv = sdesc_sw128(sm + F::kOffV, 0, 1024);
   const uint64_t dq = sdesc_sw128(sm + F::kOffQ, 0, 1024);
   const uint64_t dp = sdesc_plain(sm + F::kOffP, 128, 16 * kKvTile);
-  int i = 0, items = 0;
-  // O^T of tile t, once its weights are in shared memory
-  auto second = [&](int t) {
-    const int stage = t % F::kStages, buf = t & 1;
-    if (!kv_wait(&ctl->p_full[buf], (t >> 1) & 1, &ctl->abort, 100 + kBarP)) return false;
-    if (!kv_wait(&ctl->v_full[stage], (t / F::kStages) & 1, &ctl->abort, 100 + kBarV)) return false;
+  const bool issue = elect_one();
+  int i = 0, ks = 0, vs = 0;  // tile of the run; stages of this tile's keys and of the values of the one before
+  uint32_t k_par = 0, v_par = 0, q_par = 0;
+  // O^T of the tile before tile i, once its weights are in shared memory
+  auto second = [&]() {
+    const int buf = (i - 1) & 1;
+    if (!kv_wait_warp([&] {
+          return kv_wait(&ctl->v_full[vs], v_par, &ctl->abort, 100 + kBarV) &&
+                 kv_wait(&ctl->p_full[buf], ((i - 1) >> 1) & 1, &ctl->abort, 100 + kBarP);
+        }))
+      return false;
     tc_fence_after();
-    const uint32_t d = tmem + (2 + buf) * F::kN;
-    const uint64_t v = dv + stage * (kTileBytes >> 4), p = dp + buf * (F::kN * kKvTile >> 4);
+    if (issue) {
+      const uint32_t d = tmem + (2 + buf) * F::kN;
+      const uint64_t v = dv + vs * (kTileBytes >> 4), p = dp + buf * (F::kN * kKvTile >> 4);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mma_f8(d, v + k * 256, p + k * 32, kIdO, k > 0);
-    mma_commit(&ctl->o_full[buf]);
-    mma_commit(&ctl->v_free[stage]);
+      for (int k = 0; k < 4; ++k) mma_f8(d, v + k * 256, p + k * 32, kIdO, k > 0);
+      mma_commit(&ctl->o_full[buf]);
+      mma_commit(&ctl->v_free[vs]);
+    }
+    __syncwarp();
+    if (++vs == F::kStages) {
+      vs = 0;
+      v_par ^= 1;
+    }
     return true;
   };
   KvCursor cur;
 #pragma unroll 1
   for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
-    const int tiles = cur.tiles();
+    const int tiles = __shfl_sync(0xffffffffu, cur.tiles(), 0);
 #pragma unroll 1
-    for (int j = 0; j < tiles; ++j, ++i) {
-      const int stage = i % F::kStages, buf = i & 1;
+    for (int j = 0; j < tiles; ++j) {
       // A new item's queries arrive only after the last tile's softmax: finish that tile first.
       if (j == 0) {
-        if (i > 0 && !second(i - 1)) return;
-        if (!kv_wait(&ctl->q_full, items++ & 1, &ctl->abort, 100 + kBarQ)) return;
+        if (i > 0 && !second()) return;
+        if (!kv_wait_warp([&] { return kv_wait(&ctl->q_full, q_par, &ctl->abort, 100 + kBarQ); })) return;
+        q_par ^= 1;
       }
-      if (!kv_wait(&ctl->k_full[stage], (i / F::kStages) & 1, &ctl->abort, 100 + kBarK)) return;
+      if (!kv_wait_warp([&] { return kv_wait(&ctl->k_full[ks], k_par, &ctl->abort, 100 + kBarK); })) return;
       tc_fence_after();
-      const uint32_t d = tmem + buf * F::kN;
-      const uint64_t kk = dk + stage * (kTileBytes >> 4);
+      if (issue) {
+        const uint32_t d = tmem + (i & 1) * F::kN;
+        const uint64_t kk = dk + ks * (kTileBytes >> 4);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mma_f8(d, kk + k * 2, dq + k * 2, kIdS, k > 0);
-      mma_commit(&ctl->s_full[buf]);
-      mma_commit(&ctl->k_free[stage]);
-      if (j > 0 && !second(i - 1)) return;
+        for (int k = 0; k < 4; ++k) mma_f8(d, kk + k * 2, dq + k * 2, kIdS, k > 0);
+        mma_commit(&ctl->s_full[i & 1]);
+        mma_commit(&ctl->k_free[ks]);
+      }
+      __syncwarp();
+      if (++ks == F::kStages) {
+        ks = 0;
+        k_par ^= 1;
+      }
+      if (j > 0 && !second()) return;
+      ++i;
     }
   }
-  if (i > 0) second(i - 1);
+  if (i > 0) second();
 }
 
 // ---------------------------------------------------------------- softmax warpgroups
@@ -225,14 +248,21 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
     const int group = kv_first_q_head(a.c, cur.head + 1) - head0;
     const int tiles = cur.tiles();
     if (tiles > 0) {
-      // ---- the item's query rows, four rows a warp pass ----
-      for (int r = warp; r < R; r += 4) {
-        const int rr = cur.rt * NR + row0 + r, t = rr / a.group, g = rr % a.group;
+      // ---- the item's query rows: every fourth one is this warp's, all loads in flight ----
+      uint2 q4[R / 4];
+#pragma unroll
+      for (int k = 0; k < R / 4; ++k) {
+        const int rr = cur.rt * NR + row0 + warp + 4 * k, t = rr / a.group, g = rr - t * a.group;
+        q4[k] = make_uint2(0, 0);
+        if (t < it.n && g < group)
+          q4[k] = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                                       (int64_t)(it.tok0 + t) * a.q_stride + (head0 + g) * kHeadDim + 4 * lane));
+      }
+#pragma unroll
+      for (int k = 0; k < R / 4; ++k) {
+        const int r = warp + 4 * k, rr = cur.rt * NR + row0 + r, t = rr / a.group, g = rr - t * a.group;
         const bool live = t < it.n && g < group;
-        uint2 w = make_uint2(0, 0);
-        if (live)
-          w = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                              (int64_t)(it.tok0 + t) * a.q_stride + (head0 + g) * kHeadDim + 4 * lane);
+        const uint2 w = q4[k];
         float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                       __uint_as_float(w.y & 0xffff0000u)};
         uint32_t m = 0;
@@ -483,12 +513,13 @@ __global__ void __launch_bounds__(Few<NR>::kThreads, Few<NR>::kCtasPerSm)
     ctl.abort = 0;
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
-    if (a.n_ctas) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
   if (warp == F::kSoft / 32) {
     tmem_alloc(&ctl.tmem, F::kTmemCols);
     tmem_relinquish();
   }
+  grid_dependency_wait();
+  if (tid == 0 && a.n_ctas) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
   kv_run<F::kThreads>(a, &ctl.run);
   tc_fence_before();
   __syncthreads();
@@ -498,7 +529,7 @@ __global__ void __launch_bounds__(Few<NR>::kThreads, Few<NR>::kCtasPerSm)
     few_softmax<NR>(a, &ctl, sm, tmem);
   } else if (warp == F::kSoft / 32) {
     few_load<NR>(a, &ctl, sm, &kmap, &vmap);
-  } else if ((tid & 31) == 0) {
+  } else {
     few_mma<NR>(a, &ctl, smem_u32(sm), tmem);
   }
   __syncwarp();
@@ -522,20 +553,19 @@ __global__ void __launch_bounds__(Few<NR>::kThreads, Few<NR>::kCtasPerSm)
 template <int NR>
 cudaError_t launch(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, unsigned grid,
                    cudaStream_t st) {
-  return launch_kernel(attn_few_kernel<NR>, dim3(grid), dim3(Few<NR>::kThreads), Few<NR>::kSmem, st, false, kmap,
+  return launch_kernel(attn_few_kernel<NR>, dim3(grid), dim3(Few<NR>::kThreads), Few<NR>::kSmem, st, true, kmap,
                        vmap, a);
 }
 
 }  // namespace
 
-int kv_few_ctas_per_sm(int rows) { return rows == 64 ? Few<64>::kCtasPerSm : Few<32>::kCtasPerSm; }
+int kv_few_ctas_per_sm(int rows) { return rows == 32 ? Few<32>::kCtasPerSm : Few<16>::kCtasPerSm; }
 
 cudaError_t kv_few_setup() {
   cudaError_t e;
   if ((e = cudaFuncSetAttribute(attn_few_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<8>::kSmem)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(attn_few_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<16>::kSmem)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(attn_few_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<32>::kSmem)) != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attn_few_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<64>::kSmem);
+  return cudaFuncSetAttribute(attn_few_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<32>::kSmem);
 }
 
 cudaError_t launch_kv_attn_few(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, unsigned grid,
@@ -543,8 +573,7 @@ cudaError_t launch_kv_attn_few(const KvAttnArgs& a, const CUtensorMap& kmap, con
   switch (a.rows) {
     case 8: return launch<8>(a, kmap, vmap, grid, st);
     case 16: return launch<16>(a, kmap, vmap, grid, st);
-    case 32: return launch<32>(a, kmap, vmap, grid, st);
-    default: return launch<64>(a, kmap, vmap, grid, st);
+    default: return launch<32>(a, kmap, vmap, grid, st);
   }
 }
 

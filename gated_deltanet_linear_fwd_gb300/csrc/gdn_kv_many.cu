@@ -620,12 +620,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl.abort = 0;
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
-    if (a.n_ctas) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
   if (warp == kTmaWarp) {
     tmem_alloc(&ctl.tmem, 512);
     tmem_relinquish();
   }
+  grid_dependency_wait();
+  if (tid == 0 && a.n_ctas) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
   kv_run<kThreads>(a, &ctl.run);
   tc_fence_before();
   __syncthreads();
@@ -670,7 +671,7 @@ cudaError_t kv_many_setup() {
 
 cudaError_t launch_kv_attn_many(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, unsigned grid,
                                 cudaStream_t st) {
-  return launch_kernel(attn_many_kernel, dim3(grid), dim3(kThreads), kSmem, st, false, kmap, vmap, a);
+  return launch_kernel(attn_many_kernel, dim3(grid), dim3(kThreads), kSmem, st, true, kmap, vmap, a);
 }
 
 }  // namespace gdn

@@ -29,10 +29,6 @@ struct SimtSmem {
   KvRunScratch run;
 };
 
-__device__ __forceinline__ float load_elem(const float* p) { return *p; }
-__device__ __forceinline__ float load_elem(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store_elem(float* p, float x) { *p = x; }
-__device__ __forceinline__ void store_elem(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
   *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
 }
@@ -40,11 +36,11 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-template <typename T>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const KvAttnArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SimtSmem& sm = *reinterpret_cast<SimtSmem*>(smem_raw);
   const int tid = threadIdx.x, r = tid >> 4, c = tid & 15;
+  grid_dependency_wait();
   kv_run<kThreads>(a, &sm.run);
   const KvRun& run = sm.run.run;
   if (a.n_ctas && tid == 0) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -63,7 +59,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const KvAttnArgs a)
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       sm.q[r][c + 16 * e] =
-          live ? load_elem(reinterpret_cast<const T*>(a.q) + (int64_t)(it.tok0 + t) * a.q_stride + j * kHeadDim + c + 16 * e)
+          live ? reinterpret_cast<const float*>(a.q)[(int64_t)(it.tok0 + t) * a.q_stride + j * kHeadDim + c + 16 * e]
                : 0.f;
     float m = -__int_as_float(0x7f800000), l = 0.f, o[8] = {};
     const int page_begin = 2 * cur.tile_begin(), page_end = min(page_begin + 2 * cur.tiles(), (it.len + kPage - 1) / kPage);
@@ -142,9 +138,9 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const KvAttnArgs a)
     if (cur.whole()) {
       if (live) {
         const float inv = l == 0.f ? 0.f : 1.0f / l;
-        T* dst = reinterpret_cast<T*>(a.out) + (int64_t)(it.tok0 + t) * a.out_stride + j * kHeadDim + 8 * c;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) store_elem(dst + e, o[e] * inv);
+        float* dst = reinterpret_cast<float*>(a.out) + (int64_t)(it.tok0 + t) * a.out_stride + j * kHeadDim + 8 * c;
+        store4(dst, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+        store4(dst + 4, o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv);
         if (a.lse && c == 0) a.lse[(int64_t)(it.tok0 + t) * a.c.h_q + j] = kv_lse(m, l);
       }
     } else {
@@ -232,26 +228,17 @@ __global__ void __launch_bounds__(256) combine_kernel(const KvAttnArgs a) {
 }  // namespace
 
 cudaError_t kv_simt_setup() {
-  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)sizeof(SimtSmem));
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attn_simt_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)sizeof(SimtSmem));
+  return cudaFuncSetAttribute(attn_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SimtSmem));
 }
 
-cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, bool f32, unsigned grid, cudaStream_t st) {
-  if (f32)
-    attn_simt_kernel<float><<<grid, kThreads, sizeof(SimtSmem), st>>>(a);
-  else
-    attn_simt_kernel<__nv_bfloat16><<<grid, kThreads, sizeof(SimtSmem), st>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, unsigned grid, cudaStream_t st) {
+  return launch_kernel(attn_simt_kernel, dim3(grid), dim3(kThreads), sizeof(SimtSmem), st, true, a);
 }
 
 cudaError_t launch_kv_combine(const KvAttnArgs& a, bool f32, cudaStream_t st) {
-  // One wave of blocks (8 fit an SM) over all CTAs' items: more of them cost
-  // more in start-up than their rows take.  Up to 16 rows the parts are what
-  // there is to spread over warps.
-  const int y = a.rows <= 16 ? 4 : 8;
+  // Few rows: one wave of blocks (8 fit an SM) over all CTAs' items, and several
+  // warps a row, since there the parts are what there is to spread.
+  const int y = a.rows <= 16 ? 4 : (a.rows + 7) / 8;
   const dim3 grid(a.n_ctas, y), block(256);
   if (a.rows <= 8)
     return f32 ? launch_kernel(combine_kernel<float, 4>, grid, block, 0, st, true, a)

@@ -91,6 +91,8 @@ _lib = None
 def load(path: str = LIB_PATH):
     """Load libgdn.so (built in-tree by gated_deltanet_linear_fwd_gb300.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -336,8 +336,10 @@ def _kv_ints(kv_lens: torch.Tensor, page_table: torch.Tensor, cu_seqlens: Option
     return n, page_table.shape[1], cu_seqlens.data_ptr()
 
 
-def _raw_stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    """The stream's handle; the current one of t's device by default (asking for
+    it by index takes a fifth of the time of asking for the current device's)."""
+    return (torch.cuda.current_stream(t.device.index) if stream is None else stream).cuda_stream
 
 
 def gdn_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor,
@@ -353,7 +355,7 @@ def gdn_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_lens: tor
         raise ValueError("k and v must be alike, with 128 elements a head")
     dims = L.gdn_kv_dims(n, k.shape[0], h_kv, max_pages, 1, 0, 0.0, _DT.get(k.dtype, -1), 0, ks, vs, 0)
     st = L.load().gdn_kv_append(k.data_ptr(), v.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), cu, cache.raw,
-                                dims, _raw_stream(stream))
+                                dims, _raw_stream(stream, k))
     L.check(st, "gdn_kv_append")
 
 
@@ -377,7 +379,7 @@ def gdn_kv_read(cache: KVCache, kv_lens: torch.Tensor, page_table: torch.Tensor,
         raise ValueError("k_out and v_out must be alike, with 128 elements a head")
     dims = L.gdn_kv_dims(n, k_out.shape[0], h_kv, max_pages, 1, 0, 0.0, _DT.get(k_out.dtype, -1), 0, ks, vs, 0)
     st = L.load().gdn_kv_read(k_out.data_ptr(), v_out.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), cu,
-                              cache.raw, dims, _raw_stream(stream))
+                              cache.raw, dims, _raw_stream(stream, k_out))
     L.check(st, "gdn_kv_read")
     return k_out, v_out
 
@@ -442,6 +444,6 @@ def gdn_kv_attn(q: torch.Tensor, cache: KVCache, kv_lens: torch.Tensor, page_tab
                          _kv_rows("out", out, h_q))
     st = L.load().gdn_kv_attn(q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), cu, cache.raw, out.data_ptr(),
                               None if lse is None else lse.data_ptr(), dims, plan.raw, workspace.data_ptr(),
-                              workspace.numel(), _raw_stream(stream))
+                              workspace.numel(), _raw_stream(stream, q))
     L.check(st, "gdn_kv_attn")
     return out, lse

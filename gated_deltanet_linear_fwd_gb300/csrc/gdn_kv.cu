@@ -11,8 +11,7 @@
 // that to e4m3.
 //
 // One CTA per (page slot that receives tokens, head).  Both operators move
-// each byte once: a CTA holds its page's new tokens in registers between the
-// maximum and the conversion.
+// each byte once and are bound by that.
 #include "gdn_kv.cuh"
 
 namespace gdn {
@@ -23,20 +22,51 @@ constexpr int kChunks = kPage * kHeadDim / 8 / kThreads;  // 8-element chunks a 
 
 constexpr int kScaleMinExp = -40, kScaleMaxExp = 40;
 
-// 8 elements of a row as fp32.
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+// 8 elements of a row as they are in memory, and as fp32.
+struct Raw8f {
+  float4 a, b;
+};
+__device__ __forceinline__ Raw8f load_raw(const float* p) {
+  return {__ldg(reinterpret_cast<const float4*>(p)), __ldg(reinterpret_cast<const float4*>(p) + 1)};
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ uint4 load_raw(const __nv_bfloat16* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ void zero_raw(Raw8f& r) { r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f); }
+__device__ __forceinline__ void zero_raw(uint4& r) { r = make_uint4(0, 0, 0, 0); }
+__device__ __forceinline__ void unpack8(const Raw8f& r, float (&x)[8]) {
+  x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+  x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+}
+__device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+}
+// The largest finite magnitude (fp32 bits).
+__device__ __forceinline__ uint32_t max_bits(const Raw8f& r, uint32_t m) {
+  float x[8];
+  unpack8(r, x);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = __float_as_uint(x[e]) & 0x7fffffffu;
+    m = b < 0x7f800000u ? max(m, b) : m;
+  }
+  return m;
+}
+__device__ __forceinline__ uint32_t max_bits(const uint4& r, uint32_t m) {
+  const uint32_t w[4] = {r.x & 0x7fff7fffu, r.y & 0x7fff7fffu, r.z & 0x7fff7fffu, r.w & 0x7fff7fffu};
+  const uint32_t all = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+  const uint32_t lo = all << 16, hi = all & 0xffff0000u;
+  if (lo < 0x7f800000u && hi < 0x7f800000u) return max(m, max(lo, hi));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t a = w[e] << 16, b = w[e] & 0xffff0000u;
+    m = a < 0x7f800000u ? max(m, a) : m;
+    m = b < 0x7f800000u ? max(m, b) : m;
+  }
+  return m;
 }
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -127,13 +157,18 @@ __device__ __forceinline__ Entry find_entry(const KvAppendArgs& a, int e, int (&
   return *found;
 }
 
+// z of the grid: 0 keys, 1 values.  32 elements a thread, as they are in
+// memory, between the maximum and the conversion: 16 registers in bf16, so six
+// or more CTAs an SM have their 16 KB in flight (with keys and values in one
+// CTA as fp32, 128 registers a thread, 32768 tokens of 8 heads took 76 us).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) append_kernel(const KvAppendArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 4) append_kernel(const KvAppendArgs a) {
   __shared__ int part[kThreads / 32];
   __shared__ Entry found;
-  __shared__ uint32_t top[2];
+  __shared__ uint32_t top;
   const int tid = threadIdx.x, h = blockIdx.y;
-  if (tid < 2) top[tid] = 0;
+  const bool values = blockIdx.z != 0;
+  if (tid == 0) top = 0;
   grid_dependency_wait();
   grid_launch_dependents();
   const Entry en = find_entry(a, blockIdx.x, part, &found);
@@ -142,66 +177,47 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const KvAppendArgs a) 
   const int pos0 = en.slot * kPage;
   const int lo = max(past - pos0, 0), hi = min(en.s.len - pos0, kPage);  // rows of the page that are new
   if (hi <= lo) return;  // a sequence of length zero
+  // packed token of row r: tok0 + pos0 + r - past
+  const int64_t stride = values ? a.v_stride : a.k_stride;
+  const T* src = reinterpret_cast<const T*>(values ? a.v : a.k) + ((int64_t)en.s.tok0 + pos0 - past) * stride + h * kHeadDim;
+  decltype(load_raw(src)) x[kChunks];
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) {
+    const int c = i * kThreads + tid, r = c >> 4;
+    zero_raw(x[i]);
+    if (r >= lo && r < hi) x[i] = load_raw(src + r * stride + (c & 15) * 8);
+  }
   const int page = kv_page(a.c, en.seq, en.slot);
   if (page < 0) return;
   const size_t head = (size_t)page * a.c.h_kv + h;
-  const float old_k = a.c.k_scale[head], old_v = a.c.v_scale[head];
-  __syncthreads();  // top is zero
-
-  // packed token of row r: tok0 + pos0 + r - past
-  const int64_t row0 = (int64_t)en.s.tok0 + pos0 - past;
-  float x[2][kChunks][8];
-  uint32_t m[2] = {0, 0};
+  float* scale = (values ? a.c.v_scale : a.c.k_scale) + head;
+  const float old_s = lo > 0 ? *scale : 0.f;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kChunks; ++i) m = max_bits(x[i], m);
+  m = __reduce_max_sync(0xffffffffu, m);
+  __syncthreads();  // top is zero; everyone has read the scale
+  if ((tid & 31) == 0 && m) atomicMax(&top, m);
+  __syncthreads();
+  const float s = fmaxf(pow2f(min(e4m3_scale_exp(top, kScaleMinExp), kScaleMaxExp)), old_s);
+  const float inv = 1.0f / s;  // exact: a power of two
+  uint2* codes = reinterpret_cast<uint2*>((values ? a.c.v : a.c.k) + head * kPageBytes);
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    const int c = i * kThreads + tid, r = c >> 4, col = (c & 15) * 8;
+    const int c = i * kThreads + tid, r = c >> 4;
+    float y[8];
     if (r >= lo && r < hi) {
-      load8(reinterpret_cast<const T*>(a.k) + (row0 + r) * a.k_stride + h * kHeadDim + col, x[0][i]);
-      load8(reinterpret_cast<const T*>(a.v) + (row0 + r) * a.v_stride + h * kHeadDim + col, x[1][i]);
-    } else {
+      unpack8(x[i], y);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[0][i][e] = x[1][i][e] = 0.f;
+      for (int e = 0; e < 8; ++e)  // infinities too become NaN codes
+        y[e] = (__float_as_uint(y[e]) & 0x7fffffffu) < 0x7f800000u ? y[e] : __uint_as_float(0x7fffffffu);
+      codes[c] = encode8(y, inv);
+    } else if (r < lo && s > old_s) {
+      decode8(codes[c], old_s, y);
+      codes[c] = encode8(y, inv);
     }
   }
-#pragma unroll
-  for (int w = 0; w < 2; ++w)
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t b = __float_as_uint(x[w][i][e]) & 0x7fffffffu;
-        if (b < 0x7f800000u)
-          m[w] = max(m[w], b);
-        else
-          x[w][i][e] = __uint_as_float(0x7fffffffu);  // infinities too become NaN codes
-      }
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const uint32_t mw = __reduce_max_sync(0xffffffffu, m[w]);
-    if ((tid & 31) == 0 && mw) atomicMax(&top[w], mw);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const float old_s = w ? old_v : old_k;
-    uint8_t* codes = (w ? a.c.v : a.c.k) + head * kPageBytes;
-    float s = pow2f(min(e4m3_scale_exp(top[w], kScaleMinExp), kScaleMaxExp));
-    if (lo > 0) s = fmaxf(s, old_s);
-    const float inv = 1.0f / s;  // exact: a power of two
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int c = i * kThreads + tid, r = c >> 4;
-      if (r >= lo && r < hi) {
-        *reinterpret_cast<uint2*>(codes + (size_t)c * 8) = encode8(x[w][i], inv);
-      } else if (r < lo && s > old_s) {
-        float y[8];
-        uint2* at = reinterpret_cast<uint2*>(codes + (size_t)c * 8);
-        decode8(*at, old_s, y);
-        *at = encode8(y, inv);
-      }
-    }
-    if (tid == 0) (w ? a.c.v_scale : a.c.k_scale)[head] = s;
-  }
+  if (tid == 0) *scale = s;
 }
 
 template <typename T>
@@ -247,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const KvAppendArgs a) {
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool f32, unsigned entries, cudaStream_t st) {
-  const dim3 grid(entries, a.c.h_kv);
+  const dim3 grid(entries, a.c.h_kv, 2);
   return f32 ? launch_kernel(append_kernel<float>, grid, dim3(kThreads), 0, st, true, a)
              : launch_kernel(append_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, st, true, a);
 }

@@ -15,13 +15,15 @@
 // each weight, relative; a bf16 weight has 2^-9).  The two parts are columns of
 // one product, so no key or value is converted or read twice.
 //
-// Softmax over the keys x_j = scale log2(e) q . k_j, running per tile of 128
-// keys (two pages): thread j of a warpgroup holds key j's column of S^T.  The
-// values' page scale 2^e_v (a power of two) is folded into the exponent:
-// P_j = 2^(x_j + e_v - m), m the running maximum of x + e_v, so P . V-codes is
-// the output in units of 2^m, and the softmax's sum is of P_j 2^-e_v, kept in
-// fp32 from the unrounded P.  Each tile's O^T is read from tensor memory and
-// accumulated in fp32 registers, where the rescaling by 2^(m_old - m) happens.
+// Softmax over the keys x_j = scale log2(e) q . k_j, per tile of 128 keys (two
+// pages): thread j of a warpgroup holds key j's column of S^T.  The values'
+// page scale 2^e_v (a power of two) is folded into the exponent: with m_t the
+// tile's maximum of x + e_v, P_j = 2^(x_j + e_v - m_t + 8), so P . V-codes is the
+// tile's output in units of 2^(m_t - 8), and its sum is of P_j 2^-e_v, kept in
+// fp32 from the unrounded P.  Weights count from their own tile's maximum, so
+// what e4m3 cannot hold is below 2^-18 of that, however many keys there are.
+// Tiles are joined in fp32 registers, under the next tile's second product:
+// o <- o 2^(m - m') + O_t 2^(m_t - m'), m' the larger of m and m_t.
 //
 // Roles: warpgroups of four warps with 8 rows each (one with 16 for 16 rows),
 // one TMA warp, one MMA warp.  Two CTAs an SM hide one another's tile latency;
@@ -39,7 +41,7 @@ constexpr int kTileBytes = kKvTile * kHeadDim;  // codes of a tile of keys or va
 constexpr int kScaleRing = 8;                   // tiles whose page scales are in shared memory
 
 // Details of the bounded waits (100 + barrier), as in the other kernels.
-enum { kBarK = 1, kBarV, kBarKFree, kBarVFree, kBarQ, kBarS, kBarP, kBarO, kBarScale };
+enum { kBarK = 1, kBarV, kBarKFree, kBarVFree, kBarQ, kBarS, kBarP, kBarO, kBarScale, kBarClean };
 
 template <int NR>
 struct Few {
@@ -60,9 +62,10 @@ struct Few {
 template <int NR>
 struct FewCtl {
   uint64_t k_full[5], k_free[5], v_full[5], v_free[5];
-  uint64_t q_full, s_full[2], p_full[2], o_full[2], scale_full[kScaleRing];
+  uint64_t q_full, s_full[2], p_full[2], o_full[2], v_clean[2], scale_full[kScaleRing];
   float scale[kScaleRing][4];  // key scales of the tile's two pages, value scales
-  float f[NR];                 // score factor of a row: its power of two times scale log2(e)
+  uint32_t nan_keys[2][4];     // keys of a masked tile whose values hold a NaN code
+  alignas(16) float f[NR];     // score factor of a row: its power of two times scale log2(e)
   int key_lo[NR], key_hi[NR];  // keys a row attends to
   alignas(16) float top[Few<NR>::kWgs][2][Few<NR>::kRowsWg][4];  // tile maxima of the four warps
   alignas(16) float sum[Few<NR>::kWgs][Few<NR>::kRowsWg][4];
@@ -238,8 +241,9 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
   const int wg = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
   const int row0 = wg * R;
   const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16) + wg * 2 * R;
+  const int bar = 1 + wg;
   bool bad = false;
-  int i = 0;  // tile of the run
+  int i = 0, cleaned = 0;  // tiles of the run, and the masked ones among them
   KvCursor cur;
 #pragma unroll 1
   for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
@@ -294,76 +298,112 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
       }
       fence_proxy_async_smem();
       kv_arrive_warp(&ctl->q_full);
-      named_bar_sync(1, F::kSoft);
+      named_bar_sync(bar, 128);
     }
     // tiles that lie within every live row's keys need no mask
     const int t0 = cur.rt * NR / a.group, t1 = min(it.n - 1, (cur.rt * NR + NR - 1) / a.group);
     const int all_lo = a.window > 0 ? past + t1 - a.window + 1 : 0, all_hi = a.causal ? min(past + t0 + 1, it.len) : it.len;
-    float m[R], l[R], o[R];
+    const bool dead = cur.rt * NR + row0 >= it.n * a.group;  // no row of this warpgroup: its columns may hold anything
+    float m[R], l[R], o[R];        // up to the tile before last
+    float top[R], sum[R];          // the last tile's maximum and this key's part of its sum
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      m[r] = kNegInf;
-      l[r] = 0.f;
-      o[r] = 0.f;
+      m[r] = top[r] = kNegInf;
+      l[r] = o[r] = sum[r] = 0.f;
     }
+    // O^T of the last tile, in units of 2^(its maximum - 8), joins the rest
+    auto join = [&](int t) {
+      bad |= !kv_wait_warp([&] { return kv_wait(&ctl->o_full[t & 1], (t >> 1) & 1, &ctl->abort, 100 + kBarO); });
+      if (bad) return;
+      tc_fence_after();
+      uint32_t h[16], q[16];
+      tmem_ld16(t_lane + (2 + (t & 1)) * F::kN, h);
+      if (R == 16) {
+        tmem_ld16(t_lane + (2 + (t & 1)) * F::kN + 16, q);
+        tmem_ld_wait(h, q);
+      } else {
+        tmem_ld_wait(h);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float w = fmaxf(m[r], top[r]), ref = w == kNegInf ? 0.f : w;
+        const float alpha = ex2(m[r] - ref), beta = ex2(top[r] - ref);
+        m[r] = w;
+        l[r] = fmaf(l[r], alpha, sum[r] * beta);
+        o[r] = fmaf(o[r], alpha, (__uint_as_float(h[r]) + __uint_as_float(R == 16 ? q[r] : h[8 + r])) * beta);
+      }
+    };
 #pragma unroll 1
     for (int j = 0; j < tiles; ++j, ++i) {
       const int buf = i & 1, key0 = (cur.tile_begin() + j) * kKvTile, key = key0 + tid;
+      const int stage = i % F::kStages;
+      const bool masked = key0 < all_lo || key0 + kKvTile > all_hi;
+      if (masked) {
+        // Values no row may use must not meet a zero weight as NaN: the first
+        // warpgroup makes zeros of a key row past the sequence, or with a NaN
+        // code, before any product; in the second case the rows that do
+        // attend to it become NaN.
+        if (wg == 0) {
+          bad |= !kv_wait_warp([&] { return kv_wait(&ctl->v_full[stage], (i / F::kStages) & 1, &ctl->abort, 100 + kBarV); });
+          uint8_t* v = sm + F::kOffV + stage * kTileBytes + tid * kHeadDim;
+          uint32_t carry = 0;
+          if (!bad && key < it.len) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {  // b & 0x7f = 0x7f: adding 1 to the low seven bits carries into the eighth
+              const uint4 w = reinterpret_cast<const uint4*>(v)[e];
+              carry |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
+                       ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
+            }
+          }
+          const bool nan = (carry & 0x80808080u) != 0;
+          const uint32_t word = __ballot_sync(0xffffffffu, nan);
+          if (lane == 0) ctl->nan_keys[cleaned & 1][warp] = word;
+          if (!bad && (nan || key >= it.len)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) reinterpret_cast<uint4*>(v)[e] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          kv_arrive_warp(&ctl->v_clean[cleaned & 1]);
+        }
+        if (!dead) bad |= !kv_wait_warp([&] { return kv_wait(&ctl->v_clean[cleaned & 1], (cleaned >> 1) & 1, &ctl->abort, 100 + kBarClean); });
+        ++cleaned;
+      }
       float x[R];
-      float ev = 0.f, inv_sv = 1.f;
+      float inv_sv = 1.f;
       bad |= !kv_wait_warp([&] {
         return kv_wait(&ctl->scale_full[i % kScaleRing], (i / kScaleRing) & 1, &ctl->abort, 100 + kBarScale) &&
                kv_wait(&ctl->s_full[buf], (i >> 1) & 1, &ctl->abort, 100 + kBarS);
       });
-      const bool masked = key0 < all_lo || key0 + kKvTile > all_hi;
-      if (masked && !bad) {
-        const int stage = i % F::kStages;
-        bad |= !kv_wait_warp([&] { return kv_wait(&ctl->v_full[stage], (i / F::kStages) & 1, &ctl->abort, 100 + kBarV); });
+      if (dead) {
+        if (bad) return;
+        kv_arrive_warp(&ctl->p_full[buf]);
+        continue;
       }
       if (!bad) {
         tc_fence_after();
-        const float* sc = ctl->scale[i % kScaleRing];
-        const float sk = sc[warp >> 1], sv = sc[2 + (warp >> 1)];
-        ev = (float)((int)(__float_as_uint(sv) >> 23) - 127);  // log2 of a power of two
-        inv_sv = __int_as_float((254 << 23) - __float_as_int(sv));
         uint32_t hi[16], lo[16];
         tmem_ld16(t_lane + buf * F::kN, hi);
-        if (R == 16) {
-          tmem_ld16(t_lane + buf * F::kN + 16, lo);
+        if (R == 16) tmem_ld16(t_lane + buf * F::kN + 16, lo);
+        const float* sc = ctl->scale[i % kScaleRing];
+        const float sk = sc[warp >> 1], sv = sc[2 + (warp >> 1)];
+        const float ev = (float)((int)(__float_as_uint(sv) >> 23) - 127);  // log2 of a power of two
+        inv_sv = __int_as_float((254 << 23) - __float_as_int(sv));
+        if (R == 16)
           tmem_ld_wait(hi, lo);
-        } else {
+        else
           tmem_ld_wait(hi);
-        }
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float s = fmaf(__uint_as_float(R == 16 ? lo[r] : hi[8 + r]), 0.0625f, __uint_as_float(hi[r]));
-          x[r] = fmaf(s, ctl->f[row0 + r] * sk, ev);
+        for (int r = 0; r < R; r += 4) {
+          const float4 f4 = *reinterpret_cast<const float4*>(ctl->f + row0 + r);
+          const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float s = fmaf(__uint_as_float(R == 16 ? lo[r + e] : hi[(8 + r + e) & 15]), 0.0625f, __uint_as_float(hi[r + e]));
+            x[r + e] = fmaf(s, f[e] * sk, ev);
+          }
         }
         if (masked) {
-          // Values no row may use must not meet a zero weight as NaN: a key
-          // row past the sequence, or one that holds a NaN code, becomes
-          // zeros, and in the second case the rows that do attend to it
-          // become NaN.
-          uint8_t* v = sm + F::kOffV + (i % F::kStages) * kTileBytes + tid * kHeadDim;
-          bool nan = false;
-          if (wg == 0 || key < it.len) {
-            uint4 w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = reinterpret_cast<const uint4*>(v)[e];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              // a byte b with b & 0x7f = 0x7f: adding 1 to the low seven bits carries into the eighth
-              nan |= ((((w[e].x & 0x7f7f7f7fu) + 0x01010101u) | ((w[e].y & 0x7f7f7f7fu) + 0x01010101u) |
-                       ((w[e].z & 0x7f7f7f7fu) + 0x01010101u) | ((w[e].w & 0x7f7f7f7fu) + 0x01010101u)) &
-                      0x80808080u) != 0;
-            }
-          }
-          // every warpgroup has looked at the row before the first one clears it
-          if (F::kWgs > 1) bad = named_bar_or(2, F::kSoft, bad);
-          if (wg == 0 && (nan || key >= it.len)) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) reinterpret_cast<uint4*>(v)[e] = make_uint4(0, 0, 0, 0);
-          }
+          const bool nan = (ctl->nan_keys[(cleaned - 1) & 1][warp] >> lane) & 1;
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             const bool in = key >= ctl->key_lo[row0 + r] && key < ctl->key_hi[row0 + r];
@@ -377,21 +417,15 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
           if (lane == r) mine = w;
         }
         if (lane < R) ctl->top[wg][buf][lane][warp] = mine;
-      } else if (masked && F::kWgs > 1) {
-        named_bar_or(2, F::kSoft, true);
       }
-      bad = named_bar_or(1, F::kSoft, bad);
+      bad = named_bar_or(bar, 128, bad);
       if (bad) return;
-      float alpha[R];
+      float now[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const float4 w = *reinterpret_cast<const float4*>(ctl->top[wg][buf][r]);
-        const float top = fmaxf(fmaxf(m[r], fmaxf(w.x, w.y)), fmaxf(w.z, w.w));
-        const float ref = top == kNegInf ? 0.f : top;
-        alpha[r] = ex2(m[r] - ref);
-        m[r] = top;
-        x[r] = ex2(x[r] - ref + 8.f);
-        l[r] = fmaf(l[r], alpha[r], x[r] * inv_sv);
+        now[r] = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
+        x[r] = ex2(x[r] - (now[r] == kNegInf ? 0.f : now[r]) + 8.f);
       }
       // P^T, 16 columns of bytes a key: hi, then lo
       uint8_t* p = sm + F::kOffP + buf * (F::kN * kKvTile) + (wg * (2 * R / 16)) * (16 * kKvTile) + tid * 16;
@@ -410,49 +444,28 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
       fence_proxy_async_smem();
       tc_fence_before();
       kv_arrive_warp(&ctl->p_full[buf]);
-      // the tile before: its O^T is in units of 2^(m before this tile)
-      if (j > 0) {
-        bad |= !kv_wait_warp([&] { return kv_wait(&ctl->o_full[buf ^ 1], ((i - 1) >> 1) & 1, &ctl->abort, 100 + kBarO); });
-        if (!bad) {
-          tc_fence_after();
-          uint32_t h[16], q[16];
-          tmem_ld16(t_lane + (2 + (buf ^ 1)) * F::kN, h);
-          if (R == 16) {
-            tmem_ld16(t_lane + (2 + (buf ^ 1)) * F::kN + 16, q);
-            tmem_ld_wait(h, q);
-          } else {
-            tmem_ld_wait(h);
-          }
+      // under this tile's second product, the tile before
+      if (j > 0) join(i - 1);
 #pragma unroll
-          for (int r = 0; r < R; ++r)
-            o[r] = (o[r] + (__uint_as_float(h[r]) + __uint_as_float(R == 16 ? q[r] : h[8 + r]))) * alpha[r];
-        }
+      for (int r = 0; r < R; ++r) {
+        top[r] = now[r];
+        sum[r] = x[r] * inv_sv;
       }
     }
+    if (dead) continue;
     if (tiles > 0) {
-      const int buf = (i - 1) & 1;
-      bad |= !kv_wait_warp([&] { return kv_wait(&ctl->o_full[buf], ((i - 1) >> 1) & 1, &ctl->abort, 100 + kBarO); });
+      join(i - 1);
+      tc_fence_before();
       if (!bad) {
-        tc_fence_after();
-        uint32_t h[16], q[16];
-        tmem_ld16(t_lane + (2 + buf) * F::kN, h);
-        if (R == 16) {
-          tmem_ld16(t_lane + (2 + buf) * F::kN + 16, q);
-          tmem_ld_wait(h, q);
-        } else {
-          tmem_ld_wait(h);
-        }
-        tc_fence_before();
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          o[r] += __uint_as_float(h[r]) + __uint_as_float(R == 16 ? q[r] : h[8 + r]);
           float s = l[r];
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
           if (lane == 0) ctl->sum[wg][r][warp] = s;
         }
       }
-      bad = named_bar_or(1, F::kSoft, bad);
+      bad = named_bar_or(bar, 128, bad);
       if (bad) return;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -482,7 +495,7 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
       if (threadIdx.x == 0 && cur.off == 0)
         a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(a, ctl->run.run, cur));
     }
-    if (tiles > 0) named_bar_sync(1, F::kSoft);  // the sums are read before the next item's are written
+    if (tiles > 0) named_bar_sync(bar, 128);  // the sums are read before the next item's are written
   }
 }
 
@@ -503,6 +516,8 @@ __global__ void __launch_bounds__(Few<NR>::kThreads, Few<NR>::kCtasPerSm)
       mbar_init(&ctl.v_free[s], 1);
     }
     mbar_init(&ctl.q_full, F::kSoft / 32);
+    mbar_init(&ctl.v_clean[0], 4);
+    mbar_init(&ctl.v_clean[1], 4);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl.s_full[b], 1);
       mbar_init(&ctl.p_full[b], F::kSoft / 32);

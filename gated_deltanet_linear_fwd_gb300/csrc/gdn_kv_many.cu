@@ -17,11 +17,11 @@
 // parts instead would cost the softmax warps four more instructions a weight.
 //
 // Softmax: a thread owns a row.  x_j = scale log2(e) q . k_j; the values' page
-// scale 2^e_v is folded into the exponent, P_j = 2^(x_j + e_v - m), so P times
-// the codes is the output in units of 2^m; the softmax's sum is of P_j 2^-e_v in
+// scale 2^e_v is folded into the exponent, P_j = 2^(x_j + e_v - m + 6), so P times
+// the codes is the output in units of 2^(m - 6); the softmax's sum is of P_j 2^-e_v in
 // fp32.  m follows the running maximum of x + e_v only when that has grown by
-// more than 12, so O in tensor memory is rarely rescaled; P stays below 2^12,
-// within fp16.
+// more than 9, so O in tensor memory is rarely rescaled; P stays below 2^15,
+// within fp16, which loses only weights below 2^-30 of the largest.
 //
 // Tensor memory (512 columns): S of either tile (P over its middle) and O
 // of either tile.  Each tile has an MMA warp that alternates P V of
@@ -338,7 +338,7 @@ __device__ __forceinline__ float2 add2(float2 a, float b0, float b1) {
 }
 
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kLazy = 12.f;
+constexpr float kLazy = 9.f, kLift = 6.f;
 
 // Under the masks: -inf for keys outside [lo, hi) of these 32, NaN for keys
 // whose values hold one.
@@ -549,7 +549,7 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
         l *= alpha;
         if (grow) m = top;
       }
-      const float ref = m == kNegInf ? 0.f : m;
+      const float ref = (m == kNegInf ? 0.f : m) - kLift;
       // The weights go over scores this thread has read: columns 32 to 95.
       float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
       weights32(t_s + 64, s2, fk1, ev1 - ref, sum1);
@@ -581,9 +581,9 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
     many_output(t_o, tiles > 0, whole, l, sm + kOffQ + q * 2 * kTileBytes + warp * 8192, whole && !live ? nullptr : dst);
     tc_fence_before();
     if (whole) {
-      if (live && a.lse) a.lse[tok * a.c.h_q + head0 + g] = kv_lse(m, l);
+      if (live && a.lse) a.lse[tok * a.c.h_q + head0 + g] = kv_lse(m - kLift, l);
     } else {
-      a.ml[part] = make_float2(m, l);
+      a.ml[part] = make_float2(m - kLift, l);
       if (threadIdx.x == 0 && cur.off == 0)
         a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(a, ctl->run.run, cur));
     }

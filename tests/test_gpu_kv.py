@@ -231,6 +231,31 @@ def test_attn_scales_far_apart(gdn, dtype, n):
     check_attn(gdn, b, 4, dtype)
 
 
+@pytest.mark.parametrize("n", [1, 3, 9])
+def test_attn_one_key_against_many(gdn, n):
+    """One key with a weight 2^20 times the others', half a million of which together outweigh it."""
+    kv = 500_000
+    b = U.Batch([n], [kv], 1, seed=n)
+    pages = b.table[0].long()
+    b.k, b.ks = torch.zeros(b.n_pages, 1, 64, 128), torch.ones(b.n_pages, 1)
+    b.v, b.vs = torch.zeros(b.n_pages, 1, 64, 128), torch.ones(b.n_pages, 1)
+    b.v[pages] = 1.0
+    b.v[pages[0], 0, 0] = -1.0
+    q = torch.zeros(n, 4, 128)
+    q[..., 0] = 1.0
+    q[..., 1] = 0.5  # not a single e4m3 part of its row
+    b.k[pages[0], 0, 0, 0] = 1.0
+    scale = 20 * math.log(2.0)
+    rest = kv - n + torch.arange(n)  # keys besides the first that row t sees
+    w0 = 2.0 ** 20 / (2.0 ** 20 + rest.double())
+    cache = to_cache(gdn, b)
+    out, lse = gdn.gdn_kv_attn(q.to(BF).cuda(), cache, b.lens.cuda(), b.table.cuda(), scale=scale)
+    want = (1 - 2 * w0)[:, None, None]
+    # two bf16 roundings of weights and output, relative to the weights' sum of one
+    assert (out.double().cpu() - want).abs().max() <= 2.0 ** -7
+    assert (lse.double().cpu() - torch.log(2.0 ** 20 + rest.double())[:, None]).abs().max() <= 2.0 ** -14
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("n,window", [(1, 64), (5, 0), (5, 70), (200, 0), (300, 33)])
 def test_attn_nan_outside_masks(gdn, dtype, n, window):

@@ -384,8 +384,9 @@ constexpr int kKvPathSimt = 0;  // fp32 on the CUDA cores
 constexpr int kKvPathFew = 1;   // bf16, up to 32 rows per (sequence, key/value head)
 constexpr int kKvPathMany = 2;  // bf16, more rows
 // What parts and the second kernel cost, in key tiles: about 38 us at 1.35 us a
-// tile of 256 rows, about 6 us at 0.7 us a tile of few.
-constexpr int kKvJoinTilesMany = 28, kKvJoinTiles = 8;
+// tile of 256 rows on the tensor cores, 6 us at 0.7 us a tile of few rows, 6 us
+// at 5 to 10 us a tile on the CUDA cores.
+constexpr int kKvJoinTilesMany = 28, kKvJoinTilesFew = 8, kKvJoinTilesSimt = 1;
 
 }  // namespace
 
@@ -857,11 +858,11 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   std::memset(&p, 0, sizeof(p));
   const int group = (d->h_q + h_kv - 1) / h_kv;
   if ((int64_t)d->T * group > 0x7fffffff - 4096) return GDN_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)max_q_len * group;
   p.path = kKvPathSimt;
-  p.rows = 16;
+  p.rows = rows <= 32 ? 16 : 64;  // the larger tile reads a third of the shared memory a row
   p.item_cost = 1;
   int per_sm = 2;
-  const int64_t rows = (int64_t)max_q_len * group;
   if (d->dtype == GDN_BF16 && rows <= 32) {
     p.path = kKvPathFew;
     p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
@@ -894,11 +895,14 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
     longest_item = std::max(longest_item, cost);
     shortest = std::min(shortest, cost);
   }
+  // the kernels count units in 32 bits, whatever the lengths on the device turn out to be
+  const int64_t units_most = (int64_t)d->max_pages * kPage / kKvTile + 1 + p.item_cost;
+  if (items > 0x7fffffff / units_most) return GDN_ERR_INVALID_ARG;
   total *= (int64_t)d->n_seqs * h_kv;
   const int64_t whole = longest_item == shortest ? (items + slots - 1) / slots * longest_item
                                                  : std::max(longest_item, (total + slots - 1) / slots + shortest);
-  const int64_t runs = (total + slots - 1) / slots + (p.path == kKvPathMany ? kKvJoinTilesMany : kKvJoinTiles);
-  p.n_ctas = whole <= runs && items <= 0x7fffffff ? 0 : (int)std::min<int64_t>(slots, total);
+  const int64_t runs = (total + slots - 1) / slots + (p.path == kKvPathMany ? kKvJoinTilesMany : p.path == kKvPathFew ? kKvJoinTilesFew : kKvJoinTilesSimt);
+  p.n_ctas = whole <= runs ? 0 : (int)std::min<int64_t>(slots, total);
   p.n_seqs = d->n_seqs;
   p.T = d->T;
   p.h_q = d->h_q;

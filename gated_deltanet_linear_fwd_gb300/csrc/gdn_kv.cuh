@@ -156,7 +156,11 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs& a, int seq, int rt) 
     it.tiles = -1;
     return it;
   }
-  const int t0 = r0 / a.group, t1 = min(s.n - 1, (r0 + a.rows - 1) / a.group);
+  int t0 = 0, t1 = s.n - 1;
+  if (a.max_row_tiles > 1) {
+    t0 = r0 / a.group;
+    t1 = min(t1, (r0 + a.rows - 1) / a.group);
+  }
   const int past = s.len - s.n;  // position of the first new token; negative for idle slots
   const int hi = a.causal ? min(max(past + t1 + 1, 0), s.len) : s.len;
   const int lo = a.window > 0 ? max(0, past + t0 - a.window + 1) : 0;
@@ -172,40 +176,36 @@ __device__ __forceinline__ int kv_cost(const KvAttnArgs& a, const KvItem& it) {
 struct KvRun {
   int seq, rt, head, off;  // first item of the run and the unit of it (of item_cost + tiles) that the run starts with
   KvItem item;             // that item
-  int64_t begin, end;      // units
-  int64_t total;           // units of the call
+  uint32_t begin, end;     // units
+  uint32_t total;          // units of the call; the host refuses calls that could have 2^31
   int ctas;                // CTAs that have a run: no more than there are units
 };
 
 // A CTA's run, found by all its threads (NT of them, a multiple of 32) from
 // the lengths and left in shared memory.
 struct KvRunScratch {
-  int64_t part[32];
+  uint32_t part[32];
   KvRun run;
 };
 // Inclusive sum over the block's threads; total: the block's sum.
 template <int NT>
-__device__ __forceinline__ int64_t block_inclusive_scan(int v, KvRunScratch* sc, int64_t& total) {
+__device__ __forceinline__ uint32_t block_inclusive_scan(uint32_t v, KvRunScratch* sc, uint32_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t sum = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, sum, d);
-    if (lane >= d) sum += u;
+    const uint32_t u = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += u;
   }
   __syncthreads();
-  if (lane == 31) sc->part[warp] = sum;
+  if (lane == 31) sc->part[warp] = v;
   __syncthreads();
-  int64_t before = 0;
-  total = 0;
-#pragma unroll 1
-  for (int w = 0; w < NT / 32; ++w) {
-    const int64_t p = sc->part[w];
-    if (w < warp) before += p;
-    total += p;
-  }
-  return sum + before;
+  const uint32_t p = lane < NT / 32 ? sc->part[lane] : 0;
+  total = __reduce_add_sync(0xffffffffu, p);
+  return v + __reduce_add_sync(0xffffffffu, lane < warp ? p : 0);
 }
+// All of it is on the way to a CTA's first load, mostly as instructions not
+// yet in the cache: one scan when the threads have an entry each (any decode
+// batch of up to NT sequences), no 64-bit division.
 template <int NT>
 __device__ __noinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
   const int tid = threadIdx.x;
@@ -226,53 +226,56 @@ __device__ __noinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
     return;
   }
   const int entries = a.c.n_seqs * a.max_row_tiles;
-  // units over all entries, or, when the block's threads have one each (any
-  // decode batch of up to NT sequences), their running sum at once
-  int64_t total = 0, base = 0, incl = 0;
   KvItem it;
-  int seq = 0, rt = 0, u = 0;
-#pragma unroll 1
-  for (int e0 = 0; e0 < entries; e0 += NT) {
-    const int e = e0 + tid;
-    seq = e / a.max_row_tiles;
-    rt = e - seq * a.max_row_tiles;
+  int seq = 0, rt = 0;
+  uint32_t total = 0, base = 0, incl = 0, u = 0;
+  auto entry = [&](int e) {
+    seq = e;
+    rt = 0;
+    if (a.max_row_tiles > 1) {
+      seq = e / a.max_row_tiles;
+      rt = e - seq * a.max_row_tiles;
+    }
     u = 0;
     if (e < entries) {
       it = kv_item(a, seq, rt);
       u = kv_cost(a, it) * a.c.h_kv;
     }
-    int64_t sub;
+  };
+#pragma unroll 1
+  for (int e0 = 0; e0 < entries; e0 += NT) {
+    entry(e0 + tid);
+    uint32_t sub;
     incl = block_inclusive_scan<NT>(u, sc, sub);
     total += sub;
   }
-  const int ctas = (int)min((int64_t)a.n_ctas, total), cta = blockIdx.x;
-  const int64_t begin = cta < ctas ? total * cta / ctas : 0, end = cta < ctas ? total * (cta + 1) / ctas : 0;
+  // run c is [total c / ctas, total (c + 1) / ctas), rounded down
+  const uint32_t ctas = min((uint32_t)a.n_ctas, total), cta = blockIdx.x;
+  uint32_t begin = 0, end = 0;
+  if (cta < ctas) {
+    const uint32_t each = total / ctas, rest = total - each * ctas;
+    begin = each * cta + rest * cta / ctas;
+    end = each * (cta + 1) + rest * (cta + 1) / ctas;
+  }
   if (tid == 0) {
     sc->run.begin = begin;
     sc->run.end = end;
     sc->run.total = total;
-    sc->run.ctas = ctas;
+    sc->run.ctas = (int)ctas;
   }
 #pragma unroll 1
   for (int e0 = 0; e0 < entries && base <= begin && begin < end; e0 += NT) {
-    int64_t sub = total;
+    uint32_t sub = total;
     if (entries > NT) {
-      const int e = e0 + tid;
-      seq = e / a.max_row_tiles;
-      rt = e - seq * a.max_row_tiles;
-      u = 0;
-      if (e < entries) {
-        it = kv_item(a, seq, rt);
-        u = kv_cost(a, it) * a.c.h_kv;
-      }
+      entry(e0 + tid);
       incl = base + block_inclusive_scan<NT>(u, sc, sub);
     }
     if (incl - u <= begin && begin < incl) {
-      const int in = (int)(begin - (incl - u)), cost = kv_cost(a, it);
+      const uint32_t in = begin - (incl - u), cost = kv_cost(a, it), head = in / cost;
       sc->run.seq = seq;
       sc->run.rt = rt;
-      sc->run.head = in / cost;
-      sc->run.off = in % cost;
+      sc->run.head = (int)head;
+      sc->run.off = (int)(in - head * cost);
       sc->run.item = it;
     }
     base += sub;
@@ -329,9 +332,10 @@ struct KvCursor {
 };
 
 // The last CTA that has a part of the item whose first part this cursor
-// stands on: CTA c owns unit u when c = floor(((u + 1) ctas - 1) / total).
+// stands on: the one whose run has the item's last unit u, the largest c with
+// total c / ctas <= u, so floor(((u + 1) ctas - 1) / total).
 __device__ __forceinline__ int kv_last_cta(const KvAttnArgs& a, const KvRun& r, const KvCursor& c) {
-  const int64_t item_end = r.begin + c.base + kv_cost(a, c.it);
+  const int64_t item_end = (int64_t)r.begin + c.base + kv_cost(a, c.it);
   return (int)((item_end * r.ctas - 1) / r.total);
 }
 
@@ -380,7 +384,7 @@ __device__ __forceinline__ int e4m3_scale_exp(uint32_t a_bits, int least) {
 // ---- launchers ----
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool f32, unsigned entries, cudaStream_t st);
 cudaError_t launch_kv_read(const KvAppendArgs& a, bool f32, unsigned entries, cudaStream_t st);
-cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, unsigned grid, cudaStream_t st);  // fp32 q and out
+cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, unsigned grid, cudaStream_t st);  // fp32 q and out; 16 or 64 rows
 cudaError_t launch_kv_combine(const KvAttnArgs& a, bool f32, cudaStream_t st);
 cudaError_t kv_simt_setup();
 // rows: 8, 16 or 32 (KvAttnArgs::rows); kmap, vmap: the pools as [page and head][64][128 bytes]

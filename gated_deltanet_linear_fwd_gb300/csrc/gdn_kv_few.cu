@@ -119,16 +119,9 @@ __device__ __forceinline__ void few_load(const KvAttnArgs& a, FewCtl<NR>* ctl, u
         const uint32_t parity = (i / F::kStages) & 1;
         const int p0 = __shfl_sync(0xffffffffu, my_page, 2 * j), p1 = __shfl_sync(0xffffffffu, my_page, 2 * j + 1);
         if (!kv_wait_warp([&] { return kv_wait(&ctl->k_free[stage], parity ^ 1, &ctl->abort, 100 + kBarKFree); })) return;
-        if ((lane >> 1) == j) {
-          float* s = ctl->scale[i % kScaleRing];
-          s[lane & 1] = my_page >= 0 ? my_sk : 1.f;
-          s[2 + (lane & 1)] = my_page >= 0 ? my_sv : 1.f;
-        }
-        __syncwarp();
+        // a tile's second page may lie past the sequence: its rows keep what they hold and are masked
+        const uint32_t bytes = p1 >= 0 ? kTileBytes : kTileBytes / 2;
         if (lane == 0) {
-          mbar_arrive(&ctl->scale_full[i % kScaleRing]);
-          // a tile's second page may lie past the sequence: its rows keep what they hold and are masked
-          const uint32_t bytes = p1 >= 0 ? kTileBytes : kTileBytes / 2;
           uint8_t* dst = sm + stage * kTileBytes;
           mbar_arrive_expect_tx(&ctl->k_full[stage], bytes);
           tma_load_3d(dst, kmap, &ctl->k_full[stage], 0, 0, p0);
@@ -136,12 +129,19 @@ __device__ __forceinline__ void few_load(const KvAttnArgs& a, FewCtl<NR>* ctl, u
         }
         if (!kv_wait_warp([&] { return kv_wait(&ctl->v_free[stage], parity ^ 1, &ctl->abort, 100 + kBarVFree); })) return;
         if (lane == 0) {
-          const uint32_t bytes = p1 >= 0 ? kTileBytes : kTileBytes / 2;
           uint8_t* dst = sm + F::kOffV + stage * kTileBytes;
           mbar_arrive_expect_tx(&ctl->v_full[stage], bytes);
           tma_load_3d(dst, vmap, &ctl->v_full[stage], 0, 0, p0);
           if (p1 >= 0) tma_load_3d(dst + kTileBytes / 2, vmap, &ctl->v_full[stage], 0, 0, p1);
         }
+        // last, since the scales' loads follow the page's
+        if ((lane >> 1) == j) {
+          float* s = ctl->scale[i % kScaleRing];
+          s[lane & 1] = my_page >= 0 ? my_sk : 1.f;
+          s[2 + (lane & 1)] = my_page >= 0 ? my_sv : 1.f;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->scale_full[i % kScaleRing]);
       }
     }
   }

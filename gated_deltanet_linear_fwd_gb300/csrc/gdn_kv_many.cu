@@ -17,11 +17,11 @@
 // parts instead would cost the softmax warps four more instructions a weight.
 //
 // Softmax: a thread owns a row.  x_j = scale log2(e) q . k_j; the values' page
-// scale 2^e_v is folded into the exponent, P_j = 2^(x_j + e_v - m + 6), so P times
-// the codes is the output in units of 2^(m - 6); the softmax's sum is of P_j 2^-e_v in
+// scale 2^e_v is folded into the exponent, P_j = 2^(x_j + e_v - m + 3), so P times
+// the codes is the output in units of 2^(m - 3); the softmax's sum is of P_j 2^-e_v in
 // fp32.  m follows the running maximum of x + e_v only when that has grown by
-// more than 9, so O in tensor memory is rarely rescaled; P stays below 2^15,
-// within fp16, which loses only weights below 2^-30 of the largest.
+// more than 12, so O in tensor memory is rarely rescaled; P stays below 2^15,
+// within fp16, which loses only weights below 2^-28 of 2^m.
 //
 // Tensor memory (512 columns): S of either tile (P over its middle) and O
 // of either tile.  Each tile has an MMA warp that alternates P V of
@@ -38,7 +38,7 @@ namespace {
 constexpr int kRows = 256;
 constexpr int kThreads = 512;  // two softmax warpgroups, one converting values, one of TMA and MMA warps
 constexpr int kValuesWarp = 8, kTmaWarp = 12, kMmaWarp = 13;  // MMA warps 13 and 14
-constexpr int kSoftRegs = 168, kOtherRegs = 88;  // 256 x 168 + 256 x 88 = 512 x 128, the registers at launch
+constexpr int kSoftRegs = 184, kOtherRegs = 72;  // 256 x 184 + 256 x 72 = 512 x 128, the registers at launch
 constexpr int kTileBytes = kKvTile * kHeadDim;
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScaleRing = 8;
 
@@ -338,7 +338,7 @@ __device__ __forceinline__ float2 add2(float2 a, float b0, float b1) {
 }
 
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kLazy = 9.f, kLift = 6.f;
+constexpr float kLazy = 12.f, kLift = 3.f;
 
 // Under the masks: -inf for keys outside [lo, hi) of these 32, NaN for keys
 // whose values hold one.
@@ -374,7 +374,7 @@ __device__ __forceinline__ void weights32(uint32_t t_p, const uint32_t (&s)[32],
 
 // This thread's query row (null: zeros) into its two e4m3 parts in shared
 // memory; returns its score factor.
-__device__ __noinline__ float many_query(float scale_log2, const __nv_bfloat16* src, int row, uint8_t* hi_tile) {
+__device__ __forceinline__ float many_query(float scale_log2, const __nv_bfloat16* src, int row, uint8_t* hi_tile) {
   uint4 x[16];
 #pragma unroll
   for (int c = 0; c < 16; ++c) x[c] = src ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
@@ -401,53 +401,47 @@ __device__ __noinline__ float many_query(float scale_log2, const __nv_bfloat16* 
   return m < 0x7f800000u ? pow2f(ex) * fabsf(scale_log2) : __int_as_float(0x7fffffff);
 }
 
-// 256 bytes of each of the warp's 32 rows to global memory, 512 contiguous
-// bytes an instruction, through the warp's part of `stage` (8 KB).  dst: this
-// thread's row, or null.
-__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&w)[64], uint8_t* dst) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int c = 0; c < 16; ++c)
-    *reinterpret_cast<uint4*>(stage + lane * 256 + ((c ^ (lane & 7)) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-  __syncwarp();
-  const int c = lane & 15;
-#pragma unroll 4
-  for (int k = 0; k < 16; ++k) {
-    const int row = 2 * k + (lane >> 4);
-    uint8_t* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
-    const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 256 + ((c ^ (row & 7)) << 4));
-    if (to) reinterpret_cast<uint4*>(to)[c] = v;
-  }
-  __syncwarp();
-}
-
 // The warp's 32 rows of O out of tensor memory: divided by l in bf16, or, for
-// a part of an item, as they are.  dst: this thread's row, or null.
-__device__ __noinline__ void many_output(uint32_t t_o, bool any, bool whole, float l, uint8_t* stage, uint8_t* dst) {
-  uint32_t w[64];
-  if (whole) {
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      uint32_t o[32];
-      if (any) {
-        tmem_ld32(t_o + 32 * h, o);
-        tmem_ld_done(o);
-      }
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        w[16 * h + k] = !any || l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-    }
-    store_rows(stage, w, dst);
-  } else {
+// a part of an item, as they are.  256 bytes of each row at a time go through
+// the warp's 8 KB of `stage`, so that a store covers 512 contiguous bytes (a
+// row a thread, it took 6000 cycles instead of 4000).  dst: this thread's row,
+// or null.
+__device__ __forceinline__ void many_output(uint32_t t_o, bool any, bool whole, float l, uint8_t* stage, uint8_t* dst) {
+  const int lane = threadIdx.x & 31;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
 #pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
-      tmem_ld32(t_o + 64 * h, w);
-      tmem_ld32(t_o + 64 * h + 32, w + 32);
-      tmem_ld_done(w);
-      tmem_ld_done(w + 32);
-      store_rows(stage, w, dst + 256 * h);
+  for (int h = 0; h < (whole ? 1 : 2); ++h) {
+#pragma unroll 1
+    for (int c = 0; c < (whole ? 8 : 4); ++c) {
+      uint32_t o[16];
+      if (any) {
+        tmem_ld16(t_o + 64 * h + 16 * c, o);
+        tmem_ld_wait(o);
+      }
+      if (whole) {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          w[k] = !any || l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<uint4*>(stage + lane * 256 + (((2 * c + k) ^ (lane & 7)) << 4)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * c + k) ^ (lane & 7)) << 4)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
     }
+    __syncwarp();
+    const int c = lane & 15;
+#pragma unroll 2
+    for (int k = 0; k < 16; ++k) {
+      const int row = 2 * k + (lane >> 4);
+      uint8_t* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 256 + ((c ^ (row & 7)) << 4));
+      if (to) reinterpret_cast<uint4*>(to + 256 * h)[c] = v;
+    }
+    __syncwarp();
   }
 }
 
@@ -459,8 +453,8 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
   KvCursor cur;
 #pragma unroll 1
   for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
-    const KvItem& it = cur.it;
-    const int tiles = cur.tiles();
+    const KvItem it = cur.it;
+    const int tiles = cur.tiles(), first_key = cur.tile_begin() * kKvTile;
     const ManyItem mi = many_item(a, cur);
     if (q >= mi.q_tiles) {
       i += tiles;
@@ -478,7 +472,7 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
     }
 #pragma unroll 1
     for (int j = 0; j < tiles; ++j, ++i, ++n) {
-      const int key0 = (cur.tile_begin() + j) * kKvTile;
+      const int key0 = first_key + j * kKvTile;
       const bool masked = key0 < mi.all_lo || key0 + kKvTile > mi.all_hi;
       const int stage = i % kHStages;
       if (!kv_wait_warp([&] {

@@ -6,10 +6,13 @@
 // 2^(x_j - m), output sum 2^(x_j - m) v_j / l, one pass over the keys, both
 // rescaled by 2^(m_old - m) when m grows.
 //
-// A CTA takes 16 rows of a key/value head's group and one page (64 keys) at a
-// time: thread (r, c) forms the scores of row r with keys c, c + 16, ...,
-// then columns 8 c .. 8 c + 7 of row r's output.  Bound by shared-memory reads
-// (a key or value element feeds 16 rows) and fp32 FMAs.
+// A CTA takes 16 kR rows of a key/value head's group and one page (64 keys) at
+// a time: thread (y, x) forms the scores of rows y, y + 16, ... with keys x,
+// x + 16, x + 32, x + 48, then columns 4 x .. and 64 + 4 x .. of those rows' output.
+// Bound by shared-memory reads, and those by kR: 4 + kR 16-byte reads feed 16 kR
+// FMAs.  kR is 4 where there are the rows for it, 1 for a few (one token's
+// group, a long axis).  Keys and values take turns in one buffer, so two CTAs
+// fit an SM.
 #include "gdn_kv.cuh"
 #include "sm103_ptx.cuh"
 
@@ -17,17 +20,33 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 16;
 constexpr int kKeyStride = kHeadDim + 4;  // floats; rows 4 banks apart
 constexpr int kSStride = kPage + 4;
 
+template <int kR>
 struct SimtSmem {
-  float q[kRows][kHeadDim];
-  float k[kPage][kKeyStride];
-  float v[kPage][kHeadDim];
-  float s[kRows][kSStride];
+  float q[16 * kR][kHeadDim];
+  float kv[kPage][kKeyStride];
+  float s[16 * kR][kSStride];
   KvRunScratch run;
 };
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// A page's codes of one head as fp32; rows past the sequence, which may hold anything, as zeros.
+__device__ __forceinline__ void load_page(float (&dst)[kPage][kKeyStride], const uint8_t* codes, float scale, int rows) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int ch = i * kThreads + (int)threadIdx.x, row = ch >> 3, col = (ch & 7) * 16;
+    const uint4 w4 = row < rows ? __ldg(reinterpret_cast<const uint4*>(codes) + ch) : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = e4m3x2_to_f32x2(w[e]), b = e4m3x2_to_f32x2(w[e] >> 16);
+      *reinterpret_cast<float4*>(&dst[row][col + 4 * e]) = make_float4(a.x * scale, a.y * scale, b.x * scale, b.y * scale);
+    }
+  }
+}
 
 __device__ __forceinline__ void store4(float* p, float a, float b, float c, float d) {
   *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
@@ -36,10 +55,12 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float a, float b, float
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
 }
 
-__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const KvAttnArgs a) {
+template <int kR>
+__global__ void __launch_bounds__(kThreads, 2) attn_simt_kernel(const KvAttnArgs a) {
+  constexpr int kRows = 16 * kR;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  SimtSmem& sm = *reinterpret_cast<SimtSmem*>(smem_raw);
-  const int tid = threadIdx.x, r = tid >> 4, c = tid & 15;
+  SimtSmem<kR>& sm = *reinterpret_cast<SimtSmem<kR>*>(smem_raw);
+  const int tid = threadIdx.x, y = tid >> 4, x = tid & 15;
   grid_dependency_wait();
   kv_run<kThreads>(a, &sm.run);
   const KvRun& run = sm.run.run;
@@ -47,110 +68,133 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const KvAttnArgs a)
   KvCursor cur;
 #pragma unroll 1
   for (cur.start(a, run); cur.valid(); cur.next(a)) {
-    const KvItem& it = cur.it;
-    // row r of the item: token t of the sequence, query head j
-    const int rr = cur.rt * kRows + r, t = rr / a.group;
-    const int j = kv_first_q_head(a.c, cur.head) + rr % a.group;
-    const bool live = t < it.n && j < kv_first_q_head(a.c, cur.head + 1);
-    const int p = it.len - it.n + t;
-    const int key_end = live ? (a.causal ? min(p + 1, it.len) : it.len) : 0;
-    const int key_begin = a.window > 0 ? max(0, p - a.window + 1) : 0;
+    const KvItem it = cur.it;
+    const int head0 = kv_first_q_head(a.c, cur.head), group = kv_first_q_head(a.c, cur.head + 1) - head0;
+    // row y + 16 i of the item: token t of the sequence, query head head0 + g
+    int t[kR], g[kR], key_begin[kR], key_end[kR];
+    bool live[kR];
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      sm.q[r][c + 16 * e] =
-          live ? reinterpret_cast<const float*>(a.q)[(int64_t)(it.tok0 + t) * a.q_stride + j * kHeadDim + c + 16 * e]
-               : 0.f;
-    float m = -__int_as_float(0x7f800000), l = 0.f, o[8] = {};
+    for (int i = 0; i < kR; ++i) {
+      const int rr = cur.rt * kRows + y + 16 * i;
+      t[i] = rr / a.group;
+      g[i] = rr - t[i] * a.group;
+      live[i] = t[i] < it.n && g[i] < group;
+      const int p = it.len - it.n + t[i];
+      key_end[i] = live[i] ? (a.causal ? min(p + 1, it.len) : it.len) : 0;
+      key_begin[i] = a.window > 0 ? max(0, p - a.window + 1) : 0;
+      const float* src = reinterpret_cast<const float*>(a.q) + (int64_t)(it.tok0 + t[i]) * a.q_stride + (head0 + g[i]) * kHeadDim;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<float4*>(&sm.q[y + 16 * i][4 * x + 64 * e]) =
+            live[i] ? __ldg(reinterpret_cast<const float4*>(src + 4 * x + 64 * e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float m[kR], l[kR], o[kR][8];
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+      m[i] = kNegInf;
+      l[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[i][e] = 0.f;
+    }
     const int page_begin = 2 * cur.tile_begin(), page_end = min(page_begin + 2 * cur.tiles(), (it.len + kPage - 1) / kPage);
+#pragma unroll 1
     for (int pg = page_begin; pg < page_end; ++pg) {
-      __syncthreads();
-      const int page = kv_page(a.c, cur.seq, pg);
+      const int page = kv_page(a.c, cur.seq, pg), rows = it.len - pg * kPage;
       const size_t head = (size_t)max(page, 0) * a.c.h_kv + cur.head;
-      const float sk = a.c.k_scale[head], sv = a.c.v_scale[head];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int ch = i * kThreads + tid, row = ch >> 3, col = (ch & 7) * 16;
-        const bool in = pg * kPage + row < it.len;  // rows past the sequence may hold anything
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        const uint4 wk = in ? __ldg(reinterpret_cast<const uint4*>(a.c.k + head * kPageBytes) + ch) : zero;
-        const uint4 wv = in ? __ldg(reinterpret_cast<const uint4*>(a.c.v + head * kPageBytes) + ch) : zero;
-        const uint32_t kk[4] = {wk.x, wk.y, wk.z, wk.w}, vv[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float2 k0 = e4m3x2_to_f32x2(kk[w]), k1 = e4m3x2_to_f32x2(kk[w] >> 16);
-          const float2 v0 = e4m3x2_to_f32x2(vv[w]), v1 = e4m3x2_to_f32x2(vv[w] >> 16);
-          *reinterpret_cast<float4*>(&sm.k[row][col + 4 * w]) = make_float4(k0.x * sk, k0.y * sk, k1.x * sk, k1.y * sk);
-          *reinterpret_cast<float4*>(&sm.v[row][col + 4 * w]) = make_float4(v0.x * sv, v0.y * sv, v1.x * sv, v1.y * sv);
-        }
-      }
       __syncthreads();
-      float x[4] = {};
-#pragma unroll 4
-      for (int d = 0; d < kHeadDim; d += 4) {
-        const float4 q4 = *reinterpret_cast<const float4*>(&sm.q[r][d]);
+      load_page(sm.kv, a.c.k + head * kPageBytes, a.c.k_scale[head], rows);
+      __syncthreads();
+      float s[kR][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 k4 = *reinterpret_cast<const float4*>(&sm.k[c + 16 * i][d]);
-          x[i] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, x[i]))));
+      for (int i = 0; i < kR; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
+#pragma unroll 2
+      for (int d = 0; d < kHeadDim; d += 4) {
+        float4 k4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) k4[c] = *reinterpret_cast<const float4*>(&sm.kv[x + 16 * c][d]);
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+          const float4 q4 = *reinterpret_cast<const float4*>(&sm.q[y + 16 * i][d]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            s[i][c] = fmaf(q4.x, k4[c].x, fmaf(q4.y, k4[c].y, fmaf(q4.z, k4[c].z, fmaf(q4.w, k4[c].w, s[i][c]))));
         }
       }
-      float top = m;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = pg * kPage + c + 16 * i;
-        x[i] = key >= key_begin && key < key_end ? x[i] * a.scale_log2 : -__int_as_float(0x7f800000);
-        top = fmaxf(top, x[i]);
+      for (int i = 0; i < kR; ++i) {
+        float top = m[i];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int key = pg * kPage + x + 16 * c;
+          s[i][c] = key >= key_begin[i] && key < key_end[i] ? s[i][c] * a.scale_log2 : kNegInf;
+          top = fmaxf(top, s[i][c]);
+        }
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float ref = top == kNegInf ? 0.f : top, alpha = exp2f(m[i] - ref);
+        m[i] = top;
+        l[i] *= alpha;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float w = exp2f(s[i][c] - ref);
+          l[i] += w;
+          sm.s[y + 16 * i][x + 16 * c] = w;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[i][e] *= alpha;
       }
+      __syncthreads();  // the keys are read; a row's weights are its half warp's own
+      load_page(sm.kv, a.c.v + head * kPageBytes, a.c.v_scale[head], rows);
+      __syncthreads();
+#pragma unroll 1
+      for (int k = 0; k < kPage; k += 4) {
+        float w[kR][4];
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      const float ref = top == -__int_as_float(0x7f800000) ? 0.f : top;
-      const float alpha = exp2f(m - ref);
-      l *= alpha;
+        for (int i = 0; i < kR; ++i) *reinterpret_cast<float4*>(w[i]) = *reinterpret_cast<const float4*>(&sm.s[y + 16 * i][k]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float w = exp2f(x[i] - ref);
-        l += w;
-        sm.s[r][c + 16 * i] = w;
-      }
-      m = top;
+        for (int c = 0; c < 4; ++c) {
+          const float4 v0 = *reinterpret_cast<const float4*>(&sm.kv[k + c][4 * x]);
+          const float4 v1 = *reinterpret_cast<const float4*>(&sm.kv[k + c][64 + 4 * x]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] *= alpha;
-      __syncwarp();  // a row's 16 threads are in one warp
-#pragma unroll 4
-      for (int i = 0; i < kPage; ++i) {
-        const float w = sm.s[r][i];
-        if (w == 0.f) continue;  // a masked value may be NaN
-        const float4 v0 = *reinterpret_cast<const float4*>(&sm.v[i][8 * c]);
-        const float4 v1 = *reinterpret_cast<const float4*>(&sm.v[i][8 * c + 4]);
-        o[0] = fmaf(w, v0.x, o[0]);
-        o[1] = fmaf(w, v0.y, o[1]);
-        o[2] = fmaf(w, v0.z, o[2]);
-        o[3] = fmaf(w, v0.w, o[3]);
-        o[4] = fmaf(w, v1.x, o[4]);
-        o[5] = fmaf(w, v1.y, o[5]);
-        o[6] = fmaf(w, v1.z, o[6]);
-        o[7] = fmaf(w, v1.w, o[7]);
+          for (int i = 0; i < kR; ++i) {
+            if (w[i][c] == 0.f) continue;  // a masked value may be NaN
+            o[i][0] = fmaf(w[i][c], v0.x, o[i][0]);
+            o[i][1] = fmaf(w[i][c], v0.y, o[i][1]);
+            o[i][2] = fmaf(w[i][c], v0.z, o[i][2]);
+            o[i][3] = fmaf(w[i][c], v0.w, o[i][3]);
+            o[i][4] = fmaf(w[i][c], v1.x, o[i][4]);
+            o[i][5] = fmaf(w[i][c], v1.y, o[i][5]);
+            o[i][6] = fmaf(w[i][c], v1.z, o[i][6]);
+            o[i][7] = fmaf(w[i][c], v1.w, o[i][7]);
+          }
+        }
       }
     }
 #pragma unroll
-    for (int d = 1; d < 16; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (cur.whole()) {
-      if (live) {
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
-        float* dst = reinterpret_cast<float*>(a.out) + (int64_t)(it.tok0 + t) * a.out_stride + j * kHeadDim + 8 * c;
-        store4(dst, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-        store4(dst + 4, o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv);
-        if (a.lse && c == 0) a.lse[(int64_t)(it.tok0 + t) * a.c.h_q + j] = kv_lse(m, l);
-      }
-    } else {
-      const size_t row = (size_t)cur.slot() * kRows + r;
+    for (int i = 0; i < kR; ++i) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a.o[row * kHeadDim + 8 * c + e] = o[e];
-      if (c == 0) a.ml[row] = make_float2(m, l);
-      if (tid == 0 && cur.off == 0)
-        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(a, run, cur));
+      for (int d = 1; d < 16; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+      if (cur.whole()) {
+        if (live[i]) {
+          const float inv = l[i] == 0.f ? 0.f : 1.0f / l[i];
+          const int64_t tok = it.tok0 + t[i];
+          float* dst = reinterpret_cast<float*>(a.out) + tok * a.out_stride + (head0 + g[i]) * kHeadDim + 4 * x;
+          store4(dst, o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
+          store4(dst + 64, o[i][4] * inv, o[i][5] * inv, o[i][6] * inv, o[i][7] * inv);
+          if (a.lse && x == 0) a.lse[tok * a.c.h_q + head0 + g[i]] = kv_lse(m[i], l[i]);
+        }
+      } else {
+        const size_t row = (size_t)cur.slot() * kRows + y + 16 * i;
+        store4(a.o + row * kHeadDim + 4 * x, o[i][0], o[i][1], o[i][2], o[i][3]);
+        store4(a.o + row * kHeadDim + 4 * x + 64, o[i][4], o[i][5], o[i][6], o[i][7]);
+        if (x == 0) a.ml[row] = make_float2(m[i], l[i]);
+      }
     }
+    if (tid == 0 && !cur.whole() && cur.off == 0)
+      a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(a, run, cur));
   }
 }
 
@@ -228,11 +272,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const KvAttnArgs a) {
 }  // namespace
 
 cudaError_t kv_simt_setup() {
-  return cudaFuncSetAttribute(attn_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SimtSmem));
+  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SimtSmem<1>));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(attn_simt_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SimtSmem<4>));
 }
 
 cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, unsigned grid, cudaStream_t st) {
-  return launch_kernel(attn_simt_kernel, dim3(grid), dim3(kThreads), sizeof(SimtSmem), st, true, a);
+  return a.rows == 16 ? launch_kernel(attn_simt_kernel<1>, dim3(grid), dim3(kThreads), sizeof(SimtSmem<1>), st, true, a)
+                      : launch_kernel(attn_simt_kernel<4>, dim3(grid), dim3(kThreads), sizeof(SimtSmem<4>), st, true, a);
 }
 
 cudaError_t launch_kv_combine(const KvAttnArgs& a, bool f32, cudaStream_t st) {

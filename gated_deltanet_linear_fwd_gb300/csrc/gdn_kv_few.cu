@@ -15,20 +15,26 @@
 // each weight, relative; a bf16 weight has 2^-9).  The two parts are columns of
 // one product, so no key or value is converted or read twice.
 //
-// Softmax over the keys x_j = scale log2(e) q . k_j, per tile of 128 keys (two
-// pages): thread j of a warpgroup holds key j's column of S^T.  The values'
-// page scale 2^e_v (a power of two) is folded into the exponent: with m_t the
-// tile's maximum of x + e_v, P_j = 2^(x_j + e_v - m_t + 8), so P . V-codes is the
-// tile's output in units of 2^(m_t - 8), and its sum is of P_j 2^-e_v, kept in
-// fp32 from the unrounded P.  Weights count from their own tile's maximum, so
-// what e4m3 cannot hold is below 2^-18 of that, however many keys there are.
-// Tiles are joined in fp32 registers, under the next tile's second product:
-// o <- o 2^(m - m') + O_t 2^(m_t - m'), m' the larger of m and m_t.
+// Softmax over the keys x_j = scale log2(e) q . k_j, by steps of one or two
+// tiles of 128 keys: thread j of a warpgroup holds key j's column of S^T.  The
+// values' page scale 2^e_v (a power of two) is folded into the exponent: with
+// m_t the step's maximum of x + e_v, P_j = 2^(x_j + e_v - m_t + 8), so
+// P . V-codes is the step's output in units of 2^(m_t - 8), and its sum is of
+// P_j 2^-e_v, kept in fp32 from the unrounded P.  Weights count from their own
+// step's maximum, so what e4m3 cannot hold is below 2^-18 of that, however many
+// keys there are.  Steps are joined in fp32 registers, under the next step's
+// second product: o <- o 2^(m - m') + O_t 2^(m_t - m'), m' the larger of m and
+// m_t; the two factors of a row are found by one lane and shared.
 //
-// Roles: warpgroups of four warps with 8 rows each (one with 16 for 16 rows),
-// one TMA warp, one MMA warp.  Two CTAs an SM hide one another's tile latency;
-// 32 rows take one CTA of four warpgroups (two of 16 rows took 2600 cycles a
-// tile, four of 8 rows 1500, against 1400 for the tile's bytes from HBM).
+// Roles: a warpgroup of four warps for every 8 rows, one TMA warp, one MMA warp.
+// Up to 16 rows two CTAs an SM hide one another's latency.  More rows take one
+// CTA with a deeper ring, whose warpgroups issue 40 % of all cycles: there a step of two
+// tiles halves what a step costs a row whatever its keys (the maximum, the
+// join, the waits).  32 sequences of 1000 to 8192 tokens, 8 heads, 20 rows:
+// 60 us (209 MB, 3.5 TB/s), 82 with steps of one tile; with one row tile of 32
+// instead of 24 it is 14 % more.  256 sequences of 32 to 32768 tokens, 2 heads, 4
+// rows: 109 us (629 MB, 5.8 TB/s) with steps of one tile, 119 with two, whose
+// second tile waits longer for HBM than it saves.
 #include <cuda_fp16.h>
 
 #include "gdn_dev.cuh"
@@ -43,32 +49,40 @@ constexpr int kScaleRing = 8;                   // tiles whose page scales are i
 // Details of the bounded waits (100 + barrier), as in the other kernels.
 enum { kBarK = 1, kBarV, kBarKFree, kBarVFree, kBarQ, kBarS, kBarP, kBarO, kBarScale, kBarClean };
 
+constexpr int kRowsWg = 8;                      // query rows of a warpgroup
+
 template <int NR>
 struct Few {
-  static constexpr int kRowsWg = NR == 16 ? 16 : 8;      // rows of a warpgroup
   static constexpr int kWgs = NR / kRowsWg;
   static constexpr int kSoft = kWgs * 128;               // softmax threads
   static constexpr int kThreads = kSoft + 64;
   static constexpr int kN = 2 * NR;                      // columns of the products
-  static constexpr int kStages = NR == 32 ? 5 : 3;
-  static constexpr int kCtasPerSm = NR == 32 ? 1 : 2;
-  static constexpr uint32_t kTmemCols = 4 * kN;          // S and O, two of each
+  static constexpr int kStages = NR > 16 ? 5 : 3;
+  static constexpr int kTiles = NR > 16 ? 2 : 1;         // tiles a step takes together
+  static constexpr int kCtasPerSm = NR > 16 ? 1 : 2;
+  static constexpr uint32_t kColO = 2 * kTiles * kN;     // S of two steps, then O of two
+  static constexpr uint32_t kTmemCols = kTiles == 1 ? (NR == 8 ? 64 : 128) : 512;  // a power of two
   static constexpr uint32_t kOffV = kStages * kTileBytes;
   static constexpr uint32_t kOffQ = 2 * kStages * kTileBytes;
   static constexpr uint32_t kOffP = kOffQ + kN * kHeadDim;
-  static constexpr uint32_t kSmem = kOffP + 2 * kN * kKvTile + 1024;  // + alignment
+  static constexpr uint32_t kPBytes = kN * kKvTile;      // weights of a tile
+  static constexpr uint32_t kSmem = kOffP + 2 * kTiles * kPBytes + 1024;  // + alignment
+  static_assert(kStages > kTiles, "a step's first product runs ahead of the last step's second one");
 };
 
 template <int NR>
 struct FewCtl {
   uint64_t k_full[5], k_free[5], v_full[5], v_free[5];
-  uint64_t q_full, s_full[2], p_full[2], o_full[2], v_clean[2], scale_full[kScaleRing];
-  float scale[kScaleRing][4];  // key scales of the tile's two pages, value scales
-  uint32_t nan_keys[2][4];     // keys of a masked tile whose values hold a NaN code
+  uint64_t q_full, s_full[2], p_full[2], o_full[2], v_clean[4], scale_full[kScaleRing];
+  float4 scale[kScaleRing][2]; // a page's key scale, log2 of its value scale, 1 / value scale
+  uint32_t nan_keys[4][4];     // keys of a masked tile whose values hold a NaN code
   alignas(16) float f[NR];     // score factor of a row: its power of two times scale log2(e)
   int key_lo[NR], key_hi[NR];  // keys a row attends to
-  alignas(16) float top[Few<NR>::kWgs][2][Few<NR>::kRowsWg][4];  // tile maxima of the four warps
-  alignas(16) float sum[Few<NR>::kWgs][Few<NR>::kRowsWg][4];
+  alignas(16) float top[Few<NR>::kWgs][2][kRowsWg][4];  // tile maxima of the four warps
+  alignas(16) float sum[Few<NR>::kWgs][kRowsWg][4];
+  // a warp's copy, by row: what is added to its exponents; the factors of a join
+  alignas(16) float ref[Few<NR>::kSoft / 32][kRowsWg];
+  alignas(16) float alpha[Few<NR>::kSoft / 32][2][kRowsWg], beta[Few<NR>::kSoft / 32][2][kRowsWg];
   KvRunScratch run;
   uint32_t tmem;
   int abort;
@@ -135,11 +149,11 @@ __device__ __forceinline__ void few_load(const KvAttnArgs& a, FewCtl<NR>* ctl, u
           if (p1 >= 0) tma_load_3d(dst + kTileBytes / 2, vmap, &ctl->v_full[stage], 0, 0, p1);
         }
         // last, since the scales' loads follow the page's
-        if ((lane >> 1) == j) {
-          float* s = ctl->scale[i % kScaleRing];
-          s[lane & 1] = my_page >= 0 ? my_sk : 1.f;
-          s[2 + (lane & 1)] = my_page >= 0 ? my_sv : 1.f;
-        }
+        if ((lane >> 1) == j)  // a power of two: its log2 and reciprocal are its bits
+          ctl->scale[i % kScaleRing][lane & 1] =
+              my_page < 0 ? make_float4(1.f, 0.f, 1.f, 0.f)
+                          : make_float4(my_sk, (float)((int)(__float_as_uint(my_sv) >> 23) - 127),
+                                        __int_as_float((254 << 23) - __float_as_int(my_sv)), 0.f);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->scale_full[i % kScaleRing]);
       }
@@ -159,64 +173,72 @@ __device__ __forceinline__ void few_mma(const KvAttnArgs& a, FewCtl<NR>* ctl, ui
   const uint64_t dq = sdesc_sw128(sm + F::kOffQ, 0, 1024);
   const uint64_t dp = sdesc_plain(sm + F::kOffP, 128, 16 * kKvTile);
   const bool issue = elect_one();
-  int i = 0, ks = 0, vs = 0;  // tile of the run; stages of this tile's keys and of the values of the one before
+  int i = 0, ks = 0, vs = 0;  // step of the run; stages of its next keys and of the values of the step before
   uint32_t k_par = 0, v_par = 0, q_par = 0;
-  // O^T of the tile before tile i, once its weights are in shared memory
-  auto second = [&]() {
+  // O^T of the step before step i, of n tiles, once its weights are in shared memory
+  auto second = [&](int n) {
     const int buf = (i - 1) & 1;
-    if (!kv_wait_warp([&] {
-          return kv_wait(&ctl->v_full[vs], v_par, &ctl->abort, 100 + kBarV) &&
-                 kv_wait(&ctl->p_full[buf], ((i - 1) >> 1) & 1, &ctl->abort, 100 + kBarP);
-        }))
-      return false;
-    tc_fence_after();
-    if (issue) {
-      const uint32_t d = tmem + (2 + buf) * F::kN;
-      const uint64_t v = dv + vs * (kTileBytes >> 4), p = dp + buf * (F::kN * kKvTile >> 4);
+    if (!kv_wait_warp([&] { return kv_wait(&ctl->p_full[buf], ((i - 1) >> 1) & 1, &ctl->abort, 100 + kBarP); })) return false;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mma_f8(d, v + k * 256, p + k * 32, kIdO, k > 0);
-      mma_commit(&ctl->o_full[buf]);
-      mma_commit(&ctl->v_free[vs]);
-    }
-    __syncwarp();
-    if (++vs == F::kStages) {
-      vs = 0;
-      v_par ^= 1;
+    for (int h = 0; h < F::kTiles; ++h) {
+      if (h >= n) break;
+      if (!kv_wait_warp([&] { return kv_wait(&ctl->v_full[vs], v_par, &ctl->abort, 100 + kBarV); })) return false;
+      tc_fence_after();
+      if (issue) {
+        const uint32_t d = tmem + F::kColO + buf * F::kN;
+        const uint64_t v = dv + vs * (kTileBytes >> 4), p = dp + (buf * F::kTiles + h) * (F::kPBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_f8(d, v + k * 256, p + k * 32, kIdO, h + k > 0);
+        mma_commit(&ctl->v_free[vs]);
+        if (h == n - 1) mma_commit(&ctl->o_full[buf]);
+      }
+      __syncwarp();
+      if (++vs == F::kStages) {
+        vs = 0;
+        v_par ^= 1;
+      }
     }
     return true;
   };
+  int last = 0;  // tiles of the step before
   KvCursor cur;
 #pragma unroll 1
   for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
     const int tiles = __shfl_sync(0xffffffffu, cur.tiles(), 0);
 #pragma unroll 1
-    for (int j = 0; j < tiles; ++j) {
-      // A new item's queries arrive only after the last tile's softmax: finish that tile first.
+    for (int j = 0; j < tiles; j += F::kTiles) {
+      // A new item's queries arrive only after the last step's softmax: finish that step first.
       if (j == 0) {
-        if (i > 0 && !second()) return;
+        if (i > 0 && !second(last)) return;
         if (!kv_wait_warp([&] { return kv_wait(&ctl->q_full, q_par, &ctl->abort, 100 + kBarQ); })) return;
         q_par ^= 1;
       }
-      if (!kv_wait_warp([&] { return kv_wait(&ctl->k_full[ks], k_par, &ctl->abort, 100 + kBarK); })) return;
-      tc_fence_after();
-      if (issue) {
-        const uint32_t d = tmem + (i & 1) * F::kN;
-        const uint64_t kk = dk + ks * (kTileBytes >> 4);
+      const int n = min(F::kTiles, tiles - j);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_f8(d, kk + k * 2, dq + k * 2, kIdS, k > 0);
-        mma_commit(&ctl->s_full[i & 1]);
-        mma_commit(&ctl->k_free[ks]);
+      for (int h = 0; h < F::kTiles; ++h) {
+        if (h >= n) break;
+        if (!kv_wait_warp([&] { return kv_wait(&ctl->k_full[ks], k_par, &ctl->abort, 100 + kBarK); })) return;
+        tc_fence_after();
+        if (issue) {
+          const uint32_t d = tmem + ((i & 1) * F::kTiles + h) * F::kN;
+          const uint64_t kk = dk + ks * (kTileBytes >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_f8(d, kk + k * 2, dq + k * 2, kIdS, k > 0);
+          if (h == n - 1) mma_commit(&ctl->s_full[i & 1]);
+          mma_commit(&ctl->k_free[ks]);
+        }
+        __syncwarp();
+        if (++ks == F::kStages) {
+          ks = 0;
+          k_par ^= 1;
+        }
       }
-      __syncwarp();
-      if (++ks == F::kStages) {
-        ks = 0;
-        k_par ^= 1;
-      }
-      if (j > 0 && !second()) return;
+      if (j > 0 && !second(last)) return;
+      last = n;
       ++i;
     }
   }
-  if (i > 0) second();
+  if (i > 0) second(last);
 }
 
 // ---------------------------------------------------------------- softmax warpgroups
@@ -231,19 +253,49 @@ __device__ __forceinline__ float warp_max(float x) {
   return m;
 }
 
+// Two fp32 products and sums in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 bits2(const uint32_t* r) { return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1])); }
+
 constexpr float kNegInf = -__builtin_huge_valf();
 
 template <int NR>
 __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl, uint8_t* sm,
                                             uint32_t tmem) {
   using F = Few<NR>;
-  constexpr int R = F::kRowsWg;
+  constexpr int R = kRowsWg;
   const int wg = threadIdx.x >> 7, tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
   const int row0 = wg * R;
+  constexpr int T = F::kTiles;
   const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16) + wg * 2 * R;
   const int bar = 1 + wg;
   bool bad = false;
-  int i = 0, cleaned = 0;  // tiles of the run, and the masked ones among them
+  int i = 0, tile = 0, cleaned = 0;  // steps and tiles of the run, and the masked tiles among them
+  const int w = threadIdx.x >> 5;
   KvCursor cur;
 #pragma unroll 1
   for (cur.start(a, ctl->run.run); cur.valid(); cur.next(a)) {
@@ -304,162 +356,190 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
     const int t0 = cur.rt * NR / a.group, t1 = min(it.n - 1, (cur.rt * NR + NR - 1) / a.group);
     const int all_lo = a.window > 0 ? past + t1 - a.window + 1 : 0, all_hi = a.causal ? min(past + t0 + 1, it.len) : it.len;
     const bool dead = cur.rt * NR + row0 >= it.n * a.group;  // no row of this warpgroup: its columns may hold anything
-    float m[R], l[R], o[R];        // up to the tile before last
-    float top[R], sum[R];          // the last tile's maximum and this key's part of its sum
+    float m = kNegInf;  // running maximum of row lane % R
+    // by pairs of rows: this key's part of the sums; column tid of the output, up to the step before last
+    float2 l[R / 2], o[R / 2];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      m[r] = top[r] = kNegInf;
-      l[r] = o[r] = sum[r] = 0.f;
-    }
-    // O^T of the last tile, in units of 2^(its maximum - 8), joins the rest
+    for (int r = 0; r < R / 2; ++r) l[r] = o[r] = both(0.f);
+    // O^T of step t, in units of 2^(its maximum - 8), joins the rest
     auto join = [&](int t) {
       bad |= !kv_wait_warp([&] { return kv_wait(&ctl->o_full[t & 1], (t >> 1) & 1, &ctl->abort, 100 + kBarO); });
       if (bad) return;
       tc_fence_after();
-      uint32_t h[16], q[16];
-      tmem_ld16(t_lane + (2 + (t & 1)) * F::kN, h);
-      if (R == 16) {
-        tmem_ld16(t_lane + (2 + (t & 1)) * F::kN + 16, q);
-        tmem_ld_wait(h, q);
-      } else {
-        tmem_ld_wait(h);
-      }
+      uint32_t h[16];
+      tmem_ld16(t_lane + F::kColO + (t & 1) * F::kN, h);
+      tmem_ld_wait(h);
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float w = fmaxf(m[r], top[r]), ref = w == kNegInf ? 0.f : w;
-        const float alpha = ex2(m[r] - ref), beta = ex2(top[r] - ref);
-        m[r] = w;
-        l[r] = fmaf(l[r], alpha, sum[r] * beta);
-        o[r] = fmaf(o[r], alpha, (__uint_as_float(h[r]) + __uint_as_float(R == 16 ? q[r] : h[8 + r])) * beta);
+      for (int r = 0; r < R / 2; ++r) {
+        const float2 alpha = *reinterpret_cast<const float2*>(&ctl->alpha[w][t & 1][2 * r]);
+        const float2 beta = *reinterpret_cast<const float2*>(&ctl->beta[w][t & 1][2 * r]);
+        const float2 now = add2(bits2(h + 2 * r), bits2(h + R + 2 * r));
+        o[r] = fma2(o[r], alpha, mul2(now, beta));
       }
     };
 #pragma unroll 1
-    for (int j = 0; j < tiles; ++j, ++i) {
-      const int buf = i & 1, key0 = (cur.tile_begin() + j) * kKvTile, key = key0 + tid;
-      const int stage = i % F::kStages;
-      const bool masked = key0 < all_lo || key0 + kKvTile > all_hi;
-      if (masked) {
+    for (int j = 0; j < tiles; j += T, ++i) {
+      const int buf = i & 1, n = min(T, tiles - j), key0 = (cur.tile_begin() + j) * kKvTile;
+      bool masked[T];
+      int slot[T];
+#pragma unroll
+      for (int h = 0; h < T; ++h) {
+        const int k0 = key0 + h * kKvTile, key = k0 + tid;
+        masked[h] = h < n && (k0 < all_lo || k0 + kKvTile > all_hi);
+        slot[h] = cleaned & 3;
+        if (!masked[h]) continue;
         // Values no row may use must not meet a zero weight as NaN: the first
         // warpgroup makes zeros of a key row past the sequence, or with a NaN
         // code, before any product; in the second case the rows that do
         // attend to it become NaN.
         if (wg == 0) {
-          bad |= !kv_wait_warp([&] { return kv_wait(&ctl->v_full[stage], (i / F::kStages) & 1, &ctl->abort, 100 + kBarV); });
+          const int at = tile + h, stage = at % F::kStages;
+          bad |= !kv_wait_warp([&] { return kv_wait(&ctl->v_full[stage], (at / F::kStages) & 1, &ctl->abort, 100 + kBarV); });
           uint8_t* v = sm + F::kOffV + stage * kTileBytes + tid * kHeadDim;
           uint32_t carry = 0;
           if (!bad && key < it.len) {
-#pragma unroll
+            // each lane of eight from another chunk: no bank conflicts
+#pragma unroll 2
             for (int e = 0; e < 8; ++e) {  // b & 0x7f = 0x7f: adding 1 to the low seven bits carries into the eighth
-              const uint4 w = reinterpret_cast<const uint4*>(v)[e];
-              carry |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
-                       ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
+              const uint4 c = reinterpret_cast<const uint4*>(v)[(e + lane) & 7];
+              carry |= ((c.x & 0x7f7f7f7fu) + 0x01010101u) | ((c.y & 0x7f7f7f7fu) + 0x01010101u) |
+                       ((c.z & 0x7f7f7f7fu) + 0x01010101u) | ((c.w & 0x7f7f7f7fu) + 0x01010101u);
             }
           }
           const bool nan = (carry & 0x80808080u) != 0;
           const uint32_t word = __ballot_sync(0xffffffffu, nan);
-          if (lane == 0) ctl->nan_keys[cleaned & 1][warp] = word;
+          if (lane == 0) ctl->nan_keys[slot[h]][warp] = word;
           if (!bad && (nan || key >= it.len)) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) reinterpret_cast<uint4*>(v)[e] = make_uint4(0, 0, 0, 0);
+#pragma unroll 2
+            for (int e = 0; e < 8; ++e) reinterpret_cast<uint4*>(v)[(e + lane) & 7] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
-          kv_arrive_warp(&ctl->v_clean[cleaned & 1]);
+          kv_arrive_warp(&ctl->v_clean[slot[h]]);
         }
-        if (!dead) bad |= !kv_wait_warp([&] { return kv_wait(&ctl->v_clean[cleaned & 1], (cleaned >> 1) & 1, &ctl->abort, 100 + kBarClean); });
+        if (!dead) bad |= !kv_wait_warp([&] { return kv_wait(&ctl->v_clean[slot[h]], (cleaned >> 2) & 1, &ctl->abort, 100 + kBarClean); });
         ++cleaned;
       }
-      float x[R];
-      float inv_sv = 1.f;
       bad |= !kv_wait_warp([&] {
-        return kv_wait(&ctl->scale_full[i % kScaleRing], (i / kScaleRing) & 1, &ctl->abort, 100 + kBarScale) &&
-               kv_wait(&ctl->s_full[buf], (i >> 1) & 1, &ctl->abort, 100 + kBarS);
+        for (int h = 0; h < n; ++h)
+          if (!kv_wait(&ctl->scale_full[(tile + h) % kScaleRing], ((tile + h) / kScaleRing) & 1, &ctl->abort, 100 + kBarScale))
+            return false;
+        return kv_wait(&ctl->s_full[buf], (i >> 1) & 1, &ctl->abort, 100 + kBarS);
       });
       if (dead) {
-        if (bad) return;
+        if (bad) break;
         kv_arrive_warp(&ctl->p_full[buf]);
+        tile += n;
         continue;
       }
+      float x[T][R], inv_sv[T];
       if (!bad) {
         tc_fence_after();
-        uint32_t hi[16], lo[16];
-        tmem_ld16(t_lane + buf * F::kN, hi);
-        if (R == 16) tmem_ld16(t_lane + buf * F::kN + 16, lo);
-        const float* sc = ctl->scale[i % kScaleRing];
-        const float sk = sc[warp >> 1], sv = sc[2 + (warp >> 1)];
-        const float ev = (float)((int)(__float_as_uint(sv) >> 23) - 127);  // log2 of a power of two
-        inv_sv = __int_as_float((254 << 23) - __float_as_int(sv));
-        if (R == 16)
-          tmem_ld_wait(hi, lo);
-        else
-          tmem_ld_wait(hi);
-#pragma unroll
-        for (int r = 0; r < R; r += 4) {
-          const float4 f4 = *reinterpret_cast<const float4*>(ctl->f + row0 + r);
-          const float f[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float s = fmaf(__uint_as_float(R == 16 ? lo[r + e] : hi[(8 + r + e) & 15]), 0.0625f, __uint_as_float(hi[r + e]));
-            x[r + e] = fmaf(s, f[e] * sk, ev);
-          }
+        // a tile's columns of this warpgroup: R of hi, R of lo; of a tile that is not there, whatever they held
+        uint32_t s[2][16];
+        tmem_ld16(t_lane + buf * T * F::kN, s[0]);
+        if (T == 2) {
+          tmem_ld16(t_lane + buf * T * F::kN + F::kN, s[1]);
+          tmem_ld_wait(s[0], s[1]);
+        } else {
+          tmem_ld_wait(s[0]);
         }
-        if (masked) {
-          const bool nan = (ctl->nan_keys[(cleaned - 1) & 1][warp] >> lane) & 1;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const bool in = key >= ctl->key_lo[row0 + r] && key < ctl->key_hi[row0 + r];
-            x[r] = in ? (nan ? __int_as_float(0x7fffffff) : x[r]) : kNegInf;
+        for (int h = 0; h < T; ++h) {
+          const float4 sc = ctl->scale[(tile + min(h, n - 1)) % kScaleRing][warp >> 1];  // key scale, log2 of the value scale, its inverse
+          inv_sv[h] = sc.z;
+#pragma unroll
+          for (int r = 0; r < R; r += 2) {
+            const float2 f = mul2(*reinterpret_cast<const float2*>(ctl->f + row0 + r), both(sc.x));
+            const float2 y = fma2(bits2(s[h] + R + r), both(0.0625f), bits2(s[h] + r));
+            const float2 z = fma2(y, f, both(sc.y));
+            x[h][r] = z.x;
+            x[h][r + 1] = z.y;
+          }
+          if (masked[h]) {
+            const int key = key0 + h * kKvTile + tid;
+            const bool nan = (ctl->nan_keys[slot[h]][warp] >> lane) & 1;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              const bool in = key >= ctl->key_lo[row0 + r] && key < ctl->key_hi[row0 + r];
+              x[h][r] = in ? (nan ? __int_as_float(0x7fffffff) : x[h][r]) : kNegInf;
+            }
+          }
+          if (h >= n) {
+            inv_sv[h] = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) x[h][r] = kNegInf;
           }
         }
         float mine = kNegInf;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const float w = warp_max(x[r]);
-          if (lane == r) mine = w;
+          const float c = warp_max(T == 2 ? fmaxf(x[0][r], x[T - 1][r]) : x[0][r]);
+          if (lane == r) mine = c;
         }
         if (lane < R) ctl->top[wg][buf][lane][warp] = mine;
       }
       bad = named_bar_or(bar, 128, bad);
       if (bad) return;
-      float now[R];
+      // lane: its row's factors for this step's join
+      {
+        const float4 c = *reinterpret_cast<const float4*>(ctl->top[wg][buf][lane % R]);
+        const float top = fmaxf(fmaxf(c.x, c.y), fmaxf(c.z, c.w));
+        const float both = fmaxf(m, top), at = both == kNegInf ? 0.f : both;
+        if (lane < R) {
+          ctl->ref[w][lane] = 8.f - (top == kNegInf ? 0.f : top);
+          ctl->alpha[w][buf][lane] = ex2(m - at);
+          ctl->beta[w][buf][lane] = ex2(top - at);
+        }
+        m = both;
+        __syncwarp();
+      }
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float4 w = *reinterpret_cast<const float4*>(ctl->top[wg][buf][r]);
-        now[r] = fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w));
-        x[r] = ex2(x[r] - (now[r] == kNegInf ? 0.f : now[r]) + 8.f);
+      for (int r = 0; r < R; r += 2) {
+        const float2 ref = *reinterpret_cast<const float2*>(&ctl->ref[w][r]);
+#pragma unroll
+        for (int h = 0; h < T; ++h) {
+          const float2 z = add2(make_float2(x[h][r], x[h][r + 1]), ref);
+          x[h][r] = ex2(z.x);
+          x[h][r + 1] = ex2(z.y);
+        }
       }
       // P^T, 16 columns of bytes a key: hi, then lo
-      uint8_t* p = sm + F::kOffP + buf * (F::kN * kKvTile) + (wg * (2 * R / 16)) * (16 * kKvTile) + tid * 16;
-      uint32_t hi[R / 2], lo[R / 2];
 #pragma unroll
-      for (int r = 0; r < R / 2; ++r) split_e4m3(x[2 * r], x[2 * r + 1], hi[r], lo[r]);
-      if (R == 8) {
+      for (int h = 0; h < T; ++h) {
+        if (h >= n) break;
+        uint8_t* p = sm + F::kOffP + (buf * T + h) * F::kPBytes + wg * (16 * kKvTile) + tid * 16;
+        uint32_t hi[R / 2], lo[R / 2];
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r) split_e4m3(x[h][2 * r], x[h][2 * r + 1], hi[r], lo[r]);
         *reinterpret_cast<uint4*>(p) = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      } else {
-        *reinterpret_cast<uint4*>(p) = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[R / 2 - 4] | hi[R / 2 - 3] << 16,
-                                                  hi[R / 2 - 2] | hi[R / 2 - 1] << 16);
-        *reinterpret_cast<uint4*>(p + 16 * kKvTile) = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16,
-                                                                 lo[R / 2 - 4] | lo[R / 2 - 3] << 16,
-                                                                 lo[R / 2 - 2] | lo[R / 2 - 1] << 16);
       }
       fence_proxy_async_smem();
       tc_fence_before();
       kv_arrive_warp(&ctl->p_full[buf]);
-      // under this tile's second product, the tile before
-      if (j > 0) join(i - 1);
+      // under this step's second product: the sums, and the output of the step before
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        top[r] = now[r];
-        sum[r] = x[r] * inv_sv;
+      for (int r = 0; r < R; r += 2) {
+        const float2 alpha = *reinterpret_cast<const float2*>(&ctl->alpha[w][buf][r]);
+        const float2 beta = *reinterpret_cast<const float2*>(&ctl->beta[w][buf][r]);
+        float2 sum = mul2(make_float2(x[0][r], x[0][r + 1]), both(inv_sv[0]));
+        if (T == 2) sum = fma2(make_float2(x[T - 1][r], x[T - 1][r + 1]), both(inv_sv[T - 1]), sum);
+        l[r / 2] = fma2(l[r / 2], alpha, mul2(sum, beta));
       }
+      if (j > 0) join(i - 1);
+      tile += n;
     }
-    if (dead) continue;
+    if (dead) {
+      if (tiles > 0) bad = named_bar_or(bar, 128, bad);
+      if (bad) return;
+      continue;
+    }
     if (tiles > 0) {
       join(i - 1);
       tc_fence_before();
       if (!bad) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          float s = l[r];
+          float s = r & 1 ? l[r / 2].y : l[r / 2].x;
 #pragma unroll
           for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
           if (lane == 0) ctl->sum[wg][r][warp] = s;
@@ -469,11 +549,12 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
       if (bad) return;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float4 w = *reinterpret_cast<const float4*>(ctl->sum[wg][r]);
-        l[r] = (w.x + w.y) + (w.z + w.w);
+        const float4 c = *reinterpret_cast<const float4*>(ctl->sum[wg][r]);
+        (r & 1 ? l[r / 2].y : l[r / 2].x) = (c.x + c.y) + (c.z + c.w);
       }
     }
     // ---- thread d writes column d of each row ----
+    auto row = [](const float2* v, int r) { return r & 1 ? v[r / 2].y : v[r / 2].x; };
     if (cur.whole()) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -481,16 +562,16 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
         if (t < it.n && g < group) {
           const int64_t tok = it.tok0 + t;
           reinterpret_cast<__nv_bfloat16*>(a.out)[tok * a.out_stride + (head0 + g) * kHeadDim + tid] =
-              __float2bfloat16_rn(l[r] == 0.f ? 0.f : o[r] / l[r]);
-          if (a.lse && tid == r) a.lse[tok * a.c.h_q + head0 + g] = kv_lse(m[r] - 8.f, l[r]);
+              __float2bfloat16_rn(row(l, r) == 0.f ? 0.f : row(o, r) / row(l, r));
+          if (a.lse && tid == r) a.lse[tok * a.c.h_q + head0 + g] = kv_lse(m - 8.f, row(l, r));
         }
       }
     } else {
-      const size_t row = (size_t)cur.slot() * NR + row0;
+      const size_t at = (size_t)cur.slot() * NR + row0;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        a.o[(row + r) * kHeadDim + tid] = o[r];
-        if (tid == r) a.ml[row + r] = make_float2(m[r] - 8.f, l[r]);
+        a.o[(at + r) * kHeadDim + tid] = row(o, r);
+        if (tid == r) a.ml[at + r] = make_float2(m - 8.f, row(l, r));
       }
       if (threadIdx.x == 0 && cur.off == 0)
         a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(a, ctl->run.run, cur));
@@ -516,8 +597,7 @@ __global__ void __launch_bounds__(Few<NR>::kThreads, Few<NR>::kCtasPerSm)
       mbar_init(&ctl.v_free[s], 1);
     }
     mbar_init(&ctl.q_full, F::kSoft / 32);
-    mbar_init(&ctl.v_clean[0], 4);
-    mbar_init(&ctl.v_clean[1], 4);
+    for (int b = 0; b < 4; ++b) mbar_init(&ctl.v_clean[b], 4);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl.s_full[b], 1);
       mbar_init(&ctl.p_full[b], F::kSoft / 32);
@@ -574,12 +654,13 @@ cudaError_t launch(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorM
 
 }  // namespace
 
-int kv_few_ctas_per_sm(int rows) { return rows == 32 ? Few<32>::kCtasPerSm : Few<16>::kCtasPerSm; }
+int kv_few_ctas_per_sm(int rows) { return rows > 16 ? Few<32>::kCtasPerSm : Few<16>::kCtasPerSm; }
 
 cudaError_t kv_few_setup() {
   cudaError_t e;
   if ((e = cudaFuncSetAttribute(attn_few_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<8>::kSmem)) != cudaSuccess) return e;
   if ((e = cudaFuncSetAttribute(attn_few_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<16>::kSmem)) != cudaSuccess) return e;
+  if ((e = cudaFuncSetAttribute(attn_few_kernel<24>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<24>::kSmem)) != cudaSuccess) return e;
   return cudaFuncSetAttribute(attn_few_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<32>::kSmem);
 }
 
@@ -588,6 +669,7 @@ cudaError_t launch_kv_attn_few(const KvAttnArgs& a, const CUtensorMap& kmap, con
   switch (a.rows) {
     case 8: return launch<8>(a, kmap, vmap, grid, st);
     case 16: return launch<16>(a, kmap, vmap, grid, st);
+    case 24: return launch<24>(a, kmap, vmap, grid, st);
     default: return launch<32>(a, kmap, vmap, grid, st);
   }
 }

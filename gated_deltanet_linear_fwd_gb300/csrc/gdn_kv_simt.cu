@@ -287,9 +287,7 @@ cudaError_t launch_kv_combine(const KvAttnArgs& a, bool f32, cudaStream_t st) {
   // warps a row, since there the parts are what there is to spread.
   const int y = a.rows <= 16 ? 4 : (a.rows + 7) / 8;
   const dim3 grid(a.n_ctas, y), block(256);
-  if (a.rows <= 8)
-    return f32 ? launch_kernel(combine_kernel<float, 4>, grid, block, 0, st, true, a)
-               : launch_kernel(combine_kernel<__nv_bfloat16, 4>, grid, block, 0, st, true, a);
+  if (a.rows <= 8) return launch_kernel(combine_kernel<__nv_bfloat16, 4>, grid, block, 0, st, true, a);  // bf16 only
   if (a.rows <= 16)
     return f32 ? launch_kernel(combine_kernel<float, 2>, grid, block, 0, st, true, a)
                : launch_kernel(combine_kernel<__nv_bfloat16, 2>, grid, block, 0, st, true, a);

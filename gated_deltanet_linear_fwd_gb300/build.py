@@ -11,7 +11,7 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = ["gdn_api.cu", "gdn_wy.cu", "gdn_scan.cu", "gdn_combine.cu", "gdn_f32.cu", "gdn_decode.cu", "gdn_bwd.cu",
-           "gdn_kv.cu", "gdn_kv_simt.cu", "gdn_kv_few.cu", "gdn_kv_many.cu"]
+           "gdn_kv.cu", "gdn_kv_combine.cu", "gdn_kv_f32.cu", "gdn_kv_few.cu", "gdn_kv_many.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-ffp-contract=off",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]

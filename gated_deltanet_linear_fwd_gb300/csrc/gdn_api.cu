@@ -85,7 +85,7 @@ gdn_status device_setup(int* dev_out) {
   if ((e = combine_kernel_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = f32_kernel_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = bwd_kernel_setup()) != cudaSuccess) return cuda_fail(e);
-  if ((e = kv_simt_setup()) != cudaSuccess) return cuda_fail(e);
+  if ((e = kv_f32_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = kv_few_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = kv_many_setup()) != cudaSuccess) return cuda_fail(e);
   int sms = 0;
@@ -380,13 +380,13 @@ gdn_status encode_kv_map(CUtensorMap* m, void* base, const gdn_kv_cache* c) {
 }
 
 // Kernels of gdn_kv_attn.
-constexpr int kKvPathSimt = 0;  // fp32 on the CUDA cores
+constexpr int kKvPathF32 = 0;   // fp32
 constexpr int kKvPathFew = 1;   // bf16, up to 32 rows (tokens times heads of a group) per (sequence, key/value head)
 constexpr int kKvPathMany = 2;  // bf16, more rows
 // What parts and the second kernel cost, in key tiles: about 38 us at 1.35 us a
 // tile of 256 rows on the tensor cores, 6 us at 0.7 us a tile of few rows, 6 us
-// at 5 to 10 us a tile on the CUDA cores.
-constexpr int kKvJoinTilesMany = 28, kKvJoinTilesFew = 8, kKvJoinTilesSimt = 1;
+// at 2 us a tile of an fp32 call.
+constexpr int kKvJoinTilesMany = 28, kKvJoinTilesFew = 8, kKvJoinTilesF32 = 3;
 
 }  // namespace
 
@@ -859,15 +859,13 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   const int group = (d->h_q + h_kv - 1) / h_kv;
   if ((int64_t)d->T * group > 0x7fffffff - 4096) return GDN_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)max_q_len * group;
-  // Kernel and row tile by the rows that share a key.  Measured on 64
-  // sequences with 4 key/value heads: fp32, lengths to 8192, 8 rows 598 us in
-  // tiles of 16 and 896 in one of 64 (which reads a third of the shared memory
-  // a row), 32 rows 1300 and 904; bf16, lengths to 32768, 32 rows 221 us on the
-  // kernel for few rows and 535 on the other, 48 rows 408 (two tiles) and 331.
-  p.path = kKvPathSimt;
-  p.rows = rows <= 16 ? 16 : 64;
-  p.item_cost = 1;
-  int per_sm = 2;
+  // bf16: kernel and row tile by the rows that share a key.  Measured on 64
+  // sequences to 32768 tokens with 4 key/value heads: 32 rows 221 us on the kernel
+  // for few rows and 535 on the other, 48 rows 408 (two tiles) and 331.
+  p.path = kKvPathF32;
+  p.rows = 128;
+  p.item_cost = 2;
+  int per_sm = 1;
   if (d->dtype == GDN_BF16 && rows <= 32) {
     p.path = kKvPathFew;
     p.rows = std::max<int>(8, (int)(rows + 7) / 8 * 8);
@@ -879,7 +877,6 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
     p.path = kKvPathMany;
     p.rows = 256;
     p.item_cost = 6;
-    per_sm = 1;
   }
   p.max_row_tiles = std::max<int>(1, (int)(((int64_t)max_q_len * group + p.rows - 1) / p.rows));
   const int64_t items = (int64_t)d->n_seqs * p.max_row_tiles * h_kv;
@@ -911,7 +908,7 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   total *= (int64_t)d->n_seqs * h_kv;
   const int64_t whole = longest_item == shortest ? (items + slots - 1) / slots * longest_item
                                                  : std::max(longest_item, (total + slots - 1) / slots + shortest);
-  const int64_t runs = (total + slots - 1) / slots + (p.path == kKvPathMany ? kKvJoinTilesMany : p.path == kKvPathFew ? kKvJoinTilesFew : kKvJoinTilesSimt);
+  const int64_t runs = (total + slots - 1) / slots + (p.path == kKvPathMany ? kKvJoinTilesMany : p.path == kKvPathFew ? kKvJoinTilesFew : kKvJoinTilesF32);
   p.n_ctas = whole <= runs ? 0 : (int)std::min<int64_t>(slots, total);
   p.n_seqs = d->n_seqs;
   p.T = d->T;
@@ -932,7 +929,7 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
                        const gdn_kv_plan_t* plan, void* workspace, size_t workspace_bytes, void* stream) {
   gdn_status st = check_kv(d, cache, lens, table, cu);
   if (st != GDN_OK) return st;
-  if (!plan || plan->path < kKvPathSimt || plan->path > kKvPathMany || plan->n_seqs != d->n_seqs || plan->T != d->T || plan->h_q != d->h_q || plan->h_kv != cache->h_kv ||
+  if (!plan || plan->path < kKvPathF32 || plan->path > kKvPathMany || plan->n_seqs != d->n_seqs || plan->T != d->T || plan->h_q != d->h_q || plan->h_kv != cache->h_kv ||
       plan->dtype != d->dtype)
     return GDN_ERR_INVALID_ARG;
   if (d->causal != 0 && d->causal != 1) return GDN_ERR_UNSUPPORTED;
@@ -959,6 +956,7 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
   a.scale_log2 = (d->scale != 0.f ? d->scale : 1.0f / std::sqrt((float)kHeadDim)) * 1.44269504088896341f;
   a.group = (d->h_q + cache->h_kv - 1) / cache->h_kv;
   a.rows = plan->rows;
+  a.max_rows = plan->max_q_len * a.group;
   a.max_row_tiles = plan->max_row_tiles;
   a.n_ctas = plan->n_ctas;
   a.item_cost = plan->item_cost;
@@ -972,13 +970,13 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
   LaunchLog log;
   cudaError_t e = log.before(cs);
   if (e == cudaSuccess) {
-    if (plan->path != kKvPathSimt) {
+    if (plan->path != kKvPathF32) {
       CUtensorMap km, vm;
       if ((st = encode_kv_map(&km, cache->k, cache)) != GDN_OK) return st;
       if ((st = encode_kv_map(&vm, cache->v, cache)) != GDN_OK) return st;
       e = plan->path == kKvPathFew ? launch_kv_attn_few(a, km, vm, grid, cs) : launch_kv_attn_many(a, km, vm, grid, cs);
     } else {
-      e = launch_kv_attn_simt(a, grid, cs);
+      e = launch_kv_attn_f32(a, grid, cs);
     }
   }
   if (e == cudaSuccess) e = log.after("kv_attn", cs);

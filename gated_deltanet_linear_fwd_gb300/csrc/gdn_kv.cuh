@@ -51,6 +51,7 @@ struct KvAttnArgs {
   float scale_log2;        // score scale times log2(e)
   int group;               // query heads per key/value head, rounded up
   int rows, max_row_tiles; // rows of a row tile; row tiles per (sequence, head)
+  int max_rows;            // rows of the longest sequence the plan allows
   int n_ctas;              // 0: CTA i takes item i whole
   int item_cost;           // what beginning and ending an item costs, in key tiles
   int4* desc;              // [n_ctas] item whose first part this CTA made: {sequence, row tile, head, last CTA}
@@ -151,7 +152,7 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs& a, int seq, int rt) 
   it.len = s.len;
   it.first_tile = 0;
   const int r0 = rt * a.rows, rows = s.n * a.group;
-  if (rows > a.max_row_tiles * a.rows) report(a.c.status, kDevCheck, kDetKvLengths);  // more tokens than the plan's bound
+  if (rows > a.max_rows) report(a.c.status, kDevCheck, kDetKvLengths);
   if (r0 >= rows) {
     it.tiles = -1;
     return it;
@@ -384,9 +385,9 @@ __device__ __forceinline__ int e4m3_scale_exp(uint32_t a_bits, int least) {
 // ---- launchers ----
 cudaError_t launch_kv_append(const KvAppendArgs& a, bool f32, unsigned entries, cudaStream_t st);
 cudaError_t launch_kv_read(const KvAppendArgs& a, bool f32, unsigned entries, cudaStream_t st);
-cudaError_t launch_kv_attn_simt(const KvAttnArgs& a, unsigned grid, cudaStream_t st);  // fp32 q and out; 16 or 64 rows
+cudaError_t launch_kv_attn_f32(const KvAttnArgs& a, unsigned grid, cudaStream_t st);  // fp32 q and out
 cudaError_t launch_kv_combine(const KvAttnArgs& a, bool f32, cudaStream_t st);
-cudaError_t kv_simt_setup();
+cudaError_t kv_f32_setup();
 // rows: 8, 16 or 32 (KvAttnArgs::rows); kmap, vmap: the pools as [page and head][64][128 bytes]
 cudaError_t launch_kv_attn_few(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, unsigned grid,
                                cudaStream_t st);

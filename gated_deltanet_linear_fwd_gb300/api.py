@@ -342,6 +342,14 @@ def _raw_stream(stream, t: torch.Tensor) -> int:
     return (torch.cuda.current_stream(t.device.index) if stream is None else stream).cuda_stream
 
 
+def _kv_empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """Memory of the stream the kernels run on, so that its reuse is ordered with them."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def gdn_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor,
                   cu_seqlens: Optional[torch.Tensor] = None, *, stream=None) -> None:
     """Quantises new tokens into the cache (gdn_kv_append): k, v [T, h_kv, 128]
@@ -372,8 +380,8 @@ def gdn_kv_read(cache: KVCache, kv_lens: torch.Tensor, page_table: torch.Tensor,
         if T is None:
             raise ValueError("gdn_kv_read needs T or both outputs")
         shape = (T, h_kv, 128)
-        k_out = torch.empty(shape, dtype=dtype, device=cache.k.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=dtype, device=cache.k.device) if v_out is None else v_out
+        k_out = _kv_empty(shape, dtype, cache.k.device, stream) if k_out is None else k_out
+        v_out = _kv_empty(shape, dtype, cache.k.device, stream) if v_out is None else v_out
     ks, vs = _kv_rows("k_out", k_out, h_kv), _kv_rows("v_out", v_out, h_kv)
     if v_out.dtype != k_out.dtype or v_out.shape != k_out.shape or k_out.shape[2] != 128:
         raise ValueError("k_out and v_out must be alike, with 128 elements a head")
@@ -430,16 +438,16 @@ def gdn_kv_attn(q: torch.Tensor, cache: KVCache, kv_lens: torch.Tensor, page_tab
                                 max_q_len=max_q_len or (T // n if cu is None else T), max_kv_len=max_kv_len,
                                 max_pages=max_pages, dtype=q.dtype, causal=causal, window=window, scale=scale)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _kv_empty(q.shape, q.dtype, q.device, stream)
     elif out.dtype != q.dtype or out.shape != q.shape:
         raise ValueError("out must be like q")
     if lse is None:
         if return_lse:
-            lse = torch.empty(T, h_q, dtype=torch.float32, device=q.device)
+            lse = _kv_empty((T, h_q), torch.float32, q.device, stream)
     elif lse.dtype != torch.float32 or lse.shape != (T, h_q) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [T, h_q]")
     if workspace is None:
-        workspace = torch.empty(max(plan.workspace_bytes, 256), dtype=torch.uint8, device=q.device)
+        workspace = _kv_empty(max(plan.workspace_bytes, 256), torch.uint8, q.device, stream)
     dims = L.gdn_kv_dims(n, T, h_q, max_pages, int(plan.causal), plan.window, plan.scale, _DT.get(q.dtype, -1), qs, 0, 0,
                          _kv_rows("out", out, h_q))
     st = L.load().gdn_kv_attn(q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), cu, cache.raw, out.data_ptr(),

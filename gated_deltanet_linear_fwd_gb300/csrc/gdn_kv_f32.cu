@@ -8,7 +8,10 @@
 //     rounded one and the rounded rest, exact to 2^-24 of each element (to
 //     2^-39 of the row's largest).
 //   O [128 rows, 128 d] = P V, the weights P <= 2^14 split the same way.
-// That is twice the products of a bf16 call.  Prompts over themselves, 8 query
+// The low parts come first: the tensor cores' sums lose a little at every step,
+// in proportion to what is in them (2000 to 4000 keys, unit queries: relative error
+// 4e-7 against 64 bits, 1.1e-6 with the high parts first, 1.2e-6 for fp32 products
+// and softmax).  That is twice the products of a bf16 call.  Prompts over themselves, 8 query
 // heads on 2: 16384 tokens 1675 us (328 TFLOP/s), 2048 tokens 57 us; as fp32 FMAs on
 // the CUDA cores 2048 tokens took 278 us.  64 sequences of 1024 to 8192 tokens, 4
 // heads: 229 us for 8 rows (1.15 TB/s of codes; 598 with FMAs), 242 for 64.
@@ -239,15 +242,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const __grid_cons
       auto issue_s = [&](int j) {
         const uint64_t k = dk + (j & 1) * (2 * kPanel >> 4);
 #pragma unroll
-        for (int s = 0; s < 16; ++s)  // part, panel, 16 columns
-          mma_bf16(tmem + kColS, dq + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, k + ((s >> 2) & 1) * (kPanel >> 4) + (s & 3) * 2,
+        for (int s = 0; s < 16; ++s)  // part (low first), panel, 16 columns
+          mma_bf16(tmem + kColS, dq + ((s >> 2) ^ 2) * (kPanel >> 4) + (s & 3) * 2, k + ((s >> 2) & 1) * (kPanel >> 4) + (s & 3) * 2,
                    kIdS, s > 0);
         mma_commit(&ctl.s_full);
       };
       auto issue_o = [&]() {
 #pragma unroll
-        for (int s = 0; s < 16; ++s)  // part, 16 keys
-          mma_f16_ts(tmem + kColO, tmem + kColP + 8 * s, dv + (s & 7) * 128, kIdO, s > 0);
+        for (int s = 0; s < 16; ++s)  // part (low first), 16 keys
+          mma_f16_ts(tmem + kColO, tmem + kColP + 8 * (s ^ 8), dv + (s & 7) * 128, kIdO, s > 0);
         mma_commit(&ctl.o_full);
       };
       convert_keys(0);

@@ -202,6 +202,37 @@ def test_attn(gdn, name, mask, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("n,group", [(2, 4), (3, 3), (1, 16), (17, 1), (5, 4), (6, 4), (5, 5), (31, 1), (8, 4), (11, 3)])
+def test_attn_row_counts(gdn, n, group, window, dtype):
+    """Rows that share a key, either side of 8, 16, 24 and 32; lengths of one tile, of odd and of even
+    numbers of tiles, ending inside, at and just past one; a sequence cut between CTAs."""
+    b = U.Batch([n] * 7, [n, 128, 129, 300, 384, 513, 6000], 2, seed=n + group)
+    b.fill()
+    check_attn(gdn, b, 2 * group, dtype, window=window)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_on_another_stream(gdn, dtype):
+    """On a stream of the caller's, with outputs and workspace from the call."""
+    b = U.Batch([1, 3, 200], [900, 5000, 2000], 2, seed=4)
+    b.fill()
+    cache, q = to_cache(gdn, b), b.randn(b.T, 8, 128).to(dtype).cuda()
+    lens, table, cu = b.lens.cuda(), b.table.cuda(), b.cu.cuda()
+    want = gdn.gdn_kv_attn(q, cache, lens, table, cu)
+    kept = gdn.gdn_kv_read(cache, lens, table, cu, T=b.T, dtype=dtype)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        got = gdn.gdn_kv_attn(q, cache, lens, table, cu, stream=side)
+        read = gdn.gdn_kv_read(cache, lens, table, cu, T=b.T, dtype=dtype, stream=side)
+        torch.empty(32 << 20, dtype=torch.uint8, device="cuda").fill_(255)  # takes what the current stream has free
+    torch.cuda.current_stream().wait_stream(side)
+    for x, y in zip((*got, *read), (*want, *kept)):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_attn_sharp_and_flat(gdn, dtype):
     """Scores from far below to far above the others: one key takes all the weight, and none does."""
     b = U.Batch([1, 1, 40], [500, 500, 500], 2, seed=9, spread=0.2)
@@ -254,6 +285,25 @@ def test_attn_one_key_against_many(gdn, n):
     # two bf16 roundings of weights and output, relative to the weights' sum of one
     assert (out.double().cpu() - want).abs().max() <= 2.0 ** -7
     assert (lse.double().cpu() - torch.log(2.0 ** 20 + rest.double())[:, None]).abs().max() <= 2.0 ** -14
+
+
+def test_attn_f32_one_key_against_many(gdn):
+    """The same in fp32, to a rounding a tile: 3907 tiles of 2^-24, and 2^-22 of the exponential."""
+    kv = 500_000
+    b = U.Batch([1], [kv], 1, seed=1)
+    pages = b.table[0].long()
+    b.k, b.ks = torch.zeros(b.n_pages, 1, 64, 128), torch.ones(b.n_pages, 1)
+    b.v, b.vs = torch.zeros(b.n_pages, 1, 64, 128), torch.ones(b.n_pages, 1)
+    b.v[pages] = 1.0
+    b.v[pages[0], 0, 0] = -1.0
+    q = torch.zeros(1, 4, 128)
+    q[..., 0] = 1.0
+    q[..., 1] = 1 / 3
+    b.k[pages[0], 0, 0, 0] = 1.0
+    out, lse = gdn.gdn_kv_attn(q.cuda(), to_cache(gdn, b), b.lens.cuda(), b.table.cuda(), scale=20 * math.log(2.0))
+    w0 = 2.0 ** 20 / (2.0 ** 20 + kv - 1)
+    assert (out.double().cpu() - (1 - 2 * w0)).abs().max() <= 2.0 ** -11
+    assert (lse.double().cpu() - math.log(2.0 ** 20 + kv - 1)).abs().max() <= 2.0 ** -11
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])

@@ -383,10 +383,14 @@ gdn_status encode_kv_map(CUtensorMap* m, void* base, const gdn_kv_cache* c) {
 constexpr int kKvPathF32 = 0;   // fp32
 constexpr int kKvPathFew = 1;   // bf16, up to 32 rows (tokens times heads of a group) per (sequence, key/value head)
 constexpr int kKvPathMany = 2;  // bf16, more rows
-// What parts and the second kernel cost, in key tiles: about 38 us at 1.35 us a
-// tile of 256 rows on the tensor cores, 6 us at 0.7 us a tile of few rows, 6 us
-// at 2 us a tile of an fp32 call.
-constexpr int kKvJoinTilesMany = 28, kKvJoinTilesFew = 8, kKvJoinTilesF32 = 3;
+// What parts and the second kernel cost, in key tiles, against whole items:
+// for few rows 6 us at 0.7 us a tile; in fp32 6 us at 2 us a tile; for many rows,
+// at 1.5 us a tile, 18 us and more the longer a run is (`tiles`), since it then
+// begins and ends more items, up to some 42 us.
+int64_t kv_join_tiles(int path, int64_t tiles) {
+  return path == kKvPathMany ? std::min<int64_t>(28, 12 + tiles / 4) : path == kKvPathFew ? 8 : 3;
+}
+constexpr int kKvMaxParts = 32;  // of an item on the path for many rows: a warp of the second kernel takes a row's in turn
 
 }  // namespace
 
@@ -886,10 +890,12 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   // by a second kernel.  Both are estimated in key tiles, every sequence taken
   // at its longest: whole items end with the longest one, or with the last
   // round of equal ones; runs end together, plus the parts' way through
-  // memory and the second kernel (kKvJoinTiles).  Measured, whole and runs: 16
-  // tokens over 1024 keys of 8 heads 15.6 and 18.1 us, 19 over 4096 keys 58.8
-  // and 38.9; 4096 prompt tokens over 65536 keys, 8 query heads on 2, 792 and 690
-  // us, 8 prompts of 2048 tokens, 16 heads, 221 and 225.
+  // memory and the second kernel.  Measured, whole and runs, in us: 16 tokens
+  // over 1024 keys of 8 heads 12.6 and 14.6, 40 over 2048 keys 46.8 and 39.1;
+  // with 8 query heads on 2, 64 tokens over 512 keys 20.4 and 19.7, over 2048
+  // keys 39.6 and 21.6, prompts of 1024 tokens 28.1 and 28.5, 4096 tokens 67 and
+  // 65, 8192 tokens 119 and 147, 4096 tokens over 65536 keys 792 and 690; fp32
+  // prompts of 2048 tokens 68.8 and 53.3, 4096 tokens 128 and 141.
   int64_t total = 0, longest_item = 0, shortest = INT64_MAX;
   const int64_t past = std::max(0, max_kv_len - max_q_len);
   for (int rt = 0; rt < p.max_row_tiles; ++rt) {
@@ -908,8 +914,10 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   total *= (int64_t)d->n_seqs * h_kv;
   const int64_t whole = longest_item == shortest ? (items + slots - 1) / slots * longest_item
                                                  : std::max(longest_item, (total + slots - 1) / slots + shortest);
-  const int64_t runs = (total + slots - 1) / slots + (p.path == kKvPathMany ? kKvJoinTilesMany : p.path == kKvPathFew ? kKvJoinTilesFew : kKvJoinTilesF32);
-  p.n_ctas = whole <= runs ? 0 : (int)std::min<int64_t>(slots, total);
+  const int64_t run = (total + slots - 1) / slots, runs = run + kv_join_tiles(p.path, run);
+  int64_t ctas = std::min(slots, total);
+  if (p.path == kKvPathMany) ctas = std::min(ctas, kKvMaxParts * items);  // 64 tokens over 8192 keys: 70 parts 32.6 us, 32 27
+  p.n_ctas = whole <= runs ? 0 : (int)ctas;
   p.n_seqs = d->n_seqs;
   p.T = d->T;
   p.h_q = d->h_q;

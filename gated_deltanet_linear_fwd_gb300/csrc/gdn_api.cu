@@ -381,8 +381,8 @@ gdn_status encode_kv_map(CUtensorMap* m, void* base, const gdn_kv_cache* c) {
 
 // Kernels of gdn_kv_attn.
 constexpr int kKvPathF32 = 0;   // fp32
-constexpr int kKvPathFew = 1;   // bf16, up to 32 rows (tokens times heads of a group) per (sequence, key/value head)
-constexpr int kKvPathMany = 2;  // bf16, more rows
+constexpr int kKvPathFew = 1;   // bf16, row tiles of up to 32: few rows (tokens times heads of a group), small calls
+constexpr int kKvPathMany = 2;  // bf16, row tiles of 256
 // What parts and the second kernel cost, in key tiles, against whole items:
 // for few rows 6 us at 0.7 us a tile; in fp32 6 us at 2 us a tile; for many rows,
 // at 1.5 us a tile, 18 us and more the longer a run is (`tiles`), since it then
@@ -863,60 +863,74 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   const int group = (d->h_q + h_kv - 1) / h_kv;
   if ((int64_t)d->T * group > 0x7fffffff - 4096) return GDN_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)max_q_len * group;
-  // bf16: kernel and row tile by the rows that share a key.  Measured on 64
-  // sequences to 32768 tokens with 4 key/value heads: 32 rows 221 us on the kernel
-  // for few rows and 535 on the other, 48 rows 408 (two tiles) and 331.
+  // Key tiles, every sequence taken at its longest, with item_cost for each item.
+  struct Units {
+    int64_t total, longest_item, shortest;
+    int row_tiles;
+  };
+  auto units_of = [&](int tile_rows, int item_cost) {
+    Units u = {0, 0, INT64_MAX, (int)std::max<int64_t>(1, (rows + tile_rows - 1) / tile_rows)};
+    const int64_t past = std::max(0, max_kv_len - max_q_len);
+    for (int rt = 0; rt < u.row_tiles; ++rt) {
+      const int64_t t0 = (int64_t)rt * tile_rows / group;
+      const int64_t t1 = std::min<int64_t>(max_q_len - 1, ((int64_t)(rt + 1) * tile_rows - 1) / group);
+      const int64_t hi = d->causal ? std::min<int64_t>(past + t1 + 1, max_kv_len) : max_kv_len;
+      const int64_t lo = d->window ? std::max<int64_t>(0, past + t0 - d->window + 1) : 0;
+      const int64_t cost = item_cost + std::max<int64_t>(1, (hi + kKvTile - 1) / kKvTile - lo / kKvTile);
+      u.total += cost;
+      u.longest_item = std::max(u.longest_item, cost);
+      u.shortest = std::min(u.shortest, cost);
+    }
+    u.total *= (int64_t)d->n_seqs * h_kv;
+    return u;
+  };
   p.path = kKvPathF32;
   p.rows = 128;
   p.item_cost = 2;
   int per_sm = 1;
-  if (d->dtype == GDN_BF16 && rows <= 32) {
+  Units u;
+  if (d->dtype == GDN_BF16) {
+    // Kernel and row tile by the rows that share a key, and by how much there is
+    // to do: small calls are sooner done in tiles of 32 rows, which there are more
+    // of and which begin sooner, up to 8 units an SM.  Measured, tiles of 256 rows
+    // and of 32 or fewer, in us: 64 sequences to 32768 tokens, 4 key/value heads, 32
+    // rows 535 and 221, 48 rows 331 and 408; 8 query heads on 2, 64 tokens over 64
+    // keys 14.2 and 11.1 (1 unit an SM), over 8192 keys 28.8 and 20.2 (8), over 65536 56
+    // and 61 (55), prompts of 512 tokens 20.7 and 19.4 (9), 1024 tokens 28 and 33 (21).
     p.path = kKvPathFew;
-    p.rows = std::max<int>(8, (int)(rows + 7) / 8 * 8);
+    p.rows = (int)std::min<int64_t>(32, (rows + 7) / 8 * 8);
     // measured: 64 sequences to 65536 tokens, 16 rows, 62.7 us at 3 and 58.5 at 8; 256 to 32768, 8 rows, 116 at 3,
     // 111 at 4 and 113 at 12
     p.item_cost = p.rows <= 8 ? 4 : 8;
     per_sm = kv_few_ctas_per_sm(p.rows);
-  } else if (d->dtype == GDN_BF16) {
-    p.path = kKvPathMany;
-    p.rows = 256;
-    p.item_cost = 6;
+    if (rows > 32 && (rows >= 32 * (int64_t)sm_count || units_of(32, p.item_cost).total > 8 * (int64_t)sm_count)) {
+      p.path = kKvPathMany;
+      p.rows = 256;
+      p.item_cost = 6;
+    }
   }
-  p.max_row_tiles = std::max<int>(1, (int)(((int64_t)max_q_len * group + p.rows - 1) / p.rows));
+  u = units_of(p.rows, p.item_cost);
+  p.max_row_tiles = u.row_tiles;
   const int64_t items = (int64_t)d->n_seqs * p.max_row_tiles * h_kv;
   const int64_t slots = (int64_t)per_sm * sm_count;
   // Two ways to share out the items: each whole to one CTA, the longest first
   // (n_ctas = 0), or all key tiles in equal runs, whose cut items are joined
-  // by a second kernel.  Both are estimated in key tiles, every sequence taken
-  // at its longest: whole items end with the longest one, or with the last
+  // by a second kernel.  Whole items end with the longest one, or with the last
   // round of equal ones; runs end together, plus the parts' way through
   // memory and the second kernel.  Measured, whole and runs, in us: 16 tokens
   // over 1024 keys of 8 heads 12.6 and 14.6, 40 over 2048 keys 46.8 and 39.1;
-  // with 8 query heads on 2, 64 tokens over 512 keys 20.4 and 19.7, over 2048
-  // keys 39.6 and 21.6, prompts of 1024 tokens 28.1 and 28.5, 4096 tokens 67 and
-  // 65, 8192 tokens 119 and 147, 4096 tokens over 65536 keys 792 and 690; fp32
-  // prompts of 2048 tokens 68.8 and 53.3, 4096 tokens 128 and 141.
-  int64_t total = 0, longest_item = 0, shortest = INT64_MAX;
-  const int64_t past = std::max(0, max_kv_len - max_q_len);
-  for (int rt = 0; rt < p.max_row_tiles; ++rt) {
-    const int64_t t0 = (int64_t)rt * p.rows / group;
-    const int64_t t1 = std::min<int64_t>(max_q_len - 1, ((int64_t)(rt + 1) * p.rows - 1) / group);
-    const int64_t hi = d->causal ? std::min<int64_t>(past + t1 + 1, max_kv_len) : max_kv_len;
-    const int64_t lo = d->window ? std::max<int64_t>(0, past + t0 - d->window + 1) : 0;
-    const int64_t cost = p.item_cost + std::max<int64_t>(1, (hi + kKvTile - 1) / kKvTile - lo / kKvTile);
-    total += cost;
-    longest_item = std::max(longest_item, cost);
-    shortest = std::min(shortest, cost);
-  }
+  // with 8 query heads on 2, 1024 tokens over 4096 keys 67 and 40, prompts of
+  // 1024 tokens 28.1 and 28.5, 4096 tokens 67 and 65, 8192 tokens 119 and 147,
+  // 4096 tokens over 65536 keys 792 and 690; fp32 prompts of 2048 tokens 68.8 and
+  // 53.3, 4096 tokens 128 and 141.
   // the kernels count units in 32 bits, whatever the lengths on the device turn out to be
   const int64_t units_most = (int64_t)d->max_pages * kPage / kKvTile + 1 + p.item_cost;
   if (items > 0x7fffffff / units_most) return GDN_ERR_INVALID_ARG;
-  total *= (int64_t)d->n_seqs * h_kv;
-  const int64_t whole = longest_item == shortest ? (items + slots - 1) / slots * longest_item
-                                                 : std::max(longest_item, (total + slots - 1) / slots + shortest);
-  const int64_t run = (total + slots - 1) / slots, runs = run + kv_join_tiles(p.path, run);
-  int64_t ctas = std::min(slots, total);
-  if (p.path == kKvPathMany) ctas = std::min(ctas, kKvMaxParts * items);  // 64 tokens over 8192 keys: 70 parts 32.6 us, 32 27
+  const int64_t whole = u.longest_item == u.shortest ? (items + slots - 1) / slots * u.longest_item
+                                                     : std::max(u.longest_item, (u.total + slots - 1) / slots + u.shortest);
+  const int64_t run = (u.total + slots - 1) / slots, runs = run + kv_join_tiles(p.path, run);
+  int64_t ctas = std::min(slots, u.total);
+  if (p.path == kKvPathMany) ctas = std::min(ctas, kKvMaxParts * items);  // of 2 items, 70 parts each 32.6 us, 35 26.9
   p.n_ctas = whole <= runs ? 0 : (int)ctas;
   p.n_seqs = d->n_seqs;
   p.T = d->T;

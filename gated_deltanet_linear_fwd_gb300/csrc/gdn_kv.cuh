@@ -117,15 +117,18 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   return c;
 }
 
-// Two fp32 (below 2^9) as e4m3 parts, x = hi + lo: four leading bits and the
-// next four; through fp16, whose 11 bits the parts do not reach.
+// Two fp32 (below 2^9) as e4m3 parts, x = hi + lo / kLoScale: four leading bits
+// and the next four, to 2^-10 / kLoScale at least; through fp16, whose 11 bits
+// the parts do not reach.
+template <int kLoScale = 1>
 __device__ __forceinline__ void split_e4m3(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   uint32_t x16, h16;
   uint16_t h, l;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(x16) : "f"(x1), "f"(x0));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(x16));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h));
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x16), *reinterpret_cast<const __half2*>(&h16));
+  __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x16), *reinterpret_cast<const __half2*>(&h16));
+  if (kLoScale != 1) r = __hmul2(r, __float2half2_rn((float)kLoScale));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(*reinterpret_cast<const uint32_t*>(&r)));
   hi = h;
   lo = l;

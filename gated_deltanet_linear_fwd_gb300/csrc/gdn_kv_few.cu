@@ -11,8 +11,8 @@
 // of two so that its largest magnitude is in (224, 448], is the sum of two
 // e4m3 rows hi + lo / 16: hi has its four leading bits, lo the remaining four,
 // exactly where it is within 2^13 of the row's largest and to 2^-22 of that
-// below.  Weights P = 2^(x - m + 8) enter as hi + lo, eight bits (to 2^-8 of
-// each weight, relative; a bf16 weight has 2^-9).  The two parts are columns of
+// below.  Weights P = 2^(x - m + 8) enter as hi + lo / 16, eight bits (to 2^-8 of
+// each weight, relative, down to 2^-14 of the largest; a bf16 weight has 2^-9).  The two parts are columns of
 // one product, so no key or value is converted or read twice.
 //
 // Softmax over the keys x_j = scale log2(e) q . k_j, by steps of one or two
@@ -21,7 +21,7 @@
 // m_t the step's maximum of x + e_v, P_j = 2^(x_j + e_v - m_t + 8), so
 // P . V-codes is the step's output in units of 2^(m_t - 8), and its sum is of
 // P_j 2^-e_v, kept in fp32 from the unrounded P.  Weights count from their own
-// step's maximum, so what e4m3 cannot hold is below 2^-18 of that, however many
+// step's maximum, so what e4m3 cannot hold is below 2^-22 of that, however many
 // keys there are.  Steps are joined in fp32 registers, under the next step's
 // second product: o <- o 2^(m - m') + O_t 2^(m_t - m'), m' the larger of m and
 // m_t; the two factors of a row are found by one lane and shared.
@@ -373,7 +373,7 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
       for (int r = 0; r < R / 2; ++r) {
         const float2 alpha = *reinterpret_cast<const float2*>(&ctl->alpha[w][t & 1][2 * r]);
         const float2 beta = *reinterpret_cast<const float2*>(&ctl->beta[w][t & 1][2 * r]);
-        const float2 now = add2(bits2(h + 2 * r), bits2(h + R + 2 * r));
+        const float2 now = fma2(bits2(h + R + 2 * r), both(0.0625f), bits2(h + 2 * r));
         o[r] = fma2(o[r], alpha, mul2(now, beta));
       }
     };
@@ -510,7 +510,7 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
         uint8_t* p = sm + F::kOffP + (buf * T + h) * F::kPBytes + wg * (16 * kKvTile) + tid * 16;
         uint32_t hi[R / 2], lo[R / 2];
 #pragma unroll
-        for (int r = 0; r < R / 2; ++r) split_e4m3(x[h][2 * r], x[h][2 * r + 1], hi[r], lo[r]);
+        for (int r = 0; r < R / 2; ++r) split_e4m3<16>(x[h][2 * r], x[h][2 * r + 1], hi[r], lo[r]);
         *reinterpret_cast<uint4*>(p) = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
       }
       fence_proxy_async_smem();

@@ -287,6 +287,26 @@ def test_attn_one_key_against_many(gdn, n):
     assert (lse.double().cpu() - torch.log(2.0 ** 20 + rest.double())[:, None]).abs().max() <= 2.0 ** -14
 
 
+@pytest.mark.parametrize("n", [1, 3, 9, 100])
+def test_attn_weights_far_below_the_largest(gdn, n):
+    """The largest weight's value is zero, and the others, 2^-12.3 of it, make the output: each still has
+    eight bits, and the output's rounding is one more of nine."""
+    kv = 1000
+    b = U.Batch([n], [kv], 1, seed=n)
+    pages = b.table[0].long()
+    b.k, b.ks = torch.zeros(b.n_pages, 1, 64, 128), torch.ones(b.n_pages, 1)
+    b.v, b.vs = torch.zeros(b.n_pages, 1, 64, 128), torch.ones(b.n_pages, 1)
+    b.v[pages] = 1.0
+    b.v[pages[0], 0, 0] = 0.0
+    b.k[pages[0], 0, 0, 0] = 1.0
+    q = torch.zeros(n, 4, 128)
+    q[..., 0] = 1.0
+    out, _ = gdn.gdn_kv_attn(q.to(BF).cuda(), to_cache(gdn, b), b.lens.cuda(), b.table.cuda(), scale=12.3 * math.log(2.0))
+    w = (kv - n + torch.arange(n)).double() * 2.0 ** -12.3
+    want = (w / (1 + w))[:, None, None]
+    assert ((out.double().cpu() - want).abs() / want).max() <= 2.0 ** -8 + 2.0 ** -9 + 2.0 ** -12
+
+
 def test_attn_f32_one_key_against_many(gdn):
     """The same in fp32, to a rounding a tile: 3907 tiles of 2^-24, and 2^-22 of the exponential."""
     kv = 500_000

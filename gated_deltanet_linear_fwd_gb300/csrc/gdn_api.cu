@@ -386,8 +386,10 @@ constexpr int kKvPathMany = 2;  // bf16, row tiles of 256
 // What parts and the second kernel cost, in key tiles, against whole items:
 // for few rows 6 us at 0.7 us a tile; in fp32 6 us at 2 us a tile; for many rows,
 // at 1.5 us a tile, 18 us and more the longer a run is (`tiles`), since it then
-// begins and ends more items, up to some 42 us.
-int64_t kv_join_tiles(int path, int64_t tiles) {
+// begins and ends more items, up to some 42 us.  Items of one tile are never
+// cut: that leaves some 3 us of the second kernel's launch.
+int64_t kv_join_tiles(int path, int64_t tiles, bool one_tile) {
+  if (one_tile) return path == kKvPathMany ? 2 : path == kKvPathFew ? 4 : 1;
   return path == kKvPathMany ? std::min<int64_t>(28, 12 + tiles / 4) : path == kKvPathFew ? 8 : 3;
 }
 constexpr int kKvMaxParts = 32;  // of an item on the path for many rows: a warp of the second kernel takes a row's in turn
@@ -918,7 +920,8 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   // by a second kernel.  Whole items end with the longest one, or with the last
   // round of equal ones; runs end together, plus the parts' way through
   // memory and the second kernel.  Measured, whole and runs, in us: 16 tokens
-  // over 1024 keys of 8 heads 12.6 and 14.6, 40 over 2048 keys 46.8 and 39.1;
+  // over 1024 keys of 8 heads 12.6 and 14.6, 40 over 2048 keys 46.8 and 39.1, 147
+  // over 28 keys of 16 heads 54.9 and 42;
   // with 8 query heads on 2, 1024 tokens over 4096 keys 67 and 40, prompts of
   // 1024 tokens 28.1 and 28.5, 4096 tokens 67 and 65, 8192 tokens 119 and 147,
   // 4096 tokens over 65536 keys 792 and 690; fp32 prompts of 2048 tokens 68.8 and
@@ -926,9 +929,13 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   // the kernels count units in 32 bits, whatever the lengths on the device turn out to be
   const int64_t units_most = (int64_t)d->max_pages * kPage / kKvTile + 1 + p.item_cost;
   if (items > 0x7fffffff / units_most) return GDN_ERR_INVALID_ARG;
-  const int64_t whole = u.longest_item == u.shortest ? (items + slots - 1) / slots * u.longest_item
-                                                     : std::max(u.longest_item, (u.total + slots - 1) / slots + u.shortest);
-  const int64_t run = (u.total + slots - 1) / slots, runs = run + kv_join_tiles(p.path, run);
+  const int64_t rounds = (items + slots - 1) / slots;  // a CTA's start in each but the first counts a unit
+  const int64_t whole = rounds - 1 + (u.longest_item == u.shortest
+                                          ? rounds * u.longest_item
+                                          : std::max(u.longest_item, (u.total + slots - 1) / slots + u.shortest));
+  const bool one_tile = u.longest_item == p.item_cost + 1;  // then runs are of whole items too
+  const int64_t run = one_tile ? rounds * u.longest_item : (u.total + slots - 1) / slots;
+  const int64_t runs = run + kv_join_tiles(p.path, run, one_tile);
   int64_t ctas = std::min(slots, u.total);
   if (p.path == kKvPathMany) ctas = std::min(ctas, kKvMaxParts * items);  // of 2 items, 70 parts each 32.6 us, 35 26.9
   p.n_ctas = whole <= runs ? 0 : (int)ctas;

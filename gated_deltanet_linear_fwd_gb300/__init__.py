@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) Gated Delta Network chunked-prefill forward and its backward.
+"""GB300 (sm_103a) Gated Delta Network chunked-prefill forward and its backward,
+and the 8-bit key/value cache with the attention over it that models use beside it.
 
 The compute lives in libgdn.so (C ABI in include/gdn.h); this package is its
 thin Python binding plus the seeded input generators.

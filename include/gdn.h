@@ -455,7 +455,7 @@ typedef struct gdn_kv_plan_t {
   int path;          /* which kernel: see gdn_kv_attn_plan */
   int rows;          /* query rows (token, query head of one group) per row tile */
   int max_row_tiles; /* row tiles of one sequence and key/value head, at most */
-  int n_ctas;        /* CTAs the key tiles of all row tiles are shared out to */
+  int n_ctas;        /* CTAs the key tiles of all row tiles are shared out to; 0: a CTA each row tile */
   int item_cost;     /* what a row tile costs beyond its key tiles, in key tiles */
   int n_seqs, T, h_q, h_kv, dtype; /* copied, checked by gdn_kv_attn */
   int max_q_len;
@@ -469,7 +469,8 @@ typedef struct gdn_kv_plan_t {
  *   max_kv_len : the longest sequence expected (<= 0: 64 max_pages); sizes the
  *                split only, so replays of a captured call may pass it.
  *   sm_count   : SMs to plan for; <= 0 queries the current device.
- * Errors: INVALID_ARG, UNSUPPORTED, CUDA (device query).
+ * Errors: INVALID_ARG (also for calls past 2^31 units: row tiles times key
+ * tiles of 128), UNSUPPORTED, CUDA (device query).
  */
 gdn_status gdn_kv_attn_plan(const gdn_kv_dims* dims, int h_kv, int max_q_len, int max_kv_len, int sm_count,
                             gdn_kv_plan_t* out_plan);
@@ -489,9 +490,13 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* dims, int h_kv, int max_q_len, in
  *   workspace  : device, 256-byte aligned, >= plan->workspace_bytes; its
  *                contents on entry do not matter.  Not to be shared by calls
  *                that may run concurrently.
- * GDN_BF16 runs on the tensor cores (keys and values enter the products
- * exactly; the softmax and all sums are fp32), GDN_F32 in fp32 throughout on
- * the CUDA cores.  Asynchronous on `stream`.
+ * Both types run on the tensor cores; keys and values enter the products
+ * exactly, and the softmax and all sums are fp32.  With GDN_BF16 a weight enters
+ * with eight bits or more; with GDN_F32 queries and weights enter as two fp16
+ * parts each, 22 bits or more.  Results repeat bit for bit under the same plan.
+ * Asynchronous on `stream`; one or two kernels.
+ * A sequence that brings more tokens than the plan's max_q_len is recorded as
+ * the same device check (detail 7).
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
  */
 gdn_status gdn_kv_attn(const void* q, const int32_t* kv_lens_dev, const int32_t* page_table_dev,

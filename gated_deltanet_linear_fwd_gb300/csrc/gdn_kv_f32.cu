@@ -11,12 +11,16 @@
 // The low parts come first: the tensor cores' sums lose a little at every step,
 // in proportion to what is in them (2000 to 4000 keys, unit queries: relative error
 // 4e-7 against 64 bits, 1.1e-6 with the high parts first, 1.2e-6 for fp32 products
-// and softmax).  That is twice the products of a bf16 call.  Prompts over themselves, 8 query
-// heads on 2: 16384 tokens 1675 us (328 TFLOP/s), 2048 tokens 57 us; as fp32 FMAs on
-// the CUDA cores 2048 tokens took 278 us.  64 sequences of 1024 to 8192 tokens, 4
-// heads: 229 us for 8 rows (1.15 TB/s of codes; 598 with FMAs), 242 for 64.
-// Bound by the chain of a tile, some 2 us: conversion, product, softmax, product,
-// join, of which only the second product's neighbours overlap.
+// and softmax).
+//
+// That is twice the products of a bf16 call.  Prompts over themselves, 8 query
+// heads on 2: 16384 tokens 1595 us (345 TFLOP/s of the formula), 2048 tokens 52 us;
+// as fp32 FMAs on the CUDA cores 2048 tokens took 278 us.  64 sequences of 1024 to
+// 8192 tokens, 4 heads: 207 us for 8 rows (1.27 TB/s of codes; 598 with FMAs).
+// Bound by the chain of a tile, some 6200 cycles: converting keys 650, scores and
+// maximum 700, weights 1200, 2000 in which warp 0 issues the products as they
+// run, join and converting values 1100.  With 512 threads, half as much for each,
+// the same chain was longer (16384 tokens 1950 us).
 //
 // Softmax as in the kernel for few rows: x_j = scale log2(e) q . k_j plus the
 // log2 of the values' page scale; weights count from their own tile's maximum,
@@ -164,25 +168,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const __grid_cons
     for (int d = 0; d < 64; ++d) o[d] = 0.f;
 
     if (tiles > 0) {
-      // ---- the codes of a tile on their way: pages a tile ahead of codes, codes a tile ahead of their use ----
-      int page0, page1;  // of the next tile to load, times heads; -1: past the sequence
+      // ---- the codes of a tile on their way: a tile ahead of their use, their pages another tile ahead ----
+      int page0 = -1, page1 = -1, next0, next1;  // times heads; -1: past the sequence
       uint4 kc[4], vc[4];
       float sk, sv, next_sk = 1.f, next_sv = 1.f;  // scales of this warp's page
       auto fetch_pages = [&](int j) {
         const int slot = 2 * (cur.tile_begin() + j);
-        page0 = j < tiles && slot * kPage < it.len ? max(kv_page(a.c, cur.seq, slot), 0) * a.c.h_kv + cur.head : -1;
-        page1 = j < tiles && (slot + 1) * kPage < it.len ? max(kv_page(a.c, cur.seq, slot + 1), 0) * a.c.h_kv + cur.head : -1;
+        next0 = j < tiles && slot * kPage < it.len ? max(kv_page(a.c, cur.seq, slot), 0) * a.c.h_kv + cur.head : -1;
+        next1 = j < tiles && (slot + 1) * kPage < it.len ? max(kv_page(a.c, cur.seq, slot + 1), 0) * a.c.h_kv + cur.head : -1;
       };
-      auto fetch_codes = [&]() {
-        const int mine = key_row < kPage ? page0 : page1, of_scale = half ? page1 : page0;
+      auto fetch = [&](uint4 (&w)[4], const uint8_t* codes) {
+        const int mine = key_row < kPage ? page0 : page1;
         const size_t at = (size_t)max(mine, 0) * kPageBytes + (key_row & (kPage - 1)) * kHeadDim + half * 64;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          kc[c] = mine >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.c.k + at) + c) : make_uint4(0, 0, 0, 0);
-          vc[c] = mine >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.c.v + at) + c) : make_uint4(0, 0, 0, 0);
-        }
+        for (int c = 0; c < 4; ++c) w[c] = mine >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + at) + c) : make_uint4(0, 0, 0, 0);
+      };
+      auto fetch_values = [&]() {  // and the scales
+        fetch(vc, a.c.v);
+        const int of_scale = half ? page1 : page0;
         next_sk = of_scale >= 0 ? a.c.k_scale[of_scale] : 1.f;
         next_sv = of_scale >= 0 ? a.c.v_scale[of_scale] : 1.f;
+        page0 = next0;
+        page1 = next1;
       };
       uint32_t keep;  // of the values in vc
       // keys of tile j to shared memory; which of its values may be used
@@ -201,8 +208,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const __grid_cons
         }
       };
       fetch_pages(0);
-      fetch_codes();
+      page0 = next0;
+      page1 = next1;
       fetch_pages(1);
+      fetch(kc, a.c.k);
+      fetch_values();
 
       // ---- query rows: thread = 64 columns of one ----
       {
@@ -239,8 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const __grid_cons
         for (int d = 0; d < 64; ++d) o[d] = 0.f;
       }
       // products of the elected lane
-      auto issue_s = [&](int j) {
-        const uint64_t k = dk + (j & 1) * (2 * kPanel >> 4);
+      auto issue_s = [&](uint32_t buf) {
+        const uint64_t k = dk + buf * (2 * kPanel >> 4);
 #pragma unroll
         for (int s = 0; s < 16; ++s)  // part (low first), panel, 16 columns
           mma_bf16(tmem + kColS, dq + ((s >> 2) ^ 2) * (kPanel >> 4) + (s & 3) * 2, k + ((s >> 2) & 1) * (kPanel >> 4) + (s & 3) * 2,
@@ -257,18 +267,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const __grid_cons
       convert_row(sm + kOffV + half * kPanel, key_row, vc, keep);
       sk = next_sk;
       sv = next_sv;
-      fetch_codes();
       fetch_pages(2);
+      fetch(kc, a.c.k);
+      fetch_values();
       fence_proxy_async_smem();
       tc_fence_before();
       __syncthreads();
       tc_fence_after();
-      if (warp == 0 && elect_one()) issue_s(0);
-      __syncwarp();
+      if (warp == 0) {
+        if (elect_one()) issue_s(0);
+        __syncwarp();
+      }
 
 #pragma unroll 1
       for (int j = 0; j < tiles; ++j) {
-        if (j + 1 < tiles) convert_keys(j + 1);
+        if (j + 1 < tiles) {
+          convert_keys(j + 1);
+          fetch(kc, a.c.k);
+          fetch_pages(j + 3);
+        }
         if (!bad) bad = !kv_wait(&ctl.s_full, par, &ctl.abort, 100 + kBarS);
         tc_fence_after();
         const float ev = (float)((int)(__float_as_uint(sv) >> 23) - 127);  // log2 of a power of two
@@ -337,19 +354,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const __grid_cons
         bad = __syncthreads_or(bad);
         if (bad) break;
         tc_fence_after();
-        if (warp == 0 && elect_one()) {
-          issue_o();
-          if (j + 1 < tiles) issue_s(j + 1);
+        if (warp == 0) {
+          const uint32_t buf = __shfl_sync(0xffffffffu, (j + 1) & 1, 0), more = __shfl_sync(0xffffffffu, j + 1 < tiles, 0);
+          if (elect_one()) {
+            issue_o();
+            if (more) issue_s(buf);
+          }
+          __syncwarp();
         }
-        __syncwarp();
         // values of the next tile, in registers until this tile's product has read its own; then on to the codes after
         bad = !kv_wait(&ctl.o_full, par, &ctl.abort, 100 + kBarO);
         par ^= 1;
         tc_fence_after();
         if (j + 1 < tiles) {
           if (!bad) convert_row(sm + kOffV + half * kPanel, key_row, vc, keep);
-          fetch_codes();
-          fetch_pages(j + 3);
+          fetch_values();
         }
         if (!idle && !bad) {
 #pragma unroll

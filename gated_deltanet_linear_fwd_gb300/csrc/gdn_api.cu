@@ -946,7 +946,7 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   p.dtype = d->dtype;
   p.max_q_len = max_q_len;
   p.off_desc = 0;
-  p.off_ml = align_up((size_t)p.n_ctas * sizeof(int4), 256);
+  p.off_ml = align_up((size_t)2 * p.n_ctas * sizeof(int4), 256);
   p.off_o = align_up(p.off_ml + (size_t)2 * p.n_ctas * p.rows * sizeof(float2), 256);
   p.workspace_bytes = p.off_o + (size_t)2 * p.n_ctas * p.rows * kHeadDim * sizeof(float);
   *out = p;

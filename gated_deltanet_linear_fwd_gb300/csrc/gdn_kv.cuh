@@ -54,7 +54,7 @@ struct KvAttnArgs {
   int max_rows;            // rows of the longest sequence the plan allows
   int n_ctas;              // 0: CTA i takes item i whole
   int item_cost;           // what beginning and ending an item costs, in key tiles
-  int4* desc;              // [n_ctas] item whose first part this CTA made: {sequence, row tile, head, last CTA}
+  int4* desc;              // [2 n_ctas] item whose first part this CTA made, in two: {last CTA or -1, row tile, head}, {first token, tokens}
   float2* ml;              // [2 n_ctas, rows] running maximum (log2) and sum of a part
   float* o;                // [2 n_ctas, rows, 128] unnormalised output of a part
 };
@@ -341,6 +341,16 @@ struct KvCursor {
 __device__ __forceinline__ int kv_last_cta(const KvAttnArgs& a, const KvRun& r, const KvCursor& c) {
   const int64_t item_end = (int64_t)r.begin + c.base + kv_cost(a, c.it);
   return (int)((item_end * r.ctas - 1) / r.total);
+}
+
+// What the second kernel needs of the item this CTA began and did not end, or
+// that there is none (said by every CTA before its run).
+__device__ __forceinline__ void kv_desc_none(const KvAttnArgs& a) {
+  if (a.n_ctas) a.desc[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+}
+__device__ __forceinline__ void kv_desc_put(const KvAttnArgs& a, const KvRun& r, const KvCursor& c) {
+  a.desc[2 * blockIdx.x] = make_int4(kv_last_cta(a, r, c), c.rt, c.head, 0);
+  a.desc[2 * blockIdx.x + 1] = make_int4(c.it.tok0, c.it.n, 0, 0);
 }
 
 // Bounded wait on an mbarrier phase: gives up (false) after kWaitTries tries,

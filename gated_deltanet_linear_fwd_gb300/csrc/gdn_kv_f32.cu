@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const __grid_cons
     tmem_relinquish();
   }
   grid_dependency_wait();
-  if (tid == 0 && a.n_ctas) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (tid == 0) kv_desc_none(a);
   kv_run<kThreads>(a, &ctl.run);
   tc_fence_before();
   __syncthreads();
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const __grid_cons
         dst[c] = make_float4(o[4 * c] * by, o[4 * c + 1] * by, o[4 * c + 2] * by, o[4 * c + 3] * by);
     }
     if (tid == 0 && !cur.whole() && cur.off == 0)
-      a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(a, run, cur));
+      kv_desc_put(a, run, cur);
   }
   __syncwarp();
   grid_launch_dependents();

@@ -574,7 +574,7 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
         if (tid == r) a.ml[at + r] = make_float2(m - 8.f, row(l, r));
       }
       if (threadIdx.x == 0 && cur.off == 0)
-        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(a, ctl->run.run, cur));
+        kv_desc_put(a, ctl->run.run, cur);
     }
     if (tiles > 0) named_bar_sync(bar, 128);  // the sums are read before the next item's are written
   }
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(Few<NR>::kThreads, Few<NR>::kCtasPerSm)
     tmem_relinquish();
   }
   grid_dependency_wait();
-  if (tid == 0 && a.n_ctas) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (tid == 0) kv_desc_none(a);
   kv_run<F::kThreads>(a, &ctl.run);
   tc_fence_before();
   __syncthreads();

@@ -579,7 +579,7 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
     } else {
       a.ml[part] = make_float2(m - kLift, l);
       if (threadIdx.x == 0 && cur.off == 0)
-        a.desc[blockIdx.x] = make_int4(cur.seq, cur.rt, cur.head, kv_last_cta(a, ctl->run.run, cur));
+        kv_desc_put(a, ctl->run.run, cur);
     }
   }
 }
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   grid_dependency_wait();
-  if (tid == 0 && a.n_ctas) a.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (tid == 0) kv_desc_none(a);
   kv_run<kThreads>(a, &ctl.run);
   tc_fence_before();
   __syncthreads();

@@ -235,6 +235,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 8 : 4) append_kerne
   if (tid == 0) *scale = s;
 }
 
+// A code and its scale to a value, both exact; each CTA keys and values of one
+// (page, head), whose loads are all in flight.  348160 tokens of 2 heads (535 MB):
+// 83 us, 6.5 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) read_kernel(const KvAppendArgs a) {
   __shared__ int part[kThreads / 32];

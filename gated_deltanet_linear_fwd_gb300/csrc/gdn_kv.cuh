@@ -401,7 +401,7 @@ cudaError_t launch_kv_read(const KvAppendArgs& a, bool f32, unsigned entries, cu
 cudaError_t launch_kv_attn_f32(const KvAttnArgs& a, unsigned grid, cudaStream_t st);  // fp32 q and out
 cudaError_t launch_kv_combine(const KvAttnArgs& a, bool f32, cudaStream_t st);
 cudaError_t kv_f32_setup();
-// rows: 8, 16 or 32 (KvAttnArgs::rows); kmap, vmap: the pools as [page and head][64][128 bytes]
+// rows: 8, 16, 24 or 32 (KvAttnArgs::rows); kmap, vmap: the pools as [page and head][64][128 bytes]
 cudaError_t launch_kv_attn_few(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, unsigned grid,
                                cudaStream_t st);
 cudaError_t kv_few_setup();

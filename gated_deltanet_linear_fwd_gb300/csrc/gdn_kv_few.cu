@@ -31,10 +31,10 @@
 // CTA with a deeper ring, whose warpgroups issue 40 % of all cycles: there a step of two
 // tiles halves what a step costs a row whatever its keys (the maximum, the
 // join, the waits).  32 sequences of 1000 to 8192 tokens, 8 heads, 20 rows:
-// 60 us (209 MB, 3.5 TB/s), 82 with steps of one tile; with one row tile of 32
+// 56 us (209 MB, 3.8 TB/s), 82 with steps of one tile; with one row tile of 32
 // instead of 24 it is 14 % more.  256 sequences of 32 to 32768 tokens, 2 heads, 4
-// rows: 109 us (629 MB, 5.8 TB/s) with steps of one tile, 119 with two, whose
-// second tile waits longer for HBM than it saves.
+// rows: 107 us (629 MB, 5.9 TB/s) with steps of one tile, some 8 more with two,
+// whose second tile waits longer for HBM than it saves.
 #include <cuda_fp16.h>
 
 #include "gdn_dev.cuh"

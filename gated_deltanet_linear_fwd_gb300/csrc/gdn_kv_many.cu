@@ -407,11 +407,19 @@ __device__ __forceinline__ float many_query(float scale_log2, const __nv_bfloat1
   return m < 0x7f800000u ? pow2f(ex) * fabsf(scale_log2) : __int_as_float(0x7fffffff);
 }
 
+// Where the epilogue keeps chunk c (16 bytes, of 16) of a warp's row: c < 8 in
+// the row's high query part, the others in its low one.
+__device__ __forceinline__ uint32_t stage_offset(int row, int c) {
+  return (c >> 3) * kTileBytes + sw128_offset(row, c & 7);
+}
+
 // The warp's 32 rows of O out of tensor memory: divided by l in bf16, or, for
 // a part of an item, as they are.  256 bytes of each row at a time go through
-// the warp's 8 KB of `stage`, so that a store covers 512 contiguous bytes (a
-// row a thread, it took 6000 cycles instead of 4000).  dst: this thread's row,
-// or null.
+// shared memory, so that a store covers 512 contiguous bytes (a row a thread,
+// it took 6000 cycles instead of 4000): through the bytes of the warp's own
+// query rows, 128 a row in either part's tile, which no product reads any more.
+// The other warps' next queries go to their own rows, so the warps need not
+// wait for one another.  dst: this thread's row, or null.
 __device__ __forceinline__ void many_output(uint32_t t_o, bool any, bool whole, float l, uint8_t* stage, uint8_t* dst) {
   const int lane = threadIdx.x & 31;
   const float inv = l == 0.f ? 0.f : 1.0f / l;
@@ -431,11 +439,11 @@ __device__ __forceinline__ void many_output(uint32_t t_o, bool any, bool whole, 
           w[k] = !any || l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          *reinterpret_cast<uint4*>(stage + lane * 256 + (((2 * c + k) ^ (lane & 7)) << 4)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+          *reinterpret_cast<uint4*>(stage + stage_offset(lane, 2 * c + k)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint4*>(stage + lane * 256 + (((4 * c + k) ^ (lane & 7)) << 4)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          *reinterpret_cast<uint4*>(stage + stage_offset(lane, 4 * c + k)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
     }
     __syncwarp();
@@ -444,7 +452,7 @@ __device__ __forceinline__ void many_output(uint32_t t_o, bool any, bool whole, 
     for (int k = 0; k < 16; ++k) {
       const int row = 2 * k + (lane >> 4);
       uint8_t* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), row));
-      const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 256 + ((c ^ (row & 7)) << 4));
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + stage_offset(row, c));
       if (to) reinterpret_cast<uint4*>(to + 256 * h)[c] = v;
     }
     __syncwarp();
@@ -575,10 +583,9 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
     const int64_t tok = it.tok0 + t;
     const size_t part = (size_t)cur.slot() * kRows + q * 128 + row;
     const bool whole = cur.whole();
-    // through the tile's queries in shared memory, which no product reads any more
     uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(reinterpret_cast<__nv_bfloat16*>(a.out) + tok * a.out_stride + (head0 + g) * kHeadDim)
                          : reinterpret_cast<uint8_t*>(a.o + part * kHeadDim);
-    many_output(t_o, tiles > 0, whole, l, sm + kOffQ + q * 2 * kTileBytes + warp * 8192, whole && !live ? nullptr : dst);
+    many_output(t_o, tiles > 0, whole, l, sm + kOffQ + q * 2 * kTileBytes + warp * 32 * kHeadDim, whole && !live ? nullptr : dst);
     tc_fence_before();
     if (whole) {
       if (live && a.lse) a.lse[tok * a.c.h_q + head0 + g] = kv_lse(m - kLift, l);

@@ -1,0 +1,41 @@
+"""The many-rows attention kernel over the 8-bit cache, on calls whose plan is
+checked to take it: items that follow one another in a CTA, and contents that
+only this kernel treats in its own way."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests import kv_util as U
+from tests.test_gpu_kv import check_attn, gdn, status, to_cache  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+def many_plan(gdn, b, h_q, ctas, **kw):  # noqa: F811
+    """A plan for many rows whose CTAs take runs of items (sized for longer sequences than there are)."""
+    p = gdn.gdn_kv_attn_plan(T=b.T, n_seqs=b.n, h_q=h_q, h_kv=b.h_kv, max_q_len=max(b.q_lens), max_kv_len=20000,
+                             sm_count=ctas, **kw)
+    assert (p.raw.path, p.raw.rows, p.raw.n_ctas) == (2, 256, ctas)
+    return p
+
+
+@pytest.mark.parametrize("q,kv,h_q,h_kv", [
+    ([300] * 3, [700, 300, 411], 8, 4),      # 600 rows: a last row tile of 88, one query tile, a warp without rows
+    ([300, 37, 90], [300, 60, 222], 7, 3),   # heads that do not divide: rows without a query in every warp
+    ([130] * 4, [130, 900, 131, 150], 16, 8)])
+@pytest.mark.parametrize("ctas", [1, 3, 7])
+def test_items_in_turn(gdn, q, kv, h_q, h_kv, ctas):  # noqa: F811
+    """Several items a CTA, every head with its own keys and queries: a warp that is done with an item early
+    writes its next queries while others still hand out their output."""
+    b = U.Batch(q, kv, h_kv, seed=ctas + h_q)
+    b.fill()
+    x = b.randn(b.T, h_q, 128)
+    plan = many_plan(gdn, b, h_q, ctas)
+    first = check_attn(gdn, b, h_q, BF, q=x, plan=plan)
+    cache, lens, table, cu = to_cache(gdn, b), b.lens.cuda(), b.table.cuda(), b.cu.cuda()
+    for _ in range(20):
+        out, lse = gdn.gdn_kv_attn(x.to(BF).cuda(), cache, lens, table, cu, plan=plan)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert status(gdn, cache) == (0, 0)

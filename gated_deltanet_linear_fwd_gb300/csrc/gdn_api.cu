@@ -900,7 +900,7 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
     // keys 14.2 and 11.1 (1 unit an SM), over 8192 keys 28.8 and 20.2 (8), over 65536 56
     // and 61 (55), prompts of 512 tokens 20.7 and 19.4 (9), 1024 tokens 28 and 33 (21).
     p.path = kKvPathFew;
-    p.rows = (int)std::min<int64_t>(32, (rows + 7) / 8 * 8);
+    p.rows = (int)std::min<int64_t>(32, std::max<int64_t>(8, (rows + 7) / 8 * 8));  // at least 8: a call may bring no tokens
     // measured: 64 sequences to 65536 tokens, 16 rows, 62.7 us at 3 and 58.5 at 8; 256 to 32768, 8 rows, 116 at 3,
     // 111 at 4 and 113 at 12
     p.item_cost = p.rows <= 8 ? 4 : 8;

@@ -392,7 +392,9 @@ __device__ __forceinline__ float many_query(float scale_log2, const __nv_bfloat1
   const uint32_t m = max(m2 << 16, m2 & 0xffff0000u);
   // below 2^-102 a row's scores are zero for any key the cache can hold
   const int ex = m < 0x7f800000u ? e4m3_scale_exp(m, -110) : 0;
-  const float inv = scale_log2 < 0.f ? -pow2f(-ex) : pow2f(-ex);  // the row's factor stays positive
+  // The row's factor stays positive and finite.  A row that is not finite becomes
+  // NaN codes: its scores are NaN, and those under a mask -inf like any other's.
+  const float inv = m >= 0x7f800000u ? __int_as_float(0x7fffffff) : scale_log2 < 0.f ? -pow2f(-ex) : pow2f(-ex);
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const uint32_t w[8] = {x[2 * c].x, x[2 * c].y, x[2 * c].z, x[2 * c].w, x[2 * c + 1].x, x[2 * c + 1].y, x[2 * c + 1].z, x[2 * c + 1].w};
@@ -403,8 +405,7 @@ __device__ __forceinline__ float many_query(float scale_log2, const __nv_bfloat1
     *reinterpret_cast<uint4*>(hi_tile + at) = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
     *reinterpret_cast<uint4*>(hi_tile + kTileBytes + at) = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16, lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
   }
-  // a row that is not finite gives NaN
-  return m < 0x7f800000u ? pow2f(ex) * fabsf(scale_log2) : __int_as_float(0x7fffffff);
+  return pow2f(ex) * fabsf(scale_log2);
 }
 
 // Where the epilogue keeps chunk c (16 bytes, of 16) of a warp's row: c < 8 in
@@ -532,7 +533,7 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
       tmem_ld_done(s0);
       tmem_ld_done(s1);
       tmem_ld_done(s2);
-      // s is -inf only under a mask, and the factors are positive unless the row is NaN
+      // s is -inf only under a mask, and the factors are positive
       float top0 = max32(s0);
       tmem_ld32(t_s + 96, s0);
       top0 = fmaxf(top0, max32(s1));

@@ -39,3 +39,22 @@ def test_items_in_turn(gdn, q, kv, h_q, h_kv, ctas):  # noqa: F811
         out, lse = gdn.gdn_kv_attn(x.to(BF).cuda(), cache, lens, table, cu, plan=plan)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     assert status(gdn, cache) == (0, 0)
+
+
+@pytest.mark.parametrize("what", [float("inf"), -float("inf"), float("nan")])
+def test_bad_queries_without_keys(gdn, what):  # noqa: F811
+    """Queries that are not finite are NaN where they have a key, and zeros like any other where they have none."""
+    b = U.Batch([200, 150], [60, 400], 2, seed=5)  # the first sequence's first 140 tokens lie before position 0
+    b.fill()
+    q = b.randn(b.T, 8, 128)
+    q[::3, :, 5] = what
+    cache = to_cache(gdn, b)
+    plan = many_plan(gdn, b, 8, 5)
+    out, lse = gdn.gdn_kv_attn(q.to(BF).cuda(), cache, b.lens.cuda(), b.table.cuda(), b.cu.cuda(), plan=plan)
+    assert (out[:140] == 0).all() and (lse[:140] == -float("inf")).all()
+    bad = torch.zeros(b.T, dtype=torch.bool)
+    bad[::3] = True
+    bad[:140] = False
+    assert torch.equal(out.isnan().all(-1).cpu(), bad[:, None].expand(-1, 8))
+    assert torch.equal(out.isnan().any(-1).cpu(), bad[:, None].expand(-1, 8))
+    assert torch.equal(lse.isnan().cpu(), bad[:, None].expand(-1, 8))

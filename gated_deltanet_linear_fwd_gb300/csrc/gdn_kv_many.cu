@@ -345,6 +345,7 @@ __device__ __forceinline__ float2 add2(float2 a, float b0, float b1) {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLazy = 12.f, kLift = 3.f;
+constexpr float kLeastFactor = 0x1p-126f;
 
 // Under the masks: -inf for keys outside [lo, hi) of these 32, NaN for keys
 // whose values hold one.
@@ -528,8 +529,12 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
         tmem_ld32(t_s + 64, s2);
       }
       // log2 of the value scales, powers of two
-      const float fk0 = f * sc.x, ev0 = (float)((int)(__float_as_uint(sc.z) >> 23) - 127);
-      const float fk1 = f * sc.y, ev1 = (float)((int)(__float_as_uint(sc.w) >> 23) - 127);
+      // The factors have to stay above zero: masked scores are -inf before they
+      // meet them.  The product underflows for a tiny or zero query over a page
+      // of tiny or zero keys (2^-113 2^-40); 2^-126 in its place keeps those
+      // scores, at most 2^26 before it, below 2^-100.
+      const float fk0 = fmaxf(f * sc.x, kLeastFactor), ev0 = (float)((int)(__float_as_uint(sc.z) >> 23) - 127);
+      const float fk1 = fmaxf(f * sc.y, kLeastFactor), ev1 = (float)((int)(__float_as_uint(sc.w) >> 23) - 127);
       tmem_ld_done(s0);
       tmem_ld_done(s1);
       tmem_ld_done(s2);

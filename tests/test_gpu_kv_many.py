@@ -14,10 +14,10 @@ BF = torch.bfloat16
 
 
 def many_plan(gdn, b, h_q, ctas, **kw):  # noqa: F811
-    """A plan for many rows whose CTAs take runs of items (sized for longer sequences than there are)."""
+    """A plan for many rows, without a window one whose CTAs take runs of items (sized for longer sequences than there are)."""
     p = gdn.gdn_kv_attn_plan(T=b.T, n_seqs=b.n, h_q=h_q, h_kv=b.h_kv, max_q_len=max(b.q_lens), max_kv_len=20000,
                              sm_count=ctas, **kw)
-    assert (p.raw.path, p.raw.rows, p.raw.n_ctas) == (2, 256, ctas)
+    assert (p.raw.path, p.raw.rows, p.raw.n_ctas) == (2, 256, 0 if kw.get("window") else ctas)
     return p
 
 
@@ -58,3 +58,34 @@ def test_bad_queries_without_keys(gdn, what):  # noqa: F811
     assert torch.equal(out.isnan().all(-1).cpu(), bad[:, None].expand(-1, 8))
     assert torch.equal(out.isnan().any(-1).cpu(), bad[:, None].expand(-1, 8))
     assert torch.equal(lse.isnan().cpu(), bad[:, None].expand(-1, 8))
+
+
+@pytest.mark.parametrize("tiny", [0.0, 1e-30])
+@pytest.mark.parametrize("window", [0, 100])
+def test_zero_queries_over_zero_keys(gdn, tiny, window):  # noqa: F811
+    """Every key weighs the same, whatever scale a page of zeros has (2^-40, the least there is)."""
+    b = U.Batch([200, 300], [200, 700], 2, seed=3)
+    b.fill()
+    for i in (0, 1):
+        pages = b.table[i, :3 if i else 2].long()  # of the second sequence, the first keys only
+        b.k[pages], b.ks[pages] = 0.0, 2.0 ** -40
+    q = b.randn(b.T, 8, 128)
+    q[:250] = tiny
+    check_attn(gdn, b, 8, BF, q=q, window=window, plan=many_plan(gdn, b, 8, 5, window=window))
+
+
+def test_zero_prompt(gdn):  # noqa: F811
+    """A prompt of zeros through append and attention, as a warm-up sends it, under the call's own plan."""
+    n = 512
+    b = U.Batch([n], [n], 2, seed=1)
+    b.fill(stale_nan=False)
+    b.v, b.vs = b.randn(b.n_pages, 2, 64, 128).to(torch.float8_e4m3fn).float(), torch.ones(b.n_pages, 2)
+    assert gdn.gdn_kv_attn_plan(T=n, n_seqs=1, h_q=8, h_kv=2, max_pages=b.max_pages).raw.path == 2
+    cache, lens, table = to_cache(gdn, b), b.lens.cuda(), b.table.cuda()
+    zero = torch.zeros(n, 2, 128, dtype=BF, device="cuda")
+    gdn.gdn_kv_append(cache, zero, zero, lens, table)
+    assert (cache.k_scale[b.table[0].long()] == 2.0 ** -40).all()
+    out, lse = gdn.gdn_kv_attn(torch.zeros(n, 8, 128, dtype=BF, device="cuda"), cache, lens, table)
+    assert (out == 0).all()
+    want = torch.log(torch.arange(1, n + 1, dtype=torch.float64))[:, None].cuda()
+    assert (lse.double() - want).abs().max() <= 2.0 ** -16

@@ -322,7 +322,11 @@ def _kv_rows(name: str, t: torch.Tensor, heads: int) -> int:
     s = t.stride()
     if s[2] != 1 or (s[1] != t.size(2) and heads > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return s[0] if t.size(0) > 1 else 0
+    if t.size(0) <= 1:
+        return 0
+    if s[0] < heads * t.size(2):  # an expanded view's 0 would select packed tokens, past the end of what lies behind it
+        raise ValueError(f"{name}: tokens must not overlap")
+    return s[0]
 
 
 def _kv_ints(kv_lens: torch.Tensor, page_table: torch.Tensor, cu_seqlens: Optional[torch.Tensor]):

@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import pytest
+import torch
 
 from tests.test_kv_host import INVALID, OK, cache, dims, lib, plan  # noqa: F401
 
@@ -14,3 +15,83 @@ def test_no_tokens(lib, dtype, max_kv):  # noqa: F811
     assert st == OK and p.rows >= 8 and p.max_row_tiles == 1
     assert lib.gdn_kv_attn(None, 64, 64, None, cache(), None, None, dims(T=0, max_pages=2000, dtype=dtype), p, 4096,
                            p.workspace_bytes, None) == OK
+
+
+# ---------------------------------------------------------------- the binding, with a library that only takes note of calls
+class OnGpu(torch.Tensor):
+    """A host tensor that says it lies on GPU 0."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+class Calls:
+    def __init__(self):
+        self.made = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.made.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    from gated_deltanet_linear_fwd_gb300 import _lib, api
+    c = Calls()
+    monkeypatch.setattr(_lib, "load", lambda: c)
+    monkeypatch.setattr(api, "_raw_stream", lambda stream, t: 0)
+    return c
+
+
+def gpu(t):
+    return t.as_subclass(OnGpu)
+
+
+def batch(n=2, each=32, h_q=8, h_kv=2):
+    """(cache, q, k, lens, table, offsets) as a user would have them on the GPU."""
+    import gated_deltanet_linear_fwd_gb300 as gdn
+    codes = lambda: gpu(torch.zeros(4, h_kv, 64, 128, dtype=torch.uint8).view(torch.float8_e4m3fn))  # noqa: E731
+    c = gdn.KVCache(codes(), codes(), gpu(torch.ones(4, h_kv)), gpu(torch.ones(4, h_kv)))
+    i32 = lambda *x: gpu(torch.tensor(x, dtype=torch.int32))  # noqa: E731
+    T = n * each
+    return (c, gpu(torch.zeros(T, h_q, 128, dtype=torch.bfloat16)), gpu(torch.zeros(T, h_kv, 128, dtype=torch.bfloat16)),
+            i32(*[each] * n), i32(*range(2 * n)).view(n, 2), i32(*range(0, T + 1, each)))
+
+
+def test_accepted(calls):
+    import gated_deltanet_linear_fwd_gb300 as gdn
+    c, q, k, lens, table, cu = batch()
+    gdn.gdn_kv_append(c, k, k, lens, table, cu)
+    gdn.gdn_kv_read(c, lens, table, cu, k_out=k, v_out=k)
+    assert [name for name, _ in calls.made] == ["gdn_kv_append", "gdn_kv_read"]
+    wide = gpu(torch.zeros(64, 12, 128, dtype=torch.bfloat16))
+    gdn.gdn_kv_append(c, wide[:, 8:10], wide[:, 10:], lens, table, cu)
+    dims = calls.made[-1][1][6]
+    assert (dims.k_stride, dims.v_stride) == (12 * 128, 12 * 128)
+    one = gpu(torch.zeros(1, 1, 128, dtype=torch.bfloat16)).expand(2, 2, 128)[:1]  # a single token has no stride
+    with pytest.raises(ValueError):
+        gdn.gdn_kv_append(c, one, one, lens, table)  # but its heads have
+
+
+def overlapping(h):
+    """[64, h, 128] views whose tokens share memory."""
+    yield gpu(torch.zeros(1, h, 128, dtype=torch.bfloat16)).expand(64, h, 128)
+    yield gpu(torch.zeros(64 * h * 128, dtype=torch.bfloat16)).as_strided((64, h, 128), (64, 128, 1))
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_overlapping_tokens_refused(calls, which):
+    """A token stride below heads * 128: 0 would read as "packed", past the end of the memory behind it."""
+    import gated_deltanet_linear_fwd_gb300 as gdn
+    c, q, k, lens, table, cu = batch()
+    bad_k, bad_q = list(overlapping(2))[which], list(overlapping(8))[which]
+    for call in (lambda: gdn.gdn_kv_append(c, bad_k, k, lens, table, cu), lambda: gdn.gdn_kv_append(c, k, bad_k, lens, table, cu),
+                 lambda: gdn.gdn_kv_read(c, lens, table, cu, k_out=bad_k, v_out=k),
+                 lambda: gdn.gdn_kv_read(c, lens, table, cu, k_out=k, v_out=bad_k),
+                 lambda: gdn.gdn_kv_attn(bad_q, c, lens, table, cu), lambda: gdn.gdn_kv_attn(q, c, lens, table, cu, out=bad_q)):
+        with pytest.raises(ValueError):
+            call()
+    assert not [name for name, _ in calls.made if name != "gdn_kv_attn_plan"]

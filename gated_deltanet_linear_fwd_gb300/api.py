@@ -300,6 +300,9 @@ class KVCache:
                 raise ValueError(f"{name} must be contiguous {dt}")
         if k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
             raise ValueError("k_scale and v_scale must be [n_pages, h_kv]")
+        self.device_index = k.get_device()  # negative: not on a GPU, and of no use to the operators
+        if not v.get_device() == k_scale.get_device() == v_scale.get_device() == self.device_index:
+            raise ValueError("k, v, k_scale and v_scale must be on one device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.status = torch.zeros(2, dtype=torch.int32, device=k.device)
         self.raw = L.gdn_kv_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
@@ -313,10 +316,10 @@ class KVCache:
         return cls(codes(), codes(), scale(), scale())
 
 
-def _kv_rows(name: str, t: torch.Tensor, heads: int) -> int:
+def _kv_rows(name: str, t: torch.Tensor, heads: int, cache: KVCache) -> int:
     """Token stride of a [T, heads, 128] tensor whose tokens are whole; 0 when it is packed."""
-    if not t.is_cuda or t.dim() != 3 or t.size(1) != heads:
-        raise ValueError(f"{name} must be a CUDA tensor [T, {heads}, 128]")
+    if t.get_device() != cache.device_index or t.dim() != 3 or t.size(1) != heads:
+        raise ValueError(f"{name} must be a tensor [T, {heads}, 128] on the cache's device")
     if t.is_contiguous():
         return 0
     s = t.stride()
@@ -329,23 +332,32 @@ def _kv_rows(name: str, t: torch.Tensor, heads: int) -> int:
     return s[0]
 
 
-def _kv_ints(kv_lens: torch.Tensor, page_table: torch.Tensor, cu_seqlens: Optional[torch.Tensor]):
+def _kv_ints(cache: KVCache, kv_lens: torch.Tensor, page_table: torch.Tensor, cu_seqlens: Optional[torch.Tensor]):
+    """(sequences, row length of the table, address of the offsets), of tensors the kernels may read."""
+    dev = cache.device_index
+    if dev < 0:
+        raise ValueError("the cache must be on a GPU")
+    if kv_lens.dtype != torch.int32 or page_table.dtype != torch.int32 or not kv_lens.get_device() == page_table.get_device() == dev:
+        raise ValueError("kv_lens and page_table must be int32 tensors on the cache's device")
     n = kv_lens.shape[0]
-    if kv_lens.dtype != torch.int32 or page_table.dtype != torch.int32 or not kv_lens.is_cuda:
-        raise ValueError("kv_lens and page_table must be int32 CUDA tensors")
     if page_table.dim() != 2 or page_table.shape[0] != n or not page_table.is_contiguous() or not kv_lens.is_contiguous():
         raise ValueError("page_table must be contiguous [n_seqs, max_pages]")
     if cu_seqlens is None:
         return n, page_table.shape[1], None
-    if cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (n + 1,) or not cu_seqlens.is_contiguous():
-        raise ValueError("cu_seqlens must be contiguous int32 [n_seqs + 1]")
+    if (cu_seqlens.dtype != torch.int32 or cu_seqlens.shape != (n + 1,) or not cu_seqlens.is_contiguous()
+            or cu_seqlens.get_device() != dev):
+        raise ValueError("cu_seqlens must be contiguous int32 [n_seqs + 1] on the cache's device")
     return n, page_table.shape[1], cu_seqlens.data_ptr()
 
 
 def _raw_stream(stream, t: torch.Tensor) -> int:
     """The stream's handle; by default the current one of t's device, without a
-    Stream object around it (a microsecond of a call that takes eight)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+    Stream object around it (a microsecond of a call that takes eight).  The
+    kernels run on the current device, which t has to be on."""
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError("the tensors must be on the current device")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _kv_empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
@@ -362,9 +374,9 @@ def gdn_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_lens: tor
     bf16 or fp32, packed over the sequences by cu_seqlens (None: T / n_seqs
     each); kv_lens int32 [n_seqs] counts the new tokens too.  k and v may be
     views with a larger token stride (parts of one projection's output)."""
-    n, max_pages, cu = _kv_ints(kv_lens, page_table, cu_seqlens)
+    n, max_pages, cu = _kv_ints(cache, kv_lens, page_table, cu_seqlens)
     h_kv = cache.raw.h_kv
-    ks, vs = _kv_rows("k", k, h_kv), _kv_rows("v", v, h_kv)
+    ks, vs = _kv_rows("k", k, h_kv, cache), _kv_rows("v", v, h_kv, cache)
     if v.dtype != k.dtype or v.shape != k.shape or k.shape[2] != 128:
         raise ValueError("k and v must be alike, with 128 elements a head")
     dims = L.gdn_kv_dims(n, k.shape[0], h_kv, max_pages, 1, 0, 0.0, _DT.get(k.dtype, -1), 0, ks, vs, 0)
@@ -380,7 +392,7 @@ def gdn_kv_read(cache: KVCache, kv_lens: torch.Tensor, page_table: torch.Tensor,
     """The cache's values of the last n_i tokens of each sequence (gdn_kv_read),
     exact in bf16 or fp32: (k, v), each [T, h_kv, 128].  T: their number over
     all sequences, when no outputs are given."""
-    n, max_pages, cu = _kv_ints(kv_lens, page_table, cu_seqlens)
+    n, max_pages, cu = _kv_ints(cache, kv_lens, page_table, cu_seqlens)
     h_kv = cache.raw.h_kv
     if k_out is None or v_out is None:
         if T is None:
@@ -388,7 +400,7 @@ def gdn_kv_read(cache: KVCache, kv_lens: torch.Tensor, page_table: torch.Tensor,
         shape = (T, h_kv, 128)
         k_out = _kv_empty(shape, dtype, cache.k.device, stream) if k_out is None else k_out
         v_out = _kv_empty(shape, dtype, cache.k.device, stream) if v_out is None else v_out
-    ks, vs = _kv_rows("k_out", k_out, h_kv), _kv_rows("v_out", v_out, h_kv)
+    ks, vs = _kv_rows("k_out", k_out, h_kv, cache), _kv_rows("v_out", v_out, h_kv, cache)
     if v_out.dtype != k_out.dtype or v_out.shape != k_out.shape or k_out.shape[2] != 128:
         raise ValueError("k_out and v_out must be alike, with 128 elements a head")
     dims = L.gdn_kv_dims(n, k_out.shape[0], h_kv, max_pages, 1, 0, 0.0, _DT.get(k_out.dtype, -1), 0, ks, vs, 0)
@@ -434,9 +446,9 @@ def gdn_kv_attn(q: torch.Tensor, cache: KVCache, kv_lens: torch.Tensor, page_tab
     and v, which go into the cache first.  Returns (out [T, h_q, 128],
     lse [T, h_q] fp32 or None).  causal, window, scale and the bounds are the
     plan's when one is given; a plan holds for calls of the same sizes."""
-    n, max_pages, cu = _kv_ints(kv_lens, page_table, cu_seqlens)
+    n, max_pages, cu = _kv_ints(cache, kv_lens, page_table, cu_seqlens)
     T, h_q, d = q.shape
-    qs = _kv_rows("q", q, h_q)
+    qs = _kv_rows("q", q, h_q, cache)
     if d != 128:
         raise ValueError("q must have 128 elements a head")
     if plan is None:
@@ -450,12 +462,15 @@ def gdn_kv_attn(q: torch.Tensor, cache: KVCache, kv_lens: torch.Tensor, page_tab
     if lse is None:
         if return_lse:
             lse = _kv_empty((T, h_q), torch.float32, q.device, stream)
-    elif lse.dtype != torch.float32 or lse.shape != (T, h_q) or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous float32 [T, h_q]")
+    elif (lse.dtype != torch.float32 or lse.shape != (T, h_q) or not lse.is_contiguous()
+          or lse.get_device() != cache.device_index):
+        raise ValueError("lse must be contiguous float32 [T, h_q] on the cache's device")
     if workspace is None:
         workspace = _kv_empty(max(plan.workspace_bytes, 256), torch.uint8, q.device, stream)
+    elif workspace.get_device() != cache.device_index or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on the cache's device")
     dims = L.gdn_kv_dims(n, T, h_q, max_pages, int(plan.causal), plan.window, plan.scale, _DT.get(q.dtype, -1), qs, 0, 0,
-                         _kv_rows("out", out, h_q))
+                         _kv_rows("out", out, h_q, cache))
     st = L.load().gdn_kv_attn(q.data_ptr(), kv_lens.data_ptr(), page_table.data_ptr(), cu, cache.raw, out.data_ptr(),
                               None if lse is None else lse.data_ptr(), dims, plan.raw, workspace.data_ptr(),
                               workspace.numel(), _raw_stream(stream, q))

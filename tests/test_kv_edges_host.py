@@ -95,3 +95,39 @@ def test_overlapping_tokens_refused(calls, which):
         with pytest.raises(ValueError):
             call()
     assert not [name for name, _ in calls.made if name != "gdn_kv_attn_plan"]
+
+
+def test_tensors_elsewhere_refused(calls):
+    """Every tensor of a call lies on the cache's device, a GPU; a workspace is all there."""
+    import gated_deltanet_linear_fwd_gb300 as gdn
+    c, q, k, lens, table, cu = batch()
+    host = lambda t: torch.Tensor.as_subclass(t, torch.Tensor)  # noqa: E731
+    lse, ws = gpu(torch.zeros(64, 8)), gpu(torch.zeros(512, dtype=torch.uint8))
+    good = dict(q=q, k=k, lens=lens, table=table, cu=cu, lse=lse, workspace=ws, out=q, k_out=k)
+
+    def run(**kw):
+        a = {**good, **kw}
+        for fn in (lambda: gdn.gdn_kv_append(c, a["k"], a["k_out"], a["lens"], a["table"], a["cu"]),
+                   lambda: gdn.gdn_kv_read(c, a["lens"], a["table"], a["cu"], k_out=a["k"], v_out=a["k_out"]),
+                   lambda: gdn.gdn_kv_attn(a["q"], c, a["lens"], a["table"], a["cu"], out=a["out"], lse=a["lse"],
+                                           workspace=a["workspace"])):
+            calls.made.clear()
+            try:
+                fn()
+                yield True
+            except ValueError:
+                assert not [name for name, _ in calls.made if name != "gdn_kv_attn_plan"]
+                yield False
+
+    assert list(run()) == [True] * 3
+    for name, used in (("lens", (1, 1, 1)), ("table", (1, 1, 1)), ("cu", (1, 1, 1)), ("k", (1, 1, 0)), ("k_out", (1, 1, 0)),
+                       ("q", (0, 0, 1)), ("out", (0, 0, 1)), ("lse", (0, 0, 1)), ("workspace", (0, 0, 1))):
+        assert list(run(**{name: host(good[name])})) == [not u for u in used], name
+    assert list(run(workspace=ws[:1].expand(512))) == [True, True, False]
+    for i in range(4):  # a cache with one tensor on the host
+        parts = [c.k, c.v, c.k_scale, c.v_scale]
+        parts[i] = host(parts[i])
+        with pytest.raises(ValueError):
+            gdn.KVCache(*parts)
+    c = gdn.KVCache(*map(host, (c.k, c.v, c.k_scale, c.v_scale)))
+    assert list(run()) == [False] * 3

@@ -94,6 +94,10 @@ __device__ __forceinline__ int kv_page(const KvArgs& a, int s, int slot) {
   return -1;
 }
 
+// The first key that a window leaves a token at position p; p may be negative
+// and the window any positive number.
+__device__ __forceinline__ int kv_window_begin(int p, int window) { return window > 0 && p >= window ? p - window + 1 : 0; }
+
 // Query heads of key/value head h: those j with floor(j h_kv / h_q) = h.
 __device__ __forceinline__ int kv_first_q_head(const KvArgs& a, int h) {
   return (int)(((unsigned)h * (unsigned)a.h_q + (unsigned)a.h_kv - 1u) / (unsigned)a.h_kv);  // heads are at most 65535
@@ -167,7 +171,7 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs& a, int seq, int rt) 
   }
   const int past = s.len - s.n;  // position of the first new token; negative for idle slots
   const int hi = a.causal ? min(max(past + t1 + 1, 0), s.len) : s.len;
-  const int lo = a.window > 0 ? max(0, past + t0 - a.window + 1) : 0;
+  const int lo = kv_window_begin(past + t0, a.window);
   it.first_tile = lo / kKvTile;
   it.tiles = hi > lo ? (hi + kKvTile - 1) / kKvTile - it.first_tile : 0;
   return it;

@@ -154,10 +154,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const __grid_cons
     const bool idle = (warp & 3) * 32 >= rows;  // no row of this warp
     const int p = past + t;
     const int key_hi = live ? (a.causal ? min(max(p + 1, 0), it.len) : it.len) : 0;
-    const int key_lo = a.window > 0 ? max(0, p - a.window + 1) : 0;
+    const int key_lo = kv_window_begin(p, a.window);
     // tiles within every live row's keys need no mask
     const int t0 = r0 / a.group, t1 = min(it.n - 1, (r0 + kRows - 1) / a.group);
-    const int all_lo = a.window > 0 ? past + t1 - a.window + 1 : 0, all_hi = a.causal ? min(past + t0 + 1, it.len) : it.len;
+    const int all_lo = kv_window_begin(past + t1, a.window), all_hi = a.causal ? min(past + t0 + 1, it.len) : it.len;
     auto masked = [&](int j) {
       const int k0 = (cur.tile_begin() + j) * kKvTile;
       return k0 < all_lo || k0 + kKvTile > all_hi;

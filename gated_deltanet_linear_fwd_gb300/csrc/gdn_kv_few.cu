@@ -344,7 +344,7 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
           const int p = past + t;
           // a row that is not finite gives NaN
           ctl->f[row0 + r] = m < 0x7f800000u ? pow2f(ex) * a.scale_log2 : __int_as_float(0x7fffffff);
-          ctl->key_lo[row0 + r] = a.window > 0 ? max(0, p - a.window + 1) : 0;
+          ctl->key_lo[row0 + r] = kv_window_begin(p, a.window);
           ctl->key_hi[row0 + r] = live ? (a.causal ? min(max(p + 1, 0), it.len) : it.len) : 0;
         }
       }
@@ -354,7 +354,7 @@ __device__ __forceinline__ void few_softmax(const KvAttnArgs& a, FewCtl<NR>* ctl
     }
     // tiles that lie within every live row's keys need no mask
     const int t0 = cur.rt * NR / a.group, t1 = min(it.n - 1, (cur.rt * NR + NR - 1) / a.group);
-    const int all_lo = a.window > 0 ? past + t1 - a.window + 1 : 0, all_hi = a.causal ? min(past + t0 + 1, it.len) : it.len;
+    const int all_lo = kv_window_begin(past + t1, a.window), all_hi = a.causal ? min(past + t0 + 1, it.len) : it.len;
     const bool dead = cur.rt * NR + row0 >= it.n * a.group;  // no row of this warpgroup: its columns may hold anything
     float m = kNegInf;  // running maximum of row lane % R
     // by pairs of rows: this key's part of the sums; column tid of the output, up to the step before last

@@ -79,7 +79,7 @@ __device__ __forceinline__ ManyItem many_item(const KvAttnArgs& a, const KvCurso
   ManyItem m;
   const int r0 = c.rt * kRows, t0 = r0 / a.group, t1 = min(c.it.n - 1, (r0 + kRows - 1) / a.group);
   m.past = c.it.len - c.it.n;
-  m.all_lo = a.window > 0 ? m.past + t1 - a.window + 1 : 0;
+  m.all_lo = kv_window_begin(m.past + t1, a.window);
   m.all_hi = a.causal ? min(m.past + t0 + 1, c.it.len) : c.it.len;
   m.q_tiles = c.it.n * a.group - r0 > 128 ? 2 : 1;
   return m;
@@ -508,7 +508,7 @@ __device__ __forceinline__ void many_softmax(const KvAttnArgs& a, ManyCtl* ctl, 
       int lo = 0, hi = 0;
       if (masked) {
         const int p = mi.past + t;
-        lo = (a.window > 0 ? max(0, p - a.window + 1) : 0) - key0;
+        lo = kv_window_begin(p, a.window) - key0;
         hi = (live ? (a.causal ? min(p + 1, it.len) : it.len) : 0) - key0;
       }
       if (masked) {

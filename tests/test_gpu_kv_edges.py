@@ -26,3 +26,21 @@ def test_no_tokens(gdn, dtype, offsets):  # noqa: F811
     out, lse = gdn.gdn_kv_attn(torch.empty(0, 8, 128, dtype=dtype, device="cuda"), cache, lens, table, cu)
     assert k.shape == v.shape == (0, 2, 128) and out.shape == (0, 8, 128) and lse.shape == (0, 8)
     assert torch.equal(before, cache.k.view(torch.uint8)) and status(gdn, cache) == (0, 0)
+
+
+@pytest.mark.parametrize("dtype,n,window", [(BF, 5, 2 ** 31 - 1), (F32, 5, 2 ** 31 - 1), (BF, 200, 2 ** 31 - 1), (BF, 200, 2 ** 31 - 60),
+                                            (F32, 200, 2 ** 31 - 60), (BF, 40, 2 ** 31 - 2)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_widest_windows(gdn, dtype, n, window, causal):  # noqa: F811
+    """A window that bounds nothing, with tokens before position 0: the same as no window."""
+    b = U.Batch([n, n], [n // 2, 0], 2, seed=n)
+    b.fill()
+    cache, q = to_cache(gdn, b), b.randn(b.T, 8, 128).to(dtype).cuda()
+    for sms in (152, 4):  # for 200 tokens on 4 SMs the kernel for many rows
+        plans = [gdn.gdn_kv_attn_plan(T=b.T, n_seqs=2, h_q=8, h_kv=2, max_q_len=n, max_kv_len=n, dtype=dtype, causal=causal,
+                                      window=w, sm_count=sms) for w in (0, window)]
+        assert plans[0].raw.path == plans[1].raw.path == (0 if dtype == F32 else 2 if n * 4 > 32 and sms == 4 else 1)
+        want, got = (gdn.gdn_kv_attn(q, cache, b.lens.cuda(), b.table.cuda(), plan=p) for p in plans)
+        assert (want[1][n // 2 + n % 2:n] > -1e30).all()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert status(gdn, cache) == (0, 0)

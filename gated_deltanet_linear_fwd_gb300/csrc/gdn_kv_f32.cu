@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const __grid_cons
           fetch(kc, a.c.k);
           fetch_pages(j + 3);
         }
-        if (!bad) bad = !kv_wait(&ctl.s_full, par, &ctl.abort, 100 + kBarS);
+        // a warp's lanes agree on what they waited for: its tensor-memory accesses are the whole warp's
+        bad |= !kv_wait_warp([&] { return kv_wait(&ctl.s_full, par, &ctl.abort, 100 + kBarS); });
         tc_fence_after();
         const float ev = (float)((int)(__float_as_uint(sv) >> 23) - 127);  // log2 of a power of two
         const float inv_sv = __int_as_float((254 << 23) - __float_as_int(sv));
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_f32_kernel(const __grid_cons
           __syncwarp();
         }
         // values of the next tile, in registers until this tile's product has read its own; then on to the codes after
-        bad = !kv_wait(&ctl.o_full, par, &ctl.abort, 100 + kBarO);
+        bad = !kv_wait_warp([&] { return kv_wait(&ctl.o_full, par, &ctl.abort, 100 + kBarO); });
         par ^= 1;
         tc_fence_after();
         if (j + 1 < tiles) {

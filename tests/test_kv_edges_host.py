@@ -1,10 +1,15 @@
 """Refusals and edges of the 8-bit key/value cache's host side (no GPU)."""
 from __future__ import annotations
 
+import os
+import re
+
 import pytest
 import torch
 
 from tests.test_kv_host import INVALID, OK, cache, dims, lib, plan  # noqa: F401
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gated_deltanet_linear_fwd_gb300", "csrc")
 
 
 @pytest.mark.parametrize("dtype", [0, 1])
@@ -131,3 +136,21 @@ def test_tensors_elsewhere_refused(calls):
             gdn.KVCache(*parts)
     c = gdn.KVCache(*map(host, (c.k, c.v, c.k_scale, c.v_scale)))
     assert list(run()) == [False] * 3
+
+
+@pytest.mark.parametrize("name", ["gdn_kv_f32.cu", "gdn_kv_few.cu", "gdn_kv_many.cu"])
+def test_waits_agree_by_warp(name):
+    """Tensor-memory accesses are a whole warp's.  A bounded wait may give up in some lanes only, which no
+    GPU test can bring about without a wait that runs out; so each one stands within kv_wait_warp."""
+    with open(os.path.join(CSRC, name)) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    while "kv_wait_warp(" in text:
+        at = text.index("kv_wait_warp(")
+        end = at + len("kv_wait_warp(")
+        depth = 1
+        while depth:
+            depth += {"(": 1, ")": -1}.get(text[end], 0)
+            end += 1
+        assert "kv_wait(" in text[at:end]
+        text = text[:at] + text[end:]
+    assert "kv_wait(" not in text

@@ -427,7 +427,8 @@ def gdn_kv_attn_plan(*, T: int, n_seqs: int, h_q: int, h_kv: int, max_q_len: int
                      max_pages: int = 0, dtype: torch.dtype = torch.bfloat16, causal: bool = True, window: int = 0,
                      scale: float = 0.0, sm_count: int = 0) -> KVPlan:
     """Host-only planning of gdn_kv_attn.  max_q_len: the most tokens a sequence
-    brings (0: T); max_kv_len: the longest sequence expected (0: 64 max_pages)."""
+    brings (0: any number, planned as T / n_seqs); max_kv_len: the longest
+    sequence expected (0: 64 max_pages)."""
     if not max_pages:
         max_pages = max(1, -(-max_kv_len // L.GDN_KV_PAGE))
     dims = L.gdn_kv_dims(n_seqs, T, h_q, max_pages, int(causal), window, scale, _DT.get(dtype, -1), 0, 0, 0, 0)
@@ -453,7 +454,7 @@ def gdn_kv_attn(q: torch.Tensor, cache: KVCache, kv_lens: torch.Tensor, page_tab
         raise ValueError("q must have 128 elements a head")
     if plan is None:
         plan = gdn_kv_attn_plan(T=T, n_seqs=n, h_q=h_q, h_kv=cache.raw.h_kv,
-                                max_q_len=max_q_len or (T // n if cu is None else T), max_kv_len=max_kv_len,
+                                max_q_len=max_q_len or (0 if cu is not None else T // max(n, 1)), max_kv_len=max_kv_len,
                                 max_pages=max_pages, dtype=q.dtype, causal=causal, window=window, scale=scale)
     if out is None:
         out = _kv_empty(q.shape, q.dtype, q.device, stream)

@@ -392,6 +392,11 @@ int64_t kv_join_tiles(int path, int64_t tiles, bool one_tile) {
   if (one_tile) return path == kKvPathMany ? 2 : path == kKvPathFew ? 4 : 1;
   return path == kKvPathMany ? std::min<int64_t>(28, 12 + tiles / 4) : path == kKvPathFew ? 8 : 3;
 }
+// Row tiles of a call: no sequence has more than max_row_tiles, and all of them
+// no more than their tokens fill with one started tile each.
+int64_t kv_most_row_tiles(int n_seqs, int T, int group, int rows, int max_row_tiles) {
+  return std::min<int64_t>((int64_t)n_seqs * max_row_tiles, (int64_t)T * group / rows + n_seqs);
+}
 constexpr int kKvMaxParts = 32;  // of an item on the path for many rows: a warp of the second kernel takes a row's in turn
 
 }  // namespace
@@ -851,7 +856,11 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   if (d->n_seqs < 1 || d->T < 0 || d->h_q < 1 || h_kv < 1 || h_kv > d->h_q || d->h_q > 65535 || d->max_pages < 1 ||
       d->window < 0 || d->max_pages > 0x7fffffff / kPage || !(std::isfinite(d->scale)))
     return GDN_ERR_INVALID_ARG;
-  if (max_q_len <= 0 || max_q_len > d->T) max_q_len = d->T;
+  // With no bound a sequence may bring all the tokens; what follows then
+  // supposes equally many each, and only speed depends on that.
+  const bool bound = max_q_len > 0 && max_q_len <= d->T;
+  if (!bound) max_q_len = d->T;
+  const int q_len = bound ? max_q_len : (int)(((int64_t)d->T + d->n_seqs - 1) / d->n_seqs);
   const int64_t longest = (int64_t)d->max_pages * kPage;
   if (max_kv_len <= 0 || max_kv_len > longest) max_kv_len = (int)std::min<int64_t>(longest, 0x7fffffff);
   if (sm_count <= 0) {
@@ -864,18 +873,18 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   std::memset(&p, 0, sizeof(p));
   const int group = (d->h_q + h_kv - 1) / h_kv;
   if ((int64_t)d->T * group > 0x7fffffff - 4096) return GDN_ERR_INVALID_ARG;
-  const int64_t rows = (int64_t)max_q_len * group;
-  // Key tiles, every sequence taken at its longest, with item_cost for each item.
+  const int64_t rows = (int64_t)q_len * group;
+  // Key tiles, every sequence taken at its longest and with q tokens, with item_cost for each item.
   struct Units {
     int64_t total, longest_item, shortest;
     int row_tiles;
   };
-  auto units_of = [&](int tile_rows, int item_cost) {
-    Units u = {0, 0, INT64_MAX, (int)std::max<int64_t>(1, (rows + tile_rows - 1) / tile_rows)};
-    const int64_t past = std::max(0, max_kv_len - max_q_len);
+  auto units_of = [&](int q, int tile_rows, int item_cost) {
+    Units u = {0, 0, INT64_MAX, (int)std::max<int64_t>(1, ((int64_t)q * group + tile_rows - 1) / tile_rows)};
+    const int64_t past = std::max(0, max_kv_len - q);
     for (int rt = 0; rt < u.row_tiles; ++rt) {
       const int64_t t0 = (int64_t)rt * tile_rows / group;
-      const int64_t t1 = std::min<int64_t>(max_q_len - 1, ((int64_t)(rt + 1) * tile_rows - 1) / group);
+      const int64_t t1 = std::min<int64_t>(q - 1, ((int64_t)(rt + 1) * tile_rows - 1) / group);
       const int64_t hi = d->causal ? std::min<int64_t>(past + t1 + 1, max_kv_len) : max_kv_len;
       const int64_t lo = d->window ? std::max<int64_t>(0, past + t0 - d->window + 1) : 0;
       const int64_t cost = item_cost + std::max<int64_t>(1, (hi + kKvTile - 1) / kKvTile - lo / kKvTile);
@@ -905,15 +914,17 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
     // 111 at 4 and 113 at 12
     p.item_cost = p.rows <= 8 ? 4 : 8;
     per_sm = kv_few_ctas_per_sm(p.rows);
-    if (rows > 32 && (rows >= 32 * (int64_t)sm_count || units_of(32, p.item_cost).total > 8 * (int64_t)sm_count)) {
+    // Past 32 rows without a bound, one sequence may bring most of them, which
+    // small tiles would read all its keys for: it is taken to bring them all.
+    if (rows > 32 && (rows >= 32 * (int64_t)sm_count || units_of(max_q_len, 32, p.item_cost).total > 8 * (int64_t)sm_count)) {
       p.path = kKvPathMany;
       p.rows = 256;
       p.item_cost = 6;
     }
   }
-  u = units_of(p.rows, p.item_cost);
-  p.max_row_tiles = u.row_tiles;
-  const int64_t items = (int64_t)d->n_seqs * p.max_row_tiles * h_kv;
+  u = units_of(q_len, p.rows, p.item_cost);
+  p.max_row_tiles = (int)std::max<int64_t>(1, ((int64_t)max_q_len * group + p.rows - 1) / p.rows);
+  const int64_t items = (int64_t)d->n_seqs * u.row_tiles * h_kv;
   const int64_t slots = (int64_t)per_sm * sm_count;
   // Two ways to share out the items: each whole to one CTA, the longest first
   // (n_ctas = 0), or all key tiles in equal runs, whose cut items are joined
@@ -928,7 +939,8 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   // 53.3, 4096 tokens 128 and 141.
   // the kernels count units in 32 bits, whatever the lengths on the device turn out to be
   const int64_t units_most = (int64_t)d->max_pages * kPage / kKvTile + 1 + p.item_cost;
-  if (items > 0x7fffffff / units_most) return GDN_ERR_INVALID_ARG;
+  if (kv_most_row_tiles(d->n_seqs, d->T, group, p.rows, p.max_row_tiles) > 0x7fffffff / units_most / h_kv)
+    return GDN_ERR_INVALID_ARG;
   const int64_t rounds = (items + slots - 1) / slots;  // a CTA's start in each but the first counts a unit
   const int64_t whole = rounds - 1 + (u.longest_item == u.shortest
                                           ? rounds * u.longest_item
@@ -987,13 +999,24 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
   a.rows = plan->rows;
   a.max_rows = plan->max_q_len * a.group;
   a.max_row_tiles = plan->max_row_tiles;
+  a.slots = 0;
+  int64_t entries = (int64_t)d->n_seqs * a.max_row_tiles;
+  if (!cu) {  // equally many tokens each, however many the plan allows
+    a.max_row_tiles = std::max(1, std::min(a.max_row_tiles, (int)(((int64_t)a.c.n_each * a.group + a.rows - 1) / a.rows)));
+    entries = (int64_t)d->n_seqs * a.max_row_tiles;
+  } else {
+    // The search costs a few loads in turn: worth it from half as many entries,
+    // when these are more than the threads of a block take at once.
+    const int64_t most = kv_most_row_tiles(d->n_seqs, d->T, a.group, a.rows, a.max_row_tiles);
+    if (entries > 256 && 2 * most <= entries) entries = a.slots = (int)((int64_t)d->T * a.group / a.rows + d->n_seqs);
+  }
   a.n_ctas = plan->n_ctas;
   a.item_cost = plan->item_cost;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.desc = reinterpret_cast<int4*>(ws + plan->off_desc);
   a.ml = reinterpret_cast<float2*>(ws + plan->off_ml);
   a.o = reinterpret_cast<float*>(ws + plan->off_o);
-  const unsigned grid = a.n_ctas ? (unsigned)a.n_ctas : (unsigned)((int64_t)d->n_seqs * a.max_row_tiles * cache->h_kv);
+  const unsigned grid = a.n_ctas ? (unsigned)a.n_ctas : (unsigned)(entries * cache->h_kv);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = d->dtype == GDN_F32;
   LaunchLog log;

@@ -50,7 +50,8 @@ struct KvAttnArgs {
   int causal, window;
   float scale_log2;        // score scale times log2(e)
   int group;               // query heads per key/value head, rounded up
-  int rows, max_row_tiles; // rows of a row tile; row tiles per (sequence, head)
+  int rows, max_row_tiles; // rows of a row tile; row tiles per (sequence, head), at most
+  int slots;               // entries of the call when they are found by search (kv_entry), or 0
   int max_rows;            // rows of the longest sequence the plan allows
   int n_ctas;              // 0: CTA i takes item i whole
   int item_cost;           // what beginning and ending an item costs, in key tiles
@@ -176,6 +177,43 @@ __device__ __forceinline__ KvItem kv_item(const KvAttnArgs& a, int seq, int rt) 
   it.tiles = hi > lo ? (hi + kKvTile - 1) / kKvTile - it.first_tile : 0;
   return it;
 }
+// Entries enumerate the (sequence, row tile) pairs of a call in this order.
+// Without slots entry e is row tile e % max_row_tiles of sequence e / max_row_tiles.
+// When a sequence may bring most of the call's tokens those are up to n_seqs
+// times as many as there are row tiles.  With slots, sequence s has the entries
+// from b(s) = floor(cu[s] group / rows) + s on, as many as it has row tiles: they
+// end before b(s + 1), since floor(x) + ceil(y) <= floor(x + y) + 1, and
+// floor(T group / rows) + n_seqs entries are enough whatever the lengths.
+__device__ __forceinline__ int kv_first_slot(const KvAttnArgs& a, int s) {
+  const int tok = min(max(a.c.cu[s], 0), a.c.T);  // T * group is below 2^31
+  return (int)((uint32_t)(tok * a.group) / (uint32_t)a.rows) + s;
+}
+template <bool kSlots>
+__device__ __forceinline__ KvItem kv_entry(const KvAttnArgs& a, int e, int& seq, int& rt) {
+  seq = e;
+  rt = 0;
+  if (kSlots) {  // the last sequence whose slots begin at e or before
+    int lo = 0, hi = a.c.n_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (kv_first_slot(a, mid) <= e) lo = mid;
+      else hi = mid - 1;
+    }
+    seq = lo;
+    rt = e - kv_first_slot(a, lo);
+    if (rt < 0 || rt >= a.max_row_tiles) return {0, 0, 0, 0, -1};
+  } else if (a.max_row_tiles > 1) {
+    seq = e / a.max_row_tiles;
+    rt = e - seq * a.max_row_tiles;
+  }
+  return kv_item(a, seq, rt);
+}
+// Offsets that go back hide sequences from the search: every one is checked
+// all the same.
+__device__ __forceinline__ void kv_check_all(const KvAttnArgs& a) {
+  if (blockIdx.x == 0)
+    for (int s = threadIdx.x; s < a.c.n_seqs; s += blockDim.x) kv_seq(a.c, s);
+}
 __device__ __forceinline__ int kv_units(const KvItem& it) { return it.tiles < 0 ? 0 : max(1, it.tiles); }
 __device__ __forceinline__ int kv_cost(const KvAttnArgs& a, const KvItem& it) {
   return it.tiles < 0 ? 0 : a.item_cost + max(1, it.tiles);
@@ -214,18 +252,23 @@ __device__ __forceinline__ uint32_t block_inclusive_scan(uint32_t v, KvRunScratc
 // All of it is on the way to a CTA's first load, mostly as instructions not
 // yet in the cache: one scan when the threads have an entry each (any decode
 // batch of up to NT sequences), no 64-bit division.
-template <int NT>
-__device__ __noinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
+template <int NT, bool kSlots>
+__device__ __noinline__ void kv_run_of(const KvAttnArgs& a, KvRunScratch* sc) {
   const int tid = threadIdx.x;
+  if (kSlots) kv_check_all(a);
   if (a.n_ctas == 0) {  // one whole item a CTA
     if (tid == 0) {
       KvRun& r = sc->run;
       const int e = blockIdx.x / a.c.h_kv;  // the longest row tiles, under a causal mask the last ones, first
       r.head = blockIdx.x - e * a.c.h_kv;
-      r.rt = a.max_row_tiles - 1 - e / a.c.n_seqs;
-      r.seq = e % a.c.n_seqs;
+      if (kSlots) {
+        r.item = kv_entry<true>(a, a.slots - 1 - e, r.seq, r.rt);
+      } else {
+        r.rt = a.max_row_tiles - 1 - e / a.c.n_seqs;
+        r.seq = e % a.c.n_seqs;
+        r.item = kv_item(a, r.seq, r.rt);
+      }
       r.off = 0;
-      r.item = kv_item(a, r.seq, r.rt);
       r.begin = 0;
       r.end = r.total = kv_cost(a, r.item);
       r.ctas = 0;
@@ -233,20 +276,14 @@ __device__ __noinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
     __syncthreads();
     return;
   }
-  const int entries = a.c.n_seqs * a.max_row_tiles;
+  const int entries = kSlots ? a.slots : a.c.n_seqs * a.max_row_tiles;
   KvItem it;
   int seq = 0, rt = 0;
   uint32_t total = 0, base = 0, incl = 0, u = 0;
   auto entry = [&](int e) {
-    seq = e;
-    rt = 0;
-    if (a.max_row_tiles > 1) {
-      seq = e / a.max_row_tiles;
-      rt = e - seq * a.max_row_tiles;
-    }
     u = 0;
     if (e < entries) {
-      it = kv_item(a, seq, rt);
+      it = kv_entry<kSlots>(a, e, seq, rt);
       u = kv_cost(a, it) * a.c.h_kv;
     }
   };
@@ -289,6 +326,12 @@ __device__ __noinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
     base += sub;
   }
   __syncthreads();
+}
+
+template <int NT>
+__device__ __forceinline__ void kv_run(const KvAttnArgs& a, KvRunScratch* sc) {
+  if (a.slots) kv_run_of<NT, true>(a, sc);
+  else kv_run_of<NT, false>(a, sc);
 }
 
 // Walks the items of a run; every warp that needs it walks its own.
@@ -341,10 +384,11 @@ struct KvCursor {
 
 // The last CTA that has a part of the item whose first part this cursor
 // stands on: the one whose run has the item's last unit u, the largest c with
-// total c / ctas <= u, so floor(((u + 1) ctas - 1) / total).
+// total c / ctas <= u, so floor(((u + 1) ctas - 1) / total).  Offsets that go
+// back can put an item past the end.
 __device__ __forceinline__ int kv_last_cta(const KvAttnArgs& a, const KvRun& r, const KvCursor& c) {
   const int64_t item_end = (int64_t)r.begin + c.base + kv_cost(a, c.it);
-  return (int)((item_end * r.ctas - 1) / r.total);
+  return (int)min((item_end * r.ctas - 1) / r.total, (int64_t)r.ctas - 1);
 }
 
 // What the second kernel needs of the item this CTA began and did not end, or

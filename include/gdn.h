@@ -465,7 +465,8 @@ typedef struct gdn_kv_plan_t {
 
 /*
  * gdn_kv_attn_plan -- host-only planning of gdn_kv_attn.
- *   max_q_len  : no sequence brings more tokens than this (<= 0: T).
+ *   max_q_len  : no sequence brings more tokens than this (<= 0: unknown; any
+ *                number up to T, and the choice of kernel supposes T / n_seqs).
  *   max_kv_len : the longest sequence expected (<= 0: 64 max_pages); sizes the
  *                split only, so replays of a captured call may pass it.
  *   sm_count   : SMs to plan for; <= 0 queries the current device.

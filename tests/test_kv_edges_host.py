@@ -154,3 +154,37 @@ def test_waits_agree_by_warp(name):
         assert "kv_wait(" in text[at:end]
         text = text[:at] + text[end:]
     assert "kv_wait(" not in text
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("T,n,h_q,h_kv,pages", [(64 * 2048, 64, 32, 8, 4096), (32768, 256, 8, 2, 4096), (1 << 20, 1024, 8, 2, 4096)])
+def test_packed_batches_plan_without_a_bound(lib, dtype, T, n, h_q, h_kv, pages):  # noqa: F811
+    """However the tokens spread over the sequences, they fill T group / rows row tiles, and one more a sequence
+    that is not full: far fewer than every sequence with all the tokens."""
+    st, p = plan(lib, h_kv=h_kv, max_q=0, T=T, n_seqs=n, h_q=h_q, max_pages=pages, dtype=dtype)
+    assert st == OK
+    assert p.max_q_len == T and p.rows * p.max_row_tiles >= T * h_q // h_kv  # one sequence may bring them all
+
+
+def test_plan_still_refuses_too_many_units(lib):  # noqa: F811
+    """2^31 units are not counted in 32 bits, whatever the bound says."""
+    for max_q in (0, 1 << 20):
+        st, _ = plan(lib, max_q=max_q, T=1 << 20, n_seqs=1, h_q=64, h_kv=64, max_pages=1 << 20)
+        assert st == INVALID
+
+
+@pytest.mark.parametrize("T,n,h_q,h_kv,kv,rows", [(256, 256, 8, 2, 32768, 8), (4, 4, 16, 2, 262144, 8), (160, 32, 32, 8, 8192, 24),
+                                                  (90, 30, 8, 2, 4096, 16), (64, 8, 8, 2, 8192, 32)])
+def test_small_batches_without_a_bound(lib, T, n, h_q, h_kv, kv, rows):  # noqa: F811
+    """Generated and drafted tokens get the kernel for few rows, as with the bound."""
+    for max_q in (0, T // n):
+        st, p = plan(lib, h_kv=h_kv, max_q=max_q, T=T, n_seqs=n, h_q=h_q, max_pages=kv // 64)
+        assert st == OK and (p.path, p.rows) == (1, rows)
+
+
+def test_binding_gives_no_bound_for_offsets(calls):
+    import gated_deltanet_linear_fwd_gb300 as gdn
+    c, q, k, lens, table, cu = batch()
+    for offsets, kw, bound in ((cu, {}, 0), (None, {}, 32), (cu, dict(max_q_len=40), 40)):
+        gdn.gdn_kv_attn(q, c, lens, table, offsets, out=q, **kw)
+        assert [args[2] for name, args in calls.made if name == "gdn_kv_attn_plan"][-1] == bound

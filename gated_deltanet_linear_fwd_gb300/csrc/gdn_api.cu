@@ -397,6 +397,8 @@ int64_t kv_join_tiles(int path, int64_t tiles, bool one_tile) {
 int64_t kv_most_row_tiles(int n_seqs, int T, int group, int rows, int max_row_tiles) {
   return std::min<int64_t>((int64_t)n_seqs * max_row_tiles, (int64_t)T * group / rows + n_seqs);
 }
+// The attention kernels round lengths up to a tile of keys in 32 bits.
+constexpr int kKvMostPages = (0x7fffffff - kKvTile) / kPage;
 constexpr int kKvMaxParts = 32;  // of an item on the path for many rows: a warp of the second kernel takes a row's in turn
 
 }  // namespace
@@ -854,7 +856,7 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   if (d->dtype != GDN_BF16 && d->dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
   if (d->causal != 0 && d->causal != 1) return GDN_ERR_UNSUPPORTED;
   if (d->n_seqs < 1 || d->T < 0 || d->h_q < 1 || h_kv < 1 || h_kv > d->h_q || d->h_q > 65535 || d->max_pages < 1 ||
-      d->window < 0 || d->max_pages > 0x7fffffff / kPage || !(std::isfinite(d->scale)))
+      d->window < 0 || d->max_pages > kKvMostPages || !(std::isfinite(d->scale)))
     return GDN_ERR_INVALID_ARG;
   // With no bound a sequence may bring all the tokens; what follows then
   // supposes equally many each, and only speed depends on that.
@@ -974,7 +976,7 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
       plan->dtype != d->dtype)
     return GDN_ERR_INVALID_ARG;
   if (d->causal != 0 && d->causal != 1) return GDN_ERR_UNSUPPORTED;
-  if (d->window < 0 || !std::isfinite(d->scale)) return GDN_ERR_INVALID_ARG;
+  if (d->window < 0 || d->max_pages > kKvMostPages || !std::isfinite(d->scale)) return GDN_ERR_INVALID_ARG;
   KvAttnArgs a;
   if ((st = kv_stride(d->q_stride, d->h_q, d->dtype, &a.q_stride)) != GDN_OK) return st;
   if ((st = kv_stride(d->out_stride, d->h_q, d->dtype, &a.out_stride)) != GDN_OK) return st;

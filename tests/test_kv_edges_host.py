@@ -188,3 +188,15 @@ def test_binding_gives_no_bound_for_offsets(calls):
     for offsets, kw, bound in ((cu, {}, 0), (None, {}, 32), (cu, dict(max_q_len=40), 40)):
         gdn.gdn_kv_attn(q, c, lens, table, offsets, out=q, **kw)
         assert [args[2] for name, args in calls.made if name == "gdn_kv_attn_plan"][-1] == bound
+
+
+def test_longest_lengths(lib):  # noqa: F811
+    """A length is rounded up to a tile of 128 keys in 32 bits."""
+    most = (2 ** 31 - 1 - 128) // 64
+    for dtype in (0, 1):
+        assert plan(lib, max_q=1, T=1, n_seqs=1, max_pages=most, dtype=dtype)[0] == OK
+        for pages in (most + 1, (2 ** 31 - 1) // 64):
+            assert plan(lib, max_q=1, T=1, n_seqs=1, max_pages=pages, dtype=dtype)[0] == INVALID
+            st, p = plan(lib, max_q=1, T=1, n_seqs=1, max_pages=most, dtype=dtype)
+            assert lib.gdn_kv_attn(512, 64, 64, None, cache(), 1024, None, dims(T=1, n_seqs=1, max_pages=pages, dtype=dtype),
+                                   p, 4096, p.workspace_bytes, None) == INVALID

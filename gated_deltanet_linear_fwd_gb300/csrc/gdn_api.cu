@@ -397,6 +397,11 @@ int64_t kv_join_tiles(int path, int64_t tiles, bool one_tile) {
 int64_t kv_most_row_tiles(int n_seqs, int T, int group, int rows, int max_row_tiles) {
   return std::min<int64_t>((int64_t)n_seqs * max_row_tiles, (int64_t)T * group / rows + n_seqs);
 }
+// The kernels count units in 32 bits, whatever the lengths on the device turn out to be.
+bool kv_units_fit(const gdn_kv_dims* d, int h_kv, int group, const gdn_kv_plan_t& p) {
+  const int64_t most = (int64_t)d->max_pages * kPage / kKvTile + 1 + p.item_cost;
+  return kv_most_row_tiles(d->n_seqs, d->T, group, p.rows, p.max_row_tiles) <= 0x7fffffff / most / h_kv;
+}
 // The attention kernels round lengths up to a tile of keys in 32 bits.
 constexpr int kKvMostPages = (0x7fffffff - kKvTile) / kPage;
 constexpr int kKvMaxParts = 32;  // of an item on the path for many rows: a warp of the second kernel takes a row's in turn
@@ -926,6 +931,7 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   }
   u = units_of(q_len, p.rows, p.item_cost);
   p.max_row_tiles = (int)std::max<int64_t>(1, ((int64_t)max_q_len * group + p.rows - 1) / p.rows);
+  if (!kv_units_fit(d, h_kv, group, p)) return GDN_ERR_INVALID_ARG;
   const int64_t items = (int64_t)d->n_seqs * u.row_tiles * h_kv;
   const int64_t slots = (int64_t)per_sm * sm_count;
   // Two ways to share out the items: each whole to one CTA, the longest first
@@ -939,10 +945,6 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   // 1024 tokens 28.1 and 28.5, 4096 tokens 67 and 65, 8192 tokens 119 and 147,
   // 4096 tokens over 65536 keys 792 and 690; fp32 prompts of 2048 tokens 68.8 and
   // 53.3, 4096 tokens 128 and 141.
-  // the kernels count units in 32 bits, whatever the lengths on the device turn out to be
-  const int64_t units_most = (int64_t)d->max_pages * kPage / kKvTile + 1 + p.item_cost;
-  if (kv_most_row_tiles(d->n_seqs, d->T, group, p.rows, p.max_row_tiles) > 0x7fffffff / units_most / h_kv)
-    return GDN_ERR_INVALID_ARG;
   const int64_t rounds = (items + slots - 1) / slots;  // a CTA's start in each but the first counts a unit
   const int64_t whole = rounds - 1 + (u.longest_item == u.shortest
                                           ? rounds * u.longest_item
@@ -984,6 +986,8 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
   if (!q || !out) return GDN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return GDN_ERR_MISALIGNED;
   if (!cu && d->T / d->n_seqs > plan->max_q_len) return GDN_ERR_INVALID_ARG;
+  // the page table may be wider than the one planned for
+  if (!kv_units_fit(d, cache->h_kv, (d->h_q + cache->h_kv - 1) / cache->h_kv, *plan)) return GDN_ERR_INVALID_ARG;
   if (plan->n_ctas > 0) {
     if (!workspace || workspace_bytes < plan->workspace_bytes) return GDN_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GDN_ERR_MISALIGNED;

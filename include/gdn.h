@@ -498,7 +498,8 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* dims, int h_kv, int max_q_len, in
  * Asynchronous on `stream`; one or two kernels.
  * A sequence that brings more tokens than the plan's max_q_len is recorded as
  * the same device check (detail 7).
- * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
+ * Errors: INVALID_ARG (also, as in planning, for calls past 2^31 units under
+ * this call's max_pages), UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
  */
 gdn_status gdn_kv_attn(const void* q, const int32_t* kv_lens_dev, const int32_t* page_table_dev,
                        const int32_t* cu_seqlens_dev, const gdn_kv_cache* cache, void* out, float* lse,

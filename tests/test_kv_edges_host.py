@@ -7,7 +7,7 @@ import re
 import pytest
 import torch
 
-from tests.test_kv_host import INVALID, OK, cache, dims, lib, plan  # noqa: F401
+from tests.test_kv_host import INVALID, OK, WORKSPACE, cache, dims, lib, plan  # noqa: F401
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "gated_deltanet_linear_fwd_gb300", "csrc")
 
@@ -200,3 +200,16 @@ def test_longest_lengths(lib):  # noqa: F811
             st, p = plan(lib, max_q=1, T=1, n_seqs=1, max_pages=most, dtype=dtype)
             assert lib.gdn_kv_attn(512, 64, 64, None, cache(), 1024, None, dims(T=1, n_seqs=1, max_pages=pages, dtype=dtype),
                                    p, 4096, p.workspace_bytes, None) == INVALID
+
+
+def test_table_wider_than_the_plans(lib):  # noqa: F811
+    """The bound on units holds for the call's page table too, which may be wider than the one planned for."""
+    kw = dict(T=1 << 18, n_seqs=1 << 12, h_q=64)
+    st, p = plan(lib, h_kv=64, max_q=64, max_pages=1, **kw)
+    assert st == OK
+    assert plan(lib, h_kv=64, max_q=64, max_pages=1 << 16, **kw)[0] == INVALID
+    calls = [lib.gdn_kv_attn(512, 64, 64, None, cache(h_kv=64), 1024, None, dims(max_pages=pages, **kw), p, None, 0, None)
+             for pages in (1 << 16, 1 << 20)]
+    assert calls == [INVALID, INVALID]
+    assert p.n_ctas > 0 and lib.gdn_kv_attn(512, 64, 64, None, cache(h_kv=64), 1024, None, dims(max_pages=4, **kw), p, None, 0,
+                                            None) == WORKSPACE  # accepted so far

@@ -52,7 +52,8 @@ class DeltaMixer:
         return unit(q), unit(k), v.contiguous(), g.contiguous(), beta.contiguous()
 
     def prefill(self, x, cu_seqlens):
-        o, self.state = gdn.gdn_chunk_fwd(*self._project(x), None, cu_seqlens)
+        # a captured step goes on reading the first states' memory
+        o, self.state = gdn.gdn_chunk_fwd(*self._project(x), None, cu_seqlens, final_state=self.state)
         return o.flatten(1) @ self.w_out.T
 
     def step(self, x):

@@ -46,3 +46,18 @@ def test_steps_continue_the_prefill(ex, lens, steps):
 def test_example_runs(ex, capsys):
     ex.main()
     assert "lengths [720, 84, 21, 1310]" in capsys.readouterr().out
+
+
+def test_prompts_after_the_step_was_captured(ex):
+    """New prompts on a stack whose step has been captured: its steps go on from them, as a new stack's do."""
+    width, lens = 256, [70, 3, 128]
+    gen = torch.Generator("cuda").manual_seed(5)
+    rand = lambda n: torch.randn(n, width, device="cuda", generator=gen).bfloat16()  # noqa: E731
+    used, new = (ex.HybridStack(width=width, batch=3, max_tokens=512) for _ in range(2))
+    used.prefill(rand(40), [9, 30, 1])
+    for _ in range(2):
+        used.step(rand(3))
+    x, tokens = rand(sum(lens)), [rand(3) for _ in range(3)]
+    assert torch.equal(used.prefill(x, lens), new.prefill(x, lens))
+    for t in tokens:
+        assert torch.equal(used.step(t), new.step(t))

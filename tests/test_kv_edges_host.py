@@ -213,3 +213,22 @@ def test_table_wider_than_the_plans(lib):  # noqa: F811
     assert calls == [INVALID, INVALID]
     assert p.n_ctas > 0 and lib.gdn_kv_attn(512, 64, 64, None, cache(h_kv=64), 1024, None, dims(max_pages=4, **kw), p, None, 0,
                                             None) == WORKSPACE  # accepted so far
+
+
+@pytest.mark.parametrize("T,n,h_q,h_kv,max_q,max_kv,path,rows", [
+    (1, 1, 8, 2, 1, 333, 1, 8), (256, 256, 8, 2, 1, 32768, 1, 8), (4, 4, 16, 2, 1, 262144, 1, 8), (160, 32, 32, 8, 5, 8192, 1, 24),
+    (48, 16, 8, 2, 3, 4096, 1, 16), (64, 1, 8, 2, 64, 8192, 1, 32), (512, 1, 8, 2, 512, 512, 2, 256), (2048, 1, 16, 2, 2048, 67584, 2, 256),
+    (32768, 1, 8, 2, 32768, 32768, 2, 256)])
+def test_plan_chooses(lib, T, n, h_q, h_kv, max_q, max_kv, path, rows):  # noqa: F811
+    """Kernel and row tile, on 152 SMs; fp32 has one of each."""
+    for dtype, want in ((0, (path, rows)), (1, (0, 128))):
+        st, p = plan(lib, h_kv=h_kv, max_q=max_q, max_kv=max_kv, T=T, n_seqs=n, h_q=h_q, max_pages=-(-max_kv // 64), dtype=dtype)
+        assert st == OK and (p.path, p.rows) == want
+
+
+@pytest.mark.parametrize("n,group,rows", [(2, 4, 8), (3, 3, 16), (1, 16, 16), (17, 1, 24), (5, 4, 24), (6, 4, 24), (5, 5, 32), (31, 1, 32), (8, 4, 32)])
+@pytest.mark.parametrize("window", [0, 200])
+def test_row_counts_get_their_row_tile(lib, n, group, rows, window):  # noqa: F811
+    """What the GPU test of row counts runs on, whose calls give no bound."""
+    st, p = plan(lib, h_kv=2, max_q=0, T=7 * n, n_seqs=7, h_q=2 * group, max_pages=94, window=window)
+    assert st == OK and (p.path, p.rows) == (1, rows)

@@ -1,4 +1,4 @@
-"""Attention over the 8-bit cache against its 64-bit form, with what the bf16
+"""Attention over the 8-bit cache against its 64-bit form, with what the
 kernels drop of weights far below the largest in the bound."""
 from __future__ import annotations
 
@@ -13,7 +13,8 @@ from tests import kv_util as U
 #   few rows: P = 2^8 of the largest and hi + lo / 16 in e4m3; lo's subnormal
 #     step is 2^-9, so half a step of P is 2^-14.
 #   many rows: P = 2^3 of it or more, in fp16, whose subnormal step is 2^-24.
-FLOOR = {1: 2.0 ** -22, 2: 2.0 ** -28}
+#   fp32: P = 2^14 of it, hi + lo in fp16.
+FLOOR = {0: 2.0 ** -39, 1: 2.0 ** -22, 2: 2.0 ** -28}
 
 
 def dropped(b: U.Batch, q, path, causal=True, window=0, scale=0.0):
@@ -43,9 +44,9 @@ def dropped(b: U.Batch, q, path, causal=True, window=0, scale=0.0):
     return out
 
 
-def check(gdn, b: U.Batch, h_q, plan, q=None, use_cu=True):
-    """bf16 attention under `plan` (its masks and scale) within the bound.  Returns (out, lse)."""
-    q = (b.randn(b.T, h_q, U.D) if q is None else q).to(torch.bfloat16)
+def check(gdn, b: U.Batch, h_q, plan, q=None, use_cu=True, dtype=torch.bfloat16):
+    """Attention under `plan` (its masks and scale) within the bound.  Returns (out, lse)."""
+    q = (b.randn(b.T, h_q, U.D) if q is None else q).to(dtype)
     dev = lambda c: c.float().to(torch.float8_e4m3fn).cuda()  # noqa: E731
     cache = gdn.KVCache(dev(b.k), dev(b.v), b.ks.float().cuda(), b.vs.float().cuda())
     out, lse = gdn.gdn_kv_attn(q.cuda(), cache, b.lens.cuda(), b.table.cuda(), b.cu.cuda() if use_cu else None, plan=plan)
@@ -53,11 +54,12 @@ def check(gdn, b: U.Batch, h_q, plan, q=None, use_cu=True):
     o, z, mass, reach, top = U.attn_ref(b, q, plan.causal, plan.window, plan.scale or None)
     if plan.scale < 0:
         reach = -reach
-    bo, bz = U.attn_bounds(o, mass, reach, top, torch.bfloat16)
+    bo, bz = U.attn_bounds(o, mass, reach, top, dtype)
     bo = bo + dropped(b, q, plan.raw.path, plan.causal, plan.window, plan.scale)
     got, got_z = out.double().cpu(), lse.double().cpu()
     empty = z == -math.inf
     assert torch.equal(got_z == -math.inf, empty) and (got[empty] == 0).all()
+    assert not got.isnan().any()
     err = (got - o).abs() / bo
     assert err.max() <= 1, f"out: {err.max():.3f} of the bound"
     ez = ((got_z - z).abs() / bz)[~empty]

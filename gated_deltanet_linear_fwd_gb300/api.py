@@ -445,8 +445,10 @@ def gdn_kv_attn(q: torch.Tensor, cache: KVCache, kv_lens: torch.Tensor, page_tab
     """Attention of each new token over its sequence's cached keys and values
     (gdn_kv_attn): q [T, h_q, 128] bf16 or fp32, packed like gdn_kv_append's k
     and v, which go into the cache first.  Returns (out [T, h_q, 128],
-    lse [T, h_q] fp32 or None).  causal, window, scale and the bounds are the
-    plan's when one is given; a plan holds for calls of the same sizes."""
+    lse [T, h_q] fp32 or None); neither has a history, there is no backward.
+    causal, window, scale and the bounds are the plan's when one is given; a plan
+    holds for calls of the same sizes.  max_q_len, the most tokens a sequence
+    brings, may be left out: offsets alone then plan for T / n_seqs."""
     n, max_pages, cu = _kv_ints(cache, kv_lens, page_table, cu_seqlens)
     T, h_q, d = q.shape
     qs = _kv_rows("q", q, h_q, cache)

@@ -912,9 +912,10 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
     // to do: small calls are sooner done in tiles of 32 rows, which there are more
     // of and which begin sooner, up to 8 units an SM.  Measured, tiles of 256 rows
     // and of 32 or fewer, in us: 64 sequences to 32768 tokens, 4 key/value heads, 32
-    // rows 535 and 221, 48 rows 331 and 408; 8 query heads on 2, 64 tokens over 64
-    // keys 14.2 and 11.1 (1 unit an SM), over 8192 keys 28.8 and 20.2 (8), over 65536 56
-    // and 61 (55), prompts of 512 tokens 20.7 and 19.4 (9), 1024 tokens 28 and 33 (21).
+    // rows 324 and 216, 48 rows 326 and 399; 8 query heads on 2, 64 tokens over 64
+    // keys 14.6 and 11.0 (1 unit an SM), over 8192 keys 26.6 and 18.9 (8), over 65536
+    // 54.1 and 58.7 (55), prompts of 512 tokens 20.9 and 18.2, or 13.4 as whole items
+    // (9), 1024 tokens 28.2 and 31.9, or 26.9 as whole items (21).
     p.path = kKvPathFew;
     p.rows = (int)std::min<int64_t>(32, std::max<int64_t>(8, (rows + 7) / 8 * 8));  // at least 8: a call may bring no tokens
     // measured: 64 sequences to 65536 tokens, 16 rows, 62.7 us at 3 and 58.5 at 8; 256 to 32768, 8 rows, 116 at 3,
@@ -939,12 +940,12 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   // by a second kernel.  Whole items end with the longest one, or with the last
   // round of equal ones; runs end together, plus the parts' way through
   // memory and the second kernel.  Measured, whole and runs, in us: 16 tokens
-  // over 1024 keys of 8 heads 12.6 and 14.6, 40 over 2048 keys 46.8 and 39.1, 147
-  // over 28 keys of 16 heads 54.9 and 42;
-  // with 8 query heads on 2, 1024 tokens over 4096 keys 67 and 40, prompts of
-  // 1024 tokens 28.1 and 28.5, 4096 tokens 67 and 65, 8192 tokens 119 and 147,
-  // 4096 tokens over 65536 keys 792 and 690; fp32 prompts of 2048 tokens 68.8 and
-  // 53.3, 4096 tokens 128 and 141.
+  // over 1024 keys of 8 heads 12.6 and 14.0, 40 over 2048 keys 46.5 and 37.9, 147
+  // over 28 keys of 16 heads 55.1 and 41.2;
+  // with 8 query heads on 2, 1024 tokens over 4096 keys 69 and 40, prompts of
+  // 1024 tokens 28.9 and 28.8, 4096 tokens 67 and 66, 8192 tokens 119 and 149,
+  // 4096 tokens over 65536 keys 794 and 694; fp32 prompts of 2048 tokens 66 and
+  // 53, 4096 tokens 120 and 131 (the estimate takes runs there).
   const int64_t rounds = (items + slots - 1) / slots;  // a CTA's start in each but the first counts a unit
   const int64_t whole = rounds - 1 + (u.longest_item == u.shortest
                                           ? rounds * u.longest_item

@@ -7,16 +7,17 @@
 //     largest magnitude is in [2^14, 2^15), is the sum of two fp16 rows: the
 //     rounded one and the rounded rest, exact to 2^-24 of each element (to
 //     2^-39 of the row's largest).
-//   O [128 rows, 128 d] = P V, the weights P <= 2^14 split the same way.
+//   O [128 rows, 128 d] = P V, the weights P <= 2^14 split the same way: 22 bits
+//     down to 2^-17 of the tile's largest, 2^-39 of that below.
 // The low parts come first: the tensor cores' sums lose a little at every step,
 // in proportion to what is in them (2000 to 4000 keys, unit queries: relative error
 // 4e-7 against 64 bits, 1.1e-6 with the high parts first, 1.2e-6 for fp32 products
 // and softmax).
 //
 // That is twice the products of a bf16 call.  Prompts over themselves, 8 query
-// heads on 2: 16384 tokens 1595 us (345 TFLOP/s of the formula), 2048 tokens 52 us;
+// heads on 2: 16384 tokens 1591 us (345 TFLOP/s of the formula), 2048 tokens 53 us;
 // as fp32 FMAs on the CUDA cores 2048 tokens took 278 us.  64 sequences of 1024 to
-// 8192 tokens, 4 heads: 207 us for 8 rows (1.27 TB/s of codes; 598 with FMAs).
+// 8192 tokens, 4 heads: 209 us for 8 rows (1.27 TB/s of codes; 598 with FMAs).
 // Bound by the chain of a tile, some 6200 cycles: converting keys 650, scores and
 // maximum 700, weights 1200, 2000 in which warp 0 issues the products as they
 // run, join and converting values 1100.  With 512 threads, half as much for each,

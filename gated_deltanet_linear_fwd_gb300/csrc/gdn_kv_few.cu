@@ -12,8 +12,9 @@
 // e4m3 rows hi + lo / 16: hi has its four leading bits, lo the remaining four,
 // exactly where it is within 2^13 of the row's largest and to 2^-22 of that
 // below.  Weights P = 2^(x - m + 8) enter as hi + lo / 16, eight bits (to 2^-8 of
-// each weight, relative, down to 2^-14 of the largest; a bf16 weight has 2^-9).  The two parts are columns of
-// one product, so no key or value is converted or read twice.
+// each weight, relative, down to 2^-14 of the step's largest and to 2^-22 of that
+// below; a bf16 weight has 2^-9).  The two parts are columns of one product, so no
+// key or value is converted or read twice.
 //
 // Softmax over the keys x_j = scale log2(e) q . k_j, by steps of one or two
 // tiles of 128 keys: thread j of a warpgroup holds key j's column of S^T.  The

@@ -7,7 +7,9 @@
 //   S [128 rows, 128 keys] = Q K^T: e4m3 operands.  The keys' codes enter as
 //     they are; a bf16 query row, scaled by a power of two so that its largest
 //     magnitude is in (224, 448], is the sum of two e4m3 rows (four leading
-//     bits, then the remaining four, exact to 2^-17.8 of the row's largest).
+//     bits, then the remaining four, exact to 2^-17.8 of the row's largest, so
+//     that elements below 2^-10 of it keep fewer than their eight bits: the low
+//     part has no factor of its own, since both share one accumulator).
 //     Both accumulate into one S: as many steps as one bf16 product.
 //   O [128 rows, 128 d] += P V: fp16 operands.  The values' codes are exact in
 //     fp16 and converted once per CTA by a warpgroup of their own; the weights
@@ -21,15 +23,16 @@
 // the codes is the output in units of 2^(m - 3); the softmax's sum is of P_j 2^-e_v in
 // fp32.  m follows the running maximum of x + e_v only when that has grown by
 // more than 12, so O in tensor memory is rarely rescaled; P stays below 2^15,
-// within fp16, which loses only weights below 2^-28 of 2^m.
+// within fp16, which keeps fewer than eleven bits of weights below 2^-17 of 2^m
+// and none of those below 2^-28; the sum counts them all.
 //
 // Tensor memory (512 columns): S of either tile (P over its middle) and O
 // of either tile.  Each tile has an MMA warp that alternates P V of
 // the previous keys with Q K^T of the next; one tile's softmax runs under the
 // other's products.
 //
-// A prompt of 32768 tokens, 8 query heads on 2: 1503 us, 1.46 PFLOP/s (75 % of a
-// bf16 library product); 2048 tokens over 67584, 16 heads on 2: 757 us.  The
+// A prompt of 32768 tokens, 8 query heads on 2: 1495 us, 1.47 PFLOP/s (76 % of a
+// bf16 library product); 2048 tokens over 67584, 16 heads on 2: 753 us.  The
 // tensor pipe is busy 64 % of the time; the way from scores to weights is
 // what the other tile's products do not hide completely.  Registers set the
 // limit: 176 a softmax thread instead of 184 cost 3 %, 168 a third.

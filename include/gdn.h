@@ -492,9 +492,21 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* dims, int h_kv, int max_q_len, in
  *                contents on entry do not matter.  Not to be shared by calls
  *                that may run concurrently.
  * Both types run on the tensor cores; keys and values enter the products
- * exactly, and the softmax and all sums are fp32.  With GDN_BF16 a weight enters
- * with eight bits or more; with GDN_F32 queries and weights enter as two fp16
- * parts each, 22 bits or more.  Results repeat bit for bit under the same plan.
+ * exactly, and the softmax, the sum of the weights and all sums are fp32.
+ * Queries and weights are rounded as they enter the products.  Below, a query
+ * element stands against its row's largest, and a weight, times its value's
+ * page scale, against the row's largest such product:
+ *   GDN_BF16, plan->rows <= 32: a weight to 2^-8 of itself down to 2^-14 of the
+ *     largest, below that to 2^-22 of the largest; a query element in full down
+ *     to 2^-13 of the largest, below that to 2^-22 of it.
+ *   GDN_BF16, plan->rows = 256: a weight to 2^-11 of itself down to 2^-17 of the
+ *     largest, below that to 2^-28 of it; a query element to 2^-17.8 of the
+ *     largest, so in full down to 2^-10 of it only.
+ *   GDN_F32: a weight to 2^-22 of itself down to 2^-17 of the largest, below
+ *     that to 2^-39 of it; a query element to 2^-24 of itself, or 2^-39 of the
+ *     largest.
+ * So an output whose heavy keys all have a value of zero there is coarser than
+ * the others of its row.  Results repeat bit for bit under the same plan.
  * Asynchronous on `stream`; one or two kernels.
  * A sequence that brings more tokens than the plan's max_q_len is recorded as
  * the same device check (detail 7).

@@ -384,12 +384,13 @@ gdn_status gdn_chunk_fwd_train(const void* q, const void* k, const void* v, cons
  * the causal mask.
  *
  * The lengths and the table are device data, so a captured call may be
- * replayed while the caller advances them.  The kernels check them before
- * following them: offsets that leave [0, T] or go back, a length outside
- * [0, 64 max_pages], or a page outside [0, n_pages) is recorded as
+ * replayed as the caller advances them between calls; they, and a call's
+ * workspace, must not change while it runs.  The kernels check lengths and
+ * table before following them: offsets that leave [0, T] or go back, a length
+ * outside [0, 64 max_pages], or a page outside [0, n_pages) is recorded as
  * GDN_ERR_DEVICE_CHECK with detail 7 (offsets, length) or 8 (page) in
  * cache->status and no access follows it outside the buffers; the outputs of
- * that sequence are then undefined.  cache->status keeps the first failure
+ * that sequence (with such offsets, of any) are then undefined.  cache->status keeps the first failure
  * until the caller zeroes it; read it with gdn_get_device_status(cache->status, ...).
  */
 #define GDN_KV_PAGE 64

@@ -397,10 +397,9 @@ int64_t kv_join_tiles(int path, int64_t tiles, bool one_tile) {
 int64_t kv_most_row_tiles(int n_seqs, int T, int group, int rows, int max_row_tiles) {
   return std::min<int64_t>((int64_t)n_seqs * max_row_tiles, (int64_t)T * group / rows + n_seqs);
 }
-// The kernels count units in 32 bits, whatever the lengths on the device turn out to be.
-bool kv_units_fit(const gdn_kv_dims* d, int h_kv, int group, const gdn_kv_plan_t& p) {
-  const int64_t most = (int64_t)d->max_pages * kPage / kKvTile + 1 + p.item_cost;
-  return kv_most_row_tiles(d->n_seqs, d->T, group, p.rows, p.max_row_tiles) <= 0x7fffffff / most / h_kv;
+// Row tiles whose units the kernels can count in 32 bits, whatever the lengths on the device turn out to be.
+int64_t kv_row_tiles_counted(const gdn_kv_dims* d, int h_kv, const gdn_kv_plan_t& p) {
+  return 0x7fffffff / ((int64_t)d->max_pages * kPage / kKvTile + 1 + p.item_cost) / h_kv;
 }
 // The attention kernels round lengths up to a tile of keys in 32 bits.
 constexpr int kKvMostPages = (0x7fffffff - kKvTile) / kPage;
@@ -932,7 +931,8 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* d, int h_kv, int max_q_len, int m
   }
   u = units_of(q_len, p.rows, p.item_cost);
   p.max_row_tiles = (int)std::max<int64_t>(1, ((int64_t)max_q_len * group + p.rows - 1) / p.rows);
-  if (!kv_units_fit(d, h_kv, group, p)) return GDN_ERR_INVALID_ARG;
+  if (kv_most_row_tiles(d->n_seqs, d->T, group, p.rows, p.max_row_tiles) > kv_row_tiles_counted(d, h_kv, p))
+    return GDN_ERR_INVALID_ARG;
   const int64_t items = (int64_t)d->n_seqs * u.row_tiles * h_kv;
   const int64_t slots = (int64_t)per_sm * sm_count;
   // Two ways to share out the items: each whole to one CTA, the longest first
@@ -987,8 +987,10 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
   if (!q || !out) return GDN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return GDN_ERR_MISALIGNED;
   if (!cu && d->T / d->n_seqs > plan->max_q_len) return GDN_ERR_INVALID_ARG;
-  // the page table may be wider than the one planned for
-  if (!kv_units_fit(d, cache->h_kv, (d->h_q + cache->h_kv - 1) / cache->h_kv, *plan)) return GDN_ERR_INVALID_ARG;
+  const int group = (d->h_q + cache->h_kv - 1) / cache->h_kv;
+  const int64_t most = kv_most_row_tiles(d->n_seqs, d->T, group, plan->rows, plan->max_row_tiles);
+  const int64_t counted = kv_row_tiles_counted(d, cache->h_kv, *plan);  // the page table may be wider than the one planned for
+  if (most > counted) return GDN_ERR_INVALID_ARG;
   if (plan->n_ctas > 0) {
     if (!workspace || workspace_bytes < plan->workspace_bytes) return GDN_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return GDN_ERR_MISALIGNED;
@@ -1002,7 +1004,7 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
   a.causal = d->causal;
   a.window = d->window;
   a.scale_log2 = (d->scale != 0.f ? d->scale : 1.0f / std::sqrt((float)kHeadDim)) * 1.44269504088896341f;
-  a.group = (d->h_q + cache->h_kv - 1) / cache->h_kv;
+  a.group = group;
   a.rows = plan->rows;
   a.max_rows = plan->max_q_len * a.group;
   a.max_row_tiles = plan->max_row_tiles;
@@ -1013,9 +1015,10 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
     entries = (int64_t)d->n_seqs * a.max_row_tiles;
   } else {
     // The search costs a few loads in turn: worth it from half as many entries,
-    // when these are more than the threads of a block take at once.
-    const int64_t most = kv_most_row_tiles(d->n_seqs, d->T, a.group, a.rows, a.max_row_tiles);
-    if (entries > 256 && 2 * most <= entries) entries = a.slots = (int)((int64_t)d->T * a.group / a.rows + d->n_seqs);
+    // when these are more than the threads of a block take at once.  Offsets that
+    // go back may give every entry a row tile, which then have to be countable.
+    if ((entries > 256 && 2 * most <= entries) || entries > counted)
+      entries = a.slots = (int)((int64_t)d->T * group / a.rows + d->n_seqs);
   }
   a.n_ctas = plan->n_ctas;
   a.item_cost = plan->item_cost;

@@ -115,3 +115,25 @@ def test_tokens_of_no_sequence(gdn, dtype):  # noqa: F811
     assert (out[:50] == 7).all() and (out[50 + b.T:] == 7).all() and (lse[:50] == 7).all() and (lse[50 + b.T:] == 7).all()
     assert ((out[50:50 + b.T].double().cpu() - o).abs() <= bo).all() and ((lse[50:50 + b.T].double().cpu() - z).abs() <= bz).all()
     assert status(gdn, cache) == (0, 0)
+
+
+@pytest.mark.parametrize("runs", [False, True])
+def test_few_entries_of_many_units(gdn, runs):  # noqa: F811
+    """A page table so wide that row tiles are found by search although there are few of them."""
+    n, h = 40, 64
+    b = U.Batch([256] + [0] * 10 + [1] * 29, [300] + [5] * 10 + [2 + 7 * i for i in range(29)], h, seed=1)
+    b.fill()
+    cache, q = to_cache(gdn, b), b.randn(b.T, h, 128)
+    table = torch.zeros(n, 1 << 20, dtype=torch.int32, device="cuda")
+    table[:, :b.max_pages] = b.table.cuda()
+    p = gdn.gdn_kv_attn_plan(T=b.T, n_seqs=n, h_q=h, h_kv=h, max_q_len=256, max_kv_len=20000 if runs else 64, max_pages=1 << 20,
+                             dtype=F32, sm_count=152 if runs else 100000)
+    assert p.raw.max_row_tiles * n == 80 and (p.raw.n_ctas > 0) == runs
+    out, lse = gdn.gdn_kv_attn(q.cuda(), cache, b.lens.cuda(), table, b.cu.cuda(), plan=p)
+    o, z, mass, reach, top = U.attn_ref(b, q)
+    bo, bz = U.attn_bounds(o, mass, reach, top, F32)
+    assert ((out.double().cpu() - o).abs() <= bo).all() and ((lse.double().cpu() - z).abs() <= bz).all()
+    cu = b.cu.clone()
+    cu[20] = 0
+    gdn.gdn_kv_attn(q.cuda(), cache, b.lens.cuda(), table, cu.cuda(), plan=p)
+    assert status(gdn, cache) == (7, 7)

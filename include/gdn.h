@@ -483,8 +483,10 @@ gdn_status gdn_kv_attn_plan(const gdn_kv_dims* dims, int h_kv, int max_q_len, in
  * token at position p and query head j, over the keys the masks leave:
  *   w = softmax(scale q . k),  out = sum w v,  lse = log sum exp(scale q . k).
  * A token whose masks leave no key has out = 0 and lse = -inf.  Keys outside
- * the masks do not enter, whatever their codes; a NaN code among the attended
- * keys, or a q that is not finite, gives NaN.
+ * the masks do not enter, whatever their codes.  A NaN code in an attended key,
+ * or a q that is not finite, makes the whole row and its lse NaN; one in an
+ * attended value the element it is in, and the whole row and its lse where the
+ * masks cut the key's tile of 128.
  *   q    : device, [T, h_q, 128], dims->dtype, token stride dims->q_stride.
  *   out  : device, [T, h_q, 128], dims->dtype, token stride dims->out_stride.
  *   lse  : device, [T, h_q] fp32, or NULL.

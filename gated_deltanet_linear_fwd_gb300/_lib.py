@@ -34,9 +34,16 @@ GDN_CP_AUTO = 3
 EXPORTED = ["gdn_cp_plan", "gdn_chunk_fwd", "gdn_status_string", "gdn_last_cuda_error",
             "gdn_get_device_status", "gdn_cp_head_modes", "gdn_set_trace_events", "gdn_trace_last", "gdn_chunk_fwd_static",
             "gdn_get_static_device_status", "gdn_decode_step", "gdn_debug_stall_ns", "gdn_bwd_workspace_bytes",
-            "gdn_chunk_bwd", "gdn_chunk_fwd_train", "gdn_kv_append", "gdn_kv_read", "gdn_kv_attn_plan", "gdn_kv_attn"]
+            "gdn_chunk_bwd", "gdn_chunk_fwd_train", "gdn_kv_append", "gdn_kv_read", "gdn_kv_attn_plan", "gdn_kv_attn",
+            "gdn_rope_table", "gdn_qk_rope", "gdn_qk_rope_bwd_workspace_bytes", "gdn_qk_rope_bwd", "gdn_kv_append_rope",
+            "gdn_conv_fwd", "gdn_conv_bwd_workspace_bytes", "gdn_conv_bwd", "gdn_conv_step"]
 
 GDN_KV_PAGE = 64
+
+GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
+GDN_ROPE_PLAIN, GDN_ROPE_LINEAR, GDN_ROPE_NTK, GDN_ROPE_PARTS = 0, 1, 2, 3
+GDN_NORM_NONE, GDN_NORM_RMS, GDN_NORM_UNIT = 0, 1, 2
+GDN_ACT_NONE, GDN_ACT_SILU = 0, 1
 
 
 class gdn_dims(ctypes.Structure):
@@ -82,6 +89,28 @@ class gdn_kv_plan_t(ctypes.Structure):
                 ("h_q", ctypes.c_int), ("h_kv", ctypes.c_int), ("dtype", ctypes.c_int), ("max_q_len", ctypes.c_int),
                 ("off_desc", ctypes.c_size_t), ("off_ml", ctypes.c_size_t), ("off_o", ctypes.c_size_t),
                 ("workspace_bytes", ctypes.c_size_t)]
+
+
+class gdn_rope_opts(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int), ("scaling", ctypes.c_int), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class gdn_rope(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("layout", ctypes.c_int), ("magnitude", ctypes.c_float)]
+
+
+class gdn_rope_dims(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("T", ctypes.c_int), ("h_q", ctypes.c_int), ("h_k", ctypes.c_int),
+                ("norm", ctypes.c_int), ("eps", ctypes.c_float), ("dtype", ctypes.c_int), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64),
+                ("dq_stride", ctypes.c_int64), ("dk_stride", ctypes.c_int64)]
+
+
+class gdn_conv_dims(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("T", ctypes.c_int), ("h_qk", ctypes.c_int), ("h_v", ctypes.c_int),
+                ("width", ctypes.c_int), ("activation", ctypes.c_int), ("norm", ctypes.c_int), ("eps", ctypes.c_float),
+                ("dtype", ctypes.c_int), ("x_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -145,6 +174,19 @@ def load(path: str = LIB_PATH):
         lib.gdn_kv_attn_plan.restype = ctypes.c_int
         lib.gdn_kv_attn.argtypes = [vp, vp, vp, vp, kc, vp, vp, kd, kp, vp, ctypes.c_size_t, vp]
         lib.gdn_kv_attn.restype = ctypes.c_int
+        rp, rd, cd, sp = (ctypes.POINTER(x) for x in (gdn_rope, gdn_rope_dims, gdn_conv_dims, ctypes.c_size_t))
+        for name, args in (("gdn_rope_table", [ctypes.POINTER(gdn_rope_opts), ctypes.POINTER(ctypes.c_uint64)]),
+                           ("gdn_qk_rope", [vp] * 6 + [rp, vp, vp, rd, vp]),
+                           ("gdn_qk_rope_bwd_workspace_bytes", [sp]),
+                           ("gdn_qk_rope_bwd", [vp] * 6 + [rp] + [vp] * 6 + [rd, vp, ctypes.c_size_t, vp]),
+                           ("gdn_kv_append_rope", [vp] * 9 + [kc, kd, rp, ctypes.c_int, ctypes.c_float, vp]),
+                           ("gdn_conv_fwd", [vp] * 9 + [cd, vp]),
+                           ("gdn_conv_bwd_workspace_bytes", [cd, sp]),
+                           ("gdn_conv_bwd", [vp] * 13 + [cd, vp, ctypes.c_size_t, vp]),
+                           ("gdn_conv_step", [vp] * 7 + [cd, vp])):
+            fn = getattr(lib, name)
+            fn.argtypes = args
+            fn.restype = ctypes.c_int
         _lib = lib
         return lib
 

@@ -479,3 +479,372 @@ def gdn_kv_attn(q: torch.Tensor, cache: KVCache, kv_lens: torch.Tensor, page_tab
                               workspace.numel(), _raw_stream(stream, q))
     L.check(st, "gdn_kv_attn")
     return out, lse
+
+
+_SCALINGS = {"none": L.GDN_ROPE_PLAIN, "linear": L.GDN_ROPE_LINEAR, "ntk": L.GDN_ROPE_NTK, "parts": L.GDN_ROPE_PARTS}
+_LAYOUTS = {"half": L.GDN_ROPE_HALF, "interleaved": L.GDN_ROPE_INTERLEAVED}
+_NORMS = {"none": L.GDN_NORM_NONE, "rms": L.GDN_NORM_RMS, "unit": L.GDN_NORM_UNIT}
+_ACTIVATIONS = {"none": L.GDN_ACT_NONE, "silu": L.GDN_ACT_SILU}
+
+
+def _choice(what: str, table: dict, name: str) -> int:
+    if name not in table:
+        raise ValueError(f"{what} must be one of {', '.join(table)}")
+    return table[name]
+
+
+class Rope:
+    """Rotary positions (gdn_rope): turns int64 [rot / 2] on the device, the bits
+    of gdn_rope_table's uint64; layout "half" or "interleaved"; magnitude of the
+    turned elements (0: 1).  gdn_rope_table makes one."""
+
+    def __init__(self, turns: torch.Tensor, layout: str = "half", magnitude: float = 0.0):
+        if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+            raise ValueError("turns must be contiguous int64 [rot / 2]")
+        self.turns, self.rot, self.device_index = turns, 2 * turns.shape[0], turns.get_device()
+        self.raw = L.gdn_rope(turns.data_ptr(), self.rot, _choice("layout", _LAYOUTS, layout), magnitude)
+
+
+def gdn_rope_table(rot: int = 128, *, base: float = 10000.0, layout: str = "half", scaling: str = "none", factor: float = 1.0,
+                   original_len: float = 0.0, low: float = 1.0, high: float = 32.0, magnitude: float = 0.0,
+                   device="cuda") -> Rope:
+    """The frequencies of rotary positions (gdn_rope_table), for the first `rot`
+    elements of a head.  scaling, for contexts `factor` times longer: "none",
+    "linear", "ntk" or "parts" (by the turns a pair makes over original_len
+    tokens: up to `low` slowed down, from `high` on kept)."""
+    opts = L.gdn_rope_opts(rot, _choice("scaling", _SCALINGS, scaling), base, factor, original_len, low, high)
+    turns = (ctypes.c_uint64 * max(1, rot // 2))()
+    L.check(L.load().gdn_rope_table(opts, turns), "gdn_rope_table")
+    signed = [x - (1 << 64) if x >> 63 else x for x in turns]
+    return Rope(torch.tensor(signed, dtype=torch.int64, device=device), layout, magnitude)
+
+
+def _tokens(name: str, t: torch.Tensor, inner: int, like: torch.Tensor) -> int:
+    """Token stride of [T, ..] or [B, T, ..] whose last `inner` dimensions are a
+    token, whole, the tokens evenly spaced; 0: packed.  Of `like`'s type and device."""
+    if t.dtype != like.dtype or t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be of the call's type and on its device")
+    if t.is_contiguous():
+        return 0
+    shape, strides = t.shape, t.stride()
+    lead = len(shape) - inner
+    if strides[-1] != 1 or (inner == 2 and shape[-2] > 1 and strides[-2] != shape[-1]):
+        raise ValueError(f"{name}: a token's elements must be contiguous")
+    n, step = shape[lead - 1], strides[lead - 1]
+    if lead == 2 and shape[0] > 1:
+        if n > 1 and strides[0] != n * step:
+            raise ValueError(f"{name}: tokens must be evenly spaced")
+        n, step = shape[0] * n, step if n > 1 else strides[0]
+    if n <= 1:
+        return 0
+    if step < (shape[-1] if inner == 1 else shape[-2] * shape[-1]):
+        # an expanded view's 0 would select packed tokens, past the end of what lies behind it
+        raise ValueError(f"{name}: tokens must not overlap")
+    return step
+
+
+def _f32(name: str, t: Optional[torch.Tensor], shape, device: int):
+    """Address of a float32 tensor, or None."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be contiguous float32 {list(shape)} on the call's device")
+    return t.data_ptr()
+
+
+def _i32(name: str, t: Optional[torch.Tensor], numel: int, device: int):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() != numel or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name} must be contiguous int32 with {numel} elements on the call's device")
+    return t.data_ptr()
+
+
+def _rope_raw(rope: Optional[Rope], device: int):
+    if rope is None:
+        return None
+    if rope.device_index != device:
+        raise ValueError("rope must be on the call's device")
+    return rope.raw
+
+
+def _sequences(lead, cu_seqlens: Optional[torch.Tensor]) -> int:
+    """Sequences of a call whose tensors begin with the dimensions [T] or [B, T]."""
+    if cu_seqlens is None:
+        return lead[0] if len(lead) == 2 else 1
+    if len(lead) == 2 and lead[0] != 1:
+        raise ValueError("cu_seqlens is for packed tokens, not for a batch of rows")
+    return cu_seqlens.numel() - 1
+
+
+def _qk(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions, cu_seqlens, norm, eps, rope):
+    """(a tensor of the call, its lead, dims without strides, addresses of positions and offsets, rope)."""
+    any_ = q if q is not None else k
+    if any_ is None:
+        raise ValueError("q or k is needed")
+    for name, t in (("q", q), ("k", k)):
+        if t is not None and (t.dim() not in (3, 4) or t.shape[-1] != 128 or t.shape[:-2] != any_.shape[:-2]):
+            raise ValueError(f"{name} must be [T, heads, 128] or [B, T, heads, 128], alike in q and k")
+    dev = any_.get_device()
+    if dev < 0:
+        raise ValueError("the tensors must be on a GPU")
+    lead = any_.shape[:-2]
+    T = lead.numel()
+    n = _sequences(lead, cu_seqlens)
+    dims = L.gdn_rope_dims(n, T, 0 if q is None else q.shape[-2], 0 if k is None else k.shape[-2], _choice("norm", _NORMS, norm),
+                           eps, _DT.get(any_.dtype, -1))
+    return any_, dims, _i32("positions", positions, T, dev), _i32("cu_seqlens", cu_seqlens, n + 1, dev), _rope_raw(rope, dev)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def gdn_qk_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: Optional[Rope] = None,
+                positions: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, *, norm: str = "none",
+                q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 0.0,
+                q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Queries and keys, each head normalised ("none", "rms" or "unit"), then
+    rotated by its token's position (gdn_qk_rope): q [T, h_q, 128], k [T, h_k, 128]
+    or with a batch in front, bf16 or fp32; either may be None.  Positions: int32,
+    one a token; else counted within each sequence of cu_seqlens, or each row.
+    The tensors may be parts of one projection; an output may be its input.
+    Returns (q_out, k_out), without a history (gdn_qk_rope_bwd)."""
+    x, dims, pos, cu, raw = _qk(q, k, positions, cu_seqlens, norm, eps, rope)
+    dev = x.get_device()
+    handle = _raw_stream(stream, x)
+    if q is not None:
+        dims.q_stride = _tokens("q", q, 2, x)
+        if q_out is None:
+            q_out = _kv_empty(q.shape, q.dtype, q.device, stream)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must be like q")
+        dims.q_out_stride = _tokens("q_out", q_out, 2, x)
+    if k is not None:
+        dims.k_stride = _tokens("k", k, 2, x)
+        if k_out is None:
+            k_out = _kv_empty(k.shape, k.dtype, k.device, stream)
+        elif k_out.shape != k.shape:
+            raise ValueError("k_out must be like k")
+        dims.k_out_stride = _tokens("k_out", k_out, 2, x)
+    st = L.load().gdn_qk_rope(_at(q), _at(k), _f32("q_weight", q_weight, (128,), dev), _f32("k_weight", k_weight, (128,), dev),
+                              pos, cu, raw, _at(q_out), _at(k_out), dims, handle)
+    L.check(st, "gdn_qk_rope")
+    return q_out, k_out
+
+
+def gdn_qk_rope_bwd_workspace_bytes() -> int:
+    """Device workspace of gdn_qk_rope_bwd, whatever its sizes."""
+    n = ctypes.c_size_t(0)
+    L.check(L.load().gdn_qk_rope_bwd_workspace_bytes(n), "gdn_qk_rope_bwd_workspace_bytes")
+    return int(n.value)
+
+
+def gdn_qk_rope_bwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor], d_q_out: Optional[torch.Tensor],
+                    d_k_out: Optional[torch.Tensor], rope: Optional[Rope] = None, positions: Optional[torch.Tensor] = None,
+                    cu_seqlens: Optional[torch.Tensor] = None, *, norm: str = "none", q_weight: Optional[torch.Tensor] = None,
+                    k_weight: Optional[torch.Tensor] = None, eps: float = 0.0, d_q: Optional[torch.Tensor] = None,
+                    d_k: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of gdn_qk_rope (gdn_qk_rope_bwd), whose inputs come again.
+    Returns (d_q, d_k, d_q_weight, d_k_weight), the latter fp32 [128] and None
+    without the weight.  d_q may be d_q_out, d_k may be d_k_out."""
+    if (q is None) != (d_q_out is None) or (k is None) != (d_k_out is None):
+        raise ValueError("d_q_out and d_k_out go with q and k")
+    x, dims, pos, cu, raw = _qk(q, k, positions, cu_seqlens, norm, eps, rope)
+    dev = x.get_device()
+    handle = _raw_stream(stream, x)
+    for name, t, g in (("q", q, d_q_out), ("k", k, d_k_out)):
+        if t is not None and g.shape != t.shape:
+            raise ValueError(f"d_{name}_out must be like {name}")
+    if q is not None:
+        dims.q_stride, dims.q_out_stride = _tokens("q", q, 2, x), _tokens("d_q_out", d_q_out, 2, x)
+        if d_q is None:
+            d_q = _kv_empty(q.shape, q.dtype, q.device, stream)
+        elif d_q.shape != q.shape:
+            raise ValueError("d_q must be like q")
+        dims.dq_stride = _tokens("d_q", d_q, 2, x)
+    if k is not None:
+        dims.k_stride, dims.k_out_stride = _tokens("k", k, 2, x), _tokens("d_k_out", d_k_out, 2, x)
+        if d_k is None:
+            d_k = _kv_empty(k.shape, k.dtype, k.device, stream)
+        elif d_k.shape != k.shape:
+            raise ValueError("d_k must be like k")
+        dims.dk_stride = _tokens("d_k", d_k, 2, x)
+    qw, kw = _f32("q_weight", q_weight, (128,), dev), _f32("k_weight", k_weight, (128,), dev)
+    dqw = None if qw is None else _kv_empty((128,), torch.float32, x.device, stream)
+    dkw = None if kw is None else _kv_empty((128,), torch.float32, x.device, stream)
+    if workspace is None and (dqw is not None or dkw is not None):
+        workspace = _kv_empty(gdn_qk_rope_bwd_workspace_bytes(), torch.uint8, x.device, stream)
+    st = L.load().gdn_qk_rope_bwd(_at(q), _at(k), qw, kw, pos, cu, raw, _at(d_q_out), _at(d_k_out), _at(d_q), _at(d_k), _at(dqw),
+                                  _at(dkw), dims, *_workspace(workspace, dev), handle)
+    L.check(st, "gdn_qk_rope_bwd")
+    return d_q, d_k, dqw, dkw
+
+
+def _workspace(t: Optional[torch.Tensor], device: int):
+    """(address, bytes) of a call's workspace."""
+    if t is None:
+        return None, 0
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous, on the call's device")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def gdn_kv_append_rope(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_lens: torch.Tensor, page_table: torch.Tensor,
+                       cu_seqlens: Optional[torch.Tensor] = None, *, rope: Optional[Rope] = None, norm: str = "none",
+                       k_weight: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                       q_weight: Optional[torch.Tensor] = None, eps: float = 0.0, q_out: Optional[torch.Tensor] = None,
+                       stream=None) -> Optional[torch.Tensor]:
+    """gdn_kv_append of keys that are normalised and rotated on the way, and the
+    queries of the same tokens beside them, in one launch (gdn_kv_append_rope).
+    Positions are those of the cache.  Returns q_out [T, h_q, 128], or None
+    without q; q_out may be q itself."""
+    n, max_pages, cu = _kv_ints(cache, kv_lens, page_table, cu_seqlens)
+    dev = cache.device_index
+    h_kv = cache.raw.h_kv
+    ks, vs = _kv_rows("k", k, h_kv, cache), _kv_rows("v", v, h_kv, cache)
+    if v.dtype != k.dtype or v.shape != k.shape or k.shape[2] != 128:
+        raise ValueError("k and v must be alike, with 128 elements a head")
+    handle = _raw_stream(stream, k)
+    h_q, qs, outs = h_kv, 0, 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != 128 or q.dtype != k.dtype:
+            raise ValueError("q must be [T, h_q, 128], of the keys' type")
+        h_q = q.shape[1]
+        qs = _kv_rows("q", q, h_q, cache)
+        if q_out is None:
+            q_out = _kv_empty(q.shape, q.dtype, q.device, stream)
+        elif q_out.dtype != q.dtype or q_out.shape != q.shape:
+            raise ValueError("q_out must be like q")
+        outs = _kv_rows("q_out", q_out, h_q, cache)
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    dims = L.gdn_kv_dims(n, k.shape[0], h_q, max_pages, 1, 0, 0.0, _DT.get(k.dtype, -1), qs, ks, vs, outs)
+    st = L.load().gdn_kv_append_rope(k.data_ptr(), v.data_ptr(), _f32("k_weight", k_weight, (128,), dev), _at(q),
+                                     _f32("q_weight", q_weight, (128,), dev), _at(q_out), kv_lens.data_ptr(), page_table.data_ptr(),
+                                     cu, cache.raw, dims, _rope_raw(rope, dev), _choice("norm", _NORMS, norm), eps, handle)
+    L.check(st, "gdn_kv_append_rope")
+    return q_out
+
+
+def _conv(x: torch.Tensor, weight: torch.Tensor, h_qk: int, bias, cu_seqlens, activation: str, norm: bool, eps: float):
+    """(lead dimensions, value heads, dims, addresses of weight, bias and offsets) of a convolution of x."""
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [T, C] or [B, T, C]")
+    C, dev = x.shape[-1], x.get_device()
+    if dev < 0:
+        raise ValueError("the tensors must be on a GPU")
+    h_v = C // 128 - 2 * h_qk
+    if C % 128 or h_qk < 1 or h_v < 1:
+        raise ValueError("x must have (2 h_qk + h_v) * 128 channels")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [C, W]")
+    lead = x.shape[:-1]
+    n = _sequences(lead, cu_seqlens)
+    dims = L.gdn_conv_dims(n, lead.numel(), h_qk, h_v, weight.shape[1], _choice("activation", _ACTIVATIONS, activation),
+                           int(bool(norm)), eps, _DT.get(x.dtype, -1), _tokens("x", x, 1, x), 0)
+    return (lead, h_v, dims, _f32("weight", weight, (C, weight.shape[1]), dev), _f32("bias", bias, (C,), dev),
+            _i32("cu_seqlens", cu_seqlens, n + 1, dev))
+
+
+def _like(name: str, t: Optional[torch.Tensor], shape, x: torch.Tensor, stream, make: bool = True):
+    """t, checked to be contiguous, of that shape and of x's type and device; a new one for None if `make`."""
+    if t is None:
+        return _kv_empty(shape, x.dtype, x.device, stream) if make else None
+    if t.shape != shape or t.dtype != x.dtype or not t.is_contiguous() or t.get_device() != x.get_device():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, of x's type, on its device")
+    return t
+
+
+def gdn_conv_fwd(x: torch.Tensor, weight: torch.Tensor, h_qk: int, bias: Optional[torch.Tensor] = None,
+                 initial_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, *,
+                 activation: str = "silu", norm: bool = True, eps: float = 0.0, q: Optional[torch.Tensor] = None,
+                 k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, final_state: Optional[torch.Tensor] = None,
+                 output_final_state: bool = True, stream=None):
+    """The short causal convolution before the gated delta rule (gdn_conv_fwd):
+    x [T, C] packed by cu_seqlens, or [B, T, C], bf16 or fp32, C = (2 h_qk + h_v) *
+    128 channels of q, k and v; weight [C, W] fp32, bias [C] fp32 or None;
+    initial_state [N, W - 1, C] like x, or None.  norm: q's and k's heads to unit
+    length.  Returns (q, k, v, final_state or None), q, k, v as gdn_chunk_fwd
+    takes them, without a history (gdn_conv_bwd)."""
+    lead, h_v, dims, w, b, cu = _conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps)
+    handle = _raw_stream(stream, x)
+    states = (dims.n_seqs, dims.width - 1, x.shape[-1])
+    q = _like("q", q, (*lead, h_qk, 128), x, stream)
+    k = _like("k", k, (*lead, h_qk, 128), x, stream)
+    v = _like("v", v, (*lead, h_v, 128), x, stream)
+    initial_state = _like("initial_state", initial_state, states, x, stream, False)
+    final_state = _like("final_state", final_state, states, x, stream, output_final_state)
+    st = L.load().gdn_conv_fwd(x.data_ptr(), w, b, _at(initial_state), cu, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                               _at(final_state), dims, handle)
+    L.check(st, "gdn_conv_fwd")
+    return q, k, v, final_state
+
+
+def gdn_conv_bwd_workspace_bytes(T: int, h_qk: int, h_v: int, *, n_seqs: int = 1, width: int = 4,
+                                 dtype: torch.dtype = torch.bfloat16) -> int:
+    """Device workspace of gdn_conv_bwd for calls of T tokens in all (gdn_conv_bwd_workspace_bytes)."""
+    n = ctypes.c_size_t(0)
+    dims = L.gdn_conv_dims(n_seqs, T, h_qk, h_v, width, L.GDN_ACT_SILU, 1, 0.0, _DT.get(dtype, -1), 0, 0)
+    L.check(L.load().gdn_conv_bwd_workspace_bytes(dims, n), "gdn_conv_bwd_workspace_bytes")
+    return int(n.value)
+
+
+def gdn_conv_bwd(x: torch.Tensor, weight: torch.Tensor, h_qk: int, d_q: torch.Tensor, d_k: torch.Tensor, d_v: torch.Tensor,
+                 bias: Optional[torch.Tensor] = None, initial_state: Optional[torch.Tensor] = None,
+                 d_final_state: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None, *,
+                 activation: str = "silu", norm: bool = True, eps: float = 0.0, dx: Optional[torch.Tensor] = None,
+                 want_initial_state_grad: Optional[bool] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of gdn_conv_fwd (gdn_conv_bwd), whose inputs come again; d_q, d_k,
+    d_v and d_final_state (None: zero) like its outputs.  Returns (dx, d_weight,
+    d_bias or None, d_initial_state or None): the bias's without a bias and, unless
+    want_initial_state_grad says so, the state's without a state are None."""
+    lead, h_v, dims, w, b, cu = _conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps)
+    handle = _raw_stream(stream, x)
+    states = (dims.n_seqs, dims.width - 1, x.shape[-1])
+    d_q = _like("d_q", d_q, (*lead, h_qk, 128), x, stream, False)
+    d_k = _like("d_k", d_k, (*lead, h_qk, 128), x, stream, False)
+    d_v = _like("d_v", d_v, (*lead, h_v, 128), x, stream, False)
+    initial_state = _like("initial_state", initial_state, states, x, stream, False)
+    d_final_state = _like("d_final_state", d_final_state, states, x, stream, False)
+    if dx is None:
+        dx = _kv_empty(x.shape, x.dtype, x.device, stream)
+    elif dx.shape != x.shape:
+        raise ValueError("dx must be like x")
+    dims.dx_stride = _tokens("dx", dx, 1, x)
+    want = initial_state is not None if want_initial_state_grad is None else want_initial_state_grad
+    d_state = _kv_empty(states, x.dtype, x.device, stream) if want else None
+    d_weight = _kv_empty(weight.shape, torch.float32, x.device, stream)
+    d_bias = None if bias is None else _kv_empty(bias.shape, torch.float32, x.device, stream)
+    lib = L.load()
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        L.check(lib.gdn_conv_bwd_workspace_bytes(dims, n), "gdn_conv_bwd_workspace_bytes")
+        workspace = _kv_empty(max(256, int(n.value)), torch.uint8, x.device, stream)
+    st = lib.gdn_conv_bwd(x.data_ptr(), w, b, _at(initial_state), cu, _at(d_q), _at(d_k), _at(d_v), _at(d_final_state),
+                          dx.data_ptr(), d_weight.data_ptr(), _at(d_bias), _at(d_state), dims,
+                          *_workspace(workspace, x.get_device()), handle)
+    L.check(st, "gdn_conv_bwd")
+    return dx, d_weight, d_bias, d_state
+
+
+def gdn_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, h_qk: int, bias: Optional[torch.Tensor] = None, *,
+                  activation: str = "silu", norm: bool = True, eps: float = 0.0, q: Optional[torch.Tensor] = None,
+                  k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, stream=None):
+    """One new token a sequence (gdn_conv_step): x [N, C], state [N, W - 1, C] like x,
+    gdn_conv_fwd's final_state, updated in place.  Returns (q, k, v), [N, heads,
+    128], as gdn_decode_step takes them."""
+    if x.dim() != 2:
+        raise ValueError("x must be [N, C]")
+    lead, h_v, dims, w, b, _ = _conv(x, weight, h_qk, bias, None, activation, norm, eps)
+    dims.n_seqs = dims.T
+    handle = _raw_stream(stream, x)
+    if state is None:
+        raise ValueError("state is needed")
+    _like("state", state, (dims.T, dims.width - 1, x.shape[1]), x, stream)
+    q = _like("q", q, (*lead, h_qk, 128), x, stream)
+    k = _like("k", k, (*lead, h_qk, 128), x, stream)
+    v = _like("v", v, (*lead, h_v, 128), x, stream)
+    st = L.load().gdn_conv_step(x.data_ptr(), w, b, state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), dims, handle)
+    L.check(st, "gdn_conv_step")
+    return q, k, v

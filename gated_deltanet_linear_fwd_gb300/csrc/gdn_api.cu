@@ -5,12 +5,16 @@
 #include <cmath>
 #include <climits>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
 #include "gdn.h"
 #include "gdn_internal.cuh"
+#include "gdn_conv.cuh"
 #include "gdn_kv.cuh"
+#include "gdn_kv_page.cuh"
+#include "gdn_rope.cuh"
 
 using namespace gdn;
 
@@ -335,31 +339,174 @@ KvArgs kv_args(const gdn_kv_dims* d, const gdn_kv_cache* c, const int32_t* lens,
   return a;
 }
 
+// What moving keys and values in or out takes beside the tensors, and the
+// number of page slots of the call.
+gdn_status kv_moves(const gdn_kv_dims* d, const gdn_kv_cache* cache, const int32_t* lens, const int32_t* table,
+                    const int32_t* cu, KvAppendArgs* a, unsigned* n_entries) {
+  gdn_status st;
+  if ((st = kv_stride(d->k_stride, cache->h_kv, d->dtype, &a->k_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->v_stride, cache->h_kv, d->dtype, &a->v_stride)) != GDN_OK) return st;
+  a->c = kv_args(d, cache, lens, table, cu);
+  // n tokens from any position lie in at most (n + 62) / 64 + 1 pages
+  a->pages_each = cu ? 0 : (a->c.n_each + 62) / kPage + 1;
+  const int64_t entries = cu ? (int64_t)d->T / kPage + 2 * (int64_t)std::min(d->n_seqs, d->T)
+                             : (int64_t)d->n_seqs * a->pages_each;
+  if (entries > 0x7fffffff) return GDN_ERR_INVALID_ARG;
+  *n_entries = (unsigned)entries;
+  return GDN_OK;
+}
+
 gdn_status kv_move(bool read, void* k, void* v, const int32_t* lens, const int32_t* table, const int32_t* cu,
                    const gdn_kv_cache* cache, const gdn_kv_dims* d, void* stream) {
   gdn_status st = check_kv(d, cache, lens, table, cu);
   if (st != GDN_OK) return st;
   KvAppendArgs a;
-  if ((st = kv_stride(d->k_stride, cache->h_kv, d->dtype, &a.k_stride)) != GDN_OK) return st;
-  if ((st = kv_stride(d->v_stride, cache->h_kv, d->dtype, &a.v_stride)) != GDN_OK) return st;
+  unsigned entries = 0;
+  if ((st = kv_moves(d, cache, lens, table, cu, &a, &entries)) != GDN_OK) return st;
   if (d->T == 0) return GDN_OK;
   if (!k || !v) return GDN_ERR_INVALID_ARG;
   if (!aligned16(k) || !aligned16(v)) return GDN_ERR_MISALIGNED;
-  a.c = kv_args(d, cache, lens, table, cu);
   a.k = k;
   a.v = v;
-  // n tokens from any position lie in at most (n + 62) / 64 + 1 pages
-  a.pages_each = cu ? 0 : (a.c.n_each + 62) / kPage + 1;
-  const int64_t entries = cu ? (int64_t)d->T / kPage + 2 * (int64_t)std::min(d->n_seqs, d->T)
-                             : (int64_t)d->n_seqs * a.pages_each;
-  if (entries > 0x7fffffff) return GDN_ERR_INVALID_ARG;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const bool f32 = d->dtype == GDN_F32;
   LaunchLog log;
   cudaError_t e = log.before(cs);
-  if (e == cudaSuccess) e = read ? launch_kv_read(a, f32, (unsigned)entries, cs) : launch_kv_append(a, f32, (unsigned)entries, cs);
+  if (e == cudaSuccess) e = read ? launch_kv_read(a, f32, entries, cs) : launch_kv_append(a, f32, entries, cs);
   if (e == cudaSuccess) e = log.after(read ? "kv_read" : "kv_append", cs);
   return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+// ---- between the projections and the mixers ----
+bool misaligned16(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!aligned16(p)) return true;
+  return false;
+}
+
+// eps of a norm: 0 selects the default.  From 1e-20 on, squares that fp32 drops
+// (below 1e-38 each, 128 of them) are nothing beside it.
+gdn_status norm_eps(float given, float* out) {
+  *out = given == 0.f ? 1e-6f : given;
+  return std::isfinite(*out) && *out >= 1e-20f ? GDN_OK : GDN_ERR_INVALID_ARG;
+}
+
+gdn_status rope_args(const gdn_rope* rope, int norm, float eps, RopeArgs* r) {
+  if (norm < GDN_NORM_NONE || norm > GDN_NORM_UNIT) return GDN_ERR_UNSUPPORTED;
+  r->turns = nullptr;
+  r->rot = r->interleaved = 0;
+  r->magnitude = 1.f;
+  r->norm = norm;
+  r->inv_n = norm == GDN_NORM_RMS ? 1.0f / kRopeD : 1.0f;
+  if (rope) {
+    if (rope->rot < 0 || rope->rot > kRopeD || rope->rot % 8) return GDN_ERR_UNSUPPORTED;
+    if (rope->layout != GDN_ROPE_HALF && rope->layout != GDN_ROPE_INTERLEAVED) return GDN_ERR_UNSUPPORTED;
+    if (!std::isfinite(rope->magnitude) || rope->magnitude < 0.f) return GDN_ERR_INVALID_ARG;
+    if (rope->rot && !rope->turns) return GDN_ERR_INVALID_ARG;
+    if (rope->rot && !aligned16(rope->turns)) return GDN_ERR_MISALIGNED;
+    r->turns = rope->turns;
+    r->rot = rope->rot;
+    r->interleaved = rope->layout;
+    if (rope->magnitude != 0.f) r->magnitude = rope->magnitude;
+  }
+  return norm_eps(eps, &r->eps);
+}
+
+// Half-warps that share a token's heads: one, whose cosines then serve all
+// of them, unless the tokens are too few to fill the GPU.
+int rope_splits(int64_t T, int heads) {
+  constexpr int64_t kFill = 152 * 64;  // half-warps that are resident
+  return (int)std::min<int64_t>(heads, std::max<int64_t>(1, kFill / std::max<int64_t>(T, 1)));
+}
+
+// Checks of gdn_qk_rope and its gradient that do not need the tensors.
+gdn_status qk_rope_args(const gdn_rope_dims* d, const gdn_rope* rope, const float* q_weight, const float* k_weight,
+                        const int32_t* positions, const int32_t* cu, QkRopeArgs* a) {
+  if (!d) return GDN_ERR_INVALID_ARG;
+  if (d->dtype != GDN_BF16 && d->dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if (d->n_seqs < 1 || d->T < 0 || d->h_q < 0 || d->h_k < 0 || d->h_q > 65535 || d->h_k > 65535 || d->h_q + d->h_k < 1)
+    return GDN_ERR_INVALID_ARG;
+  if (!positions && !cu && d->T % d->n_seqs) return GDN_ERR_INVALID_ARG;
+  std::memset(a, 0, sizeof(*a));
+  gdn_status st = rope_args(rope, d->norm, d->eps, &a->r);
+  if (st != GDN_OK) return st;
+  if (d->norm == GDN_NORM_NONE && (q_weight || k_weight)) return GDN_ERR_INVALID_ARG;
+  if (misaligned16({q_weight, k_weight}) || (reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(cu)) & 3u)
+    return GDN_ERR_MISALIGNED;
+  if ((st = kv_stride(d->q_stride, d->h_q, d->dtype, &a->q_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->k_stride, d->h_k, d->dtype, &a->k_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->q_out_stride, d->h_q, d->dtype, &a->q_out_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->k_out_stride, d->h_k, d->dtype, &a->k_out_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->dq_stride, d->h_q, d->dtype, &a->dq_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->dk_stride, d->h_k, d->dtype, &a->dk_stride)) != GDN_OK) return st;
+  a->pos = {positions, cu, d->n_seqs, d->T, positions || cu ? 0 : d->T / d->n_seqs};
+  a->q_weight = q_weight;
+  a->k_weight = k_weight;
+  a->h_q = d->h_q;
+  a->h_k = d->h_k;
+  a->splits = rope_splits(d->T, d->h_q + d->h_k);
+  return GDN_OK;
+}
+
+constexpr int kRopeBwdCtas = 1024;  // rows of the workspace: CTAs of the gradient, at most
+
+// Tokens a group of lanes takes in a row: more of them read less twice (the W - 1
+// before each run), fewer fill the GPU.  `fill`: groups that are resident.
+int conv_run(int64_t T, int64_t heads, int64_t fill, int least) {
+  int run = 64;
+  while (run > least && (T + run - 1) / run * heads < fill) run >>= 1;
+  return run;
+}
+constexpr int64_t kConvFill = 152 * 64;   // half-warps
+constexpr int64_t kConvBwdFill = 152 * 24;  // warps
+
+gdn_status conv_args(const gdn_conv_dims* d, const float* weight, const float* bias, const int32_t* cu, ConvArgs* a) {
+  if (!d) return GDN_ERR_INVALID_ARG;
+  if (d->dtype != GDN_BF16 && d->dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if (d->width < 2 || d->width > kConvMaxTaps) return GDN_ERR_UNSUPPORTED;
+  if (d->activation != GDN_ACT_NONE && d->activation != GDN_ACT_SILU) return GDN_ERR_UNSUPPORTED;
+  if (d->norm != 0 && d->norm != 1) return GDN_ERR_UNSUPPORTED;
+  if (d->n_seqs < 1 || d->T < 0 || d->h_qk < 1 || d->h_v < 1 || d->h_qk > 16384 || d->h_v > 32768) return GDN_ERR_INVALID_ARG;
+  if (!cu && d->T % d->n_seqs) return GDN_ERR_INVALID_ARG;
+  std::memset(a, 0, sizeof(*a));
+  gdn_status st = norm_eps(d->eps, &a->eps);
+  if (st != GDN_OK) return st;
+  const int heads = 2 * d->h_qk + d->h_v;
+  if ((st = kv_stride(d->x_stride, heads, d->dtype, &a->x_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->dx_stride, heads, d->dtype, &a->dx_stride)) != GDN_OK) return st;
+  // what is indexed by 32-bit block numbers
+  if ((int64_t)d->T * heads >= (int64_t)1 << 33 || (int64_t)d->n_seqs * heads >= (int64_t)1 << 30) return GDN_ERR_INVALID_ARG;
+  if (misaligned16({weight, bias}) || reinterpret_cast<uintptr_t>(cu) & 3u) return GDN_ERR_MISALIGNED;
+  a->weight = weight;
+  a->bias = bias;
+  a->cu = cu;
+  a->n_seqs = d->n_seqs;
+  a->T = d->T;
+  a->n_each = cu ? 0 : d->T / d->n_seqs;
+  a->h_qk = d->h_qk;
+  a->h_v = d->h_v;
+  a->width = d->width;
+  a->silu = d->activation == GDN_ACT_SILU;
+  a->norm = d->norm;
+  return GDN_OK;
+}
+
+bool overlap(const void* a, const void* b, size_t bytes) {
+  if (!a || !b) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bytes && y < x + bytes;
+}
+size_t conv_state_bytes(const gdn_conv_dims* d) {
+  return (size_t)d->n_seqs * (d->width - 1) * (2 * d->h_qk + d->h_v) * kConvD * (d->dtype == GDN_F32 ? 4 : 2);
+}
+constexpr int kConvBwdWarps = 8;  // runs of a CTA of the gradient
+// Sets the run and the number of groups of the gradient; returns its workspace.
+size_t conv_bwd_plan(const gdn_conv_dims* d, ConvArgs* a) {
+  const int heads = 2 * d->h_qk + d->h_v;
+  a->run = conv_run(d->T, heads, kConvBwdFill, 8);
+  const int64_t runs = ((int64_t)d->T + a->run - 1) / a->run;
+  a->groups = (int)((runs + kConvBwdWarps - 1) / kConvBwdWarps);
+  return (size_t)a->groups * (d->width + 1) * heads * kConvD * sizeof(float);
 }
 
 // A pool of codes as [page and head][64 tokens][128 bytes]: boxes of one page's
@@ -1047,6 +1194,244 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* lens, const int32_t* table,
     if (e == cudaSuccess) e = launch_kv_combine(a, f32, cs);
     if (e == cudaSuccess) e = log.after("kv_combine", cs);
   }
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+gdn_status gdn_rope_table(const gdn_rope_opts* o, uint64_t* turns) {
+  if (!o || !turns) return GDN_ERR_INVALID_ARG;
+  if (o->rot < 8 || o->rot > kRopeD || o->rot % 8 || o->scaling < GDN_ROPE_PLAIN || o->scaling > GDN_ROPE_PARTS)
+    return GDN_ERR_UNSUPPORTED;
+  const double factor = o->scaling == GDN_ROPE_PLAIN ? 1.0 : o->factor;
+  if (!std::isfinite(o->base) || !(o->base > 1.0) || !std::isfinite(factor) || !(factor >= 1.0)) return GDN_ERR_INVALID_ARG;
+  if (o->scaling == GDN_ROPE_PARTS &&
+      (!std::isfinite(o->original_len) || !(o->original_len > 0.0) || !std::isfinite(o->low) || !std::isfinite(o->high) ||
+       !(o->low < o->high)))
+    return GDN_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925286766559;
+  double base = o->base;
+  if (o->scaling == GDN_ROPE_NTK) base *= std::pow(factor, (double)o->rot / (o->rot - 2));
+  for (int i = 0; i < o->rot / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / o->rot);
+    if (o->scaling == GDN_ROPE_LINEAR) f /= factor;
+    if (o->scaling == GDN_ROPE_PARTS) {
+      const double r = o->original_len * f / two_pi;
+      const double keep = std::min(1.0, std::max(0.0, (r - o->low) / (o->high - o->low)));
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    turns[i] = (uint64_t)std::nearbyint(std::ldexp(f / two_pi, 64));  // f <= 1: below 2^62
+  }
+  return GDN_OK;
+}
+
+gdn_status gdn_qk_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                       const int32_t* positions, const int32_t* cu, const gdn_rope* rope, void* q_out, void* k_out,
+                       const gdn_rope_dims* d, void* stream) {
+  QkRopeArgs a;
+  gdn_status st = qk_rope_args(d, rope, q_weight, k_weight, positions, cu, &a);
+  if (st != GDN_OK) return st;
+  if (d->T == 0) return GDN_OK;
+  if ((d->h_q && (!q || !q_out)) || (d->h_k && (!k || !k_out))) return GDN_ERR_INVALID_ARG;
+  if (misaligned16({q, k, q_out, k_out})) return GDN_ERR_MISALIGNED;
+  a.q = q;
+  a.k = k;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  LaunchLog log;
+  cudaError_t e = log.before(cs);
+  if (e == cudaSuccess) e = launch_qk_rope(a, d->dtype == GDN_F32, cs);
+  if (e == cudaSuccess) e = log.after("qk_rope", cs);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+gdn_status gdn_qk_rope_bwd_workspace_bytes(size_t* bytes) {
+  if (!bytes) return GDN_ERR_INVALID_ARG;
+  *bytes = (size_t)kRopeBwdCtas * 2 * kRopeD * sizeof(float);
+  return GDN_OK;
+}
+
+gdn_status gdn_qk_rope_bwd(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                           const int32_t* positions, const int32_t* cu, const gdn_rope* rope, const void* d_q_out,
+                           const void* d_k_out, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                           const gdn_rope_dims* d, void* workspace, size_t workspace_bytes, void* stream) {
+  QkRopeArgs a;
+  gdn_status st = qk_rope_args(d, rope, q_weight, k_weight, positions, cu, &a);
+  if (st != GDN_OK) return st;
+  if ((dq_weight && !q_weight) || (dk_weight && !k_weight)) return GDN_ERR_INVALID_ARG;
+  if (misaligned16({dq_weight, dk_weight, workspace})) return GDN_ERR_MISALIGNED;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  const bool sums = dq_weight || dk_weight;
+  if (d->T == 0) {
+    if (dq_weight) e = cudaMemsetAsync(dq_weight, 0, kRopeD * sizeof(float), cs);
+    if (e == cudaSuccess && dk_weight) e = cudaMemsetAsync(dk_weight, 0, kRopeD * sizeof(float), cs);
+    return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+  }
+  const bool read = d->norm != GDN_NORM_NONE;
+  if ((d->h_q && ((read && !q) || !d_q_out || !dq)) || (d->h_k && ((read && !k) || !d_k_out || !dk))) return GDN_ERR_INVALID_ARG;
+  if (misaligned16({q, k, d_q_out, d_k_out, dq, dk})) return GDN_ERR_MISALIGNED;
+  size_t need = 0;
+  gdn_qk_rope_bwd_workspace_bytes(&need);
+  if (sums && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  int dev = 0;
+  if ((st = device_setup(&dev)) != GDN_OK) return st;
+  a.q = q;
+  a.k = k;
+  a.q_out = const_cast<void*>(d_q_out);
+  a.k_out = const_cast<void*>(d_k_out);
+  a.dq = dq;
+  a.dk = dk;
+  a.part = sums ? static_cast<float*>(workspace) : nullptr;
+  a.dq_weight = dq_weight;
+  a.dk_weight = dk_weight;
+  const int64_t blocks = ((int64_t)d->T * a.splits + 15) / 16;
+  const int ctas = (int)std::min<int64_t>(blocks, std::min(kRopeBwdCtas, 4 * g_sm_count[dev]));
+  LaunchLog log;
+  e = log.before(cs);
+  if (e == cudaSuccess) e = launch_qk_rope_bwd(a, d->dtype == GDN_F32, ctas, cs);
+  if (e == cudaSuccess) e = log.after("qk_rope_bwd", cs);
+  if (sums) {
+    if (e == cudaSuccess) e = log.before(cs);
+    if (e == cudaSuccess) e = launch_qk_rope_weights(a, ctas, cs);
+    if (e == cudaSuccess) e = log.after("qk_rope_weights", cs);
+  }
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+gdn_status gdn_kv_append_rope(const void* k, const void* v, const float* k_weight, const void* q,
+                              const float* q_weight, void* q_out, const int32_t* lens, const int32_t* table,
+                              const int32_t* cu, const gdn_kv_cache* cache, const gdn_kv_dims* d, const gdn_rope* rope,
+                              int norm, float eps, void* stream) {
+  gdn_status st = check_kv(d, cache, lens, table, cu);
+  if (st != GDN_OK) return st;
+  KvRopeArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if ((st = rope_args(rope, norm, eps, &a.r)) != GDN_OK) return st;
+  if (norm == GDN_NORM_NONE && (q_weight || k_weight)) return GDN_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr) || (!q && q_weight)) return GDN_ERR_INVALID_ARG;
+  if (q && (d->h_q < 1 || d->h_q > 65535)) return GDN_ERR_INVALID_ARG;
+  if (misaligned16({q_weight, k_weight, q, q_out})) return GDN_ERR_MISALIGNED;
+  if ((st = kv_moves(d, cache, lens, table, cu, &a.p, &a.entries)) != GDN_OK) return st;
+  if (q) {
+    if ((st = kv_stride(d->q_stride, d->h_q, d->dtype, &a.q_stride)) != GDN_OK) return st;
+    if ((st = kv_stride(d->out_stride, d->h_q, d->dtype, &a.q_out_stride)) != GDN_OK) return st;
+    a.splits = rope_splits(d->T, d->h_q);
+  }
+  if (d->T == 0) return GDN_OK;
+  if (!k || !v) return GDN_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v)) return GDN_ERR_MISALIGNED;
+  a.p.k = const_cast<void*>(k);
+  a.p.v = const_cast<void*>(v);
+  a.k_weight = k_weight;
+  a.q_weight = q_weight;
+  a.q = q;
+  a.q_out = q_out;
+  // keys and values a block each, and at most as many again of queries as T tokens make
+  if (2 * (int64_t)a.entries * cache->h_kv + ((int64_t)d->T * std::max(1, a.splits) + 15) / 16 > 0x7fffffff)
+    return GDN_ERR_INVALID_ARG;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  LaunchLog log;
+  cudaError_t e = log.before(cs);
+  if (e == cudaSuccess) e = launch_kv_append_rope(a, d->dtype == GDN_F32, cs);
+  if (e == cudaSuccess) e = log.after("kv_append_rope", cs);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+gdn_status gdn_conv_fwd(const void* x, const float* weight, const float* bias, const void* initial_state,
+                        const int32_t* cu, void* q, void* k, void* v, void* final_state, const gdn_conv_dims* d,
+                        void* stream) {
+  ConvArgs a;
+  gdn_status st = conv_args(d, weight, bias, cu, &a);
+  if (st != GDN_OK) return st;
+  if (!weight || (d->T && (!x || !q || !k || !v))) return GDN_ERR_INVALID_ARG;
+  if (misaligned16({x, initial_state, q, k, v, final_state})) return GDN_ERR_MISALIGNED;
+  if (overlap(initial_state, final_state, conv_state_bytes(d))) return GDN_ERR_INVALID_ARG;
+  a.x = x;
+  a.state = initial_state;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.final_state = final_state;
+  a.run = conv_run(d->T, 2 * d->h_qk + d->h_v, kConvFill, 4);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  LaunchLog log;
+  if (d->T == 0 && !final_state) return GDN_OK;
+  cudaError_t e = log.before(cs);
+  if (e == cudaSuccess) e = launch_conv(a, d->dtype == GDN_F32, cs);
+  if (e == cudaSuccess) e = log.after("conv", cs);
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+gdn_status gdn_conv_bwd_workspace_bytes(const gdn_conv_dims* d, size_t* bytes) {
+  if (!d || !bytes) return GDN_ERR_INVALID_ARG;
+  static const int32_t offsets[1] = {0};  // not read: lengths do not matter here
+  ConvArgs a;
+  gdn_status st = conv_args(d, nullptr, nullptr, offsets, &a);
+  if (st != GDN_OK) return st;
+  *bytes = conv_bwd_plan(d, &a);
+  return GDN_OK;
+}
+
+gdn_status gdn_conv_bwd(const void* x, const float* weight, const float* bias, const void* initial_state,
+                        const int32_t* cu, const void* d_q, const void* d_k, const void* d_v, const void* d_final_state,
+                        void* dx, float* d_weight, float* d_bias, void* d_initial_state, const gdn_conv_dims* d,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  ConvArgs a;
+  gdn_status st = conv_args(d, weight, bias, cu, &a);
+  if (st != GDN_OK) return st;
+  if (!weight || (d->T && (!x || !d_q || !d_k || !d_v || !dx))) return GDN_ERR_INVALID_ARG;
+  if (misaligned16({x, initial_state, d_q, d_k, d_v, d_final_state, dx, d_weight, d_bias, d_initial_state, workspace}))
+    return GDN_ERR_MISALIGNED;
+  if (dx && dx == x) return GDN_ERR_INVALID_ARG;  // the inputs of a run are read by the one after it
+  if (overlap(initial_state, d_initial_state, conv_state_bytes(d)) || overlap(d_final_state, d_initial_state, conv_state_bytes(d)))
+    return GDN_ERR_INVALID_ARG;
+  const size_t need = conv_bwd_plan(d, &a);
+  a.sums = d_weight || d_bias;
+  if (a.sums && need && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+  a.x = x;
+  a.state = initial_state;
+  a.q = const_cast<void*>(d_q);
+  a.k = const_cast<void*>(d_k);
+  a.v = const_cast<void*>(d_v);
+  a.d_final = d_final_state;
+  a.dx = dx;
+  a.d_weight = d_weight;
+  a.d_bias = d_bias;
+  a.d_state = d_initial_state;
+  a.part = static_cast<float*>(workspace);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  LaunchLog log;
+  cudaError_t e = cudaSuccess;
+  if (d->T) {
+    e = log.before(cs);
+    if (e == cudaSuccess) e = launch_conv_bwd(a, d->dtype == GDN_F32, cs);
+    if (e == cudaSuccess) e = log.after("conv_bwd", cs);
+  }
+  if (a.sums || d_initial_state) {
+    if (e == cudaSuccess) e = log.before(cs);
+    if (e == cudaSuccess) e = launch_conv_bwd_sums(a, d->dtype == GDN_F32, cs);
+    if (e == cudaSuccess) e = log.after("conv_bwd_sums", cs);
+  }
+  return e == cudaSuccess ? GDN_OK : cuda_fail(e);
+}
+
+gdn_status gdn_conv_step(const void* x, const float* weight, const float* bias, void* state, void* q, void* k,
+                         void* v, const gdn_conv_dims* d, void* stream) {
+  ConvArgs a;
+  gdn_status st = conv_args(d, weight, bias, nullptr, &a);
+  if (st != GDN_OK) return st;
+  if (d->T != d->n_seqs || !x || !weight || !state || !q || !k || !v) return GDN_ERR_INVALID_ARG;
+  if (misaligned16({x, state, q, k, v})) return GDN_ERR_MISALIGNED;
+  a.x = x;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.final_state = state;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  LaunchLog log;
+  cudaError_t e = log.before(cs);
+  if (e == cudaSuccess) e = launch_conv_step(a, d->dtype == GDN_F32, cs);
+  if (e == cudaSuccess) e = log.after("conv_step", cs);
   return e == cudaSuccess ? GDN_OK : cuda_fail(e);
 }
 

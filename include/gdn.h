@@ -522,6 +522,217 @@ gdn_status gdn_kv_attn(const void* q, const int32_t* kv_lens_dev, const int32_t*
                        void* stream);
 
 /*
+ * ---- Between the projections and the mixers ----
+ * What the layers do with a projection's output before gdn_chunk_fwd,
+ * gdn_decode_step, gdn_kv_append and gdn_kv_attn take it (no counterpart on
+ * the FlashQLA pages).  Heads have 128 elements.  fp32 arithmetic; results are
+ * rounded once, to dims->dtype, to nearest even.  All asynchronous on `stream`.
+ */
+
+/* Rotary positions: the pairs of a head's first `rot` elements turn by the
+ * angle p f_i at position p, f_i = base^(-2i / rot) radians a token, i < rot/2. */
+enum { GDN_ROPE_HALF = 0,         /* pairs (i, i + rot/2) */
+       GDN_ROPE_INTERLEAVED = 1 }; /* pairs (2i, 2i + 1) */
+/* Frequencies for contexts `factor` times longer than the model was trained on: */
+enum { GDN_ROPE_PLAIN = 0,
+       GDN_ROPE_LINEAR = 1,  /* f / factor */
+       GDN_ROPE_NTK = 2,     /* base factor^(rot / (rot - 2)) instead of base: the slowest pair is slowed by factor, the fastest not */
+       GDN_ROPE_PARTS = 3 }; /* with r = original_len f / 2 pi turns over the trained length and
+                                keep = (r - low) / (high - low) held within [0, 1]: f keep + f / factor (1 - keep) */
+
+typedef struct gdn_rope_opts {
+  int rot;              /* elements of a head that turn: a multiple of 8, 8 to 128 */
+  int scaling;          /* GDN_ROPE_PLAIN, LINEAR, NTK or PARTS */
+  double base;          /* > 1 */
+  double factor;        /* >= 1 (PLAIN: not read) */
+  double original_len;  /* PARTS: > 0 tokens, and low < high turns */
+  double low, high;
+} gdn_rope_opts;
+
+/*
+ * gdn_rope_table -- host only: the frequencies as turns a token times 2^64,
+ * to nearest: uint64 [rot / 2].  Copied to the device once, they give the
+ * angle of any 32-bit position exactly, as the low 64 bits of a product.
+ * Errors: INVALID_ARG, UNSUPPORTED (rot, scaling).
+ */
+gdn_status gdn_rope_table(const gdn_rope_opts* opts, uint64_t* turns_host);
+
+typedef struct gdn_rope {
+  const uint64_t* turns;  /* device, [rot / 2], from gdn_rope_table */
+  int rot;                /* 0: nothing turns, turns is not read */
+  int layout;             /* GDN_ROPE_HALF or GDN_ROPE_INTERLEAVED */
+  float magnitude;        /* turned elements are multiplied by it; 0 selects 1 */
+} gdn_rope;
+
+/* Norms of a head x, with weight w (or 1): x r w, */
+enum { GDN_NORM_NONE = 0,
+       GDN_NORM_RMS = 1,   /* r = 1 / sqrt(sum x^2 / 128 + eps) */
+       GDN_NORM_UNIT = 2 }; /* r = 1 / sqrt(sum x^2 + eps) */
+
+typedef struct gdn_rope_dims {
+  int n_seqs;   /* sequences; without offsets and positions T / n_seqs tokens each */
+  int T;        /* tokens of the call */
+  int h_q, h_k; /* heads of q and of k; one of them may be 0, with its pointers null */
+  int norm;     /* GDN_NORM_* */
+  float eps;    /* 0 selects 1e-6; otherwise at least 1e-20 */
+  int dtype;    /* GDN_BF16 or GDN_F32 */
+  /* Elements from one token to the next, 0: heads * 128 (packed); a multiple of
+   * 16 bytes and at least heads * 128, so the tensors may be parts of one fused
+   * projection. */
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  int64_t dq_stride, dk_stride; /* gdn_qk_rope_bwd; there q_out and k_out are d_q_out and d_k_out */
+} gdn_rope_dims;
+
+/*
+ * gdn_qk_rope -- queries and keys, each head normalised, then rotated by its
+ * token's position: y = m R_p (x r w), m the magnitude.
+ *   q, k              : device, [T, h_q, 128] and [T, h_k, 128], dims->dtype.
+ *   q_weight, k_weight: device fp32 [128], or NULL (1).  Not with GDN_NORM_NONE.
+ *   positions         : device int32 [T], any values; or NULL: token t of the packed
+ *                       batch is at t - cu_seqlens_dev[i] of its sequence i, or
+ *                       with both NULL at t % (T / n_seqs).
+ *   cu_seqlens_dev    : device int32 [n_seqs + 1], not read when positions are given.
+ *                       Offsets that go back give undefined positions, and no access
+ *                       outside the buffers.
+ *   rope              : host, or NULL (nothing turns).
+ *   q_out, k_out      : device, like q and k.  Each may be its input itself (same
+ *                       address and stride); otherwise outputs overlap nothing.
+ * Where a head's sum of squares passes fp32's range it is taken of scaled
+ * elements, so finite heads of any size are normalised.  An infinite or NaN
+ * element makes NaN of itself and of its pair, NaN of the whole head.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, norm, rot, layout), MISALIGNED (16 bytes), CUDA.
+ */
+gdn_status gdn_qk_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                       const int32_t* positions, const int32_t* cu_seqlens_dev, const gdn_rope* rope, void* q_out,
+                       void* k_out, const gdn_rope_dims* dims, void* stream);
+
+/* Device workspace of gdn_qk_rope_bwd, whatever its sizes.  Errors: INVALID_ARG (NULL). */
+gdn_status gdn_qk_rope_bwd_workspace_bytes(size_t* bytes);
+
+/*
+ * gdn_qk_rope_bwd -- gradients of sum(q_out d_q_out) + sum(k_out d_k_out).  With
+ * du = m R_p^T dy and n = x r:
+ *   dw = sum over tokens and heads of du n,   dn = du w,
+ *   dx = r (dn - n sum(dn n) / 128)  (GDN_NORM_UNIT: without the 128).
+ * Inputs as gdn_qk_rope's; q and k are not read with GDN_NORM_NONE (may be NULL).
+ *   d_q_out, d_k_out      : device, [T, h, 128], dims->dtype.
+ *   dq, dk                : device, the same; each may be its d_q_out or d_k_out itself.
+ *   dq_weight, dk_weight  : device fp32 [128], or NULL (not wanted); need the weight.
+ *   workspace             : device, 16-byte aligned, of gdn_qk_rope_bwd_workspace_bytes;
+ *                           NULL without dq_weight and dk_weight.  Its contents on entry do
+ *                           not matter; not to be shared by calls that may run concurrently.
+ * The weights' gradients are summed in a fixed order: results repeat bit for bit.
+ * Errors: as gdn_qk_rope, WORKSPACE.
+ */
+gdn_status gdn_qk_rope_bwd(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                           const int32_t* positions, const int32_t* cu_seqlens_dev, const gdn_rope* rope,
+                           const void* d_q_out, const void* d_k_out, void* dq, void* dk, float* dq_weight,
+                           float* dk_weight, const gdn_rope_dims* dims, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * gdn_kv_append_rope -- gdn_kv_append of keys that are normalised and rotated on
+ * the way, each by its position p in the cache (see there), and the queries
+ * of the same tokens normalised and rotated beside them, in one launch.  The
+ * keys' fp32 results are quantised without a rounding in between: page
+ * scales, codes and what is not finite follow gdn_kv_append with them as x.
+ *   k, v, kv_lens_dev, page_table_dev, cu_seqlens_dev, cache, dims: as gdn_kv_append.
+ *   q      : device, [T, dims->h_q, 128], token stride dims->q_stride; or NULL.
+ *   q_out  : device, like q, token stride dims->out_stride; may be q itself.  A
+ *            token at p < 0 is rotated by that position.
+ *   k_weight, q_weight, rope, norm, eps: as gdn_qk_rope.
+ * Errors: as gdn_kv_append and gdn_qk_rope.
+ */
+gdn_status gdn_kv_append_rope(const void* k, const void* v, const float* k_weight, const void* q,
+                              const float* q_weight, void* q_out, const int32_t* kv_lens_dev,
+                              const int32_t* page_table_dev, const int32_t* cu_seqlens_dev, const gdn_kv_cache* cache,
+                              const gdn_kv_dims* dims, const gdn_rope* rope, int norm, float eps, void* stream);
+
+/*
+ * The short causal convolution before the gated delta rule [GDN, the layer's
+ * block design]: C = (2 h_qk + h_v) 128 channels of a projection, heads of q,
+ * then of k, then of v.  Per channel, with W taps w_0 .. w_{W-1}, a bias b and
+ * the W - 1 inputs kept from before the sequence (or zeros) as x_{-W+1} .. x_{-1}:
+ *   u_t = b + sum_j w_j x_{t - W + 1 + j},   y = u sigmoid(u)  or  y = u,
+ * then q's and k's heads scaled to unit length: y / sqrt(sum y^2 + eps).
+ */
+enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 };
+
+typedef struct gdn_conv_dims {
+  int n_seqs;     /* sequences; without offsets T / n_seqs tokens each */
+  int T;          /* tokens of the call; gdn_conv_step: n_seqs */
+  int h_qk, h_v;
+  int width;      /* taps W: 2, 3 or 4 */
+  int activation; /* GDN_ACT_* */
+  int norm;       /* 1: q's and k's heads to unit length; 0: not */
+  float eps;      /* 0 selects 1e-6; otherwise at least 1e-20 */
+  int dtype;      /* GDN_BF16 or GDN_F32: type of x, q, k, v and the states */
+  int64_t x_stride;  /* elements from one token to the next in x, 0: C.  A multiple of */
+  int64_t dx_stride; /* 16 bytes and at least C.  dx_stride: gdn_conv_bwd's dx. */
+} gdn_conv_dims;
+
+/*
+ * gdn_conv_fwd -- the convolution of packed sequences.
+ *   x              : device, [T, C], row stride dims->x_stride.
+ *   weight         : device fp32 [C, W], w_{W-1} the tap of the token itself.
+ *   bias           : device fp32 [C], or NULL.
+ *   initial_state  : device, [n_seqs, W - 1, C] inputs before each sequence, oldest
+ *                    first, or NULL (zeros).
+ *   cu_seqlens_dev : device int32 [n_seqs + 1], or NULL.  With offsets that leave [0, T]
+ *                    or go back the outputs are undefined; no access leaves the buffers.
+ *   q, k, v        : device, [T, h_qk, 128], [T, h_qk, 128], [T, h_v, 128], packed, as
+ *                    gdn_chunk_fwd takes them.
+ *   final_state    : device, like initial_state: each sequence's last W - 1 inputs, the
+ *                    state's own among them where it is shorter; or NULL.  May not
+ *                    overlap initial_state.
+ * Outputs may not overlap inputs.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, width, activation), MISALIGNED (16 bytes), CUDA.
+ */
+gdn_status gdn_conv_fwd(const void* x, const float* weight, const float* bias, const void* initial_state,
+                        const int32_t* cu_seqlens_dev, void* q, void* k, void* v, void* final_state,
+                        const gdn_conv_dims* dims, void* stream);
+
+/* Device workspace of gdn_conv_bwd for these dims.  Host only.  Errors: INVALID_ARG, UNSUPPORTED. */
+gdn_status gdn_conv_bwd_workspace_bytes(const gdn_conv_dims* dims, size_t* bytes);
+
+/*
+ * gdn_conv_bwd -- gradients of sum(q d_q) + sum(k d_k) + sum(v d_v) +
+ * sum(final_state d_final_state), gdn_conv_fwd's outputs, which are computed
+ * again.  With g the gradient of a head's output, r = 1 / sqrt(sum y^2 + eps) and
+ * n = y r:  dy = r (g - n sum(g n)) for q and k,  du = dy (s + u s (1 - s)), s =
+ * sigmoid(u),  dx_t = sum_j w_j du_{t + W - 1 - j},  dw_j = sum_t du_t x_{t - W + 1 + j},
+ * db = sum_t du_t; the gradient at the kept inputs is the initial state's.
+ *   x, weight, bias, initial_state, cu_seqlens_dev, dims: as gdn_conv_fwd.
+ *   d_q, d_k, d_v   : device, like q, k, v.
+ *   d_final_state   : device, [n_seqs, W - 1, C], or NULL (zero).
+ *   dx              : device, [T, C], row stride dims->dx_stride.
+ *   d_weight, d_bias: device fp32 [C, W] and [C], or NULL (not wanted).
+ *   d_initial_state : device, [n_seqs, W - 1, C], or NULL; written also when
+ *                     initial_state is NULL (the gradient at zero).
+ *   workspace       : device, 16-byte aligned, of gdn_conv_bwd_workspace_bytes; NULL without
+ *                     d_weight and d_bias.  Its contents on entry do not matter; not to be
+ *                     shared by calls that may run concurrently.
+ * Sums over tokens are taken in a fixed order: results repeat bit for bit.
+ * Outputs may not overlap inputs.  Errors: as gdn_conv_fwd, WORKSPACE.
+ */
+gdn_status gdn_conv_bwd(const void* x, const float* weight, const float* bias, const void* initial_state,
+                        const int32_t* cu_seqlens_dev, const void* d_q, const void* d_k, const void* d_v,
+                        const void* d_final_state, void* dx, float* d_weight, float* d_bias, void* d_initial_state,
+                        const gdn_conv_dims* dims, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_conv_step -- one new token for each of n_seqs sequences, the
+ * generation-time form of gdn_conv_fwd beside gdn_decode_step.
+ *   x       : device, [n_seqs, C], row stride dims->x_stride; dims->T = n_seqs.
+ *   state   : device, [n_seqs, W - 1, C], read, then overwritten with the last W - 1
+ *             inputs, x's row among them.
+ *   q, k, v : device, [n_seqs, h, 128], as gdn_decode_step takes them.
+ * Errors: as gdn_conv_fwd.
+ */
+gdn_status gdn_conv_step(const void* x, const float* weight, const float* bias, void* state, void* q, void* k,
+                         void* v, const gdn_conv_dims* dims, void* stream);
+
+/*
  * gdn_debug_stall_ns -- test hook of the failure path (no counterpart on the
  * FlashQLA pages).  While ns > 0, each later gdn_chunk_fwd of this process on
  * the bf16 path makes the blocks of its chunk-local kernel first wait ns

@@ -19,8 +19,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kGroups = kThreads / 16;
 
-// First token and end of the sequence that token t is in; what offsets outside
-// their bounds say is held within [0, T], around t.
+// First token and end of the sequence that token t is in, within [0, T]; seq -1
+// where it is outside every one, then with the end of such tokens.
 struct ConvSeq {
   int seq, begin, end;
 };
@@ -41,8 +41,11 @@ __device__ __forceinline__ ConvSeq conv_seq(const ConvArgs& a, int t) {
   s.seq = lo;
   s.begin = a.cu[lo];
   s.end = a.cu[lo + 1];
-  if (s.begin < 0 || s.begin > t) s.begin = t;
-  if (s.end <= t || s.end > a.T) s.end = t + 1;
+  if (s.begin < 0 || s.begin > t || s.end <= t || s.end > a.T) {
+    s.seq = -1;
+    s.end = s.begin > t ? min(s.begin, a.T) : a.T;
+    s.begin = t;
+  }
   return s;
 }
 
@@ -166,7 +169,7 @@ __device__ __forceinline__ void load_window(const ConvArgs& a, const ConvSeq& s,
     const int at = t - (W - 1) + j;
     if (at >= s.begin) {
       load_f32<T, N>(static_cast<const T*>(a.x) + at * a.x_stride + c, win[j]);
-    } else if (a.state) {
+    } else if (a.state && s.seq >= 0) {
       load_f32<T, N>(static_cast<const T*>(a.state) + ((int64_t)s.seq * (W - 1) + (W - 1) + at - s.begin) * C + c, win[j]);
     } else {
 #pragma unroll
@@ -263,6 +266,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a) {
         s = conv_seq(a, t);
         load_window<T, W, N>(a, s, t, c, C, win);
       }
+      if (s.seq < 0) continue;
       unpack<T, N>(raw[i], win[W - 1]);
       float y[N];
       taps<W, N>(win, w, b, y);
@@ -345,6 +349,7 @@ __device__ __forceinline__ void put_dx(const ConvArgs& a, const ConvSeq& s, int 
 template <typename T, int W, int N>
 __device__ __forceinline__ void end_sequence(const ConvArgs& a, const ConvSeq& s, int t0, int t1, int c, int C,
                                              float (&acc)[W][N]) {
+  if (s.seq < 0) return;
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     if (a.d_final) {
@@ -407,6 +412,7 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs a) {
           s = conv_seq(a, t);
           load_window<T, W, N>(a, s, t, c, C, win);
         }
+        if (s.seq < 0) continue;
         unpack<T, N>(rx[i], win[W - 1]);
         float u[N], sg[N], y[N], g[N];
         taps<W, N>(win, w, b, u);

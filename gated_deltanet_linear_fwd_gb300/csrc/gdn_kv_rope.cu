@@ -117,6 +117,7 @@ __device__ __forceinline__ void turn_queries(const KvRopeArgs& a, int64_t task) 
   if (t >= a.p.c.T) return;
   const int seq = a.p.c.cu ? seq_of(a.p.c.cu, a.p.c.n_seqs, t) : t / a.p.c.n_each;
   const KvSeq s = kv_seq(a.p.c, seq);
+  if (t < s.tok0 || t - s.tok0 >= s.n) return;  // a token outside every sequence
   const RopeLane l = rope_lane(a.r, lane);
   float c[4], sn[4];
   rope_angles(a.r, l, rope_freq(a.r, l, lane), s.len - s.n + t - s.tok0, c, sn);

@@ -29,8 +29,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const QkRopeArgs a) {
   grid_launch_dependents();
   if (t >= a.pos.T) return;
   const RopeLane l = rope_lane(a.r, lane);
+  int pos;
+  if (!token_position(a.pos, t, pos)) return;
   float c[4], s[4];
-  rope_angles(a.r, l, rope_freq(a.r, l, lane), token_position(a.pos, t), c, s);
+  rope_angles(a.r, l, rope_freq(a.r, l, lane), pos, c, s);
   const int heads = a.h_q + a.h_k;
   const int h0 = (int)((int64_t)part * heads / a.splits), h1 = (int)((int64_t)(part + 1) * heads / a.splits);
   const int q0 = min(h0, a.h_q), q1 = min(h1, a.h_q), k0 = max(h0 - a.h_q, 0), k1 = max(h1 - a.h_q, 0);
@@ -102,8 +104,10 @@ __global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const QkRopeArgs a) 
   float dwq[8] = {}, dwk[8] = {};
   for (int64_t task = (int64_t)blockIdx.x * kTasks + hw; task < tasks; task += (int64_t)gridDim.x * kTasks) {
     const int t = (int)(task / a.splits), part = (int)(task % a.splits);
+    int pos;
+    if (!token_position(a.pos, t, pos)) continue;
     float c[4], s[4];
-    rope_angles(a.r, l, f, token_position(a.pos, t), c, s);
+    rope_angles(a.r, l, f, pos, c, s);
     const int h0 = (int)((int64_t)part * heads / a.splits), h1 = (int)((int64_t)(part + 1) * heads / a.splits);
     const int q0 = min(h0, a.h_q), q1 = min(h1, a.h_q), k0 = max(h0 - a.h_q, 0), k1 = max(h1 - a.h_q, 0);
     turn_heads_bwd<T, kInterleaved>(a.r, l, c, s, static_cast<const T*>(a.q) + t * a.q_stride + q0 * kRopeD,

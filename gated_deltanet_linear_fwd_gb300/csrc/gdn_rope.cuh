@@ -49,10 +49,18 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int n, int t) {
   }
   return lo;
 }
-__device__ __forceinline__ int token_position(const PosArgs& a, int t) {
-  if (a.positions) return a.positions[t];
-  if (a.cu) return (int)((unsigned)t - (unsigned)a.cu[seq_of(a.cu, a.n_seqs, t)]);
-  return t % a.n_each;
+// False for a token outside every sequence.
+__device__ __forceinline__ bool token_position(const PosArgs& a, int t, int& pos) {
+  if (a.positions) {
+    pos = a.positions[t];
+  } else if (a.cu) {
+    const int seq = seq_of(a.cu, a.n_seqs, t), begin = a.cu[seq];
+    pos = (int)((unsigned)t - (unsigned)begin);
+    return t >= begin && t < a.cu[seq + 1];
+  } else {
+    pos = t % a.n_each;
+  }
+  return true;
 }
 
 struct RopeLane {

@@ -592,8 +592,10 @@ typedef struct gdn_rope_dims {
  *                       batch is at t - cu_seqlens_dev[i] of its sequence i, or
  *                       with both NULL at t % (T / n_seqs).
  *   cu_seqlens_dev    : device int32 [n_seqs + 1], not read when positions are given.
- *                       Offsets that go back give undefined positions, and no access
- *                       outside the buffers.
+ *                       Tokens outside every sequence (behind the last offset, say)
+ *                       are left as they were.  Offsets that go back leave undefined
+ *                       which tokens are done, with which positions; no access
+ *                       leaves the buffers.
  *   rope              : host, or NULL (nothing turns).
  *   q_out, k_out      : device, like q and k.  Each may be its input itself (same
  *                       address and stride); otherwise outputs overlap nothing.
@@ -617,6 +619,8 @@ gdn_status gdn_qk_rope_bwd_workspace_bytes(size_t* bytes);
  * Inputs as gdn_qk_rope's; q and k are not read with GDN_NORM_NONE (may be NULL).
  *   d_q_out, d_k_out      : device, [T, h, 128], dims->dtype.
  *   dq, dk                : device, the same; each may be its d_q_out or d_k_out itself.
+ *                           Tokens outside every sequence are left as they were, and
+ *                           do not count in the weights' gradients.
  *   dq_weight, dk_weight  : device fp32 [128], or NULL (not wanted); need the weight.
  *   workspace             : device, 16-byte aligned, of gdn_qk_rope_bwd_workspace_bytes;
  *                           NULL without dq_weight and dk_weight.  Its contents on entry do
@@ -639,7 +643,8 @@ gdn_status gdn_qk_rope_bwd(const void* q, const void* k, const float* q_weight, 
  *   k, v, kv_lens_dev, page_table_dev, cu_seqlens_dev, cache, dims: as gdn_kv_append.
  *   q      : device, [T, dims->h_q, 128], token stride dims->q_stride; or NULL.
  *   q_out  : device, like q, token stride dims->out_stride; may be q itself.  A
- *            token at p < 0 is rotated by that position.
+ *            token at p < 0 is rotated by that position; one outside every
+ *            sequence is left as it was.
  *   k_weight, q_weight, rope, norm, eps: as gdn_qk_rope.
  * Errors: as gdn_kv_append and gdn_qk_rope.
  */
@@ -678,8 +683,10 @@ typedef struct gdn_conv_dims {
  *   bias           : device fp32 [C], or NULL.
  *   initial_state  : device, [n_seqs, W - 1, C] inputs before each sequence, oldest
  *                    first, or NULL (zeros).
- *   cu_seqlens_dev : device int32 [n_seqs + 1], or NULL.  With offsets that leave [0, T]
- *                    or go back the outputs are undefined; no access leaves the buffers.
+ *   cu_seqlens_dev : device int32 [n_seqs + 1], or NULL.  Tokens outside every sequence
+ *                    (behind the last offset, say) are left as they were.  With
+ *                    offsets that leave [0, T] or go back the outputs are
+ *                    undefined; no access leaves the buffers.
  *   q, k, v        : device, [T, h_qk, 128], [T, h_qk, 128], [T, h_v, 128], packed, as
  *                    gdn_chunk_fwd takes them.
  *   final_state    : device, like initial_state: each sequence's last W - 1 inputs, the
@@ -705,7 +712,8 @@ gdn_status gdn_conv_bwd_workspace_bytes(const gdn_conv_dims* dims, size_t* bytes
  *   x, weight, bias, initial_state, cu_seqlens_dev, dims: as gdn_conv_fwd.
  *   d_q, d_k, d_v   : device, like q, k, v.
  *   d_final_state   : device, [n_seqs, W - 1, C], or NULL (zero).
- *   dx              : device, [T, C], row stride dims->dx_stride.
+ *   dx              : device, [T, C], row stride dims->dx_stride; tokens outside every
+ *                     sequence are left as they were.
  *   d_weight, d_bias: device fp32 [C, W] and [C], or NULL (not wanted).
  *   d_initial_state : device, [n_seqs, W - 1, C], or NULL; written also when
  *                     initial_state is NULL (the gradient at zero).

@@ -412,11 +412,24 @@ gdn_status rope_args(const gdn_rope* rope, int norm, float eps, RopeArgs* r) {
   return norm_eps(eps, &r->eps);
 }
 
-// Half-warps that share a token's heads: one, whose cosines then serve all
-// of them, unless the tokens are too few to fill the GPU.
-int rope_splits(int64_t T, int heads) {
-  constexpr int64_t kFill = 152 * 64;  // half-warps that are resident
-  return (int)std::min<int64_t>(heads, std::max<int64_t>(1, kFill / std::max<int64_t>(T, 1)));
+// Warps that have two tokens' heads, 2^log2 with `share` heads each: one, whose
+// cosines then serve all of them, unless the tokens are too few to fill the GPU.
+void rope_shares(int64_t T, int heads, int* log2, int* share) {
+  constexpr int64_t kFill = 152 * 24;  // warps that are resident
+  *log2 = 0;
+  while ((1 << *log2) < heads && ((T + 1) / 2 << *log2) < kFill) ++*log2;
+  *share = (heads + (1 << *log2) - 1) >> *log2;
+}
+constexpr int kRopeBwdCtas = 3 * 152;  // of a gradient: what is resident
+// Shares and CTAs of a gradient: the latter by the sides' heads, and no more than there is to do.
+void rope_bwd_plan(int64_t T, RopeSide (&side)[2]) {
+  const int heads = side[0].heads + side[1].heads;
+  for (RopeSide& s : side) {
+    if (!s.heads) continue;
+    rope_shares(T, s.heads, &s.shares_log2, &s.share);
+    const int64_t blocks = ((((T + 1) / 2) << s.shares_log2) + kRopeWarps - 1) / kRopeWarps;
+    s.ctas = (int)std::min<int64_t>(blocks, std::max<int64_t>(1, ((int64_t)kRopeBwdCtas * s.heads + heads / 2) / heads));
+  }
 }
 
 // Checks of gdn_qk_rope and its gradient that do not need the tensors.
@@ -433,22 +446,21 @@ gdn_status qk_rope_args(const gdn_rope_dims* d, const gdn_rope* rope, const floa
   if (d->norm == GDN_NORM_NONE && (q_weight || k_weight)) return GDN_ERR_INVALID_ARG;
   if (misaligned16({q_weight, k_weight}) || (reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(cu)) & 3u)
     return GDN_ERR_MISALIGNED;
-  if ((st = kv_stride(d->q_stride, d->h_q, d->dtype, &a->q_stride)) != GDN_OK) return st;
-  if ((st = kv_stride(d->k_stride, d->h_k, d->dtype, &a->k_stride)) != GDN_OK) return st;
-  if ((st = kv_stride(d->q_out_stride, d->h_q, d->dtype, &a->q_out_stride)) != GDN_OK) return st;
-  if ((st = kv_stride(d->k_out_stride, d->h_k, d->dtype, &a->k_out_stride)) != GDN_OK) return st;
-  if ((st = kv_stride(d->dq_stride, d->h_q, d->dtype, &a->dq_stride)) != GDN_OK) return st;
-  if ((st = kv_stride(d->dk_stride, d->h_k, d->dtype, &a->dk_stride)) != GDN_OK) return st;
-  a->pos = {positions, cu, d->n_seqs, d->T, positions || cu ? 0 : d->T / d->n_seqs};
-  a->q_weight = q_weight;
-  a->k_weight = k_weight;
-  a->h_q = d->h_q;
-  a->h_k = d->h_k;
-  a->splits = rope_splits(d->T, d->h_q + d->h_k);
+  RopeSide &q = a->side[0], &k = a->side[1];
+  if ((st = kv_stride(d->q_stride, d->h_q, d->dtype, &q.in_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->k_stride, d->h_k, d->dtype, &k.in_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->q_out_stride, d->h_q, d->dtype, &q.out_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->k_out_stride, d->h_k, d->dtype, &k.out_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->dq_stride, d->h_q, d->dtype, &q.dx_stride)) != GDN_OK) return st;
+  if ((st = kv_stride(d->dk_stride, d->h_k, d->dtype, &k.dx_stride)) != GDN_OK) return st;
+  a->pos = {positions, cu, nullptr, d->n_seqs, d->T, positions || cu ? 0 : d->T / d->n_seqs};
+  q.weight = q_weight;
+  k.weight = k_weight;
+  q.heads = d->h_q;
+  k.heads = d->h_k;
+  rope_shares(d->T, d->h_q + d->h_k, &a->shares_log2, &a->share);
   return GDN_OK;
 }
-
-constexpr int kRopeBwdCtas = 1024;  // rows of the workspace: CTAs of the gradient, at most
 
 // Tokens a group of lanes takes in a row: more of them read less twice (the W - 1
 // before each run), fewer fill the GPU.  `fill`: groups that are resident.
@@ -1232,10 +1244,10 @@ gdn_status gdn_qk_rope(const void* q, const void* k, const float* q_weight, cons
   if (d->T == 0) return GDN_OK;
   if ((d->h_q && (!q || !q_out)) || (d->h_k && (!k || !k_out))) return GDN_ERR_INVALID_ARG;
   if (misaligned16({q, k, q_out, k_out})) return GDN_ERR_MISALIGNED;
-  a.q = q;
-  a.k = k;
-  a.q_out = q_out;
-  a.k_out = k_out;
+  a.side[0].in = q;
+  a.side[1].in = k;
+  a.side[0].out = q_out;
+  a.side[1].out = k_out;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   LaunchLog log;
   cudaError_t e = log.before(cs);
@@ -1246,7 +1258,7 @@ gdn_status gdn_qk_rope(const void* q, const void* k, const float* q_weight, cons
 
 gdn_status gdn_qk_rope_bwd_workspace_bytes(size_t* bytes) {
   if (!bytes) return GDN_ERR_INVALID_ARG;
-  *bytes = (size_t)kRopeBwdCtas * 2 * kRopeD * sizeof(float);
+  *bytes = (size_t)(kRopeBwdCtas + 1) * kRopeD * sizeof(float);  // the sides' shares are rounded
   return GDN_OK;
 }
 
@@ -1273,26 +1285,23 @@ gdn_status gdn_qk_rope_bwd(const void* q, const void* k, const float* q_weight, 
   size_t need = 0;
   gdn_qk_rope_bwd_workspace_bytes(&need);
   if (sums && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
-  int dev = 0;
-  if ((st = device_setup(&dev)) != GDN_OK) return st;
-  a.q = q;
-  a.k = k;
-  a.q_out = const_cast<void*>(d_q_out);
-  a.k_out = const_cast<void*>(d_k_out);
-  a.dq = dq;
-  a.dk = dk;
+  a.side[0].in = q;
+  a.side[1].in = k;
+  a.side[0].out = const_cast<void*>(d_q_out);
+  a.side[1].out = const_cast<void*>(d_k_out);
+  a.side[0].dx = dq;
+  a.side[1].dx = dk;
+  a.side[0].d_weight = dq_weight;
+  a.side[1].d_weight = dk_weight;
   a.part = sums ? static_cast<float*>(workspace) : nullptr;
-  a.dq_weight = dq_weight;
-  a.dk_weight = dk_weight;
-  const int64_t blocks = ((int64_t)d->T * a.splits + 15) / 16;
-  const int ctas = (int)std::min<int64_t>(blocks, std::min(kRopeBwdCtas, 4 * g_sm_count[dev]));
+  rope_bwd_plan(d->T, a.side);
   LaunchLog log;
   e = log.before(cs);
-  if (e == cudaSuccess) e = launch_qk_rope_bwd(a, d->dtype == GDN_F32, ctas, cs);
+  if (e == cudaSuccess) e = launch_qk_rope_bwd(a, d->dtype == GDN_F32, cs);
   if (e == cudaSuccess) e = log.after("qk_rope_bwd", cs);
   if (sums) {
     if (e == cudaSuccess) e = log.before(cs);
-    if (e == cudaSuccess) e = launch_qk_rope_weights(a, ctas, cs);
+    if (e == cudaSuccess) e = launch_qk_rope_weights(a, cs);
     if (e == cudaSuccess) e = log.after("qk_rope_weights", cs);
   }
   return e == cudaSuccess ? GDN_OK : cuda_fail(e);
@@ -1306,16 +1315,22 @@ gdn_status gdn_kv_append_rope(const void* k, const void* v, const float* k_weigh
   if (st != GDN_OK) return st;
   KvRopeArgs a;
   std::memset(&a, 0, sizeof(a));
-  if ((st = rope_args(rope, norm, eps, &a.r)) != GDN_OK) return st;
+  if ((st = rope_args(rope, norm, eps, &a.q.r)) != GDN_OK) return st;
   if (norm == GDN_NORM_NONE && (q_weight || k_weight)) return GDN_ERR_INVALID_ARG;
   if ((q == nullptr) != (q_out == nullptr) || (!q && q_weight)) return GDN_ERR_INVALID_ARG;
   if (q && (d->h_q < 1 || d->h_q > 65535)) return GDN_ERR_INVALID_ARG;
   if (misaligned16({q_weight, k_weight, q, q_out})) return GDN_ERR_MISALIGNED;
   if ((st = kv_moves(d, cache, lens, table, cu, &a.p, &a.entries)) != GDN_OK) return st;
   if (q) {
-    if ((st = kv_stride(d->q_stride, d->h_q, d->dtype, &a.q_stride)) != GDN_OK) return st;
-    if ((st = kv_stride(d->out_stride, d->h_q, d->dtype, &a.q_out_stride)) != GDN_OK) return st;
-    a.splits = rope_splits(d->T, d->h_q);
+    RopeSide& s = a.q.side[0];
+    if ((st = kv_stride(d->q_stride, d->h_q, d->dtype, &s.in_stride)) != GDN_OK) return st;
+    if ((st = kv_stride(d->out_stride, d->h_q, d->dtype, &s.out_stride)) != GDN_OK) return st;
+    a.q.pos = {nullptr, cu, lens, d->n_seqs, d->T, a.p.c.n_each};
+    s.in = q;
+    s.out = q_out;
+    s.weight = q_weight;
+    s.heads = d->h_q;
+    rope_shares(d->T, d->h_q, &a.q.shares_log2, &a.q.share);
   }
   if (d->T == 0) return GDN_OK;
   if (!k || !v) return GDN_ERR_INVALID_ARG;
@@ -1323,12 +1338,8 @@ gdn_status gdn_kv_append_rope(const void* k, const void* v, const float* k_weigh
   a.p.k = const_cast<void*>(k);
   a.p.v = const_cast<void*>(v);
   a.k_weight = k_weight;
-  a.q_weight = q_weight;
-  a.q = q;
-  a.q_out = q_out;
-  // keys and values a block each, and at most as many again of queries as T tokens make
-  if (2 * (int64_t)a.entries * cache->h_kv + ((int64_t)d->T * std::max(1, a.splits) + 15) / 16 > 0x7fffffff)
-    return GDN_ERR_INVALID_ARG;
+  if (2 * (int64_t)a.entries * cache->h_kv + (rope_tasks(a.q) + kRopeWarps) / kRopeWarps > 0x7fffffff)
+    return GDN_ERR_INVALID_ARG;  // blocks
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   LaunchLog log;
   cudaError_t e = log.before(cs);

@@ -215,13 +215,8 @@ __device__ __forceinline__ void append_page(const KvAppendArgs& a, const Entry& 
 // Arguments of gdn_kv_append_rope.
 struct KvRopeArgs {
   KvAppendArgs p;
-  RopeArgs r;
   const float* k_weight;   // [128] or null
-  const float* q_weight;
-  const void* q;           // null: keys and values only
-  void* q_out;
-  int64_t q_stride, q_out_stride;
-  int splits;              // half-warps that share a token's query heads
+  QkRopeArgs q;            // the queries, without keys; no heads: none
   unsigned entries;        // page slots of the call
 };
 

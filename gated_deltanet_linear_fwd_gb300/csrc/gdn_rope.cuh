@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 
 #include "gdn_internal.cuh"
+#include "gdn_pair.cuh"
 #include "sm103_ptx.cuh"
 
 namespace gdn {
@@ -31,11 +32,12 @@ struct RopeArgs {
   float eps, inv_n;       // 1 / sqrt(inv_n sum x^2 + eps)
 };
 
-// Where a packed token stands: given, counted from its sequence's start, or
-// from its row's.
+// Where a packed token stands: given, counted from its sequence's start or its
+// row's, or, the tokens being the last of lens[i], in the cache.
 struct PosArgs {
   const int32_t* positions;  // [T] or null
   const int32_t* cu;         // [n_seqs + 1] or null
+  const int32_t* lens;       // [n_seqs] or null
   int n_seqs, T, n_each;
 };
 
@@ -53,14 +55,24 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int n, int t) {
 __device__ __forceinline__ bool token_position(const PosArgs& a, int t, int& pos) {
   if (a.positions) {
     pos = a.positions[t];
-  } else if (a.cu) {
-    const int seq = seq_of(a.cu, a.n_seqs, t), begin = a.cu[seq];
-    pos = (int)((unsigned)t - (unsigned)begin);
-    return t >= begin && t < a.cu[seq + 1];
-  } else {
-    pos = t % a.n_each;
+    return true;
   }
-  return true;
+  if (!a.cu && !a.lens && t < a.n_each) {  // a single row of tokens, for one: no division
+    pos = t;
+    return true;
+  }
+  int seq, begin, end;
+  if (a.cu) {
+    seq = seq_of(a.cu, a.n_seqs, t);
+    begin = a.cu[seq];
+    end = a.cu[seq + 1];
+  } else {
+    seq = t / a.n_each;
+    begin = seq * a.n_each;
+    end = begin + a.n_each;
+  }
+  pos = (int)((unsigned)t - (unsigned)(a.lens ? end : begin) + (a.lens ? (unsigned)a.lens[seq] : 0u));
+  return t >= begin && t < end;
 }
 
 struct RopeLane {
@@ -76,50 +88,74 @@ __device__ __forceinline__ RopeLane rope_lane(const RopeArgs& r, int l) {
   return p;
 }
 
+// Cos and sin of two angles of phase / 2^32 turns.  The nearest quarter turn
+// comes off in integers; what remains, u halves of a quarter turn, |u| <= 1,
+// goes into polynomials of u^2 whose coefficients are the minimax ones on [0, 1]
+// (Remez's exchange): u A(u^2) for sin(pi u / 4), relative error 2^-28, and B(u^2)
+// for cos, 2^-34.  Some 25 instructions an angle; with sincospif an angle took
+// 94, a fifth of the forward's.
+__device__ __forceinline__ void sincos_turns(uint32_t p0, uint32_t p1, F2& c, F2& s) {
+  const uint32_t q0 = (p0 + 0x20000000u) >> 30, q1 = (p1 + 0x20000000u) >> 30;
+  const F2 u = mul2(f2((float)(int32_t)(p0 - (q0 << 30)), (float)(int32_t)(p1 - (q1 << 30))), f2(0x1p-29f)), v = mul2(u, u);
+  const F2 sn = mul2(u, fma2(v, fma2(v, fma2(v, f2(-3.5950452e-5f), f2(2.4900010e-3f)), f2(-8.0745433e-2f)), f2(7.8539816e-1f)));
+  const F2 cs = fma2(
+      v, fma2(v, fma2(v, fma2(v, f2(3.5298113e-6f), f2(-3.2593861e-4f)), f2(1.5854325e-2f)), f2(-3.0842514e-1f)), f2(1.0f));
+  const float2 a = parts(sn), b = parts(cs);
+  auto sign = [](float x, uint32_t q) { return __uint_as_float(__float_as_uint(x) ^ (q << 30 & 0x80000000u)); };
+  s = f2(sign(q0 & 1 ? b.x : a.x, q0), sign(q1 & 1 ? b.y : a.y, q1));
+  c = f2(sign(q0 & 1 ? a.x : b.x, q0 + 1), sign(q1 & 1 ? a.y : b.y, q1 + 1));
+}
+
+// The frequencies of a lane's four pairs, and magnitude times their cosines and
+// sines at position p; of lanes that do not turn, ones and zeros.
 struct RopeFreq {
   uint64_t f[4];
 };
-__device__ __forceinline__ RopeFreq rope_freq(const RopeArgs& r, const RopeLane& p, int l) {
+__device__ __forceinline__ RopeFreq rope_freq(const RopeArgs& r, const RopeLane& p, int lane) {
   RopeFreq q = {{0, 0, 0, 0}};
   if (p.turned) {
-    const ulonglong2* t = reinterpret_cast<const ulonglong2*>(r.turns + 4 * l);
+    const ulonglong2* t = reinterpret_cast<const ulonglong2*>(r.turns + 4 * lane);
     const ulonglong2 a = __ldg(t), b = __ldg(t + 1);
     q.f[0] = a.x; q.f[1] = a.y; q.f[2] = b.x; q.f[3] = b.y;
   }
   return q;
 }
-
-// magnitude times cos and sin of the lane's pairs at position p.  The phase
-// enters as its upper 32 bits, a signed fraction of half a turn, whose
-// conversion to fp32 is off by 2^-25 of a half turn at most.
-__device__ __forceinline__ void rope_angles(const RopeArgs& r, const RopeLane& p, const RopeFreq& q, int pos, float (&c)[4],
-                                            float (&s)[4]) {
+struct Angles {
+  F2 c[2], s[2];
+};
+__device__ __forceinline__ Angles rope_angles(const RopeArgs& r, const RopeLane& l, const RopeFreq& q, int pos) {
+  Angles a;
+  const F2 m = f2(l.turned ? r.magnitude : 1.f);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    c[e] = 1.f;
-    s[e] = 0.f;
+  for (int i = 0; i < 2; ++i) {
+    sincos_turns((uint32_t)(((uint64_t)(int64_t)pos * q.f[2 * i]) >> 32),
+                 (uint32_t)(((uint64_t)(int64_t)pos * q.f[2 * i + 1]) >> 32), a.c[i], a.s[i]);
+    a.c[i] = mul2(a.c[i], m);
+    a.s[i] = mul2(a.s[i], m);
   }
-  if (!p.turned) return;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint64_t phase = (uint64_t)(int64_t)pos * q.f[e];
-    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s[e], &c[e]);
-    c[e] *= r.magnitude;
-    s[e] *= r.magnitude;
-  }
+  return a;
 }
 
-// Rotates the lane's pairs; sign -1: by the transposed rotation.
-template <bool kInterleaved>
-__device__ __forceinline__ void rope_turn(float (&x)[8], const float (&c)[4], const float (&s)[4], float sign = 1.f) {
+// A lane's 8 elements are four pairs of fp32: x[0], x[1] the first chunk, x[2],
+// x[3] the second.  Rotates them, kBack by the transposed rotation.  (A lane
+// that does not turn leaves what it has, infinities too.)
+template <bool kInterleaved, bool kBack = false>
+__device__ __forceinline__ void turn_row(const RopeLane& l, const Angles& a, F2 (&x)[4]) {
+  if (!l.turned) return;
+  if (kInterleaved) {  // the partners are the neighbours
+    const float2 c0 = parts(a.c[0]), c1 = parts(a.c[1]), s0 = parts(a.s[0]), s1 = parts(a.s[1]);
+    const float c[4] = {c0.x, c0.y, c1.x, c1.y}, s[4] = {s0.x, s0.y, s1.x, s1.y};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float& a = x[kInterleaved ? 2 * e : e];
-    float& b = x[kInterleaved ? 2 * e + 1 : e + 4];
-    const float se = sign * s[e];
-    const float ya = a * c[e] - b * se, yb = b * c[e] + a * se;
-    a = ya;
-    b = yb;
+    for (int i = 0; i < 4; ++i)
+      x[i] = fma2(swapped(x[i]), kBack ? f2(s[i], -s[i]) : f2(-s[i], s[i]), mul2(x[i], f2(c[i])));
+  } else {  // the other chunk
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const F2 down = mul2(a.s[i], f2(-1.f)), up = a.s[i];
+      const F2 y = fma2(x[i + 2], kBack ? up : down, mul2(x[i], a.c[i]));
+      x[i + 2] = fma2(x[i], kBack ? down : up, mul2(x[i + 2], a.c[i]));
+      x[i] = y;
+    }
   }
 }
 
@@ -140,127 +176,210 @@ template <>
 struct RowOf<__nv_bfloat16> {
   using type = Row8h;
 };
-__device__ __forceinline__ Row8f load_row(const float* p, const RopeLane& l) {
-  return {*reinterpret_cast<const float4*>(p + l.o0), *reinterpret_cast<const float4*>(p + l.o1)};
+// From the addresses of its chunks.
+template <typename T>
+__device__ __forceinline__ typename RowOf<T>::type load_row(const char* a, const char* b) {
+  using V = decltype(RowOf<T>::type::a);
+  return {*reinterpret_cast<const V*>(a), *reinterpret_cast<const V*>(b)};
 }
-__device__ __forceinline__ Row8h load_row(const __nv_bfloat16* p, const RopeLane& l) {
-  return {*reinterpret_cast<const uint2*>(p + l.o0), *reinterpret_cast<const uint2*>(p + l.o1)};
+__device__ __forceinline__ void unpack_row(const Row8f& r, F2 (&x)[4]) {
+  x[0] = f2(r.a.x, r.a.y);
+  x[1] = f2(r.a.z, r.a.w);
+  x[2] = f2(r.b.x, r.b.y);
+  x[3] = f2(r.b.z, r.b.w);
 }
-__device__ __forceinline__ void unpack_row(const Row8f& r, float (&x)[8]) {
-  x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
-  x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+__device__ __forceinline__ void unpack_row(const Row8h& r, F2 (&x)[4]) {
+  x[0] = bf16_pair(r.a.x);
+  x[1] = bf16_pair(r.a.y);
+  x[2] = bf16_pair(r.b.x);
+  x[3] = bf16_pair(r.b.y);
 }
-__device__ __forceinline__ void unpack_row(const Row8h& r, float (&x)[8]) {
-  const uint32_t w[4] = {r.a.x, r.a.y, r.b.x, r.b.y};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+template <typename T>
+__device__ __forceinline__ void store_row(char* a, char* b, const F2 (&x)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    const float2 p = parts(x[0]), q = parts(x[1]), r = parts(x[2]), s = parts(x[3]);
+    *reinterpret_cast<float4*>(a) = make_float4(p.x, p.y, q.x, q.y);
+    *reinterpret_cast<float4*>(b) = make_float4(r.x, r.y, s.x, s.y);
+  } else {
+    *reinterpret_cast<uint2*>(a) = make_uint2(pair_bf16(x[0]), pair_bf16(x[1]));
+    *reinterpret_cast<uint2*>(b) = make_uint2(pair_bf16(x[2]), pair_bf16(x[3]));
   }
-}
-__device__ __forceinline__ void store_row(float* p, const RopeLane& l, const float (&x)[8]) {
-  *reinterpret_cast<float4*>(p + l.o0) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(p + l.o1) = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ void store_row(__nv_bfloat16* p, const RopeLane& l, const float (&x)[8]) {
-  *reinterpret_cast<uint2*>(p + l.o0) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
-  *reinterpret_cast<uint2*>(p + l.o1) = make_uint2(pack2(x[4], x[5]), pack2(x[6], x[7]));
 }
 
 // ---- the norm ----
-// Sum over the calling half-warp; `mask` is its lanes.
-__device__ __forceinline__ unsigned half_mask() { return 0xffffu << (threadIdx.x & 16); }
-__device__ __forceinline__ float half_sum(float v, unsigned mask) {
+// Whole warps run all of this, two heads at a time: shuffles by less than 16
+// stay within a half, and with all lanes named they cost one instruction.
+__device__ __forceinline__ float half_sum(float v) {
 #pragma unroll
-  for (int d = 8; d; d >>= 1) v += __shfl_xor_sync(mask, v, d);
+  for (int d = 8; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
 }
-__device__ __forceinline__ float sum_squares(const float (&x)[8]) {
-  return ((x[0] * x[0] + x[1] * x[1]) + (x[2] * x[2] + x[3] * x[3])) +
-         ((x[4] * x[4] + x[5] * x[5]) + (x[6] * x[6] + x[7] * x[7]));
+__device__ __forceinline__ float dot_row(const F2 (&x)[4], const F2 (&y)[4]) {
+  return both(add2(fma2(x[1], y[1], mul2(x[0], y[0])), fma2(x[3], y[3], mul2(x[2], y[2]))));
+}
+__device__ __forceinline__ void scale_row(F2 (&x)[4], float f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], f2(f));
 }
 // 1 / sqrt(inv_n ss + eps), ss the head's sum of squares.  Past fp32's range
 // (elements of 2^60 and more) x is scaled by `unit` = 2^-68, beside which eps
 // is nothing, and the result belongs to the scaled x.
-__device__ __forceinline__ float head_scale(float ss, float (&x)[8], float inv_n, float eps, unsigned mask, float& unit) {
+__device__ __forceinline__ float head_scale(F2 (&x)[4], float inv_n, float eps, float& unit) {
+  float ss = half_sum(dot_row(x, x));
   unit = 1.f;
-  if (ss <= 3e38f) return rsqrtf(fmaf(ss, inv_n, eps));
-  unit = 0x1p-68f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] *= unit;
-  return rsqrtf(half_sum(sum_squares(x), mask) * inv_n);
+  if (__any_sync(0xffffffffu, !(ss <= 3e38f))) {
+    const bool large = !(ss <= 3e38f);
+    unit = large ? 0x1p-68f : 1.f;
+    scale_row(x, unit);
+    ss = half_sum(dot_row(x, x));
+    if (large) eps = 0.f;
+  }
+  return rsqrt_approx(fmaf(ss, inv_n, eps));
 }
 
-__device__ __forceinline__ void load_weight(const float* w, const RopeLane& l, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(w + l.o0)), b = __ldg(reinterpret_cast<const float4*>(w + l.o1));
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
-constexpr int kRopeBatch = 4;  // heads whose loads are in flight together
-
-// n heads of a token: in -> out.
-template <typename T, bool kInterleaved>
-__device__ __forceinline__ void turn_heads(const RopeArgs& r, const RopeLane& l, const float (&c)[4], const float (&s)[4],
-                                           const T* in, T* out, int n, const float* weight, unsigned mask) {
-  if (n <= 0) return;
-  float w[8];
-  if (weight) load_weight(weight, l, w);
-  for (int h0 = 0; h0 < n; h0 += kRopeBatch) {
-    typename RowOf<T>::type raw[kRopeBatch];
+// The lane's part of a weight, or ones.
+__device__ __forceinline__ void load_weight(const float* w, const RopeLane& l, F2 (&x)[4]) {
+  if (w) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(w + l.o0)), b = __ldg(reinterpret_cast<const float4*>(w + l.o1));
+    x[0] = f2(a.x, a.y);
+    x[1] = f2(a.z, a.w);
+    x[2] = f2(b.x, b.y);
+    x[3] = f2(b.z, b.w);
+  } else {
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i)
-      if (h0 + i < n) raw[i] = load_row(in + (h0 + i) * kRopeD, l);
-#pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
-      if (h0 + i >= n) break;
-      float x[8];
-      unpack_row(raw[i], x);
-      if (r.norm != kNormNone) {
-        float unit;
-        const float f = head_scale(half_sum(sum_squares(x), mask), x, r.inv_n, r.eps, mask, unit);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= f;
-        if (weight) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= w[e];
-        }
-      }
-      rope_turn<kInterleaved>(x, c, s);
-      store_row(out + (h0 + i) * kRopeD, l, x);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = f2(1.f);
   }
 }
 
-// Arguments of gdn_qk_rope and its gradient.
+// ---- the heads of a token ----
+// A warp takes two tokens, one a half, and their heads, or a share of them, one
+// after another, with the cosines and sines in registers.  Heads are at constant
+// distances from the first: with an address each, a table of cosines in shared
+// memory, and a token's heads cut differently in the halves, 220 instructions
+// went into a row of two heads and 34 to 70 us into 32768 tokens of 8 + 2 heads.
+constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = kRopeThreads / 32;
+template <typename T>
+constexpr int kRopeBatch = sizeof(T) == 2 ? 4 : 2;  // heads whose loads are in flight together
+
+// Queries or keys.
+struct RopeSide {
+  const void* in;
+  void* out;               // backward: the gradient of the output, read
+  void* dx;                // backward
+  const float* weight;     // [128] or null
+  float* d_weight;         // backward
+  int64_t in_stride, out_stride, dx_stride;
+  int heads;
+  int shares_log2, share;  // backward: 2^shares_log2 warps have two tokens' heads, `share` each
+  int ctas;                // backward
+};
+
+// Arguments of gdn_qk_rope and its gradient, and the queries' of gdn_kv_append_rope.
 struct QkRopeArgs {
   RopeArgs r;
   PosArgs pos;
-  const void* q;
-  const void* k;
-  const float* q_weight;   // [128] or null
-  const float* k_weight;
-  void* q_out;             // backward: the gradient of q_out, read
-  void* k_out;
-  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
-  int h_q, h_k;
-  int splits;              // half-warps that share a token's heads
-  // backward
-  void* dq;
-  void* dk;
-  int64_t dq_stride, dk_stride;
-  float* part;             // [CTAs, 2, 128] sums of the weights' gradients, or null
-  float* dq_weight;
-  float* dk_weight;
+  RopeSide side[2];        // q, then k
+  int shares_log2, share;  // forward: 2^shares_log2 warps have two tokens' heads of both, `share` each
+  float* part;             // backward: [CTAs, 128] sums of the weights' gradients, or null
 };
 
+// A warp's task: heads [h0, h1) of q and [k0, k1) of k of its half's token.
+struct RopeTask {
+  int t;                   // held within the call; in: it is in the call and in a sequence
+  bool in;
+  int h0, h1, k0, k1;
+};
+__device__ __forceinline__ RopeTask rope_task(const QkRopeArgs& a, unsigned task) {
+  RopeTask k;
+  const int t = (int)(task >> a.shares_log2) * 2 + (int)(threadIdx.x >> 4 & 1);
+  k.in = t < a.pos.T;
+  k.t = min(t, a.pos.T - 1);
+  const int h_q = a.side[0].heads, h = (int)(task & ((1u << a.shares_log2) - 1)) * a.share;
+  const int end = min(h + a.share, h_q + a.side[1].heads);
+  k.h0 = min(h, h_q);
+  k.h1 = min(end, h_q);
+  k.k0 = max(h - h_q, 0);
+  k.k1 = max(end - h_q, 0);
+  return k;
+}
+
+// A batch of heads, n of them at most, from the addresses of the first's chunks.
+template <typename T, int kBatch>
+__device__ __forceinline__ void load_batch(typename RowOf<T>::type (&raw)[kBatch], const char* x0, int gap, int n) {
+  const char* x1 = x0 + gap;
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i)
+    if (i < n) raw[i] = load_row<T>(x0 + i * kRopeD * (int)sizeof(T), x1 + i * kRopeD * (int)sizeof(T));
+}
+template <typename T>
+__device__ __forceinline__ const char* head_at(const void* base, int64_t stride, int t, int h, const RopeLane& l) {
+  return reinterpret_cast<const char*>(static_cast<const T*>(base) + t * stride + h * kRopeD + l.o0);
+}
+
+// n heads from address x0 on; raw holds the first batch.
+template <typename T, bool kInterleaved>
+__device__ __forceinline__ void turn_side(const RopeArgs& r, const float* weight, const RopeLane& l, const Angles& angle, bool in,
+                                          typename RowOf<T>::type (&raw)[kRopeBatch<T>], const char* x0, char* y0, int n) {
+  constexpr int kBatch = kRopeBatch<T>, kStep = kRopeD * sizeof(T);
+  const bool norm = r.norm != kNormNone;
+  const float inv_n = r.inv_n, eps = r.eps;
+  const int gap = (l.o1 - l.o0) * (int)sizeof(T);
+  F2 w[4];
+  load_weight(weight, l, w);
+  while (true) {
+    char* y1 = y0 + gap;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (i >= n) break;
+      F2 x[4];
+      unpack_row(raw[i], x);
+      if (norm) {
+        float unit;
+        scale_row(x, head_scale(x, inv_n, eps, unit));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], w[e]);
+      }
+      turn_row<kInterleaved>(l, angle, x);
+      if (in) store_row<T>(y0 + i * kStep, y1 + i * kStep, x);
+    }
+    n -= kBatch;
+    if (n <= 0) break;
+    x0 += kBatch * kStep;
+    y0 += kBatch * kStep;
+    load_batch<T, kBatch>(raw, x0, gap, n);
+  }
+}
+
+template <typename T, bool kInterleaved>
+__device__ __forceinline__ void turn_tokens(const QkRopeArgs& a, unsigned task) {
+  const int lane = threadIdx.x & 15;
+  const RopeLane l = rope_lane(a.r, lane);
+  const RopeTask k = rope_task(a, task);
+  const int gap = (l.o1 - l.o0) * (int)sizeof(T), n_q = k.h1 - k.h0, n_k = k.k1 - k.k0;
+  const char* q = head_at<T>(a.side[0].in, a.side[0].in_stride, k.t, k.h0, l);
+  const char* kk = head_at<T>(a.side[1].in, a.side[1].in_stride, k.t, k.k0, l);
+  typename RowOf<T>::type raw[kRopeBatch<T>];
+  load_batch<T, kRopeBatch<T>>(raw, n_q > 0 ? q : kk, gap, n_q > 0 ? n_q : n_k);
+  int pos = 0;
+  const bool in = token_position(a.pos, k.t, pos) && k.in;
+  const Angles angle = rope_angles(a.r, l, rope_freq(a.r, l, lane), pos);
+  if (n_q > 0) {
+    char* out = const_cast<char*>(head_at<T>(a.side[0].out, a.side[0].out_stride, k.t, k.h0, l));
+    turn_side<T, kInterleaved>(a.r, a.side[0].weight, l, angle, in, raw, q, out, n_q);
+    if (n_k <= 0) return;
+    load_batch<T, kRopeBatch<T>>(raw, kk, gap, n_k);
+  }
+  if (n_k > 0) {
+    char* out = const_cast<char*>(head_at<T>(a.side[1].out, a.side[1].out_stride, k.t, k.k0, l));
+    turn_side<T, kInterleaved>(a.r, a.side[1].weight, l, angle, in, raw, kk, out, n_k);
+  }
+}
+// Warps of a call, below 2^31.
+inline int64_t rope_tasks(const QkRopeArgs& a) { return (((int64_t)a.pos.T + 1) / 2) << a.shares_log2; }
+
 cudaError_t launch_qk_rope(const QkRopeArgs& a, bool f32, cudaStream_t st);
-cudaError_t launch_qk_rope_bwd(const QkRopeArgs& a, bool f32, int ctas, cudaStream_t st);
-cudaError_t launch_qk_rope_weights(const QkRopeArgs& a, int ctas, cudaStream_t st);
+cudaError_t launch_qk_rope_bwd(const QkRopeArgs& a, bool f32, cudaStream_t st);
+cudaError_t launch_qk_rope_weights(const QkRopeArgs& a, cudaStream_t st);
 
 }  // namespace gdn

@@ -126,7 +126,7 @@ def test_rope_refuses_pointers(lib):
     empty[9] = rope_dims(T=0)
     assert lib.gdn_qk_rope(*empty) == OK
     n = ctypes.c_size_t(0)
-    assert lib.gdn_qk_rope_bwd_workspace_bytes(n) == OK and n.value >= 2 * 128 * 4 * 608
+    assert lib.gdn_qk_rope_bwd_workspace_bytes(n) == OK and n.value >= 128 * 4 and n.value % (128 * 4) == 0
     assert lib.gdn_qk_rope_bwd_workspace_bytes(None) == INVALID
     good = [512, 1024, 64, 64, None, None, rope(), 2048, 4096, 512, 512, 64, 64, rope_dims(), 256, n.value, None]
     for i, bad, expect in ((9, None, INVALID), (10, None, INVALID), (14, None, WORKSPACE), (15, n.value - 1, WORKSPACE),

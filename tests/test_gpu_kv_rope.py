@@ -58,6 +58,9 @@ class Case:
         if q_out is not None:
             F.check("q", q_out, want_q, bq, self.dtype)
         k64, bk = F.rope_ref(self.k, self.pos, self.freqs, self.layout, self.mag, self.norm, self.kw)
+        # A key's cosine and sine are products of two rotations', cos a cos b - sin a sin b: each factor to
+        # 4 + 1.6 roundings, as there the one, and two more for product and sum: 8 of them beside its 19.
+        bk = bk * (27 / 19)
         ck, sk, cv, sv = K.append_ref(self.b, k64, self.v)
         assert torch.equal(self.cache.v_scale.double().cpu(), sv)
         assert torch.equal(self.cache.v.float().double().cpu(), cv)

@@ -224,6 +224,18 @@ def test_tokens_outside_every_sequence():
         assert (t[:4] == 5).all() and (t[39:] == 5).all()
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_the_rest_of_a_head_stays_apart(layout):
+    """What is not finite in the part that does not turn stays in its element, and in the other's pair."""
+    g = torch.Generator().manual_seed(20)
+    x = torch.randn(1, 2, 128, generator=g)
+    x[0, 0, [40, 101]] = math.inf
+    x[0, 1, 3] = math.nan
+    q, _ = gdn.gdn_qk_rope(x.cuda(), None, gdn.gdn_rope_table(32, layout=layout), torch.tensor([77], dtype=torch.int32, device="cuda"))
+    assert q[0, 0].isfinite().logical_not().nonzero().flatten().tolist() == [40, 101]
+    assert q[0, 1].isfinite().logical_not().nonzero().flatten().tolist() == ([3, 19] if layout == "half" else [2, 3])
+
+
 def test_no_tokens():
     c = Case([3], 2, 2, seed=12)
     q, k = gdn.gdn_qk_rope(c.gq[:0], c.gk[:0], c.rope, **c.how)

@@ -12,12 +12,13 @@
 #include <type_traits>
 
 #include "gdn_conv.cuh"
+#include "gdn_pair.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroups = kThreads / 16;
+constexpr int kWarps = kThreads / 32;
 
 // First token and end of the sequence that token t is in, within [0, T]; seq -1
 // where it is outside every one, then with the end of such tokens.
@@ -49,152 +50,153 @@ __device__ __forceinline__ ConvSeq conv_seq(const ConvArgs& a, int t) {
   return s;
 }
 
-// ---- N elements of a lane, N consecutive channels ----
-template <typename T, int N>
-struct Raw {
-  uint32_t w[N * sizeof(T) / 4];
+// ---- four consecutive channels of a lane, as two pairs of fp32 ----
+// A warp holds a head of 128 channels.
+template <typename T>
+struct RawOf;
+template <>
+struct RawOf<float> {
+  using type = float4;
 };
-template <typename T, int N>
-__device__ __forceinline__ Raw<T, N> load_raw(const void* p) {
-  Raw<T, N> r;
-  if constexpr (N * sizeof(T) == 8) {
-    const uint2 v = *static_cast<const uint2*>(p);
-    r.w[0] = v.x; r.w[1] = v.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i) {
-      const uint4 v = static_cast<const uint4*>(p)[i];
-      r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
-    }
-  }
-  return r;
+template <>
+struct RawOf<__nv_bfloat16> {
+  using type = uint2;
+};
+template <typename T>
+using Raw = typename RawOf<T>::type;
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p) {
+  return *reinterpret_cast<const Raw<T>*>(p);
 }
-template <typename T, int N>
-__device__ __forceinline__ void store_raw(void* p, const Raw<T, N>& r) {
-  if constexpr (N * sizeof(T) == 8) {
-    *static_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i)
-      static_cast<uint4*>(p)[i] = make_uint4(r.w[4 * i], r.w[4 * i + 1], r.w[4 * i + 2], r.w[4 * i + 3]);
-  }
+__device__ __forceinline__ void unpack(const float4& r, F2 (&x)[2]) {
+  x[0] = f2(r.x, r.y);
+  x[1] = f2(r.z, r.w);
 }
-template <typename T, int N>
-__device__ __forceinline__ void unpack(const Raw<T, N>& r, float (&x)[N]) {
-#pragma unroll
-  for (int i = 0; i < (int)(N * sizeof(T) / 4); ++i) {
-    if constexpr (sizeof(T) == 4) {
-      x[i] = __uint_as_float(r.w[i]);
-    } else {
-      x[2 * i] = __uint_as_float(r.w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
-    }
-  }
+__device__ __forceinline__ void unpack(const uint2& r, F2 (&x)[2]) {
+  x[0] = bf16_pair(r.x);
+  x[1] = bf16_pair(r.y);
 }
-template <typename T, int N>
-__device__ __forceinline__ Raw<T, N> pack(const float (&x)[N]) {
-  Raw<T, N> r;
-#pragma unroll
-  for (int i = 0; i < (int)(N * sizeof(T) / 4); ++i) {
-    if constexpr (sizeof(T) == 4) r.w[i] = __float_as_uint(x[i]);
-    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r.w[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
-  }
-  return r;
+__device__ __forceinline__ void store4(float* p, const F2 (&x)[2]) {
+  const float2 a = parts(x[0]), b = parts(x[1]);
+  *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
 }
-template <typename T, int N>
-__device__ __forceinline__ void load_f32(const T* p, float (&x)[N]) {
-  unpack<T, N>(load_raw<T, N>(p), x);
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const F2 (&x)[2]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pair_bf16(x[0]), pair_bf16(x[1]));
+}
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, F2 (&x)[2]) {
+  unpack(load_raw(p), x);
 }
 
-__device__ __forceinline__ float sigmoid(float u) { return __fdividef(1.f, 1.f + __expf(-u)); }
-
-template <int kLanes>
-__device__ __forceinline__ float group_sum(float v, unsigned mask) {
+// 1 / (1 + e^-u)
+__device__ __forceinline__ F2 sigmoid(F2 u) {
+  const float2 t = parts(mul2(u, f2(-1.4426950408889634f)));
+  const float2 d = parts(add2(f2(ex2_approx(t.x), ex2_approx(t.y)), f2(1.f)));
+  return f2(rcp_approx(d.x), rcp_approx(d.y));
+}
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int d = kLanes / 2; d; d >>= 1) v += __shfl_xor_sync(mask, v, d);
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
 }
-template <int N>
-__device__ __forceinline__ float dot(const float (&x)[N], const float (&y)[N]) {
-  float a = 0.f, b = 0.f;
-#pragma unroll
-  for (int e = 0; e < N; e += 2) {
-    a = fmaf(x[e], y[e], a);
-    b = fmaf(x[e + 1], y[e + 1], b);
-  }
-  return a + b;
-}
+__device__ __forceinline__ float dot(const F2 (&x)[2], const F2 (&y)[2]) { return both(fma2(x[1], y[1], mul2(x[0], y[0]))); }
 // 1 / sqrt(sum y^2 + eps) of a head; past fp32's range y is scaled by 2^-68
 // (unit), beside which eps is nothing, and the result belongs to the scaled y.
-template <int kLanes, int N>
-__device__ __forceinline__ float unit_scale(float (&y)[N], float eps, unsigned mask, float& unit) {
-  const float ss = group_sum<kLanes>(dot(y, y), mask);
+__device__ __forceinline__ float unit_scale(F2 (&y)[2], float eps, float& unit) {
+  const float ss = warp_sum(dot(y, y));
   unit = 1.f;
-  if (ss <= 3e38f) return rsqrtf(ss + eps);
+  if (ss <= 3e38f) return rsqrt_approx(ss + eps);  // all lanes have the same sum
   unit = 0x1p-68f;
-#pragma unroll
-  for (int e = 0; e < N; ++e) y[e] *= unit;
-  return rsqrtf(group_sum<kLanes>(dot(y, y), mask));
+  y[0] = mul2(y[0], f2(unit));
+  y[1] = mul2(y[1], f2(unit));
+  return rsqrt_approx(warp_sum(dot(y, y)));
 }
 
-// A lane's taps, channel by channel as they are in memory, by tap.
-template <int W, int N>
-__device__ __forceinline__ void load_taps(const float* weight, int c, float (&w)[W][N]) {
+// A lane's taps from [C, W], by tap.
+template <int W>
+__device__ __forceinline__ void load_taps(const float* weight, int c, F2 (&w)[W][2]) {
   const float4* p = reinterpret_cast<const float4*>(weight + (int64_t)c * W);
-  float f[W * N];
+  float f[W * 4];
 #pragma unroll
-  for (int i = 0; i < W * N / 4; ++i) {
+  for (int i = 0; i < W; ++i) {
     const float4 v = __ldg(p + i);
     f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
   }
 #pragma unroll
-  for (int e = 0; e < N; ++e)
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j][e] = f[e * W + j];
+  for (int j = 0; j < W; ++j) {
+    w[j][0] = f2(f[j], f[W + j]);
+    w[j][1] = f2(f[2 * W + j], f[3 * W + j]);
+  }
 }
 
-// The output row of a head: q, k or v.
+// A head's rows of the output: q, k or v.
 template <typename T>
-__device__ __forceinline__ T* head_row(const ConvArgs& a, int head, int64_t t) {
-  if (head < a.h_qk) return static_cast<T*>(a.q) + (t * a.h_qk + head) * kConvD;
-  if (head < 2 * a.h_qk) return static_cast<T*>(a.k) + (t * a.h_qk + head - a.h_qk) * kConvD;
-  return static_cast<T*>(a.v) + (t * a.h_v + head - 2 * a.h_qk) * kConvD;
+struct HeadRows {
+  T* p;
+  int64_t stride;
+};
+template <typename T>
+__device__ __forceinline__ HeadRows<T> head_rows(const ConvArgs& a, int head) {
+  if (head < a.h_qk) return {static_cast<T*>(a.q) + head * kConvD, (int64_t)a.h_qk * kConvD};
+  if (head < 2 * a.h_qk) return {static_cast<T*>(a.k) + (head - a.h_qk) * kConvD, (int64_t)a.h_qk * kConvD};
+  return {static_cast<T*>(a.v) + (head - 2 * a.h_qk) * kConvD, (int64_t)a.h_v * kConvD};
 }
 
 // The W - 1 inputs before token t: earlier tokens, then the kept state.
-template <typename T, int W, int N>
-__device__ __forceinline__ void load_window(const ConvArgs& a, const ConvSeq& s, int t, int c, int C, float (&win)[W][N]) {
+template <typename T, int W>
+__device__ __forceinline__ void load_window(const ConvArgs& a, const ConvSeq& s, int t, int c, int C, F2 (&win)[W - 1][2]) {
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     const int at = t - (W - 1) + j;
     if (at >= s.begin) {
-      load_f32<T, N>(static_cast<const T*>(a.x) + at * a.x_stride + c, win[j]);
+      load4(static_cast<const T*>(a.x) + at * a.x_stride + c, win[j]);
     } else if (a.state && s.seq >= 0) {
-      load_f32<T, N>(static_cast<const T*>(a.state) + ((int64_t)s.seq * (W - 1) + (W - 1) + at - s.begin) * C + c, win[j]);
+      load4(static_cast<const T*>(a.state) + ((int64_t)s.seq * (W - 1) + (W - 1) + at - s.begin) * C + c, win[j]);
     } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e) win[j][e] = 0.f;
+      win[j][0] = win[j][1] = f2(0.f);
     }
   }
 }
 
-// y of one token from its window; the window moves on.
-template <int W, int N>
-__device__ __forceinline__ void taps(const float (&win)[W][N], const float (&w)[W][N], const float (&b)[N], float (&u)[N]) {
+// u of the token whose inputs are x[0] .. x[W - 1].
+template <int W>
+__device__ __forceinline__ void taps(const F2 (*x)[2], const F2 (&w)[W][2], const F2 (&b)[2], F2 (&u)[2]) {
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    float v = b[e];
+  for (int i = 0; i < 2; ++i) {
+    u[i] = b[i];
 #pragma unroll
-    for (int j = 0; j < W; ++j) v = fmaf(w[j][e], win[j][e], v);
-    u[e] = v;
+    for (int j = 0; j < W; ++j) u[i] = fma2(w[j][i], x[j][i], u[i]);
   }
 }
-template <int W, int N>
-__device__ __forceinline__ void shift(float (&win)[W][N]) {
-#pragma unroll
-  for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-    for (int e = 0; e < N; ++e) win[j][e] = win[j + 1][e];
+__device__ __forceinline__ void load_bias(const float* bias, int c, F2 (&b)[2]) {
+  b[0] = b[1] = f2(0.f);
+  if (bias) load4(bias + c, b);
+}
+// ---- tokens on their way ----
+// A warp's next tokens are copied into a ring of shared memory of its own, 16
+// bytes a lane, asynchronously and group by group: in registers there is
+// room for too few (with four tokens ahead warps waited for memory three
+// times as long as they computed).
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(reinterpret_cast<uint64_t>(from)) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLater>
+__device__ __forceinline__ void copy_wait() {  // all groups but the last kLater are there
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLater) : "memory");
+}
+
+__device__ __forceinline__ void finish(F2 (&u)[2], bool silu, bool unit_head, float eps) {
+  if (silu) {
+    u[0] = mul2(u[0], sigmoid(u[0]));
+    u[1] = mul2(u[1], sigmoid(u[1]));
+  }
+  if (unit_head) {
+    float unit;
+    const F2 r = f2(unit_scale(u, eps, unit));
+    u[0] = mul2(u[0], r);
+    u[1] = mul2(u[1], r);
+  }
 }
 
 // Element i of the states after the call: row r of sequence s is the padded
@@ -202,8 +204,8 @@ __device__ __forceinline__ void shift(float (&win)[W][N]) {
 template <typename T>
 __device__ __forceinline__ void final_states(const ConvArgs& a, int64_t i, int C) {
   const int W1 = a.width - 1;
-  const int64_t row = i / (C / 8);
-  const int c = (int)(i % (C / 8)) * 8;
+  const int64_t row = i / (C / 4);
+  const int c = (int)(i % (C / 4)) * 4;
   if (row >= (int64_t)a.n_seqs * W1) return;
   const int seq = (int)(row / W1), r = (int)(row % W1);
   int begin = 0, end = 0;
@@ -215,113 +217,151 @@ __device__ __forceinline__ void final_states(const ConvArgs& a, int64_t i, int C
     end = begin + a.n_each;
   }
   const int at = end - W1 + r;
-  Raw<T, 8> v;
-  if (at >= begin) {
-    v = load_raw<T, 8>(static_cast<const T*>(a.x) + at * a.x_stride + c);
-  } else if (a.state) {
-    v = load_raw<T, 8>(static_cast<const T*>(a.state) + ((int64_t)seq * W1 + W1 + at - begin) * C + c);
-  } else {
-#pragma unroll
-    for (auto& w : v.w) w = 0;
-  }
-  store_raw<T, 8>(static_cast<T*>(a.final_state) + row * C + c, v);
+  Raw<T> v = {};
+  if (at >= begin) v = load_raw(static_cast<const T*>(a.x) + at * a.x_stride + c);
+  else if (a.state) v = load_raw(static_cast<const T*>(a.state) + ((int64_t)seq * W1 + W1 + at - begin) * C + c);
+  *reinterpret_cast<Raw<T>*>(static_cast<T*>(a.final_state) + row * C + c) = v;
 }
 
-// A half-warp a (run, head), 8 channels a lane; then CTAs for the final states.
+// A warp a (run, head); then CTAs for the final states.  Groups of four tokens
+// within a sequence go through straight code, the groups at its ends token by
+// token.
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) conv_kernel(const ConvArgs a) {
-  constexpr int N = 8, kAhead = 4;
-  const int lane = threadIdx.x & 15;
-  const unsigned mask = 0xffffu << (threadIdx.x & 16);
+__global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
+  constexpr int G = 4, kRowBytes = kConvD * sizeof(T), kRing = 4096 / kRowBytes;  // 16 tokens, or 8 of fp32
+  __shared__ alignas(16) char ring_all[kWarps][kRing * kRowBytes];
+  const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_launch_dependents();
   const int heads = 2 * a.h_qk + a.h_v, C = heads * kConvD;
-  const int64_t runs = ((int64_t)a.T + a.run - 1) / a.run, tasks = runs * heads;
-  const int64_t blocks = (tasks + kGroups - 1) / kGroups;
-  if (blockIdx.x >= blocks) {
-    final_states<T>(a, (blockIdx.x - blocks) * kThreads + threadIdx.x, C);
+  if (blockIdx.x >= (unsigned)a.blocks) {
+    final_states<T>(a, (int64_t)(blockIdx.x - a.blocks) * kThreads + threadIdx.x, C);
     return;
   }
-  const int64_t task = (int64_t)blockIdx.x * kGroups + (threadIdx.x >> 4);
-  if (task >= tasks) return;
-  const int head = (int)(task % heads), c = head * kConvD + lane * N;
-  const int t0 = (int)(task / heads) * a.run, t1 = (int)min((int64_t)a.T, (int64_t)t0 + a.run);
-  float w[W][N], b[N] = {}, win[W][N];
-  load_taps<W, N>(a.weight, c, w);
-  if (a.bias) load_f32<float, N>(a.bias + c, b);
-  ConvSeq s = conv_seq(a, t0);
-  load_window<T, W, N>(a, s, t0, c, C, win);
-  const bool unit_heads = a.norm && head < 2 * a.h_qk;
-  const T* x = static_cast<const T*>(a.x) + c;
-  for (int g = t0; g < t1; g += kAhead) {
-    Raw<T, N> raw[kAhead];
+  const unsigned task = blockIdx.x * kWarps + (threadIdx.x >> 5), run = task / (unsigned)heads;
+  const int head = (int)(task - run * heads), c = head * kConvD + 4 * lane;
+  const int64_t first = (int64_t)run * a.run;
+  if (first >= a.T) return;
+  const int t0 = (int)first, t1 = (int)min((int64_t)a.T, first + a.run);
+  const bool silu = a.silu, unit_head = a.norm && head < 2 * a.h_qk;
+  const float eps = a.eps;
+  char* ring = ring_all[threadIdx.x >> 5];
+  // the lane's part of a copy: kRows tokens at a time, 16 bytes of one of them
+  constexpr int kLanes = kRowBytes / 16, kRows = 32 / kLanes;
+  const int64_t step = kRows * a.x_stride * (int64_t)sizeof(T);
+  const char* from = static_cast<const char*>(a.x) + (((int64_t)t0 + lane / kLanes) * a.x_stride + head * kConvD) * (int64_t)sizeof(T) +
+                     lane % kLanes * 16;
+  int copied = t0 + lane / kLanes, slot = 0;  // the lane's next token; slot of the group that comes next
+  auto copy_group = [&](int at) {
+    char* to = ring + at * kRowBytes + lane * 16;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (g + i < t1) raw[i] = load_raw<T, N>(x + (g + i) * a.x_stride);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int t = g + i;
-      if (t >= t1) break;
-      if (t == s.end) {
-        s = conv_seq(a, t);
-        load_window<T, W, N>(a, s, t, c, C, win);
-      }
-      if (s.seq < 0) continue;
-      unpack<T, N>(raw[i], win[W - 1]);
-      float y[N];
-      taps<W, N>(win, w, b, y);
-      shift<W, N>(win);
-      if (a.silu) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) y[e] *= sigmoid(y[e]);
-      }
-      if (unit_heads) {
-        float unit;
-        const float r = unit_scale<16, N>(y, a.eps, mask, unit);
-#pragma unroll
-        for (int e = 0; e < N; ++e) y[e] *= r;
-      }
-      store_raw<T, N>(head_row<T>(a, head, t) + lane * N, pack<T, N>(y));
+    for (int i = 0; i < G; i += kRows) {
+      if (copied < t1) copy16(to + i * kRowBytes, from);
+      from += step;
+      copied += kRows;
     }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kRing; i += G) copy_group(i);
+  F2 w[W][2], b[2], win[W - 1][2];
+  load_taps<W>(a.weight, c, w);
+  load_bias(a.bias, c, b);
+  const HeadRows<T> rows = head_rows<T>(a, head);
+  T* y = rows.p + t0 * rows.stride + 4 * lane;
+  ConvSeq s = conv_seq(a, t0);
+  load_window<T, W>(a, s, t0, c, C, win);
+  int straight = s.seq >= 0 ? min(s.end, t1) : -1;  // where the current sequence, and straight code, ends
+  for (int g = t0; g < t1; g += G) {
+    copy_wait<kRing / G - 1>();
+    __syncwarp();
+    const T* x = reinterpret_cast<const T*>(ring + slot * kRowBytes) + 4 * lane;
+    F2 in[W - 1 + G][2];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      in[j][0] = win[j][0];
+      in[j][1] = win[j][1];
+    }
+    if (g + G <= straight) {
+      Raw<T> raw[G];
+#pragma unroll
+      for (int i = 0; i < G; ++i) raw[i] = load_raw(x + i * kConvD);
+      __syncwarp();
+      copy_group(slot);
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        unpack(raw[i], in[W - 1 + i]);
+        F2 u[2];
+        taps<W>(in + i, w, b, u);
+        finish(u, silu, unit_head, eps);
+        store4(y, u);
+        y += rows.stride;
+      }
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) {
+        win[j][0] = in[G + j][0];
+        win[j][1] = in[G + j][1];
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < min(G, t1 - g); ++i, y += rows.stride) {
+        if (g + i == s.end) {
+          s = conv_seq(a, g + i);
+          load_window<T, W>(a, s, g + i, c, C, win);
+          straight = s.seq >= 0 ? min(s.end, t1) : -1;
+        }
+        if (s.seq < 0) continue;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+          in[j][0] = win[j][0];
+          in[j][1] = win[j][1];
+        }
+        load4(x + i * kConvD, in[W - 1]);
+        F2 u[2];
+        taps<W>(in, w, b, u);
+        finish(u, silu, unit_head, eps);
+        store4(y, u);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+          win[j][0] = in[j + 1][0];
+          win[j][1] = in[j + 1][1];
+        }
+      }
+      __syncwarp();
+      copy_group(slot);
+    }
+    slot = slot + G == kRing ? 0 : slot + G;
   }
+  copy_wait<0>();
 }
 
-// One token a sequence: a half-warp a (sequence, head); the state moves on.
+// One token a sequence: a warp a (sequence, head); the state moves on.
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a) {
-  constexpr int N = 8;
-  const int lane = threadIdx.x & 15;
-  const unsigned mask = 0xffffu << (threadIdx.x & 16);
+  const int lane = threadIdx.x & 31;
   const int heads = 2 * a.h_qk + a.h_v, C = heads * kConvD;
-  const int64_t task = (int64_t)blockIdx.x * kGroups + (threadIdx.x >> 4);
+  const unsigned task = blockIdx.x * kWarps + (threadIdx.x >> 5), t = task / (unsigned)heads;
+  const int head = (int)(task - t * heads), c = head * kConvD + 4 * lane;
+  F2 w[W][2];
   grid_dependency_wait();
   grid_launch_dependents();
-  if (task >= (int64_t)a.n_seqs * heads) return;
-  const int head = (int)(task % heads), c = head * kConvD + lane * N, t = (int)(task / heads);
+  if (t >= (unsigned)a.n_seqs) return;
   T* state = static_cast<T*>(a.final_state) + (int64_t)t * (W - 1) * C + c;
-  Raw<T, N> raw[W];
+  Raw<T> raw[W];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) raw[j] = load_raw<T, N>(state + (int64_t)j * C);
-  raw[W - 1] = load_raw<T, N>(static_cast<const T*>(a.x) + t * a.x_stride + c);
-  float w[W][N], b[N] = {}, win[W][N], y[N];
-  load_taps<W, N>(a.weight, c, w);
-  if (a.bias) load_f32<float, N>(a.bias + c, b);
+  for (int j = 0; j < W - 1; ++j) raw[j] = load_raw(state + (int64_t)j * C);
+  raw[W - 1] = load_raw(static_cast<const T*>(a.x) + t * a.x_stride + c);
+  load_taps<W>(a.weight, c, w);
+  F2 in[W][2], u[2], b[2];
+  load_bias(a.bias, c, b);
 #pragma unroll
-  for (int j = 0; j < W; ++j) unpack<T, N>(raw[j], win[j]);
+  for (int j = 0; j < W; ++j) unpack(raw[j], in[j]);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) store_raw<T, N>(state + (int64_t)j * C, raw[j + 1]);
-  taps<W, N>(win, w, b, y);
-  if (a.silu) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) y[e] *= sigmoid(y[e]);
-  }
-  if (a.norm && head < 2 * a.h_qk) {
-    float unit;
-    const float r = unit_scale<16, N>(y, a.eps, mask, unit);
-#pragma unroll
-    for (int e = 0; e < N; ++e) y[e] *= r;
-  }
-  store_raw<T, N>(head_row<T>(a, head, t) + lane * N, pack<T, N>(y));
+  for (int j = 0; j < W - 1; ++j) *reinterpret_cast<Raw<T>*>(state + (int64_t)j * C) = raw[j + 1];
+  taps<W>(in, w, b, u);
+  finish(u, a.silu, a.norm && head < 2 * a.h_qk, a.eps);
+  const HeadRows<T> rows = head_rows<T>(a, head);
+  store4(rows.p + t * rows.stride + 4 * lane, u);
 }
 
 // ---- backward ----
@@ -332,143 +372,237 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a) {
 // tokens past it, whose du belong to the run's last dx; `acc` holds the W - 1
 // gradients that wait for later tokens.  The gradient before a sequence's
 // first token is its state's.
-constexpr int kWarps = kThreads / 32;
-
-template <typename T, int W, int N>
+template <typename T, int W>
 __device__ __forceinline__ void put_dx(const ConvArgs& a, const ConvSeq& s, int at, int t0, int t1, int c, int C,
-                                       const float (&v)[N]) {
+                                       const F2 (&v)[2]) {
   if (at >= s.begin) {
-    if (at >= t0 && at < t1) store_raw<T, N>(static_cast<T*>(a.dx) + at * a.dx_stride + c, pack<T, N>(v));
+    if (at >= t0 && at < t1) store4(static_cast<T*>(a.dx) + at * a.dx_stride + c, v);
   } else if (a.d_state && s.begin >= t0 && s.begin < t1) {
-    store_raw<T, N>(static_cast<T*>(a.d_state) + ((int64_t)s.seq * (W - 1) + (W - 1) + at - s.begin) * C + c, pack<T, N>(v));
+    store4(static_cast<T*>(a.d_state) + ((int64_t)s.seq * (W - 1) + (W - 1) + at - s.begin) * C + c, v);
   }
 }
 
 // The end of a sequence: nothing later adds to its last W - 1 gradients but
 // those of its final state, which are its last inputs.
-template <typename T, int W, int N>
+template <typename T, int W>
 __device__ __forceinline__ void end_sequence(const ConvArgs& a, const ConvSeq& s, int t0, int t1, int c, int C,
-                                             float (&acc)[W][N]) {
+                                             F2 (&acc)[W - 1][2]) {
   if (s.seq < 0) return;
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
     if (a.d_final) {
-      float f[N];
-      load_f32<T, N>(static_cast<const T*>(a.d_final) + ((int64_t)s.seq * (W - 1) + j) * C + c, f);
-#pragma unroll
-      for (int e = 0; e < N; ++e) acc[j][e] += f[e];
+      F2 f[2];
+      load4(static_cast<const T*>(a.d_final) + ((int64_t)s.seq * (W - 1) + j) * C + c, f);
+      acc[j][0] = add2(acc[j][0], f[0]);
+      acc[j][1] = add2(acc[j][1], f[1]);
     }
-    put_dx<T, W, N>(a, s, s.end - (W - 1) + j, t0, t1, c, C, acc[j]);
+    put_dx<T, W>(a, s, s.end - (W - 1) + j, t0, t1, c, C, acc[j]);
+    acc[j][0] = acc[j][1] = f2(0.f);
   }
+}
+
+// du of a token from its u and the gradient g of its output, in g.
+__device__ __forceinline__ void back(const F2 (&u)[2], F2 (&g)[2], bool silu, bool unit_head, float eps) {
+  F2 sg[2], y[2];
 #pragma unroll
-  for (int j = 0; j < W; ++j)
+  for (int i = 0; i < 2; ++i) {
+    sg[i] = silu ? sigmoid(u[i]) : f2(1.f);
+    y[i] = mul2(u[i], sg[i]);
+  }
+  if (unit_head) {
+    F2 n[2] = {y[0], y[1]};
+    float unit;
+    const float r = unit_scale(n, eps, unit);
+    n[0] = mul2(n[0], f2(r));
+    n[1] = mul2(n[1], f2(r));
+    const F2 m = f2(-warp_sum(dot(g, n)));
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[j][e] = 0.f;
+    for (int i = 0; i < 2; ++i) {
+      g[i] = mul2(fma2(n[i], m, g[i]), f2(r));
+      if (unit != 1.f) g[i] = mul2(g[i], f2(unit));
+    }
+  }
+  if (silu) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)  // s + y (1 - s)
+      g[i] = mul2(g[i], fma2(y[i], fma2(sg[i], f2(-1.f), f2(1.f)), sg[i]));
+  }
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const ConvArgs a) {
-  constexpr int N = 4, kAhead = 4;
-  __shared__ float sum[kWarps][W + 1][kConvD];
+__global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a) {
+  constexpr int G = sizeof(T) == 2 ? 4 : 2, kRowBytes = kConvD * sizeof(T), kRing = 2048 / kRowBytes;  // rows of x and of g: 4 KB a warp
+  __shared__ union {
+    alignas(16) char ring[kWarps][2 * kRing * kRowBytes];
+    float sum[kWarps][W + 1][kConvD];
+  } sh;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr unsigned mask = 0xffffffffu;
   grid_dependency_wait();
   grid_launch_dependents();
   const int heads = 2 * a.h_qk + a.h_v, C = heads * kConvD;
   const int head = (int)(blockIdx.x % (unsigned)heads), group = (int)(blockIdx.x / (unsigned)heads);
-  const int c = head * kConvD + lane * N;
-  float dw[W + 1][N] = {};
+  const int c = head * kConvD + 4 * lane;
+  F2 dw[W + 1][2];
+#pragma unroll
+  for (int j = 0; j <= W; ++j) dw[j][0] = dw[j][1] = f2(0.f);
   const int64_t first = ((int64_t)group * kWarps + warp) * a.run;
   if (first < a.T) {
     const int t0 = (int)first, t1 = (int)min((int64_t)a.T, first + a.run);
-    float w[W][N], b[N] = {}, win[W][N], acc[W][N] = {};
-    load_taps<W, N>(a.weight, c, w);
-    if (a.bias) load_f32<float, N>(a.bias + c, b);
-    ConvSeq s = conv_seq(a, t0);
-    load_window<T, W, N>(a, s, t0, c, C, win);
-    const bool unit_heads = a.norm && head < 2 * a.h_qk;
-    const T* x = static_cast<const T*>(a.x) + c;
-    // tokens past the run belong to it while its last sequence goes on
-    const int stop = min(t1 + W - 1, a.T);
-    bool done = false;
-    for (int g0 = t0; g0 < stop && !done; g0 += kAhead) {
-      Raw<T, N> rx[kAhead], rg[kAhead];
+    const int stop = (int)min((int64_t)a.T, first + a.run + W - 1);  // tokens past the run, while its last sequence goes on
+    const bool silu = a.silu, unit_head = a.norm && head < 2 * a.h_qk;
+    const float eps = a.eps;
+    const int64_t dxs = a.dx_stride;
+    const HeadRows<T> rows = head_rows<T>(a, head);
+    // a token's row of x, then its row of g, in the ring; bf16: a half of the warp copies either, fp32: all lanes both
+    char* ring = sh.ring[warp];
+    constexpr int kLanes = kRowBytes / 16;
+    const bool copies_g = kLanes == 16 && lane >= 16;
+    const char* from_x = reinterpret_cast<const char*>(static_cast<const T*>(a.x) + t0 * a.x_stride + head * kConvD) + lane % kLanes * 16;
+    const char* from_g = reinterpret_cast<const char*>(rows.p + t0 * rows.stride) + lane % kLanes * 16;
+    const int64_t step_x = a.x_stride * (int64_t)sizeof(T), step_g = rows.stride * (int64_t)sizeof(T);
+    const char* from = copies_g ? from_g : from_x;
+    const int64_t step = copies_g ? step_g : step_x;
+    int copied = t0, slot = 0;
+    auto copy_group = [&](int at) {
+      char* to = ring + at * 2 * kRowBytes + lane * 16;
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (g0 + i < stop) {
-          rx[i] = load_raw<T, N>(x + (g0 + i) * a.x_stride);
-          rg[i] = load_raw<T, N>(head_row<T>(a, head, g0 + i) + lane * N);
+      for (int i = 0; i < G; ++i) {
+        if (copied < stop) {
+          copy16(to + i * 2 * kRowBytes, from);
+          if (kLanes == 32) copy16(to + (i * 2 + 1) * kRowBytes, from_g);
         }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int t = g0 + i;
-        if (t >= stop) break;
-        if (t == s.end) {
-          end_sequence<T, W, N>(a, s, t0, t1, c, C, acc);
-          if (t >= t1) {
-            done = true;
-            break;
-          }
-          s = conv_seq(a, t);
-          load_window<T, W, N>(a, s, t, c, C, win);
-        }
-        if (s.seq < 0) continue;
-        unpack<T, N>(rx[i], win[W - 1]);
-        float u[N], sg[N], y[N], g[N];
-        taps<W, N>(win, w, b, u);
-        unpack<T, N>(rg[i], g);
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          sg[e] = a.silu ? sigmoid(u[e]) : 1.f;
-          y[e] = u[e] * sg[e];
-        }
-        if (unit_heads) {
-          float ys[N], unit;
-#pragma unroll
-          for (int e = 0; e < N; ++e) ys[e] = y[e];
-          const float r = unit_scale<32, N>(ys, a.eps, mask, unit);
-#pragma unroll
-          for (int e = 0; e < N; ++e) ys[e] *= r;
-          const float gn = group_sum<32>(dot(g, ys), mask);
-#pragma unroll
-          for (int e = 0; e < N; ++e) g[e] = r * (g[e] - ys[e] * gn) * unit;
-        }
-        if (a.silu) {
-#pragma unroll
-          for (int e = 0; e < N; ++e) g[e] *= sg[e] + y[e] * (1.f - sg[e]);
-        }
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-#pragma unroll
-          for (int e = 0; e < N; ++e) acc[j][e] = fmaf(w[j][e], g[e], acc[j][e]);
-        if (t < t1) {
-#pragma unroll
-          for (int j = 0; j < W; ++j)
-#pragma unroll
-            for (int e = 0; e < N; ++e) dw[j][e] = fmaf(g[e], win[j][e], dw[j][e]);
-#pragma unroll
-          for (int e = 0; e < N; ++e) dw[W][e] += g[e];
-        }
-        put_dx<T, W, N>(a, s, t - (W - 1), t0, t1, c, C, acc[0]);
-        shift<W, N>(acc);
-#pragma unroll
-        for (int e = 0; e < N; ++e) acc[W - 1][e] = 0.f;
-        shift<W, N>(win);
+        from += step;
+        if (kLanes == 32) from_g += step_g;
+        ++copied;
       }
+      copy_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kRing; i += G) copy_group(i);
+    T* dx = static_cast<T*>(a.dx) + (t0 - (W - 1)) * dxs + c;  // of the token whose gradient is whole after the group's first
+    F2 w[W][2], b[2], win[W - 1][2], acc[W - 1][2];
+    load_taps<W>(a.weight, c, w);
+    load_bias(a.bias, c, b);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) acc[j][0] = acc[j][1] = f2(0.f);
+    ConvSeq s = conv_seq(a, t0);
+    load_window<T, W>(a, s, t0, c, C, win);
+    // groups from `from_t` on that end by `straight` go through straight code
+    int straight = s.seq >= 0 ? min(s.end, t1) : -1, from_t = s.begin + W - 1;
+    bool done = false;
+    for (int g0 = t0; g0 < stop && !done; g0 += G) {
+      copy_wait<kRing / G - 1>();
+      __syncwarp();
+      const T* x = reinterpret_cast<const T*>(ring + slot * 2 * kRowBytes) + 4 * lane;
+      F2 in[W - 1 + G][2], out[W - 1 + G][2];
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          in[j][e] = win[j][e];
+          out[j][e] = acc[j][e];
+        }
+      if (g0 + G <= straight && g0 >= from_t) {
+        Raw<T> raw_x[G], raw_g[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          raw_x[i] = load_raw(x + 2 * i * kConvD);
+          raw_g[i] = load_raw(x + (2 * i + 1) * kConvD);
+        }
+        __syncwarp();
+        copy_group(slot);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          F2 u[2], g[2];
+          unpack(raw_x[i], in[W - 1 + i]);
+          unpack(raw_g[i], g);
+          taps<W>(in + i, w, b, u);
+          back(u, g, silu, unit_head, eps);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+              out[i + j][e] = j < W - 1 ? fma2(w[j][e], g[e], out[i + j][e]) : mul2(w[j][e], g[e]);
+              dw[j][e] = fma2(g[e], in[i + j][e], dw[j][e]);
+            }
+            dw[W][e] = add2(dw[W][e], g[e]);
+          }
+          if (g0 + i - (W - 1) >= t0) store4(dx, out[i]);
+          dx += dxs;
+        }
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            win[j][e] = in[G + j][e];
+            acc[j][e] = out[G + j][e];
+          }
+      } else {
+        dx += G * dxs;
+#pragma unroll 1
+        for (int i = 0; i < min(G, stop - g0); ++i) {
+          const int t = g0 + i;
+          if (t == s.end) {
+            end_sequence<T, W>(a, s, t0, t1, c, C, acc);
+            if (t >= t1) {
+              done = true;
+              break;
+            }
+            s = conv_seq(a, t);
+            load_window<T, W>(a, s, t, c, C, win);
+            straight = s.seq >= 0 ? min(s.end, t1) : -1;
+            from_t = s.begin + W - 1;
+          }
+          if (s.seq < 0) continue;
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) in[j][e] = win[j][e];
+          load4(x + 2 * i * kConvD, in[W - 1]);
+          F2 u[2], g[2], d[W][2];
+          taps<W>(in, w, b, u);
+          load4(x + (2 * i + 1) * kConvD, g);
+          back(u, g, silu, unit_head, eps);
+          const bool own = t < t1;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+              d[j][e] = j < W - 1 ? fma2(w[j][e], g[e], acc[j][e]) : mul2(w[j][e], g[e]);
+              if (own) dw[j][e] = fma2(g[e], in[j][e], dw[j][e]);
+            }
+            if (own) dw[W][e] = add2(dw[W][e], g[e]);
+          }
+          put_dx<T, W>(a, s, t - (W - 1), t0, t1, c, C, d[0]);
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              win[j][e] = in[j + 1][e];
+              acc[j][e] = d[j + 1][e];
+            }
+        }
+        __syncwarp();
+        copy_group(slot);
+      }
+      slot = slot + G == kRing ? 0 : slot + G;
     }
-    if (!done && stop == s.end) end_sequence<T, W, N>(a, s, t0, t1, c, C, acc);
+    if (!done && stop == s.end) end_sequence<T, W>(a, s, t0, t1, c, C, acc);
+    copy_wait<0>();
   }
   if (!a.sums) return;
+  __syncthreads();  // the rings are done with
 #pragma unroll
-  for (int j = 0; j <= W; ++j)
-#pragma unroll
-    for (int e = 0; e < N; ++e) sum[warp][j][lane * N + e] = dw[j][e];
+  for (int j = 0; j <= W; ++j) {
+    const float2 p = parts(dw[j][0]), q = parts(dw[j][1]);
+    *reinterpret_cast<float4*>(&sh.sum[warp][j][4 * lane]) = make_float4(p.x, p.y, q.x, q.y);
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < (W + 1) * kConvD; i += kThreads) {
     const int j = i / kConvD, at = i % kConvD;
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) v += sum[k][j][at];
+    for (int k = 0; k < kWarps; ++k) v += sh.sum[k][j][at];
     a.part[((int64_t)group * (W + 1) + j) * C + head * kConvD + at] = v;
   }
 }
@@ -485,17 +619,15 @@ __global__ void __launch_bounds__(1024) conv_bwd_sum_kernel(const ConvArgs a) {
   const int blocks = a.sums ? (W + 1) * (C / 32) : 0;
   if ((int)blockIdx.x >= blocks) {
     const int64_t i = ((int64_t)blockIdx.x - blocks) * 1024 + threadIdx.x;
-    const int64_t row = i / (C / 8);
-    const int c = (int)(i % (C / 8)) * 8;
+    const int64_t row = i / (C / 4);
+    const int c = (int)(i % (C / 4)) * 4;
     if (row >= (int64_t)a.n_seqs * (W - 1)) return;
     const int seq = (int)(row / (W - 1));
     const bool empty = a.cu ? a.cu[seq + 1] <= a.cu[seq] : a.n_each == 0;
     if (!empty) return;
-    Raw<T, 8> v;
-#pragma unroll
-    for (auto& w : v.w) w = 0;
-    if (a.d_final) v = load_raw<T, 8>(static_cast<const T*>(a.d_final) + row * C + c);
-    store_raw<T, 8>(static_cast<T*>(a.d_state) + row * C + c, v);
+    Raw<T> v = {};
+    if (a.d_final) v = load_raw(static_cast<const T*>(a.d_final) + row * C + c);
+    *reinterpret_cast<Raw<T>*>(static_cast<T*>(a.d_state) + row * C + c) = v;
     return;
   }
   const int j = blockIdx.x % (W + 1), at = (int)(blockIdx.x / (W + 1)) * 32 + lane;
@@ -523,10 +655,12 @@ cudaError_t by_width(int width, F&& f) {
 
 }  // namespace
 
-cudaError_t launch_conv(const ConvArgs& a, bool f32, cudaStream_t st) {
+cudaError_t launch_conv(const ConvArgs& args, bool f32, cudaStream_t st) {
+  ConvArgs a = args;
   const int64_t heads = 2 * a.h_qk + a.h_v, runs = ((int64_t)a.T + a.run - 1) / a.run;
-  int64_t blocks = (runs * heads + kGroups - 1) / kGroups;
-  if (a.final_state) blocks += ((int64_t)a.n_seqs * (a.width - 1) * heads * 16 + kThreads - 1) / kThreads;
+  a.blocks = (int)((runs * heads + kWarps - 1) / kWarps);
+  int64_t blocks = a.blocks;
+  if (a.final_state) blocks += ((int64_t)a.n_seqs * (a.width - 1) * heads * 32 + kThreads - 1) / kThreads;
   if (blocks == 0) return cudaSuccess;
   return by_width(a.width, [&](auto w) {
     return f32 ? launch_kernel(conv_kernel<float, decltype(w)::value>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, a)
@@ -535,7 +669,7 @@ cudaError_t launch_conv(const ConvArgs& a, bool f32, cudaStream_t st) {
 }
 
 cudaError_t launch_conv_step(const ConvArgs& a, bool f32, cudaStream_t st) {
-  const int64_t blocks = ((int64_t)a.n_seqs * (2 * a.h_qk + a.h_v) + kGroups - 1) / kGroups;
+  const int64_t blocks = ((int64_t)a.n_seqs * (2 * a.h_qk + a.h_v) + kWarps - 1) / kWarps;
   return by_width(a.width, [&](auto w) {
     return f32 ? launch_kernel(conv_step_kernel<float, decltype(w)::value>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, a)
                : launch_kernel(conv_step_kernel<__nv_bfloat16, decltype(w)::value>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, a);
@@ -553,7 +687,7 @@ cudaError_t launch_conv_bwd(const ConvArgs& a, bool f32, cudaStream_t st) {
 cudaError_t launch_conv_bwd_sums(const ConvArgs& a, bool f32, cudaStream_t st) {
   const int64_t C = (int64_t)(2 * a.h_qk + a.h_v) * kConvD;
   int64_t blocks = a.sums ? (a.width + 1) * (C / 32) : 0;
-  if (a.d_state) blocks += ((int64_t)a.n_seqs * (a.width - 1) * (C / 8) + 1023) / 1024;
+  if (a.d_state) blocks += ((int64_t)a.n_seqs * (a.width - 1) * (C / 4) + 1023) / 1024;
   if (blocks == 0) return cudaSuccess;
   return f32 ? launch_kernel(conv_bwd_sum_kernel<float>, dim3((unsigned)blocks), dim3(1024), 0, st, true, a)
              : launch_kernel(conv_bwd_sum_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(1024), 0, st, true, a);

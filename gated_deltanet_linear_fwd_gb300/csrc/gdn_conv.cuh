@@ -25,7 +25,8 @@ struct ConvArgs {
   int n_seqs, T, n_each, h_qk, h_v;
   int width, silu, norm;
   float eps;
-  int run;                 // tokens a group of lanes takes in a row
+  int run;                 // tokens a warp takes in a row
+  int blocks;              // CTAs before those for the final states
   // backward
   const void* d_final;     // [n_seqs, W - 1, C] or null (zero)
   void* dx;                // [T, C], row stride dx_stride

@@ -112,6 +112,58 @@ __device__ __forceinline__ float unit_scale(F2 (&y)[2], float eps, float& unit) 
   return rsqrt_approx(warp_sum(dot(y, y)));
 }
 
+// Sums over the warp of N values a lane, N a power of two: in the first rounds a
+// lane gives half of its values away and keeps the other half's sums, so that
+// 4 (8) values take 6 (9) shuffles and not 20 (40).  The lane ends with the sum of
+// value lane / (32 / N); group_value hands it to all.
+template <int N>
+__device__ __forceinline__ float group_sums(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  int d = 16;
+#pragma unroll
+  for (int n = N / 2; n; n >>= 1, d >>= 1) {
+    const bool upper = lane & d;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+    }
+  }
+#pragma unroll
+  for (; d; d >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], d);
+  return v[0];
+}
+template <int N>
+__device__ __forceinline__ float group_value(float sum, int i) {
+  return __shfl_sync(0xffffffffu, sum, i * (32 / N));
+}
+// Heads of G tokens to unit length at once, or one by one where a sum of
+// squares passes fp32's range.
+template <int G>
+__device__ __forceinline__ void unit_group(F2 (&y)[G][2], float eps) {
+  float v[G];
+#pragma unroll
+  for (int i = 0; i < G; ++i) v[i] = dot(y[i], y[i]);
+  const float ss = group_sums<G>(v);
+  if (__any_sync(0xffffffffu, !(ss <= 3e38f))) {
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      float unit;
+      const F2 r = f2(unit_scale(y[i], eps, unit));
+      y[i][0] = mul2(y[i][0], r);
+      y[i][1] = mul2(y[i][1], r);
+    }
+    return;
+  }
+  const float mine = rsqrt_approx(ss + eps);
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const F2 r = f2(group_value<G>(mine, i));
+    y[i][0] = mul2(y[i][0], r);
+    y[i][1] = mul2(y[i][1], r);
+  }
+}
+
 // A lane's taps from [C, W], by tap.
 template <int W>
 __device__ __forceinline__ void load_taps(const float* weight, int c, F2 (&w)[W][2]) {
@@ -186,11 +238,16 @@ __device__ __forceinline__ void copy_wait() {  // all groups but the last kLater
   asm volatile("cp.async.wait_group %0;" ::"n"(kLater) : "memory");
 }
 
-__device__ __forceinline__ void finish(F2 (&u)[2], bool silu, bool unit_head, float eps) {
-  if (silu) {
+template <bool kSilu>
+__device__ __forceinline__ void activate(F2 (&u)[2]) {
+  if (kSilu) {
     u[0] = mul2(u[0], sigmoid(u[0]));
     u[1] = mul2(u[1], sigmoid(u[1]));
   }
+}
+template <bool kSilu>
+__device__ __forceinline__ void finish(F2 (&u)[2], bool unit_head, float eps) {
+  activate<kSilu>(u);
   if (unit_head) {
     float unit;
     const F2 r = f2(unit_scale(u, eps, unit));
@@ -226,7 +283,7 @@ __device__ __forceinline__ void final_states(const ConvArgs& a, int64_t i, int C
 // A warp a (run, head); then CTAs for the final states.  Groups of four tokens
 // within a sequence go through straight code, the groups at its ends token by
 // token.
-template <typename T, int W>
+template <typename T, int W, bool kSilu>
 __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
   constexpr int G = 4, kRowBytes = kConvD * sizeof(T), kRing = 4096 / kRowBytes;  // 16 tokens, or 8 of fp32
   __shared__ alignas(16) char ring_all[kWarps][kRing * kRowBytes];
@@ -243,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
   const int64_t first = (int64_t)run * a.run;
   if (first >= a.T) return;
   const int t0 = (int)first, t1 = (int)min((int64_t)a.T, first + a.run);
-  const bool silu = a.silu, unit_head = a.norm && head < 2 * a.h_qk;
+  const bool unit_head = a.norm && head < 2 * a.h_qk;
   const float eps = a.eps;
   char* ring = ring_all[threadIdx.x >> 5];
   // the lane's part of a copy: kRows tokens at a time, 16 bytes of one of them
@@ -288,13 +345,17 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
       for (int i = 0; i < G; ++i) raw[i] = load_raw(x + i * kConvD);
       __syncwarp();
       copy_group(slot);
+      F2 u[G][2];
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         unpack(raw[i], in[W - 1 + i]);
-        F2 u[2];
-        taps<W>(in + i, w, b, u);
-        finish(u, silu, unit_head, eps);
-        store4(y, u);
+        taps<W>(in + i, w, b, u[i]);
+        activate<kSilu>(u[i]);
+      }
+      if (unit_head) unit_group<G>(u, eps);
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        store4(y, u[i]);
         y += rows.stride;
       }
 #pragma unroll
@@ -319,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
         load4(x + i * kConvD, in[W - 1]);
         F2 u[2];
         taps<W>(in, w, b, u);
-        finish(u, silu, unit_head, eps);
+        finish<kSilu>(u, unit_head, eps);
         store4(y, u);
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
@@ -336,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
 }
 
 // One token a sequence: a warp a (sequence, head); the state moves on.
-template <typename T, int W>
+template <typename T, int W, bool kSilu>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a) {
   const int lane = threadIdx.x & 31;
   const int heads = 2 * a.h_qk + a.h_v, C = heads * kConvD;
@@ -359,7 +420,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a) {
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) *reinterpret_cast<Raw<T>*>(state + (int64_t)j * C) = raw[j + 1];
   taps<W>(in, w, b, u);
-  finish(u, a.silu, a.norm && head < 2 * a.h_qk, a.eps);
+  finish<kSilu>(u, a.norm && head < 2 * a.h_qk, a.eps);
   const HeadRows<T> rows = head_rows<T>(a, head);
   store4(rows.p + t * rows.stride + 4 * lane, u);
 }
@@ -401,37 +462,64 @@ __device__ __forceinline__ void end_sequence(const ConvArgs& a, const ConvSeq& s
   }
 }
 
-// du of a token from its u and the gradient g of its output, in g.
-__device__ __forceinline__ void back(const F2 (&u)[2], F2 (&g)[2], bool silu, bool unit_head, float eps) {
-  F2 sg[2], y[2];
+// du of a token from the gradient g of its output, in g, with y and the
+// slope s + y (1 - s) of the activation.
+template <bool kSilu>
+__device__ __forceinline__ void slope_of(const F2 (&u)[2], F2 (&y)[2], F2 (&slope)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    sg[i] = silu ? sigmoid(u[i]) : f2(1.f);
-    y[i] = mul2(u[i], sg[i]);
-  }
-  if (unit_head) {
-    F2 n[2] = {y[0], y[1]};
-    float unit;
-    const float r = unit_scale(n, eps, unit);
-    n[0] = mul2(n[0], f2(r));
-    n[1] = mul2(n[1], f2(r));
-    const F2 m = f2(-warp_sum(dot(g, n)));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      g[i] = mul2(fma2(n[i], m, g[i]), f2(r));
-      if (unit != 1.f) g[i] = mul2(g[i], f2(unit));
+    if (kSilu) {
+      const F2 sg = sigmoid(u[i]);
+      y[i] = mul2(u[i], sg);
+      slope[i] = fma2(y[i], fma2(sg, f2(-1.f), f2(1.f)), sg);
+    } else {
+      y[i] = u[i];
     }
   }
-  if (silu) {
+}
+template <bool kSilu>
+__device__ __forceinline__ void times_slope(F2 (&g)[2], const F2 (&slope)[2]) {
+  if (kSilu) {
+    g[0] = mul2(g[0], slope[0]);
+    g[1] = mul2(g[1], slope[1]);
+  }
+}
+// The gradients of the y of G tokens of a head from those of its unit vectors,
+// in g: dy = r (g - y r^2 sum(g y)).  The same for each token whatever G is.
+template <int G>
+__device__ __forceinline__ void unit_back(F2 (&y)[G][2], F2 (&g)[G][2], float eps) {
+  float v[2 * G];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)  // s + y (1 - s)
-      g[i] = mul2(g[i], fma2(y[i], fma2(sg[i], f2(-1.f), f2(1.f)), sg[i]));
+  for (int i = 0; i < G; ++i) {
+    v[i] = dot(y[i], y[i]);
+    v[G + i] = dot(g[i], y[i]);
+  }
+  const float sum = group_sums<2 * G>(v);
+  if (__any_sync(0xffffffffu, !(fabsf(sum) <= 3e38f))) {  // past fp32's range: of scaled y, one by one
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      float unit;
+      const float r = unit_scale(y[i], eps, unit);
+      y[i][0] = mul2(y[i][0], f2(r));
+      y[i][1] = mul2(y[i][1], f2(r));
+      const F2 m = f2(-warp_sum(dot(g[i], y[i])));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) g[i][e] = mul2(mul2(fma2(y[i][e], m, g[i][e]), f2(r)), f2(unit));
+    }
+    return;
+  }
+  const float r_mine = rsqrt_approx(sum + eps);  // of the lanes that hold a sum of squares
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const float r = group_value<2 * G>(r_mine, i), m = -(r * r) * group_value<2 * G>(sum, G + i);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) g[i][e] = mul2(fma2(y[i][e], f2(m), g[i][e]), f2(r));
   }
 }
 
-template <typename T, int W>
+template <typename T, int W, bool kSilu>
 __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a) {
-  constexpr int G = sizeof(T) == 2 ? 4 : 2, kRowBytes = kConvD * sizeof(T), kRing = 2048 / kRowBytes;  // rows of x and of g: 4 KB a warp
+  constexpr int G = 2, kRowBytes = kConvD * sizeof(T), kRing = 2048 / kRowBytes;  // rows of x and of g: 4 KB a warp
   __shared__ union {
     alignas(16) char ring[kWarps][2 * kRing * kRowBytes];
     float sum[kWarps][W + 1][kConvD];
@@ -449,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
   if (first < a.T) {
     const int t0 = (int)first, t1 = (int)min((int64_t)a.T, first + a.run);
     const int stop = (int)min((int64_t)a.T, first + a.run + W - 1);  // tokens past the run, while its last sequence goes on
-    const bool silu = a.silu, unit_head = a.norm && head < 2 * a.h_qk;
+    const bool unit_head = a.norm && head < 2 * a.h_qk;
     const float eps = a.eps;
     const int64_t dxs = a.dx_stride;
     const HeadRows<T> rows = head_rows<T>(a, head);
@@ -511,21 +599,30 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
         }
         __syncwarp();
         copy_group(slot);
+        F2 g[G][2], slope[G][2];
+        {
+          F2 y[G][2];
+#pragma unroll
+          for (int i = 0; i < G; ++i) {
+            F2 u[2];
+            unpack(raw_x[i], in[W - 1 + i]);
+            unpack(raw_g[i], g[i]);
+            taps<W>(in + i, w, b, u);
+            slope_of<kSilu>(u, y[i], slope[i]);
+          }
+          if (unit_head) unit_back<G>(y, g, eps);
+        }
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          F2 u[2], g[2];
-          unpack(raw_x[i], in[W - 1 + i]);
-          unpack(raw_g[i], g);
-          taps<W>(in + i, w, b, u);
-          back(u, g, silu, unit_head, eps);
+          times_slope<kSilu>(g[i], slope[i]);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
             for (int j = 0; j < W; ++j) {
-              out[i + j][e] = j < W - 1 ? fma2(w[j][e], g[e], out[i + j][e]) : mul2(w[j][e], g[e]);
-              dw[j][e] = fma2(g[e], in[i + j][e], dw[j][e]);
+              out[i + j][e] = j < W - 1 ? fma2(w[j][e], g[i][e], out[i + j][e]) : mul2(w[j][e], g[i][e]);
+              dw[j][e] = fma2(g[i][e], in[i + j][e], dw[j][e]);
             }
-            dw[W][e] = add2(dw[W][e], g[e]);
+            dw[W][e] = add2(dw[W][e], g[i][e]);
           }
           if (g0 + i - (W - 1) >= t0) store4(dx, out[i]);
           dx += dxs;
@@ -559,10 +656,13 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
 #pragma unroll
             for (int e = 0; e < 2; ++e) in[j][e] = win[j][e];
           load4(x + 2 * i * kConvD, in[W - 1]);
-          F2 u[2], g[2], d[W][2];
+          F2 u[2], one[1][2], y[1][2], slope[2], d[W][2];
+          F2(&g)[2] = one[0];
           taps<W>(in, w, b, u);
           load4(x + (2 * i + 1) * kConvD, g);
-          back(u, g, silu, unit_head, eps);
+          slope_of<kSilu>(u, y[0], slope);
+          if (unit_head) unit_back<1>(y, one, eps);
+          times_slope<kSilu>(g, slope);
           const bool own = t < t1;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -647,10 +747,16 @@ __global__ void __launch_bounds__(1024) conv_bwd_sum_kernel(const ConvArgs a) {
   }
 }
 
+// f(type, taps, activation) of a call.
 template <typename F>
-cudaError_t by_width(int width, F&& f) {
-  return width == 2 ? f(std::integral_constant<int, 2>()) : width == 3 ? f(std::integral_constant<int, 3>())
-                                                                       : f(std::integral_constant<int, 4>());
+cudaError_t by_kind(const ConvArgs& a, bool f32, F&& f) {
+  auto width = [&](auto type, auto silu) {
+    return a.width == 2   ? f(type, std::integral_constant<int, 2>(), silu)
+           : a.width == 3 ? f(type, std::integral_constant<int, 3>(), silu)
+                          : f(type, std::integral_constant<int, 4>(), silu);
+  };
+  auto activation = [&](auto type) { return a.silu ? width(type, std::true_type()) : width(type, std::false_type()); };
+  return f32 ? activation(float()) : activation(__nv_bfloat16());
 }
 
 }  // namespace
@@ -662,25 +768,25 @@ cudaError_t launch_conv(const ConvArgs& args, bool f32, cudaStream_t st) {
   int64_t blocks = a.blocks;
   if (a.final_state) blocks += ((int64_t)a.n_seqs * (a.width - 1) * heads * 32 + kThreads - 1) / kThreads;
   if (blocks == 0) return cudaSuccess;
-  return by_width(a.width, [&](auto w) {
-    return f32 ? launch_kernel(conv_kernel<float, decltype(w)::value>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, a)
-               : launch_kernel(conv_kernel<__nv_bfloat16, decltype(w)::value>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, a);
+  return by_kind(a, f32, [&](auto type, auto w, auto silu) {
+    return launch_kernel(conv_kernel<decltype(type), decltype(w)::value, decltype(silu)::value>, dim3((unsigned)blocks),
+                         dim3(kThreads), 0, st, true, a);
   });
 }
 
 cudaError_t launch_conv_step(const ConvArgs& a, bool f32, cudaStream_t st) {
   const int64_t blocks = ((int64_t)a.n_seqs * (2 * a.h_qk + a.h_v) + kWarps - 1) / kWarps;
-  return by_width(a.width, [&](auto w) {
-    return f32 ? launch_kernel(conv_step_kernel<float, decltype(w)::value>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, a)
-               : launch_kernel(conv_step_kernel<__nv_bfloat16, decltype(w)::value>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, a);
+  return by_kind(a, f32, [&](auto type, auto w, auto silu) {
+    return launch_kernel(conv_step_kernel<decltype(type), decltype(w)::value, decltype(silu)::value>, dim3((unsigned)blocks),
+                         dim3(kThreads), 0, st, true, a);
   });
 }
 
 cudaError_t launch_conv_bwd(const ConvArgs& a, bool f32, cudaStream_t st) {
   const int64_t blocks = (int64_t)a.groups * (2 * a.h_qk + a.h_v);
-  return by_width(a.width, [&](auto w) {
-    return f32 ? launch_kernel(conv_bwd_kernel<float, decltype(w)::value>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, a)
-               : launch_kernel(conv_bwd_kernel<__nv_bfloat16, decltype(w)::value>, dim3((unsigned)blocks), dim3(kThreads), 0, st, true, a);
+  return by_kind(a, f32, [&](auto type, auto w, auto silu) {
+    return launch_kernel(conv_bwd_kernel<decltype(type), decltype(w)::value, decltype(silu)::value>, dim3((unsigned)blocks),
+                         dim3(kThreads), 0, st, true, a);
   });
 }
 

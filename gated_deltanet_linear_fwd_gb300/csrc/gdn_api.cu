@@ -463,16 +463,17 @@ gdn_status qk_rope_args(const gdn_rope_dims* d, const gdn_rope* rope, const floa
 }
 
 // Tokens a warp takes in a row, so that the warps (`width` of them side by side
-// over the channels) are what is resident, `fill`, or a multiple: all end together.
+// over the channels) are `fill`, what is resident or twice that, or a multiple: all end together.
 // More tokens read less twice, the W - 1 before each run; past 192 that is nothing.
-int conv_run(int64_t T, int64_t width, int64_t fill) {
-  constexpr int64_t kLeast = 8, kMost = 192;
+// A multiple of `group`, the tokens of straight code.
+int conv_run(int64_t T, int64_t width, int64_t fill, int64_t group) {
+  constexpr int64_t kLeast = 8, kMost = 192;  // both are rounded to groups
   const int64_t waves = (T * width + fill * kMost - 1) / (fill * kMost);
   const int64_t runs = std::max<int64_t>(1, std::max<int64_t>(waves, 1) * fill / width);
-  const int64_t run = (std::max<int64_t>((T + runs - 1) / runs, kLeast) + 3) / 4 * 4;
-  return (int)std::min(run, kMost);
+  const int64_t run = std::min(std::max((T + runs - 1) / runs, kLeast), kMost);
+  return (int)((run + group - 1) / group * group);
 }
-constexpr int64_t kConvFill = 152 * 24;        // warps
+constexpr int64_t kConvFill = 152 * 48;        // warps: twice what is resident
 constexpr int64_t kConvBwdFill = 152 * 2;      // CTAs
 
 gdn_status conv_args(const gdn_conv_dims* d, const float* weight, const float* bias, const int32_t* cu, ConvArgs* a) {
@@ -518,7 +519,7 @@ constexpr int kConvBwdWarps = 8;  // runs of a CTA of the gradient
 // Sets the run and the number of groups of the gradient; returns its workspace.
 size_t conv_bwd_plan(const gdn_conv_dims* d, ConvArgs* a) {
   const int heads = 2 * d->h_qk + d->h_v;
-  a->run = conv_run(((int64_t)d->T + kConvBwdWarps - 1) / kConvBwdWarps, heads, kConvBwdFill);
+  a->run = conv_run(((int64_t)d->T + kConvBwdWarps - 1) / kConvBwdWarps, heads, kConvBwdFill, 4);
   a->groups = (int)(((int64_t)d->T + a->run * kConvBwdWarps - 1) / (a->run * kConvBwdWarps));
   return (size_t)a->groups * (d->width + 1) * heads * kConvD * sizeof(float);
 }
@@ -1365,7 +1366,7 @@ gdn_status gdn_conv_fwd(const void* x, const float* weight, const float* bias, c
   a.k = k;
   a.v = v;
   a.final_state = final_state;
-  a.run = conv_run(d->T, 2 * d->h_qk + d->h_v, kConvFill);
+  a.run = conv_run(d->T, 2 * d->h_qk + d->h_v, kConvFill, 4);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   LaunchLog log;
   if (d->T == 0 && !final_state) return GDN_OK;

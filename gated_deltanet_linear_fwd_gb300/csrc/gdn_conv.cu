@@ -308,19 +308,26 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
   const int64_t step = kRows * a.x_stride * (int64_t)sizeof(T);
   const char* from = static_cast<const char*>(a.x) + (((int64_t)t0 + lane / kLanes) * a.x_stride + head * kConvD) * (int64_t)sizeof(T) +
                      lane % kLanes * 16;
-  int copied = t0 + lane / kLanes, slot = 0;  // the lane's next token; slot of the group that comes next
-  auto copy_group = [&](int at) {
+  int slot = 0;  // of the group that comes next
+  auto copy_group = [&](int at, int left) {  // left: tokens of the run from the group on
     char* to = ring + at * kRowBytes + lane * 16;
+    if (left >= G) {
 #pragma unroll
-    for (int i = 0; i < G; i += kRows) {
-      if (copied < t1) copy16(to + i * kRowBytes, from);
-      from += step;
-      copied += kRows;
+      for (int i = 0; i < G; i += kRows) {
+        copy16(to + i * kRowBytes, from);
+        from += step;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < G; i += kRows) {
+        if (i + lane / kLanes < left) copy16(to + i * kRowBytes, from);
+        from += step;
+      }
     }
     copy_commit();
   };
 #pragma unroll
-  for (int i = 0; i < kRing; i += G) copy_group(i);
+  for (int i = 0; i < kRing; i += G) copy_group(i, t1 - t0 - i);
   F2 w[W][2], b[2], win[W - 1][2];
   load_taps<W>(a.weight, c, w);
   load_bias(a.bias, c, b);
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
 #pragma unroll
       for (int i = 0; i < G; ++i) raw[i] = load_raw(x + i * kConvD);
       __syncwarp();
-      copy_group(slot);
+      copy_group(slot, t1 - g - kRing);
       F2 u[G][2];
 #pragma unroll
       for (int i = 0; i < G; ++i) {
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
         }
       }
       __syncwarp();
-      copy_group(slot);
+      copy_group(slot, t1 - g - kRing);
     }
     slot = slot + G == kRing ? 0 : slot + G;
   }
@@ -519,7 +526,8 @@ __device__ __forceinline__ void unit_back(F2 (&y)[G][2], F2 (&g)[G][2], float ep
 
 template <typename T, int W, bool kSilu>
 __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a) {
-  constexpr int G = 2, kRowBytes = kConvD * sizeof(T), kRing = 2048 / kRowBytes;  // rows of x and of g: 4 KB a warp
+  // groups of 4 tokens, 2 of fp32, done 2 at a time (with more the registers run out); a ring of 3 groups
+  constexpr int H = 2, G = sizeof(T) == 2 ? 4 : 2, kRowBytes = kConvD * sizeof(T), kRing = 3 * G;
   __shared__ union {
     alignas(16) char ring[kWarps][2 * kRing * kRowBytes];
     float sum[kWarps][W + 1][kConvD];
@@ -550,23 +558,22 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
     const int64_t step_x = a.x_stride * (int64_t)sizeof(T), step_g = rows.stride * (int64_t)sizeof(T);
     const char* from = copies_g ? from_g : from_x;
     const int64_t step = copies_g ? step_g : step_x;
-    int copied = t0, slot = 0;
-    auto copy_group = [&](int at) {
+    int slot = 0;
+    auto copy_group = [&](int at, int left) {  // left: tokens from the group on
       char* to = ring + at * 2 * kRowBytes + lane * 16;
 #pragma unroll
       for (int i = 0; i < G; ++i) {
-        if (copied < stop) {
+        if (left >= G || i < left) {
           copy16(to + i * 2 * kRowBytes, from);
           if (kLanes == 32) copy16(to + (i * 2 + 1) * kRowBytes, from_g);
         }
         from += step;
         if (kLanes == 32) from_g += step_g;
-        ++copied;
       }
       copy_commit();
     };
 #pragma unroll
-    for (int i = 0; i < kRing; i += G) copy_group(i);
+    for (int i = 0; i < kRing; i += G) copy_group(i, stop - t0 - i);
     T* dx = static_cast<T*>(a.dx) + (t0 - (W - 1)) * dxs + c;  // of the token whose gradient is whole after the group's first
     F2 w[W][2], b[2], win[W - 1][2], acc[W - 1][2];
     load_taps<W>(a.weight, c, w);
@@ -576,64 +583,58 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
     ConvSeq s = conv_seq(a, t0);
     load_window<T, W>(a, s, t0, c, C, win);
     // groups from `from_t` on that end by `straight` go through straight code
-    int straight = s.seq >= 0 ? min(s.end, t1) : -1, from_t = s.begin + W - 1;
+    int straight = s.seq >= 0 ? min(s.end, t1) : -1, from_t = max(s.begin, t0) + W - 1;
     bool done = false;
     for (int g0 = t0; g0 < stop && !done; g0 += G) {
       copy_wait<kRing / G - 1>();
       __syncwarp();
       const T* x = reinterpret_cast<const T*>(ring + slot * 2 * kRowBytes) + 4 * lane;
-      F2 in[W - 1 + G][2], out[W - 1 + G][2];
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          in[j][e] = win[j][e];
-          out[j][e] = acc[j][e];
-        }
       if (g0 + G <= straight && g0 >= from_t) {
-        Raw<T> raw_x[G], raw_g[G];
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-          raw_x[i] = load_raw(x + 2 * i * kConvD);
-          raw_g[i] = load_raw(x + (2 * i + 1) * kConvD);
-        }
-        __syncwarp();
-        copy_group(slot);
-        F2 g[G][2], slope[G][2];
-        {
-          F2 y[G][2];
+        for (int h = 0; h < G; h += H) {
+          F2 in[W - 1 + H][2], out[W - 1 + H][2], g[H][2], slope[H][2];
 #pragma unroll
-          for (int i = 0; i < G; ++i) {
-            F2 u[2];
-            unpack(raw_x[i], in[W - 1 + i]);
-            unpack(raw_g[i], g[i]);
-            taps<W>(in + i, w, b, u);
-            slope_of<kSilu>(u, y[i], slope[i]);
-          }
-          if (unit_head) unit_back<G>(y, g, eps);
-        }
+          for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-          times_slope<kSilu>(g[i], slope[i]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-              out[i + j][e] = j < W - 1 ? fma2(w[j][e], g[i][e], out[i + j][e]) : mul2(w[j][e], g[i][e]);
-              dw[j][e] = fma2(g[i][e], in[i + j][e], dw[j][e]);
+            for (int e = 0; e < 2; ++e) {
+              in[j][e] = win[j][e];
+              out[j][e] = acc[j][e];
             }
-            dw[W][e] = add2(dw[W][e], g[i][e]);
+          {
+            F2 y[H][2];
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+              F2 u[2];
+              load4(x + 2 * (h + i) * kConvD, in[W - 1 + i]);
+              load4(x + (2 * (h + i) + 1) * kConvD, g[i]);
+              taps<W>(in + i, w, b, u);
+              slope_of<kSilu>(u, y[i], slope[i]);
+            }
+            if (unit_head) unit_back<H>(y, g, eps);
           }
-          if (g0 + i - (W - 1) >= t0) store4(dx, out[i]);
-          dx += dxs;
+#pragma unroll
+          for (int i = 0; i < H; ++i) {
+            times_slope<kSilu>(g[i], slope[i]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+              for (int j = 0; j < W; ++j) {
+                out[i + j][e] = j < W - 1 ? fma2(w[j][e], g[i][e], out[i + j][e]) : mul2(w[j][e], g[i][e]);
+                dw[j][e] = fma2(g[i][e], in[i + j][e], dw[j][e]);
+              }
+              dw[W][e] = add2(dw[W][e], g[i][e]);
+            }
+            store4(dx, out[i]);
+            dx += dxs;
+          }
+#pragma unroll
+          for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              win[j][e] = in[H + j][e];
+              acc[j][e] = out[H + j][e];
+            }
         }
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            win[j][e] = in[G + j][e];
-            acc[j][e] = out[G + j][e];
-          }
       } else {
         dx += G * dxs;
 #pragma unroll 1
@@ -648,9 +649,10 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
             s = conv_seq(a, t);
             load_window<T, W>(a, s, t, c, C, win);
             straight = s.seq >= 0 ? min(s.end, t1) : -1;
-            from_t = s.begin + W - 1;
+            from_t = max(s.begin, t0) + W - 1;
           }
           if (s.seq < 0) continue;
+          F2 in[W][2];
 #pragma unroll
           for (int j = 0; j < W - 1; ++j)
 #pragma unroll
@@ -682,9 +684,9 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
               acc[j][e] = d[j + 1][e];
             }
         }
-        __syncwarp();
-        copy_group(slot);
       }
+      __syncwarp();
+      copy_group(slot, stop - g0 - kRing);
       slot = slot + G == kRing ? 0 : slot + G;
     }
     if (!done && stop == s.end) end_sequence<T, W>(a, s, t0, t1, c, C, acc);

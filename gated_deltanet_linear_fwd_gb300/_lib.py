@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -111,6 +112,28 @@ class gdn_conv_dims(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int), ("T", ctypes.c_int), ("h_qk", ctypes.c_int), ("h_v", ctypes.c_int),
                 ("width", ctypes.c_int), ("activation", ctypes.c_int), ("norm", ctypes.c_int), ("eps", ctypes.c_float),
                 ("dtype", ctypes.c_int), ("x_stride", ctypes.c_int64), ("dx_stride", ctypes.c_int64)]
+
+
+# The dims of the calls that a decode step makes, from their fields' values: a
+# third of the time that filling a Structure field by field takes.
+_pack_rope_dims = struct.Struct("@iiiiifi4x6q").pack
+_pack_conv_dims = struct.Struct("@iiiiiiifi4x2q").pack
+_pack_kv_dims = struct.Struct("@iiiiiifi4q").pack
+assert struct.calcsize("@iiiiifi4x6q") == ctypes.sizeof(gdn_rope_dims)
+assert struct.calcsize("@iiiiiiifi4x2q") == ctypes.sizeof(gdn_conv_dims)
+assert struct.calcsize("@iiiiiifi4q") == ctypes.sizeof(gdn_kv_dims)
+
+
+def rope_dims(*fields) -> gdn_rope_dims:
+    return gdn_rope_dims.from_buffer_copy(_pack_rope_dims(*fields))
+
+
+def conv_dims(*fields) -> gdn_conv_dims:
+    return gdn_conv_dims.from_buffer_copy(_pack_conv_dims(*fields))
+
+
+def kv_dims(*fields) -> gdn_kv_dims:
+    return gdn_kv_dims.from_buffer_copy(_pack_kv_dims(*fields))
 
 
 _lock = threading.Lock()

@@ -543,11 +543,18 @@ def _tokens(name: str, t: torch.Tensor, inner: int, like: torch.Tensor) -> int:
     return step
 
 
+def _place(name: str, t: torch.Tensor, shape, inner: int, like: torch.Tensor, dtype: torch.dtype, device: int):
+    """(address, token stride) of t, of like's type and device and of that shape."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, of the call's type and on its device")
+    return t.data_ptr(), 0 if t.is_contiguous() else _tokens(name, t, inner, like)
+
+
 def _f32(name: str, t: Optional[torch.Tensor], shape, device: int):
     """Address of a float32 tensor, or None."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
         raise ValueError(f"{name} must be contiguous float32 {list(shape)} on the call's device")
     return t.data_ptr()
 
@@ -555,7 +562,7 @@ def _f32(name: str, t: Optional[torch.Tensor], shape, device: int):
 def _i32(name: str, t: Optional[torch.Tensor], numel: int, device: int):
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.numel() != numel or not t.is_contiguous() or t.get_device() != device:
+    if t.dtype is not torch.int32 or t.numel() != numel or not t.is_contiguous() or t.get_device() != device:
         raise ValueError(f"{name} must be contiguous int32 with {numel} elements on the call's device")
     return t.data_ptr()
 
@@ -568,36 +575,44 @@ def _rope_raw(rope: Optional[Rope], device: int):
     return rope.raw
 
 
-def _sequences(lead, cu_seqlens: Optional[torch.Tensor]) -> int:
-    """Sequences of a call whose tensors begin with the dimensions [T] or [B, T]."""
-    if cu_seqlens is None:
-        return lead[0] if len(lead) == 2 else 1
-    if len(lead) == 2 and lead[0] != 1:
-        raise ValueError("cu_seqlens is for packed tokens, not for a batch of rows")
-    return cu_seqlens.numel() - 1
-
-
-def _qk(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions, cu_seqlens, norm, eps, rope):
-    """(a tensor of the call, its lead, dims without strides, addresses of positions and offsets, rope)."""
-    any_ = q if q is not None else k
-    if any_ is None:
-        raise ValueError("q or k is needed")
-    for name, t in (("q", q), ("k", k)):
-        if t is not None and (t.dim() not in (3, 4) or t.shape[-1] != 128 or t.shape[:-2] != any_.shape[:-2]):
-            raise ValueError(f"{name} must be [T, heads, 128] or [B, T, heads, 128], alike in q and k")
-    dev = any_.get_device()
-    if dev < 0:
+def _call(x: torch.Tensor, stream):
+    """(type, device, stream handle) of a call on x."""
+    device = x.get_device()
+    if device < 0:
         raise ValueError("the tensors must be on a GPU")
-    lead = any_.shape[:-2]
-    T = lead.numel()
-    n = _sequences(lead, cu_seqlens)
-    dims = L.gdn_rope_dims(n, T, 0 if q is None else q.shape[-2], 0 if k is None else k.shape[-2], _choice("norm", _NORMS, norm),
-                           eps, _DT.get(any_.dtype, -1))
-    return any_, dims, _i32("positions", positions, T, dev), _i32("cu_seqlens", cu_seqlens, n + 1, dev), _rope_raw(rope, dev)
+    return x.dtype, device, _raw_stream(stream, x)
+
+
+def _sequences(lead, cu_seqlens: Optional[torch.Tensor], device: int):
+    """(sequences, tokens, address of the offsets) of a call whose tensors begin with the dimensions [T] or [B, T]."""
+    if len(lead) == 1:
+        n, T = 1, lead[0]
+    else:
+        n, T = lead[0], lead[0] * lead[1]
+    if cu_seqlens is None:
+        return n, T, None
+    if len(lead) == 2 and n != 1:
+        raise ValueError("cu_seqlens is for packed tokens, not for a batch of rows")
+    n = cu_seqlens.numel() - 1
+    return n, T, _i32("cu_seqlens", cu_seqlens, n + 1, device)
 
 
 def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+def _heads(name: str, t: torch.Tensor, like: torch.Tensor, dtype: torch.dtype, device: int):
+    """(address, token stride, heads, shape) of queries or keys that go with `like`."""
+    shape = t.shape
+    n = len(shape)
+    if (n != 3 and n != 4) or shape[-1] != 128 or (t is not like and shape[:-2] != like.shape[:-2]):
+        raise ValueError(f"{name} must be [T, heads, 128] or [B, T, heads, 128], alike in q and k")
+    if t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be of the call's type and on its device")
+    return t.data_ptr(), 0 if t.is_contiguous() else _tokens(name, t, 2, like), shape[-2], shape
+
+
+_NO_HEADS = (None, 0, 0, None)
 
 
 def gdn_qk_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: Optional[Rope] = None,
@@ -610,25 +625,27 @@ def gdn_qk_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: Opti
     one a token; else counted within each sequence of cu_seqlens, or each row.
     The tensors may be parts of one projection; an output may be its input.
     Returns (q_out, k_out), without a history (gdn_qk_rope_bwd)."""
-    x, dims, pos, cu, raw = _qk(q, k, positions, cu_seqlens, norm, eps, rope)
-    dev = x.get_device()
-    handle = _raw_stream(stream, x)
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k is needed")
+    qp, qs, h_q, q_shape = _NO_HEADS if q is None else _heads("q", q, x, x.dtype, x.get_device())
+    kp, ks, h_k, k_shape = _NO_HEADS if k is None else _heads("k", k, x, x.dtype, x.get_device())
+    dtype, dev, handle = _call(x, stream)
+    n, T, cu = _sequences((q_shape or k_shape)[:-2], cu_seqlens, dev)
+    qo = ko = None
+    qos = kos = 0
     if q is not None:
-        dims.q_stride = _tokens("q", q, 2, x)
         if q_out is None:
-            q_out = _kv_empty(q.shape, q.dtype, q.device, stream)
-        elif q_out.shape != q.shape:
-            raise ValueError("q_out must be like q")
-        dims.q_out_stride = _tokens("q_out", q_out, 2, x)
+            q_out = _kv_empty(q_shape, dtype, q.device, stream)
+        qo, qos = _place("q_out", q_out, q_shape, 2, x, dtype, dev)
     if k is not None:
-        dims.k_stride = _tokens("k", k, 2, x)
         if k_out is None:
-            k_out = _kv_empty(k.shape, k.dtype, k.device, stream)
-        elif k_out.shape != k.shape:
-            raise ValueError("k_out must be like k")
-        dims.k_out_stride = _tokens("k_out", k_out, 2, x)
-    st = L.load().gdn_qk_rope(_at(q), _at(k), _f32("q_weight", q_weight, (128,), dev), _f32("k_weight", k_weight, (128,), dev),
-                              pos, cu, raw, _at(q_out), _at(k_out), dims, handle)
+            k_out = _kv_empty(k_shape, dtype, k.device, stream)
+        ko, kos = _place("k_out", k_out, k_shape, 2, x, dtype, dev)
+    st = L.load().gdn_qk_rope(qp, kp, _f32("q_weight", q_weight, (128,), dev), _f32("k_weight", k_weight, (128,), dev),
+                              _i32("positions", positions, T, dev), cu, _rope_raw(rope, dev), qo, ko,
+                              L.rope_dims(n, T, h_q, h_k, _choice("norm", _NORMS, norm), eps, _DT.get(dtype, -1), qs, ks, qos, kos,
+                                          0, 0), handle)
     L.check(st, "gdn_qk_rope")
     return q_out, k_out
 
@@ -650,33 +667,34 @@ def gdn_qk_rope_bwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor], d_q_ou
     without the weight.  d_q may be d_q_out, d_k may be d_k_out."""
     if (q is None) != (d_q_out is None) or (k is None) != (d_k_out is None):
         raise ValueError("d_q_out and d_k_out go with q and k")
-    x, dims, pos, cu, raw = _qk(q, k, positions, cu_seqlens, norm, eps, rope)
-    dev = x.get_device()
-    handle = _raw_stream(stream, x)
-    for name, t, g in (("q", q, d_q_out), ("k", k, d_k_out)):
-        if t is not None and g.shape != t.shape:
-            raise ValueError(f"d_{name}_out must be like {name}")
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k is needed")
+    qp, qs, h_q, q_shape = _NO_HEADS if q is None else _heads("q", q, x, x.dtype, x.get_device())
+    kp, ks, h_k, k_shape = _NO_HEADS if k is None else _heads("k", k, x, x.dtype, x.get_device())
+    dtype, dev, handle = _call(x, stream)
+    n, T, cu = _sequences((q_shape or k_shape)[:-2], cu_seqlens, dev)
+    gq = gk = dqp = dkp = None
+    gqs = gks = dqs = dks = 0
     if q is not None:
-        dims.q_stride, dims.q_out_stride = _tokens("q", q, 2, x), _tokens("d_q_out", d_q_out, 2, x)
+        gq, gqs = _place("d_q_out", d_q_out, q_shape, 2, x, dtype, dev)
         if d_q is None:
-            d_q = _kv_empty(q.shape, q.dtype, q.device, stream)
-        elif d_q.shape != q.shape:
-            raise ValueError("d_q must be like q")
-        dims.dq_stride = _tokens("d_q", d_q, 2, x)
+            d_q = _kv_empty(q_shape, dtype, q.device, stream)
+        dqp, dqs = _place("d_q", d_q, q_shape, 2, x, dtype, dev)
     if k is not None:
-        dims.k_stride, dims.k_out_stride = _tokens("k", k, 2, x), _tokens("d_k_out", d_k_out, 2, x)
+        gk, gks = _place("d_k_out", d_k_out, k_shape, 2, x, dtype, dev)
         if d_k is None:
-            d_k = _kv_empty(k.shape, k.dtype, k.device, stream)
-        elif d_k.shape != k.shape:
-            raise ValueError("d_k must be like k")
-        dims.dk_stride = _tokens("d_k", d_k, 2, x)
+            d_k = _kv_empty(k_shape, dtype, k.device, stream)
+        dkp, dks = _place("d_k", d_k, k_shape, 2, x, dtype, dev)
     qw, kw = _f32("q_weight", q_weight, (128,), dev), _f32("k_weight", k_weight, (128,), dev)
     dqw = None if qw is None else _kv_empty((128,), torch.float32, x.device, stream)
     dkw = None if kw is None else _kv_empty((128,), torch.float32, x.device, stream)
     if workspace is None and (dqw is not None or dkw is not None):
         workspace = _kv_empty(gdn_qk_rope_bwd_workspace_bytes(), torch.uint8, x.device, stream)
-    st = L.load().gdn_qk_rope_bwd(_at(q), _at(k), qw, kw, pos, cu, raw, _at(d_q_out), _at(d_k_out), _at(d_q), _at(d_k), _at(dqw),
-                                  _at(dkw), dims, *_workspace(workspace, dev), handle)
+    st = L.load().gdn_qk_rope_bwd(qp, kp, qw, kw, _i32("positions", positions, T, dev), cu, _rope_raw(rope, dev), gq, gk, dqp, dkp,
+                                  _at(dqw), _at(dkw),
+                                  L.rope_dims(n, T, h_q, h_k, _choice("norm", _NORMS, norm), eps, _DT.get(dtype, -1), qs, ks, gqs,
+                                              gks, dqs, dks), *_workspace(workspace, dev), handle)
     L.check(st, "gdn_qk_rope_bwd")
     return d_q, d_k, dqw, dkw
 
@@ -700,60 +718,67 @@ def gdn_kv_append_rope(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_lens
     Positions are those of the cache.  Returns q_out [T, h_q, 128], or None
     without q; q_out may be q itself."""
     n, max_pages, cu = _kv_ints(cache, kv_lens, page_table, cu_seqlens)
-    dev = cache.device_index
     h_kv = cache.raw.h_kv
-    ks, vs = _kv_rows("k", k, h_kv, cache), _kv_rows("v", v, h_kv, cache)
-    if v.dtype != k.dtype or v.shape != k.shape or k.shape[2] != 128:
-        raise ValueError("k and v must be alike, with 128 elements a head")
-    handle = _raw_stream(stream, k)
-    h_q, qs, outs = h_kv, 0, 0
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != h_kv or shape[2] != 128:
+        raise ValueError(f"k must be [T, {h_kv}, 128]")
+    dtype, dev, handle = _call(k, stream)
+    if dev != cache.device_index:
+        raise ValueError("k must be on the cache's device")
+    kp, ks = k.data_ptr(), 0 if k.is_contiguous() else _tokens("k", k, 2, k)
+    vp, vs = _place("v", v, shape, 2, k, dtype, dev)
+    h_q, qp, qo, qs, qos = h_kv, None, None, 0, 0
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != 128 or q.dtype != k.dtype:
-            raise ValueError("q must be [T, h_q, 128], of the keys' type")
-        h_q = q.shape[1]
-        qs = _kv_rows("q", q, h_q, cache)
+        qp, qs, h_q, q_shape = _heads("q", q, k, dtype, dev)
         if q_out is None:
-            q_out = _kv_empty(q.shape, q.dtype, q.device, stream)
-        elif q_out.dtype != q.dtype or q_out.shape != q.shape:
-            raise ValueError("q_out must be like q")
-        outs = _kv_rows("q_out", q_out, h_q, cache)
+            q_out = _kv_empty(q_shape, dtype, q.device, stream)
+        qo, qos = _place("q_out", q_out, q_shape, 2, k, dtype, dev)
     elif q_out is not None:
         raise ValueError("q_out goes with q")
-    dims = L.gdn_kv_dims(n, k.shape[0], h_q, max_pages, 1, 0, 0.0, _DT.get(k.dtype, -1), qs, ks, vs, outs)
-    st = L.load().gdn_kv_append_rope(k.data_ptr(), v.data_ptr(), _f32("k_weight", k_weight, (128,), dev), _at(q),
-                                     _f32("q_weight", q_weight, (128,), dev), _at(q_out), kv_lens.data_ptr(), page_table.data_ptr(),
-                                     cu, cache.raw, dims, _rope_raw(rope, dev), _choice("norm", _NORMS, norm), eps, handle)
+    st = L.load().gdn_kv_append_rope(kp, vp, _f32("k_weight", k_weight, (128,), dev), qp, _f32("q_weight", q_weight, (128,), dev), qo,
+                                     kv_lens.data_ptr(), page_table.data_ptr(), cu, cache.raw,
+                                     L.kv_dims(n, shape[0], h_q, max_pages, 1, 0, 0.0, _DT.get(dtype, -1), qs, ks, vs, qos),
+                                     _rope_raw(rope, dev), _choice("norm", _NORMS, norm), eps, handle)
     L.check(st, "gdn_kv_append_rope")
     return q_out
 
 
-def _conv(x: torch.Tensor, weight: torch.Tensor, h_qk: int, bias, cu_seqlens, activation: str, norm: bool, eps: float):
-    """(lead dimensions, value heads, dims, addresses of weight, bias and offsets) of a convolution of x."""
-    if x.dim() not in (2, 3):
-        raise ValueError("x must be [T, C] or [B, T, C]")
-    C, dev = x.shape[-1], x.get_device()
-    if dev < 0:
-        raise ValueError("the tensors must be on a GPU")
-    h_v = C // 128 - 2 * h_qk
-    if C % 128 or h_qk < 1 or h_v < 1:
-        raise ValueError("x must have (2 h_qk + h_v) * 128 channels")
-    if weight.dim() != 2:
-        raise ValueError("weight must be [C, W]")
-    lead = x.shape[:-1]
-    n = _sequences(lead, cu_seqlens)
-    dims = L.gdn_conv_dims(n, lead.numel(), h_qk, h_v, weight.shape[1], _choice("activation", _ACTIVATIONS, activation),
-                           int(bool(norm)), eps, _DT.get(x.dtype, -1), _tokens("x", x, 1, x), 0)
-    return (lead, h_v, dims, _f32("weight", weight, (C, weight.shape[1]), dev), _f32("bias", bias, (C,), dev),
-            _i32("cu_seqlens", cu_seqlens, n + 1, dev))
+class _Conv:
+    """What the calls of a convolution share: x's shape, type, device and stream,
+    the addresses of weight, bias and offsets, and the dims' values."""
+    __slots__ = ("x", "lead", "C", "h_v", "n", "T", "W", "dtype", "device", "handle", "weight", "bias", "cu", "stream", "how", "stride")
 
+    def __init__(self, x, weight, h_qk, bias, cu_seqlens, activation, norm, eps, stream):
+        shape = x.shape
+        if len(shape) not in (2, 3):
+            raise ValueError("x must be [T, C] or [B, T, C]")
+        self.x, self.lead, self.C, self.stream = x, shape[:-1], shape[-1], stream
+        self.h_v = self.C // 128 - 2 * h_qk
+        if self.C % 128 or h_qk < 1 or self.h_v < 1:
+            raise ValueError("x must have (2 h_qk + h_v) * 128 channels")
+        if weight.dim() != 2:
+            raise ValueError("weight must be [C, W]")
+        self.dtype, self.device, self.handle = _call(x, stream)
+        self.n, self.T, self.cu = _sequences(self.lead, cu_seqlens, self.device)
+        self.W = weight.size(1)
+        self.weight = _f32("weight", weight, (self.C, self.W), self.device)
+        self.bias = _f32("bias", bias, (self.C,), self.device)
+        self.stride = 0 if x.is_contiguous() else _tokens("x", x, 1, x)
+        self.how = (h_qk, self.h_v, self.W, _choice("activation", _ACTIVATIONS, activation), 1 if norm else 0, eps,
+                    _DT.get(self.dtype, -1), self.stride)
 
-def _like(name: str, t: Optional[torch.Tensor], shape, x: torch.Tensor, stream, make: bool = True):
-    """t, checked to be contiguous, of that shape and of x's type and device; a new one for None if `make`."""
-    if t is None:
-        return _kv_empty(shape, x.dtype, x.device, stream) if make else None
-    if t.shape != shape or t.dtype != x.dtype or not t.is_contiguous() or t.get_device() != x.get_device():
-        raise ValueError(f"{name} must be contiguous {list(shape)}, of x's type, on its device")
-    return t
+    def dims(self, dx_stride: int = 0, n: Optional[int] = None) -> L.gdn_conv_dims:
+        return L.conv_dims(self.n if n is None else n, self.T, *self.how, dx_stride)
+
+    def like(self, name: str, t: Optional[torch.Tensor], shape, make: bool = True):
+        """(t, address), checked to be contiguous, of that shape and of x's type and device; a new one for None if `make`."""
+        if t is None:
+            if not make:
+                return None, None
+            t = _kv_empty(shape, self.dtype, self.x.device, self.stream)
+        elif t.dtype is not self.dtype or t.get_device() != self.device or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {list(shape)}, of x's type, on its device")
+        return t, t.data_ptr()
 
 
 def gdn_conv_fwd(x: torch.Tensor, weight: torch.Tensor, h_qk: int, bias: Optional[torch.Tensor] = None,
@@ -767,16 +792,14 @@ def gdn_conv_fwd(x: torch.Tensor, weight: torch.Tensor, h_qk: int, bias: Optiona
     initial_state [N, W - 1, C] like x, or None.  norm: q's and k's heads to unit
     length.  Returns (q, k, v, final_state or None), q, k, v as gdn_chunk_fwd
     takes them, without a history (gdn_conv_bwd)."""
-    lead, h_v, dims, w, b, cu = _conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps)
-    handle = _raw_stream(stream, x)
-    states = (dims.n_seqs, dims.width - 1, x.shape[-1])
-    q = _like("q", q, (*lead, h_qk, 128), x, stream)
-    k = _like("k", k, (*lead, h_qk, 128), x, stream)
-    v = _like("v", v, (*lead, h_v, 128), x, stream)
-    initial_state = _like("initial_state", initial_state, states, x, stream, False)
-    final_state = _like("final_state", final_state, states, x, stream, output_final_state)
-    st = L.load().gdn_conv_fwd(x.data_ptr(), w, b, _at(initial_state), cu, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                               _at(final_state), dims, handle)
+    c = _Conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps, stream)
+    states, heads = (c.n, c.W - 1, c.C), (*c.lead, h_qk, 128)
+    q, qp = c.like("q", q, heads)
+    k, kp = c.like("k", k, heads)
+    v, vp = c.like("v", v, (*c.lead, c.h_v, 128))
+    _, before = c.like("initial_state", initial_state, states, False)
+    final_state, after = c.like("final_state", final_state, states, output_final_state)
+    st = L.load().gdn_conv_fwd(x.data_ptr(), c.weight, c.bias, before, c.cu, qp, kp, vp, after, c.dims(), c.handle)
     L.check(st, "gdn_conv_fwd")
     return q, k, v, final_state
 
@@ -799,31 +822,28 @@ def gdn_conv_bwd(x: torch.Tensor, weight: torch.Tensor, h_qk: int, d_q: torch.Te
     d_v and d_final_state (None: zero) like its outputs.  Returns (dx, d_weight,
     d_bias or None, d_initial_state or None): the bias's without a bias and, unless
     want_initial_state_grad says so, the state's without a state are None."""
-    lead, h_v, dims, w, b, cu = _conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps)
-    handle = _raw_stream(stream, x)
-    states = (dims.n_seqs, dims.width - 1, x.shape[-1])
-    d_q = _like("d_q", d_q, (*lead, h_qk, 128), x, stream, False)
-    d_k = _like("d_k", d_k, (*lead, h_qk, 128), x, stream, False)
-    d_v = _like("d_v", d_v, (*lead, h_v, 128), x, stream, False)
-    initial_state = _like("initial_state", initial_state, states, x, stream, False)
-    d_final_state = _like("d_final_state", d_final_state, states, x, stream, False)
+    c = _Conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps, stream)
+    states, heads = (c.n, c.W - 1, c.C), (*c.lead, h_qk, 128)
+    _, gq = c.like("d_q", d_q, heads, False)
+    _, gk = c.like("d_k", d_k, heads, False)
+    _, gv = c.like("d_v", d_v, (*c.lead, c.h_v, 128), False)
+    _, before = c.like("initial_state", initial_state, states, False)
+    _, after = c.like("d_final_state", d_final_state, states, False)
+    device = x.device
     if dx is None:
-        dx = _kv_empty(x.shape, x.dtype, x.device, stream)
-    elif dx.shape != x.shape:
-        raise ValueError("dx must be like x")
-    dims.dx_stride = _tokens("dx", dx, 1, x)
+        dx = _kv_empty(x.shape, c.dtype, device, stream)
+    dxp, dx_stride = _place("dx", dx, x.shape, 1, x, c.dtype, c.device)
     want = initial_state is not None if want_initial_state_grad is None else want_initial_state_grad
-    d_state = _kv_empty(states, x.dtype, x.device, stream) if want else None
-    d_weight = _kv_empty(weight.shape, torch.float32, x.device, stream)
-    d_bias = None if bias is None else _kv_empty(bias.shape, torch.float32, x.device, stream)
-    lib = L.load()
+    d_state = _kv_empty(states, c.dtype, device, stream) if want else None
+    d_weight = _kv_empty((c.C, c.W), torch.float32, device, stream)
+    d_bias = None if bias is None else _kv_empty((c.C,), torch.float32, device, stream)
+    lib, dims = L.load(), c.dims(dx_stride)
     if workspace is None:
         n = ctypes.c_size_t(0)
         L.check(lib.gdn_conv_bwd_workspace_bytes(dims, n), "gdn_conv_bwd_workspace_bytes")
-        workspace = _kv_empty(max(256, int(n.value)), torch.uint8, x.device, stream)
-    st = lib.gdn_conv_bwd(x.data_ptr(), w, b, _at(initial_state), cu, _at(d_q), _at(d_k), _at(d_v), _at(d_final_state),
-                          dx.data_ptr(), d_weight.data_ptr(), _at(d_bias), _at(d_state), dims,
-                          *_workspace(workspace, x.get_device()), handle)
+        workspace = _kv_empty(max(256, int(n.value)), torch.uint8, device, stream)
+    st = lib.gdn_conv_bwd(x.data_ptr(), c.weight, c.bias, before, c.cu, gq, gk, gv, after, dxp, d_weight.data_ptr(), _at(d_bias),
+                          _at(d_state), dims, *_workspace(workspace, c.device), c.handle)
     L.check(st, "gdn_conv_bwd")
     return dx, d_weight, d_bias, d_state
 
@@ -836,15 +856,14 @@ def gdn_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, h_
     128], as gdn_decode_step takes them."""
     if x.dim() != 2:
         raise ValueError("x must be [N, C]")
-    lead, h_v, dims, w, b, _ = _conv(x, weight, h_qk, bias, None, activation, norm, eps)
-    dims.n_seqs = dims.T
-    handle = _raw_stream(stream, x)
+    c = _Conv(x, weight, h_qk, bias, None, activation, norm, eps, stream)
+    heads = (c.T, h_qk, 128)
     if state is None:
         raise ValueError("state is needed")
-    _like("state", state, (dims.T, dims.width - 1, x.shape[1]), x, stream)
-    q = _like("q", q, (*lead, h_qk, 128), x, stream)
-    k = _like("k", k, (*lead, h_qk, 128), x, stream)
-    v = _like("v", v, (*lead, h_v, 128), x, stream)
-    st = L.load().gdn_conv_step(x.data_ptr(), w, b, state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), dims, handle)
+    _, sp = c.like("state", state, (c.T, c.W - 1, c.C))
+    q, qp = c.like("q", q, heads)
+    k, kp = c.like("k", k, heads)
+    v, vp = c.like("v", v, (c.T, c.h_v, 128))
+    st = L.load().gdn_conv_step(x.data_ptr(), c.weight, c.bias, sp, qp, kp, vp, c.dims(n=c.T), c.handle)
     L.check(st, "gdn_conv_step")
     return q, k, v

@@ -420,17 +420,7 @@ void rope_shares(int64_t T, int heads, int* log2, int* share) {
   while ((1 << *log2) < heads && ((T + 1) / 2 << *log2) < kFill) ++*log2;
   *share = (heads + (1 << *log2) - 1) >> *log2;
 }
-constexpr int kRopeBwdCtas = 3 * 152;  // of a gradient: what is resident
-// Shares and CTAs of a gradient: the latter by the sides' heads, and no more than there is to do.
-void rope_bwd_plan(int64_t T, RopeSide (&side)[2]) {
-  const int heads = side[0].heads + side[1].heads;
-  for (RopeSide& s : side) {
-    if (!s.heads) continue;
-    rope_shares(T, s.heads, &s.shares_log2, &s.share);
-    const int64_t blocks = ((((T + 1) / 2) << s.shares_log2) + kRopeWarps - 1) / kRopeWarps;
-    s.ctas = (int)std::min<int64_t>(blocks, std::max<int64_t>(1, ((int64_t)kRopeBwdCtas * s.heads + heads / 2) / heads));
-  }
-}
+constexpr int kRopeBwdCtas = 2 * 152;  // of a gradient: what is resident, and rows of its workspace
 
 // Checks of gdn_qk_rope and its gradient that do not need the tensors.
 gdn_status qk_rope_args(const gdn_rope_dims* d, const gdn_rope* rope, const float* q_weight, const float* k_weight,
@@ -1261,7 +1251,7 @@ gdn_status gdn_qk_rope(const void* q, const void* k, const float* q_weight, cons
 
 gdn_status gdn_qk_rope_bwd_workspace_bytes(size_t* bytes) {
   if (!bytes) return GDN_ERR_INVALID_ARG;
-  *bytes = (size_t)(kRopeBwdCtas + 1) * kRopeD * sizeof(float);  // the sides' shares are rounded
+  *bytes = (size_t)kRopeBwdCtas * 2 * kRopeD * sizeof(float);
   return GDN_OK;
 }
 
@@ -1297,7 +1287,10 @@ gdn_status gdn_qk_rope_bwd(const void* q, const void* k, const float* q_weight, 
   a.side[0].d_weight = dq_weight;
   a.side[1].d_weight = dk_weight;
   a.part = sums ? static_cast<float*>(workspace) : nullptr;
-  rope_bwd_plan(d->T, a.side);
+  // a head of two tokens for a warp, at least
+  const int64_t units = ((int64_t)d->T + 1) / 2 * (d->h_q + d->h_k);
+  a.ctas = (int)std::min<int64_t>((units + kRopeWarps - 1) / kRopeWarps, kRopeBwdCtas);
+  if (units / a.ctas / kRopeWarps >= INT_MAX - 1) return GDN_ERR_INVALID_ARG;  // a warp's heads are counted in 32 bits
   LaunchLog log;
   e = log.before(cs);
   if (e == cudaSuccess) e = launch_qk_rope_bwd(a, d->dtype == GDN_F32, cs);

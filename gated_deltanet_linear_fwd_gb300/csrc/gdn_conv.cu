@@ -224,20 +224,6 @@ __device__ __forceinline__ void load_bias(const float* bias, int c, F2 (&b)[2]) 
   b[0] = b[1] = f2(0.f);
   if (bias) load4(bias + c, b);
 }
-// ---- tokens on their way ----
-// A warp's next tokens are copied into a ring of shared memory of its own, 16
-// bytes a lane, asynchronously and group by group: in registers there is
-// room for too few (with four tokens ahead warps waited for memory three
-// times as long as they computed).
-__device__ __forceinline__ void copy16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(reinterpret_cast<uint64_t>(from)) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLater>
-__device__ __forceinline__ void copy_wait() {  // all groups but the last kLater are there
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLater) : "memory");
-}
-
 template <bool kSilu>
 __device__ __forceinline__ void activate(F2 (&u)[2]) {
   if (kSilu) {
@@ -280,7 +266,10 @@ __device__ __forceinline__ void final_states(const ConvArgs& a, int64_t i, int C
   *reinterpret_cast<Raw<T>*>(static_cast<T*>(a.final_state) + row * C + c) = v;
 }
 
-// A warp a (run, head); then CTAs for the final states.  Groups of four tokens
+// A warp a (run, head); then CTAs for the final states.  A warp's next tokens are
+// copied into a ring of shared memory of its own: in registers there is room
+// for too few (with four tokens ahead warps waited for memory three times as
+// long as they computed).  Groups of four tokens
 // within a sequence go through straight code, the groups at its ends token by
 // token.
 template <typename T, int W, bool kSilu>
@@ -295,14 +284,14 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
     final_states<T>(a, (int64_t)(blockIdx.x - a.blocks) * kThreads + threadIdx.x, C);
     return;
   }
-  const unsigned task = blockIdx.x * kWarps + (threadIdx.x >> 5), run = task / (unsigned)heads;
+  const unsigned warp = warp_index(), task = blockIdx.x * kWarps + warp, run = task / (unsigned)heads;
   const int head = (int)(task - run * heads), c = head * kConvD + 4 * lane;
   const int64_t first = (int64_t)run * a.run;
   if (first >= a.T) return;
   const int t0 = (int)first, t1 = (int)min((int64_t)a.T, first + a.run);
   const bool unit_head = a.norm && head < 2 * a.h_qk;
   const float eps = a.eps;
-  char* ring = ring_all[threadIdx.x >> 5];
+  char* ring = ring_all[warp];
   // the lane's part of a copy: kRows tokens at a time, 16 bytes of one of them
   constexpr int kLanes = kRowBytes / 16, kRows = 32 / kLanes;
   const int64_t step = kRows * a.x_stride * (int64_t)sizeof(T);
@@ -408,7 +397,7 @@ template <typename T, int W, bool kSilu>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a) {
   const int lane = threadIdx.x & 31;
   const int heads = 2 * a.h_qk + a.h_v, C = heads * kConvD;
-  const unsigned task = blockIdx.x * kWarps + (threadIdx.x >> 5), t = task / (unsigned)heads;
+  const unsigned task = blockIdx.x * kWarps + warp_index(), t = task / (unsigned)heads;
   const int head = (int)(task - t * heads), c = head * kConvD + 4 * lane;
   F2 w[W][2];
   grid_dependency_wait();
@@ -532,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
     alignas(16) char ring[kWarps][2 * kRing * kRowBytes];
     float sum[kWarps][W + 1][kConvD];
   } sh;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = (int)warp_index();
   grid_dependency_wait();
   grid_launch_dependents();
   const int heads = 2 * a.h_qk + a.h_v, C = heads * kConvD;

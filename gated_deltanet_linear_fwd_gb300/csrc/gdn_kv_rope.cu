@@ -50,8 +50,9 @@ __device__ __forceinline__ Angles further(const Angles& a, const float4& c, cons
   Angles r;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    r.c[i] = fma2(mul2(a.s[i], f2(-1.f)), ss[i], mul2(a.c[i], cc[i]));
+    r.c[i] = fma2(a.minus_s[i], ss[i], mul2(a.c[i], cc[i]));
     r.s[i] = fma2(a.c[i], ss[i], mul2(a.s[i], cc[i]));
+    r.minus_s[i] = mul2(r.s[i], f2(-1.f));
   }
   return r;
 }
@@ -93,8 +94,10 @@ __device__ __forceinline__ void append_turned_page(const KvRopeArgs& a, const En
     unpack_row(raw[i], y[i]);  // zeros where the row is not new
     if (kTasks * i >= hi || kTasks * (i + 1) <= lo) continue;
     if (norm) {
-      float unit;
-      scale_row(y[i], head_scale(y[i], a.q.r.inv_n, a.q.r.eps, unit));
+      const float ss = half_sum(dot_row(y[i], y[i]));
+      float n = rsqrt_approx(fmaf(ss, a.q.r.inv_n, a.q.r.eps)), unit;
+      if (large_heads(ss)) n = scaled_head(y[i], ss, a.q.r.inv_n, a.q.r.eps, unit);
+      scale_row(y[i], n);
       if (a.k_weight) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], w[e]);
@@ -104,7 +107,7 @@ __device__ __forceinline__ void append_turned_page(const KvRopeArgs& a, const En
     if (i > 0 && l.turned)
       here = further(angle, *reinterpret_cast<const float4*>(&sh.c[max(i - 1, 0)][4 * lane]),
                      *reinterpret_cast<const float4*>(&sh.s[max(i - 1, 0)][4 * lane]));
-    turn_row<kInterleaved>(l, here, y[i]);
+    turn_row<kInterleaved>(a.q.r.rot == kRopeD, l, here, y[i]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 p = parts(y[i][e]);
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_rope_
   unsigned b = blockIdx.x;
   const unsigned pages = a.entries * (unsigned)a.p.c.h_kv;  // the grid, 2 pages and more, is below 2^31
   if (b >= 2 * pages) {
-    const unsigned task = (b - 2 * pages) * kRopeWarps + (tid >> 5);
+    const unsigned task = (b - 2 * pages) * kRopeWarps + warp_index();
     if ((task >> a.q.shares_log2) * 2 < (unsigned)a.q.pos.T) turn_tokens<T, kInterleaved>(a.q, task);
     return;
   }

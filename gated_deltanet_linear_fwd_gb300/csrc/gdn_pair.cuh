@@ -71,4 +71,20 @@ __device__ __forceinline__ uint32_t pair_bf16(F2 x) {
   return r;
 }
 
+// The thread's warp in its block, in a way that the compiler sees is the same for
+// all lanes: what follows from it alone is then done once a warp.
+__device__ __forceinline__ unsigned warp_index() { return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0); }
+
+// ---- 16 bytes a lane into shared memory, asynchronously, in groups ----
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+               "l"(reinterpret_cast<uint64_t>(from))
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLater>
+__device__ __forceinline__ void copy_wait() {  // all groups but the last kLater are there
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLater) : "memory");
+}
+
 }  // namespace gdn

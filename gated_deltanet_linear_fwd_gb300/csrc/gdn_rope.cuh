@@ -121,7 +121,7 @@ __device__ __forceinline__ RopeFreq rope_freq(const RopeArgs& r, const RopeLane&
   return q;
 }
 struct Angles {
-  F2 c[2], s[2];
+  F2 c[2], s[2], minus_s[2];
 };
 __device__ __forceinline__ Angles rope_angles(const RopeArgs& r, const RopeLane& l, const RopeFreq& q, int pos) {
   Angles a;
@@ -132,16 +132,15 @@ __device__ __forceinline__ Angles rope_angles(const RopeArgs& r, const RopeLane&
                  (uint32_t)(((uint64_t)(int64_t)pos * q.f[2 * i + 1]) >> 32), a.c[i], a.s[i]);
     a.c[i] = mul2(a.c[i], m);
     a.s[i] = mul2(a.s[i], m);
+    a.minus_s[i] = mul2(a.s[i], f2(-1.f));
   }
   return a;
 }
 
 // A lane's 8 elements are four pairs of fp32: x[0], x[1] the first chunk, x[2],
-// x[3] the second.  Rotates them, kBack by the transposed rotation.  (A lane
-// that does not turn leaves what it has, infinities too.)
-template <bool kInterleaved, bool kBack = false>
-__device__ __forceinline__ void turn_row(const RopeLane& l, const Angles& a, F2 (&x)[4]) {
-  if (!l.turned) return;
+// x[3] the second.  Rotates them, kBack by the transposed rotation.
+template <bool kInterleaved, bool kBack>
+__device__ __forceinline__ void turn_lane(const Angles& a, F2 (&x)[4]) {
   if (kInterleaved) {  // the partners are the neighbours
     const float2 c0 = parts(a.c[0]), c1 = parts(a.c[1]), s0 = parts(a.s[0]), s1 = parts(a.s[1]);
     const float c[4] = {c0.x, c0.y, c1.x, c1.y}, s[4] = {s0.x, s0.y, s1.x, s1.y};
@@ -151,12 +150,18 @@ __device__ __forceinline__ void turn_row(const RopeLane& l, const Angles& a, F2 
   } else {  // the other chunk
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const F2 down = mul2(a.s[i], f2(-1.f)), up = a.s[i];
-      const F2 y = fma2(x[i + 2], kBack ? up : down, mul2(x[i], a.c[i]));
-      x[i + 2] = fma2(x[i], kBack ? down : up, mul2(x[i + 2], a.c[i]));
+      const F2 y = fma2(x[i + 2], kBack ? a.s[i] : a.minus_s[i], mul2(x[i], a.c[i]));
+      x[i + 2] = fma2(x[i], kBack ? a.minus_s[i] : a.s[i], mul2(x[i + 2], a.c[i]));
       x[i] = y;
     }
   }
+}
+// A lane that does not turn leaves what it has, infinities too.  `all`: every one
+// turns, the same for the whole grid, so that most calls branch without dividing.
+template <bool kInterleaved, bool kBack = false>
+__device__ __forceinline__ void turn_row(bool all, const RopeLane& l, const Angles& a, F2 (&x)[4]) {
+  if (all) turn_lane<kInterleaved, kBack>(a, x);
+  else if (l.turned) turn_lane<kInterleaved, kBack>(a, x);
 }
 
 // ---- a lane's 8 elements in memory ----
@@ -221,20 +226,18 @@ __device__ __forceinline__ void scale_row(F2 (&x)[4], float f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], f2(f));
 }
-// 1 / sqrt(inv_n ss + eps), ss the head's sum of squares.  Past fp32's range
-// (elements of 2^60 and more) x is scaled by `unit` = 2^-68, beside which eps
-// is nothing, and the result belongs to the scaled x.
-__device__ __forceinline__ float head_scale(F2 (&x)[4], float inv_n, float eps, float& unit) {
-  float ss = half_sum(dot_row(x, x));
-  unit = 1.f;
-  if (__any_sync(0xffffffffu, !(ss <= 3e38f))) {
-    const bool large = !(ss <= 3e38f);
-    unit = large ? 0x1p-68f : 1.f;
-    scale_row(x, unit);
-    ss = half_sum(dot_row(x, x));
-    if (large) eps = 0.f;
-  }
-  return rsqrt_approx(fmaf(ss, inv_n, eps));
+// A head's sum of squares, and whether it passes fp32's range in either half
+// (elements of 2^60 and more): then scaled_head takes it again of x 2^-68, which x
+// becomes and its 1 / sqrt(inv_n ss) belongs to; eps is nothing beside it.
+constexpr float kHeadUnit = 0x1p-68f;
+__device__ __forceinline__ bool large_heads(float ss) { return __any_sync(0xffffffffu, !(ss <= 3e38f)); }
+// Also whether this half's is the large one: unit is then kHeadUnit, else 1.
+__device__ __forceinline__ float scaled_head(F2 (&x)[4], float ss, float inv_n, float eps, float& unit) {
+  const bool large = !(ss <= 3e38f);
+  unit = large ? kHeadUnit : 1.f;
+  scale_row(x, unit);
+  ss = half_sum(dot_row(x, x));
+  return rsqrt_approx(fmaf(ss, inv_n, large ? 0.f : eps));
 }
 
 // The lane's part of a weight, or ones.
@@ -271,8 +274,6 @@ struct RopeSide {
   float* d_weight;         // backward
   int64_t in_stride, out_stride, dx_stride;
   int heads;
-  int shares_log2, share;  // backward: 2^shares_log2 warps have two tokens' heads, `share` each
-  int ctas;                // backward
 };
 
 // Arguments of gdn_qk_rope and its gradient, and the queries' of gdn_kv_append_rope.
@@ -280,8 +281,9 @@ struct QkRopeArgs {
   RopeArgs r;
   PosArgs pos;
   RopeSide side[2];        // q, then k
-  int shares_log2, share;  // forward: 2^shares_log2 warps have two tokens' heads of both, `share` each
-  float* part;             // backward: [CTAs, 128] sums of the weights' gradients, or null
+  int shares_log2, share;  // forward: 2^shares_log2 warps have two tokens' heads, `share` each
+  int ctas;                // backward
+  float* part;             // backward: [CTAs, 2, 128] sums of the weights' gradients, or null
 };
 
 // A warp's task: heads [h0, h1) of q and [k0, k1) of k of its half's token.
@@ -322,7 +324,7 @@ template <typename T, bool kInterleaved>
 __device__ __forceinline__ void turn_side(const RopeArgs& r, const float* weight, const RopeLane& l, const Angles& angle, bool in,
                                           typename RowOf<T>::type (&raw)[kRopeBatch<T>], const char* x0, char* y0, int n) {
   constexpr int kBatch = kRopeBatch<T>, kStep = kRopeD * sizeof(T);
-  const bool norm = r.norm != kNormNone;
+  const bool norm = r.norm != kNormNone, all = r.rot == kRopeD;
   const float inv_n = r.inv_n, eps = r.eps;
   const int gap = (l.o1 - l.o0) * (int)sizeof(T);
   F2 w[4];
@@ -335,12 +337,14 @@ __device__ __forceinline__ void turn_side(const RopeArgs& r, const float* weight
       F2 x[4];
       unpack_row(raw[i], x);
       if (norm) {
-        float unit;
-        scale_row(x, head_scale(x, inv_n, eps, unit));
+        const float ss = half_sum(dot_row(x, x));
+        float f = rsqrt_approx(fmaf(ss, inv_n, eps)), unit;
+        if (large_heads(ss)) f = scaled_head(x, ss, inv_n, eps, unit);
+        scale_row(x, f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], w[e]);
       }
-      turn_row<kInterleaved>(l, angle, x);
+      turn_row<kInterleaved>(all, l, angle, x);
       if (in) store_row<T>(y0 + i * kStep, y1 + i * kStep, x);
     }
     n -= kBatch;

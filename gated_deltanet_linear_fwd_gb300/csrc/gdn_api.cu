@@ -412,15 +412,15 @@ gdn_status rope_args(const gdn_rope* rope, int norm, float eps, RopeArgs* r) {
   return norm_eps(eps, &r->eps);
 }
 
-// Warps that have two tokens' heads, 2^log2 with `share` heads each: one, whose
-// cosines then serve all of them, unless the tokens are too few to fill the GPU.
-void rope_shares(int64_t T, int heads, int* log2, int* share) {
-  constexpr int64_t kFill = 152 * 24;  // warps that are resident
-  *log2 = 0;
-  while ((1 << *log2) < heads && ((T + 1) / 2 << *log2) < kFill) ++*log2;
-  *share = (heads + (1 << *log2) - 1) >> *log2;
+// CTAs whose warps share the heads of a call: `most`, but a head of two tokens
+// for a warp at least.  A warp's heads are counted in 32 bits.
+gdn_status rope_ctas(int64_t most, QkRopeArgs* a) {
+  const int64_t units = ((int64_t)a->pos.T + 1) / 2 * (a->side[0].heads + a->side[1].heads);
+  a->ctas = (int)std::max<int64_t>(1, std::min((units + kRopeWarps - 1) / kRopeWarps, most));
+  return units / a->ctas / kRopeWarps >= INT_MAX - 1 ? GDN_ERR_INVALID_ARG : GDN_OK;
 }
-constexpr int kRopeBwdCtas = 2 * 152;  // of a gradient: what is resident, and rows of its workspace
+constexpr int kRopeCtas = 4 * 152;     // what is resident of the forward
+constexpr int kRopeBwdCtas = 2 * 152;  // and of the gradient; rows of its workspace
 
 // Checks of gdn_qk_rope and its gradient that do not need the tensors.
 gdn_status qk_rope_args(const gdn_rope_dims* d, const gdn_rope* rope, const float* q_weight, const float* k_weight,
@@ -448,7 +448,6 @@ gdn_status qk_rope_args(const gdn_rope_dims* d, const gdn_rope* rope, const floa
   k.weight = k_weight;
   q.heads = d->h_q;
   k.heads = d->h_k;
-  rope_shares(d->T, d->h_q + d->h_k, &a->shares_log2, &a->share);
   return GDN_OK;
 }
 
@@ -1241,6 +1240,7 @@ gdn_status gdn_qk_rope(const void* q, const void* k, const float* q_weight, cons
   a.side[1].in = k;
   a.side[0].out = q_out;
   a.side[1].out = k_out;
+  if ((st = rope_ctas(kRopeCtas, &a)) != GDN_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   LaunchLog log;
   cudaError_t e = log.before(cs);
@@ -1287,10 +1287,7 @@ gdn_status gdn_qk_rope_bwd(const void* q, const void* k, const float* q_weight, 
   a.side[0].d_weight = dq_weight;
   a.side[1].d_weight = dk_weight;
   a.part = sums ? static_cast<float*>(workspace) : nullptr;
-  // a head of two tokens for a warp, at least
-  const int64_t units = ((int64_t)d->T + 1) / 2 * (d->h_q + d->h_k);
-  a.ctas = (int)std::min<int64_t>((units + kRopeWarps - 1) / kRopeWarps, kRopeBwdCtas);
-  if (units / a.ctas / kRopeWarps >= INT_MAX - 1) return GDN_ERR_INVALID_ARG;  // a warp's heads are counted in 32 bits
+  if ((st = rope_ctas(kRopeBwdCtas, &a)) != GDN_OK) return st;
   LaunchLog log;
   e = log.before(cs);
   if (e == cudaSuccess) e = launch_qk_rope_bwd(a, d->dtype == GDN_F32, cs);
@@ -1326,7 +1323,9 @@ gdn_status gdn_kv_append_rope(const void* k, const void* v, const float* k_weigh
     s.out = q_out;
     s.weight = q_weight;
     s.heads = d->h_q;
-    rope_shares(d->T, d->h_q, &a.q.shares_log2, &a.q.share);
+    // of the resident CTAs as many as their share of the bytes, read and written
+    const int64_t es = d->dtype == GDN_F32 ? 4 : 2, bytes_q = 2 * es * d->h_q, bytes_kv = 2 * (es + 1) * cache->h_kv;
+    if ((st = rope_ctas(kRopeCtas * bytes_q / (bytes_q + bytes_kv), &a.q)) != GDN_OK) return st;
   }
   if (d->T == 0) return GDN_OK;
   if (!k || !v) return GDN_ERR_INVALID_ARG;
@@ -1334,8 +1333,7 @@ gdn_status gdn_kv_append_rope(const void* k, const void* v, const float* k_weigh
   a.p.k = const_cast<void*>(k);
   a.p.v = const_cast<void*>(v);
   a.k_weight = k_weight;
-  if (2 * (int64_t)a.entries * cache->h_kv + (rope_tasks(a.q) + kRopeWarps) / kRopeWarps > 0x7fffffff)
-    return GDN_ERR_INVALID_ARG;  // blocks
+  if (2 * (int64_t)a.entries * cache->h_kv + a.q.ctas > 0x7fffffff) return GDN_ERR_INVALID_ARG;  // blocks
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   LaunchLog log;
   cudaError_t e = log.before(cs);

@@ -4,8 +4,8 @@
 //
 // Keys go through y = m R (x r w) (gdn_rope.cuh) in fp32 and from there into
 // the codes, without a rounding in between; pages, scales and codes are those
-// of gdn_kv.cu.  Blocks: keys of a (page slot, head) each, then values, then
-// queries, 8 warps' worth each.
+// of gdn_kv.cu.  Blocks: queries, 8 warps' runs each, then keys of a (page
+// slot, head) each, then values.
 #include "gdn_kv_page.cuh"
 #include "gdn_rope.cuh"
 
@@ -155,32 +155,34 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_rope_
   __shared__ int part[kThreads / 32];
   __shared__ Entry found;
   __shared__ uint32_t top;
-  __shared__ PageSteps sh;
+  __shared__ union {
+    PageSteps steps;
+    RopeRing ring;
+  } sh;
   const int tid = threadIdx.x;
   if (tid == 0) top = 0;
   grid_dependency_wait();
   grid_launch_dependents();
-  unsigned b = blockIdx.x;
-  const unsigned pages = a.entries * (unsigned)a.p.c.h_kv;  // the grid, 2 pages and more, is below 2^31
-  if (b >= 2 * pages) {
-    const unsigned task = (b - 2 * pages) * kRopeWarps + warp_index();
-    if ((task >> a.q.shares_log2) * 2 < (unsigned)a.q.pos.T) turn_tokens<T, kInterleaved>(a.q, task);
+  // queries first: theirs are long runs, beside which the pages' blocks come and go
+  if (blockIdx.x < (unsigned)a.q.ctas) {
+    turn_run<T, kInterleaved>(a.q, blockIdx.x, sh.ring);
     return;
   }
+  unsigned b = blockIdx.x - a.q.ctas;
+  const unsigned pages = a.entries * (unsigned)a.p.c.h_kv;  // the grid is below 2^31
   const bool values = b >= pages;
   if (values) b -= pages;
   const int h = (int)(b % (unsigned)a.p.c.h_kv);
   const Entry en = find_entry(a.p, (int)(b / (unsigned)a.p.c.h_kv), part, &found);
   if (en.seq < 0) return;
   if (values) append_page<T>(a.p, en, h, true, top);
-  else append_turned_page<T, kInterleaved>(a, en, h, top, sh);
+  else append_turned_page<T, kInterleaved>(a, en, h, top, sh.steps);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append_rope(const KvRopeArgs& a, bool f32, cudaStream_t st) {
-  const int64_t tasks = a.q.side[0].heads ? rope_tasks(a.q) : 0;
-  const dim3 grid((unsigned)(2 * (int64_t)a.entries * a.p.c.h_kv + (tasks + kRopeWarps - 1) / kRopeWarps)), block(kThreads);
+  const dim3 grid(a.q.ctas + 2 * a.entries * (unsigned)a.p.c.h_kv), block(kThreads);
   if (f32)
     return a.q.r.interleaved ? launch_kernel(append_rope_kernel<float, true>, grid, block, 0, st, true, a)
                            : launch_kernel(append_rope_kernel<float, false>, grid, block, 0, st, true, a);

@@ -16,33 +16,12 @@ namespace gdn {
 namespace {
 
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 ? 4 : 3) rope_kernel(const QkRopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const QkRopeArgs a) {
+  __shared__ RopeRing ring;
   grid_dependency_wait();
   grid_launch_dependents();
-  const unsigned task = blockIdx.x * kRopeWarps + warp_index();
-  if ((task >> a.shares_log2) * 2 < (unsigned)a.pos.T) turn_tokens<T, kInterleaved>(a, task);
+  turn_run<T, kInterleaved>(a, blockIdx.x, ring);
 }
-
-// A place in a warp's heads, which it takes two tokens at a time, one a half of
-// the warp, q's heads first: `left` more heads from head h of token pair `pair` on.
-struct Walk {
-  int pair, h, left;
-  // heads that come next and are of one side, at most `most`
-  __device__ __forceinline__ int batch(int h_q, int heads, int most) const {
-    return min(min(most, left), (h < h_q ? h_q : heads) - h);
-  }
-  // past n heads; true at the beginning of a side
-  __device__ __forceinline__ bool step(int n, int h_q, int heads) {
-    left -= n;
-    h += n;
-    if (h == heads) {
-      h = 0;
-      ++pair;
-      return true;
-    }
-    return h == h_q;
-  }
-};
 
 // The gradient of a row, in g, from it and the input x; dw: of the weight.
 template <bool kInterleaved>
@@ -69,11 +48,7 @@ __device__ __forceinline__ void row_back(const QkRopeArgs& a, const RopeLane& l,
   for (int e = 0; e < 4; ++e) g[e] = mul2(fma2(x[e], m, g[e]), f2(back));
 }
 
-// The heads of all tokens are cut into equal runs, one a warp, so that all end
-// together and the weights' gradients are summed in registers.  A warp's next
-// rows are copied into a ring of shared memory of its own: loads into
-// registers were in flight only while it did nothing else (34150 tokens of 8 + 2
-// heads, bf16: 91.7 us at first, 66.6 with a token's heads by turns).
+// As turn_run, with two inputs; the weights' gradients are summed in registers.
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeArgs a) {
   constexpr int kBatch = sizeof(T) == 2 ? 2 : 1, kGroups = 2 * kRopeWarps, kRow = kRopeD * sizeof(T);
@@ -93,17 +68,13 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeA
 #pragma unroll
   for (int e = 0; e < 4; ++e) dwq[e] = dwk[e] = w[e] = f2(0.f);
   char* ring = sh.ring[warp];
-  // this warp's run
-  const int64_t units = ((int64_t)T_all + 1) / 2 * heads, warps = (int64_t)gridDim.x * kRopeWarps;
-  const int64_t me = (int64_t)blockIdx.x * kRopeWarps + warp, first = me * units / warps, last = (me + 1) * units / warps;
-  Walk now = {(int)(first / heads), (int)(first % heads), (int)(last - first)}, next = now;
+  Walk now = rope_run(a, (int64_t)blockIdx.x * kRopeWarps + warp), next = now;
   const char *x = nullptr, *g = nullptr;  // the lane's 16 bytes of the next head's rows
   auto place = [&] {
     const bool key = next.h >= h_q;
     const RopeSide& s = a.side[key];
-    const int64_t t = min(2 * next.pair + half, T_all - 1), h = next.h - (key ? h_q : 0);
-    x = reinterpret_cast<const char*>(static_cast<const T*>(s.in) + t * s.in_stride + h * kRopeD) + lane * 16;
-    g = reinterpret_cast<const char*>(static_cast<const T*>(s.out) + t * s.out_stride + h * kRopeD) + lane * 16;
+    x = head_at<T>(s.in, s.in_stride, T_all, next.pair, next.h - (key ? h_q : 0)) + lane * 16;
+    g = head_at<T>(s.out, s.out_stride, T_all, next.pair, next.h - (key ? h_q : 0)) + lane * 16;
   };
   auto copy_batch = [&](int slot) {
     if (next.left > 0) {
@@ -142,8 +113,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeA
     }
     if (new_side) {
       const RopeSide& s = a.side[key];
-      const int t = min(2 * now.pair + half, T_all - 1);
-      y = const_cast<char*>(head_at<T>(s.dx, s.dx_stride, t, now.h - (key ? h_q : 0), l));
+      y = const_cast<char*>(head_at<T>(s.dx, s.dx_stride, T_all, now.pair, now.h - (key ? h_q : 0))) + l.o0 * (int)sizeof(T);
       load_weight(s.weight, l, w);
     }
     const int n = now.batch(h_q, heads, kBatch);
@@ -218,7 +188,7 @@ __global__ void __launch_bounds__(1024) rope_weight_kernel(const QkRopeArgs a) {
 }  // namespace
 
 cudaError_t launch_qk_rope(const QkRopeArgs& a, bool f32, cudaStream_t st) {
-  const dim3 grid((unsigned)((rope_tasks(a) + kRopeWarps - 1) / kRopeWarps)), block(kRopeThreads);
+  const dim3 grid(a.ctas), block(kRopeThreads);
   if (f32)
     return a.r.interleaved ? launch_kernel(rope_kernel<float, true>, grid, block, 0, st, true, a)
                            : launch_kernel(rope_kernel<float, false>, grid, block, 0, st, true, a);

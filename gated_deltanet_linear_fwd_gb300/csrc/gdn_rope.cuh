@@ -254,16 +254,15 @@ __device__ __forceinline__ void load_weight(const float* w, const RopeLane& l, F
   }
 }
 
-// ---- the heads of a token ----
-// A warp takes two tokens, one a half, and their heads, or a share of them, one
-// after another, with the cosines and sines in registers.  Heads are at constant
-// distances from the first: with an address each, a table of cosines in shared
-// memory, and a token's heads cut differently in the halves, 220 instructions
-// went into a row of two heads and 34 to 70 us into 32768 tokens of 8 + 2 heads.
+// ---- runs of heads ----
+// The heads of all tokens are cut into equal runs, one a warp, so that all end
+// together.  A warp takes two tokens at a time, one a half, and their heads one
+// after another, with the cosines and sines in registers, and copies the rows
+// that come next into a ring of shared memory of its own.  Heads are at constant
+// distances from one another: with an address each, or a table of cosines in
+// shared memory, 220 instructions went into a row of two heads.
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
-template <typename T>
-constexpr int kRopeBatch = sizeof(T) == 2 ? 4 : 2;  // heads whose loads are in flight together
 
 // Queries or keys.
 struct RopeSide {
@@ -281,106 +280,136 @@ struct QkRopeArgs {
   RopeArgs r;
   PosArgs pos;
   RopeSide side[2];        // q, then k
-  int shares_log2, share;  // forward: 2^shares_log2 warps have two tokens' heads, `share` each
-  int ctas;                // backward
+  int ctas;                // whose warps take a run each
   float* part;             // backward: [CTAs, 2, 128] sums of the weights' gradients, or null
 };
 
-// A warp's task: heads [h0, h1) of q and [k0, k1) of k of its half's token.
-struct RopeTask {
-  int t;                   // held within the call; in: it is in the call and in a sequence
-  bool in;
-  int h0, h1, k0, k1;
+// A place in a warp's heads, which it takes two tokens at a time, one a half of
+// the warp, q's heads first: `left` more heads from head h of token pair `pair` on.
+struct Walk {
+  int pair, h, left;
+  // heads that come next and are of one side, at most `most`
+  __device__ __forceinline__ int batch(int h_q, int heads, int most) const {
+    return min(min(most, left), (h < h_q ? h_q : heads) - h);
+  }
+  // past n heads; true at the beginning of a side
+  __device__ __forceinline__ bool step(int n, int h_q, int heads) {
+    left -= n;
+    h += n;
+    if (h == heads) {
+      h = 0;
+      ++pair;
+      return true;
+    }
+    return h == h_q;
+  }
 };
-__device__ __forceinline__ RopeTask rope_task(const QkRopeArgs& a, unsigned task) {
-  RopeTask k;
-  const int t = (int)(task >> a.shares_log2) * 2 + (int)(threadIdx.x >> 4 & 1);
-  k.in = t < a.pos.T;
-  k.t = min(t, a.pos.T - 1);
-  const int h_q = a.side[0].heads, h = (int)(task & ((1u << a.shares_log2) - 1)) * a.share;
-  const int end = min(h + a.share, h_q + a.side[1].heads);
-  k.h0 = min(h, h_q);
-  k.h1 = min(end, h_q);
-  k.k0 = max(h - h_q, 0);
-  k.k1 = max(end - h_q, 0);
-  return k;
+
+// The runs of a call: this warp's, of warp `me` of the call's.
+__device__ __forceinline__ Walk rope_run(const QkRopeArgs& a, int64_t me) {
+  const int heads = a.side[0].heads + a.side[1].heads;
+  const int64_t units = ((int64_t)a.pos.T + 1) / 2 * heads, warps = (int64_t)a.ctas * kRopeWarps;
+  const int64_t first = me * units / warps, last = (me + 1) * units / warps;
+  return {(int)(first / heads), (int)(first % heads), (int)(last - first)};
 }
 
-// A batch of heads, n of them at most, from the addresses of the first's chunks.
-template <typename T, int kBatch>
-__device__ __forceinline__ void load_batch(typename RowOf<T>::type (&raw)[kBatch], const char* x0, int gap, int n) {
-  const char* x1 = x0 + gap;
-#pragma unroll
-  for (int i = 0; i < kBatch; ++i)
-    if (i < n) raw[i] = load_row<T>(x0 + i * kRopeD * (int)sizeof(T), x1 + i * kRopeD * (int)sizeof(T));
-}
+// Address of head h of a side's tensor, for this half of the warp.
 template <typename T>
-__device__ __forceinline__ const char* head_at(const void* base, int64_t stride, int t, int h, const RopeLane& l) {
-  return reinterpret_cast<const char*>(static_cast<const T*>(base) + t * stride + h * kRopeD + l.o0);
+__device__ __forceinline__ const char* head_at(const void* base, int64_t stride, int T_all, int pair, int h) {
+  const int64_t t = min(2 * pair + (int)(threadIdx.x >> 4 & 1), T_all - 1);
+  return reinterpret_cast<const char*>(static_cast<const T*>(base) + t * stride + (int64_t)h * kRopeD);
 }
 
-// n heads from address x0 on; raw holds the first batch.
+// 4 KB a warp: two stages of four heads (fp32: two) of two tokens.
+struct RopeRing {
+  alignas(16) char bytes[kRopeWarps][4096];
+};
+
+// One warp's run: in -> out.
 template <typename T, bool kInterleaved>
-__device__ __forceinline__ void turn_side(const RopeArgs& r, const float* weight, const RopeLane& l, const Angles& angle, bool in,
-                                          typename RowOf<T>::type (&raw)[kRopeBatch<T>], const char* x0, char* y0, int n) {
-  constexpr int kBatch = kRopeBatch<T>, kStep = kRopeD * sizeof(T);
-  const bool norm = r.norm != kNormNone, all = r.rot == kRopeD;
-  const float inv_n = r.inv_n, eps = r.eps;
-  const int gap = (l.o1 - l.o0) * (int)sizeof(T);
+__device__ __forceinline__ void turn_run(const QkRopeArgs& a, unsigned block, RopeRing& rings) {
+  constexpr int kRow = kRopeD * sizeof(T), kStages = 2, kStage = 4096 / kStages, kBatch = kStage / (2 * kRow);
+  const int lane = threadIdx.x & 15, half = threadIdx.x >> 4 & 1;
+  const RopeLane l = rope_lane(a.r, lane);
+  const bool norm = a.r.norm != kNormNone, all = a.r.rot == kRopeD;
+  const int T_all = a.pos.T, h_q = a.side[0].heads, heads = h_q + a.side[1].heads, gap = (l.o1 - l.o0) * (int)sizeof(T);
+  const unsigned warp = warp_index();
+  char* ring = rings.bytes[warp];
+  Walk now = rope_run(a, (int64_t)block * kRopeWarps + warp), next = now;
+  const char* x = nullptr;  // the lane's 16 bytes of the next head's row
+  auto place = [&] {
+    const bool key = next.h >= h_q;
+    const RopeSide& s = a.side[key];
+    x = head_at<T>(s.in, s.in_stride, T_all, next.pair, next.h - (key ? h_q : 0)) + lane * 16;
+  };
+  auto copy_batch = [&](int slot) {
+    if (next.left > 0) {
+      const int n = next.batch(h_q, heads, kBatch);
+      char* to = ring + slot * kStage + half * kRow + lane * 16;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (i < n) {
+#pragma unroll
+          for (int j = 0; j < kRow; j += 256) copy16(to + i * 2 * kRow + j, x + i * kRow + j);
+        }
+      x += n * kRow;
+      if (next.step(n, h_q, heads)) place();
+    }
+    copy_commit();
+  };
+  place();
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) copy_batch(i);
+  int slot = 0;
+  bool in = false, new_pair = true, new_side = true;
+  Angles angle;
   F2 w[4];
-  load_weight(weight, l, w);
-  while (true) {
-    char* y1 = y0 + gap;
+  char* y = nullptr;
+  while (now.left > 0) {
+    if (new_pair) {
+      const int t2 = 2 * now.pair + half, t = min(t2, T_all - 1);
+      int pos = 0;
+      in = token_position(a.pos, t, pos) && t == t2;
+      angle = rope_angles(a.r, l, rope_freq(a.r, l, lane), pos);
+    }
+    if (new_side) {
+      const bool key = now.h >= h_q;
+      const RopeSide& s = a.side[key];
+      y = const_cast<char*>(head_at<T>(s.out, s.out_stride, T_all, now.pair, now.h - (key ? h_q : 0))) + l.o0 * (int)sizeof(T);
+      load_weight(s.weight, l, w);
+    }
+    const int n = now.batch(h_q, heads, kBatch);
+    copy_wait<kStages - 1>();
+    __syncwarp();
+    const char* from = ring + slot * kStage + half * kRow + l.o0 * (int)sizeof(T);
+    typename RowOf<T>::type raw[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) raw[i] = load_row<T>(from + i * 2 * kRow, from + i * 2 * kRow + gap);
+    __syncwarp();
+    copy_batch(slot);
+    slot = slot + 1 == kStages ? 0 : slot + 1;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if (i >= n) break;
-      F2 x[4];
-      unpack_row(raw[i], x);
+      F2 row[4];
+      unpack_row(raw[i], row);
       if (norm) {
-        const float ss = half_sum(dot_row(x, x));
-        float f = rsqrt_approx(fmaf(ss, inv_n, eps)), unit;
-        if (large_heads(ss)) f = scaled_head(x, ss, inv_n, eps, unit);
-        scale_row(x, f);
+        const float ss = half_sum(dot_row(row, row));
+        float f = rsqrt_approx(fmaf(ss, a.r.inv_n, a.r.eps)), unit;
+        if (large_heads(ss)) f = scaled_head(row, ss, a.r.inv_n, a.r.eps, unit);
+        scale_row(row, f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], w[e]);
+        for (int e = 0; e < 4; ++e) row[e] = mul2(row[e], w[e]);
       }
-      turn_row<kInterleaved>(all, l, angle, x);
-      if (in) store_row<T>(y0 + i * kStep, y1 + i * kStep, x);
+      turn_row<kInterleaved>(all, l, angle, row);
+      if (in) store_row<T>(y + i * kRow, y + i * kRow + gap, row);
     }
-    n -= kBatch;
-    if (n <= 0) break;
-    x0 += kBatch * kStep;
-    y0 += kBatch * kStep;
-    load_batch<T, kBatch>(raw, x0, gap, n);
+    y += n * kRow;
+    new_side = now.step(n, h_q, heads);
+    new_pair = now.h == 0;
   }
+  copy_wait<0>();
 }
-
-template <typename T, bool kInterleaved>
-__device__ __forceinline__ void turn_tokens(const QkRopeArgs& a, unsigned task) {
-  const int lane = threadIdx.x & 15;
-  const RopeLane l = rope_lane(a.r, lane);
-  const RopeTask k = rope_task(a, task);
-  const int gap = (l.o1 - l.o0) * (int)sizeof(T), n_q = k.h1 - k.h0, n_k = k.k1 - k.k0;
-  const char* q = head_at<T>(a.side[0].in, a.side[0].in_stride, k.t, k.h0, l);
-  const char* kk = head_at<T>(a.side[1].in, a.side[1].in_stride, k.t, k.k0, l);
-  typename RowOf<T>::type raw[kRopeBatch<T>];
-  load_batch<T, kRopeBatch<T>>(raw, n_q > 0 ? q : kk, gap, n_q > 0 ? n_q : n_k);
-  int pos = 0;
-  const bool in = token_position(a.pos, k.t, pos) && k.in;
-  const Angles angle = rope_angles(a.r, l, rope_freq(a.r, l, lane), pos);
-  if (n_q > 0) {
-    char* out = const_cast<char*>(head_at<T>(a.side[0].out, a.side[0].out_stride, k.t, k.h0, l));
-    turn_side<T, kInterleaved>(a.r, a.side[0].weight, l, angle, in, raw, q, out, n_q);
-    if (n_k <= 0) return;
-    load_batch<T, kRopeBatch<T>>(raw, kk, gap, n_k);
-  }
-  if (n_k > 0) {
-    char* out = const_cast<char*>(head_at<T>(a.side[1].out, a.side[1].out_stride, k.t, k.k0, l));
-    turn_side<T, kInterleaved>(a.r, a.side[1].weight, l, angle, in, raw, kk, out, n_k);
-  }
-}
-// Warps of a call, below 2^31.
-inline int64_t rope_tasks(const QkRopeArgs& a) { return (((int64_t)a.pos.T + 1) / 2) << a.shares_log2; }
 
 cudaError_t launch_qk_rope(const QkRopeArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_qk_rope_bwd(const QkRopeArgs& a, bool f32, cudaStream_t st);

@@ -543,6 +543,13 @@ def _tokens(name: str, t: torch.Tensor, inner: int, like: torch.Tensor) -> int:
     return step
 
 
+def _empty_like(t: torch.Tensor, stream) -> torch.Tensor:
+    """As _kv_empty, packed, of t's shape, type and device."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _kv_empty(t.shape, t.dtype, t.device, stream)
+
+
 def _place(name: str, t: torch.Tensor, shape, inner: int, like: torch.Tensor, dtype: torch.dtype, device: int):
     """(address, token stride) of t, of like's type and device and of that shape."""
     if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
@@ -636,11 +643,11 @@ def gdn_qk_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: Opti
     qos = kos = 0
     if q is not None:
         if q_out is None:
-            q_out = _kv_empty(q_shape, dtype, q.device, stream)
+            q_out = _empty_like(q, stream)
         qo, qos = _place("q_out", q_out, q_shape, 2, x, dtype, dev)
     if k is not None:
         if k_out is None:
-            k_out = _kv_empty(k_shape, dtype, k.device, stream)
+            k_out = _empty_like(k, stream)
         ko, kos = _place("k_out", k_out, k_shape, 2, x, dtype, dev)
     st = L.load().gdn_qk_rope(qp, kp, _f32("q_weight", q_weight, (128,), dev), _f32("k_weight", k_weight, (128,), dev),
                               _i32("positions", positions, T, dev), cu, _rope_raw(rope, dev), qo, ko,
@@ -679,16 +686,16 @@ def gdn_qk_rope_bwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor], d_q_ou
     if q is not None:
         gq, gqs = _place("d_q_out", d_q_out, q_shape, 2, x, dtype, dev)
         if d_q is None:
-            d_q = _kv_empty(q_shape, dtype, q.device, stream)
+            d_q = _empty_like(q, stream)
         dqp, dqs = _place("d_q", d_q, q_shape, 2, x, dtype, dev)
     if k is not None:
         gk, gks = _place("d_k_out", d_k_out, k_shape, 2, x, dtype, dev)
         if d_k is None:
-            d_k = _kv_empty(k_shape, dtype, k.device, stream)
+            d_k = _empty_like(k, stream)
         dkp, dks = _place("d_k", d_k, k_shape, 2, x, dtype, dev)
     qw, kw = _f32("q_weight", q_weight, (128,), dev), _f32("k_weight", k_weight, (128,), dev)
-    dqw = None if qw is None else _kv_empty((128,), torch.float32, x.device, stream)
-    dkw = None if kw is None else _kv_empty((128,), torch.float32, x.device, stream)
+    dqw = None if qw is None else _empty_like(q_weight, stream)
+    dkw = None if kw is None else _empty_like(k_weight, stream)
     if workspace is None and (dqw is not None or dkw is not None):
         workspace = _kv_empty(gdn_qk_rope_bwd_workspace_bytes(), torch.uint8, x.device, stream)
     st = L.load().gdn_qk_rope_bwd(qp, kp, qw, kw, _i32("positions", positions, T, dev), cu, _rope_raw(rope, dev), gq, gk, dqp, dkp,
@@ -731,7 +738,7 @@ def gdn_kv_append_rope(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_lens
     if q is not None:
         qp, qs, h_q, q_shape = _heads("q", q, k, dtype, dev)
         if q_out is None:
-            q_out = _kv_empty(q_shape, dtype, q.device, stream)
+            q_out = _empty_like(q, stream)
         qo, qos = _place("q_out", q_out, q_shape, 2, k, dtype, dev)
     elif q_out is not None:
         raise ValueError("q_out goes with q")
@@ -743,42 +750,35 @@ def gdn_kv_append_rope(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_lens
     return q_out
 
 
-class _Conv:
-    """What the calls of a convolution share: x's shape, type, device and stream,
-    the addresses of weight, bias and offsets, and the dims' values."""
-    __slots__ = ("x", "lead", "C", "h_v", "n", "T", "W", "dtype", "device", "handle", "weight", "bias", "cu", "stream", "how", "stride")
+def _conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps, stream):
+    """What the calls of a convolution share: (dimensions before the channels,
+    channels, value heads, sequences, tokens, taps, type, device, stream handle,
+    addresses of weight, bias and offsets, the dims' values after the first two)."""
+    shape = x.shape
+    if len(shape) not in (2, 3):
+        raise ValueError("x must be [T, C] or [B, T, C]")
+    lead, C = shape[:-1], shape[-1]
+    h_v = C // 128 - 2 * h_qk
+    if C % 128 or h_qk < 1 or h_v < 1:
+        raise ValueError("x must have (2 h_qk + h_v) * 128 channels")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [C, W]")
+    W = weight.shape[1]
+    dtype, device, handle = _call(x, stream)
+    n, T, cu = _sequences(lead, cu_seqlens, device)
+    how = (h_qk, h_v, W, _choice("activation", _ACTIVATIONS, activation), 1 if norm else 0, eps, _DT.get(dtype, -1),
+           0 if x.is_contiguous() else _tokens("x", x, 1, x))
+    return (lead, C, h_v, n, T, W, dtype, device, handle, _f32("weight", weight, (C, W), device), _f32("bias", bias, (C,), device), cu,
+            how)
 
-    def __init__(self, x, weight, h_qk, bias, cu_seqlens, activation, norm, eps, stream):
-        shape = x.shape
-        if len(shape) not in (2, 3):
-            raise ValueError("x must be [T, C] or [B, T, C]")
-        self.x, self.lead, self.C, self.stream = x, shape[:-1], shape[-1], stream
-        self.h_v = self.C // 128 - 2 * h_qk
-        if self.C % 128 or h_qk < 1 or self.h_v < 1:
-            raise ValueError("x must have (2 h_qk + h_v) * 128 channels")
-        if weight.dim() != 2:
-            raise ValueError("weight must be [C, W]")
-        self.dtype, self.device, self.handle = _call(x, stream)
-        self.n, self.T, self.cu = _sequences(self.lead, cu_seqlens, self.device)
-        self.W = weight.size(1)
-        self.weight = _f32("weight", weight, (self.C, self.W), self.device)
-        self.bias = _f32("bias", bias, (self.C,), self.device)
-        self.stride = 0 if x.is_contiguous() else _tokens("x", x, 1, x)
-        self.how = (h_qk, self.h_v, self.W, _choice("activation", _ACTIVATIONS, activation), 1 if norm else 0, eps,
-                    _DT.get(self.dtype, -1), self.stride)
 
-    def dims(self, dx_stride: int = 0, n: Optional[int] = None) -> L.gdn_conv_dims:
-        return L.conv_dims(self.n if n is None else n, self.T, *self.how, dx_stride)
-
-    def like(self, name: str, t: Optional[torch.Tensor], shape, make: bool = True):
-        """(t, address), checked to be contiguous, of that shape and of x's type and device; a new one for None if `make`."""
-        if t is None:
-            if not make:
-                return None, None
-            t = _kv_empty(shape, self.dtype, self.x.device, self.stream)
-        elif t.dtype is not self.dtype or t.get_device() != self.device or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous {list(shape)}, of x's type, on its device")
-        return t, t.data_ptr()
+def _packed(name: str, t: Optional[torch.Tensor], shape, dtype: torch.dtype, device: int):
+    """Address of t, checked to be contiguous, of that shape, type and device; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)}, of x's type, on its device")
+    return t.data_ptr()
 
 
 def gdn_conv_fwd(x: torch.Tensor, weight: torch.Tensor, h_qk: int, bias: Optional[torch.Tensor] = None,
@@ -792,14 +792,20 @@ def gdn_conv_fwd(x: torch.Tensor, weight: torch.Tensor, h_qk: int, bias: Optiona
     initial_state [N, W - 1, C] like x, or None.  norm: q's and k's heads to unit
     length.  Returns (q, k, v, final_state or None), q, k, v as gdn_chunk_fwd
     takes them, without a history (gdn_conv_bwd)."""
-    c = _Conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps, stream)
-    states, heads = (c.n, c.W - 1, c.C), (*c.lead, h_qk, 128)
-    q, qp = c.like("q", q, heads)
-    k, kp = c.like("k", k, heads)
-    v, vp = c.like("v", v, (*c.lead, c.h_v, 128))
-    _, before = c.like("initial_state", initial_state, states, False)
-    final_state, after = c.like("final_state", final_state, states, output_final_state)
-    st = L.load().gdn_conv_fwd(x.data_ptr(), c.weight, c.bias, before, c.cu, qp, kp, vp, after, c.dims(), c.handle)
+    lead, C, h_v, n, T, W, dtype, dev, handle, w, b, cu, how = _conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps, stream)
+    states, heads, v_heads = (n, W - 1, C), (*lead, h_qk, 128), (*lead, h_v, 128)
+    if q is None:
+        q = _kv_empty(heads, dtype, x.device, stream)
+    if k is None:
+        k = _kv_empty(heads, dtype, x.device, stream)
+    if v is None:
+        v = _kv_empty(v_heads, dtype, x.device, stream)
+    if final_state is None and output_final_state:
+        final_state = _kv_empty(states, dtype, x.device, stream)
+    st = L.load().gdn_conv_fwd(x.data_ptr(), w, b, _packed("initial_state", initial_state, states, dtype, dev), cu,
+                               _packed("q", q, heads, dtype, dev), _packed("k", k, heads, dtype, dev),
+                               _packed("v", v, v_heads, dtype, dev), _packed("final_state", final_state, states, dtype, dev),
+                               L.conv_dims(n, T, *how, 0), handle)
     L.check(st, "gdn_conv_fwd")
     return q, k, v, final_state
 
@@ -822,28 +828,26 @@ def gdn_conv_bwd(x: torch.Tensor, weight: torch.Tensor, h_qk: int, d_q: torch.Te
     d_v and d_final_state (None: zero) like its outputs.  Returns (dx, d_weight,
     d_bias or None, d_initial_state or None): the bias's without a bias and, unless
     want_initial_state_grad says so, the state's without a state are None."""
-    c = _Conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps, stream)
-    states, heads = (c.n, c.W - 1, c.C), (*c.lead, h_qk, 128)
-    _, gq = c.like("d_q", d_q, heads, False)
-    _, gk = c.like("d_k", d_k, heads, False)
-    _, gv = c.like("d_v", d_v, (*c.lead, c.h_v, 128), False)
-    _, before = c.like("initial_state", initial_state, states, False)
-    _, after = c.like("d_final_state", d_final_state, states, False)
-    device = x.device
+    lead, C, h_v, n, T, W, dtype, dev, handle, w, b, cu, how = _conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps, stream)
+    states, heads = (n, W - 1, C), (*lead, h_qk, 128)
+    gq, gk = _packed("d_q", d_q, heads, dtype, dev), _packed("d_k", d_k, heads, dtype, dev)
+    gv = _packed("d_v", d_v, (*lead, h_v, 128), dtype, dev)
+    before, after = _packed("initial_state", initial_state, states, dtype, dev), _packed("d_final_state", d_final_state, states, dtype, dev)
     if dx is None:
-        dx = _kv_empty(x.shape, c.dtype, device, stream)
-    dxp, dx_stride = _place("dx", dx, x.shape, 1, x, c.dtype, c.device)
-    want = initial_state is not None if want_initial_state_grad is None else want_initial_state_grad
-    d_state = _kv_empty(states, c.dtype, device, stream) if want else None
-    d_weight = _kv_empty((c.C, c.W), torch.float32, device, stream)
-    d_bias = None if bias is None else _kv_empty((c.C,), torch.float32, device, stream)
-    lib, dims = L.load(), c.dims(dx_stride)
+        dx = _empty_like(x, stream)
+    dxp, dx_stride = _place("dx", dx, x.shape, 1, x, dtype, dev)
+    d_state = None
+    if initial_state is not None if want_initial_state_grad is None else want_initial_state_grad:
+        d_state = _kv_empty(states, dtype, x.device, stream) if initial_state is None else _empty_like(initial_state, stream)
+    d_weight = _empty_like(weight, stream)
+    d_bias = None if bias is None else _empty_like(bias, stream)
+    lib, dims = L.load(), L.conv_dims(n, T, *how, dx_stride)
     if workspace is None:
-        n = ctypes.c_size_t(0)
-        L.check(lib.gdn_conv_bwd_workspace_bytes(dims, n), "gdn_conv_bwd_workspace_bytes")
-        workspace = _kv_empty(max(256, int(n.value)), torch.uint8, device, stream)
-    st = lib.gdn_conv_bwd(x.data_ptr(), c.weight, c.bias, before, c.cu, gq, gk, gv, after, dxp, d_weight.data_ptr(), _at(d_bias),
-                          _at(d_state), dims, *_workspace(workspace, c.device), c.handle)
+        size = ctypes.c_size_t(0)
+        L.check(lib.gdn_conv_bwd_workspace_bytes(dims, size), "gdn_conv_bwd_workspace_bytes")
+        workspace = _kv_empty(max(256, int(size.value)), torch.uint8, x.device, stream)
+    st = lib.gdn_conv_bwd(x.data_ptr(), w, b, before, cu, gq, gk, gv, after, dxp, d_weight.data_ptr(), _at(d_bias), _at(d_state), dims,
+                          *_workspace(workspace, dev), handle)
     L.check(st, "gdn_conv_bwd")
     return dx, d_weight, d_bias, d_state
 
@@ -856,14 +860,18 @@ def gdn_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, h_
     128], as gdn_decode_step takes them."""
     if x.dim() != 2:
         raise ValueError("x must be [N, C]")
-    c = _Conv(x, weight, h_qk, bias, None, activation, norm, eps, stream)
-    heads = (c.T, h_qk, 128)
+    _, C, h_v, _, n, W, dtype, dev, handle, w, b, _, how = _conv(x, weight, h_qk, bias, None, activation, norm, eps, stream)
     if state is None:
         raise ValueError("state is needed")
-    _, sp = c.like("state", state, (c.T, c.W - 1, c.C))
-    q, qp = c.like("q", q, heads)
-    k, kp = c.like("k", k, heads)
-    v, vp = c.like("v", v, (c.T, c.h_v, 128))
-    st = L.load().gdn_conv_step(x.data_ptr(), c.weight, c.bias, sp, qp, kp, vp, c.dims(n=c.T), c.handle)
+    heads, v_heads = (n, h_qk, 128), (n, h_v, 128)
+    if q is None:
+        q = _kv_empty(heads, dtype, x.device, stream)
+    if k is None:
+        k = _kv_empty(heads, dtype, x.device, stream)
+    if v is None:
+        v = _kv_empty(v_heads, dtype, x.device, stream)
+    st = L.load().gdn_conv_step(x.data_ptr(), w, b, _packed("state", state, (n, W - 1, C), dtype, dev),
+                                _packed("q", q, heads, dtype, dev), _packed("k", k, heads, dtype, dev),
+                                _packed("v", v, v_heads, dtype, dev), L.conv_dims(n, n, *how, 0), handle)
     L.check(st, "gdn_conv_step")
     return q, k, v

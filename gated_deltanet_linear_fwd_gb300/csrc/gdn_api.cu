@@ -451,19 +451,26 @@ gdn_status qk_rope_args(const gdn_rope_dims* d, const gdn_rope* rope, const floa
   return GDN_OK;
 }
 
-// Tokens a warp takes in a row, so that the warps (`width` of them side by side
-// over the channels) are `fill`, what is resident or twice that, or a multiple: all end together.
-// More tokens read less twice, the W - 1 before each run; past 192 that is nothing.
-// A multiple of `group`, the tokens of straight code.
-int conv_run(int64_t T, int64_t width, int64_t fill, int64_t group) {
-  constexpr int64_t kLeast = 8, kMost = 192;  // both are rounded to groups
-  const int64_t waves = (T * width + fill * kMost - 1) / (fill * kMost);
-  const int64_t runs = std::max<int64_t>(1, std::max<int64_t>(waves, 1) * fill / width);
-  const int64_t run = std::min(std::max((T + runs - 1) / runs, kLeast), kMost);
-  return (int)((run + group - 1) / group * group);
+// Tokens a warp (backward: each of a CTA's) takes in a row, of heads whose norm is
+// taken and of the others, so that the warps (CTAs) are `fill`, what is resident or
+// twice that, or a multiple, and all end together: the former cost `cost` times the
+// others.  More tokens read less twice, the W - 1 before each run; past 192 that
+// is nothing.  Multiples of `group`, the tokens of straight code.
+void conv_runs(int64_t T, int64_t others, int64_t fill, double cost, int64_t group, int64_t warps, ConvArgs* a) {
+  constexpr int64_t kLeast = 8, kMost = 192;
+  const double width = a->n_unit * cost + others;
+  const double waves = std::max(1.0, std::ceil((double)T / warps * width / (double)(fill * kMost)));
+  for (int i = 0; i < 2; ++i) {
+    const int64_t runs = std::max<int64_t>(1, (int64_t)(waves * fill / width * (i ? 1.0 : cost)));
+    const int64_t run = std::min(std::max((T + runs * warps - 1) / (runs * warps), kLeast), kMost);
+    a->run[i] = (int)((run + group - 1) / group * group);
+    a->runs[i] = (int)((T + a->run[i] * warps - 1) / (a->run[i] * warps));
+  }
 }
-constexpr int64_t kConvFill = 152 * 48;        // warps: twice what is resident
-constexpr int64_t kConvBwdFill = 152 * 2;      // CTAs
+constexpr int64_t kConvFill = 152 * 48;    // warps: twice what is resident
+constexpr int64_t kConvBwdFill = 152 * 2;  // CTAs
+// Measured on 2 + 2 + 8 heads: a token of a head whose norm is taken against one of the others.
+constexpr double kConvUnitCost = 1.1, kConvBwdUnitCost = 1.5;
 
 gdn_status conv_args(const gdn_conv_dims* d, const float* weight, const float* bias, const int32_t* cu, ConvArgs* a) {
   if (!d) return GDN_ERR_INVALID_ARG;
@@ -493,6 +500,7 @@ gdn_status conv_args(const gdn_conv_dims* d, const float* weight, const float* b
   a->width = d->width;
   a->silu = d->activation == GDN_ACT_SILU;
   a->norm = d->norm;
+  a->n_unit = d->norm ? 2 * d->h_qk : 0;
   return GDN_OK;
 }
 
@@ -505,12 +513,18 @@ size_t conv_state_bytes(const gdn_conv_dims* d) {
   return (size_t)d->n_seqs * (d->width - 1) * (2 * d->h_qk + d->h_v) * kConvD * (d->dtype == GDN_F32 ? 4 : 2);
 }
 constexpr int kConvBwdWarps = 8;  // runs of a CTA of the gradient
-// Sets the run and the number of groups of the gradient; returns its workspace.
+// Sets the runs of the gradient; returns its workspace, which is enough with and
+// without the norm.
 size_t conv_bwd_plan(const gdn_conv_dims* d, ConvArgs* a) {
   const int heads = 2 * d->h_qk + d->h_v;
-  a->run = conv_run(((int64_t)d->T + kConvBwdWarps - 1) / kConvBwdWarps, heads, kConvBwdFill, 4);
-  a->groups = (int)(((int64_t)d->T + a->run * kConvBwdWarps - 1) / (a->run * kConvBwdWarps));
-  return (size_t)a->groups * (d->width + 1) * heads * kConvD * sizeof(float);
+  size_t most = 0;
+  for (int n_unit : {2 * d->h_qk - a->n_unit, a->n_unit}) {  // the call's own last
+    a->n_unit = n_unit;
+    conv_runs(d->T, heads - n_unit, kConvBwdFill, kConvBwdUnitCost, 4, kConvBwdWarps, a);
+    const size_t rows = (size_t)a->runs[0] * n_unit + (size_t)a->runs[1] * (heads - n_unit);
+    most = std::max(most, rows * (d->width + 1) * kConvD * sizeof(float));
+  }
+  return most;
 }
 
 // A pool of codes as [page and head][64 tokens][128 bytes]: boxes of one page's
@@ -1357,7 +1371,7 @@ gdn_status gdn_conv_fwd(const void* x, const float* weight, const float* bias, c
   a.k = k;
   a.v = v;
   a.final_state = final_state;
-  a.run = conv_run(d->T, 2 * d->h_qk + d->h_v, kConvFill, 4);
+  conv_runs(d->T, 2 * d->h_qk + d->h_v - a.n_unit, kConvFill, kConvUnitCost, 4, 1, &a);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   LaunchLog log;
   if (d->T == 0 && !final_state) return GDN_OK;

@@ -242,6 +242,23 @@ __device__ __forceinline__ void finish(F2 (&u)[2], bool unit_head, float eps) {
   }
 }
 
+// A warp's (backward: a CTA's) head and which of its runs (groups of runs).
+struct ConvTask {
+  int head, place, run;
+  bool unit_head;
+};
+__device__ __forceinline__ ConvTask conv_task(const ConvArgs& a, unsigned i) {
+  const unsigned n_unit = a.n_unit, first = n_unit * (unsigned)a.runs[0];
+  ConvTask t;
+  t.unit_head = i < first;
+  const unsigned heads = t.unit_head ? n_unit : (unsigned)(2 * a.h_qk + a.h_v) - n_unit;
+  if (!t.unit_head) i -= first;
+  t.place = (int)(i / heads);
+  t.head = (int)(i % heads) + (t.unit_head ? 0 : (int)n_unit);
+  t.run = a.run[t.unit_head ? 0 : 1];
+  return t;
+}
+
 // Element i of the states after the call: row r of sequence s is the padded
 // row len + r of (state, tokens).
 template <typename T>
@@ -284,12 +301,13 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
     final_states<T>(a, (int64_t)(blockIdx.x - a.blocks) * kThreads + threadIdx.x, C);
     return;
   }
-  const unsigned warp = warp_index(), task = blockIdx.x * kWarps + warp, run = task / (unsigned)heads;
-  const int head = (int)(task - run * heads), c = head * kConvD + 4 * lane;
-  const int64_t first = (int64_t)run * a.run;
-  if (first >= a.T) return;
-  const int t0 = (int)first, t1 = (int)min((int64_t)a.T, first + a.run);
-  const bool unit_head = a.norm && head < 2 * a.h_qk;
+  const unsigned warp = warp_index();
+  const ConvTask task = conv_task(a, blockIdx.x * kWarps + warp);
+  const int head = task.head, c = head * kConvD + 4 * lane;
+  const int64_t first = (int64_t)task.place * task.run;
+  if (head >= heads || first >= a.T) return;
+  const int t0 = (int)first, t1 = (int)min((int64_t)a.T, first + task.run);
+  const bool unit_head = task.unit_head;
   const float eps = a.eps;
   char* ring = ring_all[warp];
   // the lane's part of a copy: kRows tokens at a time, 16 bytes of one of them
@@ -422,6 +440,13 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvArgs a) {
 }
 
 // ---- backward ----
+// Sum of tap j and channel c over group `group` of runs, in the workspace.
+__device__ __forceinline__ float* conv_part(const ConvArgs& a, bool unit_head, int group, int j, int c) {
+  const int64_t n_unit = (int64_t)a.n_unit * kConvD, others = (int64_t)(2 * a.h_qk + a.h_v) * kConvD - n_unit, rows = a.width + 1;
+  return unit_head ? a.part + (group * rows + j) * n_unit + c
+                   : a.part + a.runs[0] * rows * n_unit + (group * rows + j) * others + (c - n_unit);
+}
+
 // With g the gradient of a head's output, n = y r its unit vector:
 //   dy = r (g - n sum(g n)),  du = dy (s + u s (1 - s)),  s = sigmoid(u),
 //   dx_t = sum_j w_j du_{t + W - 1 - j},  dw_j = sum_t du_t x_{t - W + 1 + j}.
@@ -525,16 +550,16 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
   grid_dependency_wait();
   grid_launch_dependents();
   const int heads = 2 * a.h_qk + a.h_v, C = heads * kConvD;
-  const int head = (int)(blockIdx.x % (unsigned)heads), group = (int)(blockIdx.x / (unsigned)heads);
-  const int c = head * kConvD + 4 * lane;
+  const ConvTask task = conv_task(a, blockIdx.x);
+  const int head = task.head, c = head * kConvD + 4 * lane;
   F2 dw[W + 1][2];
 #pragma unroll
   for (int j = 0; j <= W; ++j) dw[j][0] = dw[j][1] = f2(0.f);
-  const int64_t first = ((int64_t)group * kWarps + warp) * a.run;
+  const int64_t first = ((int64_t)task.place * kWarps + warp) * task.run;
   if (first < a.T) {
-    const int t0 = (int)first, t1 = (int)min((int64_t)a.T, first + a.run);
-    const int stop = (int)min((int64_t)a.T, first + a.run + W - 1);  // tokens past the run, while its last sequence goes on
-    const bool unit_head = a.norm && head < 2 * a.h_qk;
+    const int t0 = (int)first, t1 = (int)min((int64_t)a.T, first + task.run);
+    const int stop = (int)min((int64_t)a.T, first + task.run + W - 1);  // tokens past the run, while its last sequence goes on
+    const bool unit_head = task.unit_head;
     const float eps = a.eps;
     const int64_t dxs = a.dx_stride;
     const HeadRows<T> rows = head_rows<T>(a, head);
@@ -694,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
     float v = 0.f;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) v += sh.sum[k][j][at];
-    a.part[((int64_t)group * (W + 1) + j) * C + head * kConvD + at] = v;
+    *conv_part(a, task.unit_head, task.place, j, c - 4 * lane + at) = v;
   }
 }
 
@@ -724,9 +749,13 @@ __global__ void __launch_bounds__(1024) conv_bwd_sum_kernel(const ConvArgs a) {
   const int j = blockIdx.x % (W + 1), at = (int)(blockIdx.x / (W + 1)) * 32 + lane;
   if (j == W && !a.d_bias) return;
   if (j < W && !a.d_weight) return;
+  const bool unit_head = at < a.n_unit * kConvD;
+  const int groups = a.runs[unit_head ? 0 : 1];
+  const float* part = conv_part(a, unit_head, 0, j, at);
+  const int64_t step = conv_part(a, unit_head, 1, j, at) - part;
   double v = 0.0;
 #pragma unroll 8
-  for (int i = warp; i < a.groups; i += 32) v += a.part[((int64_t)i * (W + 1) + j) * C + at];
+  for (int i = warp; i < groups; i += 32) v += part[i * step];
   sum[warp][lane] = v;
   __syncthreads();
   if (warp == 0) {
@@ -754,8 +783,8 @@ cudaError_t by_kind(const ConvArgs& a, bool f32, F&& f) {
 
 cudaError_t launch_conv(const ConvArgs& args, bool f32, cudaStream_t st) {
   ConvArgs a = args;
-  const int64_t heads = 2 * a.h_qk + a.h_v, runs = ((int64_t)a.T + a.run - 1) / a.run;
-  a.blocks = (int)((runs * heads + kWarps - 1) / kWarps);
+  const int64_t heads = 2 * a.h_qk + a.h_v, tasks = (int64_t)a.n_unit * a.runs[0] + (heads - a.n_unit) * a.runs[1];
+  a.blocks = (int)((tasks + kWarps - 1) / kWarps);
   int64_t blocks = a.blocks;
   if (a.final_state) blocks += ((int64_t)a.n_seqs * (a.width - 1) * heads * 32 + kThreads - 1) / kThreads;
   if (blocks == 0) return cudaSuccess;
@@ -774,7 +803,7 @@ cudaError_t launch_conv_step(const ConvArgs& a, bool f32, cudaStream_t st) {
 }
 
 cudaError_t launch_conv_bwd(const ConvArgs& a, bool f32, cudaStream_t st) {
-  const int64_t blocks = (int64_t)a.groups * (2 * a.h_qk + a.h_v);
+  const int64_t blocks = (int64_t)a.n_unit * a.runs[0] + (int64_t)(2 * a.h_qk + a.h_v - a.n_unit) * a.runs[1];
   return by_kind(a, f32, [&](auto type, auto w, auto silu) {
     return launch_kernel(conv_bwd_kernel<decltype(type), decltype(w)::value, decltype(silu)::value>, dim3((unsigned)blocks),
                          dim3(kThreads), 0, st, true, a);

@@ -25,7 +25,11 @@ struct ConvArgs {
   int n_seqs, T, n_each, h_qk, h_v;
   int width, silu, norm;
   float eps;
-  int run;                 // tokens a warp takes in a row
+  // Heads whose norm is taken, the first n_unit, and the others: they cost more, so
+  // a warp takes fewer of their tokens in a row.
+  int n_unit;
+  int run[2];              // tokens a warp takes, of the former, of the others
+  int runs[2];             // runs of all tokens (backward: groups of 8 of them)
   int blocks;              // CTAs before those for the final states
   // backward
   const void* d_final;     // [n_seqs, W - 1, C] or null (zero)
@@ -33,8 +37,7 @@ struct ConvArgs {
   void* d_state;           // [n_seqs, W - 1, C] or null
   float* d_weight;         // [C, W] or null
   float* d_bias;           // [C] or null
-  float* part;             // [groups, W + 1, C] sums of the weights' gradients
-  int groups;              // groups of 8 runs
+  float* part;             // [groups, W + 1, channels] of either, sums of the weights' gradients
   int sums;                // d_weight or d_bias is wanted
 };
 

@@ -231,11 +231,14 @@ def test_conv_refuses_pointers(lib):
 @pytest.mark.parametrize("T", [0, 1, 63, 64, 65, 4097, 32768, 348160])
 @pytest.mark.parametrize("h_qk,h_v,width", [(1, 1, 2), (2, 8, 4), (16, 16, 3)])
 def test_conv_workspace_covers(lib, T, h_qk, h_v, width):
-    """A row of W + 1 sums a channel for each group of 8 runs of 8 to 192 tokens."""
-    n = ctypes.c_size_t(0)
-    assert lib.gdn_conv_bwd_workspace_bytes(conv_dims(T=T, n_seqs=1, h_qk=h_qk, h_v=h_v, width=width), n) == OK
+    """A row of W + 1 sums a channel for each group of 8 runs of 8 to 192 tokens, with and without the norm."""
+    sizes = []
+    for norm in (0, 1):
+        n = ctypes.c_size_t(0)
+        assert lib.gdn_conv_bwd_workspace_bytes(conv_dims(T=T, n_seqs=1, h_qk=h_qk, h_v=h_v, width=width, norm=norm), n) == OK
+        sizes.append(n.value)
     row = (width + 1) * (2 * h_qk + h_v) * 128 * 4
-    assert n.value % row == 0 and -(-T // (8 * 192)) <= n.value // row <= -(-T // 64)
+    assert sizes[0] == sizes[1] and -(-T // (8 * 192)) * row <= sizes[0] <= -(-T // 64) * row
 
 
 def test_python_refuses():

@@ -1,9 +1,11 @@
 """Serving a stack that mixes gated-delta-rule layers with softmax attention.
 
 Three gated-delta-rule mixers for each attention mixer, as such models have
-them.  The prompts of a batch are packed and run through gdn_chunk_fwd, whose
-final states gdn_decode_step then advances token by token; the attention
-mixers keep an 8-bit key/value cache instead (gdn_kv_append, gdn_kv_attn).  The
+them.  The prompts of a batch are packed; a projection's q, k and v go through
+the short convolution (gdn_conv_fwd) and gdn_chunk_fwd, whose final states
+gdn_conv_step and gdn_decode_step then advance token by token.  The attention
+mixers keep an 8-bit key/value cache instead: gdn_kv_append_rope normalises and
+rotates queries and keys and writes keys and values, gdn_kv_attn reads them.  The
 decode step is captured once as a CUDA graph: its lengths and page table are
 device data, so replays follow the growing sequences.
 
@@ -33,47 +35,49 @@ def _weight(gen, rows, cols):
 
 
 class DeltaMixer:
-    """o = W_o . gated_delta_rule(q, k, v, g, beta), all from projections of x."""
+    """o = W_o . gated_delta_rule(q, k, v, g, beta), all from projections of x; q, k, v through a short convolution."""
 
-    def __init__(self, gen, width, h_qk, h_v):
+    def __init__(self, gen, width, h_qk, h_v, taps=4):
         self.h_qk, self.h_v = h_qk, h_v
         self.w_in = _weight(gen, (2 * h_qk + h_v) * D, width)
+        self.taps = torch.randn((2 * h_qk + h_v) * D, taps, device="cuda", generator=gen) / taps ** 0.5
         self.w_gate = _weight(gen, 2 * h_v, width)
         self.w_out = _weight(gen, width, h_v * D)
-        self.state = None
+        self.state = self.conv_state = None
 
-    def _project(self, x):
-        qkv = (x @ self.w_in.T).view(-1, 2 * self.h_qk + self.h_v, D)
-        q, k, v = qkv.split([self.h_qk, self.h_qk, self.h_v], dim=1)
+    def _gates(self, x):
         gate = (x @ self.w_gate.T).float()
-        g = F.logsigmoid(gate[:, :self.h_v] + 3.0)
-        beta = torch.sigmoid(gate[:, self.h_v:])
-        unit = lambda t: F.normalize(t.float(), dim=-1).bfloat16()  # noqa: E731
-        return unit(q), unit(k), v.contiguous(), g.contiguous(), beta.contiguous()
+        return F.logsigmoid(gate[:, :self.h_v] + 3.0).contiguous(), torch.sigmoid(gate[:, self.h_v:]).contiguous()
 
     def prefill(self, x, cu_seqlens):
         # a captured step goes on reading the first states' memory
-        o, self.state = gdn.gdn_chunk_fwd(*self._project(x), None, cu_seqlens, final_state=self.state)
+        q, k, v, self.conv_state = gdn.gdn_conv_fwd(x @ self.w_in.T, self.taps, self.h_qk, None, None, cu_seqlens,
+                                                    final_state=self.conv_state)
+        o, self.state = gdn.gdn_chunk_fwd(q, k, v, *self._gates(x), None, cu_seqlens, final_state=self.state)
         return o.flatten(1) @ self.w_out.T
 
     def step(self, x):
-        return gdn.gdn_decode_step(*self._project(x), self.state).flatten(1) @ self.w_out.T
+        q, k, v = gdn.gdn_conv_step(x @ self.w_in.T, self.conv_state, self.taps, self.h_qk)
+        return gdn.gdn_decode_step(q, k, v, *self._gates(x), self.state).flatten(1) @ self.w_out.T
 
 
 class AttentionMixer:
-    """o = W_o . softmax attention over an 8-bit cache."""
+    """o = W_o . softmax attention over an 8-bit cache, of normalised heads with rotary positions."""
 
     def __init__(self, gen, width, h_q, h_kv, n_pages):
         self.h_q, self.h_kv = h_q, h_kv
         self.w_in = _weight(gen, (h_q + 2 * h_kv) * D, width)
         self.w_out = _weight(gen, width, h_q * D)
+        self.q_norm, self.k_norm = (1 + 0.1 * torch.randn(D, device="cuda", generator=gen) for _ in range(2))
+        self.rope = gdn.gdn_rope_table(D // 2)  # half of each head
         self.cache = gdn.KVCache.empty(n_pages, h_kv)
 
     def __call__(self, x, kv_lens, page_table, cu_seqlens=None, *, plan=None, workspace=None):
         # the heads of one fused projection are used in place, by their strides
         qkv = (x @ self.w_in.T).view(-1, self.h_q + 2 * self.h_kv, D)
         q, k, v = qkv.split([self.h_q, self.h_kv, self.h_kv], dim=1)
-        gdn.gdn_kv_append(self.cache, k, v, kv_lens, page_table, cu_seqlens)
+        q = gdn.gdn_kv_append_rope(self.cache, k, v, kv_lens, page_table, cu_seqlens, rope=self.rope, norm="rms",
+                                   k_weight=self.k_norm, q=q, q_weight=self.q_norm, q_out=q)
         o, _ = gdn.gdn_kv_attn(q, self.cache, kv_lens, page_table, cu_seqlens, plan=plan, workspace=workspace,
                                return_lse=False)
         return o.flatten(1) @ self.w_out.T
@@ -110,6 +114,9 @@ class HybridStack:
             x = x + y
         return x
 
+    def _states(self):
+        return [t for m in self.layers if isinstance(m, DeltaMixer) for t in (m.state, m.conv_state)]
+
     def step(self, x):
         """x [batch, width]: one more token of each sequence."""
         self.kv_lens += 1
@@ -118,13 +125,13 @@ class HybridStack:
                                         max_pages=self.pages)
             workspace = torch.empty(max(256, plan.workspace_bytes), dtype=torch.uint8, device="cuda")
             self.x = x.clone()
-            states = [layer.state.clone() for layer in self.layers if isinstance(layer, DeltaMixer)]
+            states = [t.clone() for t in self._states()]
             side = torch.cuda.Stream()
             side.wait_stream(torch.cuda.current_stream())
             with torch.cuda.stream(side):  # warm-up, and undo what it did to the states (the cache's tokens are rewritten)
                 self._step(self.x, plan, workspace)
-                for layer, s in zip((m for m in self.layers if isinstance(m, DeltaMixer)), states):
-                    layer.state.copy_(s)
+                for t, s in zip(self._states(), states):
+                    t.copy_(s)
             torch.cuda.current_stream().wait_stream(side)
             self.graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(self.graph):

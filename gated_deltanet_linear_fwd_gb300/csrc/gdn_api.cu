@@ -412,6 +412,12 @@ gdn_status rope_args(const gdn_rope* rope, int norm, float eps, RopeArgs* r) {
   return norm_eps(eps, &r->eps);
 }
 
+// An output in place of its input has its token stride: with another it would
+// write rows that are yet to be read.
+bool other_rows(const void* in, int64_t in_stride, const void* out, int64_t out_stride, int T) {
+  return in && in == out && in_stride != out_stride && T > 1;
+}
+
 // CTAs whose warps share the heads of a call: `most`, but a head of two tokens
 // for a warp at least.  A warp's heads are counted in 32 bits.
 gdn_status rope_ctas(int64_t most, QkRopeArgs* a) {
@@ -1250,6 +1256,9 @@ gdn_status gdn_qk_rope(const void* q, const void* k, const float* q_weight, cons
   if (d->T == 0) return GDN_OK;
   if ((d->h_q && (!q || !q_out)) || (d->h_k && (!k || !k_out))) return GDN_ERR_INVALID_ARG;
   if (misaligned16({q, k, q_out, k_out})) return GDN_ERR_MISALIGNED;
+  if (other_rows(q, a.side[0].in_stride, q_out, a.side[0].out_stride, d->T) ||
+      other_rows(k, a.side[1].in_stride, k_out, a.side[1].out_stride, d->T))
+    return GDN_ERR_INVALID_ARG;
   a.side[0].in = q;
   a.side[1].in = k;
   a.side[0].out = q_out;
@@ -1289,6 +1298,9 @@ gdn_status gdn_qk_rope_bwd(const void* q, const void* k, const float* q_weight, 
   const bool read = d->norm != GDN_NORM_NONE;
   if ((d->h_q && ((read && !q) || !d_q_out || !dq)) || (d->h_k && ((read && !k) || !d_k_out || !dk))) return GDN_ERR_INVALID_ARG;
   if (misaligned16({q, k, d_q_out, d_k_out, dq, dk})) return GDN_ERR_MISALIGNED;
+  if (other_rows(d_q_out, a.side[0].out_stride, dq, a.side[0].dx_stride, d->T) ||
+      other_rows(d_k_out, a.side[1].out_stride, dk, a.side[1].dx_stride, d->T))
+    return GDN_ERR_INVALID_ARG;
   size_t need = 0;
   gdn_qk_rope_bwd_workspace_bytes(&need);
   if (sums && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
@@ -1332,6 +1344,7 @@ gdn_status gdn_kv_append_rope(const void* k, const void* v, const float* k_weigh
     RopeSide& s = a.q.side[0];
     if ((st = kv_stride(d->q_stride, d->h_q, d->dtype, &s.in_stride)) != GDN_OK) return st;
     if ((st = kv_stride(d->out_stride, d->h_q, d->dtype, &s.out_stride)) != GDN_OK) return st;
+    if (other_rows(q, s.in_stride, q_out, s.out_stride, d->T)) return GDN_ERR_INVALID_ARG;
     a.q.pos = {nullptr, cu, lens, d->n_seqs, d->T, a.p.c.n_each};
     s.in = q;
     s.out = q_out;

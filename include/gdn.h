@@ -598,7 +598,8 @@ typedef struct gdn_rope_dims {
  *                       leaves the buffers.
  *   rope              : host, or NULL (nothing turns).
  *   q_out, k_out      : device, like q and k.  Each may be its input itself (same
- *                       address and stride); otherwise outputs overlap nothing.
+ *                       address and stride; the same address with another stride is
+ *                       refused); otherwise outputs overlap nothing.
  * Where a head's sum of squares passes fp32's range it is taken of scaled
  * elements, so finite heads of any size are normalised.  An infinite or NaN
  * element makes NaN of itself and of its pair, NaN of the whole head.
@@ -618,7 +619,8 @@ gdn_status gdn_qk_rope_bwd_workspace_bytes(size_t* bytes);
  *   dx = r (dn - n sum(dn n) / 128)  (GDN_NORM_UNIT: without the 128).
  * Inputs as gdn_qk_rope's; q and k are not read with GDN_NORM_NONE (may be NULL).
  *   d_q_out, d_k_out      : device, [T, h, 128], dims->dtype.
- *   dq, dk                : device, the same; each may be its d_q_out or d_k_out itself.
+ *   dq, dk                : device, the same; each may be its d_q_out or d_k_out itself, as
+ *                           gdn_qk_rope's outputs their inputs.
  *                           Tokens outside every sequence are left as they were, and
  *                           do not count in the weights' gradients.
  *   dq_weight, dk_weight  : device fp32 [128], or NULL (not wanted); need the weight.

@@ -136,6 +136,20 @@ def test_rope_refuses_pointers(lib):
         assert lib.gdn_qk_rope_bwd(*a) == expect, i
 
 
+def test_in_place_needs_the_same_rows(lib):
+    """An output at its input's address with another token stride would overwrite rows that are yet to be read."""
+    for kw in (dict(q_out_stride=1024), dict(q_stride=1024)):
+        assert lib.gdn_qk_rope(512, 1024, 64, 64, None, None, rope(), 512, 4096, rope_dims(**kw), None) == INVALID
+    assert lib.gdn_qk_rope(512, 1024, 64, 64, None, None, rope(), 2048, 1024, rope_dims(k_out_stride=2048), None) == INVALID
+    for kw in (dict(q_out_stride=1024), dict(dq_stride=1024)):
+        assert lib.gdn_qk_rope_bwd(512, 1024, 64, 64, None, None, rope(), 2048, 4096, 2048, 512, 64, 64, rope_dims(**kw), 256, 1 << 30,
+                                   None) == INVALID
+    assert lib.gdn_qk_rope_bwd(512, 1024, 64, 64, None, None, rope(), 2048, 4096, 512, 4096, 64, 64, rope_dims(dk_stride=2048), 256,
+                               1 << 30, None) == INVALID
+    for kw in (dict(q_stride=1024), dict(out_stride=1024)):
+        assert lib.gdn_kv_append_rope(512, 1024, 64, 512, 64, 512, 64, 64, None, cache(), kv_dims(**kw), rope(), 1, 0.0, None) == INVALID
+
+
 def kv_dims(**kw):
     from gated_deltanet_linear_fwd_gb300 import _lib as L
     d = dict(n_seqs=2, T=4, h_q=4, max_pages=3, causal=1, window=0, scale=0.0, dtype=0, q_stride=0, k_stride=0, v_stride=0,

@@ -532,7 +532,7 @@ __device__ __forceinline__ void unit_back(F2 (&y)[G][2], F2 (&g)[G][2], float ep
   const float r_mine = rsqrt_approx(sum + eps);  // of the lanes that hold a sum of squares
 #pragma unroll
   for (int i = 0; i < G; ++i) {
-    const float r = group_value<2 * G>(r_mine, i), m = -(r * r) * group_value<2 * G>(sum, G + i);
+    const float r = group_value<2 * G>(r_mine, i), m = -r * (r * group_value<2 * G>(sum, G + i));
 #pragma unroll
     for (int e = 0; e < 2; ++e) g[i][e] = mul2(fma2(y[i][e], f2(m), g[i][e]), f2(r));
   }

@@ -163,24 +163,27 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeA
   a.part[((int64_t)blockIdx.x * 2 + side) * kRopeD + at] = v;
 }
 
-// The CTAs' sums to one, in a fixed order: CTA (side, 32 elements), a row a warp.
-__global__ void __launch_bounds__(1024) rope_weight_kernel(const QkRopeArgs a) {
-  __shared__ double sum[32][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int side = blockIdx.x >> 2, at = (blockIdx.x & 3) * 32 + lane;
+// The CTAs' sums to one, in a fixed order: CTA (side, 8 elements), a row of them
+// a quarter of a warp.  So small that it is there, and waiting, before the kernel
+// that writes the sums has ended.
+constexpr int kSumThreads = 128, kSumWidth = 8, kSumRows = kSumThreads / kSumWidth;
+__global__ void __launch_bounds__(kSumThreads) rope_weight_kernel(const QkRopeArgs a) {
+  __shared__ double sum[kSumRows][kSumWidth];
+  const int e = threadIdx.x % kSumWidth, row = threadIdx.x / kSumWidth;
+  const int side = blockIdx.x / (kRopeD / kSumWidth), at = blockIdx.x % (kRopeD / kSumWidth) * kSumWidth + e;
   grid_dependency_wait();
   grid_launch_dependents();
   float* out = a.side[side].d_weight;
   if (!out) return;
   double v = 0.0;
-#pragma unroll 8
-  for (int i = warp; i < a.ctas; i += 32) v += a.part[((int64_t)i * 2 + side) * kRopeD + at];
-  sum[warp][lane] = v;
+#pragma unroll 19
+  for (int i = row; i < a.ctas; i += kSumRows) v += a.part[((int64_t)i * 2 + side) * kRopeD + at];
+  sum[row][e] = v;
   __syncthreads();
-  if (warp == 0) {
+  if (row == 0) {
     v = 0.0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v += sum[i][lane];
+    for (int i = 0; i < kSumRows; ++i) v += sum[i][e];
     out[at] = (float)v;
   }
 }
@@ -206,7 +209,7 @@ cudaError_t launch_qk_rope_bwd(const QkRopeArgs& a, bool f32, cudaStream_t st) {
 }
 
 cudaError_t launch_qk_rope_weights(const QkRopeArgs& a, cudaStream_t st) {
-  return launch_kernel(rope_weight_kernel, dim3(8), dim3(1024), 0, st, true, a);
+  return launch_kernel(rope_weight_kernel, dim3(2 * kRopeD / kSumWidth), dim3(kSumThreads), 0, st, true, a);
 }
 
 }  // namespace gdn

@@ -6,6 +6,8 @@
 // the codes, without a rounding in between; pages, scales and codes are those
 // of gdn_kv.cu.  Blocks: queries, 8 warps' runs each, then keys of a (page
 // slot, head) each, then values.
+#include <type_traits>
+
 #include "gdn_kv_page.cuh"
 #include "gdn_rope.cuh"
 
@@ -57,6 +59,48 @@ __device__ __forceinline__ Angles further(const Angles& a, const float4& c, cons
   return r;
 }
 
+// A row of keys, normalised and rotated.  Whole warps run this.
+template <bool kInterleaved>
+__device__ __forceinline__ void key_row(const KvRopeArgs& a, const RopeLane& l, const F2 (&w)[4], const Angles& angle, F2 (&y)[4]) {
+  if (a.q.r.norm != kNormNone) {
+    const float ss = half_sum(dot_row(y, y));
+    float n = rsqrt_approx(fmaf(ss, a.q.r.inv_n, a.q.r.eps)), unit;
+    if (large_heads(ss)) n = scaled_head(y, ss, a.q.r.inv_n, a.q.r.eps, unit);
+    scale_row(y, n);
+    if (a.k_weight) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], w[e]);
+    }
+  }
+  turn_row<kInterleaved>(a.q.r.rot == kRopeD, l, angle, y);
+}
+// The largest magnitude of a lane's part of a row, as bits.
+__device__ __forceinline__ uint32_t row_bits(const F2 (&y)[4]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 p = parts(y[e]);
+    m = max(m, max(magnitude_bits(p.x), magnitude_bits(p.y)));
+  }
+  return m;
+}
+// What is not finite becomes NaN and does not count: the largest of the others.
+template <int N>
+__device__ __forceinline__ uint32_t finite_rows(F2 (&y)[N][4]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 p = parts(y[i][e]);
+      if (magnitude_bits(p.x) < 0x7f800000u) m = max(m, magnitude_bits(p.x));
+      if (magnitude_bits(p.y) < 0x7f800000u) m = max(m, magnitude_bits(p.y));
+      y[i][e] = f2(or_nan(p.x), or_nan(p.y));
+    }
+  }
+  return m;
+}
+
 template <typename T, bool kInterleaved>
 __device__ __forceinline__ void append_turned_page(const KvRopeArgs& a, const Entry& en, int h, uint32_t& top,
                                                    PageSteps& sh) {
@@ -87,46 +131,19 @@ __device__ __forceinline__ void append_turned_page(const KvRopeArgs& a, const En
   load_weight(a.k_weight, l, w);
   const Angles angle = rope_angles(a.q.r, l, rope_freq(a.q.r, l, lane), pos0 + hw);
   __syncthreads();
-  const bool norm = a.q.r.norm != kNormNone;
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     unpack_row(raw[i], y[i]);  // zeros where the row is not new
     if (kTasks * i >= hi || kTasks * (i + 1) <= lo) continue;
-    if (norm) {
-      const float ss = half_sum(dot_row(y[i], y[i]));
-      float n = rsqrt_approx(fmaf(ss, a.q.r.inv_n, a.q.r.eps)), unit;
-      if (large_heads(ss)) n = scaled_head(y[i], ss, a.q.r.inv_n, a.q.r.eps, unit);
-      scale_row(y[i], n);
-      if (a.k_weight) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[i][e] = mul2(y[i][e], w[e]);
-      }
-    }
     Angles here = angle;
     if (i > 0 && l.turned)
       here = further(angle, *reinterpret_cast<const float4*>(&sh.c[max(i - 1, 0)][4 * lane]),
                      *reinterpret_cast<const float4*>(&sh.s[max(i - 1, 0)][4 * lane]));
-    turn_row<kInterleaved>(a.q.r.rot == kRopeD, l, here, y[i]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 p = parts(y[i][e]);
-      m = max(m, max(magnitude_bits(p.x), magnitude_bits(p.y)));
-    }
+    key_row<kInterleaved>(a, l, w, here, y[i]);
+    m = max(m, row_bits(y[i]));
   }
-  if (m >= 0x7f800000u) {  // what is not finite becomes NaN codes and does not count
-    m = 0;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 p = parts(y[i][e]);
-        if (magnitude_bits(p.x) < 0x7f800000u) m = max(m, magnitude_bits(p.x));
-        if (magnitude_bits(p.y) < 0x7f800000u) m = max(m, magnitude_bits(p.y));
-        y[i][e] = f2(or_nan(p.x), or_nan(p.y));
-      }
-    }
-  }
+  if (m >= 0x7f800000u) m = finite_rows(y);
   m = __reduce_max_sync(0xffffffffu, m);
   __syncthreads();  // top is zero; everyone has read the scale
   if ((tid & 31) == 0 && m) atomicMax(&top, m);
@@ -148,6 +165,83 @@ __device__ __forceinline__ void append_turned_page(const KvRopeArgs& a, const En
     }
   }
   if (tid == 0) *scale = s;
+}
+
+// ---- few tokens a sequence ----
+// A page slot and head of keys or values, with at most kFewTokens new rows, by
+// one warp: two rows at a time, a half each.  Of a block's 16 half-warps most
+// would have no row, and a block's start and barriers are what it costs.  Back to
+// back in a graph, 8 + 2 heads, 256 sequences, with 1 / 4 / 8 tokens each: 2.8 /
+// 4.9 / 6.1 us, by blocks 6.6 / 9.7 / 10.7; 1024 sequences of 32 + 8 heads: 12.3
+// / 22.4 / 37.1 and 73 / 104 / 121.  With 16 rows a warp a single sequence takes
+// twice as long (5.9 and 3.1).
+template <typename T, bool kInterleaved, int kFewTokens>
+__device__ __forceinline__ void append_few(const KvRopeArgs& a, unsigned task) {
+  const unsigned h_kv = a.p.c.h_kv, pages = a.entries * h_kv;  // the grid is below 2^31
+  const bool values = task >= pages;
+  if (values) task -= pages;
+  if (task >= pages) return;
+  const int h = (int)(task % h_kv), e = (int)(task / h_kv), seq = e / a.p.pages_each, j = e % a.p.pages_each;
+  const KvSeq s = kv_seq(a.p.c, seq);
+  if (j >= seq_slots(s)) return;
+  const int past = s.len - s.n, slot = max(past, 0) / kPage + j, pos0 = slot * kPage;
+  const int lo = max(past - pos0, 0), hi = min(s.len - pos0, kPage);  // rows of the page that are new
+  if (hi <= lo) return;
+  const int lane = threadIdx.x & 15, half = threadIdx.x >> 4 & 1;
+  const RopeLane l = values ? RopeLane{8 * lane, 8 * lane + 4, false} : rope_lane(a.q.r, lane);
+  const int64_t stride = values ? a.p.v_stride : a.p.k_stride;
+  const T* src = static_cast<const T*>(values ? a.p.v : a.p.k) + ((int64_t)s.tok0 + pos0 - past) * stride + h * kHeadDim;
+  const char* first = reinterpret_cast<const char*>(src + l.o0);
+  const uint32_t gap = (l.o1 - l.o0) * sizeof(T);
+  typename RowOf<T>::type raw[kFewTokens / 2];
+#pragma unroll
+  for (int i = 0; i < kFewTokens / 2; ++i) {
+    const int r = lo + 2 * i + half;
+    raw[i] = {};
+    const char* p = first + r * stride * (int64_t)sizeof(T);
+    if (r < hi) raw[i] = load_row<T>(p, p + gap);
+  }
+  const int page = kv_page(a.p.c, seq, slot);
+  if (page < 0) return;
+  const size_t head = (size_t)page * h_kv + h;
+  float* scale = (values ? a.p.c.v_scale : a.p.c.k_scale) + head;
+  const float old_s = lo > 0 ? *scale : 0.f;
+  F2 y[kFewTokens / 2][4], w[4];
+  load_weight(values ? nullptr : a.k_weight, l, w);
+  const RopeFreq freq = rope_freq(a.q.r, l, lane);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kFewTokens / 2; ++i) {
+    unpack_row(raw[i], y[i]);
+    if (lo + 2 * i >= hi) continue;
+    if (!values) key_row<kInterleaved>(a, l, w, rope_angles(a.q.r, l, freq, pos0 + lo + 2 * i + half), y[i]);
+    m = max(m, row_bits(y[i]));
+  }
+  if (m >= 0x7f800000u) m = finite_rows(y);
+  m = __reduce_max_sync(0xffffffffu, m);
+  const float now_s = fmaxf(pow2f(min(e4m3_scale_exp(m, kScaleMinExp), kScaleMaxExp)), old_s);
+  const float inv = 1.0f / now_s;  // exact: a power of two
+  uint8_t* codes = (values ? a.p.c.v : a.p.c.k) + head * kPageBytes;
+#pragma unroll
+  for (int i = 0; i < kFewTokens / 2; ++i) {
+    const int r = lo + 2 * i + half;
+    if (r >= hi) continue;
+    *reinterpret_cast<uint32_t*>(codes + r * kHeadDim + l.o0) = encode4(y[i][0], y[i][1], inv);
+    *reinterpret_cast<uint32_t*>(codes + r * kHeadDim + l.o1) = encode4(y[i][2], y[i][3], inv);
+  }
+  if (now_s > old_s)  // the earlier rows follow
+    for (uint32_t* c = reinterpret_cast<uint32_t*>(codes) + (threadIdx.x & 31); c < reinterpret_cast<uint32_t*>(codes + lo * kHeadDim); c += 32)
+      *c = recode4(*c, old_s, inv);
+  if ((threadIdx.x & 31) == 0) *scale = now_s;
+}
+
+template <typename T, bool kInterleaved, int kFewTokens>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_few_kernel(const KvRopeArgs a) {
+  __shared__ RopeRing ring;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (blockIdx.x < (unsigned)a.q.ctas) turn_run<T, kInterleaved>(a.q, blockIdx.x, ring);
+  else append_few<T, kInterleaved, kFewTokens>(a, (blockIdx.x - a.q.ctas) * kRopeWarps + warp_index());
 }
 
 template <typename T, bool kInterleaved>
@@ -182,12 +276,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_rope_
 }  // namespace
 
 cudaError_t launch_kv_append_rope(const KvRopeArgs& a, bool f32, cudaStream_t st) {
-  const dim3 grid(a.q.ctas + 2 * a.entries * (unsigned)a.p.c.h_kv), block(kThreads);
-  if (f32)
-    return a.q.r.interleaved ? launch_kernel(append_rope_kernel<float, true>, grid, block, 0, st, true, a)
-                           : launch_kernel(append_rope_kernel<float, false>, grid, block, 0, st, true, a);
-  return a.q.r.interleaved ? launch_kernel(append_rope_kernel<__nv_bfloat16, true>, grid, block, 0, st, true, a)
-                         : launch_kernel(append_rope_kernel<__nv_bfloat16, false>, grid, block, 0, st, true, a);
+  const unsigned tasks = 2 * a.entries * (unsigned)a.p.c.h_kv;
+  const int most = a.p.c.cu ? kPage : a.p.c.n_each;  // new rows of a page
+  const bool few = most <= 8;
+  const dim3 grid(a.q.ctas + (few ? (tasks + kRopeWarps - 1) / kRopeWarps : tasks)), block(kThreads);
+  auto run = [&](auto type, auto interleaved) {
+    using T = decltype(type);
+    constexpr bool kInterleaved = decltype(interleaved)::value;
+    return most <= 4 ? launch_kernel(append_few_kernel<T, kInterleaved, 4>, grid, block, 0, st, true, a)
+           : few     ? launch_kernel(append_few_kernel<T, kInterleaved, 8>, grid, block, 0, st, true, a)
+                     : launch_kernel(append_rope_kernel<T, kInterleaved>, grid, block, 0, st, true, a);
+  };
+  auto typed = [&](auto type) { return a.q.r.interleaved ? run(type, std::true_type()) : run(type, std::false_type()); };
+  return f32 ? typed(float()) : typed(__nv_bfloat16());
 }
 
 }  // namespace gdn

@@ -147,9 +147,34 @@ def test_token_by_token(dtype, grow):
         n.check(n.call())
 
 
-def test_not_finite_keys():
+@pytest.mark.parametrize("n", [2, 3, 4, 5, 8, 9, 16])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_few_tokens_each(n, dtype):
+    """The same number of new tokens in every sequence, whole, across page ends, in an idle slot, with earlier rows that stay
+    or follow a scale that grows."""
+    kv = [n, n + 1, 63 + n, 64, 65 + n // 2, 64 + n, 128, 129, 300]
+    for norm, size in (("rms", 1.0), ("none", 40.0), ("none", 1e-3)):
+        c = Case([n] * len(kv), kv, 3, 2, dtype, seed=80 + n, use_cu=False, norm=norm, layout="interleaved" if n % 2 else "half", rot=96)
+        c.k, c.v = (c.k.float() * size).to(dtype), (c.v.float() * size).to(dtype)
+        c.gk, c.gv = c.k.cuda(), c.v.cuda()
+        c.check(c.call())
+    c = Case([n] * 3, [70, n, n], 2, 1, dtype, seed=81, use_cu=False)
+    lens = torch.tensor([70, n - 1, 0], dtype=torch.int32, device="cuda")  # a token before position 0; an idle slot
+    before = c.cache.k.clone()
+    c.call(q=None, q_weight=None)
+    whole = c.cache.k.view(torch.uint8).clone()
+    c.cache.k.copy_(before)
+    gdn.gdn_kv_append_rope(c.cache, c.gk, c.gv, lens, c.b.table.cuda(), **c.how)
+    one, idle = int(c.b.table[1, 0]), int(c.b.table[2, 0])
+    got = c.cache.k.view(torch.uint8)
+    assert torch.equal(got[idle], before.view(torch.uint8)[idle]) and torch.equal(got[one, :, n:], whole[one, :, n:])
+    assert gdn.gdn_get_device_status(c.cache.status) == (0, 0)
+
+
+@pytest.mark.parametrize("use_cu", [True, False])
+def test_not_finite_keys(use_cu):
     """They become NaN codes (their whole head under a norm, but for an infinity's) and do not count in the scale."""
-    c = Case([3], [3], 2, 2, F32, norm="none", seed=70)
+    c = Case([3], [3], 2, 2, F32, norm="none", seed=70, use_cu=use_cu)
     c.k[0, 0, 5] = math.inf
     c.k[1, 1, 100] = math.nan
     c.gk = c.k.cuda()
@@ -162,7 +187,7 @@ def test_not_finite_keys():
     turned[1, 1, [36, 100]] = 0
     for h in range(2):
         assert float(c.cache.k_scale[int(c.b.table[0, 0]), h]) == 2.0 ** K.scale_exp(float(turned[:, h].abs().max()))
-    c = Case([2], [2], 2, 1, F32, norm="rms", weights=False, seed=71)
+    c = Case([2], [2], 2, 1, F32, norm="rms", weights=False, seed=71, use_cu=use_cu)
     c.k[0, 0, 5] = math.nan
     c.gk = c.k.cuda()
     c.call(q=None)

@@ -6,9 +6,13 @@
 // unit length, y / sqrt(sum y^2 + eps).  And its gradients, and its form for
 // one new token of each sequence.
 //
-// All of it moves each element once and is bound by that.  A group of lanes
-// owns a head's channels over a run of tokens and keeps the last W - 1 inputs
-// in registers, so an input is read once but for the W - 1 before each run.
+// All of it moves each element once and is bound by that or, in the gradient, by
+// what it computes meanwhile.  A warp owns a head's channels over a run of tokens
+// and keeps the last W - 1 inputs in registers, so an input is read once but for
+// the W - 1 before each run.  Measured, 2 + 2 + 8 heads, 4 taps, bf16: 32768
+// tokens 35.5 us, 5.7 TB/s, 85 % of what a copy reaches; 348160 tokens 331 us, 97
+// %; the gradient of 32768 tokens 70.5 us, 4.3 TB/s (64 %); one token for 256
+// sequences 2.6 us, back to back in a graph.  First versions: 78.6, 662 and 165.
 #include <type_traits>
 
 #include "gdn_conv.cuh"
@@ -453,7 +457,11 @@ __device__ __forceinline__ float* conv_part(const ConvArgs& a, bool unit_head, i
 // A warp walks a run of tokens of one head, 4 channels a lane, and W - 1
 // tokens past it, whose du belong to the run's last dx; `acc` holds the W - 1
 // gradients that wait for later tokens.  The gradient before a sequence's
-// first token is its state's.
+// first token is its state's.  With taps, their sums, inputs and waiting
+// gradients of 4 channels in 128 registers, 16 warps fit an SM; issue slots are 57 %
+// busy, the packed arithmetic's pipe 47 %.  A run
+// length that makes two waves or more lost (84 to 99 us), and so did windows
+// that turn in registers instead of being moved (83).
 template <typename T, int W>
 __device__ __forceinline__ void put_dx(const ConvArgs& a, const ConvSeq& s, int at, int t0, int t1, int c, int C,
                                        const F2 (&v)[2]) {

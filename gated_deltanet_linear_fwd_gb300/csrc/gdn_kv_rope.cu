@@ -5,7 +5,9 @@
 // Keys go through y = m R (x r w) (gdn_rope.cuh) in fp32 and from there into
 // the codes, without a rounding in between; pages, scales and codes are those
 // of gdn_kv.cu.  Blocks: queries, 8 warps' runs each, then keys of a (page
-// slot, head) each, then values.
+// slot, head) each, then values; with few tokens a sequence, warps of keys and
+// values.  Measured, 32768 tokens of 8 heads on 2, bf16: 35.7 us, 5.2 TB/s, 78 % of
+// what a copy reaches, with issue slots 73 % busy (norm, rotation, codes).
 #include <type_traits>
 
 #include "gdn_kv_page.cuh"

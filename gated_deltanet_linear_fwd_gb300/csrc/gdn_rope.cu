@@ -8,8 +8,12 @@
 //   dx = r (dn - n inv_n sum(dn n)).
 // (From d(r) = -r^3 inv_n sum x dx, with n = x r.)
 //
-// Each element is read and written once and both are bound by that; what
-// comes next is issue slots, so the arithmetic is on pairs of fp32.
+// Each element is read and written once; what comes next to that is issue
+// slots, so the arithmetic is on pairs of fp32.  Measured, 8 + 2 heads of bf16:
+// 32768 tokens 31.0 us, 5.4 TB/s, 81 % of what a copy reaches, with issue slots
+// 74 % busy; the gradient of 34150 packed tokens, weights' sums with it, 54.2
+// us, 4.8 TB/s (73 %), of fp32 80 %.  One token 2.0 us, back to back in a graph.
+// First versions, a block a tile of tokens: 33.8 and 91.7 us.
 #include "gdn_rope.cuh"
 
 namespace gdn {
@@ -49,6 +53,9 @@ __device__ __forceinline__ void row_back(const QkRopeArgs& a, const RopeLane& l,
 }
 
 // As turn_run, with two inputs; the weights' gradients are summed in registers.
+// 113 registers, 16 warps an SM: a row's instructions wait for one another, and
+// at 59 % of issue slots neither those nor memory (68 % of a copy's) is full.
+// Taking both sums of a row at once, in 5 shuffles and not 8, changed nothing.
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeArgs a) {
   constexpr int kBatch = sizeof(T) == 2 ? 2 : 1, kGroups = 2 * kRopeWarps, kRow = kRopeD * sizeof(T);
@@ -165,7 +172,8 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeA
 
 // The CTAs' sums to one, in a fixed order: CTA (side, 8 elements), a row of them
 // a quarter of a warp.  So small that it is there, and waiting, before the kernel
-// that writes the sums has ended.
+// that writes the sums has ended: with 8 CTAs of 1024 threads, which begin after
+// it, the gradient above took 58.2 us.
 constexpr int kSumThreads = 128, kSumWidth = 8, kSumRows = kSumThreads / kSumWidth;
 __global__ void __launch_bounds__(kSumThreads) rope_weight_kernel(const QkRopeArgs a) {
   __shared__ double sum[kSumRows][kSumWidth];

@@ -170,80 +170,146 @@ __device__ __forceinline__ void append_turned_page(const KvRopeArgs& a, const En
 }
 
 // ---- few tokens a sequence ----
-// A page slot and head of keys or values, with at most kFewTokens new rows, by
-// one warp: two rows at a time, a half each.  Of a block's 16 half-warps most
-// would have no row, and a block's start and barriers are what it costs.  Back to
-// back in a graph, 8 + 2 heads, 256 sequences, with 1 / 4 / 8 tokens each: 2.8 /
-// 4.9 / 6.1 us, by blocks 6.6 / 9.7 / 10.7; 1024 sequences of 32 + 8 heads: 12.3
-// / 22.4 / 37.1 and 73 / 104 / 121.  With 16 rows a warp a single sequence takes
-// twice as long (5.9 and 3.1).
-template <typename T, bool kInterleaved, int kFewTokens>
-__device__ __forceinline__ void append_few(const KvRopeArgs& a, unsigned task) {
-  const unsigned h_kv = a.p.c.h_kv, pages = a.entries * h_kv;  // the grid is below 2^31
-  const bool values = task >= pages;
-  if (values) task -= pages;
-  if (task >= pages) return;
-  const int h = (int)(task % h_kv), e = (int)(task / h_kv), seq = e / a.p.pages_each, j = e % a.p.pages_each;
-  const KvSeq s = kv_seq(a.p.c, seq);
-  if (j >= seq_slots(s)) return;
-  const int past = s.len - s.n, slot = max(past, 0) / kPage + j, pos0 = slot * kPage;
-  const int lo = max(past - pos0, 0), hi = min(s.len - pos0, kPage);  // rows of the page that are new
-  if (hi <= lo) return;
-  const int lane = threadIdx.x & 15, half = threadIdx.x >> 4 & 1;
+// The new rows of a page slot.  Without offsets entry e is slot e % pages_each of
+// sequence e / pages_each's; with offsets it is token e's, if that is the slot's
+// first new one.
+struct PageRows {
+  Entry en;
+  int lo, hi;  // hi <= lo: none
+};
+template <bool kRagged>
+__device__ __forceinline__ PageRows page_rows(const KvAppendArgs& a, int e) {
+  PageRows p;
+  p.lo = p.hi = 0;
+  KvSeq& s = p.en.s;
+  if (kRagged) {
+    p.en.seq = seq_of(a.c.cu, a.c.n_seqs, e);
+    s = kv_seq(a.c, p.en.seq);
+    const int at = e - s.tok0, pos = s.len - s.n + at;
+    if (at < 0 || at >= s.n || pos < 0 || (at > 0 && pos % kPage)) return p;
+    p.en.slot = pos / kPage;
+  } else {
+    p.en.seq = e / a.pages_each;
+    s = kv_seq(a.c, p.en.seq);
+    const int j = e % a.pages_each;
+    if (j >= seq_slots(s)) return p;
+    p.en.slot = max(s.len - s.n, 0) / kPage + j;
+  }
+  p.lo = max(s.len - s.n - p.en.slot * kPage, 0);
+  p.hi = min(s.len - p.en.slot * kPage, kPage);
+  return p;
+}
+
+// A page slot and head of keys or values, with at most kFew new rows, by one
+// warp: two rows at a time, a half each.
+template <typename T, bool kInterleaved, int kFew>
+__device__ __forceinline__ void append_few(const KvRopeArgs& a, const PageRows& p, int h, bool values) {
+  const int lane = threadIdx.x & 15, half = threadIdx.x >> 4 & 1, pos0 = p.en.slot * kPage;
   const RopeLane l = values ? RopeLane{8 * lane, 8 * lane + 4, false} : rope_lane(a.q.r, lane);
   const int64_t stride = values ? a.p.v_stride : a.p.k_stride;
-  const T* src = static_cast<const T*>(values ? a.p.v : a.p.k) + ((int64_t)s.tok0 + pos0 - past) * stride + h * kHeadDim;
+  // packed token of row r: tok0 + pos0 + r - (len - n)
+  const T* src = static_cast<const T*>(values ? a.p.v : a.p.k) +
+                 ((int64_t)p.en.s.tok0 + pos0 - (p.en.s.len - p.en.s.n)) * stride + h * kHeadDim;
   const char* first = reinterpret_cast<const char*>(src + l.o0);
   const uint32_t gap = (l.o1 - l.o0) * sizeof(T);
-  typename RowOf<T>::type raw[kFewTokens / 2];
+  typename RowOf<T>::type raw[kFew / 2];
 #pragma unroll
-  for (int i = 0; i < kFewTokens / 2; ++i) {
-    const int r = lo + 2 * i + half;
+  for (int i = 0; i < kFew / 2; ++i) {
+    const int r = p.lo + 2 * i + half;
     raw[i] = {};
-    const char* p = first + r * stride * (int64_t)sizeof(T);
-    if (r < hi) raw[i] = load_row<T>(p, p + gap);
+    const char* at = first + r * stride * (int64_t)sizeof(T);
+    if (r < p.hi) raw[i] = load_row<T>(at, at + gap);
   }
-  const int page = kv_page(a.p.c, seq, slot);
+  const int page = kv_page(a.p.c, p.en.seq, p.en.slot);
   if (page < 0) return;
-  const size_t head = (size_t)page * h_kv + h;
+  const size_t head = (size_t)page * a.p.c.h_kv + h;
   float* scale = (values ? a.p.c.v_scale : a.p.c.k_scale) + head;
-  const float old_s = lo > 0 ? *scale : 0.f;
-  F2 y[kFewTokens / 2][4], w[4];
+  const float old_s = p.lo > 0 ? *scale : 0.f;
+  F2 y[kFew / 2][4], w[4];
   load_weight(values ? nullptr : a.k_weight, l, w);
   const RopeFreq freq = rope_freq(a.q.r, l, lane);
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kFewTokens / 2; ++i) {
+  for (int i = 0; i < kFew / 2; ++i) {
     unpack_row(raw[i], y[i]);
-    if (lo + 2 * i >= hi) continue;
-    if (!values) key_row<kInterleaved>(a, l, w, rope_angles(a.q.r, l, freq, pos0 + lo + 2 * i + half), y[i]);
+    if (p.lo + 2 * i >= p.hi) continue;
+    if (!values) key_row<kInterleaved>(a, l, w, rope_angles(a.q.r, l, freq, pos0 + p.lo + 2 * i + half), y[i]);
     m = max(m, row_bits(y[i]));
   }
   if (m >= 0x7f800000u) m = finite_rows(y);
   m = __reduce_max_sync(0xffffffffu, m);
-  const float now_s = fmaxf(pow2f(min(e4m3_scale_exp(m, kScaleMinExp), kScaleMaxExp)), old_s);
-  const float inv = 1.0f / now_s;  // exact: a power of two
+  const float s = fmaxf(pow2f(min(e4m3_scale_exp(m, kScaleMinExp), kScaleMaxExp)), old_s);
+  const float inv = 1.0f / s;  // exact: a power of two
   uint8_t* codes = (values ? a.p.c.v : a.p.c.k) + head * kPageBytes;
 #pragma unroll
-  for (int i = 0; i < kFewTokens / 2; ++i) {
-    const int r = lo + 2 * i + half;
-    if (r >= hi) continue;
+  for (int i = 0; i < kFew / 2; ++i) {
+    const int r = p.lo + 2 * i + half;
+    if (r >= p.hi) continue;
     *reinterpret_cast<uint32_t*>(codes + r * kHeadDim + l.o0) = encode4(y[i][0], y[i][1], inv);
     *reinterpret_cast<uint32_t*>(codes + r * kHeadDim + l.o1) = encode4(y[i][2], y[i][3], inv);
   }
-  if (now_s > old_s)  // the earlier rows follow
-    for (uint32_t* c = reinterpret_cast<uint32_t*>(codes) + (threadIdx.x & 31); c < reinterpret_cast<uint32_t*>(codes + lo * kHeadDim); c += 32)
+  if (s > old_s)  // the earlier rows follow
+    for (int i = threadIdx.x & 31; i < p.lo * kHeadDim / 4; i += 32) {
+      uint32_t* c = reinterpret_cast<uint32_t*>(codes) + i;
       *c = recode4(*c, old_s, inv);
-  if ((threadIdx.x & 31) == 0) *scale = now_s;
+    }
+  if ((threadIdx.x & 31) == 0) *scale = s;
 }
 
-template <typename T, bool kInterleaved, int kFewTokens>
+// Of a block's 16 half-warps most would have no row here, and a block's start,
+// barriers and, with offsets, its search for the slot cost more than the rows: so a
+// warp takes a page slot and head.  With offsets a slot may have more than kFew
+// rows after all: those the block does, one after another.  Used where a sequence has
+// up to 8 tokens, with offsets on average.  Back to back in a graph, in us, bf16:
+//   8 + 2 heads, 256 sequences of 1 / 4 / 8 tokens  2.7 / 4.9 / 6.1, by blocks 6.6 / 9.7 / 10.7
+//     the same with offsets                         3.9 / 7.0 / 11.4,          8.5 / 10.6 / 12.1
+//   32 + 8 heads, 1024 sequences                    12.6 / 23 / 38,            73 / 104 / 121
+//     the same with offsets                         18 / 54 / 119,             178 / 193 / 214
+//   8 + 2 (32 + 8) heads, 255 of 1 token and one of 1700  10.4 (23),           12.0 (36)
+//     63 of 1 token and one of 448                  7.0 (10),                  5.5 (11)
+// With 16 rows a warp a single sequence takes twice as long (5.9 and 3.1).
+template <typename T, bool kInterleaved, int kFew, bool kRagged>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_few_kernel(const KvRopeArgs a) {
-  __shared__ RopeRing ring;
+  __shared__ uint32_t top;
+  __shared__ Entry many[kRopeWarps];  // seq < 0: none
+  __shared__ union {
+    PageSteps steps;
+    RopeRing ring;
+  } sh;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (blockIdx.x < (unsigned)a.q.ctas) turn_run<T, kInterleaved>(a.q, blockIdx.x, ring);
-  else append_few<T, kInterleaved, kFewTokens>(a, (blockIdx.x - a.q.ctas) * kRopeWarps + warp_index());
+  if (blockIdx.x < (unsigned)a.q.ctas) {
+    turn_run<T, kInterleaved>(a.q, blockIdx.x, sh.ring);
+    return;
+  }
+  const unsigned block = blockIdx.x - a.q.ctas, warp = warp_index(), h_kv = a.p.c.h_kv;
+  const unsigned slots = kRagged ? (unsigned)a.p.c.T : a.entries, pages = slots * h_kv;  // of keys; as many of values
+  // with offsets heads come after one another: slots of many rows are then in different blocks
+  auto values = [&](unsigned w) { return block * kRopeWarps + w >= pages; };
+  auto place = [&](unsigned w) { return block * kRopeWarps + w - (values(w) ? pages : 0u); };
+  auto head = [&](unsigned w) { return (int)(kRagged ? place(w) / slots : place(w) % h_kv); };
+  PageRows p;
+  p.lo = p.hi = 0;
+  if (place(warp) < pages) p = page_rows<kRagged>(a.p, (int)(kRagged ? place(warp) % slots : place(warp) / h_kv));
+  if (p.hi > p.lo && p.hi - p.lo <= kFew) append_few<T, kInterleaved, kFew>(a, p, head(warp), values(warp));
+  if constexpr (kRagged) {
+    if (block == 0)  // the lengths of sequences without tokens are checked too
+      for (int i = threadIdx.x; i < a.p.c.n_seqs; i += kThreads) kv_seq(a.p.c, i);
+    const bool more = p.hi - p.lo > kFew;
+    if ((threadIdx.x & 31) == 0) {
+      many[warp] = p.en;
+      if (!more) many[warp].seq = -1;
+    }
+    if (!__syncthreads_or(more)) return;
+    for (unsigned w = 0; w < kRopeWarps; ++w) {
+      const Entry en = many[w];
+      if (en.seq < 0) continue;
+      if (threadIdx.x == 0) top = 0;
+      if (values(w)) append_page<T>(a.p, en, head(w), true, top);
+      else append_turned_page<T, kInterleaved>(a, en, head(w), top, sh.steps);
+      __syncthreads();
+    }
+  }
 }
 
 template <typename T, bool kInterleaved>
@@ -278,16 +344,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_rope_
 }  // namespace
 
 cudaError_t launch_kv_append_rope(const KvRopeArgs& a, bool f32, cudaStream_t st) {
-  const unsigned tasks = 2 * a.entries * (unsigned)a.p.c.h_kv;
-  const int most = a.p.c.cu ? kPage : a.p.c.n_each;  // new rows of a page
-  const bool few = most <= 8;
+  // with offsets the mean
+  const int64_t each = a.p.c.cu ? ((int64_t)a.p.c.T + a.p.c.n_seqs - 1) / a.p.c.n_seqs : a.p.c.n_each;
+  const bool few = each <= 8;
+  const unsigned tasks = 2 * (few && a.p.c.cu ? (unsigned)a.p.c.T : a.entries) * (unsigned)a.p.c.h_kv;
   const dim3 grid(a.q.ctas + (few ? (tasks + kRopeWarps - 1) / kRopeWarps : tasks)), block(kThreads);
   auto run = [&](auto type, auto interleaved) {
     using T = decltype(type);
     constexpr bool kInterleaved = decltype(interleaved)::value;
-    return most <= 4 ? launch_kernel(append_few_kernel<T, kInterleaved, 4>, grid, block, 0, st, true, a)
-           : few     ? launch_kernel(append_few_kernel<T, kInterleaved, 8>, grid, block, 0, st, true, a)
-                     : launch_kernel(append_rope_kernel<T, kInterleaved>, grid, block, 0, st, true, a);
+    auto launch = [&](auto kernel) { return launch_kernel(kernel, grid, block, 0, st, true, a); };
+    if (!few) return launch(append_rope_kernel<T, kInterleaved>);
+    if (a.p.c.cu)
+      return each <= 4 ? launch(append_few_kernel<T, kInterleaved, 4, true>) : launch(append_few_kernel<T, kInterleaved, 8, true>);
+    return each <= 4 ? launch(append_few_kernel<T, kInterleaved, 4, false>) : launch(append_few_kernel<T, kInterleaved, 8, false>);
   };
   auto typed = [&](auto type) { return a.q.r.interleaved ? run(type, std::true_type()) : run(type, std::false_type()); };
   return f32 ? typed(float()) : typed(__nv_bfloat16());

@@ -171,6 +171,35 @@ def test_few_tokens_each(n, dtype):
     assert gdn.gdn_get_device_status(c.cache.status) == (0, 0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("mean", [4, 8])
+def test_few_tokens_with_offsets(dtype, mean):
+    """Mostly single tokens, a few long pieces over several pages among them, empty sequences, tokens behind the last one."""
+    q = [1, 0, 2, 70, 1, 1, 5, 0, 1, 9, 1] + [1] * 20 + [0, 3, 17, 64, 0]
+    q += [1] * max(0, -((mean * len(q) - sum(q) - 3) // (mean - 1)))
+    kv = [max(n, 1) + (37 * i) % 200 for i, n in enumerate(q)]
+    kv[3], kv[-1] = 70, 65
+    assert sum(q) + 3 <= mean * len(q)
+    for norm, size, layout in (("rms", 1.0, "half"), ("unit", 1.0, "interleaved"), ("none", 50.0, "half")):
+        c = Case(q, kv, 3, 2, dtype, seed=90 + mean, norm=norm, layout=layout, weights=norm == "rms")
+        c.k = (c.k.float() * size).to(dtype)
+        pad = lambda t: torch.cat([t, torch.full((3, *t.shape[1:]), math.nan, dtype=t.dtype)]).cuda()  # noqa: E731
+        c.gk, c.gv = pad(c.k), pad(c.v)
+        out = torch.full((c.b.T + 3, 3, 128), 6.0, dtype=dtype, device="cuda")
+        c.call(q=pad(c.q), q_out=out)
+        assert (out[c.b.T:] == 6).all()
+        c.check(out[:c.b.T])
+    lens = c.b.lens.clone()
+    lens[1] = -5   # a sequence without tokens
+    gdn.gdn_kv_append_rope(c.cache, c.gk, c.gv, lens.cuda(), c.b.table.cuda(), c.cu, **c.how)
+    assert gdn.gdn_get_device_status(c.cache.status) == (7, 7)
+    for bad in ([0] * len(q) + [sum(q)], [0, 5, 3] + c.b.cu.tolist()[3:], [0] + [2 ** 30] * len(q), [-4] + c.b.cu.tolist()[1:]):
+        c.cache.status.zero_()   # offsets that leave the call or go back: no access leaves the buffers
+        gdn.gdn_kv_append_rope(c.cache, c.gk, c.gv, c.b.lens.cuda(), c.b.table.cuda(),
+                               torch.tensor(bad, dtype=torch.int32, device="cuda"), **c.how)
+        torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("use_cu", [True, False])
 def test_not_finite_keys(use_cu):
     """They become NaN codes (their whole head under a norm, but for an infinity's) and do not count in the scale."""

@@ -54,6 +54,15 @@ __device__ __forceinline__ ConvSeq conv_seq(const ConvArgs& a, int t) {
   return s;
 }
 
+// The sequence of token t, which is where s ends: mostly the next one.
+__device__ __forceinline__ ConvSeq conv_seq_after(const ConvArgs& a, const ConvSeq& s, int t) {
+  if (a.cu && s.seq >= 0 && s.seq + 2 <= a.n_seqs) {
+    const ConvSeq n = {s.seq + 1, a.cu[s.seq + 1], a.cu[s.seq + 2]};
+    if (n.begin == t && n.end > t && n.end <= a.T) return n;
+  }
+  return conv_seq(a, t);
+}
+
 // ---- four consecutive channels of a lane, as two pairs of fp32 ----
 // A warp holds a head of 128 channels.
 template <typename T>
@@ -263,28 +272,32 @@ __device__ __forceinline__ ConvTask conv_task(const ConvArgs& a, unsigned i) {
   return t;
 }
 
-// Element i of the states after the call: row r of sequence s is the padded
+// The state after the call of a sequence's head, a warp each: row r is the padded
 // row len + r of (state, tokens).
-template <typename T>
-__device__ __forceinline__ void final_states(const ConvArgs& a, int64_t i, int C) {
-  const int W1 = a.width - 1;
-  const int64_t row = i / (C / 4);
-  const int c = (int)(i % (C / 4)) * 4;
-  if (row >= (int64_t)a.n_seqs * W1) return;
-  const int seq = (int)(row / W1), r = (int)(row % W1);
-  int begin = 0, end = 0;
+template <typename T, int W>
+__device__ __forceinline__ void final_state(const ConvArgs& a, unsigned task, int heads) {
+  const unsigned seq = task / (unsigned)heads;
+  if (seq >= (unsigned)a.n_seqs) return;
+  const int C = heads * kConvD, c = (int)(task - seq * heads) * kConvD + 4 * (threadIdx.x & 31);
+  int begin, end;
   if (a.cu) {
     begin = min(max(a.cu[seq], 0), a.T);
     end = min(max(a.cu[seq + 1], begin), a.T);
   } else {
-    begin = seq * a.n_each;
+    begin = (int)seq * a.n_each;
     end = begin + a.n_each;
   }
-  const int at = end - W1 + r;
-  Raw<T> v = {};
-  if (at >= begin) v = load_raw(static_cast<const T*>(a.x) + at * a.x_stride + c);
-  else if (a.state) v = load_raw(static_cast<const T*>(a.state) + ((int64_t)seq * W1 + W1 + at - begin) * C + c);
-  *reinterpret_cast<Raw<T>*>(static_cast<T*>(a.final_state) + row * C + c) = v;
+  const int64_t row = (int64_t)seq * (W - 1);
+  Raw<T> v[W - 1];
+#pragma unroll
+  for (int r = 0; r < W - 1; ++r) {
+    const int at = end - (W - 1) + r;
+    v[r] = {};
+    if (at >= begin) v[r] = load_raw(static_cast<const T*>(a.x) + at * a.x_stride + c);
+    else if (a.state) v[r] = load_raw(static_cast<const T*>(a.state) + (row + (W - 1) + at - begin) * C + c);
+  }
+#pragma unroll
+  for (int r = 0; r < W - 1; ++r) *reinterpret_cast<Raw<T>*>(static_cast<T*>(a.final_state) + (row + r) * C + c) = v[r];
 }
 
 // A warp a (run, head); then CTAs for the final states.  A warp's next tokens are
@@ -301,11 +314,11 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int heads = 2 * a.h_qk + a.h_v, C = heads * kConvD;
+  const unsigned warp = warp_index();
   if (blockIdx.x >= (unsigned)a.blocks) {
-    final_states<T>(a, (int64_t)(blockIdx.x - a.blocks) * kThreads + threadIdx.x, C);
+    final_state<T, W>(a, (blockIdx.x - a.blocks) * kWarps + warp, heads);
     return;
   }
-  const unsigned warp = warp_index();
   const ConvTask task = conv_task(a, blockIdx.x * kWarps + warp);
   const int head = task.head, c = head * kConvD + 4 * lane;
   const int64_t first = (int64_t)task.place * task.run;
@@ -344,10 +357,15 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
   load_bias(a.bias, c, b);
   const HeadRows<T> rows = head_rows<T>(a, head);
   T* y = rows.p + t0 * rows.stride + 4 * lane;
-  ConvSeq s = conv_seq(a, t0);
-  load_window<T, W>(a, s, t0, c, C, win);
-  int straight = s.seq >= 0 ? min(s.end, t1) : -1;  // where the current sequence, and straight code, ends
+  ConvSeq s = {-1, 0, t0};
+  int straight = 0;  // where the current sequence, and straight code, ends
+  auto begin_sequence = [&](int t) {
+    s = conv_seq_after(a, s, t);
+    load_window<T, W>(a, s, t, c, C, win);
+    straight = s.seq >= 0 ? min(s.end, t1) : -1;
+  };
   for (int g = t0; g < t1; g += G) {
+    if (g == s.end) begin_sequence(g);
     copy_wait<kRing / G - 1>();
     __syncwarp();
     const T* x = reinterpret_cast<const T*>(ring + slot * kRowBytes) + 4 * lane;
@@ -384,11 +402,7 @@ __global__ void __launch_bounds__(kThreads, 3) conv_kernel(const ConvArgs a) {
     } else {
 #pragma unroll 1
       for (int i = 0; i < min(G, t1 - g); ++i, y += rows.stride) {
-        if (g + i == s.end) {
-          s = conv_seq(a, g + i);
-          load_window<T, W>(a, s, g + i, c, C, win);
-          straight = s.seq >= 0 ? min(s.end, t1) : -1;
-        }
+        if (g + i == s.end) begin_sequence(g + i);
         if (s.seq < 0) continue;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
@@ -602,10 +616,14 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
     load_bias(a.bias, c, b);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) acc[j][0] = acc[j][1] = f2(0.f);
-    ConvSeq s = conv_seq(a, t0);
-    load_window<T, W>(a, s, t0, c, C, win);
-    // groups from `from_t` on that end by `straight` go through straight code
-    int straight = s.seq >= 0 ? min(s.end, t1) : -1, from_t = max(s.begin, t0) + W - 1;
+    ConvSeq s = {-1, 0, t0};
+    int straight = 0, from_t = 0;  // groups from `from_t` on that end by `straight` go through straight code
+    auto begin_sequence = [&](int t) {
+      s = conv_seq_after(a, s, t);
+      load_window<T, W>(a, s, t, c, C, win);
+      straight = s.seq >= 0 ? min(s.end, t1) : -1;
+      from_t = max(s.begin, t0) + W - 1;
+    };
     bool done = false;
     for (int g0 = t0; g0 < stop && !done; g0 += G) {
       copy_wait<kRing / G - 1>();
@@ -668,10 +686,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
               done = true;
               break;
             }
-            s = conv_seq(a, t);
-            load_window<T, W>(a, s, t, c, C, win);
-            straight = s.seq >= 0 ? min(s.end, t1) : -1;
-            from_t = max(s.begin, t0) + W - 1;
+            begin_sequence(t);
           }
           if (s.seq < 0) continue;
           F2 in[W][2];
@@ -742,16 +757,14 @@ __global__ void __launch_bounds__(1024) conv_bwd_sum_kernel(const ConvArgs a) {
   grid_launch_dependents();
   const int blocks = a.sums ? (W + 1) * (C / 32) : 0;
   if ((int)blockIdx.x >= blocks) {
-    const int64_t i = ((int64_t)blockIdx.x - blocks) * 1024 + threadIdx.x;
-    const int64_t row = i / (C / 4);
-    const int c = (int)(i % (C / 4)) * 4;
-    if (row >= (int64_t)a.n_seqs * (W - 1)) return;
-    const int seq = (int)(row / (W - 1));
-    const bool empty = a.cu ? a.cu[seq + 1] <= a.cu[seq] : a.n_each == 0;
-    if (!empty) return;
-    Raw<T> v = {};
-    if (a.d_final) v = load_raw(static_cast<const T*>(a.d_final) + row * C + c);
-    *reinterpret_cast<Raw<T>*>(static_cast<T*>(a.d_state) + row * C + c) = v;
+    const int64_t seq = ((int64_t)blockIdx.x - blocks) * 32 + warp;  // a warp a sequence
+    if (seq >= a.n_seqs || (a.cu ? a.cu[seq + 1] > a.cu[seq] : a.n_each > 0)) return;
+    const int64_t n = (int64_t)(W - 1) * C;
+    for (int64_t i = 4 * lane; i < n; i += 4 * 32) {
+      Raw<T> v = {};
+      if (a.d_final) v = load_raw(static_cast<const T*>(a.d_final) + seq * n + i);
+      *reinterpret_cast<Raw<T>*>(static_cast<T*>(a.d_state) + seq * n + i) = v;
+    }
     return;
   }
   const int j = blockIdx.x % (W + 1), at = (int)(blockIdx.x / (W + 1)) * 32 + lane;
@@ -794,7 +807,7 @@ cudaError_t launch_conv(const ConvArgs& args, bool f32, cudaStream_t st) {
   const int64_t heads = 2 * a.h_qk + a.h_v, tasks = (int64_t)a.n_unit * a.runs[0] + (heads - a.n_unit) * a.runs[1];
   a.blocks = (int)((tasks + kWarps - 1) / kWarps);
   int64_t blocks = a.blocks;
-  if (a.final_state) blocks += ((int64_t)a.n_seqs * (a.width - 1) * heads * 32 + kThreads - 1) / kThreads;
+  if (a.final_state) blocks += ((int64_t)a.n_seqs * heads + kWarps - 1) / kWarps;
   if (blocks == 0) return cudaSuccess;
   return by_kind(a, f32, [&](auto type, auto w, auto silu) {
     return launch_kernel(conv_kernel<decltype(type), decltype(w)::value, decltype(silu)::value>, dim3((unsigned)blocks),
@@ -821,7 +834,7 @@ cudaError_t launch_conv_bwd(const ConvArgs& a, bool f32, cudaStream_t st) {
 cudaError_t launch_conv_bwd_sums(const ConvArgs& a, bool f32, cudaStream_t st) {
   const int64_t C = (int64_t)(2 * a.h_qk + a.h_v) * kConvD;
   int64_t blocks = a.sums ? (a.width + 1) * (C / 32) : 0;
-  if (a.d_state) blocks += ((int64_t)a.n_seqs * (a.width - 1) * (C / 4) + 1023) / 1024;
+  if (a.d_state) blocks += ((int64_t)a.n_seqs + 31) / 32;
   if (blocks == 0) return cudaSuccess;
   return f32 ? launch_kernel(conv_bwd_sum_kernel<float>, dim3((unsigned)blocks), dim3(1024), 0, st, true, a)
              : launch_kernel(conv_bwd_sum_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(1024), 0, st, true, a);

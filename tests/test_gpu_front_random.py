@@ -99,6 +99,29 @@ def test_conv(seed):
     F.check("d_state", got[3], want[3], bound[3], dtype)
 
 
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_conv_of_many_short_sequences(W, dtype):
+    """Hundreds of sequences of 0 to 9 tokens, runs of empty ones among them, states on both sides."""
+    r, g = random.Random(W), torch.Generator().manual_seed(200 + W)
+    rnd = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    lens = [r.choice([0, 1, 2, 3, 4, 4, 5, 8, 9]) for _ in range(150)] + [0] * 40 + [4] * 64 + [r.randint(0, 9) for _ in range(60)] + [0, 0]
+    T, C, n = sum(lens), 512, len(lens)
+    x, w, state, d_final = rnd(T, C).to(dtype), rnd(C, W) / 2, rnd(n, W - 1, C).to(dtype), rnd(n, W - 1, C).to(dtype)
+    d = [rnd(T, h, 128).to(dtype) for h in (1, 1, 2)]
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    ref = F.Conv(x, w, 1, None, state, lens)
+    q, k, v, last = gdn.gdn_conv_fwd(x.cuda(), w.cuda(), 1, None, state.cuda(), cu)
+    for got, want, bound in zip((q, k, v), ref.out, ref.bounds):
+        F.check("out", got, want, bound, dtype)
+    assert torch.equal(last.double().cpu(), ref.last)
+    got = gdn.gdn_conv_bwd(x.cuda(), w.cuda(), 1, *[t.cuda() for t in d], None, state.cuda(), d_final.cuda(), cu)
+    want, bound = ref.backward(*d, d_final)
+    F.check("dx", got[0], want[0], bound[0], dtype)
+    F.check("dw", got[1], want[1], bound[1])
+    F.check("d_state", got[3], want[3], bound[3], dtype)
+
+
 # ---- more than 2^31 elements: the last tokens against a call on them alone, bit for bit ----
 FAR, LAST = 2 ** 31 // 512 + 5000, 300
 

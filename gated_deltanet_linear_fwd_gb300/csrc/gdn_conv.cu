@@ -11,7 +11,7 @@
 // and keeps the last W - 1 inputs in registers, so an input is read once but for
 // the W - 1 before each run.  Measured, 2 + 2 + 8 heads, 4 taps, bf16: 32768
 // tokens 35.5 us, 5.7 TB/s, 85 % of what a copy reaches; 348160 tokens 331 us, 97
-// %; the gradient of 32768 tokens 70.5 us, 4.3 TB/s (64 %); one token for 256
+// %; the gradient of 32768 tokens 69.6 us, 4.3 TB/s (65 %); one token for 256
 // sequences 2.6 us, back to back in a graph.  First versions: 78.6, 662 and 165.
 #include <type_traits>
 
@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(const ConvArgs a)
 // state gradients of sequences without tokens, which are their final state's.
 template <typename T>
 __global__ void __launch_bounds__(1024) conv_bwd_sum_kernel(const ConvArgs a) {
-  __shared__ double sum[32][33];
+  __shared__ float2 sum[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int W = a.width, C = (2 * a.h_qk + a.h_v) * kConvD;
   grid_dependency_wait();
@@ -774,17 +774,17 @@ __global__ void __launch_bounds__(1024) conv_bwd_sum_kernel(const ConvArgs a) {
   const int groups = a.runs[unit_head ? 0 : 1];
   const float* part = conv_part(a, unit_head, 0, j, at);
   const int64_t step = conv_part(a, unit_head, 1, j, at) - part;
-  double v = 0.0;
+  Sum2 v;
 #pragma unroll 8
-  for (int i = warp; i < groups; i += 32) v += part[i * step];
-  sum[warp][lane] = v;
+  for (int i = warp; i < groups; i += 32) v.add(part[i * step]);
+  sum[warp][lane] = make_float2(v.hi, v.lo);
   __syncthreads();
   if (warp == 0) {
-    v = 0.0;
+    v = {};
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v += sum[i][lane];
-    if (j == W) a.d_bias[at] = (float)v;
-    else a.d_weight[(int64_t)at * W + j] = (float)v;
+    for (int i = 0; i < 32; ++i) v.add({sum[i][lane].x, sum[i][lane].y});
+    if (j == W) a.d_bias[at] = v.value();
+    else a.d_weight[(int64_t)at * W + j] = v.value();
   }
 }
 

@@ -2,6 +2,7 @@
 // multiply-adds an issue slot, and the kernels that use them are otherwise bound
 // by issue slots before memory.  Also the approximate functions they use.
 #pragma once
+#include <cmath>
 #include <cstdint>
 
 namespace gdn {
@@ -61,6 +62,22 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+
+// A sum in two fp32, what the additions round off in the second [Knuth's sum of two
+// numbers and its exact error]: 64-bit additions issue at a small fraction of the rate.
+struct Sum2 {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float t = __fadd_rn(hi, x), z = __fsub_rn(t, hi);
+    lo += __fsub_rn(hi, __fsub_rn(t, z)) + __fsub_rn(x, z);
+    hi = t;
+  }
+  __device__ __forceinline__ void add(const Sum2& s) {
+    add(s.hi);
+    lo += s.lo;
+  }
+  __device__ __forceinline__ float value() const { return fabsf(hi) < INFINITY ? hi + lo : hi; }
+};
 
 // Two bf16 in a word as fp32 (exact), and back (nearest even).
 __device__ __forceinline__ F2 bf16_pair(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }

@@ -11,8 +11,8 @@
 // Each element is read and written once; what comes next to that is issue
 // slots, so the arithmetic is on pairs of fp32.  Measured, 8 + 2 heads of bf16:
 // 32768 tokens 31.0 us, 5.4 TB/s, 81 % of what a copy reaches, with issue slots
-// 74 % busy; the gradient of 34150 packed tokens, weights' sums with it, 54.2
-// us, 4.8 TB/s (73 %), of fp32 80 %.  One token 2.0 us, back to back in a graph.
+// 74 % busy; the gradient of 34150 packed tokens, weights' sums with it, 52.7
+// us, 5.0 TB/s (75 %), of fp32 80 %.  One token 2.0 us, back to back in a graph.
 // First versions, a block a tile of tokens: 33.8 and 91.7 us.
 #include "gdn_rope.cuh"
 
@@ -173,26 +173,26 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeA
 // The CTAs' sums to one, in a fixed order: CTA (side, 8 elements), a row of them
 // a quarter of a warp.  So small that it is there, and waiting, before the kernel
 // that writes the sums has ended: with 8 CTAs of 1024 threads, which begin after
-// it, the gradient above took 58.2 us.
+// it, the gradient took 58.2 us and not 54.2; with 64-bit additions 54.2 and not 52.7.
 constexpr int kSumThreads = 128, kSumWidth = 8, kSumRows = kSumThreads / kSumWidth;
 __global__ void __launch_bounds__(kSumThreads) rope_weight_kernel(const QkRopeArgs a) {
-  __shared__ double sum[kSumRows][kSumWidth];
+  __shared__ float2 sum[kSumRows][kSumWidth];
   const int e = threadIdx.x % kSumWidth, row = threadIdx.x / kSumWidth;
   const int side = blockIdx.x / (kRopeD / kSumWidth), at = blockIdx.x % (kRopeD / kSumWidth) * kSumWidth + e;
   grid_dependency_wait();
   grid_launch_dependents();
   float* out = a.side[side].d_weight;
   if (!out) return;
-  double v = 0.0;
+  Sum2 v;
 #pragma unroll 19
-  for (int i = row; i < a.ctas; i += kSumRows) v += a.part[((int64_t)i * 2 + side) * kRopeD + at];
-  sum[row][e] = v;
+  for (int i = row; i < a.ctas; i += kSumRows) v.add(a.part[((int64_t)i * 2 + side) * kRopeD + at]);
+  sum[row][e] = make_float2(v.hi, v.lo);
   __syncthreads();
   if (row == 0) {
-    v = 0.0;
+    v = {};
 #pragma unroll
-    for (int i = 0; i < kSumRows; ++i) v += sum[i][e];
-    out[at] = (float)v;
+    for (int i = 0; i < kSumRows; ++i) v.add({sum[i][e].x, sum[i][e].y});
+    out[at] = v.value();
   }
 }
 

@@ -122,6 +122,26 @@ def test_conv_of_many_short_sequences(W, dtype):
     F.check("d_state", got[3], want[3], bound[3], dtype)
 
 
+def test_infinite_gradients_in_sums():
+    """An infinity among what is summed is the sum, with its sign, as in one plain sum."""
+    g = torch.Generator().manual_seed(7)
+    q, d = torch.randn(40, 3, 128, generator=g), torch.randn(40, 3, 128, generator=g)
+    d[17, 1, 3] = -torch.inf
+    w = torch.ones(128)
+    pos = F.places([40])[1]
+    dw = gdn.gdn_qk_rope_bwd(q.cuda(), None, d.cuda(), None, gdn.gdn_rope_table(128), norm="rms", q_weight=w.cuda())[2].cpu()
+    n, ang = F.normed(q, "rms", None, 1e-6)[17, 1], 17 * F.frequencies(128)[3]
+    assert dw.isinf().nonzero().flatten().tolist() == [3, 67] and not dw.isnan().any()
+    # du of the pair: cos (-inf) and sin inf
+    assert (dw[3] < 0) == (torch.cos(ang) * n[3] > 0) and (dw[67] > 0) == (torch.sin(ang) * n[67] > 0) and pos[17] == 17
+    x, taps, bias = torch.randn(40, 512, generator=g), torch.randn(512, 4, generator=g), torch.zeros(512)
+    dv = torch.randn(40, 2, 128, generator=g)
+    dv[9, 1, 5] = torch.inf
+    zero = torch.zeros(40, 1, 128).cuda()
+    db = gdn.gdn_conv_bwd(x.cuda(), taps.cuda(), 1, zero, zero, dv.cuda(), bias.cuda(), activation="none")[2].cpu()
+    assert db.isinf().nonzero().flatten().tolist() == [389] and db[389] > 0 and not db.isnan().any()
+
+
 # ---- more than 2^31 elements: the last tokens against a call on them alone, bit for bit ----
 FAR, LAST = 2 ** 31 // 512 + 5000, 300
 

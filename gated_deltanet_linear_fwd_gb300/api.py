@@ -519,13 +519,9 @@ def gdn_rope_table(rot: int = 128, *, base: float = 10000.0, layout: str = "half
     return Rope(torch.tensor(signed, dtype=torch.int64, device=device), layout, magnitude)
 
 
-def _tokens(name: str, t: torch.Tensor, inner: int, like: torch.Tensor) -> int:
-    """Token stride of [T, ..] or [B, T, ..] whose last `inner` dimensions are a
-    token, whole, the tokens evenly spaced; 0: packed.  Of `like`'s type and device."""
-    if t.dtype != like.dtype or t.get_device() != like.get_device():
-        raise ValueError(f"{name} must be of the call's type and on its device")
-    if t.is_contiguous():
-        return 0
+def _spacing(name: str, t: torch.Tensor, inner: int) -> int:
+    """Token stride of [T, ..] or [B, T, ..], not packed, whose last `inner` dimensions
+    are a token, whole, the tokens evenly spaced; 0 for one token."""
     shape, strides = t.shape, t.stride()
     lead = len(shape) - inner
     if strides[-1] != 1 or (inner == 2 and shape[-2] > 1 and strides[-2] != shape[-1]):
@@ -550,11 +546,11 @@ def _empty_like(t: torch.Tensor, stream) -> torch.Tensor:
     return _kv_empty(t.shape, t.dtype, t.device, stream)
 
 
-def _place(name: str, t: torch.Tensor, shape, inner: int, like: torch.Tensor, dtype: torch.dtype, device: int):
-    """(address, token stride) of t, of like's type and device and of that shape."""
+def _place(name: str, t: torch.Tensor, shape, inner: int, dtype: torch.dtype, device: int):
+    """(address, token stride) of t, checked to be of that shape, type and device."""
     if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, of the call's type and on its device")
-    return t.data_ptr(), 0 if t.is_contiguous() else _tokens(name, t, inner, like)
+    return t.data_ptr(), 0 if t.is_contiguous() else _spacing(name, t, inner)
 
 
 def _f32(name: str, t: Optional[torch.Tensor], shape, device: int):
@@ -616,7 +612,7 @@ def _heads(name: str, t: torch.Tensor, like: torch.Tensor, dtype: torch.dtype, d
         raise ValueError(f"{name} must be [T, heads, 128] or [B, T, heads, 128], alike in q and k")
     if t.dtype is not dtype or t.get_device() != device:
         raise ValueError(f"{name} must be of the call's type and on its device")
-    return t.data_ptr(), 0 if t.is_contiguous() else _tokens(name, t, 2, like), shape[-2], shape
+    return t.data_ptr(), 0 if t.is_contiguous() else _spacing(name, t, 2), shape[-2], shape
 
 
 _NO_HEADS = (None, 0, 0, None)
@@ -635,20 +631,20 @@ def gdn_qk_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: Opti
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is needed")
-    qp, qs, h_q, q_shape = _NO_HEADS if q is None else _heads("q", q, x, x.dtype, x.get_device())
-    kp, ks, h_k, k_shape = _NO_HEADS if k is None else _heads("k", k, x, x.dtype, x.get_device())
     dtype, dev, handle = _call(x, stream)
+    qp, qs, h_q, q_shape = _NO_HEADS if q is None else _heads("q", q, x, dtype, dev)
+    kp, ks, h_k, k_shape = _NO_HEADS if k is None else _heads("k", k, x, dtype, dev)
     n, T, cu = _sequences((q_shape or k_shape)[:-2], cu_seqlens, dev)
     qo = ko = None
     qos = kos = 0
     if q is not None:
         if q_out is None:
             q_out = _empty_like(q, stream)
-        qo, qos = _place("q_out", q_out, q_shape, 2, x, dtype, dev)
+        qo, qos = _place("q_out", q_out, q_shape, 2, dtype, dev)
     if k is not None:
         if k_out is None:
             k_out = _empty_like(k, stream)
-        ko, kos = _place("k_out", k_out, k_shape, 2, x, dtype, dev)
+        ko, kos = _place("k_out", k_out, k_shape, 2, dtype, dev)
     st = L.load().gdn_qk_rope(qp, kp, _f32("q_weight", q_weight, (128,), dev), _f32("k_weight", k_weight, (128,), dev),
                               _i32("positions", positions, T, dev), cu, _rope_raw(rope, dev), qo, ko,
                               L.rope_dims(n, T, h_q, h_k, _choice("norm", _NORMS, norm), eps, _DT.get(dtype, -1), qs, ks, qos, kos,
@@ -677,22 +673,22 @@ def gdn_qk_rope_bwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor], d_q_ou
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is needed")
-    qp, qs, h_q, q_shape = _NO_HEADS if q is None else _heads("q", q, x, x.dtype, x.get_device())
-    kp, ks, h_k, k_shape = _NO_HEADS if k is None else _heads("k", k, x, x.dtype, x.get_device())
     dtype, dev, handle = _call(x, stream)
+    qp, qs, h_q, q_shape = _NO_HEADS if q is None else _heads("q", q, x, dtype, dev)
+    kp, ks, h_k, k_shape = _NO_HEADS if k is None else _heads("k", k, x, dtype, dev)
     n, T, cu = _sequences((q_shape or k_shape)[:-2], cu_seqlens, dev)
     gq = gk = dqp = dkp = None
     gqs = gks = dqs = dks = 0
     if q is not None:
-        gq, gqs = _place("d_q_out", d_q_out, q_shape, 2, x, dtype, dev)
+        gq, gqs = _place("d_q_out", d_q_out, q_shape, 2, dtype, dev)
         if d_q is None:
             d_q = _empty_like(q, stream)
-        dqp, dqs = _place("d_q", d_q, q_shape, 2, x, dtype, dev)
+        dqp, dqs = _place("d_q", d_q, q_shape, 2, dtype, dev)
     if k is not None:
-        gk, gks = _place("d_k_out", d_k_out, k_shape, 2, x, dtype, dev)
+        gk, gks = _place("d_k_out", d_k_out, k_shape, 2, dtype, dev)
         if d_k is None:
             d_k = _empty_like(k, stream)
-        dkp, dks = _place("d_k", d_k, k_shape, 2, x, dtype, dev)
+        dkp, dks = _place("d_k", d_k, k_shape, 2, dtype, dev)
     qw, kw = _f32("q_weight", q_weight, (128,), dev), _f32("k_weight", k_weight, (128,), dev)
     dqw = None if qw is None else _empty_like(q_weight, stream)
     dkw = None if kw is None else _empty_like(k_weight, stream)
@@ -732,14 +728,14 @@ def gdn_kv_append_rope(cache: KVCache, k: torch.Tensor, v: torch.Tensor, kv_lens
     dtype, dev, handle = _call(k, stream)
     if dev != cache.device_index:
         raise ValueError("k must be on the cache's device")
-    kp, ks = k.data_ptr(), 0 if k.is_contiguous() else _tokens("k", k, 2, k)
-    vp, vs = _place("v", v, shape, 2, k, dtype, dev)
+    kp, ks = k.data_ptr(), 0 if k.is_contiguous() else _spacing("k", k, 2)
+    vp, vs = _place("v", v, shape, 2, dtype, dev)
     h_q, qp, qo, qs, qos = h_kv, None, None, 0, 0
     if q is not None:
         qp, qs, h_q, q_shape = _heads("q", q, k, dtype, dev)
         if q_out is None:
             q_out = _empty_like(q, stream)
-        qo, qos = _place("q_out", q_out, q_shape, 2, k, dtype, dev)
+        qo, qos = _place("q_out", q_out, q_shape, 2, dtype, dev)
     elif q_out is not None:
         raise ValueError("q_out goes with q")
     st = L.load().gdn_kv_append_rope(kp, vp, _f32("k_weight", k_weight, (128,), dev), qp, _f32("q_weight", q_weight, (128,), dev), qo,
@@ -767,7 +763,7 @@ def _conv(x, weight, h_qk, bias, cu_seqlens, activation, norm, eps, stream):
     dtype, device, handle = _call(x, stream)
     n, T, cu = _sequences(lead, cu_seqlens, device)
     how = (h_qk, h_v, W, _choice("activation", _ACTIVATIONS, activation), 1 if norm else 0, eps, _DT.get(dtype, -1),
-           0 if x.is_contiguous() else _tokens("x", x, 1, x))
+           0 if x.is_contiguous() else _spacing("x", x, 1))
     return (lead, C, h_v, n, T, W, dtype, device, handle, _f32("weight", weight, (C, W), device), _f32("bias", bias, (C,), device), cu,
             how)
 
@@ -835,7 +831,7 @@ def gdn_conv_bwd(x: torch.Tensor, weight: torch.Tensor, h_qk: int, d_q: torch.Te
     before, after = _packed("initial_state", initial_state, states, dtype, dev), _packed("d_final_state", d_final_state, states, dtype, dev)
     if dx is None:
         dx = _empty_like(x, stream)
-    dxp, dx_stride = _place("dx", dx, x.shape, 1, x, dtype, dev)
+    dxp, dx_stride = _place("dx", dx, x.shape, 1, dtype, dev)
     d_state = None
     if initial_state is not None if want_initial_state_grad is None else want_initial_state_grad:
         d_state = _kv_empty(states, dtype, x.device, stream) if initial_state is None else _empty_like(initial_state, stream)

@@ -279,18 +279,18 @@ def test_python_refuses():
 
 def test_token_strides():
     """Views whose tokens are whole and evenly spaced give their stride, others are refused."""
-    from gated_deltanet_linear_fwd_gb300.api import _tokens
+    from gated_deltanet_linear_fwd_gb300.api import _spacing
     x = torch.zeros(6, 5, 128)
-    assert _tokens("x", x, 2, x) == 0 and _tokens("x", x[:, 1:3], 2, x) == 640 and _tokens("x", x[::2], 2, x) == 1280
-    assert _tokens("x", x[:1, 1:3], 2, x) == 0
+    assert _spacing("x", x[:, 1:3], 2) == 640 and _spacing("x", x[::2], 2) == 1280
+    assert _spacing("x", x[:1, 1:3], 2) == 0
     b = torch.zeros(2, 3, 5, 128)
-    assert _tokens("b", b[:, :, 2:], 2, b) == 640 and _tokens("b", b[:, ::3], 2, b) == 1920 and _tokens("b", b[:1, :, :1], 2, b) == 640
+    assert _spacing("b", b[:, :, 2:], 2) == 640 and _spacing("b", b[:, ::3], 2) == 1920 and _spacing("b", b[:1, :, :1], 2) == 640
     c = torch.zeros(4, 640)
-    assert _tokens("c", c[:, :512], 1, c) == 640 and _tokens("c", c.view(2, 2, 640)[:, :, :512], 1, c) == 640
+    assert _spacing("c", c[:, :512], 1) == 640 and _spacing("c", c.view(2, 2, 640)[:, :, :512], 1) == 640
     for bad, inner in ((x[:, ::2], 2), (x[:, :, ::2], 2), (x[:1, :2].expand(6, 2, 128), 2), (b[:, :2], 2), (c.T, 1), (c[:, ::2], 1),
-                       (x.transpose(0, 1)[:, :2], 2), (x.double(), 2)):
+                       (x.transpose(0, 1)[:, :2], 2)):
         with pytest.raises(ValueError):
-            _tokens("bad", bad, inner, x)
+            _spacing("bad", bad, inner)
 
 
 # ---------------------------------------------------------------- pins of the plain forms

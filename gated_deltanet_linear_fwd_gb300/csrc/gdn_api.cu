@@ -425,8 +425,7 @@ gdn_status rope_ctas(int64_t most, QkRopeArgs* a) {
   a->ctas = (int)std::max<int64_t>(1, std::min((units + kRopeWarps - 1) / kRopeWarps, most));
   return units / a->ctas / kRopeWarps >= INT_MAX - 1 ? GDN_ERR_INVALID_ARG : GDN_OK;
 }
-constexpr int kRopeCtas = 4 * 152;     // what is resident of the forward
-constexpr int kRopeBwdCtas = 2 * 152;  // and of the gradient; rows of its workspace
+constexpr int kRopeCtas = 4 * 152;  // what is resident of the forward
 
 // Checks of gdn_qk_rope and its gradient that do not need the tensors.
 gdn_status qk_rope_args(const gdn_rope_dims* d, const gdn_rope* rope, const float* q_weight, const float* k_weight,

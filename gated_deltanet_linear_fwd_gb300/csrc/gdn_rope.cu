@@ -183,9 +183,16 @@ __global__ void __launch_bounds__(kSumThreads) rope_weight_kernel(const QkRopeAr
   grid_launch_dependents();
   float* out = a.side[side].d_weight;
   if (!out) return;
+  constexpr int kEach = (kRopeBwdCtas + kSumRows - 1) / kSumRows;
+  float x[kEach];  // all at once: one after another they would be waited for
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int cta = row + i * kSumRows;
+    x[i] = cta < a.ctas ? a.part[((int64_t)cta * 2 + side) * kRopeD + at] : 0.f;
+  }
   Sum2 v;
-#pragma unroll 19
-  for (int i = row; i < a.ctas; i += kSumRows) v.add(a.part[((int64_t)i * 2 + side) * kRopeD + at]);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) v.add(x[i]);
   sum[row][e] = make_float2(v.hi, v.lo);
   __syncthreads();
   if (row == 0) {

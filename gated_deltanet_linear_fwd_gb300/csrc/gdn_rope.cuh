@@ -263,6 +263,7 @@ __device__ __forceinline__ void load_weight(const float* w, const RopeLane& l, F
 // shared memory, 220 instructions went into a row of two heads.
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
+constexpr int kRopeBwdCtas = 2 * 152;  // what is resident of the gradient; rows of its workspace
 
 // Queries or keys.
 struct RopeSide {

@@ -11,7 +11,7 @@
 // Each element is read and written once; what comes next to that is issue
 // slots, so the arithmetic is on pairs of fp32.  Measured, 8 + 2 heads of bf16:
 // 32768 tokens 31.0 us, 5.4 TB/s, 81 % of what a copy reaches, with issue slots
-// 74 % busy; the gradient of 34150 packed tokens, weights' sums with it, 52.7
+// 74 % busy; the gradient of 34150 packed tokens, weights' sums with it, 52.2
 // us, 5.0 TB/s (75 %), of fp32 80 %.  One token 2.0 us, back to back in a graph.
 // First versions, a block a tile of tokens: 33.8 and 91.7 us.
 #include "gdn_rope.cuh"
@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeA
   for (int i = 0; i < kStages; ++i) copy_batch(i);
   int slot = 0;
   bool in = false, all_in = false, new_pair = true, new_side = true;
+  TokenSeq seq;
   Angles angle;
   char* y = nullptr;
   while (now.left > 0) {
@@ -114,7 +115,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeA
     if (new_pair) {
       const int t2 = 2 * now.pair + half, t = min(t2, T_all - 1);
       int pos = 0;
-      in = token_position(a.pos, t, pos) && t == t2;
+      in = token_position(a.pos, t, seq, pos) && t == t2;
       all_in = __all_sync(0xffffffffu, in);
       angle = rope_angles(a.r, l, rope_freq(a.r, l, lane), pos);
     }
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeA
 // The CTAs' sums to one, in a fixed order: CTA (side, 8 elements), a row of them
 // a quarter of a warp.  So small that it is there, and waiting, before the kernel
 // that writes the sums has ended: with 8 CTAs of 1024 threads, which begin after
-// it, the gradient took 58.2 us and not 54.2; with 64-bit additions 54.2 and not 52.7.
+// it, the gradient took 58.2 us and not 54.2; with 64-bit additions 1.5 us more.
 constexpr int kSumThreads = 128, kSumWidth = 8, kSumRows = kSumThreads / kSumWidth;
 __global__ void __launch_bounds__(kSumThreads) rope_weight_kernel(const QkRopeArgs a) {
   __shared__ float2 sum[kSumRows][kSumWidth];

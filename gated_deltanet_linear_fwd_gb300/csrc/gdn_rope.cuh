@@ -51,28 +51,31 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int n, int t) {
   }
   return lo;
 }
-// False for a token outside every sequence.
-__device__ __forceinline__ bool token_position(const PosArgs& a, int t, int& pos) {
+// The sequence of the last token asked for: token t of it is at t - shift.
+struct TokenSeq {
+  int begin = 0, end = 0, shift = 0;
+};
+// False for a token outside every sequence.  Searches only where s is not the token's.
+__device__ __forceinline__ bool token_position(const PosArgs& a, int t, TokenSeq& s, int& pos) {
   if (a.positions) {
     pos = a.positions[t];
     return true;
   }
-  if (!a.cu && !a.lens && t < a.n_each) {  // a single row of tokens, for one: no division
-    pos = t;
-    return true;
+  if (t < s.begin || t >= s.end) {
+    int seq;
+    if (a.cu) {
+      seq = seq_of(a.cu, a.n_seqs, t);
+      s.begin = a.cu[seq];
+      s.end = a.cu[seq + 1];
+    } else {
+      seq = t / a.n_each;
+      s.begin = seq * a.n_each;
+      s.end = s.begin + a.n_each;
+    }
+    s.shift = a.lens ? (int)((unsigned)s.end - (unsigned)a.lens[seq]) : s.begin;
   }
-  int seq, begin, end;
-  if (a.cu) {
-    seq = seq_of(a.cu, a.n_seqs, t);
-    begin = a.cu[seq];
-    end = a.cu[seq + 1];
-  } else {
-    seq = t / a.n_each;
-    begin = seq * a.n_each;
-    end = begin + a.n_each;
-  }
-  pos = (int)((unsigned)t - (unsigned)(a.lens ? end : begin) + (a.lens ? (unsigned)a.lens[seq] : 0u));
-  return t >= begin && t < end;
+  pos = (int)((unsigned)t - (unsigned)s.shift);
+  return t >= s.begin && t < s.end;
 }
 
 struct RopeLane {
@@ -363,6 +366,7 @@ __device__ __forceinline__ void turn_run(const QkRopeArgs& a, unsigned block, Ro
   for (int i = 0; i < kStages; ++i) copy_batch(i);
   int slot = 0;
   bool in = false, new_pair = true, new_side = true;
+  TokenSeq seq;
   Angles angle;
   F2 w[4];
   char* y = nullptr;
@@ -370,7 +374,7 @@ __device__ __forceinline__ void turn_run(const QkRopeArgs& a, unsigned block, Ro
     if (new_pair) {
       const int t2 = 2 * now.pair + half, t = min(t2, T_all - 1);
       int pos = 0;
-      in = token_position(a.pos, t, pos) && t == t2;
+      in = token_position(a.pos, t, seq, pos) && t == t2;
       angle = rope_angles(a.r, l, rope_freq(a.r, l, lane), pos);
     }
     if (new_side) {

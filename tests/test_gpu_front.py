@@ -190,6 +190,27 @@ def test_captured_append_follows_the_lengths():
             assert torch.equal(getattr(one, name + "_scale"), getattr(two, name + "_scale"))
 
 
+def test_captured_graphs_share_a_workspace():
+    """Two captured gradients with one workspace, replayed in turn on a stream: what one left there does not matter to the other."""
+    g = torch.Generator().manual_seed(11)
+    rnd = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    x, taps, bias = rnd(300, 512), rnd(512, 4), rnd(512)
+    d = [rnd(300, h, 128) for h in (1, 1, 2)]
+    q, dq, w, rope = rnd(500, 3, 128), rnd(500, 3, 128), rnd(128).abs(), gdn.gdn_rope_table(64)
+    n = max(gdn.gdn_conv_bwd_workspace_bytes(300, 1, 2, dtype=F32), gdn.gdn_qk_rope_bwd_workspace_bytes())
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")   # NaN bits
+    runs = [lambda: gdn.gdn_conv_bwd(x, taps, 1, *d, bias, workspace=ws)[:3],
+            lambda: [t for t in gdn.gdn_qk_rope_bwd(q, None, dq, None, rope, norm="rms", q_weight=w, workspace=ws) if t is not None]]
+    graphs = [capture(run) for run in runs]
+    want = [[t.clone() for t in run()] for run in runs]
+    for graph, kept in graphs * 2:
+        for t in kept:
+            t.zero_()
+        graph.replay()
+    for (_, kept), ref in zip(graphs, want):
+        assert all(torch.equal(a, b) for a, b in zip(kept, ref))
+
+
 def test_gradients_captured_beside_an_eager_graph():
     """A captured backward while an eager autograd graph over the same leaves is alive."""
     s = Layer([64], seed=7)

@@ -122,6 +122,36 @@ def test_conv_of_many_short_sequences(W, dtype):
     F.check("d_state", got[3], want[3], bound[3], dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_heads(dtype):
+    """More heads than tokens, and than a call has warps."""
+    g = torch.Generator().manual_seed(8)
+    rnd = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    q, k, w = rnd(3, 5003, 128).to(dtype), rnd(3, 301, 128).to(dtype), 1 + 0.2 * rnd(128)
+    rope, f, pos = gdn.gdn_rope_table(96), F.frequencies(96), torch.arange(3)
+    dev = [t.cuda() for t in (q, k)]
+    how = dict(norm="rms", q_weight=w.cuda(), k_weight=w.cuda())
+    for got, x in zip(gdn.gdn_qk_rope(*dev, rope, **how), (q, k)):
+        F.check("out", got, *F.rope_ref(x, pos, f, norm="rms", weight=w), dtype)
+    grads = gdn.gdn_qk_rope_bwd(*dev, dev[0].flip(1), dev[1].flip(1), rope, **how)
+    for i, x in enumerate((q, k)):
+        dx, dw, bx, bw = F.rope_bwd_ref(x, x.flip(1), pos, f, norm="rms", weight=w)
+        F.check("dx", grads[i], dx, bx, dtype)
+        F.check("dw", grads[2 + i], dw, bw)
+    h_qk, h_v, lens = 70, 131, [2, 5]
+    x, taps = rnd(7, (2 * h_qk + h_v) * 128).to(dtype), rnd((2 * h_qk + h_v) * 128, 3) / 2
+    d = [rnd(7, h, 128).to(dtype) for h in (h_qk, h_qk, h_v)]
+    cu = torch.tensor([0, 2, 7], dtype=torch.int32, device="cuda")
+    ref = F.Conv(x, taps, h_qk, lens=lens)
+    out = gdn.gdn_conv_fwd(x.cuda(), taps.cuda(), h_qk, None, None, cu)
+    for got, want, bound in zip(out, ref.out, ref.bounds):
+        F.check("out", got, want, bound, dtype)
+    got = gdn.gdn_conv_bwd(x.cuda(), taps.cuda(), h_qk, *[t.cuda() for t in d], None, None, None, cu)
+    want, bound = ref.backward(*d)
+    F.check("dx", got[0], want[0], bound[0], dtype)
+    F.check("dw", got[1], want[1], bound[1])
+
+
 def test_infinite_gradients_in_sums():
     """An infinity among what is summed is the sum, with its sign, as in one plain sum."""
     g = torch.Generator().manual_seed(7)

@@ -385,10 +385,12 @@ bool misaligned16(std::initializer_list<const void*> ps) {
 }
 
 // eps of a norm: 0 selects the default.  From 1e-20 on, squares that fp32 drops
-// (below 1e-38 each, 128 of them) are nothing beside it.
+// (below 1e-38 each, 128 of them) are nothing beside it; up to 1e20 it is nothing
+// beside a sum of squares past 3e38 (its mean past 2e36), which the kernels take
+// of scaled elements and without it.
 gdn_status norm_eps(float given, float* out) {
   *out = given == 0.f ? 1e-6f : given;
-  return std::isfinite(*out) && *out >= 1e-20f ? GDN_OK : GDN_ERR_INVALID_ARG;
+  return *out >= 1e-20f && *out <= 1e20f ? GDN_OK : GDN_ERR_INVALID_ARG;
 }
 
 gdn_status rope_args(const gdn_rope* rope, int norm, float eps, RopeArgs* r) {

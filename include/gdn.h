@@ -574,7 +574,7 @@ typedef struct gdn_rope_dims {
   int T;        /* tokens of the call */
   int h_q, h_k; /* heads of q and of k; one of them may be 0, with its pointers null */
   int norm;     /* GDN_NORM_* */
-  float eps;    /* 0 selects 1e-6; otherwise at least 1e-20 */
+  float eps;    /* 0 selects 1e-6; otherwise 1e-20 to 1e20 */
   int dtype;    /* GDN_BF16 or GDN_F32 */
   /* Elements from one token to the next, 0: heads * 128 (packed); a multiple of
    * 16 bytes and at least heads * 128, so the tensors may be parts of one fused
@@ -672,7 +672,7 @@ typedef struct gdn_conv_dims {
   int width;      /* taps W: 2, 3 or 4 */
   int activation; /* GDN_ACT_* */
   int norm;       /* 1: q's and k's heads to unit length; 0: not */
-  float eps;      /* 0 selects 1e-6; otherwise at least 1e-20 */
+  float eps;      /* 0 selects 1e-6; otherwise 1e-20 to 1e20 */
   int dtype;      /* GDN_BF16 or GDN_F32: type of x, q, k, v and the states */
   int64_t x_stride;  /* elements from one token to the next in x, 0: C.  A multiple of */
   int64_t dx_stride; /* 16 bytes and at least C.  dx_stride: gdn_conv_bwd's dx. */

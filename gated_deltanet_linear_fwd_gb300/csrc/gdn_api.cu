@@ -1361,7 +1361,7 @@ gdn_status gdn_kv_append_rope(const void* k, const void* v, const float* k_weigh
   a.p.k = const_cast<void*>(k);
   a.p.v = const_cast<void*>(v);
   a.k_weight = k_weight;
-  if (2 * (int64_t)a.entries * cache->h_kv + a.q.ctas > 0x7fffffff) return GDN_ERR_INVALID_ARG;  // blocks
+  if (append_tasks(a) + a.q.ctas > 0x7fffffff) return GDN_ERR_INVALID_ARG;  // blocks, or warps of them
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   LaunchLog log;
   cudaError_t e = log.before(cs);

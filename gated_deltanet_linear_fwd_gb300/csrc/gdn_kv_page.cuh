@@ -220,6 +220,15 @@ struct KvRopeArgs {
   unsigned entries;        // page slots of the call
 };
 
+// Tokens of a sequence, with offsets the mean.
+inline int64_t append_each(const KvArgs& c) { return c.cu ? ((int64_t)c.T + c.n_seqs - 1) / c.n_seqs : c.n_each; }
+// Up to 8 go by warps, where with offsets each token may begin a page slot.
+inline bool append_by_warps(const KvArgs& c) { return append_each(c) <= 8; }
+// Page slots and heads of keys, and as many of values.
+inline int64_t append_tasks(const KvRopeArgs& a) {
+  return 2 * (append_by_warps(a.p.c) && a.p.c.cu ? (int64_t)a.p.c.T : (int64_t)a.entries) * a.p.c.h_kv;
+}
+
 cudaError_t launch_kv_append_rope(const KvRopeArgs& a, bool f32, cudaStream_t st);
 
 }  // namespace gdn

@@ -344,10 +344,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_rope_
 }  // namespace
 
 cudaError_t launch_kv_append_rope(const KvRopeArgs& a, bool f32, cudaStream_t st) {
-  // with offsets the mean
-  const int64_t each = a.p.c.cu ? ((int64_t)a.p.c.T + a.p.c.n_seqs - 1) / a.p.c.n_seqs : a.p.c.n_each;
-  const bool few = each <= 8;
-  const unsigned tasks = 2 * (few && a.p.c.cu ? (unsigned)a.p.c.T : a.entries) * (unsigned)a.p.c.h_kv;
+  const int64_t each = append_each(a.p.c);
+  const bool few = append_by_warps(a.p.c);
+  const unsigned tasks = (unsigned)append_tasks(a);  // below 2^31
   const dim3 grid(a.q.ctas + (few ? (tasks + kRopeWarps - 1) / kRopeWarps : tasks)), block(kThreads);
   auto run = [&](auto type, auto interleaved) {
     using T = decltype(type);

@@ -27,3 +27,12 @@ def test_eps_that_is_taken(lib, eps):  # noqa: F811
     assert lib.gdn_qk_rope(None, None, 64, 64, None, None, rope(), None, None, rope_dims(T=0, eps=eps), None) == OK
     n = ctypes.c_size_t(0)
     assert lib.gdn_conv_bwd_workspace_bytes(conv_dims(eps=eps), n) == OK
+
+
+def test_append_of_more_tokens_than_its_warps_are_counted(lib):  # noqa: F811
+    """With offsets and up to 8 tokens a sequence a warp a token, head, and keys or values: their number stays below 2^31."""
+    for T, n_seqs, h_kv in ((1 << 29, 1 << 26, 7), (1 << 28, 1 << 25, 4), (1 << 30, 1 << 27, 3)):
+        many, offsets = kv_dims(T=T, n_seqs=n_seqs, h_q=1), 64
+        assert 2 * (T // 64 + 2 * n_seqs) * h_kv < 2 ** 31 <= 2 * T * h_kv
+        a = [512, 1024, 64, None, None, None, 64, 64, offsets, cache(h_kv=h_kv), many, rope(), 1, 0.0, None]
+        assert lib.gdn_kv_append_rope(*a) == INVALID

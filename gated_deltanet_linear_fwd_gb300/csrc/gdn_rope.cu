@@ -34,12 +34,9 @@ __device__ __forceinline__ void row_back(const QkRopeArgs& a, const RopeLane& l,
   turn_row<kInterleaved, true>(all, l, angle, g);
   if (!norm) return;
   const float ss = half_sum(dot_row(x, x));
-  float f = rsqrt_approx(fmaf(ss, a.r.inv_n, a.r.eps)), back = f;
-  if (large_heads(ss)) {
-    float unit;
-    f = scaled_head(x, ss, a.r.inv_n, a.r.eps, unit);
-    back = f * unit;
-  }
+  float f = rsqrt_approx(fmaf(ss, a.r.inv_n, a.r.eps)), unit = 1.f;
+  const bool large = large_heads(ss);
+  if (large) f = scaled_head(x, ss, a.r.inv_n, a.r.eps, unit);
   scale_row(x, f);
   if (in) {
 #pragma unroll
@@ -49,7 +46,8 @@ __device__ __forceinline__ void row_back(const QkRopeArgs& a, const RopeLane& l,
   for (int e = 0; e < 4; ++e) g[e] = mul2(g[e], w[e]);
   const F2 m = f2(-half_sum(dot_row(g, x)) * a.r.inv_n);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) g[e] = mul2(fma2(x[e], m, g[e]), f2(back));
+  for (int e = 0; e < 4; ++e) g[e] = mul2(fma2(x[e], m, g[e]), f2(f));
+  if (large) scale_row(g, unit);  // f unit itself may be below fp32's normal numbers
 }
 
 // As turn_run, with two inputs; the weights' gradients are summed in registers.

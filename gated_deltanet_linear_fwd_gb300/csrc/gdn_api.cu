@@ -92,6 +92,7 @@ gdn_status device_setup(int* dev_out) {
   if ((e = kv_f32_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = kv_few_setup()) != cudaSuccess) return cuda_fail(e);
   if ((e = kv_many_setup()) != cudaSuccess) return cuda_fail(e);
+  if ((e = rope_bwd_setup()) != cudaSuccess) return cuda_fail(e);
   int sms = 0;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return cuda_fail(e);
   g_sm_count[dev] = sms;
@@ -1315,6 +1316,10 @@ gdn_status gdn_qk_rope_bwd(const void* q, const void* k, const float* q_weight, 
   a.side[1].d_weight = dk_weight;
   a.part = sums ? static_cast<float*>(workspace) : nullptr;
   if ((st = rope_ctas(kRopeBwdCtas, &a)) != GDN_OK) return st;
+  const int64_t units = ((int64_t)d->T + 1) / 2 * (d->h_q + d->h_k);
+  a.fold = sums && units > (int64_t)kRopeFold * a.ctas * kRopeWarps;
+  int dev = 0;
+  if (a.fold && (st = device_setup(&dev)) != GDN_OK) return st;
   LaunchLog log;
   e = log.before(cs);
   if (e == cudaSuccess) e = launch_qk_rope_bwd(a, d->dtype == GDN_F32, cs);

@@ -50,6 +50,21 @@ __device__ __forceinline__ void row_back(const QkRopeArgs& a, const RopeLane& l,
   if (large) scale_row(g, unit);  // f unit itself may be below fp32's normal numbers
 }
 
+// A lane's sums of the weights' gradients go to its pairs of fp32, [16][threads].
+constexpr int kKept = 16, kKeptBytes = kKept * kRopeThreads * sizeof(float2);
+__device__ __forceinline__ void put_away(float2* kept, F2 (&dwq)[4], F2 (&dwk)[4]) {
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) {
+    const F2 pair = i < 8 ? dwq[i / 2] : dwk[i / 2 - 4];
+    float2& at = kept[i * kRopeThreads + threadIdx.x];
+    Sum2 s = {at.x, at.y};
+    s.add(i % 2 ? parts(pair).y : parts(pair).x);
+    at = make_float2(s.hi, s.lo);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) dwq[e] = dwk[e] = f2(0.f);
+}
+
 // As turn_run, with two inputs; the weights' gradients are summed in registers.
 // 113 registers, 16 warps an SM: a row's instructions wait for one another, and
 // at 59 % of issue slots neither those nor memory (68 % of a copy's) is full.
@@ -74,6 +89,12 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeA
   for (int e = 0; e < 4; ++e) dwq[e] = dwk[e] = w[e] = f2(0.f);
   char* ring = sh.ring[warp];
   Walk now = rope_run(a, (int64_t)blockIdx.x * kRopeWarps + warp), next = now;
+  extern __shared__ float2 kept[];
+  int mark = -1;  // what is left of a long run when the sums are put away next
+  if (a.fold && now.left > kRopeFold) {
+    mark = now.left - kRopeFold;
+    for (int i = 0; i < kKept; ++i) kept[i * kRopeThreads + threadIdx.x] = make_float2(0.f, 0.f);
+  }
   const char *x = nullptr, *g = nullptr;  // the lane's 16 bytes of the next head's rows
   auto place = [&] {
     const bool key = next.h >= h_q;
@@ -148,9 +169,24 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeA
     y += n * kRow;
     new_side = now.step(n, h_q, heads);
     new_pair = now.h == 0;
+    if (now.left <= mark) {
+      put_away(kept, dwq, dwk);
+      mark = max(now.left - kRopeFold, 0);
+    }
   }
   copy_wait<0>();
   if (!a.part) return;
+  if (mark >= 0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      auto value = [&](int i) {
+        const float2 v = kept[i * kRopeThreads + threadIdx.x];
+        return Sum2{v.x, v.y}.value();
+      };
+      dwq[e] = f2(value(2 * e), value(2 * e + 1));
+      dwk[e] = f2(value(8 + 2 * e), value(9 + 2 * e));
+    }
+  }
   __syncthreads();  // the rings are done with
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -213,13 +249,23 @@ cudaError_t launch_qk_rope(const QkRopeArgs& a, bool f32, cudaStream_t st) {
                          : launch_kernel(rope_kernel<__nv_bfloat16, false>, grid, block, 0, st, true, a);
 }
 
+cudaError_t rope_bwd_setup() {
+  auto allow = [](auto kernel) { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeptBytes); };
+  cudaError_t e = allow(rope_bwd_kernel<float, true>);
+  if (e == cudaSuccess) e = allow(rope_bwd_kernel<float, false>);
+  if (e == cudaSuccess) e = allow(rope_bwd_kernel<__nv_bfloat16, true>);
+  if (e == cudaSuccess) e = allow(rope_bwd_kernel<__nv_bfloat16, false>);
+  return e;
+}
+
 cudaError_t launch_qk_rope_bwd(const QkRopeArgs& a, bool f32, cudaStream_t st) {
   const dim3 grid(a.ctas), block(kRopeThreads);
+  const size_t smem = a.fold ? kKeptBytes : 0;
   if (f32)
-    return a.r.interleaved ? launch_kernel(rope_bwd_kernel<float, true>, grid, block, 0, st, true, a)
-                           : launch_kernel(rope_bwd_kernel<float, false>, grid, block, 0, st, true, a);
-  return a.r.interleaved ? launch_kernel(rope_bwd_kernel<__nv_bfloat16, true>, grid, block, 0, st, true, a)
-                         : launch_kernel(rope_bwd_kernel<__nv_bfloat16, false>, grid, block, 0, st, true, a);
+    return a.r.interleaved ? launch_kernel(rope_bwd_kernel<float, true>, grid, block, smem, st, true, a)
+                           : launch_kernel(rope_bwd_kernel<float, false>, grid, block, smem, st, true, a);
+  return a.r.interleaved ? launch_kernel(rope_bwd_kernel<__nv_bfloat16, true>, grid, block, smem, st, true, a)
+                         : launch_kernel(rope_bwd_kernel<__nv_bfloat16, false>, grid, block, smem, st, true, a);
 }
 
 cudaError_t launch_qk_rope_weights(const QkRopeArgs& a, cudaStream_t st) {

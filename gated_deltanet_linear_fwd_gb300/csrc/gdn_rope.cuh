@@ -267,6 +267,10 @@ __device__ __forceinline__ void load_weight(const float* w, const RopeLane& l, F
 constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeBwdCtas = 2 * 152;  // what is resident of the gradient; rows of its workspace
+// Heads of the weights' gradients that a lane adds up in one fp32 number, and one
+// more: longer runs put them away in pairs of fp32, so that sums lose no more the
+// longer the call is.  The pairs take shared memory, which shorter calls go without.
+constexpr int kRopeFold = 255;
 
 // Queries or keys.
 struct RopeSide {
@@ -286,6 +290,7 @@ struct QkRopeArgs {
   RopeSide side[2];        // q, then k
   int ctas;                // whose warps take a run each
   float* part;             // backward: [CTAs, 2, 128] sums of the weights' gradients, or null
+  int fold;                // backward: a run is longer than kRopeFold, and part is wanted
 };
 
 // A place in a warp's heads, which it takes two tokens at a time, one a half of
@@ -416,6 +421,7 @@ __device__ __forceinline__ void turn_run(const QkRopeArgs& a, unsigned block, Ro
   copy_wait<0>();
 }
 
+cudaError_t rope_bwd_setup();  // before calls with fold
 cudaError_t launch_qk_rope(const QkRopeArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_qk_rope_bwd(const QkRopeArgs& a, bool f32, cudaStream_t st);
 cudaError_t launch_qk_rope_weights(const QkRopeArgs& a, cudaStream_t st);

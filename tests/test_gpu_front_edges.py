@@ -34,3 +34,34 @@ def test_gradients_of_the_largest_heads(norm):
     r = F.inv_norm(x.double(), norm, 1e-6)
     n, k = x.double() * r, 1 / 128 if norm == "rms" else 1.0
     F.check("dx", got, want, F.U * r * (10 * dy.double() + 39 * n.abs() * (dy.double() * n.abs()).sum(-1, keepdim=True) * k))
+
+
+def in_pieces(T, f, step=1 << 17):
+    return sum(f(slice(i, min(i + step, T))) for i in range(0, T, step))
+
+
+# Heads of a lane that one fp32 number sums, and the half-warps of a CTA, whose sums are then added up in fp32 too;
+# the CTAs' are added in pairs of fp32.
+ROPE_ROWS = 256 + 16
+
+
+@pytest.mark.parametrize("dtype,rows", [(F32, 700), (BF16, 700), (BF16, 5500)])
+def test_rope_weights_gradients_of_many_tokens(dtype, rows):
+    """Every element against 64 bits, `rows` heads a lane.  Of the first 64 elements all terms are equal, where the
+    roundings of a running sum do not cancel: with numbers of 2^12 it drops half a term's last 12 bits each time."""
+    T = rows * (2 * 152) * 16 // 4
+    g = torch.Generator("cuda").manual_seed(2)
+    x = [torch.randint(0, 2, (T, h, 128), device="cuda", generator=g, dtype=torch.int8).mul_(2).sub_(1).to(dtype) for h in (3, 1)]
+    d = [torch.randn(T, h, 128, device="cuda", generator=g, dtype=dtype) for h in (3, 1)]
+    for a, b in zip(x, d):
+        b[..., :64] = a[..., :64]
+    magnitude = 1 + 0.45 * 2.0 ** -12     # du n of the first 64, but for r
+    rope = gdn.gdn_rope_table(128, magnitude=magnitude)
+    w = torch.ones(128, device="cuda")
+    grads = gdn.gdn_qk_rope_bwd(*x, *d, rope, torch.zeros(T, dtype=torch.int32, device="cuda"), norm="rms", q_weight=w, k_weight=w)
+    factor = float(torch.tensor(magnitude, dtype=F32)) / (1 + 1e-6) ** 0.5
+    for a, b, got in zip(x, d, grads[2:]):
+        want = factor * in_pieces(T, lambda s: (a[s].double() * b[s].double()).sum((0, 1)))
+        mass = factor * in_pieces(T, lambda s: b[s].abs().sum((0, 1), dtype=torch.float64))
+        # du to 9 roundings (of one element alone: cos 1, sin 0), n to 10 and 2 for the product and the end
+        F.check("dw", got, want.cpu(), ((9 + 10 + 2 + ROPE_ROWS) * F.U * mass).cpu())

@@ -65,3 +65,26 @@ def test_rope_weights_gradients_of_many_tokens(dtype, rows):
         mass = factor * in_pieces(T, lambda s: b[s].abs().sum((0, 1), dtype=torch.float64))
         # du to 9 roundings (of one element alone: cos 1, sin 0), n to 10 and 2 for the product and the end
         F.check("dw", got, want.cpu(), ((9 + 10 + 2 + ROPE_ROWS) * F.U * mass).cpu())
+
+
+def test_conv_weights_gradients_of_many_tokens():
+    """Every tap and bias against 64 bits, where dx_t and the products are plain: no activation, no norm."""
+    T, W = 2 ** 22 + 77, 4
+    g = torch.Generator("cuda").manual_seed(3)
+    x = torch.randn(T, 384, device="cuda", generator=g, dtype=BF16)
+    d = [torch.randn(T, 1, 128, device="cuda", generator=g, dtype=BF16) for _ in range(3)]
+    d[2] += 1    # sums that grow
+    w, b = torch.randn(384, W, device="cuda", generator=g), torch.zeros(384, device="cuda")
+    _, dw, db, _ = gdn.gdn_conv_bwd(x, w, 1, *d, b, activation="none", norm=False)
+    # a running sum takes 192 tokens, then 8 warps'; the CTAs' are added in pairs of fp32; a product, and the end
+    roundings = (192 + 8 + 2) * F.U
+    for i, du in enumerate(d):
+        xc, du = x[:, 128 * i:128 * i + 128], du[:, 0]
+        want = in_pieces(T, lambda s: du[s].sum(0, dtype=torch.float64))
+        F.check("db", db[128 * i:128 * i + 128], want.cpu(), roundings * in_pieces(T, lambda s: du[s].abs().sum(0, dtype=torch.float64)).cpu())
+        for j in range(W):
+            late = W - 1 - j     # du_t meets x_{t - late}
+            a, c = xc[:T - late], du[late:]
+            want = in_pieces(T - late, lambda s: (a[s].double() * c[s].double()).sum(0))
+            mass = in_pieces(T - late, lambda s: (a[s].double() * c[s].double()).abs().sum(0))
+            F.check("dw", dw[128 * i:128 * i + 128, j], want.cpu(), (roundings * mass).cpu())

@@ -1357,8 +1357,10 @@ gdn_status gdn_kv_append_rope(const void* k, const void* v, const float* k_weigh
     s.weight = q_weight;
     s.heads = d->h_q;
     // of the resident CTAs as many as their share of the bytes, read and written
-    const int64_t es = d->dtype == GDN_F32 ? 4 : 2, bytes_q = 2 * es * d->h_q, bytes_kv = 2 * (es + 1) * cache->h_kv;
-    if ((st = rope_ctas(kRopeCtas * bytes_q / (bytes_q + bytes_kv), &a.q)) != GDN_OK) return st;
+    const bool f32 = d->dtype == GDN_F32;
+    const int64_t es = f32 ? 4 : 2, bytes_q = 2 * es * d->h_q, bytes_kv = 2 * (es + 1) * cache->h_kv;
+    const int64_t ctas = 152 * (f32 ? kAppendRopeCtas<float> : kAppendRopeCtas<__nv_bfloat16>);
+    if ((st = rope_ctas(ctas * bytes_q / (bytes_q + bytes_kv), &a.q)) != GDN_OK) return st;
   }
   if (d->T == 0) return GDN_OK;
   if (!k || !v) return GDN_ERR_INVALID_ARG;

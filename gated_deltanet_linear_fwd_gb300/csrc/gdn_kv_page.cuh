@@ -220,6 +220,10 @@ struct KvRopeArgs {
   unsigned entries;        // page slots of the call
 };
 
+// CTAs of the rotated append that an SM holds: fp32's take some 100 registers a thread.
+template <typename T>
+constexpr int kAppendRopeCtas = sizeof(T) == 2 ? 4 : 2;
+
 // Tokens of a sequence, with offsets the mean.
 inline int64_t append_each(const KvArgs& c) { return c.cu ? ((int64_t)c.T + c.n_seqs - 1) / c.n_seqs : c.n_each; }
 // Up to 8 go by warps, where with offsets each token may begin a page slot.

@@ -269,7 +269,7 @@ __device__ __forceinline__ void append_few(const KvRopeArgs& a, const PageRows& 
 //     63 of 1 token and one of 448                  7.0 (10),                  5.5 (11)
 // With 16 rows a warp a single sequence takes twice as long (5.9 and 3.1).
 template <typename T, bool kInterleaved, int kFew, bool kRagged>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_few_kernel(const KvRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kAppendRopeCtas<T>) append_few_kernel(const KvRopeArgs a) {
   __shared__ uint32_t top;
   __shared__ Entry many[kRopeWarps];  // seq < 0: none
   __shared__ union {
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_few_k
 }
 
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) append_rope_kernel(const KvRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kAppendRopeCtas<T>) append_rope_kernel(const KvRopeArgs a) {
   __shared__ int part[kThreads / 32];
   __shared__ Entry found;
   __shared__ uint32_t top;

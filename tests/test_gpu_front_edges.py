@@ -1,5 +1,5 @@
 """The operators between the projections and the mixers where fp32 ends: heads
-near its largest numbers, and sums over millions of tokens."""
+near its largest numbers, and sums over millions of tokens; long fp32 appends."""
 from __future__ import annotations
 
 import pytest
@@ -13,6 +13,7 @@ if not torch.cuda.is_available():  # pragma: no cover - collected on CPU, skippe
     pytest.skip("needs a CUDA GPU", allow_module_level=True)
 
 import gated_deltanet_linear_fwd_gb300 as gdn  # noqa: E402
+from tests.test_gpu_kv_rope import Case  # noqa: E402
 
 BF16, F32 = torch.bfloat16, torch.float32
 
@@ -88,3 +89,10 @@ def test_conv_weights_gradients_of_many_tokens():
             want = in_pieces(T - late, lambda s: (a[s].double() * c[s].double()).sum(0))
             mass = in_pieces(T - late, lambda s: (a[s].double() * c[s].double()).abs().sum(0))
             F.check("dw", dw[128 * i:128 * i + 128, j], want.cpu(), (roundings * mass).cpu())
+
+
+@pytest.mark.parametrize("h_q,h_kv", [(8, 2), (2, 4)])
+def test_long_append_of_fp32(h_q, h_kv):
+    """More queries' heads than the resident warps take one of, pages beside them, behind earlier tokens."""
+    c = Case([2900, 1, 333], [2900, 70, 1000], h_q, h_kv, F32, seed=4)
+    c.check(c.call())

@@ -631,6 +631,8 @@ def gdn_qk_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], rope: Opti
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is needed")
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("q_out and k_out go with q and k")
     dtype, dev, handle = _call(x, stream)
     qp, qs, h_q, q_shape = _NO_HEADS if q is None else _heads("q", q, x, dtype, dev)
     kp, ks, h_k, k_shape = _NO_HEADS if k is None else _heads("k", k, x, dtype, dev)
@@ -670,6 +672,8 @@ def gdn_qk_rope_bwd(q: Optional[torch.Tensor], k: Optional[torch.Tensor], d_q_ou
     without the weight.  d_q may be d_q_out, d_k may be d_k_out."""
     if (q is None) != (d_q_out is None) or (k is None) != (d_k_out is None):
         raise ValueError("d_q_out and d_k_out go with q and k")
+    if (q is None and d_q is not None) or (k is None and d_k is not None):
+        raise ValueError("d_q and d_k go with q and k")
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is needed")

@@ -5,6 +5,7 @@ from __future__ import annotations
 import ctypes
 
 import pytest
+import torch
 
 from tests.test_front_host import INVALID, OK, cache, conv_dims, kv_dims, lib, rope, rope_dims  # noqa: F401
 
@@ -36,3 +37,13 @@ def test_append_of_more_tokens_than_its_warps_are_counted(lib):  # noqa: F811
         assert 2 * (T // 64 + 2 * n_seqs) * h_kv < 2 ** 31 <= 2 * T * h_kv
         a = [512, 1024, 64, None, None, None, 64, 64, offsets, cache(h_kv=h_kv), many, rope(), 1, 0.0, None]
         assert lib.gdn_kv_append_rope(*a) == INVALID
+
+
+def test_an_output_without_its_input():
+    """It would come back as it was, as if it were the result."""
+    import gated_deltanet_linear_fwd_gb300 as gdn
+    x, y = torch.zeros(3, 2, 128), torch.ones(3, 2, 128)
+    for call in (lambda: gdn.gdn_qk_rope(None, x, q_out=y), lambda: gdn.gdn_qk_rope(x, None, k_out=y),
+                 lambda: gdn.gdn_qk_rope_bwd(None, x, None, x, d_q=y), lambda: gdn.gdn_qk_rope_bwd(x, None, x, None, d_k=y)):
+        with pytest.raises(ValueError, match="goes? with"):
+            call()

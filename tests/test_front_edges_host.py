@@ -45,5 +45,5 @@ def test_an_output_without_its_input():
     x, y = torch.zeros(3, 2, 128), torch.ones(3, 2, 128)
     for call in (lambda: gdn.gdn_qk_rope(None, x, q_out=y), lambda: gdn.gdn_qk_rope(x, None, k_out=y),
                  lambda: gdn.gdn_qk_rope_bwd(None, x, None, x, d_q=y), lambda: gdn.gdn_qk_rope_bwd(x, None, x, None, d_k=y)):
-        with pytest.raises(ValueError, match="goes? with"):
+        with pytest.raises(ValueError, match="go with"):
             call()

@@ -6,8 +6,9 @@
 // the codes, without a rounding in between; pages, scales and codes are those
 // of gdn_kv.cu.  Blocks: queries, 8 warps' runs each, then keys of a (page
 // slot, head) each, then values; with few tokens a sequence, warps of keys and
-// values.  Measured, 32768 tokens of 8 heads on 2, bf16: 35.7 us, 5.2 TB/s, 78 % of
-// what a copy reaches, with issue slots 73 % busy (norm, rotation, codes).
+// values.  Measured, 32768 tokens of 8 heads on 2, bf16: 35.7 us, 5.2 TB/s, 77 % of
+// what a copy reaches, with issue slots 73 % busy (norm, rotation, codes); of
+// fp32 58.9 us, 90 %.
 #include <type_traits>
 
 #include "gdn_kv_page.cuh"
@@ -35,7 +36,9 @@ __device__ __forceinline__ float or_nan(float x) { return magnitude_bits(x) < 0x
 
 // The rotations by 16, 32 and 48 tokens: a half-warp's rows are 16 apart, and all
 // but the first turn by the first's angles and then by these, a product a
-// pair instead of a cosine and a sine.
+// pair instead of a cosine and a sine.  A cosine is then off by both factors'
+// errors and two roundings more, 13 of 2^-24 and not 6, and a key by up to 27 and not
+// 19 in all; its e4m3 code rounds to 2^-4.
 struct alignas(16) PageSteps {
   float c[kRows - 1][kRopeD / 2], s[kRows - 1][kRopeD / 2];
 };
@@ -267,7 +270,9 @@ __device__ __forceinline__ void append_few(const KvRopeArgs& a, const PageRows& 
 //     the same with offsets                         18 / 54 / 119,             178 / 193 / 214
 //   8 + 2 (32 + 8) heads, 255 of 1 token and one of 1700  10.4 (23),           12.0 (36)
 //     63 of 1 token and one of 448                  7.0 (10),                  5.5 (11)
-// With 16 rows a warp a single sequence takes twice as long (5.9 and 3.1).
+// With 16 rows a warp a single sequence takes twice as long (5.9 and 3.1).  At
+// 64 registers bf16 spills 16 to 124 bytes a thread of 8 rows, and 36 to 72 of 4 with offsets;
+// three CTAs an SM, without spills, are slower.
 template <typename T, bool kInterleaved, int kFew, bool kRagged>
 __global__ void __launch_bounds__(kThreads, kAppendRopeCtas<T>) append_few_kernel(const KvRopeArgs a) {
   __shared__ uint32_t top;
@@ -312,6 +317,8 @@ __global__ void __launch_bounds__(kThreads, kAppendRopeCtas<T>) append_few_kerne
   }
 }
 
+// bf16: at the 64 registers of four CTAs an SM some 50 bytes a thread are spilled;
+// with three and none 38.0 us for 32768 tokens, with four 35.4.
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, kAppendRopeCtas<T>) append_rope_kernel(const KvRopeArgs a) {
   __shared__ int part[kThreads / 32];

@@ -11,8 +11,9 @@
 // Each element is read and written once; what comes next to that is issue
 // slots, so the arithmetic is on pairs of fp32.  Measured, 8 + 2 heads of bf16:
 // 32768 tokens 31.0 us, 5.4 TB/s, 81 % of what a copy reaches, with issue slots
-// 74 % busy; the gradient of 34150 packed tokens, weights' sums with it, 52.2
-// us, 5.0 TB/s (75 %), of fp32 80 %.  One token 2.0 us, back to back in a graph.
+// 74 % busy; the gradient of 34150 packed tokens, weights' sums with it, 52.5
+// us, 5.0 TB/s (75 %).  32768 tokens of fp32 57.7 us (87 %), their gradient 87.9
+// (86 %).  One token 2.0 us, back to back in a graph.
 // First versions, a block a tile of tokens: 33.8 and 91.7 us.
 #include "gdn_rope.cuh"
 
@@ -51,6 +52,8 @@ __device__ __forceinline__ void row_back(const QkRopeArgs& a, const RopeLane& l,
 }
 
 // A lane's sums of the weights' gradients go to its pairs of fp32, [16][threads].
+// 5500 equal terms a lane: without this off by 800 roundings of 2^-24.  2^20 tokens of
+// 8 + 2 heads, 2100 terms a lane, take 1356 us, and took 1350.
 constexpr int kKept = 16, kKeptBytes = kKept * kRopeThreads * sizeof(float2);
 __device__ __forceinline__ void put_away(float2* kept, F2 (&dwq)[4], F2 (&dwk)[4]) {
 #pragma unroll
@@ -66,8 +69,8 @@ __device__ __forceinline__ void put_away(float2* kept, F2 (&dwq)[4], F2 (&dwk)[4
 }
 
 // As turn_run, with two inputs; the weights' gradients are summed in registers.
-// 113 registers, 16 warps an SM: a row's instructions wait for one another, and
-// at 59 % of issue slots neither those nor memory (68 % of a copy's) is full.
+// 105 to 119 registers, 16 warps an SM: a row's instructions wait for one another,
+// and at 59 % of issue slots neither those nor memory (75 % of a copy's) is full.
 // Taking both sums of a row at once, in 5 shuffles and not 8, changed nothing.
 template <typename T, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const QkRopeArgs a) {

@@ -9,8 +9,11 @@
 //
 // The angle of pair i at position p is p f_i.  Frequencies come as turns a
 // token times 2^64, so the low 64 bits of p F are the angle in turns modulo
-// one, exact for every 32-bit position: nothing is lost at far ones, where
-// a product in fp32 is off by 2^-24 of hundreds of thousands of radians.
+// one, and that product is exact for every 32-bit position.  What is off is the
+// table (fp64 frequencies to a few of 2^-53 of themselves, to 2^-65 turns: 2^-34
+// turns at position 2^31) and the cut to the top 32 bits (2^-32 turns): less
+// than fp32 can hold of a cosine.  A product in fp32 would be off by 2^-24 of
+// hundreds of thousands of radians at far positions.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -94,9 +97,10 @@ __device__ __forceinline__ RopeLane rope_lane(const RopeArgs& r, int l) {
 // Cos and sin of two angles of phase / 2^32 turns.  The nearest quarter turn
 // comes off in integers; what remains, u halves of a quarter turn, |u| <= 1,
 // goes into polynomials of u^2 whose coefficients are the minimax ones on [0, 1]
-// (Remez's exchange): u A(u^2) for sin(pi u / 4), relative error 2^-28, and B(u^2)
-// for cos, 2^-34.  Some 25 instructions an angle; with sincospif an angle took
-// 94, a fifth of the forward's.
+// (Remez's exchange): u A(u^2) for sin(pi u / 4) and B(u^2) for cos.  With the
+// coefficients rounded to fp32 and as computed here, all u on a grid of 2^-22: sine
+// to 2^-22.9 and cosine to 2^-23.5 of themselves, within 2 ulp.  Some 25
+// instructions an angle; with sincospif an angle took 94, a fifth of the forward's.
 __device__ __forceinline__ void sincos_turns(uint32_t p0, uint32_t p1, F2& c, F2& s) {
   const uint32_t q0 = (p0 + 0x20000000u) >> 30, q1 = (p1 + 0x20000000u) >> 30;
   const F2 u = mul2(f2((float)(int32_t)(p0 - (q0 << 30)), (float)(int32_t)(p1 - (q1 << 30))), f2(0x1p-29f)), v = mul2(u, u);

@@ -552,7 +552,9 @@ typedef struct gdn_rope_opts {
 /*
  * gdn_rope_table -- host only: the frequencies as turns a token times 2^64,
  * to nearest: uint64 [rot / 2].  Copied to the device once, they give the
- * angle of any 32-bit position exactly, as the low 64 bits of a product.
+ * angle of any 32-bit position as the low 64 bits of a product, which is exact;
+ * the table itself is off by half a unit (2^-65 turns a token) and by a few
+ * roundings of fp64 in the frequency.
  * Errors: INVALID_ARG, UNSUPPORTED (rot, scaling).
  */
 gdn_status gdn_rope_table(const gdn_rope_opts* opts, uint64_t* turns_host);
@@ -601,8 +603,10 @@ typedef struct gdn_rope_dims {
  *                       address and stride; the same address with another stride is
  *                       refused); otherwise outputs overlap nothing.
  * Where a head's sum of squares passes fp32's range it is taken of scaled
- * elements, so finite heads of any size are normalised.  An infinite or NaN
- * element makes NaN of itself and of its pair, NaN of the whole head.
+ * elements, so finite heads of any size are normalised.  Under a norm a NaN makes
+ * NaN of its whole head, and an infinity NaN of itself and zeros of the others (r = 0).
+ * A NaN that is turned makes NaN of its pair; an infinity makes infinities or NaN of
+ * its pair, as its products with cosine and sine are.
  * Errors: INVALID_ARG, UNSUPPORTED (dtype, norm, rot, layout), MISALIGNED (16 bytes), CUDA.
  */
 gdn_status gdn_qk_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,

@@ -222,7 +222,7 @@ struct KvRopeArgs {
 
 // CTAs of the rotated append that an SM holds: fp32's kernels take 74 to 128
 // registers a thread.  With queries cut for four of them an SM 32768 tokens of
-// 32 + 8 heads took 240 us, for two 235; 512 sequences of 8 tokens 20.5 and 16.4.
+// 32 + 8 heads took 240 us, for two 235; 512 sequences of 8 tokens 20.5 and 16.4 (dirty L2).
 template <typename T>
 constexpr int kAppendRopeCtas = sizeof(T) == 2 ? 4 : 2;
 

@@ -46,9 +46,13 @@ __device__ __forceinline__ void row_back(const QkRopeArgs& a, const RopeLane& l,
 #pragma unroll
   for (int e = 0; e < 4; ++e) g[e] = mul2(g[e], w[e]);
   const F2 m = f2(-half_sum(dot_row(g, x)) * a.r.inv_n);
+  // unit comes in halves, one with f: f unit may be below fp32's normal numbers, and
+  // a gradient times f past the largest
+  const float root = large && unit != 1.f ? kHeadUnitRoot : 1.f;
+  f *= root;
 #pragma unroll
   for (int e = 0; e < 4; ++e) g[e] = mul2(fma2(x[e], m, g[e]), f2(f));
-  if (large) scale_row(g, unit);  // f unit itself may be below fp32's normal numbers
+  if (large) scale_row(g, root);
 }
 
 // A lane's sums of the weights' gradients go to its pairs of fp32, [16][threads].

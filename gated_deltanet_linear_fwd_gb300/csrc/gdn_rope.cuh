@@ -236,7 +236,7 @@ __device__ __forceinline__ void scale_row(F2 (&x)[4], float f) {
 // A head's sum of squares, and whether it passes fp32's range in either half
 // (elements of 2^60 and more): then scaled_head takes it again of x 2^-68, which x
 // becomes and its 1 / sqrt(inv_n ss) belongs to; eps is nothing beside it.
-constexpr float kHeadUnit = 0x1p-68f;
+constexpr float kHeadUnit = 0x1p-68f, kHeadUnitRoot = 0x1p-34f;
 __device__ __forceinline__ bool large_heads(float ss) { return __any_sync(0xffffffffu, !(ss <= 3e38f)); }
 // Also whether this half's is the large one: unit is then kHeadUnit, else 1.
 __device__ __forceinline__ float scaled_head(F2 (&x)[4], float ss, float inv_n, float eps, float& unit) {

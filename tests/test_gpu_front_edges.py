@@ -37,6 +37,15 @@ def test_gradients_of_the_largest_heads(norm):
     F.check("dx", got, want, F.U * r * (10 * dy.double() + 39 * n.abs() * (dy.double() * n.abs()).sum(-1, keepdim=True) * k))
 
 
+def test_large_gradients_of_large_heads():
+    """r is large beside the scale there: dx is far within fp32's range, as is each product on the way."""
+    x, dy = torch.full((3, 1, 128), 1.65e18), torch.zeros(3, 1, 128)     # squares' sum 3.5e38
+    dy[:, 0, 7] = torch.tensor([1e37, -2e37, 1e36])
+    got = gdn.gdn_qk_rope_bwd(x.cuda(), None, dy.cuda(), None, norm="rms")[0]
+    want, _, bound, _ = F.rope_bwd_ref(x, dy, torch.arange(3), F.frequencies(0), norm="rms")
+    F.check("dx", got, want, bound)
+
+
 def in_pieces(T, f, step=1 << 17):
     return sum(f(slice(i, min(i + step, T))) for i in range(0, T, step))
 

@@ -548,8 +548,9 @@ __device__ __forceinline__ void unit_back(F2 (&y)[G][2], F2 (&g)[G][2], float ep
       y[i][0] = mul2(y[i][0], f2(r));
       y[i][1] = mul2(y[i][1], f2(r));
       const F2 m = f2(-warp_sum(dot(g[i], y[i])));
+      const float root = unit == 1.f ? 1.f : 0x1p-34f;  // by halves: g r may leave fp32's range, and so may r unit
 #pragma unroll
-      for (int e = 0; e < 2; ++e) g[i][e] = mul2(mul2(fma2(y[i][e], m, g[i][e]), f2(r)), f2(unit));
+      for (int e = 0; e < 2; ++e) g[i][e] = mul2(mul2(fma2(y[i][e], m, g[i][e]), f2(r * root)), f2(root));
     }
     return;
   }

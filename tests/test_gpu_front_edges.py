@@ -46,6 +46,17 @@ def test_large_gradients_of_large_heads():
     F.check("dx", got, want, bound)
 
 
+def test_large_gradients_of_large_heads_before_the_delta_rule():
+    """The same behind the convolution's unit norm, whose taps are one of the token itself."""
+    x, w = torch.full((3, 384), 1.65e18), torch.zeros(384, 2)
+    w[:, 1] = 1
+    d = [torch.zeros(3, 1, 128) for _ in range(3)]
+    d[0][:, 0, 7] = d[1][:, 0, 9] = torch.tensor([3e37, -9e37, 1e36])
+    got = gdn.gdn_conv_bwd(x.cuda(), w.cuda(), 1, *[t.cuda() for t in d], activation="none")[0]
+    want, bound = F.Conv(x, w, 1, silu=False).backward(*d)
+    F.check("dx", got, want[0], bound[0])
+
+
 def in_pieces(T, f, step=1 << 17):
     return sum(f(slice(i, min(i + step, T))) for i in range(0, T, step))
 
